@@ -4,7 +4,8 @@ Every step of the producer runs in the CUDA library ``lib/libmsa_producer.so``;
 this module only turns Python/torch arguments into the C call.  There is no CPU
 or eager fallback: if the library has not been built, every call raises.
 
-Names follow ``include/msa_producer.h``.
+Names follow ``include/msa_producer.h``, ``include/msa_projection.h`` and
+``include/msa_attention.h``.
 """
 from __future__ import annotations
 
@@ -37,7 +38,8 @@ EXPORTED = ("msa_producer_forward", "msa_producer_validate", "msa_producer_launc
             "msa_host_buffer_device_address",
             "msa_status_string",
             "msa_last_error_detail", "msa_projection_forward", "msa_projection_validate",
-            "msa_checked_violations")
+            "msa_checked_violations", "msa_attention_workspace_bytes",
+            "msa_sparse_attention_forward", "msa_prefix_attention_forward")
 
 MSA_STATUS_WAIT_TIMEOUT = 1
 
@@ -90,6 +92,20 @@ class MsaIndexerCfg(ctypes.Structure):
     ]
 
 
+class MsaAttentionCfg(ctypes.Structure):
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("block_tokens", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("scale_mode", ctypes.c_int32),
+        ("reserved", ctypes.c_int32 * 2),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -136,6 +152,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.msa_projection_forward.restype = ctypes.c_int
         L.msa_projection_validate.argtypes = proj
         L.msa_projection_validate.restype = ctypes.c_int
+        attnp = ctypes.POINTER(MsaAttentionCfg)
+        L.msa_attention_workspace_bytes.argtypes = [attnp, i64, i64, ctypes.POINTER(i64)]
+        L.msa_attention_workspace_bytes.restype = ctypes.c_int
+        L.msa_sparse_attention_forward.argtypes = [attnp, i64, vp, vp, vp, vp, i64, vp, cachep, cachep,
+                                                   vp, vp, vp, vp, i64, i32, vp]
+        L.msa_sparse_attention_forward.restype = ctypes.c_int
+        L.msa_prefix_attention_forward.argtypes = [attnp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64,
+                                                   cachep, cachep, vp, vp, vp, vp, i64, i32, vp]
+        L.msa_prefix_attention_forward.restype = ctypes.c_int
         L.msa_host_buffer_device_address.argtypes = [vp, ctypes.POINTER(ctypes.c_void_p)]
         L.msa_host_buffer_device_address.restype = ctypes.c_int
         L.msa_checked_violations.argtypes = [ctypes.POINTER(ctypes.c_uint64), i32]
@@ -323,6 +348,61 @@ def msa_indexer_forward_fused_noalloc(cfg, num_queries, idx_q, kv_len, table_off
     return s
 
 
+def make_attention_cfg(num_q_heads, num_kv_heads, head_dim, page_size=64, block_tokens=128, topk=16,
+                       softmax_scale=None, scale_mode=MSA_SCALE_PER_TENSOR) -> MsaAttentionCfg:
+    """``softmax_scale`` defaults to head_dim ** -0.5."""
+    c = MsaAttentionCfg()
+    c.num_q_heads, c.num_kv_heads = int(num_q_heads), int(num_kv_heads)
+    c.head_dim, c.page_size = int(head_dim), int(page_size)
+    c.block_tokens, c.topk = int(block_tokens), int(topk)
+    c.softmax_scale = float(head_dim) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    c.scale_mode = int(scale_mode)
+    c.reserved[0] = c.reserved[1] = 0
+    return c
+
+
+def msa_attention_workspace_bytes(cfg, num_queries, num_groups=0) -> int:
+    """Bytes of workspace the attention calls need (0 groups: the sparse one, or no
+    shared prefix)."""
+    n = ctypes.c_int64(0)
+    s = load().msa_attention_workspace_bytes(ctypes.byref(cfg) if cfg is not None else None,
+                                             int(num_queries), int(num_groups), ctypes.byref(n))
+    if s != MSA_OK:
+        raise MsaError(s, "msa_attention_workspace_bytes", last_error_detail())
+    return int(n.value)
+
+
+def msa_sparse_attention_forward(cfg, num_queries, q, kv_len, table_offset, page_table,
+                                 page_table_len, topk_ids, k_cache, v_cache, scales, out, lse=None,
+                                 workspace=None, workspace_bytes=0, launch_flags=0, stream=0,
+                                 check=True) -> int:
+    """The C entry point; pointers are integers or None.  Raises MsaError unless the
+    call returns MSA_OK (``check=False`` returns the status)."""
+    s = load().msa_sparse_attention_forward(
+        ctypes.byref(cfg) if cfg is not None else None, int(num_queries), q, kv_len, table_offset,
+        page_table, int(page_table_len), topk_ids, _ref(k_cache), _ref(v_cache), scales, out, lse,
+        workspace, int(workspace_bytes), int(launch_flags), stream)
+    if check and s != MSA_OK:
+        raise MsaError(s, "msa_sparse_attention_forward", last_error_detail())
+    return s
+
+
+def msa_prefix_attention_forward(cfg, num_queries, q, num_groups, group_start, prefix_len,
+                                 prefix_offset, kv_len, table_offset, page_table, page_table_len,
+                                 k_cache, v_cache, scales, out, lse=None, workspace=None,
+                                 workspace_bytes=0, launch_flags=0, stream=0, check=True) -> int:
+    """The C entry point; pointers are integers or None.  Raises MsaError unless the
+    call returns MSA_OK (``check=False`` returns the status)."""
+    s = load().msa_prefix_attention_forward(
+        ctypes.byref(cfg) if cfg is not None else None, int(num_queries), q, int(num_groups),
+        group_start, prefix_len, prefix_offset, kv_len, table_offset, page_table,
+        int(page_table_len), _ref(k_cache), _ref(v_cache), scales, out, lse, workspace,
+        int(workspace_bytes), int(launch_flags), stream)
+    if check and s != MSA_OK:
+        raise MsaError(s, "msa_prefix_attention_forward", last_error_detail())
+    return s
+
+
 def msa_checked_violations(reset: bool = True):
     """Stores skipped by a checked build since the last reset (synchronises the
     device); None for a normal build."""
@@ -395,3 +475,80 @@ def forward_tensors(cfg: MsaProducerCfg, qkv, positions, slot_mapping, page_tabl
                          _ptr(slot_mapping), _ptr(page_table), pt_len, _ptr(wq), _ptr(wk),
                          _ptr(wiq), _ptr(wik), _ptr(q_out), _ptr(idx_q_out), k_cache, v_cache,
                          idx_k_cache, _ptr(scales), launch_flags, stream.cuda_stream)
+
+
+def _tensor(name, t, shape, dtypes, device):
+    """Checks a tensor argument of the attention calls: shape, dtype, contiguous, on
+    ``device``; returns its address (None for None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtypes[0]} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q on {device}")
+    return t.data_ptr()
+
+
+def _attention_call(fn, cfg, q, before, kv_len, table_offset, page_table, after, k_cache, v_cache,
+                    scales, out, lse, workspace, num_groups, launch_flags, stream):
+    import torch
+    bf16 = (torch.bfloat16, torch.int16)
+    dev, i32, i64 = q.device, (torch.int32,), (torch.int64,)
+    if dev.type != "cuda":
+        raise ValueError(f"q is on {dev}; the attention calls take CUDA tensors")
+    T, Hq, D = int(q.shape[0]), cfg.num_q_heads, cfg.head_dim
+    ns = 2 * cfg.num_kv_heads if cfg.scale_mode == MSA_SCALE_PER_HEAD else 2
+    if scales is not None and (scales.dim() != 1 or scales.numel() < ns):
+        raise ValueError(f"scales: expected at least {ns} values, got shape {tuple(scales.shape)}")
+    with torch.cuda.device(dev):
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        if workspace is None:
+            n = msa_attention_workspace_bytes(cfg, T, num_groups)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        args = ([_tensor("q", q, (T, Hq, D), bf16, dev)] + before(dev)
+                + [_tensor("kv_len", kv_len, (T,), i32, dev),
+                   _tensor("table_offset", table_offset, (T,), i64, dev),
+                   _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel()]
+                + after(dev)
+                + [k_cache, v_cache,
+                   _tensor("scales", scales, () if scales is None else scales.shape, (torch.float32,), dev),
+                   _tensor("out", out, (T, Hq, D), bf16, dev),
+                   _tensor("lse", lse, (T, Hq), (torch.float32,), dev),
+                   workspace.data_ptr() or None, workspace.numel() * workspace.element_size()])
+        fn(cfg, T, *args, launch_flags, stream.cuda_stream)
+
+
+def sparse_attention_tensors(cfg: MsaAttentionCfg, q, topk_ids, kv_len, table_offset, page_table,
+                             k_cache, v_cache, scales, out, lse=None, workspace=None,
+                             launch_flags=0, stream=None) -> None:
+    """msa_sparse_attention_forward on contiguous torch CUDA tensors (caches are
+    MsaCacheDesc).  ``workspace``: a uint8 tensor of at least
+    ``msa_attention_workspace_bytes(cfg, T)`` bytes, or None to allocate one.  Runs on
+    ``stream`` or the current stream of q's device."""
+    import torch
+    _attention_call(msa_sparse_attention_forward, cfg, q, lambda dev: [], kv_len, table_offset,
+                    page_table,
+                    lambda dev: [_tensor("topk_ids", topk_ids, (q.shape[0], cfg.topk), (torch.int32,), dev)],
+                    k_cache, v_cache, scales, out, lse, workspace, 0, launch_flags, stream)
+
+
+def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, prefix_offset, kv_len,
+                             table_offset, page_table, k_cache, v_cache, scales, out, lse=None,
+                             workspace=None, launch_flags=0, stream=None) -> None:
+    """msa_prefix_attention_forward on contiguous torch CUDA tensors; the three group
+    tensors are None when no prefix is shared.  ``workspace`` and ``stream`` as for
+    ``sparse_attention_tensors`` (the bytes also depend on the number of groups)."""
+    import torch
+    n = 0 if prefix_len is None else int(prefix_len.shape[0])
+
+    def groups(dev):
+        return [n, _tensor("group_start", group_start, (n + 1,), (torch.int32,), dev),
+                _tensor("prefix_len", prefix_len, (n,), (torch.int32,), dev),
+                _tensor("prefix_offset", prefix_offset, (n,), (torch.int64,), dev)]
+
+    _attention_call(msa_prefix_attention_forward, cfg, q, groups, kv_len, table_offset, page_table,
+                    lambda dev: [], k_cache, v_cache, scales, out, lse, workspace, n, launch_flags,
+                    stream)

@@ -13,8 +13,9 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", n) for n in ("msa_producer.cu", "msa_indexer.cu", "msa_projection.cu")]
-HEADERS = [os.path.join(PKG, "csrc", "msa_internal.h")]
+SOURCES = [os.path.join(PKG, "csrc", n) for n in ("msa_producer.cu", "msa_indexer.cu", "msa_projection.cu",
+                                                    "msa_attention.cu")]
+HEADERS = [os.path.join(PKG, "csrc", n) for n in ("msa_internal.h", "msa_attention_internal.h")]
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB_NAME = "libmsa_producer.so"
@@ -70,7 +71,8 @@ def _link_flags() -> list:
     return ["-cudart", "shared", "-Xlinker", f"-rpath,{libdir}"]
 
 
-DEPENDENCIES = SOURCES + HEADERS + [os.path.join(INCLUDE, h) for h in ("msa_producer.h", "msa_projection.h")]
+DEPENDENCIES = SOURCES + HEADERS + [os.path.join(INCLUDE, h) for h in ("msa_producer.h", "msa_projection.h",
+                                                                         "msa_attention.h")]
 STAMP_PATH = LIB_PATH + ".sha256"
 
 

@@ -1,0 +1,453 @@
+// Attention over the paged K/V caches: argument checks, dispatch, and the kernel for
+// every layout.
+//
+// What is computed is stated in include/msa_attention.h.
+
+#include "msa_attention_internal.h"
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// the kernel for every layout: one CTA per (query, up to eight heads of a K/V head)
+// ---------------------------------------------------------------------------
+//
+// 128 threads walk the visible tokens 128 at a time with the running maximum and sum
+// of an online softmax.  Scores: a thread holds one token and multiplies its key row
+// with the CTA's (at most eight) query rows, kept as fp32 in shared memory.  Output: a
+// thread holds one dim (of 64 dims, one dim of every other token) of the eight rows
+// and adds the tokens' values times their weights.  Rows are read 8 elements (FP8) or
+// 8 elements of 16 bits at a time, the alignment that every accepted layout has.  It
+// is bound by its fp32 multiply-adds and serves the layouts that the tensor-core
+// kernels do not take.
+constexpr int kRowThreads = 128;
+constexpr int kRowHeads = 8;
+
+__device__ __forceinline__ void load8(const uint8_t *base, bool fp8, int64_t elem, float (&x)[8])
+{
+    if (fp8) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(base + elem);
+        const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = attn_e4m3x2_to_f2((ww[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4 *>(base + 2 * elem);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(ww[i] << 16);
+            x[2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) msa_attention_rows_kernel(const __grid_constant__ AttnParams p)
+{
+    __shared__ float s_q[kRowHeads][D];
+    __shared__ float s_p[kRowThreads][kRowHeads];
+    __shared__ int64_t s_v[kRowThreads];        // element offset of the token's value row, -1: not visible
+    __shared__ float s_red[2][4][kRowHeads];
+    __shared__ int32_t s_ids[64];
+    __shared__ int s_n, s_group;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int chunks = (p.group + kRowHeads - 1) / kRowHeads;
+    const int64_t bid = blockIdx.x;
+    const int hc = (int)(bid % chunks);
+    const int c = (int)((bid / chunks) % p.hkv);
+    const int64_t t = bid / ((int64_t)chunks * p.hkv);
+    const int h0 = c * p.group + hc * kRowHeads;
+    const int nh = min(kRowHeads, p.group - hc * kRowHeads);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    const int32_t own = max(p.kv_len[t], 0);
+    if (tid == 0) {
+        s_group = 0x7fffffff;
+        s_n = 0;
+        if (p.topk_ids) {   // the ids of this query that name a block, each once
+            const int64_t nb = ((int64_t)own + p.block_tokens - 1) / p.block_tokens;
+            int n = 0;
+            for (int i = 0; i < p.topk; ++i) {
+                const int32_t id = p.topk_ids[t * p.topk + i];
+                bool keep = id >= 0 && id < nb;
+                for (int j = 0; j < n && keep; ++j)
+                    keep = s_ids[j] != id;
+                if (keep)
+                    s_ids[n++] = id;
+            }
+            s_n = n;
+        }
+    }
+    const float qs = p.scale_log2 * attn_k_scale(p, c);
+    for (int i = tid; i < kRowHeads * D; i += kRowThreads) {
+        const int h = i / D;
+        s_q[h][i % D] = h < nh ? __uint_as_float((uint32_t)p.q[(t * p.hq + h0 + h) * D + i % D] << 16) : 0.0f;
+    }
+    __syncthreads();
+    for (int i = tid; i <= p.num_groups && p.num_groups > 0; i += kRowThreads)
+        if (p.group_start[i] > t)
+            atomicMin(&s_group, i);
+    __syncthreads();
+
+    constexpr int kSlices = kRowThreads / D;     // threads per dim
+    const int dim = tid % D, slice = tid / D;
+    float acc[kRowHeads] = {}, m[kRowHeads], l[kRowHeads] = {};
+#pragma unroll
+    for (int h = 0; h < kRowHeads; ++h)
+        m[h] = -INFINITY;
+
+    // the prefix of the query's group, then its own history
+    const int g = s_group - 1;
+    const bool has_prefix = g >= 0 && g < p.num_groups;
+    for (int part = has_prefix ? 0 : 1; part < 2; ++part) {
+        const int64_t off = part == 0 ? p.prefix_offset[g] : p.table_offset[t];
+        const int64_t len = part == 0 ? max(p.prefix_len[g], 0) : own;
+        const bool sparse = p.topk_ids != nullptr;
+        const int64_t total = sparse ? (int64_t)s_n * p.block_tokens : len;
+        for (int64_t v0 = 0; v0 < total; v0 += kRowThreads) {
+            const int64_t v = v0 + tid;
+            int64_t j = v;
+            if (sparse && v < total)
+                j = (int64_t)s_ids[v / p.block_tokens] * p.block_tokens + v % p.block_tokens;
+            const int32_t pg = (v < total && j < len) ? attn_page(p, off, j) : -1;
+            float s[kRowHeads];
+#pragma unroll
+            for (int h = 0; h < kRowHeads; ++h)
+                s[h] = 0.0f;
+            int64_t voff = -1;
+            if (pg >= 0) {
+                const int64_t row = attn_page_row(p, j);
+                const int64_t koff = (int64_t)pg * p.k.stride_page + (int64_t)c * p.k.stride_head + row * p.k.stride_token;
+                voff = (int64_t)pg * p.v.stride_page + (int64_t)c * p.v.stride_head + row * p.v.stride_token;
+                for (int d = 0; d < D; d += 8) {
+                    float x[8];
+                    load8(p.k.data, p.k.fp8, koff + d, x);
+#pragma unroll
+                    for (int h = 0; h < kRowHeads; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            s[h] = fmaf(s_q[h][d + e], x[e], s[h]);
+                }
+            }
+            float mx[kRowHeads];
+#pragma unroll
+            for (int h = 0; h < kRowHeads; ++h) {
+                s[h] = pg >= 0 ? s[h] * qs : -INFINITY;
+                mx[h] = s[h];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], o));
+                if (lane == 0)
+                    s_red[0][warp][h] = mx[h];
+            }
+            s_v[tid] = voff;
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < kRowHeads; ++h) {
+                const float mn = fmaxf(fmaxf(fmaxf(s_red[0][0][h], s_red[0][1][h]),
+                                             fmaxf(s_red[0][2][h], s_red[0][3][h])), m[h]);
+                const float alpha = mn == -INFINITY ? 1.0f : exp2f(m[h] - mn);
+                const float e = s[h] == -INFINITY ? 0.0f : exp2f(s[h] - mn);
+                s_p[tid][h] = e;
+                float sum = e;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0)
+                    s_red[1][warp][h] = sum;
+                m[h] = mn;
+                l[h] *= alpha;
+                acc[h] *= alpha;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < kRowHeads; ++h)
+                l[h] += s_red[1][0][h] + s_red[1][1][h] + s_red[1][2][h] + s_red[1][3][h];
+            const int last = (int)min((int64_t)kRowThreads, total - v0);
+            for (int i = slice; i < last; i += kSlices) {
+                const int64_t vo = s_v[i];
+                if (vo < 0)
+                    continue;
+                const float x = p.v.fp8 ? attn_e4m3x2_to_f2(p.v.data[vo + dim]).x
+                                        : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p.v.data)[vo + dim] << 16);
+#pragma unroll
+                for (int h = 0; h < kRowHeads; ++h)
+                    acc[h] = fmaf(s_p[i][h], x, acc[h]);
+            }
+            __syncthreads();
+        }
+    }
+    if (kSlices > 1) {   // the dims of the other tokens
+#pragma unroll
+        for (int h = 0; h < kRowHeads; ++h)
+            if (slice > 0)
+                s_p[tid][h] = acc[h];
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kRowHeads; ++h)
+            if (slice == 0)
+                for (int i = 1; i < kSlices; ++i)
+                    acc[h] += s_p[i * D + dim][h];
+    }
+    const float vs = attn_v_scale(p, c);
+    if (slice == 0) {
+#pragma unroll
+        for (int h = 0; h < kRowHeads; ++h)
+            if (h < nh) {
+                const int64_t row = t * p.hq + h0 + h;
+                p.out[row * D + dim] = attn_bf16(l[h] == 0.0f ? 0.0f : acc[h] * (vs / l[h]));
+                if (dim == 0 && p.lse)
+                    p.lse[row] = attn_lse(m[h], l[h]);
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+msa_status fail(msa_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+msa_status fail(msa_status s, const char *fmt, ...)
+{
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    msa_internal_set_detail(buf);
+    return s;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+msa_status check_cfg(const msa_attention_cfg *cfg, int64_t T, bool sparse)
+{
+    msa_internal_set_detail("");
+    if (!cfg)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "cfg is NULL");
+    if (cfg->num_kv_heads < 1 || cfg->num_q_heads < 1)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "%d query heads, %d K/V heads", cfg->num_q_heads, cfg->num_kv_heads);
+    if (cfg->num_q_heads % cfg->num_kv_heads)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "num_q_heads %d is not a multiple of num_kv_heads %d",
+                    cfg->num_q_heads, cfg->num_kv_heads);
+    if (cfg->num_kv_heads > 1024 || cfg->num_q_heads / cfg->num_kv_heads > 128)
+        return fail(MSA_ERR_UNSUPPORTED, "%d K/V heads (1..1024), %d query heads on each (1..128)",
+                    cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads);
+    if (cfg->head_dim != 64 && cfg->head_dim != 128)
+        return fail(MSA_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", cfg->head_dim);
+    if (cfg->page_size <= 0)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "page_size %d", cfg->page_size);
+    if (sparse && (cfg->block_tokens < 32 || cfg->block_tokens > 1024 || cfg->block_tokens % 32))
+        return fail(MSA_ERR_UNSUPPORTED, "block_tokens %d (multiple of 32, 32..1024)", cfg->block_tokens);
+    if (sparse && (cfg->topk < 1 || cfg->topk > 64))
+        return fail(MSA_ERR_UNSUPPORTED, "topk %d (1..64)", cfg->topk);
+    if (!(cfg->softmax_scale > 0.0f) || !std::isfinite(cfg->softmax_scale))
+        return fail(MSA_ERR_INVALID_ARGUMENT, "softmax_scale %g", (double)cfg->softmax_scale);
+    if (cfg->scale_mode != MSA_SCALE_PER_TENSOR && cfg->scale_mode != MSA_SCALE_PER_HEAD)
+        return fail(MSA_ERR_UNSUPPORTED, "scale_mode %d", cfg->scale_mode);
+    if (cfg->reserved[0] || cfg->reserved[1])
+        return fail(MSA_ERR_INVALID_ARGUMENT, "reserved fields must be 0");
+    if (T < 0)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "num_queries %lld", (long long)T);
+    // the kernels' grids: one CTA per query and (a piece of) a K/V head at most
+    const int64_t per = (int64_t)cfg->num_kv_heads * ((cfg->num_q_heads / cfg->num_kv_heads + kRowHeads - 1) / kRowHeads);
+    if (T > (int64_t)0x7fffffff / per)
+        return fail(MSA_ERR_UNSUPPORTED, "num_queries %lld x heads exceeds the grid", (long long)T);
+    return MSA_OK;
+}
+
+// The arguments that both operators have (after check_cfg, num_queries > 0).
+msa_status check_common(const msa_attention_cfg *cfg, const void *q, const int32_t *kv_len,
+                        const int64_t *table_offset, const int32_t *page_table, int64_t page_table_len,
+                        const msa_cache_desc *kc, const msa_cache_desc *vc, const float *scales, const void *out,
+                        const float *lse, const void *workspace, int64_t workspace_bytes, int64_t needed)
+{
+    if (!q || !kv_len || !table_offset || !page_table || !kc || !vc || !out)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (page_table_len <= 0)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "page_table_len %lld", (long long)page_table_len);
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(kv_len, 4) || !aligned(table_offset, 8) ||
+        !aligned(page_table, 4) || !aligned(lse, 4))
+        return fail(MSA_ERR_MISALIGNED, "a buffer is misaligned");
+    msa_status s = msa_internal_check_cache("k_cache", kc, cfg->num_kv_heads, cfg->head_dim, cfg->page_size);
+    if (s == MSA_OK)
+        s = msa_internal_check_cache("v_cache", vc, cfg->num_kv_heads, cfg->head_dim, cfg->page_size);
+    if (s != MSA_OK)
+        return s;
+    if (kc->dtype == MSA_DTYPE_FP8_E4M3 || vc->dtype == MSA_DTYPE_FP8_E4M3) {
+        if (!scales)
+            return fail(MSA_ERR_INVALID_ARGUMENT, "an FP8 cache needs scales");
+        if (!aligned(scales, 4))
+            return fail(MSA_ERR_MISALIGNED, "scales is misaligned");
+    }
+    if (workspace_bytes < needed || (needed > 0 && !workspace))
+        return fail(MSA_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed",
+                    workspace ? (long long)workspace_bytes : 0LL, (long long)needed);
+    if (!aligned(workspace, 16))
+        return fail(MSA_ERR_MISALIGNED, "workspace is misaligned");
+    return MSA_OK;
+}
+
+AttnCache cache_of(const msa_cache_desc *c)
+{
+    AttnCache a;
+    a.data = static_cast<const uint8_t *>(c->data);
+    a.num_pages = c->num_pages;
+    a.stride_page = c->stride_page;
+    a.stride_head = c->stride_head;
+    a.stride_token = c->stride_token;
+    a.fp8 = c->dtype == MSA_DTYPE_FP8_E4M3;
+    return a;
+}
+
+AttnParams params_of(const msa_attention_cfg *cfg, int64_t T, const void *q, const int32_t *kv_len,
+                     const int64_t *table_offset, const int32_t *page_table, int64_t page_table_len,
+                     const msa_cache_desc *kc, const msa_cache_desc *vc, const float *scales, void *out, float *lse)
+{
+    AttnParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const uint16_t *>(q);
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.kv_len = kv_len;
+    p.table_offset = table_offset;
+    p.page_table = page_table;
+    p.page_table_len = page_table_len;
+    p.scales = scales;
+    p.k = cache_of(kc);
+    p.v = cache_of(vc);
+    p.num_queries = T;
+    p.hq = cfg->num_q_heads;
+    p.hkv = cfg->num_kv_heads;
+    p.group = cfg->num_q_heads / cfg->num_kv_heads;
+    p.page_size = cfg->page_size;
+    p.page_shift = -1;
+    for (int sh = 0; sh < 31; ++sh)
+        if ((1 << sh) == cfg->page_size)
+            p.page_shift = sh;
+    p.block_tokens = cfg->block_tokens;
+    p.topk = cfg->topk;
+    p.per_head_scales = cfg->scale_mode == MSA_SCALE_PER_HEAD;
+    p.scale_log2 = cfg->softmax_scale * 1.4426950408889634f;
+    return p;
+}
+
+msa_status launch(const void *fn, const char *what, int64_t grid, int block, int smem, bool pdl, cudaStream_t stream,
+                  void **args)
+{
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof lc);
+    lc.gridDim = dim3((unsigned)grid);
+    lc.blockDim = dim3((unsigned)block);
+    lc.dynamicSmemBytes = (size_t)smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = pdl ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
+    if (e != cudaSuccess)
+        return fail(MSA_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+    return MSA_OK;
+}
+
+msa_status launch_rows(const AttnParams &p, int head_dim, bool pdl, cudaStream_t stream)
+{
+    const int64_t grid = p.num_queries * p.hkv * ((p.group + kRowHeads - 1) / kRowHeads);
+    void *args[] = {const_cast<AttnParams *>(&p)};
+    return launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_rows_kernel<128>)
+                                  : reinterpret_cast<const void *>(&msa_attention_rows_kernel<64>),
+                  "attention kernel", grid, kRowThreads, 0, pdl, stream, args);
+}
+
+int64_t workspace_needed(const msa_attention_cfg *, int64_t, int64_t) { return 0; }
+
+}  // namespace
+
+extern "C" msa_status msa_attention_workspace_bytes(const msa_attention_cfg *cfg, int64_t num_queries,
+                                                    int64_t num_groups, int64_t *bytes)
+{
+    msa_status s = check_cfg(cfg, num_queries, false);
+    if (s != MSA_OK)
+        return s;
+    if (!bytes)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    if (num_groups < 0 || num_groups > kAttnMaxGroups)
+        return fail(MSA_ERR_UNSUPPORTED, "num_groups %lld (0..%d)", (long long)num_groups, kAttnMaxGroups);
+    *bytes = workspace_needed(cfg, num_queries, num_groups);
+    return MSA_OK;
+}
+
+extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg, int64_t num_queries, const void *q,
+                                                   const int32_t *kv_len, const int64_t *table_offset,
+                                                   const int32_t *page_table, int64_t page_table_len,
+                                                   const int32_t *topk_ids, const msa_cache_desc *k_cache,
+                                                   const msa_cache_desc *v_cache, const float *scales, void *out,
+                                                   float *lse, void *workspace, int64_t workspace_bytes,
+                                                   int32_t launch_flags, cudaStream_t stream)
+{
+    msa_status s = check_cfg(cfg, num_queries, true);
+    if (s != MSA_OK)
+        return s;
+    if (launch_flags & ~(MSA_LAUNCH_PDL | MSA_LAUNCH_QUERY_RUNS))
+        return fail(MSA_ERR_INVALID_ARGUMENT, "launch flags 0x%x (MSA_LAUNCH_PDL, MSA_LAUNCH_QUERY_RUNS)", launch_flags);
+    if (num_queries == 0)
+        return MSA_OK;
+    if (!topk_ids)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "topk_ids is NULL");
+    if (!aligned(topk_ids, 4))
+        return fail(MSA_ERR_MISALIGNED, "topk_ids is misaligned");
+    s = check_common(cfg, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache, scales, out, lse,
+                     workspace, workspace_bytes, workspace_needed(cfg, num_queries, 0));
+    if (s != MSA_OK)
+        return s;
+    AttnParams p = params_of(cfg, num_queries, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache,
+                             scales, out, lse);
+    p.topk_ids = topk_ids;
+    return launch_rows(p, cfg->head_dim, launch_flags & MSA_LAUNCH_PDL, stream);
+}
+
+extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg, int64_t num_queries, const void *q,
+                                                   int64_t num_groups, const int32_t *group_start,
+                                                   const int32_t *prefix_len, const int64_t *prefix_offset,
+                                                   const int32_t *kv_len, const int64_t *table_offset,
+                                                   const int32_t *page_table, int64_t page_table_len,
+                                                   const msa_cache_desc *k_cache, const msa_cache_desc *v_cache,
+                                                   const float *scales, void *out, float *lse, void *workspace,
+                                                   int64_t workspace_bytes, int32_t launch_flags, cudaStream_t stream)
+{
+    msa_status s = check_cfg(cfg, num_queries, false);
+    if (s != MSA_OK)
+        return s;
+    if (launch_flags & ~MSA_LAUNCH_PDL)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "launch flags 0x%x (MSA_LAUNCH_PDL)", launch_flags);
+    if (num_groups < 0 || num_groups > kAttnMaxGroups)
+        return fail(MSA_ERR_UNSUPPORTED, "num_groups %lld (0..%d)", (long long)num_groups, kAttnMaxGroups);
+    if (num_queries == 0)
+        return MSA_OK;
+    if (num_groups > 0 && (!group_start || !prefix_len || !prefix_offset))
+        return fail(MSA_ERR_INVALID_ARGUMENT, "a group array is NULL");
+    if (!aligned(group_start, 4) || !aligned(prefix_len, 4) || !aligned(prefix_offset, 8))
+        return fail(MSA_ERR_MISALIGNED, "a group array is misaligned");
+    s = check_common(cfg, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache, scales, out, lse,
+                     workspace, workspace_bytes, workspace_needed(cfg, num_queries, num_groups));
+    if (s != MSA_OK)
+        return s;
+    AttnParams p = params_of(cfg, num_queries, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache,
+                             scales, out, lse);
+    p.group_start = group_start;
+    p.prefix_len = prefix_len;
+    p.prefix_offset = prefix_offset;
+    p.num_groups = (int32_t)num_groups;
+    return launch_rows(p, cfg->head_dim, launch_flags & MSA_LAUNCH_PDL, stream);
+}

@@ -1,0 +1,99 @@
+// Shared by the translation units of the attention operators (not exported).
+#pragma once
+
+#include "msa_attention.h"
+#include "msa_internal.h"
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+constexpr int kAttnMaxGroups = 1024;
+
+// One cache as the kernels see it; strides in elements.
+struct AttnCache {
+    const uint8_t *data;
+    int64_t num_pages;
+    int64_t stride_page, stride_head, stride_token;
+    int32_t fp8;
+};
+
+struct AttnParams {
+    const uint16_t *q;               // [T, Hq, D] bf16
+    uint16_t *out;                   // [T, Hq, D] bf16
+    float *lse;                      // [T, Hq] or nullptr
+    const int32_t *kv_len;
+    const int64_t *table_offset;
+    const int32_t *page_table;
+    int64_t page_table_len;
+    const int32_t *topk_ids;         // [T, topk]; nullptr: dense (prefix attention)
+    const int32_t *group_start;      // [num_groups + 1]
+    const int32_t *prefix_len;
+    const int64_t *prefix_offset;
+    const float *scales;
+    AttnCache k, v;
+    int64_t num_queries;
+    int32_t num_groups;
+    int32_t hq, hkv, group;          // heads; group = hq / hkv
+    int32_t page_size;
+    int32_t page_shift;              // log2(page_size) when a power of two, else -1
+    int32_t block_tokens, topk;
+    int32_t per_head_scales;
+    float scale_log2;                // softmax_scale * log2(e): scores are kept as powers of two
+};
+
+#ifdef __CUDACC__
+
+// Dequantisation scales of K/V head c (1 for bf16 caches).
+__device__ __forceinline__ float attn_k_scale(const AttnParams &p, int c)
+{
+    return p.k.fp8 ? __ldg(p.scales + (p.per_head_scales ? c : 0)) : 1.0f;
+}
+
+__device__ __forceinline__ float attn_v_scale(const AttnParams &p, int c)
+{
+    return p.v.fp8 ? __ldg(p.scales + (p.per_head_scales ? p.hkv + c : 1)) : 1.0f;
+}
+
+// The page of token j of the history whose table row starts at `off`, or -1.
+__device__ __forceinline__ int32_t attn_page(const AttnParams &p, int64_t off, int64_t j)
+{
+    const int64_t blk = p.page_shift >= 0 ? (j >> p.page_shift) : j / p.page_size;
+    const int64_t i = off + blk;
+    if (i < 0 || i >= p.page_table_len)
+        return -1;
+    const int32_t pg = __ldg(p.page_table + i);
+    return (pg >= 0 && (int64_t)pg < p.k.num_pages && (int64_t)pg < p.v.num_pages) ? pg : -1;
+}
+
+__device__ __forceinline__ int32_t attn_page_row(const AttnParams &p, int64_t j)
+{
+    return (int32_t)(p.page_shift >= 0 ? (j & (p.page_size - 1)) : j % p.page_size);
+}
+
+// two E4M3 codes -> (low code, high code)
+__device__ __forceinline__ float2 attn_e4m3x2_to_f2(uint32_t codes)
+{
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)codes));
+    float lo, hi;
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h; }"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h2));
+    return make_float2(lo, hi);
+}
+
+__device__ __forceinline__ uint16_t attn_bf16(float x)
+{
+    uint16_t r;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+    return r;
+}
+
+// ln of the sum, from the maximum (of the scores times log2 e) and the sum relative to it
+__device__ __forceinline__ float attn_lse(float m, float l)
+{
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+#endif

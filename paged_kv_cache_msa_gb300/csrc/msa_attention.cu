@@ -341,8 +341,124 @@ AttnParams params_of(const msa_attention_cfg *cfg, int64_t T, const void *q, con
     return p;
 }
 
-msa_status launch(const void *fn, const char *what, int64_t grid, int block, int smem, bool pdl, cudaStream_t stream,
-                  void **args)
+msa_status launched(cudaError_t e)
+{
+    return e == cudaSuccess ? MSA_OK : fail(MSA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+}
+
+msa_status launch_rows(const AttnParams &p, int head_dim, bool pdl, cudaStream_t stream)
+{
+    const int64_t grid = p.num_queries * p.hkv * ((p.group + kRowHeads - 1) / kRowHeads);
+    void *args[] = {const_cast<AttnParams *>(&p)};
+    return launched(attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_rows_kernel<128>)
+                                                : reinterpret_cast<const void *>(&msa_attention_rows_kernel<64>),
+                                grid, kRowThreads, 0, pdl, stream, args));
+}
+
+// Workspace: the window's prefix sums, then its pieces.
+constexpr int64_t kPreBytes = (kAttnWindow + 1) * 8 + 248;   // a multiple of 256
+static_assert(kPreBytes % 256 == 0, "alignment of the pieces");
+
+int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t)
+{
+    if (T == 0)
+        return 0;
+    const int64_t nh = attn_decode_heads(cfg->num_q_heads / cfg->num_kv_heads);
+    return kPreBytes + 2 * (int64_t)kAttnMaxCtas * nh * (cfg->head_dim + 2) * 4;
+}
+
+// Rows of the widest TMA box that never crosses a page or a selected block: a power of two.
+int box_rows(const AttnParams &p)
+{
+    int br = 128;
+    while (br > 1 && (p.page_size % br || (p.topk_ids && p.block_tokens % br)))
+        br /= 2;
+    return br;
+}
+
+// A cache as a map of (dims, rows of a page, heads, pages), boxes of `rows` rows and at
+// most 128 bytes.  False when TMA cannot take the layout.
+bool encode_cache(CUtensorMap *m, const AttnCache &c, int head_dim, int heads, int page_size, int rows)
+{
+    const int es = c.fp8 ? 1 : 2;
+    const int width = head_dim * es < 128 ? head_dim * es : 128;
+    int64_t st = c.stride_token * es, sh = c.stride_head * es, sp = c.stride_page * es;
+    // the stride of a dimension of one entry is never used
+    if (heads == 1)
+        sh = 16;
+    if (c.num_pages == 1)
+        sp = 16;
+    const int64_t limit = (int64_t)1 << 40;
+    if (st % 16 || sh % 16 || sp % 16 || st <= 0 || sh <= 0 || sp <= 0 || st >= limit || sh >= limit || sp >= limit ||
+        c.num_pages < 1 || c.num_pages >= 0x7fffffff)
+        return false;
+    const int64_t dims[4] = {head_dim, page_size, heads, c.num_pages};
+    const int64_t strides[3] = {st, sh, sp};
+    const int32_t box[4] = {width / es, rows, 1, 1};
+    return msa_internal_encode_tiled(m, c.data, es, 4, dims, strides, box, width);
+}
+
+// The current device's SMs, 0 when it has no tcgen05 tensor cores or cannot be asked.
+int tensor_sms()
+{
+    int dev = 0, major = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || major != 10)
+        return 0;
+    return sms;
+}
+
+// What the tensor-core kernels need to know of the caches; box_rows 0 when they do not
+// take the layout: caches of one dtype whose strides are multiples of 16 bytes, pages
+// (and blocks) a multiple of 8 tokens.  Fewer rows a box would mean more than 16 copies
+// a tile.
+struct Maps {
+    alignas(64) CUtensorMap k, v;
+    int box_rows, sms;
+    int32_t oob_page;
+};
+
+void make_maps(Maps *m, const AttnParams &p, int head_dim)
+{
+    memset(m, 0, sizeof *m);
+    m->sms = tensor_sms();
+    const int br = box_rows(p);
+    if (m->sms == 0 || br < 8 || p.k.fp8 != p.v.fp8 || !encode_cache(&m->k, p.k, head_dim, p.hkv, p.page_size, br) ||
+        !encode_cache(&m->v, p.v, head_dim, p.hkv, p.page_size, br))
+        return;
+    m->box_rows = br;
+    m->oob_page = (int32_t)(p.k.num_pages > p.v.num_pages ? p.k.num_pages : p.v.num_pages);
+}
+
+// Single queries: windows of kAttnWindow queries, each the decode kernel and the join.
+msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void *workspace, bool pdl,
+                      cudaStream_t stream)
+{
+    AttnPieces w;
+    memset(&w, 0, sizeof w);
+    w.pre = static_cast<int64_t *>(workspace);
+    w.pieces = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kPreBytes);
+    w.heads = attn_decode_heads(p.group);
+    w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
+    w.ctas = maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas;
+    w.box_rows = maps.box_rows;
+    w.oob_page = maps.oob_page;
+    for (int64_t q0 = 0; q0 < p.num_queries; q0 += kAttnWindow) {
+        w.q0 = q0;
+        w.nq = p.num_queries - q0 < kAttnWindow ? p.num_queries - q0 : kAttnWindow;
+        msa_status s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, pdl || q0 > 0, stream));
+        if (s == MSA_OK)
+            s = launched(attn_join(p, w, head_dim, stream));
+        if (s != MSA_OK)
+            return s;
+    }
+    return MSA_OK;
+}
+
+}  // namespace
+
+cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, bool pdl, cudaStream_t stream, void **args)
 {
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
@@ -355,24 +471,8 @@ msa_status launch(const void *fn, const char *what, int64_t grid, int block, int
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = pdl ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
-    if (e != cudaSuccess)
-        return fail(MSA_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
-    return MSA_OK;
+    return cudaLaunchKernelExC(&lc, fn, args);
 }
-
-msa_status launch_rows(const AttnParams &p, int head_dim, bool pdl, cudaStream_t stream)
-{
-    const int64_t grid = p.num_queries * p.hkv * ((p.group + kRowHeads - 1) / kRowHeads);
-    void *args[] = {const_cast<AttnParams *>(&p)};
-    return launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_rows_kernel<128>)
-                                  : reinterpret_cast<const void *>(&msa_attention_rows_kernel<64>),
-                  "attention kernel", grid, kRowThreads, 0, pdl, stream, args);
-}
-
-int64_t workspace_needed(const msa_attention_cfg *, int64_t, int64_t) { return 0; }
-
-}  // namespace
 
 extern "C" msa_status msa_attention_workspace_bytes(const msa_attention_cfg *cfg, int64_t num_queries,
                                                     int64_t num_groups, int64_t *bytes)
@@ -414,7 +514,12 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
     AttnParams p = params_of(cfg, num_queries, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache,
                              scales, out, lse);
     p.topk_ids = topk_ids;
-    return launch_rows(p, cfg->head_dim, launch_flags & MSA_LAUNCH_PDL, stream);
+    const bool pdl = launch_flags & MSA_LAUNCH_PDL;
+    Maps maps;
+    make_maps(&maps, p, cfg->head_dim);
+    if (maps.box_rows == 0)
+        return launch_rows(p, cfg->head_dim, pdl, stream);
+    return run_decode(p, maps, cfg->head_dim, workspace, pdl, stream);
 }
 
 extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg, int64_t num_queries, const void *q,
@@ -449,5 +554,10 @@ extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg,
     p.prefix_len = prefix_len;
     p.prefix_offset = prefix_offset;
     p.num_groups = (int32_t)num_groups;
-    return launch_rows(p, cfg->head_dim, launch_flags & MSA_LAUNCH_PDL, stream);
+    const bool pdl = launch_flags & MSA_LAUNCH_PDL;
+    Maps maps;
+    make_maps(&maps, p, cfg->head_dim);
+    if (maps.box_rows == 0 || num_groups > 0)
+        return launch_rows(p, cfg->head_dim, pdl, stream);
+    return run_decode(p, maps, cfg->head_dim, workspace, pdl, stream);
 }

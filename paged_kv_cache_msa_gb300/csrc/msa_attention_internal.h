@@ -9,6 +9,8 @@
 #include <cstdint>
 
 constexpr int kAttnMaxGroups = 1024;
+constexpr int kAttnWindow = 512;     // queries a launch of the tensor-core decode kernel takes
+constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
 
 // One cache as the kernels see it; strides in elements.
 struct AttnCache {
@@ -41,6 +43,32 @@ struct AttnParams {
     int32_t per_head_scales;
     float scale_log2;                // softmax_scale * log2(e): scores are kept as powers of two
 };
+
+// What the decode and join kernels need beside AttnParams: a window of queries and its
+// part of the workspace.  CTA i holds the items [total * i / ctas, total * (i + 1) / ctas)
+// of the list over (query, head chunk, tile); the piece of a (query, head chunk) that
+// began in another CTA is in slot i, of one that goes on in the next in slot ctas + i, and
+// (joined) a whole one in slot 2 * ctas + query * head_chunks + head chunk.  A piece is
+// [heads][D] of output (relative to the maximum), then the maxima, then the sums.
+struct AttnPieces {
+    int64_t *pre;                    // [nq + 1]: tiles before each query of the window
+    float *pieces;
+    int64_t q0, nq;                  // the window
+    int32_t heads;                   // query heads of a head chunk: 8 or 16
+    int32_t head_chunks;             // of all K/V heads
+    int32_t ctas;
+    int32_t box_rows;                // rows of a TMA box
+    int32_t oob_page;                // a page past both caches
+    int32_t joined;                  // every piece goes to the workspace
+};
+
+// One launch; `pdl` with programmatic dependent launch.
+cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, bool pdl, cudaStream_t stream, void **args);
+
+int attn_decode_heads(int group);
+cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
+                        const CUtensorMap &vmap, bool pdl, cudaStream_t stream);
+cudaError_t attn_join(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream);
 
 #ifdef __CUDACC__
 

@@ -55,3 +55,9 @@ msa_status msa_internal_projection_violations(uint64_t *count, int32_t reset);
 // swizzle.  False when the driver's encoder is unavailable or rejects the layout.
 bool msa_internal_encode_byte_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t stride_bytes,
                                    int box_rows);
+
+// A TMA tensor map of up to four dimensions over elements of elem_size bytes (1 or 2),
+// strides[i] in bytes between entries of dimension i + 1, swizzled by swizzle_bytes (64 or
+// 128, the box's inner bytes); elements outside it read as zero.  False as above.
+bool msa_internal_encode_tiled(CUtensorMap *m, const void *base, int elem_size, int rank, const int64_t *dims,
+                               const int64_t *strides, const int32_t *box, int swizzle_bytes);

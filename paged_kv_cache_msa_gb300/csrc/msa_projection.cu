@@ -1679,6 +1679,26 @@ bool msa_internal_encode_byte_rows(CUtensorMap *m, const void *base, int64_t row
     return encode_map(m, base, rows, kBKBytes, stride_bytes, box_rows, 1);
 }
 
+bool msa_internal_encode_tiled(CUtensorMap *m, const void *base, int elem_size, int rank, const int64_t *dims,
+                               const int64_t *strides, const int32_t *box, int swizzle_bytes)
+{
+    EncodeTiledFn enc = encoder();
+    if (!enc || rank < 1 || rank > 4)
+        return false;
+    cuuint64_t d[4] = {}, st[4] = {};
+    cuuint32_t b[4] = {}, one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = (cuuint64_t)dims[i];
+        b[i] = (cuuint32_t)box[i];
+        if (i + 1 < rank)
+            st[i] = (cuuint64_t)strides[i];
+    }
+    return enc(m, elem_size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
+               const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" msa_status msa_projection_validate(
     const msa_producer_cfg *cfg, int64_t num_tokens, const void *hidden, int64_t hidden_size,
     int64_t hidden_row_stride, const void *weight, int64_t weight_row_stride,

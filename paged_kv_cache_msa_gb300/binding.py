@@ -378,7 +378,7 @@ def msa_sparse_attention_forward(cfg, num_queries, q, kv_len, table_offset, page
                                  check=True) -> int:
     """The C entry point; pointers are integers or None.  Raises MsaError unless the
     call returns MSA_OK (``check=False`` returns the status)."""
-    s = load().msa_sparse_attention_forward(
+    s = (_lib or load()).msa_sparse_attention_forward(
         ctypes.byref(cfg) if cfg is not None else None, int(num_queries), q, kv_len, table_offset,
         page_table, int(page_table_len), topk_ids, _ref(k_cache), _ref(v_cache), scales, out, lse,
         workspace, int(workspace_bytes), int(launch_flags), stream)
@@ -393,7 +393,7 @@ def msa_prefix_attention_forward(cfg, num_queries, q, num_groups, group_start, p
                                  workspace_bytes=0, launch_flags=0, stream=0, check=True) -> int:
     """The C entry point; pointers are integers or None.  Raises MsaError unless the
     call returns MSA_OK (``check=False`` returns the status)."""
-    s = load().msa_prefix_attention_forward(
+    s = (_lib or load()).msa_prefix_attention_forward(
         ctypes.byref(cfg) if cfg is not None else None, int(num_queries), q, int(num_groups),
         group_start, prefix_len, prefix_offset, kv_len, table_offset, page_table,
         int(page_table_len), _ref(k_cache), _ref(v_cache), scales, out, lse, workspace,
@@ -482,57 +482,63 @@ def _tensor(name, t, shape, dtypes, device):
     ``device``; returns its address (None for None)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtypes[0]} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+                         f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, q on {device}")
     return t.data_ptr()
 
 
-def _attention_call(fn, cfg, q, before, kv_len, table_offset, page_table, after, k_cache, v_cache,
-                    scales, out, lse, workspace, num_groups, launch_flags, stream):
+def _attention_call(forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse, workspace,
+                    num_groups, launch_flags, stream):
+    """Checks the tensors both attention operators have and calls ``forward`` with them on
+    q's device; ``tensors(bf16, i32, i64, dev)`` gives the arguments between q and the
+    caches."""
     import torch
-    bf16 = (torch.bfloat16, torch.int16)
-    dev, i32, i64 = q.device, (torch.int32,), (torch.int64,)
+    dev = q.device
     if dev.type != "cuda":
         raise ValueError(f"q is on {dev}; the attention calls take CUDA tensors")
-    T, Hq, D = int(q.shape[0]), cfg.num_q_heads, cfg.head_dim
-    ns = 2 * cfg.num_kv_heads if cfg.scale_mode == MSA_SCALE_PER_HEAD else 2
-    if scales is not None and (scales.dim() != 1 or scales.numel() < ns):
-        raise ValueError(f"scales: expected at least {ns} values, got shape {tuple(scales.shape)}")
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        if workspace is None:
-            n = msa_attention_workspace_bytes(cfg, T, num_groups)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        args = ([_tensor("q", q, (T, Hq, D), bf16, dev)] + before(dev)
-                + [_tensor("kv_len", kv_len, (T,), i32, dev),
-                   _tensor("table_offset", table_offset, (T,), i64, dev),
-                   _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel()]
-                + after(dev)
-                + [k_cache, v_cache,
-                   _tensor("scales", scales, () if scales is None else scales.shape, (torch.float32,), dev),
-                   _tensor("out", out, (T, Hq, D), bf16, dev),
-                   _tensor("lse", lse, (T, Hq), (torch.float32,), dev),
-                   workspace.data_ptr() or None, workspace.numel() * workspace.element_size()])
-        fn(cfg, T, *args, launch_flags, stream.cuda_stream)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _attention_call(forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse,
+                                   workspace, num_groups, launch_flags, stream)
+    bf16, i32, i64, f32 = (torch.bfloat16, torch.int16), (torch.int32,), (torch.int64,), (torch.float32,)
+    rows = (q.shape[0], cfg.num_q_heads, cfg.head_dim)
+    if scales is not None:
+        ns = 2 * cfg.num_kv_heads if cfg.scale_mode == MSA_SCALE_PER_HEAD else 2
+        if scales.dim() != 1 or scales.shape[0] < ns:
+            raise ValueError(f"scales: expected at least {ns} values, got shape {tuple(scales.shape)}")
+        scales = _tensor("scales", scales, scales.shape, f32, dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if workspace is None:
+        n = msa_attention_workspace_bytes(cfg, rows[0], num_groups)
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}, got one on {workspace.device}")
+    forward(cfg, rows[0], _tensor("q", q, rows, bf16, dev), *tensors(i32, i64, dev), k_cache, v_cache,
+            scales, _tensor("out", out, rows, bf16, dev), _tensor("lse", lse, rows[:2], f32, dev),
+            workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), launch_flags,
+            stream.cuda_stream)
 
 
 def sparse_attention_tensors(cfg: MsaAttentionCfg, q, topk_ids, kv_len, table_offset, page_table,
                              k_cache, v_cache, scales, out, lse=None, workspace=None,
                              launch_flags=0, stream=None) -> None:
     """msa_sparse_attention_forward on contiguous torch CUDA tensors (caches are
-    MsaCacheDesc).  ``workspace``: a uint8 tensor of at least
+    MsaCacheDesc).  ``workspace``: a tensor of at least
     ``msa_attention_workspace_bytes(cfg, T)`` bytes, or None to allocate one.  Runs on
     ``stream`` or the current stream of q's device."""
-    import torch
-    _attention_call(msa_sparse_attention_forward, cfg, q, lambda dev: [], kv_len, table_offset,
-                    page_table,
-                    lambda dev: [_tensor("topk_ids", topk_ids, (q.shape[0], cfg.topk), (torch.int32,), dev)],
-                    k_cache, v_cache, scales, out, lse, workspace, 0, launch_flags, stream)
+    def tensors(i32, i64, dev):
+        T = (q.shape[0],)
+        return (_tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
+                _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel(),
+                _tensor("topk_ids", topk_ids, (T[0], cfg.topk), i32, dev))
+
+    _attention_call(msa_sparse_attention_forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse,
+                    workspace, 0, launch_flags, stream)
 
 
 def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, prefix_offset, kv_len,
@@ -541,14 +547,15 @@ def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, p
     """msa_prefix_attention_forward on contiguous torch CUDA tensors; the three group
     tensors are None when no prefix is shared.  ``workspace`` and ``stream`` as for
     ``sparse_attention_tensors`` (the bytes also depend on the number of groups)."""
-    import torch
-    n = 0 if prefix_len is None else int(prefix_len.shape[0])
+    n = 0 if prefix_len is None else prefix_len.shape[0]
 
-    def groups(dev):
-        return [n, _tensor("group_start", group_start, (n + 1,), (torch.int32,), dev),
-                _tensor("prefix_len", prefix_len, (n,), (torch.int32,), dev),
-                _tensor("prefix_offset", prefix_offset, (n,), (torch.int64,), dev)]
+    def tensors(i32, i64, dev):
+        T = (q.shape[0],)
+        return (n, _tensor("group_start", group_start, (n + 1,), i32, dev),
+                _tensor("prefix_len", prefix_len, (n,), i32, dev),
+                _tensor("prefix_offset", prefix_offset, (n,), i64, dev),
+                _tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
+                _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel())
 
-    _attention_call(msa_prefix_attention_forward, cfg, q, groups, kv_len, table_offset, page_table,
-                    lambda dev: [], k_cache, v_cache, scales, out, lse, workspace, n, launch_flags,
-                    stream)
+    _attention_call(msa_prefix_attention_forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse,
+                    workspace, n, launch_flags, stream)

@@ -5,6 +5,7 @@
 
 #include "msa_attention_internal.h"
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -355,8 +356,9 @@ msa_status launch_rows(const AttnParams &p, int head_dim, bool pdl, cudaStream_t
                                 grid, kRowThreads, 0, pdl, stream, args));
 }
 
-// Workspace: the window's prefix sums, then its pieces.
-constexpr int64_t kPreBytes = (kAttnWindow + 1) * 8 + 248;   // a multiple of 256
+// Workspace: the cuts, the total, the window's prefix sums, then its pieces.
+constexpr int64_t kCutBytes = kAttnMaxCtas * 16;
+constexpr int64_t kPreBytes = kCutBytes + 256 + (kAttnWindow + 1) * 8 + 248;
 static_assert(kPreBytes % 256 == 0, "alignment of the pieces");
 
 int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t)
@@ -401,11 +403,18 @@ bool encode_cache(CUtensorMap *m, const AttnCache &c, int head_dim, int heads, i
 // The current device's SMs, 0 when it has no tcgen05 tensor cores or cannot be asked.
 int tensor_sms()
 {
+    static std::atomic<int> known[64];     // SMs + 1 of each device, once asked
     int dev = 0, major = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || major != 10)
+    if (cudaGetDevice(&dev) != cudaSuccess)
         return 0;
+    if (dev < 64 && known[dev].load(std::memory_order_relaxed))
+        return known[dev].load(std::memory_order_relaxed) - 1;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    sms = major == 10 ? sms : 0;
+    if (dev < 64)
+        known[dev].store(sms + 1, std::memory_order_relaxed);
     return sms;
 }
 
@@ -437,8 +446,11 @@ msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void 
 {
     AttnPieces w;
     memset(&w, 0, sizeof w);
-    w.pre = static_cast<int64_t *>(workspace);
-    w.pieces = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kPreBytes);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    w.cut = reinterpret_cast<int4 *>(ws);
+    w.total = reinterpret_cast<int64_t *>(ws + kCutBytes);
+    w.pre = reinterpret_cast<int64_t *>(ws + kCutBytes + 256);
+    w.pieces = reinterpret_cast<float *>(ws + kPreBytes);
     w.heads = attn_decode_heads(p.group);
     w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
     w.ctas = maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas;
@@ -449,7 +461,7 @@ msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void 
         w.nq = p.num_queries - q0 < kAttnWindow ? p.num_queries - q0 : kAttnWindow;
         msa_status s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, pdl || q0 > 0, stream));
         if (s == MSA_OK)
-            s = launched(attn_join(p, w, head_dim, stream));
+            s = launched(attn_join_cut(p, w, head_dim, stream));
         if (s != MSA_OK)
             return s;
     }

@@ -15,29 +15,40 @@
 // run on kind::f8f6f4 with Q and P split into E4M3 halves hi | lo side by side in the
 // columns, so that a tile is still read once from shared memory; bf16 on kind::f16.
 //
-// Up to kChunk tiles of one (query, K/V head) form a chunk: all of their scores are held
-// in tensor memory, so that the maximum is reduced over the 128 threads once a chunk, and
-// their value products accumulate in one tensor-memory tile.  The key tiles of the next
-// chunk are copied and multiplied before the value tiles of the current one, which keeps
-// the copies going while the softmax runs.
-//   warp 0    TMA: page lookups and tile copies into a ring of stages
-//   warp 1    query tiles, one (query, K/V head) ahead
-//   warp 2    MMAs; zeroes value rows past the history before they are multiplied
-//   warps 4-7 softmax and output: a thread is a token of each tile, then a dim
+// Up to kChunk tiles of one (query, K/V head) form a chunk, whose scores are held in
+// tensor memory together, so that the maximum is reduced over the 128 threads once a
+// chunk, and whose value products accumulate in one tensor-memory tile.  Keys are
+// copied and multiplied ahead of the values, and successive (query, K/V head)s go to
+// kGroups softmax groups in turn, so that neither the copies nor the MMAs wait for one
+// softmax: short histories make chunks of one tile, whose
+// softmax (about 1 us of latency) is longer than their copies (0.7 us).
+//   warps 0, 1 TMA: key tiles, value tiles, each into a ring of stages
+//   warps 2, 3 MMAs of the scores, of the values (one MMA costs its warp about 85 cycles of
+//              issue, a tile 8 of them, close to the tile's share of HBM time: two warps);
+//              warp 3 zeroes value rows past the history before they are multiplied
+//   warp 4     block lists and page lookups
+//   warp 5     query tiles, ahead of their use; queries that see nothing
+//   warps 8-15 two softmax and output groups: a thread is a token of each tile, then a dim
 // A (query, K/V head) that one CTA holds whole is written as bf16 right away; the pieces
 // of one that is cut between CTAs (at most two a CTA) go to the workspace, and a second,
-// dependent kernel joins them, together with the pieces of a shared prefix.
+// dependent kernel joins them.
 
 #include "msa_attention_internal.h"
 #include "msa_tcgen05.cuh"
 
 #include <cstring>
+#include <type_traits>
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kInfo = 4;          // chunks whose box lists are held
-constexpr int kQSlots = 3;
+constexpr int kGroups = 2;        // softmax groups
+constexpr int kThreads = 256 + 128 * kGroups;
+// Score buffers and box lists belong to a group, in turn: a group that waits on a barrier
+// has then waited on every phase before, as waiting by parity needs.
+constexpr int kGroupBufs = 3, kSBufs = kGroups * kGroupBufs;
+constexpr int kGroupInfo = 4, kInfo = kGroups * kGroupInfo;
+constexpr int kQSlots = 2 * kGroups;   // a multiple of the groups: a slot belongs to one
+constexpr int kSmallIds = 1024;   // ids of a window kept in shared memory
 constexpr int kMaxBoxes = 16;     // boxes of a tile: 128 / 8 rows
 
 template <int D, bool FP8, int NH>
@@ -47,17 +58,25 @@ struct Shape {
     static constexpr int kAtoms = kRowBytes / kSwz;                      // boxes side by side in a row
     static constexpr int kTileBytes = 128 * kRowBytes;
     static constexpr int kN = FP8 ? 2 * NH : 16;                         // MMA columns: hi | lo, or at least 16
-    static constexpr int kChunk = NH == 8 ? 8 : 4;                       // 64 scores a thread
-    static constexpr int kPBytes = 128 * kN * (FP8 ? 1 : 2);             // weights of one tile
+    static constexpr int kChunk = kN == 16 ? 4 : 2;                      // 64 columns of scores
+    // Weights of one tile: [token][16 bytes] pieces of the columns.  bf16 weights of 8 heads
+    // are the first piece alone, taken twice for the 16 columns.
+    static constexpr int kPBytes = 128 * (FP8 ? kN : NH * 2);
     static constexpr int kQBytes = kN * kRowBytes;
-    static constexpr int kRest = 1024 + kChunk * kPBytes + kQSlots * kQBytes;
-    static constexpr int kStages = (210 * 1024 - kRest) / kTileBytes;    // what the lists below leave of 227 KB
-    static constexpr int kSmem = kRest + kStages * kTileBytes;
+    static constexpr int kRest = 1024 + kGroups * kChunk * kPBytes + kQSlots * kQBytes;
+    static constexpr int kStages = (207 * 1024 - kRest) / kTileBytes / 2;   // of each ring, in what the lists leave
+    static constexpr int kSmem = kRest + 2 * kStages * kTileBytes;
     static constexpr int kSCols = kChunk * kN;                           // columns of one chunk's scores
     static constexpr int kTmem = 512;
-    static_assert(2 * kSCols + kN <= kTmem, "tensor memory");
+    static_assert(kSBufs * kSCols + kGroups * kN <= kTmem, "tensor memory");
     static_assert(kQBytes % 1024 == 0 && (kChunk * kPBytes) % 1024 == 0, "swizzle pattern alignment");
 };
+
+// a / b for a >= 0, b > 0, in 32 bits where both fit
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
+{
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // A chunk: tiles [tile, tile + n) of (query q, head chunk hc), item `it` of the CTA's share.
 struct Walk {
@@ -72,7 +91,7 @@ struct Walk {
         if (it < end) {
             const int64_t base = pre[q] * hcs;
             nt = (int32_t)(pre[q + 1] - pre[q]);
-            hc = (int)((it - base) / nt);
+            hc = (int)div64(it - base, nt);
             tile = (int32_t)((it - base) - (int64_t)hc * nt);
         }
     }
@@ -82,6 +101,7 @@ struct Walk {
         const int64_t a = min((int64_t)(nt - tile), end - it);
         return (int)min((int64_t)chunk, a);
     }
+    __device__ bool last(int n) const { return tile + n == nt || it + n == end; }   // of its segment
     __device__ void step(int n)
     {
         it += n;
@@ -97,6 +117,32 @@ struct Walk {
                     nt = (int32_t)(pre[q + 1] - pre[q]);
             }
         }
+    }
+};
+
+// The group of each segment and, in it, the number of the chunk: every role counts alike.
+struct Turn {
+    uint32_t seg = 0, count[kGroups] = {};
+
+    __device__ int group() const { return (int)(seg % kGroups); }
+    __device__ uint32_t chunk() const
+    {
+        uint32_t k = count[0];
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i)
+            k = group() == i ? count[i] : k;
+        return k;
+    }
+    __device__ int info() const { return group() * kGroupInfo + (int)(chunk() % kGroupInfo); }
+    __device__ uint32_t info_phase() const { return (chunk() / kGroupInfo) & 1u; }
+    __device__ int buf() const { return group() * kGroupBufs + (int)(chunk() % kGroupBufs); }
+    __device__ uint32_t buf_phase() const { return (chunk() / kGroupBufs) & 1u; }
+    __device__ void step(bool last)
+    {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+            count[i] += group() == i;
+        seg += last;
     }
 };
 
@@ -139,27 +185,29 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     using S = Shape<D, FP8, NH>;
     constexpr int ST = S::kStages, N = S::kN, CH = S::kChunk;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_full[ST], bar_empty[ST];
+    __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
     __shared__ __align__(8) uint64_t bar_info_full[kInfo], bar_info_empty[kInfo];
     __shared__ __align__(8) uint64_t bar_q_full[kQSlots], bar_q_empty[kQSlots];
-    __shared__ __align__(8) uint64_t bar_s_full[2], bar_s_empty[2];
-    __shared__ __align__(8) uint64_t bar_p_full, bar_o_full, bar_drain;
+    __shared__ __align__(8) uint64_t bar_s_full[kSBufs], bar_s_empty[kSBufs];
+    __shared__ __align__(8) uint64_t bar_p_full[kGroups], bar_o_full[kGroups], bar_drain;
     __shared__ int64_t s_pre[kAttnWindow + 1];
     __shared__ int64_t s_toff[kAttnWindow];
     __shared__ int32_t s_len[kAttnWindow];
+    __shared__ int32_t s_cnt[kAttnWindow];             // ids that name a block
+    __shared__ int32_t s_ids[kSmallIds];               // of a small batch
     __shared__ int64_t s_wsum[kThreads / 32];
     __shared__ int2 s_box[kInfo][CH][kMaxBoxes];       // row in the page, page
     __shared__ uint8_t s_nv[kInfo][CH][kMaxBoxes];     // visible rows of the box
-    __shared__ int32_t s_list[64];                     // block ids of the loader's query
+    __shared__ int32_t s_list[64];                     // block ids of the list warp's query
     __shared__ float s_qinv[kQSlots];
-    __shared__ float s_red[4][16];
+    __shared__ float s_red[kGroups][4][16];
     __shared__ int s_qlo;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t pbase = ring + (uint32_t)(ST * S::kTileBytes);
-    const uint32_t qbase = pbase + (uint32_t)(CH * S::kPBytes);
+    const uint32_t pbase = ring + (uint32_t)(2 * ST * S::kTileBytes);     // key stages, value stages
+    const uint32_t qbase = pbase + (uint32_t)(kGroups * CH * S::kPBytes);
     volatile int *abort_flag = &s_abort;
     const int nq = (int)w.nq;
 
@@ -167,24 +215,28 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
         for (int i = 0; i < ST; ++i) {
-            mbar_init(smem_u32(&bar_full[i]), 1);
-            mbar_init(smem_u32(&bar_empty[i]), 1);
+            mbar_init(smem_u32(&bar_k_full[i]), 1);
+            mbar_init(smem_u32(&bar_k_empty[i]), 1);
+            mbar_init(smem_u32(&bar_v_full[i]), 1);
+            mbar_init(smem_u32(&bar_v_empty[i]), 1);
         }
         for (int i = 0; i < kInfo; ++i) {
             mbar_init(smem_u32(&bar_info_full[i]), 1);
-            mbar_init(smem_u32(&bar_info_empty[i]), 5);    // the MMA warp and the softmax warps
+            mbar_init(smem_u32(&bar_info_empty[i]), 7);    // the copy warps, the value MMAs, a group
         }
         for (int i = 0; i < kQSlots; ++i) {
             mbar_init(smem_u32(&bar_q_full[i]), 1);
-            mbar_init(smem_u32(&bar_q_empty[i]), 5);       // the MMAs and the softmax warps
+            mbar_init(smem_u32(&bar_q_empty[i]), 5);       // the MMAs and a softmax group
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kSBufs; ++i) {
             mbar_init(smem_u32(&bar_s_full[i]), 1);
             mbar_init(smem_u32(&bar_s_empty[i]), 4);
         }
-        mbar_init(smem_u32(&bar_p_full), 4);
-        mbar_init(smem_u32(&bar_o_full), 1);
-        mbar_init(smem_u32(&bar_drain), 1);
+        for (int i = 0; i < kGroups; ++i) {
+            mbar_init(smem_u32(&bar_p_full[i]), 4);
+            mbar_init(smem_u32(&bar_o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&bar_drain), 2);
         s_abort = 0;
         s_qlo = 0;
         s_pre[0] = 0;
@@ -195,33 +247,47 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
 
-    // tiles of each query, and their prefix sums: thread t holds queries 2t and 2t + 1
-    constexpr int kPer = kAttnWindow / kThreads;
-    int64_t mine[kPer], sum = 0;
+    // Tiles of each query and their prefix sums, a query a thread.  Lengths, table offsets
+    // and the first ids are read in one round of loads; the ids of small batches stay in
+    // shared memory for the lists.
+    static_assert(kAttnWindow <= kThreads, "a thread holds one query");
+    const int32_t len = tid < nq ? max(__ldg(p.kv_len + w.q0 + tid), 0) : 0;
+    if (tid < nq) {
+        s_toff[tid] = __ldg(p.table_offset + w.q0 + tid);
+        s_len[tid] = len;
+        s_cnt[tid] = 0;
+    }
+    if (p.topk_ids) {
+        constexpr int kBatch = 4;
+        const int ids = nq * p.topk;
+        const int32_t *src = p.topk_ids + w.q0 * p.topk;
+        for (int x0 = 0; x0 < ids; x0 += kBatch * kThreads) {
+            int32_t id[kBatch];
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
-        const int q = tid * kPer + r;
-        int64_t nt = 0;
-        if (q < nq) {
-            const int32_t len = max(__ldg(p.kv_len + w.q0 + q), 0);
-            s_len[q] = len;
-            s_toff[q] = __ldg(p.table_offset + w.q0 + q);
-            nt = ((int64_t)len + 127) / 128;
-            if (p.topk_ids) {
-                const int64_t nb = ((int64_t)len + p.block_tokens - 1) / p.block_tokens;
-                const int32_t *ids = p.topk_ids + (w.q0 + q) * p.topk;
-                int n = 0;
-#pragma unroll 8
-                for (int i = 0; i < p.topk; ++i) {
-                    const int32_t id = __ldg(ids + i);
-                    n += id >= 0 && id < nb;
+            for (int i = 0; i < kBatch; ++i) {
+                const int x = x0 + i * kThreads + tid;
+                id[i] = x < ids ? __ldg(src + x) : -1;
+                if (x < kSmallIds)
+                    s_ids[x] = id[i];
+            }
+            if (x0 == 0)
+                __syncthreads();       // the lengths and zeroed counts
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int x = x0 + i * kThreads + tid;
+                if (id[i] >= 0) {
+                    const int q = (int)((uint32_t)x / (uint32_t)p.topk);
+                    // the id names a block when the block's first token is visible
+                    if ((int64_t)id[i] * p.block_tokens < s_len[q])
+                        atomicAdd(&s_cnt[q], 1);
                 }
-                nt = ((int64_t)n * p.block_tokens + 127) / 128;
             }
         }
-        mine[r] = nt;
-        sum += nt;
+        __syncthreads();
     }
+    int64_t sum = 0;
+    if (tid < nq)
+        sum = p.topk_ids ? (s_cnt[tid] * p.block_tokens + 127) / 128 : ((int64_t)len + 127) / 128;
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -243,121 +309,67 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     }
     const int hcs = w.head_chunks;
     total *= hcs;
-    const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
-#pragma unroll
-    for (int r = 0; r < kPer; ++r) {
-        const int q = tid * kPer + r;
-        if (q < nq) {
-            if (before * hcs <= i0 && i0 < (before + mine[r]) * hcs)
-                s_qlo = q;
-            before += mine[r];
-            s_pre[q + 1] = before;
-            if (blockIdx.x == 0)
-                w.pre[q + 1] = before;
-        }
+    const int64_t i0 = div64(total * blockIdx.x, gridDim.x), i1 = div64(total * (blockIdx.x + 1), gridDim.x);
+    if (tid < nq) {
+        if (before * hcs <= i0 && i0 < (before + sum) * hcs)
+            s_qlo = tid;
+        s_pre[tid + 1] = before + sum;
+        if (blockIdx.x == 0 && w.joined)
+            w.pre[tid + 1] = before + sum;
     }
-    if (blockIdx.x == 0 && tid == 0)
+    if (blockIdx.x == 0 && tid == 0 && w.joined)
         w.pre[0] = 0;
+    if (tid == 0 && !w.joined)
+        w.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (blockIdx.x == 0 && tid == 0)
+        *w.total = total;
     __syncthreads();
     Walk wk;
     wk.start(s_pre, nq, hcs, i0, i1, s_qlo);
     const int nchunk_heads = (p.group + NH - 1) / NH;      // head chunks of a K/V head
 
-    if (warp == 0) {
-        // ---------------- tile copies ----------------
+    if (warp < 2) {
+        // ---------------- tile copies: warp 0 keys, warp 1 values ----------------
         const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = 128 >> lb;
-        uint32_t ring_it = 0, c = 0;
-        int list_q = -1, cnt = 0;
+        const CUtensorMap *map = warp == 0 ? &kmap : &vmap;
+        uint64_t *full_bars = warp == 0 ? bar_k_full : bar_v_full, *empty_bars = warp == 0 ? bar_k_empty : bar_v_empty;
+        const uint32_t stages = ring + (uint32_t)(warp * ST * S::kTileBytes);
+        uint32_t it = 0;
+        Turn turn;
         bool ok = true;
-        // copies the tiles of the chunk in info slot `slot` into the ring
-        auto copy = [&](const CUtensorMap *map, int slot, int n, int head) {
-            for (int i = 0; i < n && ok; ++i, ++ring_it) {
-                const uint32_t s = ring_it % ST, par = ((ring_it / ST) & 1u) ^ 1u;
-                ok = warp_wait(smem_u32(&bar_empty[s]), par, abort_flag);
+        while (!wk.done() && ok) {
+            const int n = wk.count(CH), slot = turn.info(), head = wk.hc / nchunk_heads;
+            ok = warp_wait(smem_u32(&bar_info_full[slot]), turn.info_phase(), abort_flag);
+            for (int i = 0; i < n && ok; ++i, ++it) {
+                const uint32_t s = it % ST;
+                ok = warp_wait(smem_u32(&empty_bars[s]), ((it / ST) & 1u) ^ 1u, abort_flag);
                 if (!ok)
                     break;
-                const uint32_t full = smem_u32(&bar_full[s]);
 #ifndef MSA_STARVE
+                const uint32_t full = smem_u32(&full_bars[s]);
                 if (lane == 0)
                     mbar_expect_tx(full, (uint32_t)S::kTileBytes);
                 __syncwarp();
                 if (lane < nbox * S::kAtoms) {
-                    const int b = lane & (nbox - 1), at = lane / nbox;
+                    const int b = lane & (nbox - 1), at = lane >> (7 - lb);
                     const int2 box = s_box[slot][i][b];
-                    tma_load_box(ring + s * (uint32_t)S::kTileBytes + (uint32_t)(at * 128 + b * BR) * S::kSwz, map,
+                    tma_load_box(stages + s * (uint32_t)S::kTileBytes + (uint32_t)(at * 128 + b * BR) * S::kSwz, map,
                                  at * (S::kSwz / (FP8 ? 1 : 2)), box.x, head, box.y, full);
                 }
 #endif
             }
-        };
-        int pn = 0, phead = 0, pslot = 0;
-        for (; !wk.done() && ok; ++c) {
-            const int n = wk.count(CH), slot = (int)(c % kInfo);
-            ok = warp_wait(smem_u32(&bar_info_empty[slot]), ((c / kInfo) & 1u) ^ 1u, abort_flag);
-            if (!ok)
-                break;
-            const int64_t len = s_len[wk.q];
-            if (p.topk_ids && list_q != wk.q) {
-                // the ids that name a block, in order; a repeated one is kept as -1
-                list_q = wk.q;
-                const int64_t nb = (len + p.block_tokens - 1) / p.block_tokens;
-                const int32_t *ids = p.topk_ids + (w.q0 + wk.q) * p.topk;
-                const int32_t a0 = lane < p.topk ? __ldg(ids + lane) : -1;
-                const int32_t a1 = lane + 32 < p.topk ? __ldg(ids + lane + 32) : -1;
-                const bool v0 = a0 >= 0 && a0 < nb, v1 = a1 >= 0 && a1 < nb;
-                const uint32_t m0 = __ballot_sync(0xffffffffu, v0), m1 = __ballot_sync(0xffffffffu, v1);
-                const uint32_t below = (1u << lane) - 1u;
-                const uint32_t same0 = __match_any_sync(0xffffffffu, v0 ? a0 : -1 - lane);
-                const uint32_t same1 = __match_any_sync(0xffffffffu, v1 ? a1 : -1 - lane);
-                bool dup0 = (same0 & below) != 0, dup1 = (same1 & below) != 0;
-                if (m1)   // the second half against the first
-                    for (int i = 0; i < 32; ++i)
-                        dup1 |= __shfl_sync(0xffffffffu, a0, i) == a1;
-                __syncwarp();
-                if (v0)
-                    s_list[__popc(m0 & below)] = dup0 ? -1 : a0;
-                if (v1)
-                    s_list[__popc(m0) + __popc(m1 & below)] = dup1 ? -1 : a1;
-                cnt = __popc(m0) + __popc(m1);
-                __syncwarp();
-            }
-            for (int x = lane; x < n * nbox; x += 32) {
-                const int i = x / nbox, b = x & (nbox - 1);
-                const int64_t v = (int64_t)(wk.tile + i) * 128 + b * BR;
-                int64_t j = v;
-                bool in = true;
-                if (p.topk_ids) {
-                    const int64_t k = v / p.block_tokens;
-                    const int32_t id = k < cnt ? s_list[k] : -1;
-                    in = id >= 0;
-                    j = (int64_t)id * p.block_tokens + (v - k * p.block_tokens);
-                }
-                in = in && j < len;
-                const int32_t pg = in ? attn_page(p, s_toff[wk.q], j) : -1;
-                // a box that shows nothing is copied from past the last page: zeros
-                s_box[slot][i][b] = pg >= 0 ? make_int2(attn_page_row(p, j), pg) : make_int2(0, w.oob_page);
-                s_nv[slot][i][b] = (uint8_t)(pg >= 0 ? min((int64_t)BR, len - j) : 0);
-            }
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&bar_info_full[slot]));
-            const int head = wk.hc / nchunk_heads;
-            copy(&kmap, slot, n, head);
-            if (c > 0)
-                copy(&vmap, pslot, pn, phead);
-            pn = n;
-            phead = head;
-            pslot = slot;
+            if (ok && lane == 0)
+                mbar_arrive(smem_u32(&bar_info_empty[slot]));
+            turn.step(wk.last(n));
             wk.step(n);
         }
-        if (ok && c > 0)
-            copy(&vmap, pslot, pn, phead);
 #ifndef MSA_STARVE
         // every copy has landed before the CTA finishes
-        for (uint32_t s = 0; s < (uint32_t)ST && s < ring_it; ++s)
-            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[s]), ((ring_it - 1u - s) / ST) & 1u));
+        for (uint32_t s = 0; s < (uint32_t)ST && s < it; ++s)
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bars[s]), ((it - 1u - s) / ST) & 1u));
 #endif
-    } else if (warp == 1) {
+    } else if (warp == 5) {
         // ---------------- query tiles ----------------
         uint32_t seg = 0;
         bool ok = true;
@@ -438,27 +450,81 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             wk.step((int)min((int64_t)(wk.nt - wk.tile), wk.end - wk.it));
             ++seg;
         }
+        // queries that see nothing are in no CTA's share
+        for (int q = blockIdx.x; q < nq && !w.joined; q += gridDim.x)
+            if (s_pre[q + 1] == s_pre[q]) {
+                const int64_t row = (w.q0 + q) * p.hq;
+                uint32_t *out = reinterpret_cast<uint32_t *>(p.out + row * D);
+                for (int64_t i = lane; i < (int64_t)p.hq * D / 2; i += 32)
+                    out[i] = 0u;
+                for (int h = lane; h < p.hq && p.lse; h += 32)
+                    p.lse[row + h] = -INFINITY;
+            }
     } else if (warp == 2) {
-        // ---------------- MMAs ----------------
-        constexpr uint32_t kIdS = mma_idesc(FP8, 128, N, false, false);
-        constexpr uint32_t kIdO = mma_idesc(FP8, 128, N, true, true);
+        // ---------------- MMAs of the scores ----------------
+        constexpr uint32_t kId = mma_idesc(FP8, 128, N, false, false);
         constexpr int kKB = 32;                               // bytes of K a step takes of a K-major row
-        constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step
-        const int BR = w.box_rows, nbox = 128 / BR;
-        const uint32_t o_tmem = tmem + 2 * S::kSCols;
-        uint32_t ring_it = 0, c = 0, seg = 0;
+        uint32_t it = 0;
+        Turn turn;
         bool ok = true, fresh = true;
-        auto values = [&](uint32_t cc, int n) {   // the value products of chunk cc
-            ok = warp_wait(smem_u32(&bar_p_full), cc & 1u, abort_flag);
-            tc_fence_after();
-            const int slot = (int)(cc % kInfo);
-            for (int i = 0; i < n && ok; ++i, ++ring_it) {
-                const uint32_t s = ring_it % ST;
-                ok = warp_wait(smem_u32(&bar_full[s]), (ring_it / ST) & 1u, abort_flag);
+        while (!wk.done() && ok) {
+            const int n = wk.count(CH), sb = turn.buf();
+            const uint32_t x = turn.seg % kQSlots;
+            if (fresh)
+                ok = warp_wait(smem_u32(&bar_q_full[x]), (turn.seg / kQSlots) & 1u, abort_flag);
+            ok = ok && warp_wait(smem_u32(&bar_s_empty[sb]), turn.buf_phase() ^ 1u, abort_flag);
+            const uint32_t qt = qbase + x * (uint32_t)S::kQBytes;
+            for (int i = 0; i < n && ok; ++i, ++it) {
+                const uint32_t s = it % ST;
+                ok = warp_wait(smem_u32(&bar_k_full[s]), (it / ST) & 1u, abort_flag);
                 if (!ok)
                     break;
                 tc_fence_after();
-                const uint32_t vt = ring + s * (uint32_t)S::kTileBytes;
+                const uint32_t kt = ring + s * (uint32_t)S::kTileBytes;
+                const uint32_t d = tmem + (uint32_t)(sb * S::kSCols + i * N);
+#pragma unroll
+                for (int ks = 0; ks < S::kRowBytes / kKB; ++ks) {
+                    const uint32_t at = (uint32_t)(ks * kKB) / S::kSwz, col = (uint32_t)(ks * kKB) % S::kSwz;
+                    mma_ss<FP8>(d, smem_desc(kt + at * (128u * S::kSwz) + col, S::kSwz, 16u, 8u * S::kSwz),
+                                smem_desc(qt + at * (uint32_t)(N * S::kSwz) + col, S::kSwz, 16u, 8u * S::kSwz), kId, ks > 0);
+                }
+                mma_commit(smem_u32(&bar_k_empty[s]));
+            }
+            __syncwarp();
+            if (!ok)
+                break;
+            mma_commit(smem_u32(&bar_s_full[sb]));
+            fresh = wk.last(n);
+            if (fresh)
+                mma_commit(smem_u32(&bar_q_empty[x]));
+            turn.step(fresh);
+            wk.step(n);
+        }
+        if (!ok)
+            *abort_flag = 1;
+        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
+        (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
+    } else if (warp == 3) {
+        // ---------------- MMAs of the values ----------------
+        constexpr uint32_t kId = mma_idesc(FP8, 128, N, true, true);
+        constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step
+        const int BR = w.box_rows, nbox = 128 / BR;
+        const uint32_t vring = ring + (uint32_t)(ST * S::kTileBytes);
+        uint32_t it = 0;
+        Turn turn;
+        bool ok = true;
+        while (!wk.done() && ok) {
+            const int n = wk.count(CH), slot = turn.info(), g = turn.group();
+            ok = warp_wait(smem_u32(&bar_info_full[slot]), turn.info_phase(), abort_flag);
+            ok = ok && warp_wait(smem_u32(&bar_p_full[g]), turn.chunk() & 1u, abort_flag);
+            const uint32_t d = tmem + (uint32_t)(kSBufs * S::kSCols + g * N);
+            for (int i = 0; i < n && ok; ++i, ++it) {
+                const uint32_t s = it % ST;
+                ok = warp_wait(smem_u32(&bar_v_full[s]), (it / ST) & 1u, abort_flag);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t vt = vring + s * (uint32_t)S::kTileBytes;
                 // rows past the history may hold anything: a weight of zero would not
                 // hide an infinity or a NaN
                 const int nv = lane < nbox ? s_nv[slot][i][lane] : 0;
@@ -469,92 +535,119 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         partial &= partial - 1;
                         const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
                         for (int at = 0; at < S::kAtoms; ++at)
-                            for (int x = r0 * (S::kSwz / 16) + lane; x < r1 * (S::kSwz / 16); x += 32)
-                                sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)x * 16u, 0u, 0u, 0u, 0u);
+                            for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
+                                sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
                     }
                     fence_async_smem();
                     __syncwarp();
                 }
-                const uint32_t pt = pbase + (uint32_t)(i * S::kPBytes);
+                const uint32_t pt = pbase + (uint32_t)((g * CH + i) * S::kPBytes);
 #pragma unroll
-                for (int ks = 0; ks < 128 / kTok; ++ks) {
+                for (int ks = 0; ks < 128 / kTok; ++ks)
                     // of 64 dims the 128 rows are the same 64 twice
-                    const uint64_t a = smem_desc(vt + (uint32_t)(ks * kTok * S::kSwz), S::kSwz,
-                                                 S::kAtoms == 2 ? 128u * S::kSwz : 0u, 8u * S::kSwz);
-                    const uint64_t b = smem_desc(pt + (uint32_t)(ks * kTok * 16), 0, 128u, 2048u);
-                    mma_ss<FP8>(o_tmem, a, b, kIdO, i > 0 || ks > 0);
-                }
-                mma_commit(smem_u32(&bar_empty[s]));
-            }
-            __syncwarp();
-            if (ok) {
-                mma_commit(smem_u32(&bar_o_full));
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bar_info_empty[slot]));
-            }
-        };
-        int pn = 0;
-        for (; !wk.done() && ok; ++c) {
-            const int n = wk.count(CH);
-            const uint32_t x = seg % kQSlots;
-            if (fresh)
-                ok = warp_wait(smem_u32(&bar_q_full[x]), (seg / kQSlots) & 1u, abort_flag);
-            ok = ok && warp_wait(smem_u32(&bar_s_empty[c & 1]), ((c >> 1) & 1u) ^ 1u, abort_flag);
-            // the chunk's box list, which the value products read
-            ok = ok && warp_wait(smem_u32(&bar_info_full[c % kInfo]), (c / kInfo) & 1u, abort_flag);
-            if (!ok)
-                break;
-            tc_fence_after();
-            const uint32_t qt = qbase + x * (uint32_t)S::kQBytes;
-            for (int i = 0; i < n; ++i, ++ring_it) {
-                const uint32_t s = ring_it % ST;
-                ok = warp_wait(smem_u32(&bar_full[s]), (ring_it / ST) & 1u, abort_flag);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t kt = ring + s * (uint32_t)S::kTileBytes;
-                const uint32_t d = tmem + (c & 1u) * S::kSCols + (uint32_t)(i * N);
-#pragma unroll
-                for (int ks = 0; ks < S::kRowBytes / kKB; ++ks) {
-                    const uint32_t at = (uint32_t)(ks * kKB) / S::kSwz, col = (uint32_t)(ks * kKB) % S::kSwz;
-                    mma_ss<FP8>(d, smem_desc(kt + at * (128u * S::kSwz) + col, S::kSwz, 16u, 8u * S::kSwz),
-                                smem_desc(qt + at * (uint32_t)(N * S::kSwz) + col, S::kSwz, 16u, 8u * S::kSwz), kIdS, ks > 0);
-                }
-                mma_commit(smem_u32(&bar_empty[s]));
+                    mma_ss<FP8>(d, smem_desc(vt + (uint32_t)(ks * kTok * S::kSwz), S::kSwz,
+                                             S::kAtoms == 2 ? 128u * S::kSwz : 0u, 8u * S::kSwz),
+                                smem_desc(pt + (uint32_t)(ks * kTok * 16), 0, 128u, S::kPBytes == 2048 ? 0u : 2048u), kId,
+                                i > 0 || ks > 0);
+                mma_commit(smem_u32(&bar_v_empty[s]));
             }
             __syncwarp();
             if (!ok)
                 break;
-            mma_commit(smem_u32(&bar_s_full[c & 1]));
-            fresh = wk.tile + n == wk.nt || wk.it + n == wk.end;
-            if (fresh) {
-                mma_commit(smem_u32(&bar_q_empty[x]));
-                ++seg;
-            }
+            mma_commit(smem_u32(&bar_o_full[g]));
+            if (lane == 0)
+                mbar_arrive(smem_u32(&bar_info_empty[slot]));
+            turn.step(wk.last(n));
             wk.step(n);
-            if (c > 0)
-                values(c - 1, pn);
-            pn = n;
         }
-        if (ok && c > 0)
-            values(c - 1, pn);
         if (!ok)
             *abort_flag = 1;
-        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
+        mma_commit(smem_u32(&bar_drain));
         (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
-    } else if (warp >= 4) {
-        // ---------------- softmax and output ----------------
-        const int quarter = warp & 3, row = quarter * 32 + lane;
+    } else if (warp == 4) {
+        // ---------------- block lists and page lookups ----------------
+        const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = 128 >> lb;
+        int list_q = -1, cnt = 0;
+        Turn turn;
+        bool ok = true;
+        while (!wk.done() && ok) {
+            const int n = wk.count(CH), slot = turn.info();
+            ok = warp_wait(smem_u32(&bar_info_empty[slot]), turn.info_phase() ^ 1u, abort_flag);
+            if (!ok)
+                break;
+            const int64_t len = s_len[wk.q];
+            if (p.topk_ids && list_q != wk.q) {
+                // the ids that name a block, in order; a repeated one is kept as -1
+                list_q = wk.q;
+                const int64_t nb = (len + p.block_tokens - 1) / p.block_tokens;
+                int32_t a0 = -1, a1 = -1;
+                if (nq * p.topk <= kSmallIds) {
+                    a0 = lane < p.topk ? s_ids[wk.q * p.topk + lane] : -1;
+                    a1 = lane + 32 < p.topk ? s_ids[wk.q * p.topk + lane + 32] : -1;
+                } else {
+                    const int32_t *ids = p.topk_ids + (w.q0 + wk.q) * p.topk;
+                    a0 = lane < p.topk ? __ldg(ids + lane) : -1;
+                    a1 = lane + 32 < p.topk ? __ldg(ids + lane + 32) : -1;
+                }
+                const bool v0 = a0 >= 0 && a0 < nb, v1 = a1 >= 0 && a1 < nb;
+                const uint32_t m0 = __ballot_sync(0xffffffffu, v0), m1 = __ballot_sync(0xffffffffu, v1);
+                const uint32_t below = (1u << lane) - 1u;
+                const uint32_t same0 = __match_any_sync(0xffffffffu, v0 ? a0 : -1 - lane);
+                const uint32_t same1 = __match_any_sync(0xffffffffu, v1 ? a1 : -1 - lane);
+                const bool dup0 = (same0 & below) != 0;
+                bool dup1 = (same1 & below) != 0;
+                if (m1)   // the second half against the first
+                    for (int i = 0; i < 32; ++i)
+                        dup1 |= __shfl_sync(0xffffffffu, a0, i) == a1;
+                __syncwarp();
+                if (v0)
+                    s_list[__popc(m0 & below)] = dup0 ? -1 : a0;
+                if (v1)
+                    s_list[__popc(m0) + __popc(m1 & below)] = dup1 ? -1 : a1;
+                cnt = __popc(m0) + __popc(m1);
+                __syncwarp();
+            }
+            for (int x = lane; x < n * nbox; x += 32) {
+                const int i = x >> (7 - lb), b = x & (nbox - 1);
+                const int64_t v = (int64_t)(wk.tile + i) * 128 + b * BR;
+                int64_t j = v;
+                bool in = true;
+                if (p.topk_ids) {
+                    const int64_t k = (uint32_t)v / (uint32_t)p.block_tokens;   // below 64 * 1024 tokens
+                    const int32_t id = k < cnt ? s_list[k] : -1;
+                    in = id >= 0;
+                    j = (int64_t)id * p.block_tokens + (v - k * p.block_tokens);
+                }
+                in = in && j < len;
+                const int32_t pg = in ? attn_page(p, s_toff[wk.q], j) : -1;
+                // a box that shows nothing is copied from past the last page: zeros
+                s_box[slot][i][b] = pg >= 0 ? make_int2(attn_page_row(p, j), pg) : make_int2(0, w.oob_page);
+                s_nv[slot][i][b] = (uint8_t)(pg >= 0 ? min((int64_t)BR, len - j) : 0);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&bar_info_full[slot]));
+            turn.step(wk.last(n));
+            wk.step(n);
+        }
+    } else if (warp >= 8) {
+        // ---------------- softmax and output: group g takes the segments s with s % kGroups == g ----------------
+        // (a segment: what the CTA holds of a (query, head chunk))
+        const int g = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const int BR = w.box_rows, lb = __ffs(BR) - 1;
-        const uint32_t o_tmem = tmem + lane_off + 2 * S::kSCols;
+        const uint32_t o_tmem = tmem + lane_off + (uint32_t)(kSBufs * S::kSCols + g * N);
+        const uint32_t ptile = pbase + (uint32_t)(g * CH * S::kPBytes);
+        float (*red)[16] = s_red[g];
         constexpr float kPScale = FP8 ? 256.0f : 1.0f;   // E4M3 weights use the range up to 448
         float m[NH], l[NH], acc[NH];
-        uint32_t c = 0, seg = 0;
-        bool ok = true, first = true, pending = false;
-        auto group_sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-        auto add_output = [&](uint32_t cc) {   // adds the value products of chunk cc
-            ok = ok && warp_wait(smem_u32(&bar_o_full), cc & 1u, abort_flag);
+        uint32_t k = 0, seg = 0, o_phase = 0;      // k: chunks of this group
+        bool ok = true, first = true;
+        float vs = 1.0f, ks = 1.0f;
+        auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
+        auto add_output = [&]() {   // adds the value products of this group's last chunk
+            ok = ok && warp_wait(smem_u32(&bar_o_full[g]), o_phase, abort_flag);
+            o_phase ^= 1u;
             if (ok) {
                 tc_fence_after();
                 uint32_t r[N];
@@ -569,8 +662,27 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     acc[h] += FP8 ? __uint_as_float(r[h]) + __uint_as_float(r[NH + h]) : __uint_as_float(r[h]);
             }
         };
-        for (; !wk.done(); ++c) {
-            const int n = wk.count(CH), slot = (int)(c % kInfo);
+        // reduces a value of each head over the 128 threads of the group; every thread gets all
+        auto group_reduce = [&](float (&v)[NH], auto max_tag) {
+            constexpr bool MAX = decltype(max_tag)::value;
+            const float x = butterfly<NH, MAX>(v, lane);
+            if ((lane & (32 / NH - 1)) == 0)
+                red[quarter][lane / (32 / NH)] = x;
+            group_sync();
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+                v[h] = MAX ? fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]))
+                           : (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]);
+        };
+        while (!wk.done()) {
+            if ((int)(seg % kGroups) != g) {
+                wk.step((int)min((int64_t)(wk.nt - wk.tile), wk.end - wk.it));
+                ++seg;
+                continue;
+            }
+            const int n = wk.count(CH), slot = g * kGroupInfo + (int)(k % kGroupInfo);
+            const int sb = g * kGroupBufs + (int)(k % kGroupBufs);
+            const bool last = wk.last(n);
             const uint32_t x = seg % kQSlots;
             const int hcol = wk.hc % nchunk_heads * NH, head = wk.hc / nchunk_heads;
             if (first) {
@@ -580,95 +692,72 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     l[h] = 0.0f;
                     acc[h] = 0.0f;
                 }
-                pending = false;
+                ks = attn_k_scale(p, head) * p.scale_log2;      // in flight while the scores are made
+                vs = attn_v_scale(p, head);
             }
-            const bool last = wk.tile + n == wk.nt || wk.it + n == wk.end;
-            ok = ok && warp_wait(smem_u32(&bar_info_full[slot]), (c / kInfo) & 1u, abort_flag);
+            ok = ok && warp_wait(smem_u32(&bar_info_full[slot]), (k / kGroupInfo) & 1u, abort_flag);
             ok = ok && warp_wait(smem_u32(&bar_q_full[x]), (seg / kQSlots) & 1u, abort_flag);
-            ok = ok && warp_wait(smem_u32(&bar_s_full[c & 1]), (c >> 1) & 1u, abort_flag);
-            // all four warps go on or none does
+            ok = ok && warp_wait(smem_u32(&bar_s_full[sb]), (k / kGroupBufs) & 1u, abort_flag);
             if (!ok)
                 *abort_flag = 1;
-            float s[CH][NH];
-            uint32_t seen = 0;          // tiles whose row `row` is visible
+            // Two passes over the chunk's scores in tensor memory, each a loop over the
+            // tiles: the unrolled form held them in registers, and its length cost more in
+            // instruction fetches (2.3 of the 4 cycles a warp instruction took) than
+            // reading them twice does.
+            const uint32_t sbuf = tmem + lane_off + (uint32_t)(sb * S::kSCols);
+            const float qs = ok ? ks * s_qinv[x] : 0.0f;
+            auto scores = [&](int i, float (&z)[NH]) {     // of this thread's token of tile i
+                uint32_t r[N];
+                if (N == 16)
+                    tmem_ld16(sbuf + (uint32_t)(i * N), r);
+                else
+                    tmem_ld32(sbuf + (uint32_t)(i * N), r);
+                const bool seen = (row & (BR - 1)) < s_nv[slot][i][row >> lb];
+                tc_wait_ld();
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    z[h] = FP8 ? __uint_as_float(r[h]) + __uint_as_float(r[NH + h]) : __uint_as_float(r[h]);
+                    z[h] = seen ? z[h] * qs : -INFINITY;
+                }
+                return seen;
+            };
             float mx[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+                mx[h] = -INFINITY;
             if (ok) {
                 tc_fence_after();
-                const float qs = p.scale_log2 * attn_k_scale(p, head) * s_qinv[x];
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    float z[NH];
+                    (void)scores(i, z);
 #pragma unroll
-                for (int i = 0; i < CH; ++i)
-                    if (i < n && (row & (BR - 1)) < s_nv[slot][i][row >> lb])
-                        seen |= 1u << i;
-#pragma unroll
-                for (int i0c = 0; i0c < CH; i0c += 4) {
-                    uint32_t r[4][N];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i0c + i < CH) {
-                            const uint32_t a = tmem + lane_off + (c & 1u) * S::kSCols + (uint32_t)((i0c + i) * N);
-                            if (N == 16)
-                                tmem_ld16(a, r[i]);
-                            else
-                                tmem_ld32(a, r[i]);
-                        }
-                    tc_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i0c + i < CH)
-#pragma unroll
-                            for (int h = 0; h < NH; ++h) {
-                                const float z = FP8 ? __uint_as_float(r[i][h]) + __uint_as_float(r[i][NH + h])
-                                                    : __uint_as_float(r[i][h]);
-                                s[i0c + i][h] = (seen >> (i0c + i)) & 1u ? z * qs : -INFINITY;
-                            }
+                    for (int h = 0; h < NH; ++h)
+                        mx[h] = fmaxf(mx[h], z[h]);
                 }
-                tc_fence_before();
             }
-            __syncwarp();
-            if (ok && lane == 0) {
-                mbar_arrive(smem_u32(&bar_s_empty[c & 1]));
-                mbar_arrive(smem_u32(&bar_info_empty[slot]));
-                if (last)
-                    mbar_arrive(smem_u32(&bar_q_empty[x]));
-            }
+            group_reduce(mx, std::true_type());
+            if (!first)
+                add_output();
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                mx[h] = -INFINITY;
-                if (ok)
-#pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        mx[h] = fmaxf(mx[h], s[i][h]);
-            }
-            const float wm = butterfly<NH, true>(mx, lane);
-            if ((lane & (32 / NH - 1)) == 0)
-                s_red[quarter][lane / (32 / NH)] = wm;
-            group_sync();
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const float cm = fmaxf(fmaxf(s_red[0][h], s_red[1][h]), fmaxf(s_red[2][h], s_red[3][h]));
-                mx[h] = fmaxf(m[h], cm);
-            }
-            if (pending)
-                add_output(c - 1);
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
+                mx[h] = fmaxf(m[h], mx[h]);
                 const float alpha = m[h] == mx[h] ? 1.0f : exp2_approx(m[h] - mx[h]);
                 m[h] = mx[h];
                 l[h] *= alpha;
                 acc[h] *= alpha;
             }
             if (ok) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    if (i >= n)
-                        break;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
                     float e[NH];
+                    const bool seen = scores(i, e);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        e[h] = (seen >> i) & 1u ? exp2_approx(s[i][h] - m[h]) : 0.0f;
+                        e[h] = seen ? exp2_approx(e[h] - m[h]) : 0.0f;
                         l[h] += e[h];
                     }
-                    const uint32_t a = pbase + (uint32_t)(i * S::kPBytes + row * 16);
+                    const uint32_t a = ptile + (uint32_t)(i * S::kPBytes + row * 16);
                     if (FP8) {
                         uint32_t hw[NH / 4], lw[NH / 4];
 #pragma unroll
@@ -701,54 +790,61 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                 fence_async_smem();
             }
             __syncwarp();
-            if (ok && lane == 0)
-                mbar_arrive(smem_u32(&bar_p_full));
-            pending = true;
+            if (ok && lane == 0) {
+                mbar_arrive(smem_u32(&bar_p_full[g]));
+                mbar_arrive(smem_u32(&bar_s_empty[sb]));
+                mbar_arrive(smem_u32(&bar_info_empty[slot]));
+                if (last)
+                    mbar_arrive(smem_u32(&bar_q_empty[x]));
+            }
             if (last) {
-                add_output(c);
-                // the sum over the tokens; then a thread is a dim
-                const float ws = butterfly<NH, false>(l, lane);
-                group_sync();                    // s_red has been read
-                if ((lane & (32 / NH - 1)) == 0)
-                    s_red[quarter][lane / (32 / NH)] = ws;
+                // the sum over the tokens while the values are multiplied; then a thread is a dim
+                group_sync();                    // every thread has read the maxima
+                group_reduce(l, std::false_type());
+                add_output();
+                if (!ok)
+                    *abort_flag = 1;
                 group_sync();
                 // a wait of any warp that ran out spoils the whole (query, head chunk)
-                const bool good = ok && *abort_flag == 0;
+                const bool good = *abort_flag == 0;
                 const float bad = __int_as_float(0x7fc00000);
                 const bool whole = wk.tile + n == wk.nt && wk.it + n - i0 >= wk.nt;
+                const bool began = wk.it - wk.tile >= i0;      // in this CTA
                 const int nh = min(NH, p.group - hcol);
                 const int64_t t = w.q0 + wk.q;
-                const float vs = attn_v_scale(p, head);
-                float *piece = nullptr;
-                if (w.joined || !whole) {
-                    const int64_t sl = whole ? 2 * (int64_t)gridDim.x + (int64_t)wk.q * hcs + wk.hc
-                                       : wk.it + n - i0 < wk.tile + n ? (int64_t)blockIdx.x      // began in another CTA
-                                                                      : (int64_t)gridDim.x + blockIdx.x;
-                    piece = w.pieces + sl * (int64_t)(NH * (D + 2));
-                }
+                if (whole && !w.joined) {
+                    const int64_t hr = t * p.hq + head * p.group + hcol;
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const float sum = s_red[0][h] + s_red[1][h] + s_red[2][h] + s_red[3][h];
-                    if (h < nh && row < D) {
-                        const int64_t hr = t * p.hq + head * p.group + hcol + h;
-                        if (piece) {
+                    for (int h = 0; h < NH; ++h)
+                        if (h < nh && row < D) {
+                            const float o = l[h] == 0.0f ? 0.0f : acc[h] * __fdividef(vs * (1.0f / kPScale), l[h]);
+                            p.out[(hr + h) * D + row] = attn_bf16(good ? o : bad);
+                            if (row == 0 && p.lse)
+                                p.lse[hr + h] = good ? attn_lse(m[h], l[h]) : bad;
+                        }
+                } else {
+                    const int64_t sl = whole ? 2 * (int64_t)gridDim.x + (int64_t)wk.q * hcs + wk.hc
+                                             : (began ? (int64_t)gridDim.x : 0) + blockIdx.x;
+                    float *piece = w.pieces + sl * (int64_t)(NH * (D + 2));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        if (row < D) {
                             piece[h * D + row] = good ? acc[h] * (vs * (1.0f / kPScale)) : bad;
                             if (row == 0) {
                                 piece[NH * D + h] = good ? m[h] : bad;
-                                piece[NH * D + NH + h] = good ? sum : bad;
+                                piece[NH * D + NH + h] = good ? l[h] : bad;
                             }
-                        } else {
-                            const float o = sum == 0.0f ? 0.0f : acc[h] * (vs * (1.0f / kPScale) / sum);
-                            p.out[hr * D + row] = attn_bf16(good ? o : bad);
-                            if (row == 0 && p.lse)
-                                p.lse[hr] = good ? attn_lse(m[h], sum) : bad;
                         }
+                    // the CTA in which it began lists it for the join
+                    if (began && !whole && !w.joined && row == 0) {
+                        const int64_t base = wk.it - wk.tile;
+                        w.cut[blockIdx.x] = make_int4(wk.q, wk.hc, (int)div64((base + wk.nt) * gridDim.x - 1, total), 0);
                     }
                 }
-                group_sync();                    // s_red is free again
                 ++seg;
             }
             first = last;
+            ++k;
             wk.step(n);
         }
     }
@@ -762,71 +858,99 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
 }
 
 // ---------------------------------------------------------------------------
-// the join: one warp per (query, query head)
+// the join of pieces
 // ---------------------------------------------------------------------------
 //
-// Adds the pieces of a (query, K/V head) that was cut between CTAs, those of its group's
-// prefix, and writes the queries that see nothing.  The pieces lie in the workspace, most
-// of them in L2.  A warp whose rows are already written leaves at once.
-constexpr int kJoinWarps = 8;
+// A row of pieces is summed by one warp; the maxima and sums are brought a piece a lane,
+// so that a row costs three rounds of loads whatever the number of pieces.  Most of them
+// lie in L2.
+template <int D>
+struct Row {
+    static constexpr int E = D / 32;
+    float m = -INFINITY, l = 0.0f, acc[E] = {};
 
-// a / b for a >= 0, b > 0, in 32 bits where both fit
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
+    // adds up to 32 pieces: lane i brings piece i (its row of output o, maximum pm, sum pl)
+    __device__ __forceinline__ void add(int count, const float *o, float pm, float pl, int lane)
+    {
+        const bool seen = lane < count && pl != 0.0f;       // a NaN goes on
+        float mn = seen ? pm : -INFINITY;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+        mn = fmaxf(mn, m);
+        const float a = m == -INFINITY ? 0.0f : exp2f(m - mn);
+        const float b = seen ? exp2f(pm - mn) : 0.0f;
+        float sum = seen ? pl * b : 0.0f;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l = l * a + sum;
+        m = mn;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] *= a;
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+            const float *oi = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)o, i));
+            const float bi = __shfl_sync(0xffffffffu, b, i);
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[e] = __ldcg(oi + lane + 32 * e);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] += bi == 0.0f ? 0.0f : x[e] * bi;
+        }
+    }
+    __device__ __forceinline__ void write(const AttnParams &p, int64_t row, int lane)
+    {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            p.out[row * D + lane + 32 * e] = attn_bf16(l == 0.0f ? 0.0f : acc[e] / l);
+        if (lane == 0 && p.lse)
+            p.lse[row] = attn_lse(m, l);
+    }
+};
+
+// Adds the pieces that CTAs c0 .. c1 hold of a (query, head chunk), column `col`; `whole`
+// is the slot of one that a single CTA holds.
+template <int D>
+__device__ __forceinline__ void add_pieces(Row<D> &r, const AttnPieces &w, int64_t total, int64_t c0, int64_t c1,
+                                           int64_t whole, int col, int lane)
 {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+    const int64_t n = w.ctas, size = (int64_t)w.heads * (D + 2);
+    for (int64_t i0 = c0; i0 <= c1; i0 += 32) {
+        // CTA i holds items [total * i / n, total * (i + 1) / n), maybe none
+        const int64_t i = i0 + lane;
+        const bool has = i <= c1 && (i == c0 || div64(total * i, n) < div64(total * (i + 1), n));
+        const uint32_t mask = __ballot_sync(0xffffffffu, has);
+        const int src = lane < __popc(mask) ? (int)__fns(mask, 0, lane + 1) : 0;
+        const int64_t j = i0 + src;
+        const float *piece = w.pieces + (j > c0 ? j : c0 == c1 ? whole : n + c0) * size;
+        const bool in = lane < __popc(mask);
+        r.add(__popc(mask), piece + col * D, in ? __ldcg(piece + w.heads * D + col) : 0.0f,
+              in ? __ldcg(piece + w.heads * D + w.heads + col) : 0.0f, lane);
+    }
 }
 
+// The (query, head chunk)s that a CTA began and did not finish: one block a CTA, one warp
+// a head.
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPieces w)
+__global__ void __launch_bounds__(512)
+msa_attention_join_cut_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPieces w)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (r >= w.nq * p.hq)
+    const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;
+    const int4 cut = __ldcg(w.cut + blockIdx.x);
+    const int64_t total = __ldcg(w.total);
+    const int nch = (p.group + w.heads - 1) / w.heads;
+    const int head = cut.y / nch, hcol = cut.y % nch * w.heads;
+    if (cut.x < 0 || hcol + col >= p.group)
         return;
-    const int q = (int)(r / p.hq), h = (int)(r % p.hq);
-    const int NH = w.heads;
-    const int c = h / p.group, hg = h % p.group, nch = (p.group + NH - 1) / NH;
-    const int hc = c * nch + hg / NH, col = hg % NH;
-    constexpr int E = D / 32;
-    float m = -INFINITY, l = 0.0f, acc[E] = {};
-    auto add = [&](const float *o, float pm, float pl) {
-        if (pl == 0.0f)                       // nothing seen (a NaN goes on)
-            return;
-        const float mn = isnan(pm) ? pm : fmaxf(m, pm);
-        const float a = m == -INFINITY ? 0.0f : exp2f(m - mn), b = exp2f(pm - mn);
-        l = l * a + pl * b;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = acc[e] * a + o[lane + 32 * e] * b;
-        m = mn;
-    };
-    const int64_t nt = w.pre[q + 1] - w.pre[q];
-    if (nt > 0) {
-        const int64_t total = w.pre[w.nq] * w.head_chunks, n = w.ctas;
-        const int64_t base = w.pre[q] * w.head_chunks + hc * nt;
-        // CTA i holds items [total * i / n, total * (i + 1) / n), maybe none
-        const int64_t c0 = div64((base + 1) * n - 1, total), c1 = div64((base + nt) * n - 1, total);
-        if (c0 == c1 && !w.joined)
-            return;
-        const int64_t size = (int64_t)NH * (D + 2);
-        for (int64_t i = c0;;) {
-            const int64_t sl = i > c0 ? i : c0 == c1 ? 2 * n + (int64_t)q * w.head_chunks + hc : n + c0;
-            const float *piece = w.pieces + sl * size;
-            add(piece + col * D, piece[NH * D + col], piece[NH * D + NH + col]);
-            if (i >= c1)
-                break;
-            i = div64((div64(total * (i + 1), n) + 1) * n - 1, total);   // the CTA of the next item
-        }
-    }
-    const int64_t row = (w.q0 + q) * p.hq + h;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        p.out[row * D + lane + 32 * e] = attn_bf16(l == 0.0f ? 0.0f : acc[e] / l);
-    if (lane == 0 && p.lse)
-        p.lse[row] = attn_lse(m, l);
+    Row<D> r;
+    add_pieces<D>(r, w, total, blockIdx.x, cut.z, 0, col, lane);
+    r.write(p, (w.q0 + cut.x) * p.hq + head * p.group + hcol + col, lane);
 }
 
 template <int D, bool FP8, int NH>
@@ -862,11 +986,10 @@ cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, 
                     : launch_decode<64, false, 16>(p, w, kmap, vmap, pdl, stream));
 }
 
-cudaError_t attn_join(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream)
+cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream)
 {
     void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w)};
-    const int64_t grid = (w.nq * p.hq + kJoinWarps - 1) / kJoinWarps;
-    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_kernel<128>)
-                                       : reinterpret_cast<const void *>(&msa_attention_join_kernel<64>),
-                       grid, kJoinWarps * 32, 0, true, stream, args);
+    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<128>)
+                                       : reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<64>),
+                       w.ctas, w.heads * 32, 0, true, stream, args);
 }

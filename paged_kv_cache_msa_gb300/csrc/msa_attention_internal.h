@@ -9,7 +9,7 @@
 #include <cstdint>
 
 constexpr int kAttnMaxGroups = 1024;
-constexpr int kAttnWindow = 512;     // queries a launch of the tensor-core decode kernel takes
+constexpr int kAttnWindow = 384;     // queries a launch of the tensor-core decode kernel takes
 constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
 
 // One cache as the kernels see it; strides in elements.
@@ -51,7 +51,10 @@ struct AttnParams {
 // (joined) a whole one in slot 2 * ctas + query * head_chunks + head chunk.  A piece is
 // [heads][D] of output (relative to the maximum), then the maxima, then the sums.
 struct AttnPieces {
-    int64_t *pre;                    // [nq + 1]: tiles before each query of the window
+    int64_t *total;                  // items of the list
+    int4 *cut;                       // [ctas]: query, head chunk and last CTA of the one that
+                                     // began in a CTA and goes on in the next; query -1: none
+    int64_t *pre;                    // [nq + 1]: tiles before each query of the window (joined)
     float *pieces;
     int64_t q0, nq;                  // the window
     int32_t heads;                   // query heads of a head chunk: 8 or 16
@@ -68,7 +71,7 @@ cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, bool 
 int attn_decode_heads(int group);
 cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
                         const CUtensorMap &vmap, bool pdl, cudaStream_t stream);
-cudaError_t attn_join(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream);
+cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream);
 
 #ifdef __CUDACC__
 

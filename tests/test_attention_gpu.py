@@ -64,6 +64,18 @@ def test_sparse_decode_batches(lens, dtype):
     Problem(12, lens=lens, dtype=dtype, topk=16).device().run().check()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(heads=(64, 8), topk=16), dict(heads=(32, 2), topk=16, dtype="bf16"), dict(heads=(8, 2), head_dim=64, topk=9),
+    dict(heads=(16, 8), ids=None),                 # dense, no prefix
+    dict(heads=(32, 2), ids=None, dtype="bf16"),
+], ids=_name)
+def test_long_and_short_histories_side_by_side(kw):
+    """Histories of one tile between histories of many, on every SM: the pipeline's groups
+    get ahead of and behind one another."""
+    lens = [(1, 5000, 100, 130, 7000, 3, 3000 + 7 * i, 250)[i % 8] for i in range(60)]
+    Problem(16, lens=lens, **kw).device().run().check()
+
+
 def _runs(*spans):
     """Consecutive queries of sequences: (first visible length, count) each."""
     lens, seq = [], []

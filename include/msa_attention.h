@@ -102,8 +102,10 @@ msa_status msa_attention_workspace_bytes(const msa_attention_cfg *cfg, int64_t n
  * lse            device fp32 [num_queries, Hq], or NULL.
  * workspace      device, 16-byte aligned, msa_attention_workspace_bytes(cfg,
  *                num_queries, 0) bytes; NULL only where that is 0.
- * launch_flags   MSA_LAUNCH_PDL: the first kernel is launched with programmatic
- *                dependent launch; everything is read and written after its wait.
+ * launch_flags   MSA_LAUNCH_PDL: accepted; the kernels are launched with programmatic
+ *                dependent launch in any case, since they read and write memory only
+ *                after waiting for the kernels ahead of them on the stream, and let the
+ *                next one start as soon as they have waited.
  *                MSA_LAUNCH_QUERY_RUNS: consecutive queries mostly belong to one
  *                sequence (the same table_offset) and agree on many blocks, as in a
  *                prefill chunk, so tiles of consecutive queries share the blocks that

@@ -347,18 +347,18 @@ msa_status launched(cudaError_t e)
     return e == cudaSuccess ? MSA_OK : fail(MSA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
 }
 
-msa_status launch_rows(const AttnParams &p, int head_dim, bool pdl, cudaStream_t stream)
+msa_status launch_rows(const AttnParams &p, int head_dim, cudaStream_t stream)
 {
     const int64_t grid = p.num_queries * p.hkv * ((p.group + kRowHeads - 1) / kRowHeads);
     void *args[] = {const_cast<AttnParams *>(&p)};
     return launched(attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_rows_kernel<128>)
                                                 : reinterpret_cast<const void *>(&msa_attention_rows_kernel<64>),
-                                grid, kRowThreads, 0, pdl, stream, args));
+                                grid, kRowThreads, 0, stream, args));
 }
 
-// Workspace: the cuts, the total, the window's prefix sums, then its pieces.
+// Workspace: the cuts, the window's prefix sums, then its pieces.
 constexpr int64_t kCutBytes = kAttnMaxCtas * 16;
-constexpr int64_t kPreBytes = kCutBytes + 256 + (kAttnWindow + 1) * 8 + 248;
+constexpr int64_t kPreBytes = kCutBytes + (kAttnWindow + 1) * 8 + 248;
 static_assert(kPreBytes % 256 == 0, "alignment of the pieces");
 
 int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t)
@@ -423,7 +423,7 @@ int tensor_sms()
 // (and blocks) a multiple of 8 tokens.  Fewer rows a box would mean more than 16 copies
 // a tile.
 struct Maps {
-    alignas(64) CUtensorMap k, v;
+    CUtensorMap k, v;
     int box_rows, sms;
     int32_t oob_page;
 };
@@ -441,15 +441,13 @@ void make_maps(Maps *m, const AttnParams &p, int head_dim)
 }
 
 // Single queries: windows of kAttnWindow queries, each the decode kernel and the join.
-msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void *workspace, bool pdl,
-                      cudaStream_t stream)
+msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void *workspace, cudaStream_t stream)
 {
     AttnPieces w;
     memset(&w, 0, sizeof w);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     w.cut = reinterpret_cast<int4 *>(ws);
-    w.total = reinterpret_cast<int64_t *>(ws + kCutBytes);
-    w.pre = reinterpret_cast<int64_t *>(ws + kCutBytes + 256);
+    w.pre = reinterpret_cast<int64_t *>(ws + kCutBytes);
     w.pieces = reinterpret_cast<float *>(ws + kPreBytes);
     w.heads = attn_decode_heads(p.group);
     w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
@@ -459,7 +457,7 @@ msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void 
     for (int64_t q0 = 0; q0 < p.num_queries; q0 += kAttnWindow) {
         w.q0 = q0;
         w.nq = p.num_queries - q0 < kAttnWindow ? p.num_queries - q0 : kAttnWindow;
-        msa_status s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, pdl || q0 > 0, stream));
+        msa_status s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, stream));
         if (s == MSA_OK)
             s = launched(attn_join_cut(p, w, head_dim, stream));
         if (s != MSA_OK)
@@ -470,7 +468,7 @@ msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void 
 
 }  // namespace
 
-cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, bool pdl, cudaStream_t stream, void **args)
+cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, cudaStream_t stream, void **args)
 {
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
@@ -482,7 +480,7 @@ cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, bool 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = pdl ? 1 : 0;
+    lc.numAttrs = 1;
     return cudaLaunchKernelExC(&lc, fn, args);
 }
 
@@ -526,12 +524,11 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
     AttnParams p = params_of(cfg, num_queries, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache,
                              scales, out, lse);
     p.topk_ids = topk_ids;
-    const bool pdl = launch_flags & MSA_LAUNCH_PDL;
     Maps maps;
     make_maps(&maps, p, cfg->head_dim);
     if (maps.box_rows == 0)
-        return launch_rows(p, cfg->head_dim, pdl, stream);
-    return run_decode(p, maps, cfg->head_dim, workspace, pdl, stream);
+        return launch_rows(p, cfg->head_dim, stream);
+    return run_decode(p, maps, cfg->head_dim, workspace, stream);
 }
 
 extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg, int64_t num_queries, const void *q,
@@ -566,10 +563,9 @@ extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg,
     p.prefix_len = prefix_len;
     p.prefix_offset = prefix_offset;
     p.num_groups = (int32_t)num_groups;
-    const bool pdl = launch_flags & MSA_LAUNCH_PDL;
     Maps maps;
     make_maps(&maps, p, cfg->head_dim);
     if (maps.box_rows == 0 || num_groups > 0)
-        return launch_rows(p, cfg->head_dim, pdl, stream);
-    return run_decode(p, maps, cfg->head_dim, workspace, pdl, stream);
+        return launch_rows(p, cfg->head_dim, stream);
+    return run_decode(p, maps, cfg->head_dim, workspace, stream);
 }

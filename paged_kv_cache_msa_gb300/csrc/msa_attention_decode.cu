@@ -27,7 +27,7 @@
 //              issue, a tile 8 of them, close to the tile's share of HBM time: two warps);
 //              warp 3 zeroes value rows past the history before they are multiplied
 //   warp 4     block lists and page lookups
-//   warp 5     query tiles, ahead of their use; queries that see nothing
+//   warps 5-7  query tiles, in turn, ahead of their use; queries that see nothing
 //   warps 8-15 two softmax and output groups: a thread is a token of each tile, then a dim
 // A (query, K/V head) that one CTA holds whole is written as bf16 right away; the pieces
 // of one that is cut between CTAs (at most two a CTA) go to the workspace, and a second,
@@ -47,7 +47,8 @@ constexpr int kThreads = 256 + 128 * kGroups;
 // has then waited on every phase before, as waiting by parity needs.
 constexpr int kGroupBufs = 3, kSBufs = kGroups * kGroupBufs;
 constexpr int kGroupInfo = 4, kInfo = kGroups * kGroupInfo;
-constexpr int kQSlots = 2 * kGroups;   // a multiple of the groups: a slot belongs to one
+constexpr int kBuilders = 3;      // warps that make query tiles, in turn
+constexpr int kQSlots = 6;        // a multiple of the groups and builders: a slot belongs to one of each
 constexpr int kSmallIds = 1024;   // ids of a window kept in shared memory
 constexpr int kMaxBoxes = 16;     // boxes of a tile: 128 / 8 rows
 
@@ -69,13 +70,16 @@ struct Shape {
     static constexpr int kSCols = kChunk * kN;                           // columns of one chunk's scores
     static constexpr int kTmem = 512;
     static_assert(kSBufs * kSCols + kGroups * kN <= kTmem, "tensor memory");
+    static_assert(kQSlots % kGroups == 0 && kQSlots % kBuilders == 0, "slots");
     static_assert(kQBytes % 1024 == 0 && (kChunk * kPBytes) % 1024 == 0, "swizzle pattern alignment");
 };
+
+__device__ __noinline__ int64_t div_slow(int64_t a, int64_t b) { return a / b; }
 
 // a / b for a >= 0, b > 0, in 32 bits where both fit
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
 {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : div_slow(a, b);
 }
 
 // A chunk: tiles [tile, tile + n) of (query q, head chunk hc), item `it` of the CTA's share.
@@ -251,40 +255,42 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     // and the first ids are read in one round of loads; the ids of small batches stay in
     // shared memory for the lists.
     static_assert(kAttnWindow <= kThreads, "a thread holds one query");
-    const int32_t len = tid < nq ? max(__ldg(p.kv_len + w.q0 + tid), 0) : 0;
-    if (tid < nq) {
-        s_toff[tid] = __ldg(p.table_offset + w.q0 + tid);
-        s_len[tid] = len;
-        s_cnt[tid] = 0;
-    }
-    if (p.topk_ids) {
-        constexpr int kBatch = 4;
-        const int ids = nq * p.topk;
-        const int32_t *src = p.topk_ids + w.q0 * p.topk;
-        for (int x0 = 0; x0 < ids; x0 += kBatch * kThreads) {
-            int32_t id[kBatch];
+    constexpr int kBatch = 4;
+    const int ids = p.topk_ids ? nq * p.topk : 0;
+    const int32_t *src = p.topk_ids + w.q0 * p.topk;
+    int32_t len = tid < nq ? __ldg(p.kv_len + w.q0 + tid) : 0;
+    const int64_t toff = tid < nq ? __ldg(p.table_offset + w.q0 + tid) : 0;
+    for (int x0 = 0; x0 == 0 || x0 < ids; x0 += kBatch * kThreads) {
+        int32_t id[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int x = x0 + i * kThreads + tid;
-                id[i] = x < ids ? __ldg(src + x) : -1;
-                if (x < kSmallIds)
-                    s_ids[x] = id[i];
+        for (int i = 0; i < kBatch; ++i) {
+            const int x = x0 + i * kThreads + tid;
+            id[i] = x < ids ? __ldg(src + x) : -1;
+        }
+        if (x0 == 0) {
+            len = max(len, 0);
+            if (tid < nq) {
+                s_toff[tid] = toff;
+                s_len[tid] = len;
+                s_cnt[tid] = 0;
             }
-            if (x0 == 0)
-                __syncthreads();       // the lengths and zeroed counts
+            __syncthreads();
+        }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int x = x0 + i * kThreads + tid;
-                if (id[i] >= 0) {
-                    const int q = (int)((uint32_t)x / (uint32_t)p.topk);
-                    // the id names a block when the block's first token is visible
-                    if ((int64_t)id[i] * p.block_tokens < s_len[q])
-                        atomicAdd(&s_cnt[q], 1);
-                }
+        for (int i = 0; i < kBatch; ++i) {
+            const int x = x0 + i * kThreads + tid;
+            if (x < kSmallIds && x < ids)
+                s_ids[x] = id[i];
+            if (id[i] >= 0) {
+                const int q = (int)((uint32_t)x / (uint32_t)p.topk);
+                // the id names a block when the block's first token is visible
+                if ((int64_t)id[i] * p.block_tokens < s_len[q])
+                    atomicAdd(&s_cnt[q], 1);
             }
         }
-        __syncthreads();
     }
+    if (ids > 0)
+        __syncthreads();
     int64_t sum = 0;
     if (tid < nq)
         sum = p.topk_ids ? (s_cnt[tid] * p.block_tokens + 127) / 128 : ((int64_t)len + 127) / 128;
@@ -301,15 +307,15 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    int64_t before = inc - sum, total = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    int64_t before = inc - sum, tiles = 0;
+    for (int i = 0; i < (nq + 31) / 32; ++i) {
         before += i < warp ? s_wsum[i] : 0;
-        total += s_wsum[i];
+        tiles += s_wsum[i];
     }
+    // equal shares, the last ones shorter or empty
     const int hcs = w.head_chunks;
-    total *= hcs;
-    const int64_t i0 = div64(total * blockIdx.x, gridDim.x), i1 = div64(total * (blockIdx.x + 1), gridDim.x);
+    const int64_t total = tiles * hcs, share = div64(total + gridDim.x - 1, gridDim.x);
+    const int64_t i0 = min(total, share * blockIdx.x), i1 = min(total, i0 + share);
     if (tid < nq) {
         if (before * hcs <= i0 && i0 < (before + sum) * hcs)
             s_qlo = tid;
@@ -317,12 +323,11 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         if (blockIdx.x == 0 && w.joined)
             w.pre[tid + 1] = before + sum;
     }
-    if (blockIdx.x == 0 && tid == 0 && w.joined)
-        w.pre[0] = 0;
-    if (tid == 0 && !w.joined)
+    if (tid == 0) {
+        if (blockIdx.x == 0 && w.joined)
+            w.pre[0] = 0;
         w.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (blockIdx.x == 0 && tid == 0)
-        *w.total = total;
+    }
     __syncthreads();
     Walk wk;
     wk.start(s_pre, nq, hcs, i0, i1, s_qlo);
@@ -369,12 +374,17 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         for (uint32_t s = 0; s < (uint32_t)ST && s < it; ++s)
             (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bars[s]), ((it - 1u - s) / ST) & 1u));
 #endif
-    } else if (warp == 5) {
-        // ---------------- query tiles ----------------
+    } else if (warp >= 5 && warp < 5 + kBuilders) {
+        // ---------------- query tiles: warp 5 + b the segments s with s % kBuilders == b ----------------
         uint32_t seg = 0;
         bool ok = true;
         while (!wk.done() && ok) {
             const uint32_t x = seg % kQSlots;
+            if ((int)(seg % kBuilders) != warp - 5) {
+                wk.step((int)min((int64_t)(wk.nt - wk.tile), wk.end - wk.it));
+                ++seg;
+                continue;
+            }
             ok = warp_wait(smem_u32(&bar_q_empty[x]), ((seg / kQSlots) & 1u) ^ 1u, abort_flag);
             if (!ok)
                 break;
@@ -382,44 +392,41 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             const int nh = min(NH, p.group - h0);
             const uint16_t *src = p.q + ((w.q0 + wk.q) * p.hq + c * p.group + h0) * D;
             constexpr int E = D / 32;                       // elements of a lane
-            uint32_t v[NH][E / 2];
-            float amax = 0.0f;
+            auto load = [&](int h, uint32_t (&v)[E / 2]) {
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    v[h][e] = h < nh ? __ldg(reinterpret_cast<const uint32_t *>(src + h * D) + lane * (E / 2) + e) : 0u;
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[h][e] << 16)),
-                                             fabsf(__uint_as_float(v[h][e] & 0xFFFF0000u))));
-                }
+                for (int e = 0; e < E / 2; ++e)
+                    v[e] = h < nh ? __ldg(reinterpret_cast<const uint32_t *>(src + h * D) + lane * (E / 2) + e) : 0u;
+            };
             const uint32_t tile = qbase + x * (uint32_t)S::kQBytes;
             if (FP8) {
                 // halves hi | lo under the power of two that brings the largest magnitude
                 // of the heads into [128, 256): hi has 4 significant bits, lo the next 4
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                int e2 = 0;
-                if (amax > 0.0f) {
-                    e2 = 7 - ((int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
-                    e2 = e2 > 126 ? 126 : e2;
-                }
-                const float sc = __int_as_float((e2 + 127) << 23);
-                const uint32_t byte = (uint32_t)lane * E;
+                uint32_t big = 0;                           // magnitudes compare as integers
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
-                    uint32_t hw = 0, lw = 0;
+                    uint32_t v[E / 2];
+                    load(h, v);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e)
+                        big = max(big, max((v[e] & 0x7FFFu) << 16, v[e] & 0x7FFF0000u));
+                }
+                big = __reduce_max_sync(0xffffffffu, big) >> 23;
+                const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
+                const float sc = __int_as_float((e2 + 127) << 23);
+#pragma unroll 2
+                for (int h = 0; h < NH; ++h) {              // read again, from L1
+                    uint32_t v[E / 2], hw = 0, lw = 0;
+                    load(h, v);
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
-                        const float x0 = __uint_as_float(v[h][e] << 16) * sc;
-                        const float x1 = __uint_as_float(v[h][e] & 0xFFFF0000u) * sc;
+                        const float x0 = __uint_as_float(v[e] << 16) * sc, x1 = __uint_as_float(v[e] & 0xFFFF0000u) * sc;
                         const uint32_t hi = e4m3x2_from_f32(x0, x1);
                         const float2 d = attn_e4m3x2_to_f2(hi);
                         hw |= hi << (16 * e);
                         lw |= e4m3x2_from_f32(x0 - d.x, x1 - d.y) << (16 * e);
                     }
-                    const uint32_t a = tile + swizzle<S::kSwz>((uint32_t)h * S::kSwz + byte);
-                    const uint32_t b = tile + swizzle<S::kSwz>((uint32_t)(NH + h) * S::kSwz + byte);
+                    const uint32_t a = tile + swizzle<S::kSwz>((uint32_t)(h * S::kSwz + lane * E));
+                    const uint32_t b = tile + swizzle<S::kSwz>((uint32_t)((NH + h) * S::kSwz + lane * E));
                     if (E == 4) {
                         sts32(a, hw);
                         sts32(b, lw);
@@ -432,12 +439,14 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     s_qinv[x] = __int_as_float((127 - e2) << 23);
             } else {
                 const uint32_t byte = (uint32_t)lane * 2 * E, at = byte / S::kSwz, col = byte % S::kSwz;
-#pragma unroll
+#pragma unroll 4
                 for (int h = 0; h < NH; ++h) {
+                    uint32_t v[E / 2];
+                    load(h, v);
                     const uint32_t a = tile + at * (uint32_t)(N * S::kSwz) + swizzle<S::kSwz>((uint32_t)h * S::kSwz + col);
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e)
-                        sts32(a + 4 * e, v[h][e]);
+                        sts32(a + 4 * e, v[e]);
                 }
                 if (lane == 0)
                     s_qinv[x] = 1.0f;
@@ -451,7 +460,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             ++seg;
         }
         // queries that see nothing are in no CTA's share
-        for (int q = blockIdx.x; q < nq && !w.joined; q += gridDim.x)
+        for (int q = blockIdx.x; q < nq && !w.joined && warp == 5; q += gridDim.x)
             if (s_pre[q + 1] == s_pre[q]) {
                 const int64_t row = (w.q0 + q) * p.hq;
                 uint32_t *out = reinterpret_cast<uint32_t *>(p.out + row * D);
@@ -592,13 +601,16 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                 const bool v0 = a0 >= 0 && a0 < nb, v1 = a1 >= 0 && a1 < nb;
                 const uint32_t m0 = __ballot_sync(0xffffffffu, v0), m1 = __ballot_sync(0xffffffffu, v1);
                 const uint32_t below = (1u << lane) - 1u;
-                const uint32_t same0 = __match_any_sync(0xffffffffu, v0 ? a0 : -1 - lane);
-                const uint32_t same1 = __match_any_sync(0xffffffffu, v1 ? a1 : -1 - lane);
-                const bool dup0 = (same0 & below) != 0;
-                bool dup1 = (same1 & below) != 0;
-                if (m1)   // the second half against the first
-                    for (int i = 0; i < 32; ++i)
-                        dup1 |= __shfl_sync(0xffffffffu, a0, i) == a1;
+                bool dup0 = false, dup1 = false;       // of an id before it
+                for (int i = 0; i < min(p.topk, 32); ++i) {
+                    const int32_t x = __shfl_sync(0xffffffffu, a0, i);
+                    dup0 |= i < lane && x == a0;
+                    dup1 |= x == a1;
+                }
+                for (int i = 32; i < p.topk; ++i) {
+                    const int32_t x = __shfl_sync(0xffffffffu, a1, i - 32);
+                    dup1 |= i < lane + 32 && x == a1;
+                }
                 __syncwarp();
                 if (v0)
                     s_list[__popc(m0 & below)] = dup0 ? -1 : a0;
@@ -811,34 +823,40 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                 const bool whole = wk.tile + n == wk.nt && wk.it + n - i0 >= wk.nt;
                 const bool began = wk.it - wk.tile >= i0;      // in this CTA
                 const int nh = min(NH, p.group - hcol);
-                const int64_t t = w.q0 + wk.q;
+                const int64_t hr = (w.q0 + wk.q) * p.hq + head * p.group + hcol;
+                float hm = m[0], hl = l[0];      // of head `row`, for the threads that have one
+#pragma unroll
+                for (int h = 1; h < NH; ++h) {
+                    hm = row == h ? m[h] : hm;
+                    hl = row == h ? l[h] : hl;
+                }
+                const float scale = vs * (1.0f / kPScale);
                 if (whole && !w.joined) {
-                    const int64_t hr = t * p.hq + head * p.group + hcol;
+                    uint16_t *out = p.out + hr * D + row;
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
                         if (h < nh && row < D) {
-                            const float o = l[h] == 0.0f ? 0.0f : acc[h] * __fdividef(vs * (1.0f / kPScale), l[h]);
-                            p.out[(hr + h) * D + row] = attn_bf16(good ? o : bad);
-                            if (row == 0 && p.lse)
-                                p.lse[hr + h] = good ? attn_lse(m[h], l[h]) : bad;
+                            const float o = l[h] == 0.0f ? 0.0f : acc[h] * __fdividef(scale, l[h]);
+                            out[h * D] = attn_bf16(good ? o : bad);
                         }
+                    if (row < nh && p.lse)
+                        p.lse[hr + row] = good ? attn_lse(hm, hl) : bad;
                 } else {
                     const int64_t sl = whole ? 2 * (int64_t)gridDim.x + (int64_t)wk.q * hcs + wk.hc
                                              : (began ? (int64_t)gridDim.x : 0) + blockIdx.x;
                     float *piece = w.pieces + sl * (int64_t)(NH * (D + 2));
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
-                        if (row < D) {
-                            piece[h * D + row] = good ? acc[h] * (vs * (1.0f / kPScale)) : bad;
-                            if (row == 0) {
-                                piece[NH * D + h] = good ? m[h] : bad;
-                                piece[NH * D + NH + h] = good ? l[h] : bad;
-                            }
-                        }
+                        if (row < D)
+                            piece[h * D + row] = good ? acc[h] * scale : bad;
+                    if (row < NH) {
+                        piece[NH * D + row] = good ? hm : bad;
+                        piece[NH * D + NH + row] = good ? hl : bad;
+                    }
                     // the CTA in which it began lists it for the join
                     if (began && !whole && !w.joined && row == 0) {
                         const int64_t base = wk.it - wk.tile;
-                        w.cut[blockIdx.x] = make_int4(wk.q, wk.hc, (int)div64((base + wk.nt) * gridDim.x - 1, total), 0);
+                        w.cut[blockIdx.x] = make_int4(wk.q, wk.hc, (int)div64(base + wk.nt - 1, share), 0);
                     }
                 }
                 ++seg;
@@ -912,24 +930,17 @@ struct Row {
     }
 };
 
-// Adds the pieces that CTAs c0 .. c1 hold of a (query, head chunk), column `col`; `whole`
-// is the slot of one that a single CTA holds.
+// Adds column `col` of the pieces of a (query, head chunk) that began in CTA c0 and ended
+// in c1: the slots ctas + c0, c0 + 1, ..., c1, or `whole` where c1 == c0.
 template <int D>
-__device__ __forceinline__ void add_pieces(Row<D> &r, const AttnPieces &w, int64_t total, int64_t c0, int64_t c1,
-                                           int64_t whole, int col, int lane)
+__device__ __forceinline__ void add_pieces(Row<D> &r, const AttnPieces &w, int c0, int c1, int64_t whole, int col,
+                                           int lane)
 {
-    const int64_t n = w.ctas, size = (int64_t)w.heads * (D + 2);
-    for (int64_t i0 = c0; i0 <= c1; i0 += 32) {
-        // CTA i holds items [total * i / n, total * (i + 1) / n), maybe none
-        const int64_t i = i0 + lane;
-        const bool has = i <= c1 && (i == c0 || div64(total * i, n) < div64(total * (i + 1), n));
-        const uint32_t mask = __ballot_sync(0xffffffffu, has);
-        const int src = lane < __popc(mask) ? (int)__fns(mask, 0, lane + 1) : 0;
-        const int64_t j = i0 + src;
-        const float *piece = w.pieces + (j > c0 ? j : c0 == c1 ? whole : n + c0) * size;
-        const bool in = lane < __popc(mask);
-        r.add(__popc(mask), piece + col * D, in ? __ldcg(piece + w.heads * D + col) : 0.0f,
-              in ? __ldcg(piece + w.heads * D + w.heads + col) : 0.0f, lane);
+    const int size = w.heads * (D + 2);
+    for (int i0 = c0; i0 <= c1; i0 += 32) {
+        const int i = min(i0 + lane, c1), count = min(32, c1 - i0 + 1);
+        const float *piece = w.pieces + (i > c0 ? (int64_t)i : c0 == c1 ? whole : (int64_t)w.ctas + c0) * size;
+        r.add(count, piece + col * D, __ldcg(piece + w.heads * D + col), __ldcg(piece + w.heads * (D + 1) + col), lane);
     }
 }
 
@@ -943,19 +954,18 @@ msa_attention_join_cut_kernel(const __grid_constant__ AttnParams p, const __grid
     asm volatile("griddepcontrol.launch_dependents;" :::);
     const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;
     const int4 cut = __ldcg(w.cut + blockIdx.x);
-    const int64_t total = __ldcg(w.total);
     const int nch = (p.group + w.heads - 1) / w.heads;
     const int head = cut.y / nch, hcol = cut.y % nch * w.heads;
     if (cut.x < 0 || hcol + col >= p.group)
         return;
     Row<D> r;
-    add_pieces<D>(r, w, total, blockIdx.x, cut.z, 0, col, lane);
+    add_pieces<D>(r, w, blockIdx.x, cut.z, 0, col, lane);
     r.write(p, (w.q0 + cut.x) * p.hq + head * p.group + hcol + col, lane);
 }
 
 template <int D, bool FP8, int NH>
 cudaError_t launch_decode(const AttnParams &p, const AttnPieces &w, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                          bool pdl, cudaStream_t stream)
+                          cudaStream_t stream)
 {
     using S = Shape<D, FP8, NH>;
     const void *fn = reinterpret_cast<const void *>(&msa_attention_decode_kernel<D, FP8, NH>);
@@ -964,7 +974,7 @@ cudaError_t launch_decode(const AttnParams &p, const AttnPieces &w, const CUtens
         return e;
     void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w), const_cast<CUtensorMap *>(&kmap),
                     const_cast<CUtensorMap *>(&vmap)};
-    return attn_launch(fn, w.ctas, kThreads, S::kSmem, pdl, stream, args);
+    return attn_launch(fn, w.ctas, kThreads, S::kSmem, stream, args);
 }
 
 }  // namespace
@@ -972,18 +982,18 @@ cudaError_t launch_decode(const AttnParams &p, const AttnPieces &w, const CUtens
 int attn_decode_heads(int group) { return group <= 8 ? 8 : 16; }
 
 cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
-                        const CUtensorMap &vmap, bool pdl, cudaStream_t stream)
+                        const CUtensorMap &vmap, cudaStream_t stream)
 {
     const bool f8 = p.k.fp8, h8 = w.heads == 8;
     if (head_dim == 128)
-        return f8 ? (h8 ? launch_decode<128, true, 8>(p, w, kmap, vmap, pdl, stream)
-                        : launch_decode<128, true, 16>(p, w, kmap, vmap, pdl, stream))
-                  : (h8 ? launch_decode<128, false, 8>(p, w, kmap, vmap, pdl, stream)
-                        : launch_decode<128, false, 16>(p, w, kmap, vmap, pdl, stream));
-    return f8 ? (h8 ? launch_decode<64, true, 8>(p, w, kmap, vmap, pdl, stream)
-                    : launch_decode<64, true, 16>(p, w, kmap, vmap, pdl, stream))
-              : (h8 ? launch_decode<64, false, 8>(p, w, kmap, vmap, pdl, stream)
-                    : launch_decode<64, false, 16>(p, w, kmap, vmap, pdl, stream));
+        return f8 ? (h8 ? launch_decode<128, true, 8>(p, w, kmap, vmap, stream)
+                        : launch_decode<128, true, 16>(p, w, kmap, vmap, stream))
+                  : (h8 ? launch_decode<128, false, 8>(p, w, kmap, vmap, stream)
+                        : launch_decode<128, false, 16>(p, w, kmap, vmap, stream));
+    return f8 ? (h8 ? launch_decode<64, true, 8>(p, w, kmap, vmap, stream)
+                    : launch_decode<64, true, 16>(p, w, kmap, vmap, stream))
+              : (h8 ? launch_decode<64, false, 8>(p, w, kmap, vmap, stream)
+                    : launch_decode<64, false, 16>(p, w, kmap, vmap, stream));
 }
 
 cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream)
@@ -991,5 +1001,5 @@ cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim
     void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w)};
     return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<128>)
                                        : reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<64>),
-                       w.ctas, w.heads * 32, 0, true, stream, args);
+                       w.ctas, w.heads * 32, 0, stream, args);
 }

@@ -45,13 +45,12 @@ struct AttnParams {
 };
 
 // What the decode and join kernels need beside AttnParams: a window of queries and its
-// part of the workspace.  CTA i holds the items [total * i / ctas, total * (i + 1) / ctas)
-// of the list over (query, head chunk, tile); the piece of a (query, head chunk) that
+// part of the workspace.  CTA i holds the items [share * i, share * (i + 1)) of the list
+// over (query, head chunk, tile), share = ceil(items / ctas); the piece of a (query, head chunk) that
 // began in another CTA is in slot i, of one that goes on in the next in slot ctas + i, and
 // (joined) a whole one in slot 2 * ctas + query * head_chunks + head chunk.  A piece is
 // [heads][D] of output (relative to the maximum), then the maxima, then the sums.
 struct AttnPieces {
-    int64_t *total;                  // items of the list
     int4 *cut;                       // [ctas]: query, head chunk and last CTA of the one that
                                      // began in a CTA and goes on in the next; query -1: none
     int64_t *pre;                    // [nq + 1]: tiles before each query of the window (joined)
@@ -65,12 +64,13 @@ struct AttnPieces {
     int32_t joined;                  // every piece goes to the workspace
 };
 
-// One launch; `pdl` with programmatic dependent launch.
-cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, bool pdl, cudaStream_t stream, void **args);
+// One launch, with programmatic dependent launch: every kernel of these operators waits
+// for the kernels ahead of it before it touches memory, so it may always start early.
+cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, cudaStream_t stream, void **args);
 
 int attn_decode_heads(int group);
 cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
-                        const CUtensorMap &vmap, bool pdl, cudaStream_t stream);
+                        const CUtensorMap &vmap, cudaStream_t stream);
 cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream);
 
 #ifdef __CUDACC__

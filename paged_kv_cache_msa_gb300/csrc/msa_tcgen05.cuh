@@ -48,7 +48,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 
 // true once the phase with the given parity has completed; false after the limit
 // (MSA_WAIT_LIMIT_NS, 2 s)
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
+__device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 {
     if (mbar_try(bar, parity))
         return true;

@@ -131,7 +131,7 @@ msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg, int64_t nu
  * no prefix.  (With group_start non-decreasing, group g holds the queries
  * group_start[g] .. group_start[g + 1] - 1.)
  *
- * num_groups     0..1024; 0: no prefixes, and the three group arrays may be NULL.
+ * num_groups     0..512; 0: no prefixes, and the three group arrays may be NULL.
  * group_start    device int32 [num_groups + 1].
  * prefix_len     device int32 [num_groups] (< 0 as 0); any length, whole pages or not.
  * prefix_offset  device int64 [num_groups].

@@ -14,7 +14,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("msa_producer.cu", "msa_indexer.cu", "msa_projection.cu",
-                                                    "msa_attention.cu", "msa_attention_decode.cu")]
+                                                    "msa_attention.cu", "msa_attention_decode.cu",
+                                                    "msa_attention_tile.cu")]
 HEADERS = [os.path.join(PKG, "csrc", n) for n in ("msa_internal.h", "msa_attention_internal.h",
                                                     "msa_tcgen05.cuh")]
 INCLUDE = os.path.join(ROOT, "include")

@@ -356,17 +356,34 @@ msa_status launch_rows(const AttnParams &p, int head_dim, cudaStream_t stream)
                                 grid, kRowThreads, 0, stream, args));
 }
 
-// Workspace: the cuts, the window's prefix sums, then its pieces.
-constexpr int64_t kCutBytes = kAttnMaxCtas * 16;
-constexpr int64_t kPreBytes = kCutBytes + (kAttnWindow + 1) * 8 + 248;
-static_assert(kPreBytes % 256 == 0, "alignment of the pieces");
+// The workspace: cuts, prefix sums and groups of a window, the decode kernel's slots, the
+// tile kernel's slots, and with groups the whole units' rows of both.  Sizes are those of
+// the largest grids, so that they do not depend on the device.
+struct Layout {
+    int64_t pre, groups, pieces, tile_pieces, rows, tile_rows, bytes;
+};
 
-int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t)
+constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+Layout layout_of(const msa_attention_cfg *cfg, int64_t T, int64_t num_groups)
 {
-    if (T == 0)
-        return 0;
-    const int64_t nh = attn_decode_heads(cfg->num_q_heads / cfg->num_kv_heads);
-    return kPreBytes + 2 * (int64_t)kAttnMaxCtas * nh * (cfg->head_dim + 2) * 4;
+    const int64_t nh = attn_decode_heads(cfg->num_q_heads / cfg->num_kv_heads), D = cfg->head_dim;
+    const int64_t window = T < kAttnWindow ? T : kAttnWindow;
+    const int64_t rows = num_groups > 0 ? align256(window * cfg->num_q_heads * (D + 4) * 4) : 0;
+    Layout l;
+    l.pre = align256(kAttnMaxCtas * 16);
+    l.groups = l.pre + align256((kAttnWindow + 1) * 8);
+    l.pieces = l.groups + align256(sizeof(AttnGroups));
+    l.tile_pieces = l.pieces + align256(2 * (int64_t)kAttnMaxCtas * nh * (D + 2) * 4);
+    l.rows = l.tile_pieces + align256(2 * (int64_t)(2 * kAttnMaxCtas) * 128 * (D + 2) * 4);
+    l.tile_rows = l.rows + rows;
+    l.bytes = T == 0 ? 0 : l.tile_rows + rows;
+    return l;
+}
+
+int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t num_groups)
+{
+    return layout_of(cfg, T, num_groups).bytes;
 }
 
 // Rows of the widest TMA box that never crosses a page or a selected block: a power of two.
@@ -440,26 +457,102 @@ void make_maps(Maps *m, const AttnParams &p, int head_dim)
     m->oob_page = (int32_t)(p.k.num_pages > p.v.num_pages ? p.k.num_pages : p.v.num_pages);
 }
 
-// Single queries: windows of kAttnWindow queries, each the decode kernel and the join.
-msa_status run_decode(const AttnParams &p, const Maps &maps, int head_dim, void *workspace, cudaStream_t stream)
+AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, void *workspace)
 {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     AttnPieces w;
     memset(&w, 0, sizeof w);
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
     w.cut = reinterpret_cast<int4 *>(ws);
-    w.pre = reinterpret_cast<int64_t *>(ws + kCutBytes);
-    w.pieces = reinterpret_cast<float *>(ws + kPreBytes);
+    w.pre = reinterpret_cast<int64_t *>(ws + l.pre);
+    w.pieces = reinterpret_cast<float *>(ws + l.pieces);
+    w.rows = reinterpret_cast<float *>(ws + l.rows);
     w.heads = attn_decode_heads(p.group);
     w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
     w.ctas = maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas;
     w.box_rows = maps.box_rows;
     w.oob_page = maps.oob_page;
-    for (int64_t q0 = 0; q0 < p.num_queries; q0 += kAttnWindow) {
-        w.q0 = q0;
-        w.nq = p.num_queries - q0 < kAttnWindow ? p.num_queries - q0 : kAttnWindow;
+    return w;
+}
+
+// gp_shift: rows of a query, a power of two that holds the heads on a K/V head.
+AttnTiles tiles_of(const AttnParams &p, const Maps &maps, const Layout &l, void *workspace, int gp_shift)
+{
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    AttnTiles t;
+    memset(&t, 0, sizeof t);
+    t.groups = reinterpret_cast<AttnGroups *>(ws + l.groups);
+    t.pieces = reinterpret_cast<float *>(ws + l.tile_pieces);
+    t.rows = reinterpret_cast<float *>(ws + l.tile_rows);
+    t.nq = p.num_queries;
+    t.gp_shift = gp_shift;
+    t.splits = 1;
+    t.ctas = 2 * (maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas);     // two a SM
+    t.box_rows = maps.box_rows;
+    t.oob_page = maps.oob_page;
+    return t;
+}
+
+int group_shift(int group)
+{
+    int s = 0;
+    while ((1 << s) < group)
+        ++s;
+    return s;
+}
+
+// Single queries: windows of kAttnWindow queries, each the decode kernel and the join of
+// what was cut between its CTAs.
+msa_status run_decode(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace,
+                      cudaStream_t stream)
+{
+    AttnPieces w = pieces_of(p, maps, l, workspace);
+    for (w.q0 = 0; w.q0 < p.num_queries; w.q0 += kAttnWindow) {
+        w.nq = p.num_queries - w.q0 < kAttnWindow ? p.num_queries - w.q0 : kAttnWindow;
         msa_status s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, stream));
         if (s == MSA_OK)
             s = launched(attn_join_cut(p, w, head_dim, stream));
+        if (s != MSA_OK)
+            return s;
+    }
+    return MSA_OK;
+}
+
+// Runs of queries: a CTA for each tile and K/V head, or, where these are fewer than the
+// machine holds, several that share its blocks and a join.
+msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace,
+                          cudaStream_t stream)
+{
+    int shift = group_shift(p.group);
+    while ((128 >> shift) > 32 || (128 >> shift) * p.topk > kAttnTileList)
+        ++shift;
+    AttnTiles t = tiles_of(p, maps, l, workspace, shift);
+    const int64_t qt = 128 >> shift, units = (p.num_queries + qt - 1) / qt * p.hkv;
+    const int64_t fit = t.ctas / units;
+    t.splits = fit > 1 ? (int32_t)(fit < 16 ? fit : 16) : 1;
+    t.ctas = (int32_t)(units * t.splits);
+    msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
+    if (s == MSA_OK && t.splits > 1)
+        s = launched(attn_join_splits(p, t, head_dim, stream));
+    return s;
+}
+
+// Prefixes: windows of queries, each the tile kernel over the prefixes, the decode kernel
+// over the queries' own tokens, and the join of both.
+msa_status run_prefix(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace,
+                      cudaStream_t stream)
+{
+    AttnPieces w = pieces_of(p, maps, l, workspace);
+    AttnTiles t = tiles_of(p, maps, l, workspace, group_shift(p.group));
+    w.joined = 1;
+    for (w.q0 = 0; w.q0 < p.num_queries; w.q0 += kAttnWindow) {
+        w.nq = p.num_queries - w.q0 < kAttnWindow ? p.num_queries - w.q0 : kAttnWindow;
+        t.q0 = w.q0;
+        t.nq = w.nq;
+        msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
+        if (s == MSA_OK)
+            s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, stream));
+        if (s == MSA_OK)
+            s = launched(attn_join_rows(p, w, t, head_dim, stream));
         if (s != MSA_OK)
             return s;
     }
@@ -528,7 +621,11 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
     make_maps(&maps, p, cfg->head_dim);
     if (maps.box_rows == 0)
         return launch_rows(p, cfg->head_dim, stream);
-    return run_decode(p, maps, cfg->head_dim, workspace, stream);
+    const Layout l = layout_of(cfg, num_queries, 0);
+    // tiles are of 128 tokens of one block
+    if ((launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % 128 == 0)
+        return run_query_runs(p, maps, l, cfg->head_dim, workspace, stream);
+    return run_decode(p, maps, l, cfg->head_dim, workspace, stream);
 }
 
 extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg, int64_t num_queries, const void *q,
@@ -565,7 +662,9 @@ extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg,
     p.num_groups = (int32_t)num_groups;
     Maps maps;
     make_maps(&maps, p, cfg->head_dim);
-    if (maps.box_rows == 0 || num_groups > 0)
+    if (maps.box_rows == 0)
         return launch_rows(p, cfg->head_dim, stream);
-    return run_decode(p, maps, cfg->head_dim, workspace, stream);
+    const Layout l = layout_of(cfg, num_queries, num_groups);
+    return num_groups > 0 ? run_prefix(p, maps, l, cfg->head_dim, workspace, stream)
+                          : run_decode(p, maps, l, cfg->head_dim, workspace, stream);
 }

@@ -841,10 +841,18 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         }
                     if (row < nh && p.lse)
                         p.lse[hr + row] = good ? attn_lse(hm, hl) : bad;
+                } else if (whole) {
+                    float *rows = w.rows + ((int64_t)wk.q * p.hq + head * p.group + hcol) * (D + 4);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        if (h < nh && row < D)
+                            rows[h * (D + 4) + row] = good ? acc[h] * scale : bad;
+                    if (row < nh) {
+                        rows[row * (D + 4) + D] = good ? hm : bad;
+                        rows[row * (D + 4) + D + 1] = good ? hl : bad;
+                    }
                 } else {
-                    const int64_t sl = whole ? 2 * (int64_t)gridDim.x + (int64_t)wk.q * hcs + wk.hc
-                                             : (began ? (int64_t)gridDim.x : 0) + blockIdx.x;
-                    float *piece = w.pieces + sl * (int64_t)(NH * (D + 2));
+                    float *piece = w.pieces + ((began ? (int64_t)gridDim.x : 0) + blockIdx.x) * (int64_t)(NH * (D + 2));
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
                         if (row < D)
@@ -854,7 +862,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         piece[NH * D + NH + row] = good ? hl : bad;
                     }
                     // the CTA in which it began lists it for the join
-                    if (began && !whole && !w.joined && row == 0) {
+                    if (began && !w.joined && row == 0) {
                         const int64_t base = wk.it - wk.tile;
                         w.cut[blockIdx.x] = make_int4(wk.q, wk.hc, (int)div64(base + wk.nt - 1, share), 0);
                     }
@@ -930,18 +938,30 @@ struct Row {
     }
 };
 
-// Adds column `col` of the pieces of a (query, head chunk) that began in CTA c0 and ended
-// in c1: the slots ctas + c0, c0 + 1, ..., c1, or `whole` where c1 == c0.
+// Adds the pieces 0 .. n - 1; piece(i, o, ml) gives where piece i's output row, maximum and
+// sum are.
+template <int D, typename Fn>
+__device__ __forceinline__ void add_pieces(Row<D> &r, int n, int lane, Fn &&piece)
+{
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const float *o, *pm, *pl;
+        piece(min(i0 + lane, n - 1), o, pm, pl);
+        r.add(min(32, n - i0), o, __ldcg(pm), __ldcg(pl), lane);
+    }
+}
+
+// Column `col` of a (query, head chunk) that began in CTA c0 and ended in c1 > c0: the
+// slots ctas + c0, c0 + 1, ..., c1.
 template <int D>
-__device__ __forceinline__ void add_pieces(Row<D> &r, const AttnPieces &w, int c0, int c1, int64_t whole, int col,
-                                           int lane)
+__device__ __forceinline__ void add_cut(Row<D> &r, const AttnPieces &w, int c0, int c1, int col, int lane)
 {
     const int size = w.heads * (D + 2);
-    for (int i0 = c0; i0 <= c1; i0 += 32) {
-        const int i = min(i0 + lane, c1), count = min(32, c1 - i0 + 1);
-        const float *piece = w.pieces + (i > c0 ? (int64_t)i : c0 == c1 ? whole : (int64_t)w.ctas + c0) * size;
-        r.add(count, piece + col * D, __ldcg(piece + w.heads * D + col), __ldcg(piece + w.heads * (D + 1) + col), lane);
-    }
+    add_pieces<D>(r, c1 - c0 + 1, lane, [&](int i, const float *&o, const float *&pm, const float *&pl) {
+        const float *piece = w.pieces + (int64_t)(i > 0 ? c0 + i : w.ctas + c0) * size;
+        o = piece + col * D;
+        pm = piece + w.heads * D + col;
+        pl = pm + w.heads;
+    });
 }
 
 // The (query, head chunk)s that a CTA began and did not finish: one block a CTA, one warp
@@ -959,8 +979,97 @@ msa_attention_join_cut_kernel(const __grid_constant__ AttnParams p, const __grid
     if (cut.x < 0 || hcol + col >= p.group)
         return;
     Row<D> r;
-    add_pieces<D>(r, w, blockIdx.x, cut.z, 0, col, lane);
+    add_cut<D>(r, w, blockIdx.x, cut.z, col, lane);
     r.write(p, (w.q0 + cut.x) * p.hq + head * p.group + hcol + col, lane);
+}
+
+constexpr int kJoinWarps = 8;
+
+// A window's rows: each query's own tokens and the prefix of its group.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+msa_attention_join_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPieces w,
+                               const __grid_constant__ AttnTiles tl)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    const int lane = threadIdx.x & 31;
+    const int x = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);       // below 384 x 128 x 1024
+    if (x >= w.nq * p.hq)
+        return;
+    const int q = x / p.hq, h = x - q * p.hq, c = h / p.group, hg = h - c * p.group;
+    Row<D> r;
+    auto add_whole = [&](const float *rows) {
+        add_pieces<D>(r, 1, lane, [&](int, const float *&o, const float *&pm, const float *&pl) {
+            o = rows + (int64_t)x * (D + 4);
+            pm = o + D;
+            pl = o + D + 1;
+        });
+    };
+    // its own tokens
+    const int64_t lo = __ldcg(w.pre + q), nt = __ldcg(w.pre + q + 1) - lo;
+    if (nt > 0) {
+        const int nch = (p.group + w.heads - 1) / w.heads;
+        const int64_t share = div64(__ldcg(w.pre + w.nq) * w.head_chunks + w.ctas - 1, w.ctas);
+        const int64_t base = lo * w.head_chunks + (int64_t)(c * nch + hg / w.heads) * nt;
+        const int c0 = (int)div64(base, share), c1 = (int)div64(base + nt - 1, share);
+        if (c0 == c1)
+            add_whole(w.rows);
+        else
+            add_cut<D>(r, w, c0, c1, hg % w.heads, lane);
+    }
+    // its group's prefix: the group before the first that starts after it
+    int g = -1;
+    for (int i0 = 0; i0 <= p.num_groups && g < 0; i0 += 32) {
+        const bool after = i0 + lane <= p.num_groups && __ldcg(tl.groups->start + min(i0 + lane, p.num_groups)) > q;
+        const uint32_t first = __ballot_sync(0xffffffffu, after);
+        if (first)
+            g = i0 + __ffs(first) - 1;
+    }
+    if (--g >= 0) {
+        const int64_t nb = ((int64_t)__ldcg(tl.groups->len + g) + 127) / 128;
+        if (nb > 0) {
+            const int at = q - __ldcg(tl.groups->start + g), qt = 128 >> tl.gp_shift;
+            const int64_t share = __ldcg(&tl.groups->share);
+            const int64_t base = __ldcg(tl.groups->item + g) + ((int64_t)(at / qt) * p.hkv + c) * nb;
+            const int c0 = (int)div64(base, share), c1 = (int)div64(base + nb - 1, share);
+            const int row = ((at % qt) << tl.gp_shift) + hg;
+            if (c0 == c1)
+                add_whole(tl.rows);
+            else
+                add_pieces<D>(r, c1 - c0 + 1, lane, [&](int i, const float *&o, const float *&pm, const float *&pl) {
+                    const float *piece = tl.pieces + (int64_t)(i > 0 ? c0 + i : tl.ctas + c0) * (128 * (D + 2));
+                    o = piece + row * D;
+                    pm = piece + 128 * D + 2 * row;
+                    pl = pm + 1;
+                });
+        }
+    }
+    r.write(p, w.q0 * p.hq + x, lane);
+}
+
+// Sparse tiles whose blocks several CTAs share.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+msa_attention_join_splits_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnTiles tl)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    const int lane = threadIdx.x & 31;
+    const int x = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    if (x >= p.num_queries * p.hq)
+        return;
+    const int q = x / p.hq, h = x - q * p.hq, c = h / p.group, hg = h - c * p.group;
+    const int qt = 128 >> tl.gp_shift, row = ((q % qt) << tl.gp_shift) + hg;
+    const int64_t unit = (int64_t)(q / qt) * p.hkv + c;
+    Row<D> r;
+    add_pieces<D>(r, tl.splits, lane, [&](int i, const float *&o, const float *&pm, const float *&pl) {
+        const float *piece = tl.pieces + (unit * tl.splits + i) * (128 * (D + 2));
+        o = piece + row * D;
+        pm = piece + 128 * D + 2 * row;
+        pl = pm + 1;
+    });
+    r.write(p, x, lane);
 }
 
 template <int D, bool FP8, int NH>
@@ -1002,4 +1111,21 @@ cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim
     return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<128>)
                                        : reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<64>),
                        w.ctas, w.heads * 32, 0, stream, args);
+}
+
+cudaError_t attn_join_rows(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim,
+                           cudaStream_t stream)
+{
+    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w), const_cast<AttnTiles *>(&tiles)};
+    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_rows_kernel<128>)
+                                       : reinterpret_cast<const void *>(&msa_attention_join_rows_kernel<64>),
+                       (w.nq * p.hq + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, args);
+}
+
+cudaError_t attn_join_splits(const AttnParams &p, const AttnTiles &tiles, int head_dim, cudaStream_t stream)
+{
+    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnTiles *>(&tiles)};
+    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_splits_kernel<128>)
+                                       : reinterpret_cast<const void *>(&msa_attention_join_splits_kernel<64>),
+                       (p.num_queries * p.hq + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, args);
 }

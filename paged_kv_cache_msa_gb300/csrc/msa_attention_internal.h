@@ -8,9 +8,10 @@
 
 #include <cstdint>
 
-constexpr int kAttnMaxGroups = 1024;
+constexpr int kAttnMaxGroups = 512;
 constexpr int kAttnWindow = 384;     // queries a launch of the tensor-core decode kernel takes
 constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
+constexpr int kAttnTileList = 1024;  // (query, id) pairs of a sparse tile
 
 // One cache as the kernels see it; strides in elements.
 struct AttnCache {
@@ -44,17 +45,21 @@ struct AttnParams {
     float scale_log2;                // softmax_scale * log2(e): scores are kept as powers of two
 };
 
-// What the decode and join kernels need beside AttnParams: a window of queries and its
-// part of the workspace.  CTA i holds the items [share * i, share * (i + 1)) of the list
-// over (query, head chunk, tile), share = ceil(items / ctas); the piece of a (query, head chunk) that
-// began in another CTA is in slot i, of one that goes on in the next in slot ctas + i, and
-// (joined) a whole one in slot 2 * ctas + query * head_chunks + head chunk.  A piece is
-// [heads][D] of output (relative to the maximum), then the maxima, then the sums.
+// A piece of a row's attention: its output relative to the maximum, the maximum (of the
+// scores times log2 e) and the sum.  Pieces of whole units are rows of D + 4 floats
+// [output | maximum | sum | unused], indexed by (query of the window, query head).
+//
+// What the decode kernel needs beside AttnParams: a window of queries and its part of the
+// workspace.  CTA i holds the items [share * i, share * (i + 1)) of the list over (query,
+// head chunk, tile), share = ceil(items / ctas); the piece of a (query, head chunk) that
+// began in another CTA is in slot i, of one that goes on in the next in slot ctas + i: a
+// slot is [heads][D] of output, then the maxima, then the sums.
 struct AttnPieces {
     int4 *cut;                       // [ctas]: query, head chunk and last CTA of the one that
                                      // began in a CTA and goes on in the next; query -1: none
     int64_t *pre;                    // [nq + 1]: tiles before each query of the window (joined)
-    float *pieces;
+    float *pieces;                   // slots
+    float *rows;                     // whole units (joined)
     int64_t q0, nq;                  // the window
     int32_t heads;                   // query heads of a head chunk: 8 or 16
     int32_t head_chunks;             // of all K/V heads
@@ -64,6 +69,29 @@ struct AttnPieces {
     int32_t joined;                  // every piece goes to the workspace
 };
 
+// The groups of a window, made by the tile kernel: queries start[g] .. start[g + 1] - 1 of
+// the window have a prefix of len[g] tokens; item[g] items come before theirs.
+struct AttnGroups {
+    int64_t item[kAttnMaxGroups + 1];
+    int64_t share;                   // items of a CTA
+    int32_t start[kAttnMaxGroups + 1];
+    int32_t len[kAttnMaxGroups];
+};
+
+// What the tile kernel needs beside AttnParams.  Sparse: CTA = (tile, K/V head, split), a
+// split tile's piece in slot CTA.  Prefix: items over (group, tile, K/V head, 128 tokens),
+// slots as in AttnPieces.  A slot is [128 rows][D], then [128][maximum, sum].
+struct AttnTiles {
+    AttnGroups *groups;              // prefix
+    float *pieces;                   // slots
+    float *rows;                     // prefix: whole units
+    int64_t q0, nq;                  // the window (sparse: every query)
+    int32_t gp_shift;                // log2 of the rows of a query
+    int32_t splits;                  // sparse: CTAs that share a tile's blocks
+    int32_t ctas;
+    int32_t box_rows, oob_page;
+};
+
 // One launch, with programmatic dependent launch: every kernel of these operators waits
 // for the kernels ahead of it before it touches memory, so it may always start early.
 cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, cudaStream_t stream, void **args);
@@ -71,6 +99,13 @@ cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, cudaS
 int attn_decode_heads(int group);
 cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
                         const CUtensorMap &vmap, cudaStream_t stream);
+cudaError_t attn_tiles(const AttnParams &p, const AttnTiles &w, int head_dim, const CUtensorMap &kmap,
+                       const CUtensorMap &vmap, cudaStream_t stream);
+// Joins the pieces of: (query, head chunk)s cut between CTAs; a window's own tokens and
+// prefixes; split sparse tiles.
+cudaError_t attn_join_rows(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim,
+                           cudaStream_t stream);
+cudaError_t attn_join_splits(const AttnParams &p, const AttnTiles &tiles, int head_dim, cudaStream_t stream);
 cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream);
 
 #ifdef __CUDACC__
@@ -112,6 +147,13 @@ __device__ __forceinline__ float2 attn_e4m3x2_to_f2(uint32_t codes)
         : "=f"(lo), "=f"(hi)
         : "r"(h2));
     return make_float2(lo, hi);
+}
+
+// One element of a cache, not scaled.
+__device__ __forceinline__ float attn_value(const AttnCache &c, int64_t elem)
+{
+    return c.fp8 ? attn_e4m3x2_to_f2(c.data[elem]).x
+                 : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(c.data)[elem] << 16);
 }
 
 __device__ __forceinline__ uint16_t attn_bf16(float x)

@@ -1,0 +1,883 @@
+// Attention of tiles of queries on the tcgen05 tensor cores: prefill chunks over the
+// blocks their queries selected, and groups of queries over a prefix they share.
+//
+// What is computed is stated in include/msa_attention.h.
+//
+// A tile is 128 rows: QT queries times the heads of one K/V head, padded to a power of two.
+// Per 128 tokens the CTA computes S [128 rows, 128 tokens] = Q . K^T and
+// O [128 rows, D] += P . V, each product read from shared memory as TMA copied it (K-major
+// keys, N-major values) with P as the A operand in tensor memory, where it takes the place
+// of the scores.  E4M3 caches run on kind::f8f6f4 with Q and P split into E4M3 halves
+// hi | lo (twice the MMAs at twice the rate: no conversion of keys or values, and half the
+// bytes in shared memory); bf16 on kind::f16.
+//   warp 0     TMA: page lookups one tile ahead, key and value copies
+//   warp 1     MMAs; zeroes value rows past the history before they are multiplied
+//   warps 2-5  softmax and output, a thread per row
+// The chain scores -> softmax -> values of one CTA leaves the tensor cores idle during the
+// softmax, so two CTAs share an SM (192 threads of up to 168 registers, half the tensor
+// memory and half the shared memory each) and fill each other's gaps: a tile is 1,024
+// cycles of MMA and as many of exponentials.
+//
+// The running maximum is a reference that follows the true one lazily: weights are taken
+// relative to it until the true maximum is kLazy powers of two above, and only then is the
+// output in tensor memory rescaled, which few tiles after the first need.
+//
+// Sparse (DENSE = false): the tile's queries run over the union of their blocks, each row
+// masked to its own.  A weight of zero does not hide an infinity or a NaN in the values of
+// a token that another row of the tile sees, so a row whose output is not finite is
+// computed again from its own tokens alone.
+// Prefix (DENSE = true): (tile, K/V head, 128 tokens) items laid end to end over the groups,
+// an equal share for each CTA; every piece goes to the workspace and is joined with the
+// queries' own tokens.
+
+#include "msa_attention_internal.h"
+#include "msa_tcgen05.cuh"
+
+#include <cstring>
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kInfo = 4;            // tiles whose validity words are held
+constexpr int kMaxBoxes = 16;
+constexpr int kMaxList = kAttnTileList;      // blocks of a tile's list
+constexpr int kTileQueries = 32;    // queries of a tile at most (a mask word)
+
+template <int D, bool FP8>
+struct TileShape {
+    static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+    static constexpr int kSwz = kRowBytes < 128 ? kRowBytes : 128;
+    static constexpr int kAtoms = kRowBytes / kSwz;
+    static constexpr int kTileBytes = 128 * kRowBytes;
+    static constexpr int kQBytes = 128 * D * 2;                   // bf16, or E4M3 hi | lo
+    static constexpr int kStages = kTileBytes == 32768 ? 1 : 2;   // of keys, and of values
+    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
+    static constexpr int kTmem = 256;                             // scores (and weights) | output
+    static constexpr int kPSteps = FP8 ? 4 : 8;                   // MMA steps along 128 tokens
+    static_assert(2 * kStages * kTileBytes >= 4 * kMaxList * 8, "scratch of the list");
+};
+
+constexpr float kLazyBf16 = 8.0f, kLazyFp8 = 4.0f;
+constexpr float kPOffset = 4.0f;    // E4M3 weights are 2^4 times larger: up to 2^8 of 448
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Two weights -> their E4M3 halves (hi pair, lo pair), through f16: 11 bits hold what the
+// halves keep (8), and its pairs convert and subtract two at a time.
+__device__ __forceinline__ void split_weights(float x0, float x1, uint32_t &hi, uint32_t &lo)
+{
+    asm("{\n\t.reg .b32 p, b, d;\n\t.reg .b16 h, l;\n\t"
+        "cvt.rn.f16x2.f32 p, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h, p;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
+        "sub.rn.f16x2 d, p, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
+        "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(x0), "f"(x1));
+}
+
+// What a CTA works on: rows of the tile, a K/V head and a range of 128-token tiles.
+struct Segment {
+    int64_t t0;              // first query
+    int nq;                  // queries in the tile
+    int c;                   // K/V head
+    int64_t p0, p1;          // tiles
+    int64_t off;             // DENSE: the prefix's table row and length
+    int64_t len;
+    bool whole, began;       // DENSE: all of its unit; it starts the unit
+    int group;
+};
+
+struct DenseWalk {
+    const AttnGroups *tab;    // group g has tiles x K/V heads units of nb 128-token tiles
+    int64_t it, end, base;   // base: items before the unit
+    int ngroups, hkv, qt, g, unit;
+
+    __device__ int64_t nb() const { return ((int64_t)tab->len[g] + 127) / 128; }
+    __device__ void find()
+    {
+        while (g < ngroups && tab->item[g + 1] <= it) {
+            ++g;
+            unit = 0;
+        }
+        if (g < ngroups && it < end) {
+            const int64_t n = nb();
+            unit = (int)((it - tab->item[g]) / n);
+            base = tab->item[g] + unit * n;
+        }
+    }
+    __device__ bool get(Segment &s) const
+    {
+        if (it >= end || g >= ngroups)
+            return false;
+        const int tile = unit / hkv;
+        s.c = unit - tile * hkv;
+        s.t0 = tab->start[g] + tile * qt;
+        s.nq = min(qt, tab->start[g + 1] - (int)s.t0);
+        s.group = g;
+        s.len = tab->len[g];
+        s.p0 = it - base;
+        s.p1 = min(nb(), end - base);
+        s.began = s.p0 == 0;
+        s.whole = s.began && s.p1 == nb();
+        return true;
+    }
+    __device__ void next(const Segment &s)
+    {
+        it = base + s.p1;
+        find();
+    }
+};
+
+template <int D, bool FP8, bool DENSE>
+__global__ void __launch_bounds__(kThreads, 2)
+msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnTiles w,
+                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using S = TileShape<D, FP8>;
+    constexpr int ST = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
+    __shared__ __align__(8) uint64_t bar_info[kInfo];
+    __shared__ __align__(8) uint64_t bar_q, bar_s, bar_p, bar_pv, bar_o, bar_drain;
+    __shared__ uint8_t s_nv[kInfo][kMaxBoxes];     // visible rows of each box
+    __shared__ uint32_t s_gap[kInfo];              // boxes without a page before the history's end
+    __shared__ union {
+        AttnGroups groups;                         // DENSE
+        struct {
+            int32_t block[kMaxList];               // the list: block, and the sequence's first query above it
+            uint32_t mask[kMaxList];               // the tile's queries that selected it
+            int64_t toff[kTileQueries];
+            int32_t len[kTileQueries], lead[kTileQueries], maxlen[kTileQueries];
+        } sp;
+    } u;
+    __shared__ int s_n;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t qsm = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t kring = qsm + S::kQBytes, vring = kring + ST * S::kTileBytes;
+    volatile int *abort_flag = &s_abort;
+    const int qt = 128 >> w.gp_shift;
+
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(smem_u32(&bar_k_full[i]), 1);
+            mbar_init(smem_u32(&bar_k_empty[i]), 1);
+            mbar_init(smem_u32(&bar_v_full[i]), 1);
+            mbar_init(smem_u32(&bar_v_empty[i]), 1);
+        }
+        for (int i = 0; i < kInfo; ++i)
+            mbar_init(smem_u32(&bar_info[i]), 1);
+        mbar_init(smem_u32(&bar_q), 4);
+        mbar_init(smem_u32(&bar_s), 1);
+        mbar_init(smem_u32(&bar_p), 4);
+        mbar_init(smem_u32(&bar_pv), 1);
+        mbar_init(smem_u32(&bar_o), 1);
+        mbar_init(smem_u32(&bar_drain), 1);
+        s_abort = 0;
+        s_n = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1)
+        tmem_alloc(smem_u32(&s_tmem), S::kTmem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+
+    Segment seg;
+    DenseWalk dw;
+    if (DENSE) {
+        // the groups' queries within the window, and their items, by one warp
+        if (warp == 0) {
+            int64_t items = 0;
+            int32_t edge = 0;                        // queries before, a running maximum
+            const int n = p.num_groups;
+            for (int g0 = 0; g0 <= n; g0 += 32) {
+                const int g = g0 + lane;
+                int64_t e64 = g <= n ? (int64_t)__ldg(p.group_start + g) - w.q0 : 0;
+                int32_t e = (int32_t)max((int64_t)0, min(e64, w.nq));
+                const int32_t len = g < n ? max(__ldg(p.prefix_len + g), 0) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t x = __shfl_up_sync(0xffffffffu, e, o);
+                    if (lane >= o)
+                        e = max(e, x);
+                }
+                e = max(e, edge);
+                if (g <= n)
+                    u.groups.start[g] = e;
+                if (g < n)
+                    u.groups.len[g] = len;
+                edge = __shfl_sync(0xffffffffu, e, 31);
+            }
+            __syncwarp();
+            for (int g0 = 0; g0 < n; g0 += 32) {
+                const int g = g0 + lane;
+                int64_t x = 0;
+                if (g < n) {
+                    const int q = u.groups.start[g + 1] - u.groups.start[g];
+                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (((int64_t)u.groups.len[g] + 127) / 128);
+                }
+                int64_t inc = x;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o)
+                        inc += y;
+                }
+                if (g < n)
+                    u.groups.item[g] = items + inc - x;
+                items += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0)
+                u.groups.item[n] = items;
+        }
+    } else {
+        // the union of the queries' blocks: a hash of (sequence, block) in the ring's memory,
+        // then sorted by rank, so that the order does not depend on the insertions'
+        seg.t0 = (int64_t)(blockIdx.x / (p.hkv * w.splits)) * qt;
+        seg.nq = (int)min((int64_t)qt, p.num_queries - seg.t0);
+        seg.c = (int)(blockIdx.x / w.splits % p.hkv);
+        if (tid < kTileQueries) {
+            u.sp.len[tid] = tid < seg.nq ? max(__ldg(p.kv_len + seg.t0 + tid), 0) : 0;
+            u.sp.toff[tid] = tid < seg.nq ? __ldg(p.table_offset + seg.t0 + tid) : 0;
+            u.sp.maxlen[tid] = 0;
+        }
+        const int ids = seg.nq * p.topk;
+        int slots = 64;
+        while (slots < 2 * ids)
+            slots *= 2;
+        int32_t *keys = reinterpret_cast<int32_t *>(smem_raw + (kring - smem_u32(smem_raw)));
+        uint32_t *masks = reinterpret_cast<uint32_t *>(keys + slots);
+        for (int i = tid; i < slots; i += kThreads) {
+            keys[i] = -1;
+            masks[i] = 0;
+        }
+        __syncthreads();
+        if (tid < seg.nq) {   // the first query of the same sequence
+            int l = 0;
+            while (u.sp.toff[l] != u.sp.toff[tid])
+                ++l;
+            u.sp.lead[tid] = l;
+            atomicMax(&u.sp.maxlen[l], u.sp.len[tid]);
+        }
+        __syncthreads();
+        for (int i = tid; i < ids; i += kThreads) {
+            const int q = i / p.topk;
+            const int32_t id = __ldg(p.topk_ids + seg.t0 * p.topk + i);
+            if (id >= 0 && (int64_t)id * p.block_tokens < u.sp.len[q]) {
+                // below 2^24 blocks of at least 128 tokens, and 32 sequences
+                const int32_t key = (u.sp.lead[q] << 24) | id;
+                uint32_t h = ((uint32_t)key * 2654435761u) & (uint32_t)(slots - 1);
+                for (;;) {      // at most half of the slots fill up
+                    const int32_t old = atomicCAS(&keys[h], -1, key);
+                    if (old == -1 || old == key)
+                        break;
+                    h = (h + 1) & (uint32_t)(slots - 1);
+                }
+                atomicOr(&masks[h], 1u << q);
+            }
+        }
+        __syncthreads();
+        int32_t *found = reinterpret_cast<int32_t *>(masks + slots);     // the entries, in no order
+        uint32_t *found_mask = reinterpret_cast<uint32_t *>(found + slots);
+        for (int i = tid; i < slots; i += kThreads)
+            if (keys[i] != -1) {
+                const int k = atomicAdd(&s_n, 1);
+                found[k] = keys[i];
+                found_mask[k] = masks[i];
+            }
+        __syncthreads();
+        for (int i = tid; i < s_n; i += kThreads) {
+            int rank = 0;
+            for (int j = 0; j < s_n; ++j)
+                rank += found[j] < found[i];
+            u.sp.block[rank] = found[i];
+            u.sp.mask[rank] = found_mask[i];
+        }
+        // the scratch is TMA's from here on
+        fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int per_block = DENSE ? 1 : p.block_tokens / 128;     // 128-token tiles of a block
+    if (DENSE) {
+        const int64_t total = u.groups.item[p.num_groups], share = (total + gridDim.x - 1) / gridDim.x;
+        dw.tab = &u.groups;
+        dw.ngroups = p.num_groups;
+        dw.hkv = p.hkv;
+        dw.qt = qt;
+        dw.g = 0;
+        dw.unit = 0;
+        dw.it = min(total, share * blockIdx.x);
+        dw.end = min(total, dw.it + share);
+        dw.base = 0;
+        dw.find();
+        if (blockIdx.x == 0)   // what the join needs of the groups
+            for (int g = tid; g <= p.num_groups; g += kThreads) {
+                w.groups->item[g] = u.groups.item[g];
+                w.groups->start[g] = u.groups.start[g];
+                if (g < p.num_groups)
+                    w.groups->len[g] = u.groups.len[g];
+                else
+                    w.groups->share = share;
+            }
+    } else {
+        const int64_t n = (int64_t)s_n * per_block, sp = blockIdx.x % w.splits;
+        seg.p0 = n * sp / w.splits;
+        seg.p1 = n * (sp + 1) / w.splits;
+    }
+    bool once = true;
+    // the next segment of this CTA
+    auto next_segment = [&](bool first) -> bool {
+        if (DENSE) {
+            if (!first)
+                dw.next(seg);
+            if (!dw.get(seg))
+                return false;
+            seg.off = __ldg(p.prefix_offset + seg.group);
+            return true;
+        }
+        const bool r = once;
+        once = false;
+        return r;
+    };
+
+    if (warp == 0) {
+        // ---------------- copies ----------------
+        const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = 128 >> lb;
+        uint32_t it = 0;
+        bool ok = true;
+        for (bool first = true; ok && next_segment(first); first = false) {
+            // the box of this lane in tile v: row in the page, page (one past the last for a
+            // box that shows nothing: zeros), rows that some query sees, and whether the
+            // history goes on without a page
+            auto look = [&](int64_t v, int2 &box, int &nv, bool &gap) {
+                box = make_int2(0, w.oob_page);
+                nv = 0;
+                gap = false;
+                if (lane >= nbox || v >= seg.p1)
+                    return;
+                int64_t tok, off, len;
+                if (DENSE) {
+                    tok = v * 128;
+                    off = seg.off;
+                    len = seg.len;
+                } else {
+                    const int32_t e = u.sp.block[v / per_block];
+                    tok = (int64_t)(e & 0xFFFFFF) * p.block_tokens + v % per_block * 128;
+                    off = u.sp.toff[e >> 24];
+                    len = u.sp.maxlen[e >> 24];
+                }
+                tok += lane * BR;
+                if (tok >= len)
+                    return;
+                const int32_t pg = attn_page(p, off, tok);
+                gap = pg < 0;
+                if (pg >= 0) {
+                    box = make_int2(attn_page_row(p, tok), pg);
+                    nv = (int)min((int64_t)BR, len - tok);
+                }
+            };
+            int2 box, nbx;
+            int nv, nnv;
+            bool gap, ngap;
+            look(seg.p0, box, nv, gap);
+            for (int64_t v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+                const uint32_t s = it % ST, par = ((it / ST) & 1u) ^ 1u, slot = it % kInfo;
+                ok = warp_wait(smem_u32(&bar_k_empty[s]), par, abort_flag);
+                if (!ok)
+                    break;
+                // the slot's last readers were done before this stage's keys were multiplied
+                if (lane < nbox)
+                    s_nv[slot][lane] = (uint8_t)nv;
+                const uint32_t gaps = __ballot_sync(0xffffffffu, gap);
+                if (lane == 0)
+                    s_gap[slot] = gaps;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bar_info[slot]));
+                auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full) {
+#ifndef MSA_STARVE
+                    if (lane == 0)
+                        mbar_expect_tx(full, (uint32_t)S::kTileBytes);
+                    __syncwarp();
+                    if (lane < nbox)
+#pragma unroll
+                        for (int at = 0; at < S::kAtoms; ++at)
+                            tma_load_box(dst + (uint32_t)(at * 128 + lane * BR) * S::kSwz, map,
+                                         at * (S::kSwz / (FP8 ? 1 : 2)), box.x, seg.c, box.y, full);
+#endif
+                };
+                copy(&kmap, kring + s * (uint32_t)S::kTileBytes, smem_u32(&bar_k_full[s]));
+                look(v + 1, nbx, nnv, ngap);
+                ok = warp_wait(smem_u32(&bar_v_empty[s]), par, abort_flag);
+                if (!ok)
+                    break;
+                copy(&vmap, vring + s * (uint32_t)S::kTileBytes, smem_u32(&bar_v_full[s]));
+                box = nbx;
+                nv = nnv;
+                gap = ngap;
+            }
+        }
+        if (!ok)
+            *abort_flag = 1;
+#ifndef MSA_STARVE
+        // every copy has landed before the CTA finishes (of the last tile of an aborted
+        // CTA the values may not have been asked for; that wait runs out)
+        for (uint32_t s = 0; s < (uint32_t)ST && s < it; ++s) {
+            const uint32_t par = ((it - 1u - s) / ST) & 1u;
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), par));
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_v_full[s]), par));
+        }
+        if (!ok)
+            for (uint32_t s = 0; s < (uint32_t)ST; ++s)
+                (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), (it / ST) & 1u));
+#endif
+    } else if (warp == 1) {
+        // ---------------- MMAs ----------------
+        constexpr uint32_t kIdS = mma_idesc(FP8, 128, 128, false, false);
+        constexpr uint32_t kIdO = mma_idesc(FP8, 128, D, false, true);
+        constexpr int kTok = 128 / S::kPSteps;
+        const int BR = w.box_rows, nbox = 128 / BR;
+        uint32_t it = 0, nseg = 0;
+        bool ok = true;
+        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
+            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
+            for (int64_t v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+                const uint32_t s = it % ST, ph = (it / ST) & 1u;
+                ok = warp_wait(smem_u32(&bar_k_full[s]), ph, abort_flag);
+                // the weights of the tile before, which the scores overwrite, are multiplied
+                ok = ok && (it == 0 || warp_wait(smem_u32(&bar_pv), (it - 1u) & 1u, abort_flag));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t kt = kring + s * (uint32_t)S::kTileBytes;
+#pragma unroll
+                for (int half = 0; half < (FP8 ? 2 : 1); ++half)
+#pragma unroll
+                    for (int ks = 0; ks < S::kRowBytes / 32; ++ks) {
+                        const uint32_t at = (uint32_t)(ks * 32) / S::kSwz, col = (uint32_t)(ks * 32) % S::kSwz;
+                        mma_ss<FP8>(tmem,
+                                    smem_desc(qsm + (uint32_t)(half * 128 * D) + at * (128u * S::kSwz) + col, S::kSwz, 16u,
+                                              8u * S::kSwz),
+                                    smem_desc(kt + at * (128u * S::kSwz) + col, S::kSwz, 16u, 8u * S::kSwz), kIdS,
+                                    half > 0 || ks > 0);
+                    }
+                mma_commit(smem_u32(&bar_s));
+                mma_commit(smem_u32(&bar_k_empty[s]));
+                ok = warp_wait(smem_u32(&bar_v_full[s]), ph, abort_flag);
+                if (!ok)
+                    break;
+                const uint32_t vt = vring + s * (uint32_t)S::kTileBytes;
+                // rows past the history may hold anything: a weight of zero would not hide
+                // an infinity or a NaN
+                const int nv = lane < nbox ? s_nv[it % kInfo][lane] : 0;
+                uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
+                if (partial) {
+                    while (partial) {
+                        const int b = __ffs(partial) - 1;
+                        partial &= partial - 1;
+                        const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
+                        for (int at = 0; at < S::kAtoms; ++at)
+                            for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
+                                sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                ok = warp_wait(smem_u32(&bar_p), it & 1u, abort_flag);
+                if (!ok)
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int half = 0; half < (FP8 ? 2 : 1); ++half)
+#pragma unroll
+                    for (int ks = 0; ks < S::kPSteps; ++ks)
+                        mma_ts<FP8>(tmem + 128u, tmem + (uint32_t)(half * 32 + ks * 8),
+                                    smem_desc(vt + (uint32_t)(ks * kTok * S::kSwz), S::kSwz, 128u * S::kSwz, 8u * S::kSwz),
+                                    kIdO, v > seg.p0 || half > 0 || ks > 0);
+                mma_commit(smem_u32(&bar_pv));
+                mma_commit(smem_u32(&bar_v_empty[s]));
+            }
+            __syncwarp();
+            if (ok)
+                mma_commit(smem_u32(&bar_o));
+        }
+        if (!ok)
+            *abort_flag = 1;
+        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
+        (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
+    } else {
+        // ---------------- softmax and output ----------------
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16), ot = st + 128u;
+        const int gp = 1 << w.gp_shift, qi = row >> w.gp_shift, hi = row & (gp - 1);
+        const int BR = w.box_rows, lb = __ffs(BR) - 1;
+        constexpr float kLazy = FP8 ? kLazyFp8 : kLazyBf16, kOff = FP8 ? kPOffset : 0.0f;
+        const float nan = __int_as_float(0x7fc00000);
+        uint32_t it = 0, nseg = 0;
+        bool ok = true;
+        for (bool first = true; next_segment(first); first = false, ++nseg) {
+            // ---- the row's query into shared memory ----
+            const bool real = qi < seg.nq && hi < p.group;
+            const int64_t hr = (w.q0 + seg.t0 + qi) * p.hq + seg.c * p.group + hi;     // its row of q and out
+            const float ks = attn_k_scale(p, seg.c) * p.scale_log2;
+            float qs = fabsf(ks);                          // a negative scale goes into the query
+            {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + hr * D);
+                const uint32_t flip = ks < 0.0f ? 0x80008000u : 0u;
+                float sc = 1.0f;
+                if (FP8) {
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            big = max(big, max((xs[j] & 0x7FFFu) << 16, xs[j] & 0x7FFF0000u));
+                    }
+                    big >>= 23;
+                    const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
+                    sc = __int_as_float((e2 + 127) << 23);
+                    qs *= __int_as_float((127 - e2) << 23);
+                }
+#pragma unroll 2
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t xs[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+                    if (FP8) {
+                        uint32_t hw[2], lw[2];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x0 = __uint_as_float(xs[j] << 16) * sc;
+                            const float x1 = __uint_as_float(xs[j] & 0xFFFF0000u) * sc;
+                            const uint32_t h = e4m3x2_from_f32(x0, x1);
+                            const float2 d = attn_e4m3x2_to_f2(h);
+                            const uint32_t l = e4m3x2_from_f32(x0 - d.x, x1 - d.y);
+                            hw[j / 2] = j & 1 ? hw[j / 2] | (h << 16) : h;
+                            lw[j / 2] = j & 1 ? lw[j / 2] | (l << 16) : l;
+                        }
+                        const uint32_t a = swizzle<S::kSwz>((uint32_t)(row * S::kSwz + i * 8));
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + a), "r"(hw[0]), "r"(hw[1]) : "memory");
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + 128 * D + a), "r"(lw[0]), "r"(lw[1])
+                                     : "memory");
+                    } else {
+                        const uint32_t byte = (uint32_t)i * 16, at = byte / S::kSwz, col = byte % S::kSwz;
+                        sts128(qsm + at * (128u * S::kSwz) + swizzle<S::kSwz>((uint32_t)row * S::kSwz + col), xs[0], xs[1],
+                               xs[2], xs[3]);
+                    }
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&bar_q));
+            const int len = DENSE ? (int)seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
+            float m = -INFINITY, l = 0.0f;
+
+            // visible tokens of this row in tile v, from its first
+            auto visible = [&](int64_t v) -> int {
+                int64_t tok = v * 128;
+                bool sees = real;
+                if (!DENSE) {
+                    const int e = (int)(v / per_block);
+                    tok = (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + v % per_block * 128;
+                    sees = real && ((u.sp.mask[e] >> qi) & 1u);
+                }
+                return sees ? (int)max((int64_t)0, min((int64_t)128, len - tok)) : 0;
+            };
+            for (int64_t v = seg.p0; v < seg.p1; ++v, ++it) {
+                ok = ok && warp_wait(smem_u32(&bar_info[it % kInfo]), (it / kInfo) & 1u, abort_flag);
+                const int vis = visible(v);
+                const uint32_t gaps = ok ? s_gap[it % kInfo] : 0u;
+                ok = ok && warp_wait(smem_u32(&bar_s), it & 1u, abort_flag);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (!__any_sync(0xffffffffu, vis > 0)) {
+                    uint32_t z[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        z[j] = 0u;
+                    tmem_st32(st, z);
+                    tmem_st32(st + 32u, z);
+                } else {
+                    uint32_t x[128];
+#pragma unroll
+                    for (int j = 0; j < 128; j += 32)
+                        tmem_ld32(st + (uint32_t)j, x + j);
+                    tc_wait_ld();
+                    if (vis < 128 || gaps) {
+#pragma unroll
+                        for (int j = 0; j < 128; ++j)
+                            if (j >= vis || ((gaps >> (j >> lb)) & 1u))
+                                x[j] = 0xff800000u;
+                    }
+                    float mx = -INFINITY;
+                    {
+                        float a = -INFINITY, b = -INFINITY, c2 = -INFINITY, d2 = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 128; j += 4) {
+                            a = fmaxf(a, __uint_as_float(x[j]));
+                            b = fmaxf(b, __uint_as_float(x[j + 1]));
+                            c2 = fmaxf(c2, __uint_as_float(x[j + 2]));
+                            d2 = fmaxf(d2, __uint_as_float(x[j + 3]));
+                        }
+                        mx = fmaxf(fmaxf(a, b), fmaxf(c2, d2)) * qs;
+                    }
+                    // (-inf + kLazy is -inf: the first visible tile sets the reference)
+                    const bool grow = mx > m + kLazy;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float alpha = grow ? exp2_approx(m - mx) : 1.0f;
+                        m = grow ? mx : m;
+                        l *= alpha;
+                        if (v > seg.p0) {
+#pragma unroll
+                            for (int j = 0; j < D; j += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(ot + (uint32_t)j, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(ot + (uint32_t)j, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.0f : kOff - m;
+                    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 128; j += 32) {
+                        uint32_t hw[16], lw[8];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float p0 = exp2_approx(fmaf(__uint_as_float(x[j + e]), qs, ref));
+                            const float p1 = exp2_approx(fmaf(__uint_as_float(x[j + e + 1]), qs, ref));
+                            const float p2 = exp2_approx(fmaf(__uint_as_float(x[j + e + 2]), qs, ref));
+                            const float p3 = exp2_approx(fmaf(__uint_as_float(x[j + e + 3]), qs, ref));
+                            s0 += p0 + p1;
+                            s1 += p2 + p3;
+                            if (FP8) {
+                                uint32_t h0, l0, h1, l1;
+                                split_weights(p0, p1, h0, l0);
+                                split_weights(p2, p3, h1, l1);
+                                hw[e / 4] = h0 | (h1 << 16);
+                                lw[e / 4] = l0 | (l1 << 16);
+                            } else {
+                                hw[e / 2] = bf16x2_from_f32(p0, p1);
+                                hw[e / 2 + 1] = bf16x2_from_f32(p2, p3);
+                            }
+                        }
+                        if (FP8) {
+                            tmem_st8(st + (uint32_t)(j / 4), hw);
+                            tmem_st8(st + 32u + (uint32_t)(j / 4), lw);
+                        } else {
+                            tmem_st16(st + (uint32_t)(j / 2), hw);
+                        }
+                    }
+                    l += s0 + s1;
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bar_p));
+            }
+            if (!ok)
+                *abort_flag = 1;
+            ok = ok && warp_wait(smem_u32(&bar_o), nseg & 1u, abort_flag);
+            // ---- output ----
+            tc_fence_after();
+            const bool empty = seg.p1 <= seg.p0;
+            const float vs = attn_v_scale(p, seg.c);
+            const bool piece = DENSE || w.splits > 1;
+            const float inv = piece ? vs * (1.0f / (1 << (int)kOff)) : l == 0.0f ? 0.0f : vs / l;
+            if (FP8)
+                l *= 1.0f / (1 << (int)kOff);      // the sum itself
+            float *dst = nullptr;
+            float *ml = nullptr;
+            if (piece) {
+                if (DENSE && seg.whole) {
+                    dst = w.rows + ((seg.t0 + qi) * p.hq + seg.c * p.group + hi) * (D + 4);
+                    ml = dst + D;
+                } else {
+                    const int64_t sl = DENSE ? (seg.began ? (int64_t)gridDim.x : 0) + blockIdx.x : (int64_t)blockIdx.x;
+                    float *base = w.pieces + sl * (int64_t)(128 * (D + 2));
+                    dst = base + row * D;
+                    ml = base + 128 * D + 2 * row;
+                }
+            }
+            bool finite = true;
+            const uint32_t stage = qsm + (uint32_t)(quarter * 32 * D * 2);      // this warp's rows of the query tile
+#pragma unroll 1
+            for (int j = 0; j < D; j += 32) {
+                uint32_t o[32];
+                if (ok && !empty) {
+                    tmem_ld32(ot + (uint32_t)j, o);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float x = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+                    finite = finite && fabsf(x) < INFINITY;
+                    o[e] = __float_as_uint(ok ? x : nan);
+                }
+                if (piece) {
+                    if (real)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(dst + j + e) =
+                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                            __uint_as_float(o[e + 3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        const int chunk = (j + e) / 8;
+                        sts128(stage + (uint32_t)(lane * D * 2 + ((chunk ^ (lane & 7)) << 4)),
+                               bf16x2_from_f32(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                               bf16x2_from_f32(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                               bf16x2_from_f32(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
+                               bf16x2_from_f32(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+                    }
+                }
+            }
+            tc_fence_before();
+            if (piece) {
+                if (real) {
+                    ml[0] = ok ? m : nan;
+                    ml[1] = ok ? l : nan;
+                }
+            } else {
+                if (real && p.lse)
+                    p.lse[hr] = ok ? attn_lse(m, l) : nan;
+                __syncwarp();
+                // rows of 2 * D bytes, several a step
+                constexpr int kLanes = D / 8;
+                for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
+                    const int rr = quarter * 32 + r, q2 = rr >> w.gp_shift, h2 = rr & (gp - 1), ch = lane % kLanes;
+                    if (q2 < seg.nq && h2 < p.group) {
+                        uint4 x;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(stage + (uint32_t)(r * D * 2 + ((ch ^ (r & 7)) << 4))));
+                        const int64_t o = (w.q0 + seg.t0 + q2) * p.hq + seg.c * p.group + h2;
+                        *reinterpret_cast<uint4 *>(p.out + o * D + ch * 8) = x;
+                    }
+                }
+                __syncwarp();
+            }
+            // ---- rows that values of tokens they do not see may have reached ----
+            if (!DENSE && ok) {
+                uint32_t again = __ballot_sync(0xffffffffu, real && !finite);
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    const int64_t hr2 = __shfl_sync(0xffffffffu, hr, src);
+                    const int len2 = __shfl_sync(0xffffffffu, len, src), q2 = __shfl_sync(0xffffffffu, qi, src);
+                    const float m2 = __shfl_sync(0xffffffffu, m, src), inv2 = __shfl_sync(0xffffffffu, inv, src);
+                    float *dst2 = reinterpret_cast<float *>(__shfl_sync(0xffffffffu, (unsigned long long)dst, src));
+                    float acc[D / 32] = {};
+                    for (int64_t v = seg.p0; v < seg.p1; ++v) {
+                        const int e = (int)(v / per_block);
+                        if (!((u.sp.mask[e] >> q2) & 1u))
+                            continue;
+                        const int32_t blk = u.sp.block[e];
+                        const int64_t tok0 = (int64_t)(blk & 0xFFFFFF) * p.block_tokens + v % per_block * 128;
+                        for (int j = 0; j < 128 && tok0 + j < len2; ++j) {
+                            const int32_t pg = attn_page(p, u.sp.toff[blk >> 24], tok0 + j);
+                            if (pg < 0)
+                                continue;
+                            const int64_t r = attn_page_row(p, tok0 + j);
+                            const int64_t ko = (int64_t)pg * p.k.stride_page + seg.c * p.k.stride_head + r * p.k.stride_token;
+                            const int64_t vo = (int64_t)pg * p.v.stride_page + seg.c * p.v.stride_head + r * p.v.stride_token;
+                            float dot = 0.0f;
+                            for (int d = lane; d < D; d += 32)
+                                dot = fmaf(attn_value(p.k, ko + d), __uint_as_float((uint32_t)p.q[hr2 * D + d] << 16), dot);
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1)
+                                dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                            const float wgt = exp2_approx(dot * ks - m2 + kOff);
+#pragma unroll
+                            for (int d = 0; d < D / 32; ++d)
+                                acc[d] = fmaf(wgt, attn_value(p.v, vo + lane + 32 * d), acc[d]);
+                        }
+                    }
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d) {
+                        if (dst2)
+                            dst2[lane + 32 * d] = acc[d] * inv2;
+                        else
+                            p.out[hr2 * D + lane + 32 * d] = attn_bf16(acc[d] * inv2);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, S::kTmem);
+    }
+}
+
+template <int D, bool FP8, bool DENSE>
+cudaError_t launch_tiles(const AttnParams &p, const AttnTiles &w, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                         cudaStream_t stream)
+{
+    using S = TileShape<D, FP8>;
+    const void *fn = reinterpret_cast<const void *>(&msa_attention_tile_kernel<D, FP8, DENSE>);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnTiles *>(&w), const_cast<CUtensorMap *>(&kmap),
+                    const_cast<CUtensorMap *>(&vmap)};
+    return attn_launch(fn, w.ctas, kThreads, S::kSmem, stream, args);
+}
+
+template <int D>
+cudaError_t launch_tiles_of(const AttnParams &p, const AttnTiles &w, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                            cudaStream_t stream)
+{
+    if (p.topk_ids)
+        return p.k.fp8 ? launch_tiles<D, true, false>(p, w, kmap, vmap, stream)
+                       : launch_tiles<D, false, false>(p, w, kmap, vmap, stream);
+    return p.k.fp8 ? launch_tiles<D, true, true>(p, w, kmap, vmap, stream)
+                   : launch_tiles<D, false, true>(p, w, kmap, vmap, stream);
+}
+
+}  // namespace
+
+cudaError_t attn_tiles(const AttnParams &p, const AttnTiles &w, int head_dim, const CUtensorMap &kmap,
+                       const CUtensorMap &vmap, cudaStream_t stream)
+{
+    return head_dim == 128 ? launch_tiles_of<128>(p, w, kmap, vmap, stream)
+                           : launch_tiles_of<64>(p, w, kmap, vmap, stream);
+}

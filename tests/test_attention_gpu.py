@@ -165,3 +165,52 @@ PREFIX = [
 def test_prefix(kw):
     p = Problem(15, ids=None, **kw)
     p.device().run().check()
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("splits", [False, True], ids=["whole", "split"])
+def test_values_of_unseen_tokens_never_reach_a_row(dtype, splits):
+    """NaN and infinity written as the value of a token: only the queries that see the
+    token get them, although their tile multiplies it for all."""
+    n = 1200 if not splits else 40          # enough tiles for a CTA each, or blocks shared by several
+    p = Problem(17, lens=list(range(2000, 2000 + n)), seq_of=[0] * n, heads=(16, 8), dtype=dtype, ids="near", topk=4)
+    clean = p.device()
+    tok = 2000 + n // 2                     # from the middle query on it is visible
+    pg, row = int(p.table[0, tok // p.page]), tok % p.page
+    dirty = p.device()
+    raw = p.v.clone().view(torch.uint8) if dtype == "e4m3" else p.v.clone()
+    raw[pg, 3, row, 5] = 0x7F if dtype == "e4m3" else float("inf")
+    dirty.vpool = (raw.view(torch.float8_e4m3fn) if dtype == "e4m3" else raw).contiguous().cuda()
+    dirty.v = B.cache_from_tensor(dirty.vpool)
+    clean.run(RUNS)
+    dirty.run(RUNS)
+    a, b = clean.out.float(), dirty.out.float()
+    sees = torch.zeros(n, 16, p.d, dtype=torch.bool)
+    for t in range(n):
+        if int(p.lens[t]) > tok and (p.ids[t] == tok // p.block).any():
+            sees[t, 6:8, 5] = True          # the two query heads on K/V head 3
+    assert sees.any() and not sees.all()
+    assert not torch.isfinite(b[sees.cuda()]).any()
+    rest = ~sees.cuda()
+    # a row computed again sums in another order: as far off as two roundings
+    assert torch.isfinite(b[rest]).all()
+    _, _, tol, _ = p.reference() if n < 100 else (None, None, None, None)
+    if tol is not None:
+        assert ((a - b).abs()[rest] <= 2 * tol.cuda()[rest]).all()
+    else:
+        assert ((a - b).abs()[rest] <= 2.0 ** -6 * a.abs()[rest] + 2.0 ** -6).all()
+    assert torch.equal(clean.lse, dirty.lse)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(dtype="bf16"), dict(ids=None, prefixes=(900,), groups=(0, 9)),
+                                dict(ids=None, prefixes=(900,), groups=(0, 9), dtype="bf16")], ids=_name)
+def test_a_call_repeats_bit_for_bit(kw):
+    p = Problem(18, **{**dict(lens=(1, 700, 300, 64, 2000, 129, 0, 90, 1500), heads=(16, 2)), **kw})
+    d = p.device().run()
+    for flags in ([0, PDL] if kw.get("ids", 1) is None else [0, PDL, RUNS, RUNS]):
+        e = p.device().run(flags)
+        if flags == RUNS:
+            e2 = p.device().run(flags)
+            assert torch.equal(e.out, e2.out) and torch.equal(e.lse, e2.lse)
+        else:
+            assert torch.equal(d.out, e.out) and torch.equal(d.lse, e.lse)

@@ -124,7 +124,7 @@ def test_sparse_refuses(over, status):
 
 @pytest.mark.parametrize("over,status", [
     (dict(num_groups=-1), UNS),
-    (dict(num_groups=1025), UNS),
+    (dict(num_groups=513), UNS),
     (dict(group_start=None), INV),
     (dict(prefix_len=None), INV),
     (dict(prefix_offset=None), INV),
@@ -150,7 +150,7 @@ def test_workspace_size_and_refusals():
     assert B.msa_attention_workspace_bytes(cfg(), 64, 5) >= 0
     assert B.msa_attention_workspace_bytes(cfg(), 0) >= 0
     for bad in (dict(cfg=cfg(head_dim=32), num_queries=1), dict(cfg=cfg(), num_queries=-1),
-                dict(cfg=cfg(), num_queries=1, num_groups=1025), dict(cfg=None, num_queries=1)):
+                dict(cfg=cfg(), num_queries=1, num_groups=513), dict(cfg=None, num_queries=1)):
         with pytest.raises(B.MsaError):
             B.msa_attention_workspace_bytes(**bad)
     if n1 > 0:

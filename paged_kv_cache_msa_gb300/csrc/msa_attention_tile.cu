@@ -12,11 +12,11 @@
 // bytes in shared memory); bf16 on kind::f16.
 //   warp 0     TMA: page lookups one tile ahead, key and value copies
 //   warp 1     MMAs; zeroes value rows past the history before they are multiplied
-//   warps 2-5  softmax and output, a thread per row
+//   warps 2-9  softmax and output, two threads per row (64 tokens of a tile, half the dims)
 // The chain scores -> softmax -> values of one CTA leaves the tensor cores idle during the
-// softmax, so two CTAs share an SM (192 threads of up to 168 registers, half the tensor
-// memory and half the shared memory each) and fill each other's gaps: a tile is 1,024
-// cycles of MMA and as many of exponentials.
+// softmax, so two CTAs share an SM (half the tensor memory and half the shared memory each)
+// and fill each other's gaps: a tile is 1,024 cycles of MMA, as many of exponentials, and
+// about 1,200 issue slots of a scheduler.
 //
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
@@ -37,7 +37,7 @@
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kInfo = 4;            // tiles whose validity words are held
 constexpr int kMaxBoxes = 16;
 constexpr int kMaxList = kAttnTileList;      // blocks of a tile's list
@@ -60,6 +60,14 @@ struct TileShape {
 constexpr float kLazyBf16 = 8.0f, kLazyFp8 = 4.0f;
 constexpr float kPOffset = 4.0f;    // E4M3 weights are 2^4 times larger: up to 2^8 of 448
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -75,6 +83,40 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// Pairs of fp32 as one 64-bit operand: two multiply-adds or sums an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Two weights -> their E4M3 halves (hi pair, lo pair), through f16: 11 bits hold what the
@@ -94,14 +136,12 @@ __device__ __forceinline__ void split_weights(float x0, float x1, uint32_t &hi, 
 
 // What a CTA works on: rows of the tile, a K/V head and a range of 128-token tiles.
 struct Segment {
-    int64_t t0;              // first query
+    int t0;                  // first query (prefix: of the window)
     int nq;                  // queries in the tile
     int c;                   // K/V head
-    int64_t p0, p1;          // tiles
-    int64_t off;             // DENSE: the prefix's table row and length
-    int64_t len;
-    bool whole, began;       // DENSE: all of its unit; it starts the unit
-    int group;
+    int p0, p1;              // 128-token tiles
+    int group, len;          // prefix: the group, its tokens
+    bool whole, began;       // prefix: all of its unit; it starts the unit
 };
 
 struct DenseWalk {
@@ -109,7 +149,7 @@ struct DenseWalk {
     int64_t it, end, base;   // base: items before the unit
     int ngroups, hkv, qt, g, unit;
 
-    __device__ int64_t nb() const { return ((int64_t)tab->len[g] + 127) / 128; }
+    __device__ int nb() const { return (int)(((uint32_t)tab->len[g] + 127u) / 128u); }
     __device__ void find()
     {
         while (g < ngroups && tab->item[g + 1] <= it) {
@@ -117,9 +157,9 @@ struct DenseWalk {
             unit = 0;
         }
         if (g < ngroups && it < end) {
-            const int64_t n = nb();
+            const int n = nb();
             unit = (int)((it - tab->item[g]) / n);
-            base = tab->item[g] + unit * n;
+            base = tab->item[g] + (int64_t)unit * n;
         }
     }
     __device__ bool get(Segment &s) const
@@ -129,11 +169,11 @@ struct DenseWalk {
         const int tile = unit / hkv;
         s.c = unit - tile * hkv;
         s.t0 = tab->start[g] + tile * qt;
-        s.nq = min(qt, tab->start[g + 1] - (int)s.t0);
+        s.nq = min(qt, tab->start[g + 1] - s.t0);
         s.group = g;
         s.len = tab->len[g];
-        s.p0 = it - base;
-        s.p1 = min(nb(), end - base);
+        s.p0 = (int)(it - base);
+        s.p1 = (int)min((int64_t)nb(), end - base);
         s.began = s.p0 == 0;
         s.whole = s.began && s.p1 == nb();
         return true;
@@ -167,6 +207,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             int32_t len[kTileQueries], lead[kTileQueries], maxlen[kTileQueries];
         } sp;
     } u;
+    __shared__ float s_row[2][128];                // exchange between the two threads of a row
+    __shared__ int s_ok[2][4];
     __shared__ int s_n;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -187,9 +229,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         }
         for (int i = 0; i < kInfo; ++i)
             mbar_init(smem_u32(&bar_info[i]), 1);
-        mbar_init(smem_u32(&bar_q), 4);
+        mbar_init(smem_u32(&bar_q), 8);
         mbar_init(smem_u32(&bar_s), 1);
-        mbar_init(smem_u32(&bar_p), 4);
+        mbar_init(smem_u32(&bar_p), 8);
         mbar_init(smem_u32(&bar_pv), 1);
         mbar_init(smem_u32(&bar_o), 1);
         mbar_init(smem_u32(&bar_drain), 1);
@@ -253,7 +295,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     } else {
         // the union of the queries' blocks: a hash of (sequence, block) in the ring's memory,
         // then sorted by rank, so that the order does not depend on the insertions'
-        seg.t0 = (int64_t)(blockIdx.x / (p.hkv * w.splits)) * qt;
+        seg.t0 = (int)(blockIdx.x / (p.hkv * w.splits)) * qt;
         seg.nq = (int)min((int64_t)qt, p.num_queries - seg.t0);
         seg.c = (int)(blockIdx.x / w.splits % p.hkv);
         if (tid < kTileQueries) {
@@ -282,7 +324,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         __syncthreads();
         for (int i = tid; i < ids; i += kThreads) {
             const int q = i / p.topk;
-            const int32_t id = __ldg(p.topk_ids + seg.t0 * p.topk + i);
+            const int32_t id = __ldg(p.topk_ids + (int64_t)seg.t0 * p.topk + i);
             if (id >= 0 && (int64_t)id * p.block_tokens < u.sp.len[q]) {
                 // below 2^24 blocks of at least 128 tokens, and 32 sequences
                 const int32_t key = (u.sp.lead[q] << 24) | id;
@@ -343,20 +385,22 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     w.groups->share = share;
             }
     } else {
-        const int64_t n = (int64_t)s_n * per_block, sp = blockIdx.x % w.splits;
+        const int n = s_n * per_block, sp = (int)(blockIdx.x % w.splits);
         seg.p0 = n * sp / w.splits;
         seg.p1 = n * (sp + 1) / w.splits;
     }
+    // first token of tile v of the list, and its entry
+    auto list_tile = [&](int v, int &e) -> int64_t {
+        e = per_block == 1 ? v : v / per_block;
+        return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * 128;
+    };
     bool once = true;
     // the next segment of this CTA
     auto next_segment = [&](bool first) -> bool {
         if (DENSE) {
             if (!first)
                 dw.next(seg);
-            if (!dw.get(seg))
-                return false;
-            seg.off = __ldg(p.prefix_offset + seg.group);
-            return true;
+            return dw.get(seg);
         }
         const bool r = once;
         once = false;
@@ -372,7 +416,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             // the box of this lane in tile v: row in the page, page (one past the last for a
             // box that shows nothing: zeros), rows that some query sees, and whether the
             // history goes on without a page
-            auto look = [&](int64_t v, int2 &box, int &nv, bool &gap) {
+            const int64_t prefix_off = DENSE ? __ldg(p.prefix_offset + seg.group) : 0;
+            auto look = [&](int v, int2 &box, int &nv, bool &gap) {
                 box = make_int2(0, w.oob_page);
                 nv = 0;
                 gap = false;
@@ -380,14 +425,14 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     return;
                 int64_t tok, off, len;
                 if (DENSE) {
-                    tok = v * 128;
-                    off = seg.off;
+                    tok = (int64_t)v * 128;
+                    off = prefix_off;
                     len = seg.len;
                 } else {
-                    const int32_t e = u.sp.block[v / per_block];
-                    tok = (int64_t)(e & 0xFFFFFF) * p.block_tokens + v % per_block * 128;
-                    off = u.sp.toff[e >> 24];
-                    len = u.sp.maxlen[e >> 24];
+                    int e;
+                    tok = list_tile(v, e);
+                    off = u.sp.toff[u.sp.block[e] >> 24];
+                    len = u.sp.maxlen[u.sp.block[e] >> 24];
                 }
                 tok += lane * BR;
                 if (tok >= len)
@@ -403,7 +448,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             int nv, nnv;
             bool gap, ngap;
             look(seg.p0, box, nv, gap);
-            for (int64_t v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
                 const uint32_t s = it % ST, par = ((it / ST) & 1u) ^ 1u, slot = it % kInfo;
                 ok = warp_wait(smem_u32(&bar_k_empty[s]), par, abort_flag);
                 if (!ok)
@@ -464,7 +509,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         bool ok = true;
         for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
             ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
-            for (int64_t v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
                 const uint32_t s = it % ST, ph = (it / ST) & 1u;
                 ok = warp_wait(smem_u32(&bar_k_full[s]), ph, abort_flag);
                 // the weights of the tile before, which the scores overwrite, are multiplied
@@ -530,27 +575,31 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
     } else {
         // ---------------- softmax and output ----------------
-        const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16), ot = st + 128u;
+        const int quarter = warp & 3, row = quarter * 32 + lane, half = (warp - 2) >> 2;
+        const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16), ot = st + 128u + (uint32_t)(half * (D / 2));
         const int gp = 1 << w.gp_shift, qi = row >> w.gp_shift, hi = row & (gp - 1);
         const int BR = w.box_rows, lb = __ffs(BR) - 1;
         constexpr float kLazy = FP8 ? kLazyFp8 : kLazyBf16, kOff = FP8 ? kPOffset : 0.0f;
+        constexpr int kD2 = D / 2;                      // dims of this thread
         const float nan = __int_as_float(0x7fc00000);
+        // the two warps that hold a row's halves
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
         uint32_t it = 0, nseg = 0;
         bool ok = true;
         for (bool first = true; next_segment(first); first = false, ++nseg) {
             // ---- the row's query into shared memory ----
             const bool real = qi < seg.nq && hi < p.group;
-            const int64_t hr = (w.q0 + seg.t0 + qi) * p.hq + seg.c * p.group + hi;     // its row of q and out
+            // its row of q and out
+            auto head_row = [&]() -> int64_t { return (w.q0 + seg.t0 + qi) * p.hq + seg.c * p.group + hi; };
             const float ks = attn_k_scale(p, seg.c) * p.scale_log2;
             float qs = fabsf(ks);                          // a negative scale goes into the query
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + hr * D);
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + head_row() * D);
                 const uint32_t flip = ks < 0.0f ? 0x80008000u : 0u;
                 float sc = 1.0f;
                 if (FP8) {
                     uint32_t big = 0;
-#pragma unroll
+#pragma unroll 4
                     for (int i = 0; i < D / 8; ++i) {
                         const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
                         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
@@ -564,7 +613,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     qs *= __int_as_float((127 - e2) << 23);
                 }
 #pragma unroll 2
-                for (int i = 0; i < D / 8; ++i) {
+                for (int i = half * (kD2 / 8); i < (half + 1) * (kD2 / 8); ++i) {
                     const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
                     const uint32_t xs[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
                     if (FP8) {
@@ -594,110 +643,123 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_u32(&bar_q));
-            const int len = DENSE ? (int)seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
+            const int len = DENSE ? seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
             float m = -INFINITY, l = 0.0f;
-
-            // visible tokens of this row in tile v, from its first
-            auto visible = [&](int64_t v) -> int {
-                int64_t tok = v * 128;
-                bool sees = real;
-                if (!DENSE) {
-                    const int e = (int)(v / per_block);
-                    tok = (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + v % per_block * 128;
-                    sees = real && ((u.sp.mask[e] >> qi) & 1u);
-                }
-                return sees ? (int)max((int64_t)0, min((int64_t)128, len - tok)) : 0;
-            };
-            for (int64_t v = seg.p0; v < seg.p1; ++v, ++it) {
+            for (int v = seg.p0; v < seg.p1; ++v, ++it) {
                 ok = ok && warp_wait(smem_u32(&bar_info[it % kInfo]), (it / kInfo) & 1u, abort_flag);
-                const int vis = visible(v);
+                // tokens of this thread's half that the row sees, from its first; -1: it sees none
+                // of the whole tile
+                int vis;
+                if (DENSE) {
+                    vis = len - v * 128;
+                } else {
+                    int e;
+                    const int64_t tok = list_tile(v, e);
+                    vis = (int)max((int64_t)-1, min((int64_t)128, len - tok));
+                    vis = (u.sp.mask[e] >> qi) & 1u ? vis : -1;
+                }
+                vis = real ? vis - half * 64 : -1;
                 const uint32_t gaps = ok ? s_gap[it % kInfo] : 0u;
                 ok = ok && warp_wait(smem_u32(&bar_s), it & 1u, abort_flag);
-                if (!ok)
-                    break;
                 tc_fence_after();
-                if (!__any_sync(0xffffffffu, vis > 0)) {
-                    uint32_t z[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        z[j] = 0u;
-                    tmem_st32(st, z);
-                    tmem_st32(st + 32u, z);
-                } else {
-                    uint32_t x[128];
-#pragma unroll
-                    for (int j = 0; j < 128; j += 32)
-                        tmem_ld32(st + (uint32_t)j, x + j);
+                uint32_t x[64] = {};
+                auto score = [&](int j) { return __uint_as_float(x[j]); };
+                float mx = -INFINITY;
+                const bool any = __any_sync(0xffffffffu, vis > 0);
+                if (ok && any) {
+                    tmem_ld32(st + (uint32_t)(half * 64), x);
+                    tmem_ld32(st + (uint32_t)(half * 64 + 32), x + 32);
                     tc_wait_ld();
-                    if (vis < 128 || gaps) {
+                    // rows that see all or nothing need no masks here: a row that sees
+                    // nothing has its weights cleared below
+                    if (__any_sync(0xffffffffu, (vis > 0 && vis < 64) || gaps != 0)) {
 #pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (j >= vis || ((gaps >> (j >> lb)) & 1u))
+                        for (int j = 0; j < 64; ++j)
+                            if (j >= vis || ((gaps >> ((half * 64 + j) >> lb)) & 1u))
                                 x[j] = 0xff800000u;
                     }
-                    float mx = -INFINITY;
-                    {
-                        float a = -INFINITY, b = -INFINITY, c2 = -INFINITY, d2 = -INFINITY;
+                    float a = max3(score(0), score(1), score(2)), b = max3(score(3), score(4), score(5));
 #pragma unroll
-                        for (int j = 0; j < 128; j += 4) {
-                            a = fmaxf(a, __uint_as_float(x[j]));
-                            b = fmaxf(b, __uint_as_float(x[j + 1]));
-                            c2 = fmaxf(c2, __uint_as_float(x[j + 2]));
-                            d2 = fmaxf(d2, __uint_as_float(x[j + 3]));
-                        }
-                        mx = fmaxf(fmaxf(a, b), fmaxf(c2, d2)) * qs;
+                    for (int j = 6; j < 62; j += 4) {
+                        a = max3(a, score(j), score(j + 1));
+                        b = max3(b, score(j + 2), score(j + 3));
                     }
-                    // (-inf + kLazy is -inf: the first visible tile sets the reference)
-                    const bool grow = mx > m + kLazy;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float alpha = grow ? exp2_approx(m - mx) : 1.0f;
-                        m = grow ? mx : m;
-                        l *= alpha;
-                        if (v > seg.p0) {
+                    mx = fmaxf(max3(a, score(62), score(63)), b);
+                    mx = vis > 0 ? mx * qs : -INFINITY;
+                }
+                s_row[half][row] = mx;
+                s_ok[half][quarter] = ok;
+                pair_sync();          // both halves have also read their scores: the weights may take their place
+                mx = fmaxf(mx, s_row[half ^ 1][row]);
+                ok = ok && s_ok[half ^ 1][quarter];      // both go on or neither does
+                if (!ok)
+                    break;
+                // (-inf + kLazy is -inf: the first visible tile sets the reference)
+                const bool grow = mx > m + kLazy;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float alpha = grow ? exp2_approx(m - mx) : 1.0f;
+                    m = grow ? mx : m;
+                    l *= alpha;
+                    if (v > seg.p0) {
+#pragma unroll 1
+                        for (int j = 0; j < kD2; j += 8) {
+                            uint32_t o[8];
+                            tmem_ld8(ot + (uint32_t)j, o);
+                            tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < D; j += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(ot + (uint32_t)j, o);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                tmem_st16(ot + (uint32_t)j, o);
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st8(ot + (uint32_t)j, o);
                         }
                     }
+                }
+                if (any) {
                     const float ref = m == -INFINITY ? 0.0f : kOff - m;
-                    float s0 = 0.0f, s1 = 0.0f;
+                    const uint64_t qs2 = pack2(qs, qs), ref2 = pack2(ref, ref);
+                    const uint32_t keep = vis > 0 ? 0xffffffffu : 0u;
+                    uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                    for (int j = 0; j < 128; j += 32) {
-                        uint32_t hw[16], lw[8];
+                    for (int j = 0; j < 64; j += 32) {
+                        uint32_t hw[FP8 ? 8 : 16], lw[8];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            const float p0 = exp2_approx(fmaf(__uint_as_float(x[j + e]), qs, ref));
-                            const float p1 = exp2_approx(fmaf(__uint_as_float(x[j + e + 1]), qs, ref));
-                            const float p2 = exp2_approx(fmaf(__uint_as_float(x[j + e + 2]), qs, ref));
-                            const float p3 = exp2_approx(fmaf(__uint_as_float(x[j + e + 3]), qs, ref));
-                            s0 += p0 + p1;
-                            s1 += p2 + p3;
+                            float p0, p1, p2, p3;
+                            unpack2(fma2(pack2(score(j + e), score(j + e + 1)), qs2, ref2), p0, p1);
+                            unpack2(fma2(pack2(score(j + e + 2), score(j + e + 3)), qs2, ref2), p2, p3);
+                            p0 = exp2_approx(p0);
+                            p1 = exp2_approx(p1);
+                            p2 = exp2_approx(p2);
+                            p3 = exp2_approx(p3);
+                            sum0 = add2(sum0, pack2(p0, p1));
+                            sum1 = add2(sum1, pack2(p2, p3));
                             if (FP8) {
                                 uint32_t h0, l0, h1, l1;
                                 split_weights(p0, p1, h0, l0);
                                 split_weights(p2, p3, h1, l1);
-                                hw[e / 4] = h0 | (h1 << 16);
-                                lw[e / 4] = l0 | (l1 << 16);
+                                hw[e / 4] = (h0 | (h1 << 16)) & keep;
+                                lw[e / 4] = (l0 | (l1 << 16)) & keep;
                             } else {
-                                hw[e / 2] = bf16x2_from_f32(p0, p1);
-                                hw[e / 2 + 1] = bf16x2_from_f32(p2, p3);
+                                hw[e / 2] = bf16x2_from_f32(p0, p1) & keep;
+                                hw[e / 2 + 1] = bf16x2_from_f32(p2, p3) & keep;
                             }
                         }
                         if (FP8) {
-                            tmem_st8(st + (uint32_t)(j / 4), hw);
-                            tmem_st8(st + 32u + (uint32_t)(j / 4), lw);
+                            tmem_st8(st + (uint32_t)(half * 16 + j / 4), hw);
+                            tmem_st8(st + 32u + (uint32_t)(half * 16 + j / 4), lw);
                         } else {
-                            tmem_st16(st + (uint32_t)(j / 2), hw);
+                            tmem_st16(st + (uint32_t)(half * 32 + j / 2), hw);
                         }
                     }
-                    l += s0 + s1;
+                    float a, b;
+                    unpack2(add2(sum0, sum1), a, b);
+                    l += keep ? a + b : 0.0f;
+                } else {
+                    uint32_t z[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        z[j] = 0u;
+                    tmem_st16(st + (uint32_t)(half * (FP8 ? 16 : 32)), z);
+                    tmem_st16(st + (FP8 ? 32u : 16u) + (uint32_t)(half * (FP8 ? 16 : 32)), z);
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -710,17 +772,20 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             ok = ok && warp_wait(smem_u32(&bar_o), nseg & 1u, abort_flag);
             // ---- output ----
             tc_fence_after();
+            pair_sync();                              // the exchange's maxima have been read
+            s_row[half][row] = l;
+            pair_sync();
+            l = s_row[0][row] + s_row[1][row];
+            pair_sync();                              // before the next segment's maxima
             const bool empty = seg.p1 <= seg.p0;
             const float vs = attn_v_scale(p, seg.c);
             const bool piece = DENSE || w.splits > 1;
             const float inv = piece ? vs * (1.0f / (1 << (int)kOff)) : l == 0.0f ? 0.0f : vs / l;
-            if (FP8)
-                l *= 1.0f / (1 << (int)kOff);      // the sum itself
-            float *dst = nullptr;
-            float *ml = nullptr;
+            l *= 1.0f / (1 << (int)kOff);             // the sum itself
+            float *dst = nullptr, *ml = nullptr;
             if (piece) {
                 if (DENSE && seg.whole) {
-                    dst = w.rows + ((seg.t0 + qi) * p.hq + seg.c * p.group + hi) * (D + 4);
+                    dst = w.rows + ((int64_t)(seg.t0 + qi) * p.hq + seg.c * p.group + hi) * (D + 4);
                     ml = dst + D;
                 } else {
                     const int64_t sl = DENSE ? (seg.began ? (int64_t)gridDim.x : 0) + blockIdx.x : (int64_t)blockIdx.x;
@@ -728,66 +793,65 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     dst = base + row * D;
                     ml = base + 128 * D + 2 * row;
                 }
+                dst += half * kD2;
             }
             bool finite = true;
-            const uint32_t stage = qsm + (uint32_t)(quarter * 32 * D * 2);      // this warp's rows of the query tile
+            // this warp's half rows, in the query tile, which no MMA reads any more
+            const uint32_t stage = qsm + (uint32_t)((half * 4 + quarter) * 32 * kD2 * 2);
 #pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
-                uint32_t o[32];
+            for (int j = 0; j < kD2; j += 16) {
+                uint32_t o[16];
                 if (ok && !empty) {
-                    tmem_ld32(ot + (uint32_t)j, o);
+                    tmem_ld16(ot + (uint32_t)j, o);
                     tc_wait_ld();
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 16; ++e)
                         o[e] = 0u;
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float x = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
-                    finite = finite && fabsf(x) < INFINITY;
-                    o[e] = __float_as_uint(ok ? x : nan);
+                for (int e = 0; e < 16; ++e) {
+                    const float y = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+                    finite = finite && fabsf(y) < INFINITY;
+                    o[e] = __float_as_uint(ok ? y : nan);
                 }
                 if (piece) {
                     if (real)
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
+                        for (int e = 0; e < 16; e += 4)
                             *reinterpret_cast<float4 *>(dst + j + e) =
                                 make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                             __uint_as_float(o[e + 3]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        const int chunk = (j + e) / 8;
-                        sts128(stage + (uint32_t)(lane * D * 2 + ((chunk ^ (lane & 7)) << 4)),
+                    for (int e = 0; e < 16; e += 8)
+                        sts128(stage + (uint32_t)(lane * kD2 * 2 + ((((j + e) / 8) ^ (lane & (kD2 / 8 - 1))) << 4)),
                                bf16x2_from_f32(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
                                bf16x2_from_f32(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
                                bf16x2_from_f32(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
                                bf16x2_from_f32(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-                    }
                 }
             }
             tc_fence_before();
             if (piece) {
-                if (real) {
+                if (real && half == 0) {
                     ml[0] = ok ? m : nan;
                     ml[1] = ok ? l : nan;
                 }
             } else {
-                if (real && p.lse)
-                    p.lse[hr] = ok ? attn_lse(m, l) : nan;
+                if (real && half == 0 && p.lse)
+                    p.lse[head_row()] = ok ? attn_lse(m, l) : nan;
                 __syncwarp();
-                // rows of 2 * D bytes, several a step
-                constexpr int kLanes = D / 8;
+                constexpr int kLanes = kD2 / 8;      // 16-byte pieces of a half row
                 for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
                     const int rr = quarter * 32 + r, q2 = rr >> w.gp_shift, h2 = rr & (gp - 1), ch = lane % kLanes;
                     if (q2 < seg.nq && h2 < p.group) {
-                        uint4 x;
+                        uint4 y;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                     : "r"(stage + (uint32_t)(r * D * 2 + ((ch ^ (r & 7)) << 4))));
+                                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                     : "r"(stage + (uint32_t)(r * kD2 * 2 + ((ch ^ (r & (kLanes - 1))) << 4))));
                         const int64_t o = (w.q0 + seg.t0 + q2) * p.hq + seg.c * p.group + h2;
-                        *reinterpret_cast<uint4 *>(p.out + o * D + ch * 8) = x;
+                        *reinterpret_cast<uint4 *>(p.out + o * D + half * kD2 + ch * 8) = y;
                     }
                 }
                 __syncwarp();
@@ -798,24 +862,24 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;
-                    const int64_t hr2 = __shfl_sync(0xffffffffu, hr, src);
+                    const int64_t hr2 = __shfl_sync(0xffffffffu, head_row(), src);
                     const int len2 = __shfl_sync(0xffffffffu, len, src), q2 = __shfl_sync(0xffffffffu, qi, src);
                     const float m2 = __shfl_sync(0xffffffffu, m, src), inv2 = __shfl_sync(0xffffffffu, inv, src);
                     float *dst2 = reinterpret_cast<float *>(__shfl_sync(0xffffffffu, (unsigned long long)dst, src));
-                    float acc[D / 32] = {};
-                    for (int64_t v = seg.p0; v < seg.p1; ++v) {
-                        const int e = (int)(v / per_block);
+                    float acc[kD2 / 32] = {};
+                    for (int v = seg.p0; v < seg.p1; ++v) {
+                        int e;
+                        const int64_t tok0 = list_tile(v, e);
                         if (!((u.sp.mask[e] >> q2) & 1u))
                             continue;
-                        const int32_t blk = u.sp.block[e];
-                        const int64_t tok0 = (int64_t)(blk & 0xFFFFFF) * p.block_tokens + v % per_block * 128;
                         for (int j = 0; j < 128 && tok0 + j < len2; ++j) {
-                            const int32_t pg = attn_page(p, u.sp.toff[blk >> 24], tok0 + j);
+                            const int32_t pg = attn_page(p, u.sp.toff[u.sp.block[e] >> 24], tok0 + j);
                             if (pg < 0)
                                 continue;
                             const int64_t r = attn_page_row(p, tok0 + j);
                             const int64_t ko = (int64_t)pg * p.k.stride_page + seg.c * p.k.stride_head + r * p.k.stride_token;
-                            const int64_t vo = (int64_t)pg * p.v.stride_page + seg.c * p.v.stride_head + r * p.v.stride_token;
+                            const int64_t vo = (int64_t)pg * p.v.stride_page + seg.c * p.v.stride_head +
+                                               r * p.v.stride_token + half * kD2;
                             float dot = 0.0f;
                             for (int d = lane; d < D; d += 32)
                                 dot = fmaf(attn_value(p.k, ko + d), __uint_as_float((uint32_t)p.q[hr2 * D + d] << 16), dot);
@@ -824,16 +888,16 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                                 dot += __shfl_xor_sync(0xffffffffu, dot, o);
                             const float wgt = exp2_approx(dot * ks - m2 + kOff);
 #pragma unroll
-                            for (int d = 0; d < D / 32; ++d)
+                            for (int d = 0; d < kD2 / 32; ++d)
                                 acc[d] = fmaf(wgt, attn_value(p.v, vo + lane + 32 * d), acc[d]);
                         }
                     }
 #pragma unroll
-                    for (int d = 0; d < D / 32; ++d) {
+                    for (int d = 0; d < kD2 / 32; ++d) {
                         if (dst2)
                             dst2[lane + 32 * d] = acc[d] * inv2;
                         else
-                            p.out[hr2 * D + lane + 32 * d] = attn_bf16(acc[d] * inv2);
+                            p.out[hr2 * D + half * kD2 + lane + 32 * d] = attn_bf16(acc[d] * inv2);
                     }
                 }
             }

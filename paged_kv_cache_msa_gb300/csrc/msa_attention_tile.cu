@@ -12,15 +12,17 @@
 // bytes in shared memory); bf16 on kind::f16.
 //   warp 0     TMA: page lookups one tile ahead, key and value copies
 //   warp 1     MMAs; zeroes value rows past the history before they are multiplied
-//   warps 2-9  softmax and output, two threads per row (64 tokens of a tile, half the dims)
-// The chain scores -> softmax -> values of one CTA leaves the tensor cores idle during the
-// softmax, so two CTAs share an SM (half the tensor memory and half the shared memory each)
-// and fill each other's gaps: a tile is 1,024 cycles of MMA, as many of exponentials, and
-// about 1,200 issue slots of a scheduler.
-//
+//   warps 2-9  softmax and output: two groups of four, a thread per row; group g takes the
+//              tokens 64 g .. 64 g + 63 of every tile, then D / 2 of the dims
+// Scores are made 64 tokens at a time into two buffers, one a group, so that the scores of
+// one half are ready while the other's softmax runs, and two CTAs share an SM (half the
+// tensor memory and half the shared memory each).  A tile of E4M3 keys takes about 1,280
+// cycles of the tensor pipe (the 64-token score MMAs read the queries from shared memory
+// twice), 1,024 of exponentials and 1,000 issue slots of a scheduler.
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
-// output in tensor memory rescaled, which few tiles after the first need.
+// output in tensor memory rescaled, which few tiles after the first need.  The groups hand
+// the reference of a row to one another half by half.
 //
 // Sparse (DENSE = false): the tile's queries run over the union of their blocks, each row
 // masked to its own.  A weight of zero does not hide an infinity or a NaN in the values of
@@ -53,7 +55,6 @@ struct TileShape {
     static constexpr int kStages = kTileBytes == 32768 ? 1 : 2;   // of keys, and of values
     static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
     static constexpr int kTmem = 256;                             // scores (and weights) | output
-    static constexpr int kPSteps = FP8 ? 4 : 8;                   // MMA steps along 128 tokens
     static_assert(2 * kStages * kTileBytes >= 4 * kMaxList * 8, "scratch of the list");
 };
 
@@ -72,6 +73,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 
@@ -195,7 +203,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
     __shared__ __align__(8) uint64_t bar_info[kInfo];
-    __shared__ __align__(8) uint64_t bar_q, bar_s, bar_p, bar_pv, bar_o, bar_drain;
+    __shared__ __align__(8) uint64_t bar_q, bar_s[2], bar_p[2], bar_pv, bar_o, bar_drain;
+    __shared__ __align__(8) uint64_t bar_ref[2][4];
     __shared__ uint8_t s_nv[kInfo][kMaxBoxes];     // visible rows of each box
     __shared__ uint32_t s_gap[kInfo];              // boxes without a page before the history's end
     __shared__ union {
@@ -207,7 +216,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             int32_t len[kTileQueries], lead[kTileQueries], maxlen[kTileQueries];
         } sp;
     } u;
-    __shared__ float s_row[2][128];                // exchange between the two threads of a row
+    __shared__ float s_ref[128], s_row[2][128];    // exchange between the two threads of a row
     __shared__ int s_ok[2][4];
     __shared__ int s_n;
     __shared__ uint32_t s_tmem;
@@ -230,8 +239,12 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         for (int i = 0; i < kInfo; ++i)
             mbar_init(smem_u32(&bar_info[i]), 1);
         mbar_init(smem_u32(&bar_q), 8);
-        mbar_init(smem_u32(&bar_s), 1);
-        mbar_init(smem_u32(&bar_p), 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar_s[i]), 1);
+            mbar_init(smem_u32(&bar_p[i]), 4);
+            for (int j = 0; j < 4; ++j)
+                mbar_init(smem_u32(&bar_ref[i][j]), 1);
+        }
         mbar_init(smem_u32(&bar_pv), 1);
         mbar_init(smem_u32(&bar_o), 1);
         mbar_init(smem_u32(&bar_drain), 1);
@@ -501,69 +514,98 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
 #endif
     } else if (warp == 1) {
         // ---------------- MMAs ----------------
-        constexpr uint32_t kIdS = mma_idesc(FP8, 128, 128, false, false);
+        constexpr uint32_t kIdS = mma_idesc(FP8, 128, 64, false, false);
         constexpr uint32_t kIdO = mma_idesc(FP8, 128, D, false, true);
-        constexpr int kTok = 128 / S::kPSteps;
+        constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step of the values
+        constexpr int kStep = kTok * S::kSwz / 16;
         const int BR = w.box_rows, nbox = 128 / BR;
-        uint32_t it = 0, nseg = 0;
+        const uint64_t q_desc = smem_desc(qsm, S::kSwz, 16u, 8u * S::kSwz);
+        const uint64_t k_desc = smem_desc(kring, S::kSwz, 16u, 8u * S::kSwz);
+        const uint64_t v_desc = smem_desc(vring, S::kSwz, 128u * S::kSwz, 8u * S::kSwz);
+        uint32_t it = 0, nseg = 0;        // it: tiles whose values were multiplied
         bool ok = true;
         for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
-            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
-            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
-                const uint32_t s = it % ST, ph = (it / ST) & 1u;
-                ok = warp_wait(smem_u32(&bar_k_full[s]), ph, abort_flag);
-                // the weights of the tile before, which the scores overwrite, are multiplied
-                ok = ok && (it == 0 || warp_wait(smem_u32(&bar_pv), (it - 1u) & 1u, abort_flag));
+            // the scores of half g of the CTA's tile i; `after`: right after the values of that
+            // half of tile i - 1 (the first tile of a segment comes after everything, since
+            // its queries are made when the output before was read)
+            auto scores = [&](uint32_t i, int g, bool after) {
+                const uint32_t s = i % ST;
+                if (g == 0)
+                    ok = warp_wait(smem_u32(&bar_k_full[s]), (i / ST) & 1u, abort_flag);
+                // the weights of the half before, whose place the scores take, are multiplied
+                ok = ok && (!after || warp_wait(smem_u32(&bar_pv), (uint32_t)g, abort_flag));
                 if (!ok)
-                    break;
+                    return;
                 tc_fence_after();
-                const uint32_t kt = kring + s * (uint32_t)S::kTileBytes;
+                const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
+                const uint32_t d = tmem + (uint32_t)(g * 64);
+                if (S::kSwz == 128) {
+                    // a swizzle atom is four steps; the halves, or the atoms of a row, follow
+                    mma_ss4<FP8, 2, 2>(d, q_desc, kd, kIdS, 0);
+                    if (D == 128)
+                        mma_ss4<FP8, 2, 2>(d, q_desc + 128 * 128 / 16, FP8 ? kd : kd + 128 * 128 / 16, kIdS, 1);
+                } else {
 #pragma unroll
-                for (int half = 0; half < (FP8 ? 2 : 1); ++half)
-#pragma unroll
-                    for (int ks = 0; ks < S::kRowBytes / 32; ++ks) {
-                        const uint32_t at = (uint32_t)(ks * 32) / S::kSwz, col = (uint32_t)(ks * 32) % S::kSwz;
-                        mma_ss<FP8>(tmem,
-                                    smem_desc(qsm + (uint32_t)(half * 128 * D) + at * (128u * S::kSwz) + col, S::kSwz, 16u,
-                                              8u * S::kSwz),
-                                    smem_desc(kt + at * (128u * S::kSwz) + col, S::kSwz, 16u, 8u * S::kSwz), kIdS,
-                                    half > 0 || ks > 0);
-                    }
-                mma_commit(smem_u32(&bar_s));
-                mma_commit(smem_u32(&bar_k_empty[s]));
-                ok = warp_wait(smem_u32(&bar_v_full[s]), ph, abort_flag);
-                if (!ok)
-                    break;
-                const uint32_t vt = vring + s * (uint32_t)S::kTileBytes;
-                // rows past the history may hold anything: a weight of zero would not hide
-                // an infinity or a NaN
-                const int nv = lane < nbox ? s_nv[it % kInfo][lane] : 0;
-                uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
-                if (partial) {
-                    while (partial) {
-                        const int b = __ffs(partial) - 1;
-                        partial &= partial - 1;
-                        const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
-                        for (int at = 0; at < S::kAtoms; ++at)
-                            for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
-                                sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
+                    for (int ks = 0; ks < 4; ++ks)    // two steps of hi, two of lo
+                        mma_ss<FP8>(d, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
+                                    kd + (uint64_t)((ks & 1) * 2), kIdS, ks > 0);
                 }
-                ok = warp_wait(smem_u32(&bar_p), it & 1u, abort_flag);
-                if (!ok)
-                    break;
-                tc_fence_after();
+                mma_commit(smem_u32(&bar_s[g]));
+                if (g == 1)
+                    mma_commit(smem_u32(&bar_k_empty[s]));
+            };
+            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
+            if (ok && seg.p0 < seg.p1) {
+                scores(it, 0, false);
+                if (ok)
+                    scores(it, 1, false);
+            }
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+                const uint32_t s = it % ST;
+                for (int g = 0; g < 2 && ok; ++g) {
+                    const uint32_t vt = vring + s * (uint32_t)S::kTileBytes;
+                    if (g == 0) {
+                        ok = warp_wait(smem_u32(&bar_v_full[s]), (it / ST) & 1u, abort_flag);
+                        if (!ok)
+                            break;
+                        // rows past the history may hold anything: a weight of zero would not
+                        // hide an infinity or a NaN
+                        const int nv = lane < nbox ? s_nv[it % kInfo][lane] : 0;
+                        uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
+                        if (partial) {
+                            while (partial) {
+                                const int b = __ffs(partial) - 1;
+                                partial &= partial - 1;
+                                const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
+                                for (int at = 0; at < S::kAtoms; ++at)
+                                    for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
+                                        sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
+                            }
+                            fence_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    ok = warp_wait(smem_u32(&bar_p[g]), it & 1u, abort_flag);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
+                    const uint32_t pt = tmem + (uint32_t)(g * 64), acc = v > seg.p0 || g > 0;
+                    if (FP8) {      // two steps of hi, two of lo against the same values
 #pragma unroll
-                for (int half = 0; half < (FP8 ? 2 : 1); ++half)
-#pragma unroll
-                    for (int ks = 0; ks < S::kPSteps; ++ks)
-                        mma_ts<FP8>(tmem + 128u, tmem + (uint32_t)(half * 32 + ks * 8),
-                                    smem_desc(vt + (uint32_t)(ks * kTok * S::kSwz), S::kSwz, 128u * S::kSwz, 8u * S::kSwz),
-                                    kIdO, v > seg.p0 || half > 0 || ks > 0);
-                mma_commit(smem_u32(&bar_pv));
-                mma_commit(smem_u32(&bar_v_empty[s]));
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts<FP8>(tmem + 128u, pt + (uint32_t)(ks * 8), vd + (uint64_t)((ks & 1) * kStep), kIdO,
+                                        acc | (uint32_t)ks);
+                    } else {
+                        mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kIdO, acc);
+                    }
+                    mma_commit(smem_u32(&bar_pv));
+                    if (g == 1)
+                        mma_commit(smem_u32(&bar_v_empty[s]));
+                    // the half's next scores, when these values are multiplied
+                    if (v + 1 < seg.p1)
+                        scores(it + 1, g, true);
+                }
             }
             __syncwarp();
             if (ok)
@@ -576,7 +618,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     } else {
         // ---------------- softmax and output ----------------
         const int quarter = warp & 3, row = quarter * 32 + lane, half = (warp - 2) >> 2;
-        const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16), ot = st + 128u + (uint32_t)(half * (D / 2));
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t st = lanes + (uint32_t)(half * 64), ot = lanes + 128u;
         const int gp = 1 << w.gp_shift, qi = row >> w.gp_shift, hi = row & (gp - 1);
         const int BR = w.box_rows, lb = __ffs(BR) - 1;
         constexpr float kLazy = FP8 ? kLazyFp8 : kLazyBf16, kOff = FP8 ? kPOffset : 0.0f;
@@ -644,11 +687,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             if (lane == 0)
                 mbar_arrive(smem_u32(&bar_q));
             const int len = DENSE ? seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;                 // the reference that l is relative to
             for (int v = seg.p0; v < seg.p1; ++v, ++it) {
                 ok = ok && warp_wait(smem_u32(&bar_info[it % kInfo]), (it / kInfo) & 1u, abort_flag);
-                // tokens of this thread's half that the row sees, from its first; -1: it sees none
-                // of the whole tile
+                // tokens of this thread's half that the row sees, from its first
                 int vis;
                 if (DENSE) {
                     vis = len - v * 128;
@@ -660,16 +702,18 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 }
                 vis = real ? vis - half * 64 : -1;
                 const uint32_t gaps = ok ? s_gap[it % kInfo] : 0u;
-                ok = ok && warp_wait(smem_u32(&bar_s), it & 1u, abort_flag);
+                ok = ok && warp_wait(smem_u32(&bar_s[half]), it & 1u, abort_flag);
+                if (!ok)
+                    break;
                 tc_fence_after();
-                uint32_t x[64] = {};
+                uint32_t x[64];
+                tmem_ld32(st, x);
+                tmem_ld32(st + 32u, x + 32);
+                tc_wait_ld();
                 auto score = [&](int j) { return __uint_as_float(x[j]); };
                 float mx = -INFINITY;
                 const bool any = __any_sync(0xffffffffu, vis > 0);
-                if (ok && any) {
-                    tmem_ld32(st + (uint32_t)(half * 64), x);
-                    tmem_ld32(st + (uint32_t)(half * 64 + 32), x + 32);
-                    tc_wait_ld();
+                if (any) {
                     // rows that see all or nothing need no masks here: a row that sees
                     // nothing has its weights cleared below
                     if (__any_sync(0xffffffffu, (vis > 0 && vis < 64) || gaps != 0)) {
@@ -687,22 +731,27 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     mx = fmaxf(max3(a, score(62), score(63)), b);
                     mx = vis > 0 ? mx * qs : -INFINITY;
                 }
-                s_row[half][row] = mx;
-                s_ok[half][quarter] = ok;
-                pair_sync();          // both halves have also read their scores: the weights may take their place
-                mx = fmaxf(mx, s_row[half ^ 1][row]);
-                ok = ok && s_ok[half ^ 1][quarter];      // both go on or neither does
-                if (!ok)
-                    break;
-                // (-inf + kLazy is -inf: the first visible tile sets the reference)
-                const bool grow = mx > m + kLazy;
+                // the reference, from the half before
+                float ref = -INFINITY;
+                if (half > 0 || v > seg.p0) {
+                    ok = warp_wait(smem_u32(&bar_ref[half ^ 1][quarter]), (half > 0 ? it : it - 1u) & 1u, abort_flag);
+                    if (!ok)
+                        break;
+                    ref = s_ref[row];
+                }
+                // (-inf + kLazy is -inf: the first visible half sets the reference)
+                const bool grow = mx > ref + kLazy;
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float alpha = grow ? exp2_approx(m - mx) : 1.0f;
-                    m = grow ? mx : m;
-                    l *= alpha;
-                    if (v > seg.p0) {
+                    const float alpha = grow ? exp2_approx(ref - mx) : 1.0f;
+                    ref = grow ? mx : ref;
+                    if (half > 0 || v > seg.p0) {
+                        // the values of the half before are in the output
+                        ok = warp_wait(smem_u32(&bar_pv), (uint32_t)(half ^ 1), abort_flag);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
 #pragma unroll 1
-                        for (int j = 0; j < kD2; j += 8) {
+                        for (int j = 0; j < D; j += 8) {
                             uint32_t o[8];
                             tmem_ld8(ot + (uint32_t)j, o);
                             tc_wait_ld();
@@ -713,19 +762,25 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                         }
                     }
                 }
+                s_ref[row] = ref;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bar_ref[half][quarter]));
+                l = m == ref ? l : l * exp2_approx(m - ref);
+                m = ref;
                 if (any) {
-                    const float ref = m == -INFINITY ? 0.0f : kOff - m;
-                    const uint64_t qs2 = pack2(qs, qs), ref2 = pack2(ref, ref);
+                    const float off = m == -INFINITY ? 0.0f : kOff - m;
+                    const uint64_t qs2 = pack2(qs, qs), off2 = pack2(off, off);
                     const uint32_t keep = vis > 0 ? 0xffffffffu : 0u;
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 32) {
-                        uint32_t hw[FP8 ? 8 : 16], lw[8];
+                    for (int j = 0; j < 64; j += 16) {
+                        uint32_t hw[FP8 ? 4 : 8], lw[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
+                        for (int e = 0; e < 16; e += 4) {
                             float p0, p1, p2, p3;
-                            unpack2(fma2(pack2(score(j + e), score(j + e + 1)), qs2, ref2), p0, p1);
-                            unpack2(fma2(pack2(score(j + e + 2), score(j + e + 3)), qs2, ref2), p2, p3);
+                            unpack2(fma2(pack2(score(j + e), score(j + e + 1)), qs2, off2), p0, p1);
+                            unpack2(fma2(pack2(score(j + e + 2), score(j + e + 3)), qs2, off2), p2, p3);
                             p0 = exp2_approx(p0);
                             p1 = exp2_approx(p1);
                             p2 = exp2_approx(p2);
@@ -743,11 +798,11 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                                 hw[e / 2 + 1] = bf16x2_from_f32(p2, p3) & keep;
                             }
                         }
-                        if (FP8) {
-                            tmem_st8(st + (uint32_t)(half * 16 + j / 4), hw);
-                            tmem_st8(st + 32u + (uint32_t)(half * 16 + j / 4), lw);
+                        if (FP8) {      // 16 columns of hi, 16 of lo
+                            tmem_st4(st + (uint32_t)(j / 4), hw);
+                            tmem_st4(st + 16u + (uint32_t)(j / 4), lw);
                         } else {
-                            tmem_st16(st + (uint32_t)(half * 32 + j / 2), hw);
+                            tmem_st8(st + (uint32_t)(j / 2), hw);
                         }
                     }
                     float a, b;
@@ -758,25 +813,29 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         z[j] = 0u;
-                    tmem_st16(st + (uint32_t)(half * (FP8 ? 16 : 32)), z);
-                    tmem_st16(st + (FP8 ? 32u : 16u) + (uint32_t)(half * (FP8 ? 16 : 32)), z);
+                    tmem_st16(st, z);
+                    tmem_st16(st + 16u, z);
                 }
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_u32(&bar_p));
+                    mbar_arrive(smem_u32(&bar_p[half]));
             }
             if (!ok)
                 *abort_flag = 1;
             ok = ok && warp_wait(smem_u32(&bar_o), nseg & 1u, abort_flag);
             // ---- output ----
             tc_fence_after();
-            pair_sync();                              // the exchange's maxima have been read
-            s_row[half][row] = l;
+            s_ok[half][quarter] = ok;
+            pair_sync();                              // both halves are through
+            ok = ok && s_ok[half ^ 1][quarter];
+            const float top = seg.p1 > seg.p0 ? s_ref[row] : -INFINITY;
+            s_row[half][row] = m == top ? l : l * exp2_approx(m - top);
+            m = top;
             pair_sync();
             l = s_row[0][row] + s_row[1][row];
-            pair_sync();                              // before the next segment's maxima
+            pair_sync();                              // read before the next segment writes
             const bool empty = seg.p1 <= seg.p0;
             const float vs = attn_v_scale(p, seg.c);
             const bool piece = DENSE || w.splits > 1;
@@ -802,7 +861,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             for (int j = 0; j < kD2; j += 16) {
                 uint32_t o[16];
                 if (ok && !empty) {
-                    tmem_ld16(ot + (uint32_t)j, o);
+                    tmem_ld16(ot + (uint32_t)(half * kD2 + j), o);
                     tc_wait_ld();
                 } else {
 #pragma unroll

@@ -163,6 +163,71 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
             : "memory");
 }
 
+// Four MMAs in a row, whose operands lie AS and BS apart (in descriptor units of 16 bytes;
+// for A in tensor memory, columns): one election, and operands made in place, since the
+// issue of an MMA costs its warp several times the instructions that describe it.
+template <bool FP8, int AS, int BS>
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if (FP8)
+        asm volatile(
+            "{\n\t.reg .pred pp, pe;\n\t.reg .b64 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
+            "add.u64 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
+            "add.u64 a2, a1, %5;\n\tadd.u64 b2, b1, %6;\n\t"
+            "add.u64 a3, a2, %5;\n\tadd.u64 b3, b2, %6;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, pp;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred pp, pe;\n\t.reg .b64 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
+            "add.u64 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
+            "add.u64 a2, a1, %5;\n\tadd.u64 b2, b1, %6;\n\t"
+            "add.u64 a3, a2, %5;\n\tadd.u64 b3, b2, %6;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pp;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
+            : "memory");
+}
+
+template <bool FP8, int AS, int BS>
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if (FP8)
+        asm volatile(
+            "{\n\t.reg .pred pp, pe;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
+            "add.u32 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
+            "add.u32 a2, a1, %5;\n\tadd.u64 b2, b1, %6;\n\t"
+            "add.u32 a3, a2, %5;\n\tadd.u64 b3, b2, %6;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, pp;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a1], b1, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a2], b2, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred pp, pe;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
+            "add.u32 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
+            "add.u32 a2, a1, %5;\n\tadd.u64 b2, b1, %6;\n\t"
+            "add.u32 a3, a2, %5;\n\tadd.u64 b3, b2, %6;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pp;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
+            : "memory");
+}
+
 // Arrives on `bar` when every MMA this warp's elected lane has issued is complete.
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {

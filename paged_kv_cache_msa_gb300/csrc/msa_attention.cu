@@ -386,10 +386,11 @@ int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t num_gr
     return layout_of(cfg, T, num_groups).bytes;
 }
 
-// Rows of the widest TMA box that never crosses a page or a selected block: a power of two.
-int box_rows(const AttnParams &p)
+// Rows of the widest TMA box, at most `limit`, that never crosses a page or a selected
+// block: a power of two.
+int box_rows(const AttnParams &p, int limit)
 {
-    int br = 128;
+    int br = limit;
     while (br > 1 && (p.page_size % br || (p.topk_ids && p.block_tokens % br)))
         br /= 2;
     return br;
@@ -445,11 +446,12 @@ struct Maps {
     int32_t oob_page;
 };
 
-void make_maps(Maps *m, const AttnParams &p, int head_dim)
+// `limit`: rows of a box at most (128, or a step of the tile kernel).
+void make_maps(Maps *m, const AttnParams &p, int head_dim, int limit)
 {
     memset(m, 0, sizeof *m);
     m->sms = tensor_sms();
-    const int br = box_rows(p);
+    const int br = box_rows(p, limit);
     if (m->sms == 0 || br < 8 || p.k.fp8 != p.v.fp8 || !encode_cache(&m->k, p.k, head_dim, p.hkv, p.page_size, br) ||
         !encode_cache(&m->v, p.v, head_dim, p.hkv, p.page_size, br))
         return;
@@ -532,7 +534,7 @@ msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l
     t.ctas = (int32_t)(units * t.splits);
     msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
     if (s == MSA_OK && t.splits > 1)
-        s = launched(attn_join_splits(p, t, head_dim, stream));
+        s = launched(attn_join_splits(p, pieces_of(p, maps, l, workspace), t, head_dim, stream));
     return s;
 }
 
@@ -617,13 +619,14 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
     AttnParams p = params_of(cfg, num_queries, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache,
                              scales, out, lse);
     p.topk_ids = topk_ids;
+    // a step of the tile kernel lies in one block
+    const bool tiled = (launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % kAttnStep == 0;
     Maps maps;
-    make_maps(&maps, p, cfg->head_dim);
+    make_maps(&maps, p, cfg->head_dim, tiled ? kAttnStep : 128);
     if (maps.box_rows == 0)
         return launch_rows(p, cfg->head_dim, stream);
     const Layout l = layout_of(cfg, num_queries, 0);
-    // tiles are of 128 tokens of one block
-    if ((launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % 128 == 0)
+    if (tiled)
         return run_query_runs(p, maps, l, cfg->head_dim, workspace, stream);
     return run_decode(p, maps, l, cfg->head_dim, workspace, stream);
 }
@@ -661,7 +664,7 @@ extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg,
     p.prefix_offset = prefix_offset;
     p.num_groups = (int32_t)num_groups;
     Maps maps;
-    make_maps(&maps, p, cfg->head_dim);
+    make_maps(&maps, p, cfg->head_dim, num_groups > 0 ? kAttnStep : 128);
     if (maps.box_rows == 0)
         return launch_rows(p, cfg->head_dim, stream);
     const Layout l = layout_of(cfg, num_queries, num_groups);

@@ -887,189 +887,186 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
 // the join of pieces
 // ---------------------------------------------------------------------------
 //
-// A row of pieces is summed by one warp; the maxima and sums are brought a piece a lane,
-// so that a row costs three rounds of loads whatever the number of pieces.  Most of them
-// lie in L2.
-template <int D>
-struct Row {
-    static constexpr int E = D / 32;
-    float m = -INFINITY, l = 0.0f, acc[E] = {};
+// One block joins the pieces of up to 16 heads of one query on one K/V head: the maxima
+// and sums of 32 pieces at a time are brought a piece a lane and become weights in shared
+// memory, then a thread adds four dims over the pieces.  The pieces lie in L2, so the time
+// is a few rounds of loads; the code is kept short because it runs once.
+enum JoinMode { kJoinCut, kJoinRows, kJoinSplits };
 
-    // adds up to 32 pieces: lane i brings piece i (its row of output o, maximum pm, sum pl)
-    __device__ __forceinline__ void add(int count, const float *o, float pm, float pl, int lane)
-    {
-        const bool seen = lane < count && pl != 0.0f;       // a NaN goes on
-        float mn = seen ? pm : -INFINITY;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
-            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-        mn = fmaxf(mn, m);
-        const float a = m == -INFINITY ? 0.0f : exp2f(m - mn);
-        const float b = seen ? exp2f(pm - mn) : 0.0f;
-        float sum = seen ? pl * b : 0.0f;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l = l * a + sum;
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] *= a;
-#pragma unroll 8
-        for (int i = 0; i < count; ++i) {
-            const float *oi = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)o, i));
-            const float bi = __shfl_sync(0xffffffffu, b, i);
-            float x[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[e] = __ldcg(oi + lane + 32 * e);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] += bi == 0.0f ? 0.0f : x[e] * bi;
-        }
-    }
-    __device__ __forceinline__ void write(const AttnParams &p, int64_t row, int lane)
-    {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            p.out[row * D + lane + 32 * e] = attn_bf16(l == 0.0f ? 0.0f : acc[e] / l);
-        if (lane == 0 && p.lse)
-            p.lse[row] = attn_lse(m, l);
-    }
+constexpr int kJoinHeads = 16;
+
+// Where piece i is: output rows and maxima of the block's heads, each `stride` floats
+// apart, the sums `sums` floats after the maxima.
+struct PieceAt {
+    const float *o, *m;
+    int stride, mstride, sums;
 };
 
-// Adds the pieces 0 .. n - 1; piece(i, o, ml) gives where piece i's output row, maximum and
-// sum are.
-template <int D, typename Fn>
-__device__ __forceinline__ void add_pieces(Row<D> &r, int n, int lane, Fn &&piece)
+template <int D, JoinMode MODE>
+__global__ void __launch_bounds__(kJoinHeads * D / 4)
+msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPieces w,
+                          const __grid_constant__ AttnTiles tl)
 {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const float *o, *pm, *pl;
-        piece(min(i0 + lane, n - 1), o, pm, pl);
-        r.add(min(32, n - i0), o, __ldcg(pm), __ldcg(pl), lane);
-    }
-}
-
-// Column `col` of a (query, head chunk) that began in CTA c0 and ended in c1 > c0: the
-// slots ctas + c0, c0 + 1, ..., c1.
-template <int D>
-__device__ __forceinline__ void add_cut(Row<D> &r, const AttnPieces &w, int c0, int c1, int col, int lane)
-{
-    const int size = w.heads * (D + 2);
-    add_pieces<D>(r, c1 - c0 + 1, lane, [&](int i, const float *&o, const float *&pm, const float *&pl) {
-        const float *piece = w.pieces + (int64_t)(i > 0 ? c0 + i : w.ctas + c0) * size;
-        o = piece + col * D;
-        pm = piece + w.heads * D + col;
-        pl = pm + w.heads;
-    });
-}
-
-// The (query, head chunk)s that a CTA began and did not finish: one block a CTA, one warp
-// a head.
-template <int D>
-__global__ void __launch_bounds__(512)
-msa_attention_join_cut_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPieces w)
-{
+    __shared__ float s_w[32][kJoinHeads];            // weights of the pieces
+    __shared__ float s_scale[kJoinHeads];            // of what was added before them
+    __shared__ float s_m[kJoinHeads], s_l[kJoinHeads];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;
-    const int4 cut = __ldcg(w.cut + blockIdx.x);
-    const int nch = (p.group + w.heads - 1) / w.heads;
-    const int head = cut.y / nch, hcol = cut.y % nch * w.heads;
-    if (cut.x < 0 || hcol + col >= p.group)
-        return;
-    Row<D> r;
-    add_cut<D>(r, w, blockIdx.x, cut.z, col, lane);
-    r.write(p, (w.q0 + cut.x) * p.hq + head * p.group + hcol + col, lane);
-}
-
-constexpr int kJoinWarps = 8;
-
-// A window's rows: each query's own tokens and the prefix of its group.
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-msa_attention_join_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPieces w,
-                               const __grid_constant__ AttnTiles tl)
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int lane = threadIdx.x & 31;
-    const int x = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);       // below 384 x 128 x 1024
-    if (x >= w.nq * p.hq)
-        return;
-    const int q = x / p.hq, h = x - q * p.hq, c = h / p.group, hg = h - c * p.group;
-    Row<D> r;
-    auto add_whole = [&](const float *rows) {
-        add_pieces<D>(r, 1, lane, [&](int, const float *&o, const float *&pm, const float *&pl) {
-            o = rows + (int64_t)x * (D + 4);
-            pm = o + D;
-            pl = o + D + 1;
-        });
-    };
-    // its own tokens
-    const int64_t lo = __ldcg(w.pre + q), nt = __ldcg(w.pre + q + 1) - lo;
-    if (nt > 0) {
+    int q, c, hcol, nh;                              // query of the window, K/V head, its first head here, heads
+    int own0 = 0, own1 = -1, pre0 = 0, pre1 = -1;    // CTAs that hold the pieces
+    int prow = 0;                                    // row of the first head in a tile slot
+    if (MODE == kJoinCut) {
+        const int4 cut = __ldcg(w.cut + blockIdx.x);
+        if (cut.x < 0)
+            return;
         const int nch = (p.group + w.heads - 1) / w.heads;
-        const int64_t share = div64(__ldcg(w.pre + w.nq) * w.head_chunks + w.ctas - 1, w.ctas);
-        const int64_t base = lo * w.head_chunks + (int64_t)(c * nch + hg / w.heads) * nt;
-        const int c0 = (int)div64(base, share), c1 = (int)div64(base + nt - 1, share);
-        if (c0 == c1)
-            add_whole(w.rows);
-        else
-            add_cut<D>(r, w, c0, c1, hg % w.heads, lane);
-    }
-    // its group's prefix: the group before the first that starts after it
-    int g = -1;
-    for (int i0 = 0; i0 <= p.num_groups && g < 0; i0 += 32) {
-        const bool after = i0 + lane <= p.num_groups && __ldcg(tl.groups->start + min(i0 + lane, p.num_groups)) > q;
-        const uint32_t first = __ballot_sync(0xffffffffu, after);
-        if (first)
-            g = i0 + __ffs(first) - 1;
-    }
-    if (--g >= 0) {
-        const int64_t nb = ((int64_t)__ldcg(tl.groups->len + g) + 127) / 128;
-        if (nb > 0) {
-            const int at = q - __ldcg(tl.groups->start + g), qt = 128 >> tl.gp_shift;
-            const int64_t share = __ldcg(&tl.groups->share);
-            const int64_t base = __ldcg(tl.groups->item + g) + ((int64_t)(at / qt) * p.hkv + c) * nb;
-            const int c0 = (int)div64(base, share), c1 = (int)div64(base + nb - 1, share);
-            const int row = ((at % qt) << tl.gp_shift) + hg;
-            if (c0 == c1)
-                add_whole(tl.rows);
-            else
-                add_pieces<D>(r, c1 - c0 + 1, lane, [&](int i, const float *&o, const float *&pm, const float *&pl) {
-                    const float *piece = tl.pieces + (int64_t)(i > 0 ? c0 + i : tl.ctas + c0) * (128 * (D + 2));
-                    o = piece + row * D;
-                    pm = piece + 128 * D + 2 * row;
-                    pl = pm + 1;
-                });
+        q = cut.x;
+        c = cut.y / nch;
+        hcol = cut.y % nch * w.heads;
+        nh = min(w.heads, p.group - hcol);
+        own0 = blockIdx.x;
+        own1 = cut.z;
+    } else {
+        const int nch = (p.group + w.heads - 1) / w.heads, x = blockIdx.x / nch;
+        hcol = (blockIdx.x - x * nch) * w.heads;
+        q = x / p.hkv;
+        c = x - q * p.hkv;
+        nh = min(w.heads, p.group - hcol);
+        const int qt = 128 >> tl.gp_shift;
+        if (MODE == kJoinSplits) {
+            pre0 = ((q / qt) * p.hkv + c) * tl.splits;
+            pre1 = pre0 + tl.splits - 1;
+            prow = ((q % qt) << tl.gp_shift) + hcol;
+        } else {
+            const int64_t lo = __ldcg(w.pre + q), nt = __ldcg(w.pre + q + 1) - lo, tiles = __ldcg(w.pre + w.nq);
+            // the group before the first that starts after the query
+            int g = -1;
+            for (int i0 = 0; i0 <= p.num_groups && g < 0; i0 += 32) {
+                const bool after = i0 + lane <= p.num_groups && __ldcg(tl.groups->start + min(i0 + lane, p.num_groups)) > q;
+                const uint32_t first = __ballot_sync(0xffffffffu, after);
+                if (first)
+                    g = i0 + __ffs(first) - 1;
+            }
+            if (nt > 0) {
+                const int64_t share = div64(tiles * w.head_chunks + w.ctas - 1, w.ctas);
+                const int64_t base = lo * w.head_chunks + (int64_t)(c * nch + hcol / w.heads) * nt;
+                own0 = (int)div64(base, share);
+                own1 = (int)div64(base + nt - 1, share);
+            }
+            if (--g >= 0) {
+                const int nb = (__ldcg(tl.groups->len + g) + kAttnStep - 1) / kAttnStep;
+                if (nb > 0) {
+                    const int at = q - __ldcg(tl.groups->start + g);
+                    const int64_t share = __ldcg(&tl.groups->share);
+                    const int64_t base = __ldcg(tl.groups->item + g) + (int64_t)((at / qt) * p.hkv + c) * nb;
+                    pre0 = (int)div64(base, share);
+                    pre1 = (int)div64(base + nb - 1, share);
+                    prow = ((at % qt) << tl.gp_shift) + hcol;
+                }
+            }
         }
     }
-    r.write(p, w.q0 * p.hq + x, lane);
-}
-
-// Sparse tiles whose blocks several CTAs share.
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-msa_attention_join_splits_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnTiles tl)
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int lane = threadIdx.x & 31;
-    const int x = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (x >= p.num_queries * p.hq)
-        return;
-    const int q = x / p.hq, h = x - q * p.hq, c = h / p.group, hg = h - c * p.group;
-    const int qt = 128 >> tl.gp_shift, row = ((q % qt) << tl.gp_shift) + hg;
-    const int64_t unit = (int64_t)(q / qt) * p.hkv + c;
-    Row<D> r;
-    add_pieces<D>(r, tl.splits, lane, [&](int i, const float *&o, const float *&pm, const float *&pl) {
-        const float *piece = tl.pieces + (unit * tl.splits + i) * (128 * (D + 2));
-        o = piece + row * D;
-        pm = piece + 128 * D + 2 * row;
-        pl = pm + 1;
-    });
-    r.write(p, x, lane);
+    const int n_own = own1 - own0 + 1, n = n_own + pre1 - pre0 + 1;
+    const int head0 = c * p.group + hcol;
+    auto piece = [&](int i) {
+        PieceAt a;
+        const bool own = i < n_own;
+        const int c0 = own ? own0 : pre0, c1 = own ? own1 : pre1;
+        if (!own)
+            i -= n_own;
+        if (MODE == kJoinRows && c0 == c1) {         // one CTA held it whole
+            a.o = (own ? w.rows : tl.rows) + ((int64_t)q * p.hq + head0) * (D + 4);
+            a.m = a.o + D;
+            a.stride = a.mstride = D + 4;
+            a.sums = 1;
+        } else if (own) {
+            a.o = w.pieces + (int64_t)(i > 0 ? c0 + i : w.ctas + c0) * (w.heads * (D + 2));
+            a.m = a.o + w.heads * D;
+            a.stride = D;
+            a.mstride = 1;
+            a.sums = w.heads;
+        } else {
+            const int slot = MODE == kJoinSplits ? c0 + i : i > 0 ? c0 + i : tl.ctas + c0;
+            const float *base = tl.pieces + (int64_t)slot * (128 * (D + 2));
+            a.o = base + prow * D;
+            a.m = base + 128 * D + 2 * prow;
+            a.stride = D;
+            a.mstride = 2;
+            a.sums = 1;
+        }
+        return a;
+    };
+    const int h = tid / (D / 4), d = tid % (D / 4) * 4;        // this thread's head and dims
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (tid < kJoinHeads) {
+        s_m[tid] = -INFINITY;
+        s_l[tid] = 0.0f;
+    }
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int count = min(32, n - i0);
+        __syncthreads();
+        // weights: a warp per head, a lane per piece
+        for (int k = warp; k < nh; k += blockDim.x >> 5) {
+            float pm = -INFINITY, pl = 0.0f;
+            if (lane < count) {
+                const PieceAt a = piece(i0 + lane);
+                pm = __ldcg(a.m + k * a.mstride);
+                pl = __ldcg(a.m + k * a.mstride + a.sums);
+            }
+            const bool seen = pl != 0.0f;                       // a NaN goes on
+            float mx = seen ? pm : -INFINITY;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float before = s_m[k];
+            mx = fmaxf(mx, before);
+            const float wt = seen ? exp2_approx(pm - mx) : 0.0f;
+            float sum = pl * wt;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            s_w[lane][k] = wt;
+            __syncwarp();
+            if (lane == 0) {
+                const float a = before == -INFINITY ? 0.0f : exp2_approx(before - mx);
+                s_scale[k] = a;
+                s_m[k] = mx;
+                s_l[k] = s_l[k] * a + sum;
+            }
+        }
+        __syncthreads();
+        if (h < nh) {
+            const float a = s_scale[h];
+            acc.x *= a;
+            acc.y *= a;
+            acc.z *= a;
+            acc.w *= a;
+#pragma unroll 4
+            for (int i = 0; i < count; ++i) {
+                const PieceAt at = piece(i0 + i);
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(at.o + h * at.stride + d));
+                const float wt = s_w[i][h];
+                if (wt != 0.0f) {                               // nothing seen: the row may hold anything
+                    acc.x = fmaf(x.x, wt, acc.x);
+                    acc.y = fmaf(x.y, wt, acc.y);
+                    acc.z = fmaf(x.z, wt, acc.z);
+                    acc.w = fmaf(x.w, wt, acc.w);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (h < nh) {
+        const int64_t row = (w.q0 + q) * p.hq + head0 + h;
+        const float l = s_l[h], inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+        uint2 o;
+        o.x = bf16x2_from_f32(acc.x * inv, acc.y * inv);
+        o.y = bf16x2_from_f32(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(p.out + row * D + d) = o;
+        if (d == 0 && p.lse)
+            p.lse[row] = attn_lse(s_m[h], l);
+    }
 }
 
 template <int D, bool FP8, int NH>
@@ -1105,27 +1102,33 @@ cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, 
                     : launch_decode<64, false, 16>(p, w, kmap, vmap, stream));
 }
 
+namespace {
+
+template <JoinMode MODE>
+cudaError_t launch_join(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim, int64_t grid,
+                        cudaStream_t stream)
+{
+    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w), const_cast<AttnTiles *>(&tiles)};
+    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_kernel<128, MODE>)
+                                       : reinterpret_cast<const void *>(&msa_attention_join_kernel<64, MODE>),
+                       grid, w.heads * head_dim / 4, 0, stream, args);
+}
+
+}  // namespace
+
 cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream)
 {
-    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w)};
-    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<128>)
-                                       : reinterpret_cast<const void *>(&msa_attention_join_cut_kernel<64>),
-                       w.ctas, w.heads * 32, 0, stream, args);
+    return launch_join<kJoinCut>(p, w, AttnTiles(), head_dim, w.ctas, stream);
 }
 
 cudaError_t attn_join_rows(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim,
                            cudaStream_t stream)
 {
-    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnPieces *>(&w), const_cast<AttnTiles *>(&tiles)};
-    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_rows_kernel<128>)
-                                       : reinterpret_cast<const void *>(&msa_attention_join_rows_kernel<64>),
-                       (w.nq * p.hq + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, args);
+    return launch_join<kJoinRows>(p, w, tiles, head_dim, w.nq * w.head_chunks, stream);
 }
 
-cudaError_t attn_join_splits(const AttnParams &p, const AttnTiles &tiles, int head_dim, cudaStream_t stream)
+cudaError_t attn_join_splits(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim,
+                             cudaStream_t stream)
 {
-    void *args[] = {const_cast<AttnParams *>(&p), const_cast<AttnTiles *>(&tiles)};
-    return attn_launch(head_dim == 128 ? reinterpret_cast<const void *>(&msa_attention_join_splits_kernel<128>)
-                                       : reinterpret_cast<const void *>(&msa_attention_join_splits_kernel<64>),
-                       (p.num_queries * p.hq + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, args);
+    return launch_join<kJoinSplits>(p, w, tiles, head_dim, p.num_queries * w.head_chunks, stream);
 }

@@ -11,6 +11,7 @@
 constexpr int kAttnMaxGroups = 512;
 constexpr int kAttnWindow = 384;     // queries a launch of the tensor-core decode kernel takes
 constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
+constexpr int kAttnStep = 64;        // tokens of a step of the tile kernel
 constexpr int kAttnTileList = 1024;  // (query, id) pairs of a sparse tile
 
 // One cache as the kernels see it; strides in elements.
@@ -79,7 +80,7 @@ struct AttnGroups {
 };
 
 // What the tile kernel needs beside AttnParams.  Sparse: CTA = (tile, K/V head, split), a
-// split tile's piece in slot CTA.  Prefix: items over (group, tile, K/V head, 128 tokens),
+// split tile's piece in slot CTA.  Prefix: items over (group, tile, K/V head, step),
 // slots as in AttnPieces.  A slot is [128 rows][D], then [128][maximum, sum].
 struct AttnTiles {
     AttnGroups *groups;              // prefix
@@ -105,7 +106,8 @@ cudaError_t attn_tiles(const AttnParams &p, const AttnTiles &w, int head_dim, co
 // prefixes; split sparse tiles.
 cudaError_t attn_join_rows(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim,
                            cudaStream_t stream);
-cudaError_t attn_join_splits(const AttnParams &p, const AttnTiles &tiles, int head_dim, cudaStream_t stream);
+cudaError_t attn_join_splits(const AttnParams &p, const AttnPieces &w, const AttnTiles &tiles, int head_dim,
+                             cudaStream_t stream);
 cudaError_t attn_join_cut(const AttnParams &p, const AttnPieces &w, int head_dim, cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -4,32 +4,33 @@
 // What is computed is stated in include/msa_attention.h.
 //
 // A tile is 128 rows: QT queries times the heads of one K/V head, padded to a power of two.
-// Per 128 tokens the CTA computes S [128 rows, 128 tokens] = Q . K^T and
-// O [128 rows, D] += P . V, each product read from shared memory as TMA copied it (K-major
-// keys, N-major values) with P as the A operand in tensor memory, where it takes the place
-// of the scores.  E4M3 caches run on kind::f8f6f4 with Q and P split into E4M3 halves
-// hi | lo (twice the MMAs at twice the rate: no conversion of keys or values, and half the
-// bytes in shared memory); bf16 on kind::f16.
-//   warp 0     TMA: page lookups one tile ahead, key and value copies
+// A step is 64 tokens: the CTA computes S [128 rows, 64 tokens] = Q . K^T and
+// O [128 rows, D] += P . V, keys and values read from shared memory as TMA copied them
+// (K-major keys, N-major values), P as the A operand in tensor memory.  E4M3 caches run on
+// kind::f8f6f4 with Q and P split into E4M3 halves hi | lo (twice the MMAs at twice the
+// rate: no conversion of keys or values, and half the bytes in shared memory); bf16 on
+// kind::f16.
+//   warp 0     TMA: page lookups in batches, one ahead, key and value copies
 //   warp 1     MMAs; zeroes value rows past the history before they are multiplied
-//   warps 2-9  softmax and output: two groups of four, a thread per row; group g takes the
-//              tokens 64 g .. 64 g + 63 of every tile, then D / 2 of the dims
-// Scores are made 64 tokens at a time into two buffers, one a group, so that the scores of
-// one half are ready while the other's softmax runs, and two CTAs share an SM (half the
-// tensor memory and half the shared memory each).  A tile of E4M3 keys takes about 1,280
-// cycles of the tensor pipe (the 64-token score MMAs read the queries from shared memory
-// twice), 1,024 of exponentials and 1,000 issue slots of a scheduler.
+//   warps 2-9  softmax and output: two groups of four warps, a thread per row; the groups
+//              take alternate steps, then half of the dims each
+// Tensor memory (256 columns): S | P of group 0 | P of group 1 | O.  S is read into
+// registers at once, so the next step's scores are made while this step's softmax runs, and
+// the scores run two steps ahead of the values; two CTAs share an SM and fill what gaps
+// are left.  Eight MMAs of N = 128 take 530 cycles of the tensor pipe, eight of N = 64 with
+// A in shared memory 390 (reading A binds), so 128 tokens take about 1,310 cycles.
+//
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
-// output in tensor memory rescaled, which few tiles after the first need.  The groups hand
-// the reference of a row to one another half by half.
+// output in tensor memory rescaled, which few steps after the first need.  The groups hand
+// the reference of a row to one another step by step.
 //
 // Sparse (DENSE = false): the tile's queries run over the union of their blocks, each row
 // masked to its own.  A weight of zero does not hide an infinity or a NaN in the values of
 // a token that another row of the tile sees, so a row whose output is not finite is
 // computed again from its own tokens alone.
-// Prefix (DENSE = true): (tile, K/V head, 128 tokens) items laid end to end over the groups,
-// an equal share for each CTA; every piece goes to the workspace and is joined with the
+// Prefix (DENSE = true): (tile, K/V head, step) items laid end to end over the groups, an
+// equal share for each CTA; every piece goes to the workspace and is joined with the
 // queries' own tokens.
 
 #include "msa_attention_internal.h"
@@ -40,8 +41,9 @@
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kInfo = 4;            // tiles whose validity words are held
-constexpr int kMaxBoxes = 16;
+constexpr int kTok = kAttnStep;     // tokens of a step
+constexpr int kInfo = 8;            // steps whose validity words are held
+constexpr int kMaxBoxes = 8;
 constexpr int kMaxList = kAttnTileList;      // blocks of a tile's list
 constexpr int kTileQueries = 32;    // queries of a tile at most (a mask word)
 
@@ -50,12 +52,12 @@ struct TileShape {
     static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
     static constexpr int kSwz = kRowBytes < 128 ? kRowBytes : 128;
     static constexpr int kAtoms = kRowBytes / kSwz;
-    static constexpr int kTileBytes = 128 * kRowBytes;
+    static constexpr int kStepBytes = kTok * kRowBytes;
     static constexpr int kQBytes = 128 * D * 2;                   // bf16, or E4M3 hi | lo
-    static constexpr int kStages = kTileBytes == 32768 ? 1 : 2;   // of keys, and of values
-    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
-    static constexpr int kTmem = 256;                             // scores (and weights) | output
-    static_assert(2 * kStages * kTileBytes >= 4 * kMaxList * 8, "scratch of the list");
+    static constexpr int kStages = kStepBytes == 16384 ? 2 : 4;   // of keys, and of values
+    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kStepBytes;
+    static constexpr int kTmem = 256;
+    static_assert(2 * kStages * kStepBytes >= 4 * kMaxList * 8, "scratch of the list");
 };
 
 constexpr float kLazyBf16 = 8.0f, kLazyFp8 = 4.0f;
@@ -127,19 +129,25 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// Two weights -> their E4M3 halves (hi pair, lo pair), through f16: 11 bits hold what the
+// Four weights -> their E4M3 halves, four codes each, through f16: 11 bits hold what the
 // halves keep (8), and its pairs convert and subtract two at a time.
-__device__ __forceinline__ void split_weights(float x0, float x1, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ void split_weights(float x0, float x1, float x2, float x3, uint32_t &hi, uint32_t &lo)
 {
-    asm("{\n\t.reg .b32 p, b, d;\n\t.reg .b16 h, l;\n\t"
+    asm("{\n\t.reg .b32 p, q, b, c, d, e;\n\t.reg .b16 h0, h1, l0, l1;\n\t"
         "cvt.rn.f16x2.f32 p, %3, %2;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 h, p;\n\t"
-        "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
+        "cvt.rn.f16x2.f32 q, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h0, p;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h1, q;\n\t"
+        "mov.b32 %0, {h0, h1};\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, h0;\n\t"
+        "cvt.rn.f16x2.e4m3x2 c, h1;\n\t"
         "sub.rn.f16x2 d, p, b;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
-        "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+        "sub.rn.f16x2 e, q, c;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l0, d;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l1, e;\n\t"
+        "mov.b32 %1, {l0, l1};\n\t}"
         : "=r"(hi), "=r"(lo)
-        : "f"(x0), "f"(x1));
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
 
 // What a CTA works on: rows of the tile, a K/V head and a range of 128-token tiles.
@@ -147,17 +155,17 @@ struct Segment {
     int t0;                  // first query (prefix: of the window)
     int nq;                  // queries in the tile
     int c;                   // K/V head
-    int p0, p1;              // 128-token tiles
+    int p0, p1;              // steps
     int group, len;          // prefix: the group, its tokens
     bool whole, began;       // prefix: all of its unit; it starts the unit
 };
 
 struct DenseWalk {
-    const AttnGroups *tab;    // group g has tiles x K/V heads units of nb 128-token tiles
+    const AttnGroups *tab;    // group g has tiles x K/V heads units of nb steps
     int64_t it, end, base;   // base: items before the unit
     int ngroups, hkv, qt, g, unit;
 
-    __device__ int nb() const { return (int)(((uint32_t)tab->len[g] + 127u) / 128u); }
+    __device__ int nb() const { return (int)(((uint32_t)tab->len[g] + kTok - 1) / kTok); }
     __device__ void find()
     {
         while (g < ngroups && tab->item[g + 1] <= it) {
@@ -203,7 +211,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
     __shared__ __align__(8) uint64_t bar_info[kInfo];
-    __shared__ __align__(8) uint64_t bar_q, bar_s[2], bar_p[2], bar_pv, bar_o, bar_drain;
+    __shared__ __align__(8) uint64_t bar_q, bar_s[2], bar_read, bar_p[2], bar_pv[2], bar_o, bar_drain;
     __shared__ __align__(8) uint64_t bar_ref[2][4];
     __shared__ uint8_t s_nv[kInfo][kMaxBoxes];     // visible rows of each box
     __shared__ uint32_t s_gap[kInfo];              // boxes without a page before the history's end
@@ -223,7 +231,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t qsm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t kring = qsm + S::kQBytes, vring = kring + ST * S::kTileBytes;
+    const uint32_t kring = qsm + S::kQBytes, vring = kring + ST * S::kStepBytes;
     volatile int *abort_flag = &s_abort;
     const int qt = 128 >> w.gp_shift;
 
@@ -242,10 +250,11 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar_s[i]), 1);
             mbar_init(smem_u32(&bar_p[i]), 4);
+            mbar_init(smem_u32(&bar_pv[i]), 1);
             for (int j = 0; j < 4; ++j)
                 mbar_init(smem_u32(&bar_ref[i][j]), 1);
         }
-        mbar_init(smem_u32(&bar_pv), 1);
+        mbar_init(smem_u32(&bar_read), 4);
         mbar_init(smem_u32(&bar_o), 1);
         mbar_init(smem_u32(&bar_drain), 1);
         s_abort = 0;
@@ -289,7 +298,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 int64_t x = 0;
                 if (g < n) {
                     const int q = u.groups.start[g + 1] - u.groups.start[g];
-                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (((int64_t)u.groups.len[g] + 127) / 128);
+                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (((int64_t)u.groups.len[g] + kTok - 1) / kTok);
                 }
                 int64_t inc = x;
 #pragma unroll
@@ -375,7 +384,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int per_block = DENSE ? 1 : p.block_tokens / 128;     // 128-token tiles of a block
+    const int per_block = DENSE ? 1 : p.block_tokens / kTok;    // steps of a block
     if (DENSE) {
         const int64_t total = u.groups.item[p.num_groups], share = (total + gridDim.x - 1) / gridDim.x;
         dw.tab = &u.groups;
@@ -402,10 +411,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         seg.p0 = n * sp / w.splits;
         seg.p1 = n * (sp + 1) / w.splits;
     }
-    // first token of tile v of the list, and its entry
-    auto list_tile = [&](int v, int &e) -> int64_t {
-        e = per_block == 1 ? v : v / per_block;
-        return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * 128;
+    // first token of step v of the list, and its entry
+    auto list_step = [&](int v, int &e) -> int64_t {
+        e = per_block == 2 ? v >> 1 : v / per_block;
+        return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * kTok;
     };
     bool once = true;
     // the next segment of this CTA
@@ -422,32 +431,34 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
 
     if (warp == 0) {
         // ---------------- copies ----------------
-        const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = 128 >> lb;
-        uint32_t it = 0;
+        const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = kTok >> lb;
+        uint32_t n = 0;                // steps of the CTA
         bool ok = true;
         for (bool first = true; ok && next_segment(first); first = false) {
-            // the box of this lane in tile v: row in the page, page (one past the last for a
-            // box that shows nothing: zeros), rows that some query sees, and whether the
-            // history goes on without a page
             const int64_t prefix_off = DENSE ? __ldg(p.prefix_offset + seg.group) : 0;
-            auto look = [&](int v, int2 &box, int &nv, bool &gap) {
+            // A batch of 32 / nbox steps is looked up at once, a box a lane, one batch ahead:
+            // row in the page, page (one past the last for a box that shows nothing: zeros),
+            // rows that some query sees, and whether the history goes on without a page.
+            const int batch = 32 >> (6 - lb), my_step = lane >> (6 - lb), my_box = lane & (nbox - 1);
+            auto look = [&](int v0, int2 &box, int &nv, bool &gap) {
                 box = make_int2(0, w.oob_page);
                 nv = 0;
                 gap = false;
-                if (lane >= nbox || v >= seg.p1)
+                const int v = v0 + my_step;
+                if (v >= seg.p1)
                     return;
                 int64_t tok, off, len;
                 if (DENSE) {
-                    tok = (int64_t)v * 128;
+                    tok = (int64_t)v * kTok;
                     off = prefix_off;
                     len = seg.len;
                 } else {
                     int e;
-                    tok = list_tile(v, e);
+                    tok = list_step(v, e);
                     off = u.sp.toff[u.sp.block[e] >> 24];
                     len = u.sp.maxlen[u.sp.block[e] >> 24];
                 }
-                tok += lane * BR;
+                tok += my_box * BR;
                 if (tok >= len)
                     return;
                 const int32_t pg = attn_page(p, off, tok);
@@ -457,19 +468,30 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     nv = (int)min((int64_t)BR, len - tok);
                 }
             };
-            int2 box, nbx;
-            int nv, nnv;
-            bool gap, ngap;
-            look(seg.p0, box, nv, gap);
-            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
-                const uint32_t s = it % ST, par = ((it / ST) & 1u) ^ 1u, slot = it % kInfo;
+            int2 boxes, next_boxes;
+            int nvs, next_nvs;
+            bool gaps_of, next_gaps;
+            look(seg.p0, next_boxes, next_nvs, next_gaps);
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++n) {
+                const int at_batch = (v - seg.p0) & (batch - 1);
+                if (at_batch == 0) {
+                    boxes = next_boxes;
+                    nvs = next_nvs;
+                    gaps_of = next_gaps;
+                    look(v + batch, next_boxes, next_nvs, next_gaps);
+                }
+                const int from = at_batch * nbox + (lane & (nbox - 1));
+                const int2 box = make_int2(__shfl_sync(0xffffffffu, boxes.x, from), __shfl_sync(0xffffffffu, boxes.y, from));
+                const int nv = __shfl_sync(0xffffffffu, nvs, from);
+                const uint32_t gaps = (__ballot_sync(0xffffffffu, gaps_of) >> (at_batch * nbox)) & ((1u << nbox) - 1u);
+                const uint32_t s = n % ST, par = ((n / ST) & 1u) ^ 1u, slot = n % kInfo;
                 ok = warp_wait(smem_u32(&bar_k_empty[s]), par, abort_flag);
                 if (!ok)
                     break;
-                // the slot's last readers were done before this stage's keys were multiplied
+                // the slot's readers, eight steps before, are done: the scores that freed this
+                // stage were made after the group had read later ones
                 if (lane < nbox)
                     s_nv[slot][lane] = (uint8_t)nv;
-                const uint32_t gaps = __ballot_sync(0xffffffffu, gap);
                 if (lane == 0)
                     s_gap[slot] = gaps;
                 __syncwarp();
@@ -478,134 +500,116 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full) {
 #ifndef MSA_STARVE
                     if (lane == 0)
-                        mbar_expect_tx(full, (uint32_t)S::kTileBytes);
+                        mbar_expect_tx(full, (uint32_t)S::kStepBytes);
                     __syncwarp();
                     if (lane < nbox)
 #pragma unroll
                         for (int at = 0; at < S::kAtoms; ++at)
-                            tma_load_box(dst + (uint32_t)(at * 128 + lane * BR) * S::kSwz, map,
+                            tma_load_box(dst + (uint32_t)(at * kTok + lane * BR) * S::kSwz, map,
                                          at * (S::kSwz / (FP8 ? 1 : 2)), box.x, seg.c, box.y, full);
 #endif
                 };
-                copy(&kmap, kring + s * (uint32_t)S::kTileBytes, smem_u32(&bar_k_full[s]));
-                look(v + 1, nbx, nnv, ngap);
+                copy(&kmap, kring + s * (uint32_t)S::kStepBytes, smem_u32(&bar_k_full[s]));
                 ok = warp_wait(smem_u32(&bar_v_empty[s]), par, abort_flag);
                 if (!ok)
                     break;
-                copy(&vmap, vring + s * (uint32_t)S::kTileBytes, smem_u32(&bar_v_full[s]));
-                box = nbx;
-                nv = nnv;
-                gap = ngap;
+                copy(&vmap, vring + s * (uint32_t)S::kStepBytes, smem_u32(&bar_v_full[s]));
             }
         }
         if (!ok)
             *abort_flag = 1;
 #ifndef MSA_STARVE
-        // every copy has landed before the CTA finishes (of the last tile of an aborted
+        // every copy has landed before the CTA finishes (of the last step of an aborted
         // CTA the values may not have been asked for; that wait runs out)
-        for (uint32_t s = 0; s < (uint32_t)ST && s < it; ++s) {
-            const uint32_t par = ((it - 1u - s) / ST) & 1u;
+        for (uint32_t s = 0; s < (uint32_t)ST && s < n; ++s) {
+            const uint32_t par = ((n - 1u - s) / ST) & 1u;
             (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), par));
             (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_v_full[s]), par));
         }
         if (!ok)
-            for (uint32_t s = 0; s < (uint32_t)ST; ++s)
-                (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), (it / ST) & 1u));
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[n % ST]), (n / ST) & 1u));
 #endif
     } else if (warp == 1) {
         // ---------------- MMAs ----------------
-        constexpr uint32_t kIdS = mma_idesc(FP8, 128, 64, false, false);
+        constexpr uint32_t kIdS = mma_idesc(FP8, 128, kTok, false, false);
         constexpr uint32_t kIdO = mma_idesc(FP8, 128, D, false, true);
-        constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step of the values
-        constexpr int kStep = kTok * S::kSwz / 16;
-        const int BR = w.box_rows, nbox = 128 / BR;
+        constexpr int kStep = (FP8 ? 32 : 16) * S::kSwz / 16;      // descriptor units of one MMA's tokens
+        const int BR = w.box_rows, nbox = kTok / BR;
         const uint64_t q_desc = smem_desc(qsm, S::kSwz, 16u, 8u * S::kSwz);
         const uint64_t k_desc = smem_desc(kring, S::kSwz, 16u, 8u * S::kSwz);
-        const uint64_t v_desc = smem_desc(vring, S::kSwz, 128u * S::kSwz, 8u * S::kSwz);
-        uint32_t it = 0, nseg = 0;        // it: tiles whose values were multiplied
+        const uint64_t v_desc = smem_desc(vring, S::kSwz, (uint32_t)kTok * S::kSwz, 8u * S::kSwz);
+        uint32_t n = 0, nseg = 0;         // steps of the CTA whose values were multiplied
         bool ok = true;
-        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
-            // the scores of half g of the CTA's tile i; `after`: right after the values of that
-            // half of tile i - 1 (the first tile of a segment comes after everything, since
-            // its queries are made when the output before was read)
-            auto scores = [&](uint32_t i, int g, bool after) {
-                const uint32_t s = i % ST;
-                if (g == 0)
-                    ok = warp_wait(smem_u32(&bar_k_full[s]), (i / ST) & 1u, abort_flag);
-                // the weights of the half before, whose place the scores take, are multiplied
-                ok = ok && (!after || warp_wait(smem_u32(&bar_pv), (uint32_t)g, abort_flag));
-                if (!ok)
-                    return;
-                tc_fence_after();
-                const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
-                const uint32_t d = tmem + (uint32_t)(g * 64);
-                if (S::kSwz == 128) {
-                    // a swizzle atom is four steps; the halves, or the atoms of a row, follow
-                    mma_ss4<FP8, 2, 2>(d, q_desc, kd, kIdS, 0);
-                    if (D == 128)
-                        mma_ss4<FP8, 2, 2>(d, q_desc + 128 * 128 / 16, FP8 ? kd : kd + 128 * 128 / 16, kIdS, 1);
-                } else {
+        // the scores of step i; `wait_read`: once those of the step before have been read
+        auto scores = [&](uint32_t i, bool wait_read) {
+            const uint32_t s = i % ST;
+            ok = ok && (!wait_read || warp_wait(smem_u32(&bar_read), (i - 1u) & 1u, abort_flag));
+            ok = ok && warp_wait(smem_u32(&bar_k_full[s]), (i / ST) & 1u, abort_flag);
+            if (!ok)
+                return;
+            tc_fence_after();
+            const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
+            if (S::kSwz == 128) {
+                // a swizzle atom is four MMAs; the halves, or the atoms of a row, follow
+                mma_ss4<FP8, 2, 2>(tmem, q_desc, kd, kIdS, 0);
+                if (D == 128)
+                    mma_ss4<FP8, 2, 2>(tmem, q_desc + 128 * 128 / 16, FP8 ? kd : kd + kTok * 128 / 16, kIdS, 1);
+            } else {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)    // two steps of hi, two of lo
-                        mma_ss<FP8>(d, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
-                                    kd + (uint64_t)((ks & 1) * 2), kIdS, ks > 0);
-                }
-                mma_commit(smem_u32(&bar_s[g]));
-                if (g == 1)
-                    mma_commit(smem_u32(&bar_k_empty[s]));
-            };
-            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
-            if (ok && seg.p0 < seg.p1) {
-                scores(it, 0, false);
-                if (ok)
-                    scores(it, 1, false);
+                for (int ks = 0; ks < 4; ++ks)    // two of hi, two of lo
+                    mma_ss<FP8>(tmem, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
+                                kd + (uint64_t)((ks & 1) * 2), kIdS, ks > 0);
             }
-            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
-                const uint32_t s = it % ST;
-                for (int g = 0; g < 2 && ok; ++g) {
-                    const uint32_t vt = vring + s * (uint32_t)S::kTileBytes;
-                    if (g == 0) {
-                        ok = warp_wait(smem_u32(&bar_v_full[s]), (it / ST) & 1u, abort_flag);
-                        if (!ok)
-                            break;
-                        // rows past the history may hold anything: a weight of zero would not
-                        // hide an infinity or a NaN
-                        const int nv = lane < nbox ? s_nv[it % kInfo][lane] : 0;
-                        uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
-                        if (partial) {
-                            while (partial) {
-                                const int b = __ffs(partial) - 1;
-                                partial &= partial - 1;
-                                const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
-                                for (int at = 0; at < S::kAtoms; ++at)
-                                    for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
-                                        sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
-                            }
-                            fence_async_smem();
-                            __syncwarp();
-                        }
+            mma_commit(smem_u32(&bar_s[i & 1]));
+            mma_commit(smem_u32(&bar_k_empty[s]));
+        };
+        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
+            const int steps = seg.p1 - seg.p0;
+            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
+            if (steps > 0)
+                scores(n, n > 0);
+            if (steps > 1)
+                scores(n + 1, true);
+            for (int v = 0; v < steps && ok; ++v, ++n) {
+                if (v + 2 < steps)
+                    scores(n + 2, true);
+                const uint32_t s = n % ST, g = n & 1u;
+                ok = ok && warp_wait(smem_u32(&bar_v_full[s]), (n / ST) & 1u, abort_flag);
+                if (!ok)
+                    break;
+                // rows past the history may hold anything: a weight of zero would not hide an
+                // infinity or a NaN
+                const int nv = lane < nbox ? s_nv[n % kInfo][lane] : 0;
+                uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
+                if (partial) {
+                    const uint32_t vt = vring + s * (uint32_t)S::kStepBytes;
+                    while (partial) {
+                        const int b = __ffs(partial) - 1;
+                        partial &= partial - 1;
+                        const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
+                        for (int at = 0; at < S::kAtoms; ++at)
+                            for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
+                                sts128(vt + (uint32_t)(at * kTok) * S::kSwz + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
                     }
-                    ok = warp_wait(smem_u32(&bar_p[g]), it & 1u, abort_flag);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
-                    const uint32_t pt = tmem + (uint32_t)(g * 64), acc = v > seg.p0 || g > 0;
-                    if (FP8) {      // two steps of hi, two of lo against the same values
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ts<FP8>(tmem + 128u, pt + (uint32_t)(ks * 8), vd + (uint64_t)((ks & 1) * kStep), kIdO,
-                                        acc | (uint32_t)ks);
-                    } else {
-                        mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kIdO, acc);
-                    }
-                    mma_commit(smem_u32(&bar_pv));
-                    if (g == 1)
-                        mma_commit(smem_u32(&bar_v_empty[s]));
-                    // the half's next scores, when these values are multiplied
-                    if (v + 1 < seg.p1)
-                        scores(it + 1, g, true);
+                    fence_async_smem();
+                    __syncwarp();
                 }
+                ok = warp_wait(smem_u32(&bar_p[g]), (n >> 1) & 1u, abort_flag);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
+                const uint32_t pt = tmem + 64u + g * 32u, acc = v > 0;
+                if (FP8) {      // two of hi, two of lo against the same values
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts<FP8>(tmem + 128u, pt + (uint32_t)(ks * 8), vd + (uint64_t)((ks & 1) * kStep), kIdO,
+                                    acc | (uint32_t)ks);
+                } else {
+                    mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kIdO, acc);
+                }
+                mma_commit(smem_u32(&bar_pv[g]));
+                mma_commit(smem_u32(&bar_v_empty[s]));
             }
             __syncwarp();
             if (ok)
@@ -619,7 +623,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         // ---------------- softmax and output ----------------
         const int quarter = warp & 3, row = quarter * 32 + lane, half = (warp - 2) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t st = lanes + (uint32_t)(half * 64), ot = lanes + 128u;
+        const uint32_t st = lanes, pt = lanes + 64u + (uint32_t)(half * 32), ot = lanes + 128u;
         const int gp = 1 << w.gp_shift, qi = row >> w.gp_shift, hi = row & (gp - 1);
         const int BR = w.box_rows, lb = __ffs(BR) - 1;
         constexpr float kLazy = FP8 ? kLazyFp8 : kLazyBf16, kOff = FP8 ? kPOffset : 0.0f;
@@ -627,7 +631,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         const float nan = __int_as_float(0x7fc00000);
         // the two warps that hold a row's halves
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
-        uint32_t it = 0, nseg = 0;
+        uint32_t n = 0, nseg = 0;                       // steps of the CTA before the segment
         bool ok = true;
         for (bool first = true; next_segment(first); first = false, ++nseg) {
             // ---- the row's query into shared memory ----
@@ -688,21 +692,24 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 mbar_arrive(smem_u32(&bar_q));
             const int len = DENSE ? seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
             float m = -INFINITY, l = 0.0f;                 // the reference that l is relative to
-            for (int v = seg.p0; v < seg.p1; ++v, ++it) {
-                ok = ok && warp_wait(smem_u32(&bar_info[it % kInfo]), (it / kInfo) & 1u, abort_flag);
-                // tokens of this thread's half that the row sees, from its first
+            const uint32_t n0 = n;
+            n += (uint32_t)(seg.p1 - seg.p0);
+            for (uint32_t i = n0 + ((n0 ^ (uint32_t)half) & 1u); i < n; i += 2) {
+                const int v = seg.p0 + (int)(i - n0);
+                ok = ok && warp_wait(smem_u32(&bar_info[i % kInfo]), (i / kInfo) & 1u, abort_flag);
+                // tokens of the step that the row sees, from its first
                 int vis;
                 if (DENSE) {
-                    vis = len - v * 128;
+                    vis = len - v * kTok;
                 } else {
                     int e;
-                    const int64_t tok = list_tile(v, e);
-                    vis = (int)max((int64_t)-1, min((int64_t)128, len - tok));
-                    vis = (u.sp.mask[e] >> qi) & 1u ? vis : -1;
+                    const int64_t tok = list_step(v, e);
+                    vis = (int)max((int64_t)0, min((int64_t)kTok, len - tok));
+                    vis = (u.sp.mask[e] >> qi) & 1u ? vis : 0;
                 }
-                vis = real ? vis - half * 64 : -1;
-                const uint32_t gaps = ok ? s_gap[it % kInfo] : 0u;
-                ok = ok && warp_wait(smem_u32(&bar_s[half]), it & 1u, abort_flag);
+                vis = real ? vis : 0;
+                const uint32_t gaps = ok ? s_gap[i % kInfo] : 0u;
+                ok = ok && warp_wait(smem_u32(&bar_s[half]), (i >> 1) & 1u, abort_flag);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -710,16 +717,20 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 tmem_ld32(st, x);
                 tmem_ld32(st + 32u, x + 32);
                 tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bar_read));
                 auto score = [&](int j) { return __uint_as_float(x[j]); };
                 float mx = -INFINITY;
                 const bool any = __any_sync(0xffffffffu, vis > 0);
                 if (any) {
                     // rows that see all or nothing need no masks here: a row that sees
-                    // nothing has its weights cleared below
-                    if (__any_sync(0xffffffffu, (vis > 0 && vis < 64) || gaps != 0)) {
+                    // nothing takes an offset that clears its weights
+                    if (__any_sync(0xffffffffu, (vis > 0 && vis < kTok) || gaps != 0)) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
-                            if (j >= vis || ((gaps >> ((half * 64 + j) >> lb)) & 1u))
+                            if (j >= vis || ((gaps >> (j >> lb)) & 1u))
                                 x[j] = 0xff800000u;
                     }
                     float a = max3(score(0), score(1), score(2)), b = max3(score(3), score(4), score(5));
@@ -731,22 +742,28 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     mx = fmaxf(max3(a, score(62), score(63)), b);
                     mx = vis > 0 ? mx * qs : -INFINITY;
                 }
-                // the reference, from the half before
+                // this group's weights before are multiplied: their place is free
+                if (i >= 2) {
+                    ok = warp_wait(smem_u32(&bar_pv[half]), ((i >> 1) - 1u) & 1u, abort_flag);
+                    if (!ok)
+                        break;
+                }
+                // the reference, from the step before
                 float ref = -INFINITY;
-                if (half > 0 || v > seg.p0) {
-                    ok = warp_wait(smem_u32(&bar_ref[half ^ 1][quarter]), (half > 0 ? it : it - 1u) & 1u, abort_flag);
+                if (i > n0) {
+                    ok = warp_wait(smem_u32(&bar_ref[half ^ 1][quarter]), ((i - 1u) >> 1) & 1u, abort_flag);
                     if (!ok)
                         break;
                     ref = s_ref[row];
                 }
-                // (-inf + kLazy is -inf: the first visible half sets the reference)
+                // (-inf + kLazy is -inf: the first visible step sets the reference)
                 const bool grow = mx > ref + kLazy;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float alpha = grow ? exp2_approx(ref - mx) : 1.0f;
                     ref = grow ? mx : ref;
-                    if (half > 0 || v > seg.p0) {
-                        // the values of the half before are in the output
-                        ok = warp_wait(smem_u32(&bar_pv), (uint32_t)(half ^ 1), abort_flag);
+                    if (i > n0) {
+                        // the values of the step before are in the output
+                        ok = warp_wait(smem_u32(&bar_pv[half ^ 1]), ((i - 1u) >> 1) & 1u, abort_flag);
                         if (!ok)
                             break;
                         tc_fence_after();
@@ -769,9 +786,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 l = m == ref ? l : l * exp2_approx(m - ref);
                 m = ref;
                 if (any) {
-                    const float off = m == -INFINITY ? 0.0f : kOff - m;
+                    // (scores that are not finite of tokens the row does not see can still
+                    // make weights that are not: its output is then computed again)
+                    const float off = vis > 0 && m > -INFINITY ? kOff - m : -INFINITY;
                     const uint64_t qs2 = pack2(qs, qs), off2 = pack2(off, off);
-                    const uint32_t keep = vis > 0 ? 0xffffffffu : 0u;
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int j = 0; j < 64; j += 16) {
@@ -788,33 +806,29 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                             sum0 = add2(sum0, pack2(p0, p1));
                             sum1 = add2(sum1, pack2(p2, p3));
                             if (FP8) {
-                                uint32_t h0, l0, h1, l1;
-                                split_weights(p0, p1, h0, l0);
-                                split_weights(p2, p3, h1, l1);
-                                hw[e / 4] = (h0 | (h1 << 16)) & keep;
-                                lw[e / 4] = (l0 | (l1 << 16)) & keep;
+                                split_weights(p0, p1, p2, p3, hw[e / 4], lw[e / 4]);
                             } else {
-                                hw[e / 2] = bf16x2_from_f32(p0, p1) & keep;
-                                hw[e / 2 + 1] = bf16x2_from_f32(p2, p3) & keep;
+                                hw[e / 2] = bf16x2_from_f32(p0, p1);
+                                hw[e / 2 + 1] = bf16x2_from_f32(p2, p3);
                             }
                         }
                         if (FP8) {      // 16 columns of hi, 16 of lo
-                            tmem_st4(st + (uint32_t)(j / 4), hw);
-                            tmem_st4(st + 16u + (uint32_t)(j / 4), lw);
+                            tmem_st4(pt + (uint32_t)(j / 4), hw);
+                            tmem_st4(pt + 16u + (uint32_t)(j / 4), lw);
                         } else {
-                            tmem_st8(st + (uint32_t)(j / 2), hw);
+                            tmem_st8(pt + (uint32_t)(j / 2), hw);
                         }
                     }
                     float a, b;
                     unpack2(add2(sum0, sum1), a, b);
-                    l += keep ? a + b : 0.0f;
+                    l += vis > 0 ? a + b : 0.0f;
                 } else {
                     uint32_t z[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         z[j] = 0u;
-                    tmem_st16(st, z);
-                    tmem_st16(st + 16u, z);
+                    tmem_st16(pt, z);
+                    tmem_st16(pt + 16u, z);
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -928,10 +942,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     float acc[kD2 / 32] = {};
                     for (int v = seg.p0; v < seg.p1; ++v) {
                         int e;
-                        const int64_t tok0 = list_tile(v, e);
+                        const int64_t tok0 = list_step(v, e);
                         if (!((u.sp.mask[e] >> q2) & 1u))
                             continue;
-                        for (int j = 0; j < 128 && tok0 + j < len2; ++j) {
+                        for (int j = 0; j < kTok && tok0 + j < len2; ++j) {
                             const int32_t pg = attn_page(p, u.sp.toff[u.sp.block[e] >> 24], tok0 + j);
                             if (pg < 0)
                                 continue;

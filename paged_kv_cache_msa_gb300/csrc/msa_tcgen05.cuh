@@ -46,19 +46,28 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// The same, asleep for up to 20 us: a warp that polls takes issue slots from the others.
+__device__ __forceinline__ bool mbar_try_asleep(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000)
+        : "memory");
+    return ok != 0;
+}
+
 // true once the phase with the given parity has completed; false after the limit
 // (MSA_WAIT_LIMIT_NS, 2 s)
 __device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 {
-    if (mbar_try(bar, parity))
-        return true;
     const uint64_t t0 = globaltimer();
-    for (uint32_t n = 1;; ++n) {
-        if (mbar_try(bar, parity))
+    do
+        if (mbar_try_asleep(bar, parity))
             return true;
-        if ((n & 63) == 0 && globaltimer() - t0 > MSA_WAIT_LIMIT_NS)
-            return false;
-    }
+    while (globaltimer() - t0 <= MSA_WAIT_LIMIT_NS);
+    return false;
 }
 
 // A whole warp waits; false (and the CTA's abort flag set) when the wait ran out or

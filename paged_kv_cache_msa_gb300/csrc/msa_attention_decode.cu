@@ -910,6 +910,8 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
     __shared__ float s_w[32][kJoinHeads];            // weights of the pieces
     __shared__ float s_scale[kJoinHeads];            // of what was added before them
     __shared__ float s_m[kJoinHeads], s_l[kJoinHeads];
+    __shared__ const float *s_at[32];                // output of the pieces' first head
+    __shared__ int s_stride[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
@@ -1007,13 +1009,14 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
         const int count = min(32, n - i0);
         __syncthreads();
         // weights: a warp per head, a lane per piece
+        const PieceAt a = piece(i0 + min(lane, count - 1));
+        if (warp == 0) {
+            s_at[lane] = a.o;
+            s_stride[lane] = a.stride;
+        }
         for (int k = warp; k < nh; k += blockDim.x >> 5) {
-            float pm = -INFINITY, pl = 0.0f;
-            if (lane < count) {
-                const PieceAt a = piece(i0 + lane);
-                pm = __ldcg(a.m + k * a.mstride);
-                pl = __ldcg(a.m + k * a.mstride + a.sums);
-            }
+            const float pm = __ldcg(a.m + k * a.mstride);
+            const float pl = lane < count ? __ldcg(a.m + k * a.mstride + a.sums) : 0.0f;
             const bool seen = pl != 0.0f;                       // a NaN goes on
             float mx = seen ? pm : -INFINITY;
 #pragma unroll
@@ -1042,16 +1045,22 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
             acc.y *= a;
             acc.z *= a;
             acc.w *= a;
-#pragma unroll 4
-            for (int i = 0; i < count; ++i) {
-                const PieceAt at = piece(i0 + i);
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(at.o + h * at.stride + d));
-                const float wt = s_w[i][h];
-                if (wt != 0.0f) {                               // nothing seen: the row may hold anything
-                    acc.x = fmaf(x.x, wt, acc.x);
-                    acc.y = fmaf(x.y, wt, acc.y);
-                    acc.z = fmaf(x.z, wt, acc.z);
-                    acc.w = fmaf(x.w, wt, acc.w);
+            // eight loads in flight; past the last piece, that one again with no weight
+            for (int i = 0; i < count; i += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = min(i + e, count - 1);
+                    x[e] = __ldcg(reinterpret_cast<const float4 *>(s_at[j] + h * s_stride[j] + d));
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float wt = i + e < count ? s_w[i + e][h] : 0.0f;
+                    const bool seen = wt != 0.0f;               // nothing seen: the row may hold anything
+                    acc.x = seen ? fmaf(x[e].x, wt, acc.x) : acc.x;
+                    acc.y = seen ? fmaf(x[e].y, wt, acc.y) : acc.y;
+                    acc.z = seen ? fmaf(x[e].z, wt, acc.z) : acc.z;
+                    acc.w = seen ? fmaf(x[e].w, wt, acc.w) : acc.w;
                 }
             }
         }

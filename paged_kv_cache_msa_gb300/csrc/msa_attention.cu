@@ -487,7 +487,7 @@ AttnTiles tiles_of(const AttnParams &p, const Maps &maps, const Layout &l, void 
     t.rows = reinterpret_cast<float *>(ws + l.tile_rows);
     t.nq = p.num_queries;
     t.gp_shift = gp_shift;
-    t.splits = 1;
+    t.splits = t.cta_heads = 1;
     t.ctas = 2 * (maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas);     // two a SM
     t.box_rows = maps.box_rows;
     t.oob_page = maps.oob_page;
@@ -531,7 +531,11 @@ msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l
     const int64_t qt = 128 >> shift, units = (p.num_queries + qt - 1) / qt * p.hkv;
     const int64_t fit = t.ctas / units;
     t.splits = fit > 1 ? (int32_t)(fit < 16 ? fit : 16) : 1;
-    t.ctas = (int32_t)(units * t.splits);
+    // K/V heads of a tile share its list of blocks: as many a CTA as leave five rounds of CTAs
+    t.cta_heads = 1;
+    while (t.cta_heads < p.hkv && units / (2 * t.cta_heads) >= 5 * (int64_t)t.ctas)
+        t.cta_heads *= 2;
+    t.ctas = (int32_t)((p.num_queries + qt - 1) / qt * ((p.hkv + t.cta_heads - 1) / t.cta_heads) * t.splits);
     msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
     if (s == MSA_OK && t.splits > 1)
         s = launched(attn_join_splits(p, pieces_of(p, maps, l, workspace), t, head_dim, stream));

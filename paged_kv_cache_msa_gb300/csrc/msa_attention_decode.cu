@@ -248,7 +248,11 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     }
     if (warp == 2)
         tmem_alloc(smem_u32(&s_tmem), S::kTmem);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Behind a shared prefix the kernel ahead is the tile kernel, which waited for all before
+    // it and whose pieces are not read here: this one may run beside it, and waits for it
+    // only at the end, so that the join comes after both.
+    if (!w.joined)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
 
     // Tiles of each query and their prefix sums, a query a thread.  Lengths, table offsets
@@ -881,6 +885,8 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         tc_fence_after();
         tmem_free(tmem, S::kTmem);
     }
+    if (w.joined)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------

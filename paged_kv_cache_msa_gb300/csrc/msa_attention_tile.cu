@@ -10,8 +10,9 @@
 // kind::f8f6f4 with Q and P split into E4M3 halves hi | lo (twice the MMAs at twice the
 // rate: no conversion of keys or values, and half the bytes in shared memory); bf16 on
 // kind::f16.
-//   warp 0     TMA: page lookups in batches, one ahead, key and value copies
-//   warp 1     MMAs; zeroes value rows past the history before they are multiplied
+//   warp 0     key copies (TMA) and the MMAs of the scores
+//   warp 1     value copies and the MMAs of the values; zeroes value rows past the history
+//              before they are multiplied
 //   warps 2-9  softmax and output: two groups of four warps, a thread per row; the groups
 //              take alternate steps, then half of the dims each
 // Tensor memory (256 columns): S | P of group 0 | P of group 1 | O.  S is read into
@@ -43,7 +44,6 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kTok = kAttnStep;     // tokens of a step
 constexpr int kInfo = 8;            // steps whose validity words are held
-constexpr int kMaxBoxes = 8;
 constexpr int kMaxList = kAttnTileList;      // blocks of a tile's list
 constexpr int kTileQueries = 32;    // queries of a tile at most (a mask word)
 
@@ -209,11 +209,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     using S = TileShape<D, FP8>;
     constexpr int ST = S::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
+    __shared__ __align__(8) uint64_t bar_k_full[ST], bar_v_full[ST];
     __shared__ __align__(8) uint64_t bar_info[kInfo];
     __shared__ __align__(8) uint64_t bar_q, bar_s[2], bar_read, bar_p[2], bar_pv[2], bar_o, bar_drain;
     __shared__ __align__(8) uint64_t bar_ref[2][4];
-    __shared__ uint8_t s_nv[kInfo][kMaxBoxes];     // visible rows of each box
     __shared__ uint32_t s_gap[kInfo];              // boxes without a page before the history's end
     __shared__ union {
         AttnGroups groups;                         // DENSE
@@ -240,9 +239,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
         for (int i = 0; i < ST; ++i) {
             mbar_init(smem_u32(&bar_k_full[i]), 1);
-            mbar_init(smem_u32(&bar_k_empty[i]), 1);
             mbar_init(smem_u32(&bar_v_full[i]), 1);
-            mbar_init(smem_u32(&bar_v_empty[i]), 1);
         }
         for (int i = 0; i < kInfo; ++i)
             mbar_init(smem_u32(&bar_info[i]), 1);
@@ -256,7 +253,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         }
         mbar_init(smem_u32(&bar_read), 4);
         mbar_init(smem_u32(&bar_o), 1);
-        mbar_init(smem_u32(&bar_drain), 1);
+        mbar_init(smem_u32(&bar_drain), 2);
         s_abort = 0;
         s_n = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -317,9 +314,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     } else {
         // the union of the queries' blocks: a hash of (sequence, block) in the ring's memory,
         // then sorted by rank, so that the order does not depend on the insertions'
-        seg.t0 = (int)(blockIdx.x / (p.hkv * w.splits)) * qt;
+        const int sets = (p.hkv + w.cta_heads - 1) / w.cta_heads;      // of K/V heads
+        seg.t0 = (int)(blockIdx.x / (sets * w.splits)) * qt;
         seg.nq = (int)min((int64_t)qt, p.num_queries - seg.t0);
-        seg.c = (int)(blockIdx.x / w.splits % p.hkv);
+        seg.c = (int)(blockIdx.x / w.splits % sets) * w.cta_heads;
         if (tid < kTileQueries) {
             u.sp.len[tid] = tid < seg.nq ? max(__ldg(p.kv_len + seg.t0 + tid), 0) : 0;
             u.sp.toff[tid] = tid < seg.nq ? __ldg(p.table_offset + seg.t0 + tid) : 0;
@@ -416,180 +414,193 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         e = per_block == 2 ? v >> 1 : v / per_block;
         return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * kTok;
     };
-    bool once = true;
     // the next segment of this CTA
+    const int c_end = DENSE ? 0 : min(p.hkv, seg.c + w.cta_heads);
     auto next_segment = [&](bool first) -> bool {
         if (DENSE) {
             if (!first)
                 dw.next(seg);
             return dw.get(seg);
         }
-        const bool r = once;
-        once = false;
-        return r;
+        seg.c += !first;
+        return seg.c < c_end;
+    };
+
+    // Copies of a segment's steps, by one warp: the pages of 32 / nbox steps are looked up at
+    // once, a box a lane, a batch ahead of their use.
+    const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = kTok >> lb;
+    struct Boxes {
+        int2 at;             // row in the page, page (one past the last: zeros, for a box that shows nothing)
+        int nv;              // rows that some query sees
+        bool gap;            // the history goes on without a page
+    };
+    auto look = [&](int v0) -> Boxes {
+        Boxes b = {make_int2(0, w.oob_page), 0, false};
+        const int v = v0 + (lane >> (6 - lb));
+        if (v >= seg.p1)
+            return b;
+        int64_t tok, off, len;
+        if (DENSE) {
+            tok = (int64_t)v * kTok;
+            off = __ldg(p.prefix_offset + seg.group);
+            len = seg.len;
+        } else {
+            int e;
+            tok = list_step(v, e);
+            off = u.sp.toff[u.sp.block[e] >> 24];
+            len = u.sp.maxlen[u.sp.block[e] >> 24];
+        }
+        tok += (lane & (nbox - 1)) * BR;
+        if (tok >= len)
+            return b;
+        const int32_t pg = attn_page(p, off, tok);
+        b.gap = pg < 0;
+        if (pg >= 0) {
+            b.at = make_int2(attn_page_row(p, tok), pg);
+            b.nv = (int)min((int64_t)BR, len - tok);
+        }
+        return b;
+    };
+    const int batch = 32 >> (6 - lb);
+    Boxes now, next;
+    // the boxes of step v (steps come in order), a box a lane; its gaps
+    auto boxes_of = [&](int v, int2 &at, int &nv) -> uint32_t {
+        const int k = (v - seg.p0) & (batch - 1);
+        if (v == seg.p0)
+            next = look(v);
+        if (k == 0) {
+            now = next;
+            next = look(v + batch);
+        }
+        const int from = k * nbox + (lane & (nbox - 1));
+        at = make_int2(__shfl_sync(0xffffffffu, now.at.x, from), __shfl_sync(0xffffffffu, now.at.y, from));
+        nv = __shfl_sync(0xffffffffu, now.nv, from);
+        return (__ballot_sync(0xffffffffu, now.gap) >> (k * nbox)) & ((1u << nbox) - 1u);
+    };
+    auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, int2 at) {
+#ifndef MSA_STARVE
+        if (lane == 0)
+            mbar_expect_tx(full, (uint32_t)S::kStepBytes);
+        __syncwarp();
+        if (lane < nbox)
+#pragma unroll
+            for (int k = 0; k < S::kAtoms; ++k)
+                tma_load_box(dst + (uint32_t)(k * kTok + lane * BR) * S::kSwz, map, k * (S::kSwz / (FP8 ? 1 : 2)), at.x,
+                             seg.c, at.y, full);
+#endif
+    };
+    // the copies of `n` steps have landed before the CTA finishes
+    auto drain = [&](uint64_t *full, uint32_t n) {
+#ifndef MSA_STARVE
+        for (uint32_t s = 0; s < (uint32_t)ST && s < n; ++s)
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), ((n - 1u - s) / ST) & 1u));
+#endif
     };
 
     if (warp == 0) {
-        // ---------------- copies ----------------
-        const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = kTok >> lb;
-        uint32_t n = 0;                // steps of the CTA
+        // ---------------- key copies and the MMAs of the scores ----------------
+        constexpr uint32_t kId = mma_idesc(FP8, 128, kTok, false, false);
+        const uint64_t q_desc = smem_desc(qsm, S::kSwz, 16u, 8u * S::kSwz);
+        const uint64_t k_desc = smem_desc(kring, S::kSwz, 16u, 8u * S::kSwz);
+        uint32_t n = 0, copied = 0, nseg = 0;         // steps of the CTA: scores made, keys asked for
         bool ok = true;
-        for (bool first = true; ok && next_segment(first); first = false) {
-            const int64_t prefix_off = DENSE ? __ldg(p.prefix_offset + seg.group) : 0;
-            // A batch of 32 / nbox steps is looked up at once, a box a lane, one batch ahead:
-            // row in the page, page (one past the last for a box that shows nothing: zeros),
-            // rows that some query sees, and whether the history goes on without a page.
-            const int batch = 32 >> (6 - lb), my_step = lane >> (6 - lb), my_box = lane & (nbox - 1);
-            auto look = [&](int v0, int2 &box, int &nv, bool &gap) {
-                box = make_int2(0, w.oob_page);
-                nv = 0;
-                gap = false;
-                const int v = v0 + my_step;
-                if (v >= seg.p1)
-                    return;
-                int64_t tok, off, len;
-                if (DENSE) {
-                    tok = (int64_t)v * kTok;
-                    off = prefix_off;
-                    len = seg.len;
-                } else {
-                    int e;
-                    tok = list_step(v, e);
-                    off = u.sp.toff[u.sp.block[e] >> 24];
-                    len = u.sp.maxlen[u.sp.block[e] >> 24];
+        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
+            auto keys = [&](int v) {
+                int2 at;
+                int nv;
+                const uint32_t gaps = boxes_of(v, at, nv);
+                // the slot's readers, eight steps before, are done: scores that came after
+                // have been read
+                if (lane == 0) {
+                    s_gap[copied % kInfo] = gaps;
+                    mbar_arrive(smem_u32(&bar_info[copied % kInfo]));
                 }
-                tok += my_box * BR;
-                if (tok >= len)
-                    return;
-                const int32_t pg = attn_page(p, off, tok);
-                gap = pg < 0;
-                if (pg >= 0) {
-                    box = make_int2(attn_page_row(p, tok), pg);
-                    nv = (int)min((int64_t)BR, len - tok);
-                }
+                copy(&kmap, kring + copied % ST * (uint32_t)S::kStepBytes, smem_u32(&bar_k_full[copied % ST]), at);
+                ++copied;
             };
-            int2 boxes, next_boxes;
-            int nvs, next_nvs;
-            bool gaps_of, next_gaps;
-            look(seg.p0, next_boxes, next_nvs, next_gaps);
+            // the scores of step n - 1 have been read: they are complete, its keys are free
+            if (n > 0)
+                ok = warp_wait(smem_u32(&bar_read), (n - 1u) & 1u, abort_flag);
+            for (int v = seg.p0; v < min(seg.p1, seg.p0 + ST) && ok; ++v)
+                keys(v);
+            ok = ok && warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
             for (int v = seg.p0; v < seg.p1 && ok; ++v, ++n) {
-                const int at_batch = (v - seg.p0) & (batch - 1);
-                if (at_batch == 0) {
-                    boxes = next_boxes;
-                    nvs = next_nvs;
-                    gaps_of = next_gaps;
-                    look(v + batch, next_boxes, next_nvs, next_gaps);
-                }
-                const int from = at_batch * nbox + (lane & (nbox - 1));
-                const int2 box = make_int2(__shfl_sync(0xffffffffu, boxes.x, from), __shfl_sync(0xffffffffu, boxes.y, from));
-                const int nv = __shfl_sync(0xffffffffu, nvs, from);
-                const uint32_t gaps = (__ballot_sync(0xffffffffu, gaps_of) >> (at_batch * nbox)) & ((1u << nbox) - 1u);
-                const uint32_t s = n % ST, par = ((n / ST) & 1u) ^ 1u, slot = n % kInfo;
-                ok = warp_wait(smem_u32(&bar_k_empty[s]), par, abort_flag);
+                const uint32_t s = n % ST;
+                ok = warp_wait(smem_u32(&bar_k_full[s]), (n / ST) & 1u, abort_flag);
+                if (v > seg.p0)
+                    ok = ok && warp_wait(smem_u32(&bar_read), (n - 1u) & 1u, abort_flag);
                 if (!ok)
                     break;
-                // the slot's readers, eight steps before, are done: the scores that freed this
-                // stage were made after the group had read later ones
-                if (lane < nbox)
-                    s_nv[slot][lane] = (uint8_t)nv;
-                if (lane == 0)
-                    s_gap[slot] = gaps;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bar_info[slot]));
-                auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full) {
-#ifndef MSA_STARVE
-                    if (lane == 0)
-                        mbar_expect_tx(full, (uint32_t)S::kStepBytes);
-                    __syncwarp();
-                    if (lane < nbox)
+                tc_fence_after();
+                const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
+                if (S::kSwz == 128) {
+                    // a swizzle atom is four MMAs; the halves, or the atoms of a row, follow
+                    mma_ss4<FP8, 2, 2>(tmem, q_desc, kd, kId, 0);
+                    if (D == 128)
+                        mma_ss4<FP8, 2, 2>(tmem, q_desc + 128 * 128 / 16, FP8 ? kd : kd + kTok * 128 / 16, kId, 1);
+                } else {
 #pragma unroll
-                        for (int at = 0; at < S::kAtoms; ++at)
-                            tma_load_box(dst + (uint32_t)(at * kTok + lane * BR) * S::kSwz, map,
-                                         at * (S::kSwz / (FP8 ? 1 : 2)), box.x, seg.c, box.y, full);
-#endif
-                };
-                copy(&kmap, kring + s * (uint32_t)S::kStepBytes, smem_u32(&bar_k_full[s]));
-                ok = warp_wait(smem_u32(&bar_v_empty[s]), par, abort_flag);
-                if (!ok)
-                    break;
-                copy(&vmap, vring + s * (uint32_t)S::kStepBytes, smem_u32(&bar_v_full[s]));
+                    for (int ks = 0; ks < 4; ++ks)    // two of hi, two of lo
+                        mma_ss<FP8>(tmem, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
+                                    kd + (uint64_t)((ks & 1) * 2), kId, ks > 0);
+                }
+                mma_commit(smem_u32(&bar_s[n & 1]));
+                if (v > seg.p0 && v - 1 + ST < seg.p1)
+                    keys(v - 1 + ST);
             }
+            __syncwarp();
         }
         if (!ok)
             *abort_flag = 1;
-#ifndef MSA_STARVE
-        // every copy has landed before the CTA finishes (of the last step of an aborted
-        // CTA the values may not have been asked for; that wait runs out)
-        for (uint32_t s = 0; s < (uint32_t)ST && s < n; ++s) {
-            const uint32_t par = ((n - 1u - s) / ST) & 1u;
-            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), par));
-            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_v_full[s]), par));
-        }
-        if (!ok)
-            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[n % ST]), (n / ST) & 1u));
-#endif
+        drain(bar_k_full, copied);
+        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
+        (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
     } else if (warp == 1) {
-        // ---------------- MMAs ----------------
-        constexpr uint32_t kIdS = mma_idesc(FP8, 128, kTok, false, false);
-        constexpr uint32_t kIdO = mma_idesc(FP8, 128, D, false, true);
+        // ---------------- value copies and the MMAs of the values ----------------
+        constexpr uint32_t kId = mma_idesc(FP8, 128, D, false, true);
         constexpr int kStep = (FP8 ? 32 : 16) * S::kSwz / 16;      // descriptor units of one MMA's tokens
-        const int BR = w.box_rows, nbox = kTok / BR;
-        const uint64_t q_desc = smem_desc(qsm, S::kSwz, 16u, 8u * S::kSwz);
-        const uint64_t k_desc = smem_desc(kring, S::kSwz, 16u, 8u * S::kSwz);
         const uint64_t v_desc = smem_desc(vring, S::kSwz, (uint32_t)kTok * S::kSwz, 8u * S::kSwz);
-        uint32_t n = 0, nseg = 0;         // steps of the CTA whose values were multiplied
+        uint32_t n = 0, copied = 0;
         bool ok = true;
-        // the scores of step i; `wait_read`: once those of the step before have been read
-        auto scores = [&](uint32_t i, bool wait_read) {
-            const uint32_t s = i % ST;
-            ok = ok && (!wait_read || warp_wait(smem_u32(&bar_read), (i - 1u) & 1u, abort_flag));
-            ok = ok && warp_wait(smem_u32(&bar_k_full[s]), (i / ST) & 1u, abort_flag);
-            if (!ok)
-                return;
-            tc_fence_after();
-            const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
-            if (S::kSwz == 128) {
-                // a swizzle atom is four MMAs; the halves, or the atoms of a row, follow
-                mma_ss4<FP8, 2, 2>(tmem, q_desc, kd, kIdS, 0);
-                if (D == 128)
-                    mma_ss4<FP8, 2, 2>(tmem, q_desc + 128 * 128 / 16, FP8 ? kd : kd + kTok * 128 / 16, kIdS, 1);
-            } else {
+        for (bool first = true; ok && next_segment(first); first = false) {
+            // Rows past the history, in one box at most of a segment's or block's last step, may
+            // hold anything, and a weight of zero would not hide an infinity or a NaN: the rows
+            // of each box that are to be kept, of the steps asked for (8 bits each)
+            uint32_t kept[ST];
+            auto values = [&](int v) {
+                int2 at;
+                int nv;
+                boxes_of(v, at, nv);
+                copy(&vmap, vring + copied % ST * (uint32_t)S::kStepBytes, smem_u32(&bar_v_full[copied % ST]), at);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)    // two of hi, two of lo
-                    mma_ss<FP8>(tmem, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
-                                kd + (uint64_t)((ks & 1) * 2), kIdS, ks > 0);
-            }
-            mma_commit(smem_u32(&bar_s[i & 1]));
-            mma_commit(smem_u32(&bar_k_empty[s]));
-        };
-        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
-            const int steps = seg.p1 - seg.p0;
-            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
-            if (steps > 0)
-                scores(n, n > 0);
-            if (steps > 1)
-                scores(n + 1, true);
-            for (int v = 0; v < steps && ok; ++v, ++n) {
-                if (v + 2 < steps)
-                    scores(n + 2, true);
+                for (int k = 0; k < ST; ++k)
+                    kept[k] = copied % ST == k ? (uint32_t)nv : kept[k];
+                ++copied;
+            };
+            // the values of step n - 1 are multiplied: they are free
+            if (n > 0)
+                ok = warp_wait(smem_u32(&bar_pv[(n - 1u) & 1u]), ((n - 1u) >> 1) & 1u, abort_flag);
+            for (int v = seg.p0; v < min(seg.p1, seg.p0 + ST) && ok; ++v)
+                values(v);
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++n) {
                 const uint32_t s = n % ST, g = n & 1u;
-                ok = ok && warp_wait(smem_u32(&bar_v_full[s]), (n / ST) & 1u, abort_flag);
+                ok = warp_wait(smem_u32(&bar_v_full[s]), (n / ST) & 1u, abort_flag);
                 if (!ok)
                     break;
-                // rows past the history may hold anything: a weight of zero would not hide an
-                // infinity or a NaN
-                const int nv = lane < nbox ? s_nv[n % kInfo][lane] : 0;
-                uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
+                uint32_t nv = kept[0];
+#pragma unroll
+                for (int k = 1; k < ST; ++k)
+                    nv = s == k ? kept[k] : nv;
+                uint32_t partial = __ballot_sync(0xffffffffu, lane < nbox && nv > 0 && nv < (uint32_t)BR);
                 if (partial) {
                     const uint32_t vt = vring + s * (uint32_t)S::kStepBytes;
                     while (partial) {
                         const int b = __ffs(partial) - 1;
                         partial &= partial - 1;
-                        const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
-                        for (int at = 0; at < S::kAtoms; ++at)
+                        const int r0 = b * BR + (int)__shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
+                        for (int k = 0; k < S::kAtoms; ++k)
                             for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
-                                sts128(vt + (uint32_t)(at * kTok) * S::kSwz + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
+                                sts128(vt + (uint32_t)(k * kTok) * S::kSwz + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -599,17 +610,17 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     break;
                 tc_fence_after();
                 const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
-                const uint32_t pt = tmem + 64u + g * 32u, acc = v > 0;
-                if (FP8) {      // two of hi, two of lo against the same values
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ts<FP8>(tmem + 128u, pt + (uint32_t)(ks * 8), vd + (uint64_t)((ks & 1) * kStep), kIdO,
-                                    acc | (uint32_t)ks);
-                } else {
-                    mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kIdO, acc);
-                }
+                const uint32_t pt = tmem + 64u + g * 32u, acc = v > seg.p0;
+                if (FP8)        // two of hi, two of lo against the same values
+                    mma_ts22<kStep>(tmem + 128u, pt, vd, kId, acc);
+                else
+                    mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kId, acc);
                 mma_commit(smem_u32(&bar_pv[g]));
-                mma_commit(smem_u32(&bar_v_empty[s]));
+                if (v > seg.p0 && v - 1 + ST < seg.p1) {
+                    ok = warp_wait(smem_u32(&bar_pv[g ^ 1u]), ((n - 1u) >> 1) & 1u, abort_flag);
+                    if (ok)
+                        values(v - 1 + ST);
+                }
             }
             __syncwarp();
             if (ok)
@@ -617,7 +628,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         }
         if (!ok)
             *abort_flag = 1;
-        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
+        drain(bar_v_full, copied);
+        mma_commit(smem_u32(&bar_drain));
         (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
     } else {
         // ---------------- softmax and output ----------------
@@ -625,7 +637,6 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t st = lanes, pt = lanes + 64u + (uint32_t)(half * 32), ot = lanes + 128u;
         const int gp = 1 << w.gp_shift, qi = row >> w.gp_shift, hi = row & (gp - 1);
-        const int BR = w.box_rows, lb = __ffs(BR) - 1;
         constexpr float kLazy = FP8 ? kLazyFp8 : kLazyBf16, kOff = FP8 ? kPOffset : 0.0f;
         constexpr int kD2 = D / 2;                      // dims of this thread
         const float nan = __int_as_float(0x7fc00000);
@@ -634,55 +645,64 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         uint32_t n = 0, nseg = 0;                       // steps of the CTA before the segment
         bool ok = true;
         for (bool first = true; next_segment(first); first = false, ++nseg) {
-            // ---- the row's query into shared memory ----
+            // ---- the row's query into shared memory (where the outputs before were staged) ----
+            if (!first)
+                asm volatile("bar.sync 5, 256;" ::: "memory");
             const bool real = qi < seg.nq && hi < p.group;
             // its row of q and out
             auto head_row = [&]() -> int64_t { return (w.q0 + seg.t0 + qi) * p.hq + seg.c * p.group + hi; };
             const float ks = attn_k_scale(p, seg.c) * p.scale_log2;
             float qs = fabsf(ks);                          // a negative scale goes into the query
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + head_row() * D);
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + head_row() * D) + half * (kD2 / 8);
                 const uint32_t flip = ks < 0.0f ? 0x80008000u : 0u;
+                uint32_t xs[kD2 / 2];
+#pragma unroll
+                for (int i = 0; i < kD2 / 8; ++i) {
+                    const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    xs[4 * i] = x.x ^ flip;
+                    xs[4 * i + 1] = x.y ^ flip;
+                    xs[4 * i + 2] = x.z ^ flip;
+                    xs[4 * i + 3] = x.w ^ flip;
+                }
                 float sc = 1.0f;
                 if (FP8) {
+                    // halves hi | lo under the power of two that brings the row's largest
+                    // magnitude (magnitudes compare as integers) into [128, 256)
                     uint32_t big = 0;
-#pragma unroll 4
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            big = max(big, max((xs[j] & 0x7FFFu) << 16, xs[j] & 0x7FFF0000u));
-                    }
-                    big >>= 23;
+                    for (int i = 0; i < kD2 / 2; ++i)
+                        big = max(big, max((xs[i] & 0x7FFFu) << 16, xs[i] & 0x7FFF0000u));
+                    s_row[half][row] = __uint_as_float(big);
+                    pair_sync();
+                    big = max(big, __float_as_uint(s_row[half ^ 1][row])) >> 23;
                     const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
                     sc = __int_as_float((e2 + 127) << 23);
                     qs *= __int_as_float((127 - e2) << 23);
                 }
-#pragma unroll 2
-                for (int i = half * (kD2 / 8); i < (half + 1) * (kD2 / 8); ++i) {
-                    const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t xs[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+#pragma unroll
+                for (int i = 0; i < kD2 / 8; ++i) {
+                    const int chunk = half * (kD2 / 8) + i;
                     if (FP8) {
                         uint32_t hw[2], lw[2];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float x0 = __uint_as_float(xs[j] << 16) * sc;
-                            const float x1 = __uint_as_float(xs[j] & 0xFFFF0000u) * sc;
+                            const float x0 = __uint_as_float(xs[4 * i + j] << 16) * sc;
+                            const float x1 = __uint_as_float(xs[4 * i + j] & 0xFFFF0000u) * sc;
                             const uint32_t h = e4m3x2_from_f32(x0, x1);
                             const float2 d = attn_e4m3x2_to_f2(h);
                             const uint32_t l = e4m3x2_from_f32(x0 - d.x, x1 - d.y);
                             hw[j / 2] = j & 1 ? hw[j / 2] | (h << 16) : h;
                             lw[j / 2] = j & 1 ? lw[j / 2] | (l << 16) : l;
                         }
-                        const uint32_t a = swizzle<S::kSwz>((uint32_t)(row * S::kSwz + i * 8));
+                        const uint32_t a = swizzle<S::kSwz>((uint32_t)(row * S::kSwz + chunk * 8));
                         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + a), "r"(hw[0]), "r"(hw[1]) : "memory");
                         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + 128 * D + a), "r"(lw[0]), "r"(lw[1])
                                      : "memory");
                     } else {
-                        const uint32_t byte = (uint32_t)i * 16, at = byte / S::kSwz, col = byte % S::kSwz;
-                        sts128(qsm + at * (128u * S::kSwz) + swizzle<S::kSwz>((uint32_t)row * S::kSwz + col), xs[0], xs[1],
-                               xs[2], xs[3]);
+                        const uint32_t byte = (uint32_t)chunk * 16, at = byte / S::kSwz, col = byte % S::kSwz;
+                        sts128(qsm + at * (128u * S::kSwz) + swizzle<S::kSwz>((uint32_t)row * S::kSwz + col), xs[4 * i],
+                               xs[4 * i + 1], xs[4 * i + 2], xs[4 * i + 3]);
                     }
                 }
             }

@@ -154,24 +154,6 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
             : "memory");
 }
 
-// The same with A in tensor memory.
-template <bool FP8>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
-{
-    if (FP8)
-        asm volatile(
-            "{\n\t.reg .pred pp, pe;\n\telect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
-            "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, pp;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred pp, pe;\n\telect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
-            "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pp;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
-
 // Four MMAs in a row, whose operands lie AS and BS apart (in descriptor units of 16 bytes;
 // for A in tensor memory, columns): one election, and operands made in place, since the
 // issue of an MMA costs its warp several times the instructions that describe it.
@@ -235,6 +217,23 @@ __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint
             "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
             "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
             : "memory");
+}
+
+// Four E4M3 MMAs with A in tensor memory, 8 columns apart, the third and fourth against the
+// B of the first two, which are BS apart.
+template <int BS>
+__device__ __forceinline__ void mma_ts22(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred pp, pe;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u64 b1, %2, %5;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, pp;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a1], b1, %3, 1;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a2], %2, %3, 1;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a3], b1, %3, 1;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(BS)
+        : "memory");
 }
 
 // Arrives on `bar` when every MMA this warp's elected lane has issued is complete.

@@ -173,10 +173,12 @@ class DecodeLayer:
     """One MSA decode layer's hot path on the device: the producer (rows -> compact
     Q / index-Q, K/V/index-K into the caches) followed by the indexer on what the
     producer wrote (its compact index-Q and index-K cache), each token's visible
-    history being its position + 1 tokens in its sequence's page-table row."""
+    history being its position + 1 tokens in its sequence's page-table row.  With
+    ``attention``, the sparse attention of the compact Q over the K/V caches and the
+    blocks the indexer selected comes last (``attn_out``, ``attn_lse``)."""
 
     def __init__(self, dw: DeviceWorkload, max_blocks_per_seq: int, block_tokens: int = 128,
-                 topk: int = 16):
+                 topk: int = 16, attention: bool = False):
         import torch
         self.dw = dw
         w = dw.w
@@ -198,10 +200,19 @@ class DecodeLayer:
                                         device=dw.device)
         self.topk_ids = torch.empty((T, topk), dtype=torch.int32, device=dw.device)
         self.counters = torch.zeros((T,), dtype=torch.int32, device=dw.device)
+        self.attn_cfg = None
+        if attention:
+            self.attn_cfg = B.make_attention_cfg(s["num_q_heads"], s["num_kv_heads"], s["head_dim"], P,
+                                                 block_tokens, topk, scale_mode=s.get("scale_mode", 0))
+            self.attn_out = torch.empty_like(dw.q_out)
+            self.attn_lse = torch.empty(dw.q_out.shape[:2], dtype=torch.float32, device=dw.device)
+            self.attn_workspace = torch.empty(B.msa_attention_workspace_bytes(self.attn_cfg, T),
+                                              dtype=torch.uint8, device=dw.device)
 
     def run(self, stream, flags=0, fused=False):
         """The producer, then the indexer on what it wrote (with ``fused``, the
-        single-launch indexer on this layer's zeroed counters)."""
+        single-launch indexer on this layer's zeroed counters), then the attention of a
+        layer that has it."""
         dw = self.dw
         p = lambda t: int(t.data_ptr())
         dw.run(B.MSA_LAUNCH_PERSISTENT | (flags & B.MSA_LAUNCH_PDL), stream=stream)
@@ -213,3 +224,9 @@ class DecodeLayer:
                                         stream=stream.cuda_stream)
         else:
             B.msa_indexer_forward(*args, flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)
+        if self.attn_cfg is not None:
+            B.msa_sparse_attention_forward(
+                self.attn_cfg, dw.w.num_tokens, p(dw.q_out), p(self.kv_len), p(self.table_offset),
+                p(dw.page_table), dw.page_table.numel(), p(self.topk_ids), dw.caches["k"], dw.caches["v"],
+                p(dw.scales), p(self.attn_out), p(self.attn_lse), p(self.attn_workspace),
+                self.attn_workspace.numel(), flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)

@@ -214,3 +214,177 @@ def test_a_call_repeats_bit_for_bit(kw):
             assert torch.equal(e.out, e2.out) and torch.equal(e.lse, e2.lse)
         else:
             assert torch.equal(d.out, e.out) and torch.equal(d.lse, e.lse)
+
+
+def _both():
+    return [(Problem(19, lens=(1, 700, 300, 64, 2000, 129, 0, 90, 1500), heads=(16, 2), topk=6), 0),
+            (Problem(20, **_runs((1000, 90)), heads=(16, 2), topk=6, ids="near"), RUNS),
+            (Problem(21, lens=(3, 500, 0, 77) * 6, prefixes=(1500, 200), groups=(0, 20, 24), heads=(16, 2), ids=None), 0)]
+
+
+def test_captured_and_replayed():
+    """A capture of the three kinds of call, replayed on changed queries."""
+    items = [(p, p.device(), flags) for p, flags in _both()]
+    for _, d, flags in items:
+        d.run(flags)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _, d, flags in items:
+            d.run(flags)
+    for p, d, _ in items:
+        p.q = (0.5 * p.q.flip(0)).to(torch.bfloat16).contiguous()
+        d.q.copy_(p.q)
+        d.out.fill_(float("nan"))
+        d.ws.fill_(0xFF)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for _, d, _ in items:
+        d.check()
+
+
+def test_two_calls_at_once_on_other_streams():
+    """Calls in flight together on streams that are not the current one, each with its own
+    workspace, many times over."""
+    items = [(p, p.device(), flags, torch.cuda.Stream()) for p, flags in _both()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _, d, flags, s in items:
+            d.run(flags, stream=s)
+    torch.cuda.synchronize()
+    for _, d, _, _ in items:
+        d.check()
+
+
+@pytest.mark.parametrize("which", [0, 1, 2], ids=["decode", "runs", "prefix"])
+def test_nothing_past_the_buffers_is_written(which):
+    """Outputs and workspace between guard bands; the caches and inputs as they were."""
+    p, flags = _both()[which]
+    d = p.device()
+    pad = 4096
+    bufs = {}
+    for name in ("out", "lse", "ws"):
+        t = getattr(d, name)
+        n = t.numel() * t.element_size()
+        raw = torch.full((n + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+        raw[pad:pad + n] = 0xFF
+        setattr(d, name, raw[pad:pad + n].view(t.dtype).view(t.shape))
+        bufs[name] = (raw, n)
+    d.ws = bufs["ws"][0][pad:pad + B.msa_attention_workspace_bytes(d.cfg, p.T, 0 if p.groups is None else len(p.prefixes))]
+    before = [x.clone() for x in (d.kpool.view(torch.uint8), d.vpool.view(torch.uint8), d.q, d.lens, d.toff, d.table)]
+    d.run(flags)
+    torch.cuda.synchronize()
+    for raw, n in bufs.values():
+        assert (raw[:pad] == 0xA5).all() and (raw[pad + n:] == 0xA5).all()
+    for a, b in zip(before, (d.kpool.view(torch.uint8), d.vpool.view(torch.uint8), d.q, d.lens, d.toff, d.table)):
+        assert torch.equal(a, b)
+    d.check()
+
+
+def test_without_lse_and_without_a_workspace():
+    for p, flags in _both():
+        d = p.device().run(flags)
+        e = p.device()
+        e.ws = None
+        e.run(flags, lse=False)
+        torch.cuda.synchronize()
+        assert torch.equal(d.out, e.out) and torch.isnan(e.lse).all()
+
+
+def test_more_queries_than_a_window():
+    """Several launches of the decode kernel, and windows that cut groups."""
+    n = 900
+    lens = [(i * 37) % 200 for i in range(n)]
+    Problem(22, lens=lens, heads=(4, 2), topk=2).device().run().check()
+    Problem(23, lens=lens, heads=(4, 2), ids=None, prefixes=(300, 150, 70), groups=(10, 350, 500, 880)).device().run().check()
+
+
+def test_offsets_past_32_bits():
+    """Cache elements past 2^32, page strides that leave holes between the pages."""
+    P, D, pages = 64, 128, 40
+    stride = 2**32 // 32 + 1024                       # elements: page 33 lies past 2^32
+    for dtype, tdt in ((B.MSA_DTYPE_FP8_E4M3, torch.float8_e4m3fn),):
+        raw = torch.zeros(pages * stride, dtype=torch.uint8, device="cuda")
+        view = torch.as_strided(raw, (pages, 2, P, D), (stride, P * D, D, 1))
+        g = torch.Generator(device="cuda").manual_seed(5)
+        vals = (torch.randn(pages, 2, P, D, generator=g, device="cuda") / 0.05).to(tdt).view(torch.uint8)
+        view.copy_(vals)
+        table = torch.randperm(pages, generator=torch.Generator().manual_seed(6)).to(torch.int32).cuda()
+        T, n = 3, pages * P
+        q = torch.randn(T, 8, D, generator=g, device="cuda").to(torch.bfloat16)
+        cfg = B.make_attention_cfg(8, 2, D, P, 128, 8)
+        lens = torch.full((T,), n, dtype=torch.int32, device="cuda")
+        off = torch.zeros(T, dtype=torch.int64, device="cuda")
+        ids = torch.arange(20, dtype=torch.int32, device="cuda").flip(0)[:8].repeat(T, 1).contiguous()
+        scales = torch.tensor([0.05, 0.05], device="cuda")
+        c = B.cache_from_tensor(view)
+        outs = []
+        for flags in (0, RUNS):
+            out = torch.empty_like(q)
+            B.sparse_attention_tensors(cfg, q, ids, lens, off, table, c, c, scales, out, launch_flags=flags)
+            outs.append(out)
+        kv = vals[table.long()].view(tdt).double() * float(scales[0])         # [pages, 2, P, D] in token order
+        kv = kv.permute(1, 0, 2, 3).reshape(2, n, D)[:, 12 * 128:]
+        s = torch.einsum("thgd,hnd->thgn", q.double().view(T, 2, 4, D), kv) * D ** -0.5
+        ref = torch.einsum("thgn,hnd->thgd", s.softmax(-1), kv).reshape(T, 8, D)
+        tol = 2.0 ** -8 * ref.abs() + 2.0 ** -7 * kv.abs().mean() * 1.5
+        for out in outs:
+            assert ((out.double() - ref).abs() <= tol).all()
+
+
+def test_a_decode_layer_end_to_end():
+    """Producer, indexer and sparse attention of one decode step, the attention against its
+    definition on what the producer and the indexer wrote; then, on the same caches, dense
+    attention behind a shared prefix."""
+    from paged_kv_cache_msa_gb300 import workloads as wl
+    from paged_kv_cache_msa_gb300.device import DecodeLayer, DeviceWorkload
+    w = wl.config2_decode64()
+    pools = {k: torch.randint(0, 120, (n,), dtype=torch.uint8, device="cuda") for k, n in w.pools.items()}
+    dw = DeviceWorkload(w, pools_on_device=pools)
+    layer = DecodeLayer(dw, 144, attention=True)
+    s = torch.cuda.current_stream()
+    for flags in (0, PDL):
+        layer.run(s, flags)
+    torch.cuda.synchronize()
+    K, V = (pools[k][4096:] for k in ("k", "v"))
+    kc = w.caches["k"]
+    table, toff, kv_len = dw.page_table.cpu(), layer.table_offset.cpu(), layer.kv_len.cpu()
+    ids = layer.topk_ids.cpu()
+    q = dw.q_out.view(torch.bfloat16).double()
+    out = layer.attn_out.view(torch.bfloat16).double()
+    ks, vs = float(w.scales[0]), float(w.scales[1])
+
+    def rows(pool, t, js):
+        pg = table[int(toff[t]) + js // 64].long()
+        base = pg * kc.stride_page + (js % 64) * kc.stride_token
+        idx = base[:, None, None] + (torch.arange(8) * kc.stride_head)[None, :, None] + torch.arange(128)
+        return pool[idx.cuda()].view(torch.float8_e4m3fn).double()
+
+    for t in (0, 7, 20, 41, 63):
+        n = int(kv_len[t])
+        js = torch.cat([torch.arange(b * 128, min(n, b * 128 + 128)) for b in sorted(ids[t][ids[t] >= 0].tolist())])
+        k, v = rows(K, t, js) * ks, rows(V, t, js) * vs
+        z = torch.einsum("hgd,nhd->hgn", q[t].view(8, 8, 128), k) * 128 ** -0.5
+        ref = torch.einsum("hgn,nhd->hgd", z.softmax(-1), v).reshape(64, 128)
+        mean = torch.einsum("hgn,nhd->hgd", z.softmax(-1), v.abs()).reshape(64, 128)
+        # weights off by 2^-8 of themselves, scores by 2^-16 of their terms' magnitudes
+        mag = torch.einsum("hgd,nhd->hgn", q[t].view(8, 8, 128).abs(), k.abs()).amax(-1).reshape(64, 1) * 128 ** -0.5
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -14 * mag + 2.0 ** -14 * len(js)) * mean
+        assert ((out[t] - ref).abs() <= tol).all(), t
+    # dense attention of the same queries, the first 8 behind sequence 0's first 512 tokens
+    cfg = layer.attn_cfg
+    T = w.num_tokens
+    plen = min(512, int(kv_len.max()))
+    row = int(toff[int(kv_len.argmax())])
+    args = dict(kv_len=layer.kv_len, table_offset=layer.table_offset, page_table=dw.page_table,
+                k_cache=dw.caches["k"], v_cache=dw.caches["v"], scales=dw.scales)
+    a, b = torch.empty_like(dw.q_out), torch.empty_like(dw.q_out)
+    B.prefix_attention_tensors(cfg, dw.q_out, torch.tensor([0, 8], dtype=torch.int32, device="cuda"),
+                               torch.tensor([plen], dtype=torch.int32, device="cuda"),
+                               torch.tensor([row], dtype=torch.int64, device="cuda"), out=a, **args)
+    B.prefix_attention_tensors(cfg, dw.q_out, None, None, None, out=b, **args)
+    torch.cuda.synchronize()
+    assert torch.equal(a[8:], b[8:]) or (a[8:].view(torch.bfloat16).double() - b[8:].view(torch.bfloat16).double()).abs().max() <= 2.0 ** -7 * b.view(torch.bfloat16).abs().max()
+    assert not torch.equal(a[:8], b[:8])
+    assert torch.isfinite(a.view(torch.bfloat16)).all()

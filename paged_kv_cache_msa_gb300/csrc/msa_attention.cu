@@ -386,11 +386,10 @@ int64_t workspace_needed(const msa_attention_cfg *cfg, int64_t T, int64_t num_gr
     return layout_of(cfg, T, num_groups).bytes;
 }
 
-// Rows of the widest TMA box, at most `limit`, that never crosses a page or a selected
-// block: a power of two.
-int box_rows(const AttnParams &p, int limit)
+// Rows of the widest TMA box that never crosses a page or a selected block: a power of two.
+int box_rows(const AttnParams &p)
 {
-    int br = limit;
+    int br = kAttnTokens;
     while (br > 1 && (p.page_size % br || (p.topk_ids && p.block_tokens % br)))
         br /= 2;
     return br;
@@ -446,12 +445,11 @@ struct Maps {
     int32_t oob_page;
 };
 
-// `limit`: rows of a box at most (128, or a step of the tile kernel).
-void make_maps(Maps *m, const AttnParams &p, int head_dim, int limit)
+void make_maps(Maps *m, const AttnParams &p, int head_dim)
 {
     memset(m, 0, sizeof *m);
     m->sms = tensor_sms();
-    const int br = box_rows(p, limit);
+    const int br = box_rows(p);
     if (m->sms == 0 || br < 8 || p.k.fp8 != p.v.fp8 || !encode_cache(&m->k, p.k, head_dim, p.hkv, p.page_size, br) ||
         !encode_cache(&m->v, p.v, head_dim, p.hkv, p.page_size, br))
         return;
@@ -487,7 +485,7 @@ AttnTiles tiles_of(const AttnParams &p, const Maps &maps, const Layout &l, void 
     t.rows = reinterpret_cast<float *>(ws + l.tile_rows);
     t.nq = p.num_queries;
     t.gp_shift = gp_shift;
-    t.splits = t.cta_heads = 1;
+    t.splits = 1;
     t.ctas = 2 * (maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas);     // two a SM
     t.box_rows = maps.box_rows;
     t.oob_page = maps.oob_page;
@@ -531,11 +529,7 @@ msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l
     const int64_t qt = 128 >> shift, units = (p.num_queries + qt - 1) / qt * p.hkv;
     const int64_t fit = t.ctas / units;
     t.splits = fit > 1 ? (int32_t)(fit < 16 ? fit : 16) : 1;
-    // K/V heads of a tile share its list of blocks: as many a CTA as leave five rounds of CTAs
-    t.cta_heads = 1;
-    while (t.cta_heads < p.hkv && units / (2 * t.cta_heads) >= 5 * (int64_t)t.ctas)
-        t.cta_heads *= 2;
-    t.ctas = (int32_t)((p.num_queries + qt - 1) / qt * ((p.hkv + t.cta_heads - 1) / t.cta_heads) * t.splits);
+    t.ctas = (int32_t)(units * t.splits);
     msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
     if (s == MSA_OK && t.splits > 1)
         s = launched(attn_join_splits(p, pieces_of(p, maps, l, workspace), t, head_dim, stream));
@@ -623,14 +617,13 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
     AttnParams p = params_of(cfg, num_queries, q, kv_len, table_offset, page_table, page_table_len, k_cache, v_cache,
                              scales, out, lse);
     p.topk_ids = topk_ids;
-    // a step of the tile kernel lies in one block
-    const bool tiled = (launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % kAttnStep == 0;
     Maps maps;
-    make_maps(&maps, p, cfg->head_dim, tiled ? kAttnStep : 128);
+    make_maps(&maps, p, cfg->head_dim);
     if (maps.box_rows == 0)
         return launch_rows(p, cfg->head_dim, stream);
     const Layout l = layout_of(cfg, num_queries, 0);
-    if (tiled)
+    // a tile of the tile kernel lies in one block
+    if ((launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % kAttnTokens == 0)
         return run_query_runs(p, maps, l, cfg->head_dim, workspace, stream);
     return run_decode(p, maps, l, cfg->head_dim, workspace, stream);
 }
@@ -668,7 +661,7 @@ extern "C" msa_status msa_prefix_attention_forward(const msa_attention_cfg *cfg,
     p.prefix_offset = prefix_offset;
     p.num_groups = (int32_t)num_groups;
     Maps maps;
-    make_maps(&maps, p, cfg->head_dim, num_groups > 0 ? kAttnStep : 128);
+    make_maps(&maps, p, cfg->head_dim);
     if (maps.box_rows == 0)
         return launch_rows(p, cfg->head_dim, stream);
     const Layout l = layout_of(cfg, num_queries, num_groups);

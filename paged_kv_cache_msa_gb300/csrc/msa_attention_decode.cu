@@ -963,7 +963,7 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 own1 = (int)div64(base + nt - 1, share);
             }
             if (--g >= 0) {
-                const int nb = (__ldcg(tl.groups->len + g) + kAttnStep - 1) / kAttnStep;
+                const int nb = (__ldcg(tl.groups->len + g) + kAttnTokens - 1) / kAttnTokens;
                 if (nb > 0) {
                     const int at = q - __ldcg(tl.groups->start + g);
                     const int64_t share = __ldcg(&tl.groups->share);

@@ -11,7 +11,7 @@
 constexpr int kAttnMaxGroups = 512;
 constexpr int kAttnWindow = 384;     // queries a launch of the tensor-core decode kernel takes
 constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
-constexpr int kAttnStep = 64;        // tokens of a step of the tile kernel
+constexpr int kAttnTokens = 128;     // tokens of a tile of keys and values
 constexpr int kAttnTileList = 1024;  // (query, id) pairs of a sparse tile
 
 // One cache as the kernels see it; strides in elements.
@@ -79,8 +79,8 @@ struct AttnGroups {
     int32_t len[kAttnMaxGroups];
 };
 
-// What the tile kernel needs beside AttnParams.  Sparse: CTA = (tile, cta_heads K/V heads,
-// split), a split tile's piece in slot CTA.  Prefix: items over (group, tile, K/V head, step),
+// What the tile kernel needs beside AttnParams.  Sparse: CTA = (tile, K/V head, split), a
+// split tile's piece in slot CTA.  Prefix: items over (group, tile, K/V head, 128 tokens),
 // slots as in AttnPieces.  A slot is [128 rows][D], then [128][maximum, sum].
 struct AttnTiles {
     AttnGroups *groups;              // prefix
@@ -88,8 +88,7 @@ struct AttnTiles {
     float *rows;                     // prefix: whole units
     int64_t q0, nq;                  // the window (sparse: every query)
     int32_t gp_shift;                // log2 of the rows of a query
-    int32_t splits;                  // sparse: CTAs that share a tile's blocks (then cta_heads is 1)
-    int32_t cta_heads;               // sparse: K/V heads a CTA takes one after the other
+    int32_t splits;                  // sparse: CTAs that share a tile's blocks
     int32_t ctas;
     int32_t box_rows, oob_page;
 };

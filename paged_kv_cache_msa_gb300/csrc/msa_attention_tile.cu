@@ -4,34 +4,32 @@
 // What is computed is stated in include/msa_attention.h.
 //
 // A tile is 128 rows: QT queries times the heads of one K/V head, padded to a power of two.
-// A step is 64 tokens: the CTA computes S [128 rows, 64 tokens] = Q . K^T and
-// O [128 rows, D] += P . V, keys and values read from shared memory as TMA copied them
-// (K-major keys, N-major values), P as the A operand in tensor memory.  E4M3 caches run on
-// kind::f8f6f4 with Q and P split into E4M3 halves hi | lo (twice the MMAs at twice the
-// rate: no conversion of keys or values, and half the bytes in shared memory); bf16 on
-// kind::f16.
-//   warp 0     key copies (TMA) and the MMAs of the scores
-//   warp 1     value copies and the MMAs of the values; zeroes value rows past the history
-//              before they are multiplied
-//   warps 2-9  softmax and output: two groups of four warps, a thread per row; the groups
-//              take alternate steps, then half of the dims each
-// Tensor memory (256 columns): S | P of group 0 | P of group 1 | O.  S is read into
-// registers at once, so the next step's scores are made while this step's softmax runs, and
-// the scores run two steps ahead of the values; two CTAs share an SM and fill what gaps
-// are left.  Eight MMAs of N = 128 take 530 cycles of the tensor pipe, eight of N = 64 with
-// A in shared memory 390 (reading A binds), so 128 tokens take about 1,310 cycles.
-//
+// Per 128 tokens the CTA computes S [128 rows, 128 tokens] = Q . K^T and
+// O [128 rows, D] += P . V, each product read from shared memory as TMA copied it (K-major
+// keys, N-major values) with P as the A operand in tensor memory, where it takes the place
+// of the scores.  E4M3 caches run on kind::f8f6f4 with Q and P split into E4M3 halves
+// hi | lo (twice the MMAs at twice the rate: no conversion of keys or values, and half the
+// bytes in shared memory); bf16 on kind::f16.
+//   warp 0     TMA: page lookups one tile ahead, key and value copies
+//   warp 1     MMAs; zeroes value rows past the history before they are multiplied
+//   warps 2-9  softmax and output: two groups of four, a thread per row; group g takes the
+//              tokens 64 g .. 64 g + 63 of every tile, then D / 2 of the dims
+// Scores are made 64 tokens at a time into two buffers, one a group, so that the scores of
+// one half are ready while the other's softmax runs, and two CTAs share an SM (half the
+// tensor memory and half the shared memory each).  A tile of E4M3 keys takes about 1,280
+// cycles of the tensor pipe (the 64-token score MMAs read the queries from shared memory
+// twice), 1,024 of exponentials and 1,000 issue slots of a scheduler.
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
-// output in tensor memory rescaled, which few steps after the first need.  The groups hand
-// the reference of a row to one another step by step.
+// output in tensor memory rescaled, which few tiles after the first need.  The groups hand
+// the reference of a row to one another half by half.
 //
 // Sparse (DENSE = false): the tile's queries run over the union of their blocks, each row
 // masked to its own.  A weight of zero does not hide an infinity or a NaN in the values of
 // a token that another row of the tile sees, so a row whose output is not finite is
 // computed again from its own tokens alone.
-// Prefix (DENSE = true): (tile, K/V head, step) items laid end to end over the groups, an
-// equal share for each CTA; every piece goes to the workspace and is joined with the
+// Prefix (DENSE = true): (tile, K/V head, 128 tokens) items laid end to end over the groups,
+// an equal share for each CTA; every piece goes to the workspace and is joined with the
 // queries' own tokens.
 
 #include "msa_attention_internal.h"
@@ -42,8 +40,8 @@
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kTok = kAttnStep;     // tokens of a step
-constexpr int kInfo = 8;            // steps whose validity words are held
+constexpr int kInfo = 4;            // tiles whose validity words are held
+constexpr int kMaxBoxes = 16;
 constexpr int kMaxList = kAttnTileList;      // blocks of a tile's list
 constexpr int kTileQueries = 32;    // queries of a tile at most (a mask word)
 
@@ -52,12 +50,12 @@ struct TileShape {
     static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
     static constexpr int kSwz = kRowBytes < 128 ? kRowBytes : 128;
     static constexpr int kAtoms = kRowBytes / kSwz;
-    static constexpr int kStepBytes = kTok * kRowBytes;
+    static constexpr int kTileBytes = 128 * kRowBytes;
     static constexpr int kQBytes = 128 * D * 2;                   // bf16, or E4M3 hi | lo
-    static constexpr int kStages = kStepBytes == 16384 ? 2 : 4;   // of keys, and of values
-    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kStepBytes;
-    static constexpr int kTmem = 256;
-    static_assert(2 * kStages * kStepBytes >= 4 * kMaxList * 8, "scratch of the list");
+    static constexpr int kStages = kTileBytes == 32768 ? 1 : 2;   // of keys, and of values
+    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
+    static constexpr int kTmem = 256;                             // scores (and weights) | output
+    static_assert(2 * kStages * kTileBytes >= 4 * kMaxList * 8, "scratch of the list");
 };
 
 constexpr float kLazyBf16 = 8.0f, kLazyFp8 = 4.0f;
@@ -75,13 +73,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 
@@ -155,17 +146,17 @@ struct Segment {
     int t0;                  // first query (prefix: of the window)
     int nq;                  // queries in the tile
     int c;                   // K/V head
-    int p0, p1;              // steps
+    int p0, p1;              // 128-token tiles
     int group, len;          // prefix: the group, its tokens
     bool whole, began;       // prefix: all of its unit; it starts the unit
 };
 
 struct DenseWalk {
-    const AttnGroups *tab;    // group g has tiles x K/V heads units of nb steps
+    const AttnGroups *tab;    // group g has tiles x K/V heads units of nb 128-token tiles
     int64_t it, end, base;   // base: items before the unit
     int ngroups, hkv, qt, g, unit;
 
-    __device__ int nb() const { return (int)(((uint32_t)tab->len[g] + kTok - 1) / kTok); }
+    __device__ int nb() const { return (int)(((uint32_t)tab->len[g] + 127u) / 128u); }
     __device__ void find()
     {
         while (g < ngroups && tab->item[g + 1] <= it) {
@@ -209,10 +200,11 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     using S = TileShape<D, FP8>;
     constexpr int ST = S::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_k_full[ST], bar_v_full[ST];
+    __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
     __shared__ __align__(8) uint64_t bar_info[kInfo];
-    __shared__ __align__(8) uint64_t bar_q, bar_s[2], bar_read, bar_p[2], bar_pv[2], bar_o, bar_drain;
+    __shared__ __align__(8) uint64_t bar_q, bar_s[2], bar_p[2], bar_pv, bar_o, bar_drain;
     __shared__ __align__(8) uint64_t bar_ref[2][4];
+    __shared__ uint8_t s_nv[kInfo][kMaxBoxes];     // visible rows of each box
     __shared__ uint32_t s_gap[kInfo];              // boxes without a page before the history's end
     __shared__ union {
         AttnGroups groups;                         // DENSE
@@ -230,7 +222,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t qsm = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t kring = qsm + S::kQBytes, vring = kring + ST * S::kStepBytes;
+    const uint32_t kring = qsm + S::kQBytes, vring = kring + ST * S::kTileBytes;
     volatile int *abort_flag = &s_abort;
     const int qt = 128 >> w.gp_shift;
 
@@ -239,7 +231,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
         for (int i = 0; i < ST; ++i) {
             mbar_init(smem_u32(&bar_k_full[i]), 1);
+            mbar_init(smem_u32(&bar_k_empty[i]), 1);
             mbar_init(smem_u32(&bar_v_full[i]), 1);
+            mbar_init(smem_u32(&bar_v_empty[i]), 1);
         }
         for (int i = 0; i < kInfo; ++i)
             mbar_init(smem_u32(&bar_info[i]), 1);
@@ -247,13 +241,12 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar_s[i]), 1);
             mbar_init(smem_u32(&bar_p[i]), 4);
-            mbar_init(smem_u32(&bar_pv[i]), 1);
             for (int j = 0; j < 4; ++j)
                 mbar_init(smem_u32(&bar_ref[i][j]), 1);
         }
-        mbar_init(smem_u32(&bar_read), 4);
+        mbar_init(smem_u32(&bar_pv), 1);
         mbar_init(smem_u32(&bar_o), 1);
-        mbar_init(smem_u32(&bar_drain), 2);
+        mbar_init(smem_u32(&bar_drain), 1);
         s_abort = 0;
         s_n = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -295,7 +288,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 int64_t x = 0;
                 if (g < n) {
                     const int q = u.groups.start[g + 1] - u.groups.start[g];
-                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (((int64_t)u.groups.len[g] + kTok - 1) / kTok);
+                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (((int64_t)u.groups.len[g] + 127) / 128);
                 }
                 int64_t inc = x;
 #pragma unroll
@@ -314,10 +307,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     } else {
         // the union of the queries' blocks: a hash of (sequence, block) in the ring's memory,
         // then sorted by rank, so that the order does not depend on the insertions'
-        const int sets = (p.hkv + w.cta_heads - 1) / w.cta_heads;      // of K/V heads
-        seg.t0 = (int)(blockIdx.x / (sets * w.splits)) * qt;
+        seg.t0 = (int)(blockIdx.x / (p.hkv * w.splits)) * qt;
         seg.nq = (int)min((int64_t)qt, p.num_queries - seg.t0);
-        seg.c = (int)(blockIdx.x / w.splits % sets) * w.cta_heads;
+        seg.c = (int)(blockIdx.x / w.splits % p.hkv);
         if (tid < kTileQueries) {
             u.sp.len[tid] = tid < seg.nq ? max(__ldg(p.kv_len + seg.t0 + tid), 0) : 0;
             u.sp.toff[tid] = tid < seg.nq ? __ldg(p.table_offset + seg.t0 + tid) : 0;
@@ -382,7 +374,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int per_block = DENSE ? 1 : p.block_tokens / kTok;    // steps of a block
+    const int per_block = DENSE ? 1 : p.block_tokens / 128;     // 128-token tiles of a block
     if (DENSE) {
         const int64_t total = u.groups.item[p.num_groups], share = (total + gridDim.x - 1) / gridDim.x;
         dw.tab = &u.groups;
@@ -409,217 +401,213 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         seg.p0 = n * sp / w.splits;
         seg.p1 = n * (sp + 1) / w.splits;
     }
-    // first token of step v of the list, and its entry
-    auto list_step = [&](int v, int &e) -> int64_t {
-        e = per_block == 2 ? v >> 1 : v / per_block;
-        return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * kTok;
+    // first token of tile v of the list, and its entry
+    auto list_tile = [&](int v, int &e) -> int64_t {
+        e = per_block == 1 ? v : v / per_block;
+        return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * 128;
     };
+    bool once = true;
     // the next segment of this CTA
-    const int c_end = DENSE ? 0 : min(p.hkv, seg.c + w.cta_heads);
     auto next_segment = [&](bool first) -> bool {
         if (DENSE) {
             if (!first)
                 dw.next(seg);
             return dw.get(seg);
         }
-        seg.c += !first;
-        return seg.c < c_end;
-    };
-
-    // Copies of a segment's steps, by one warp: the pages of 32 / nbox steps are looked up at
-    // once, a box a lane, a batch ahead of their use.
-    const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = kTok >> lb;
-    struct Boxes {
-        int2 at;             // row in the page, page (one past the last: zeros, for a box that shows nothing)
-        int nv;              // rows that some query sees
-        bool gap;            // the history goes on without a page
-    };
-    auto look = [&](int v0) -> Boxes {
-        Boxes b = {make_int2(0, w.oob_page), 0, false};
-        const int v = v0 + (lane >> (6 - lb));
-        if (v >= seg.p1)
-            return b;
-        int64_t tok, off, len;
-        if (DENSE) {
-            tok = (int64_t)v * kTok;
-            off = __ldg(p.prefix_offset + seg.group);
-            len = seg.len;
-        } else {
-            int e;
-            tok = list_step(v, e);
-            off = u.sp.toff[u.sp.block[e] >> 24];
-            len = u.sp.maxlen[u.sp.block[e] >> 24];
-        }
-        tok += (lane & (nbox - 1)) * BR;
-        if (tok >= len)
-            return b;
-        const int32_t pg = attn_page(p, off, tok);
-        b.gap = pg < 0;
-        if (pg >= 0) {
-            b.at = make_int2(attn_page_row(p, tok), pg);
-            b.nv = (int)min((int64_t)BR, len - tok);
-        }
-        return b;
-    };
-    const int batch = 32 >> (6 - lb);
-    Boxes now, next;
-    // the boxes of step v (steps come in order), a box a lane; its gaps
-    auto boxes_of = [&](int v, int2 &at, int &nv) -> uint32_t {
-        const int k = (v - seg.p0) & (batch - 1);
-        if (v == seg.p0)
-            next = look(v);
-        if (k == 0) {
-            now = next;
-            next = look(v + batch);
-        }
-        const int from = k * nbox + (lane & (nbox - 1));
-        at = make_int2(__shfl_sync(0xffffffffu, now.at.x, from), __shfl_sync(0xffffffffu, now.at.y, from));
-        nv = __shfl_sync(0xffffffffu, now.nv, from);
-        return (__ballot_sync(0xffffffffu, now.gap) >> (k * nbox)) & ((1u << nbox) - 1u);
-    };
-    auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, int2 at) {
-#ifndef MSA_STARVE
-        if (lane == 0)
-            mbar_expect_tx(full, (uint32_t)S::kStepBytes);
-        __syncwarp();
-        if (lane < nbox)
-#pragma unroll
-            for (int k = 0; k < S::kAtoms; ++k)
-                tma_load_box(dst + (uint32_t)(k * kTok + lane * BR) * S::kSwz, map, k * (S::kSwz / (FP8 ? 1 : 2)), at.x,
-                             seg.c, at.y, full);
-#endif
-    };
-    // the copies of `n` steps have landed before the CTA finishes
-    auto drain = [&](uint64_t *full, uint32_t n) {
-#ifndef MSA_STARVE
-        for (uint32_t s = 0; s < (uint32_t)ST && s < n; ++s)
-            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), ((n - 1u - s) / ST) & 1u));
-#endif
+        const bool r = once;
+        once = false;
+        return r;
     };
 
     if (warp == 0) {
-        // ---------------- key copies and the MMAs of the scores ----------------
-        constexpr uint32_t kId = mma_idesc(FP8, 128, kTok, false, false);
-        const uint64_t q_desc = smem_desc(qsm, S::kSwz, 16u, 8u * S::kSwz);
-        const uint64_t k_desc = smem_desc(kring, S::kSwz, 16u, 8u * S::kSwz);
-        uint32_t n = 0, copied = 0, nseg = 0;         // steps of the CTA: scores made, keys asked for
+        // ---------------- copies ----------------
+        const int BR = w.box_rows, lb = __ffs(BR) - 1, nbox = 128 >> lb;
+        uint32_t it = 0;
         bool ok = true;
-        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
-            auto keys = [&](int v) {
-                int2 at;
-                int nv;
-                const uint32_t gaps = boxes_of(v, at, nv);
-                // the slot's readers, eight steps before, are done: scores that came after
-                // have been read
-                if (lane == 0) {
-                    s_gap[copied % kInfo] = gaps;
-                    mbar_arrive(smem_u32(&bar_info[copied % kInfo]));
+        for (bool first = true; ok && next_segment(first); first = false) {
+            // A batch of 32 / nbox tiles is looked up at once, a box a lane, one batch ahead:
+            // row in the page, page (one past the last for a box that shows nothing: zeros),
+            // rows that some query sees, and whether the history goes on without a page.
+            const int64_t prefix_off = DENSE ? __ldg(p.prefix_offset + seg.group) : 0;
+            const int batch = 32 >> (7 - lb);
+            auto look = [&](int v0, int2 &box, int &nv, bool &gap) {
+                box = make_int2(0, w.oob_page);
+                nv = 0;
+                gap = false;
+                const int v = v0 + (lane >> (7 - lb));
+                if (v >= seg.p1)
+                    return;
+                int64_t tok, off, len;
+                if (DENSE) {
+                    tok = (int64_t)v * 128;
+                    off = prefix_off;
+                    len = seg.len;
+                } else {
+                    int e;
+                    tok = list_tile(v, e);
+                    off = u.sp.toff[u.sp.block[e] >> 24];
+                    len = u.sp.maxlen[u.sp.block[e] >> 24];
                 }
-                copy(&kmap, kring + copied % ST * (uint32_t)S::kStepBytes, smem_u32(&bar_k_full[copied % ST]), at);
-                ++copied;
+                tok += (lane & (nbox - 1)) * BR;
+                if (tok >= len)
+                    return;
+                const int32_t pg = attn_page(p, off, tok);
+                gap = pg < 0;
+                if (pg >= 0) {
+                    box = make_int2(attn_page_row(p, tok), pg);
+                    nv = (int)min((int64_t)BR, len - tok);
+                }
             };
-            // the scores of step n - 1 have been read: they are complete, its keys are free
-            if (n > 0)
-                ok = warp_wait(smem_u32(&bar_read), (n - 1u) & 1u, abort_flag);
-            for (int v = seg.p0; v < min(seg.p1, seg.p0 + ST) && ok; ++v)
-                keys(v);
-            ok = ok && warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
-            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++n) {
-                const uint32_t s = n % ST;
-                ok = warp_wait(smem_u32(&bar_k_full[s]), (n / ST) & 1u, abort_flag);
-                if (v > seg.p0)
-                    ok = ok && warp_wait(smem_u32(&bar_read), (n - 1u) & 1u, abort_flag);
+            int2 boxes, next_boxes;
+            int nvs, next_nvs;
+            bool gaps_of, next_gaps;
+            look(seg.p0, next_boxes, next_nvs, next_gaps);
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+                const int k = (v - seg.p0) & (batch - 1);
+                if (k == 0) {
+                    boxes = next_boxes;
+                    nvs = next_nvs;
+                    gaps_of = next_gaps;
+                    look(v + batch, next_boxes, next_nvs, next_gaps);
+                }
+                const int from = k * nbox + (lane & (nbox - 1));
+                const int2 box = make_int2(__shfl_sync(0xffffffffu, boxes.x, from), __shfl_sync(0xffffffffu, boxes.y, from));
+                const int nv = __shfl_sync(0xffffffffu, nvs, from);
+                const uint32_t gaps = (__ballot_sync(0xffffffffu, gaps_of) >> (k * nbox)) & ((1u << nbox) - 1u);
+                const uint32_t s = it % ST, par = ((it / ST) & 1u) ^ 1u, slot = it % kInfo;
+                ok = warp_wait(smem_u32(&bar_k_empty[s]), par, abort_flag);
                 if (!ok)
                     break;
-                tc_fence_after();
-                const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
-                if (S::kSwz == 128) {
-                    // a swizzle atom is four MMAs; the halves, or the atoms of a row, follow
-                    mma_ss4<FP8, 2, 2>(tmem, q_desc, kd, kId, 0);
-                    if (D == 128)
-                        mma_ss4<FP8, 2, 2>(tmem, q_desc + 128 * 128 / 16, FP8 ? kd : kd + kTok * 128 / 16, kId, 1);
-                } else {
+                // the slot's last readers were done before this stage's keys were multiplied
+                if (lane < nbox)
+                    s_nv[slot][lane] = (uint8_t)nv;
+                if (lane == 0)
+                    s_gap[slot] = gaps;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bar_info[slot]));
+                auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full) {
+#ifndef MSA_STARVE
+                    if (lane == 0)
+                        mbar_expect_tx(full, (uint32_t)S::kTileBytes);
+                    __syncwarp();
+                    if (lane < nbox)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)    // two of hi, two of lo
-                        mma_ss<FP8>(tmem, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
-                                    kd + (uint64_t)((ks & 1) * 2), kId, ks > 0);
-                }
-                mma_commit(smem_u32(&bar_s[n & 1]));
-                if (v > seg.p0 && v - 1 + ST < seg.p1)
-                    keys(v - 1 + ST);
+                        for (int at = 0; at < S::kAtoms; ++at)
+                            tma_load_box(dst + (uint32_t)(at * 128 + lane * BR) * S::kSwz, map,
+                                         at * (S::kSwz / (FP8 ? 1 : 2)), box.x, seg.c, box.y, full);
+#endif
+                };
+                copy(&kmap, kring + s * (uint32_t)S::kTileBytes, smem_u32(&bar_k_full[s]));
+                ok = warp_wait(smem_u32(&bar_v_empty[s]), par, abort_flag);
+                if (!ok)
+                    break;
+                copy(&vmap, vring + s * (uint32_t)S::kTileBytes, smem_u32(&bar_v_full[s]));
             }
-            __syncwarp();
         }
         if (!ok)
             *abort_flag = 1;
-        drain(bar_k_full, copied);
-        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
-        (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
+#ifndef MSA_STARVE
+        // every copy has landed before the CTA finishes (of the last tile of an aborted
+        // CTA the values may not have been asked for; that wait runs out)
+        for (uint32_t s = 0; s < (uint32_t)ST && s < it; ++s) {
+            const uint32_t par = ((it - 1u - s) / ST) & 1u;
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), par));
+            (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_v_full[s]), par));
+        }
+        if (!ok)
+            for (uint32_t s = 0; s < (uint32_t)ST; ++s)
+                (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_k_full[s]), (it / ST) & 1u));
+#endif
     } else if (warp == 1) {
-        // ---------------- value copies and the MMAs of the values ----------------
-        constexpr uint32_t kId = mma_idesc(FP8, 128, D, false, true);
-        constexpr int kStep = (FP8 ? 32 : 16) * S::kSwz / 16;      // descriptor units of one MMA's tokens
-        const uint64_t v_desc = smem_desc(vring, S::kSwz, (uint32_t)kTok * S::kSwz, 8u * S::kSwz);
-        uint32_t n = 0, copied = 0;
+        // ---------------- MMAs ----------------
+        constexpr uint32_t kIdS = mma_idesc(FP8, 128, 64, false, false);
+        constexpr uint32_t kIdO = mma_idesc(FP8, 128, D, false, true);
+        constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step of the values
+        constexpr int kStep = kTok * S::kSwz / 16;
+        const int BR = w.box_rows, nbox = 128 / BR;
+        const uint64_t q_desc = smem_desc(qsm, S::kSwz, 16u, 8u * S::kSwz);
+        const uint64_t k_desc = smem_desc(kring, S::kSwz, 16u, 8u * S::kSwz);
+        const uint64_t v_desc = smem_desc(vring, S::kSwz, 128u * S::kSwz, 8u * S::kSwz);
+        uint32_t it = 0, nseg = 0;        // it: tiles whose values were multiplied
         bool ok = true;
-        for (bool first = true; ok && next_segment(first); first = false) {
-            // Rows past the history, in one box at most of a segment's or block's last step, may
-            // hold anything, and a weight of zero would not hide an infinity or a NaN: the rows
-            // of each box that are to be kept, of the steps asked for (8 bits each)
-            uint32_t kept[ST];
-            auto values = [&](int v) {
-                int2 at;
-                int nv;
-                boxes_of(v, at, nv);
-                copy(&vmap, vring + copied % ST * (uint32_t)S::kStepBytes, smem_u32(&bar_v_full[copied % ST]), at);
-#pragma unroll
-                for (int k = 0; k < ST; ++k)
-                    kept[k] = copied % ST == k ? (uint32_t)nv : kept[k];
-                ++copied;
-            };
-            // the values of step n - 1 are multiplied: they are free
-            if (n > 0)
-                ok = warp_wait(smem_u32(&bar_pv[(n - 1u) & 1u]), ((n - 1u) >> 1) & 1u, abort_flag);
-            for (int v = seg.p0; v < min(seg.p1, seg.p0 + ST) && ok; ++v)
-                values(v);
-            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++n) {
-                const uint32_t s = n % ST, g = n & 1u;
-                ok = warp_wait(smem_u32(&bar_v_full[s]), (n / ST) & 1u, abort_flag);
+        for (bool first = true; ok && next_segment(first); first = false, ++nseg) {
+            // the scores of half g of the CTA's tile i; `after`: right after the values of that
+            // half of tile i - 1 (the first tile of a segment comes after everything, since
+            // its queries are made when the output before was read)
+            auto scores = [&](uint32_t i, int g, bool after) {
+                const uint32_t s = i % ST;
+                if (g == 0)
+                    ok = warp_wait(smem_u32(&bar_k_full[s]), (i / ST) & 1u, abort_flag);
+                // the weights of the half before, whose place the scores take, are multiplied
+                ok = ok && (!after || warp_wait(smem_u32(&bar_pv), (uint32_t)g, abort_flag));
                 if (!ok)
-                    break;
-                uint32_t nv = kept[0];
-#pragma unroll
-                for (int k = 1; k < ST; ++k)
-                    nv = s == k ? kept[k] : nv;
-                uint32_t partial = __ballot_sync(0xffffffffu, lane < nbox && nv > 0 && nv < (uint32_t)BR);
-                if (partial) {
-                    const uint32_t vt = vring + s * (uint32_t)S::kStepBytes;
-                    while (partial) {
-                        const int b = __ffs(partial) - 1;
-                        partial &= partial - 1;
-                        const int r0 = b * BR + (int)__shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
-                        for (int k = 0; k < S::kAtoms; ++k)
-                            for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
-                                sts128(vt + (uint32_t)(k * kTok) * S::kSwz + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                ok = warp_wait(smem_u32(&bar_p[g]), (n >> 1) & 1u, abort_flag);
-                if (!ok)
-                    break;
+                    return;
                 tc_fence_after();
-                const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kStepBytes / 16));
-                const uint32_t pt = tmem + 64u + g * 32u, acc = v > seg.p0;
-                if (FP8)        // two of hi, two of lo against the same values
-                    mma_ts22<kStep>(tmem + 128u, pt, vd, kId, acc);
-                else
-                    mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kId, acc);
-                mma_commit(smem_u32(&bar_pv[g]));
-                if (v > seg.p0 && v - 1 + ST < seg.p1) {
-                    ok = warp_wait(smem_u32(&bar_pv[g ^ 1u]), ((n - 1u) >> 1) & 1u, abort_flag);
-                    if (ok)
-                        values(v - 1 + ST);
+                const uint64_t kd = k_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
+                const uint32_t d = tmem + (uint32_t)(g * 64);
+                if (S::kSwz == 128) {
+                    // a swizzle atom is four steps; the halves, or the atoms of a row, follow
+                    mma_ss4<FP8, 2, 2>(d, q_desc, kd, kIdS, 0);
+                    if (D == 128)
+                        mma_ss4<FP8, 2, 2>(d, q_desc + 128 * 128 / 16, FP8 ? kd : kd + 128 * 128 / 16, kIdS, 1);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)    // two steps of hi, two of lo
+                        mma_ss<FP8>(d, q_desc + (uint64_t)((ks >> 1) * (128 * 64 / 16) + (ks & 1) * 2),
+                                    kd + (uint64_t)((ks & 1) * 2), kIdS, ks > 0);
+                }
+                mma_commit(smem_u32(&bar_s[g]));
+                if (g == 1)
+                    mma_commit(smem_u32(&bar_k_empty[s]));
+            };
+            ok = warp_wait(smem_u32(&bar_q), nseg & 1u, abort_flag);
+            if (ok && seg.p0 < seg.p1) {
+                scores(it, 0, false);
+                if (ok)
+                    scores(it, 1, false);
+            }
+            for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
+                const uint32_t s = it % ST;
+                for (int g = 0; g < 2 && ok; ++g) {
+                    const uint32_t vt = vring + s * (uint32_t)S::kTileBytes;
+                    if (g == 0) {
+                        ok = warp_wait(smem_u32(&bar_v_full[s]), (it / ST) & 1u, abort_flag);
+                        if (!ok)
+                            break;
+                        // rows past the history may hold anything: a weight of zero would not
+                        // hide an infinity or a NaN
+                        const int nv = lane < nbox ? s_nv[it % kInfo][lane] : 0;
+                        uint32_t partial = __ballot_sync(0xffffffffu, nv > 0 && nv < BR);
+                        if (partial) {
+                            while (partial) {
+                                const int b = __ffs(partial) - 1;
+                                partial &= partial - 1;
+                                const int r0 = b * BR + __shfl_sync(0xffffffffu, nv, b), r1 = (b + 1) * BR;
+                                for (int at = 0; at < S::kAtoms; ++at)
+                                    for (int y = r0 * (S::kSwz / 16) + lane; y < r1 * (S::kSwz / 16); y += 32)
+                                        sts128(vt + (uint32_t)at * (128u * S::kSwz) + (uint32_t)y * 16u, 0u, 0u, 0u, 0u);
+                            }
+                            fence_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    ok = warp_wait(smem_u32(&bar_p[g]), it & 1u, abort_flag);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
+                    const uint32_t pt = tmem + (uint32_t)(g * 64), acc = v > seg.p0 || g > 0;
+                    if (FP8)        // two steps of hi, two of lo against the same values
+                        mma_ts22<kStep>(tmem + 128u, pt, vd, kIdO, acc);
+                    else
+                        mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kIdO, acc);
+                    mma_commit(smem_u32(&bar_pv));
+                    if (g == 1)
+                        mma_commit(smem_u32(&bar_v_empty[s]));
+                    // the half's next scores, when these values are multiplied
+                    if (v + 1 < seg.p1)
+                        scores(it + 1, g, true);
                 }
             }
             __syncwarp();
@@ -628,26 +616,24 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         }
         if (!ok)
             *abort_flag = 1;
-        drain(bar_v_full, copied);
-        mma_commit(smem_u32(&bar_drain));
+        mma_commit(smem_u32(&bar_drain));   // every MMA has completed before tensor memory is released
         (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
     } else {
         // ---------------- softmax and output ----------------
         const int quarter = warp & 3, row = quarter * 32 + lane, half = (warp - 2) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t st = lanes, pt = lanes + 64u + (uint32_t)(half * 32), ot = lanes + 128u;
+        const uint32_t st = lanes + (uint32_t)(half * 64), ot = lanes + 128u;
         const int gp = 1 << w.gp_shift, qi = row >> w.gp_shift, hi = row & (gp - 1);
+        const int BR = w.box_rows, lb = __ffs(BR) - 1;
         constexpr float kLazy = FP8 ? kLazyFp8 : kLazyBf16, kOff = FP8 ? kPOffset : 0.0f;
         constexpr int kD2 = D / 2;                      // dims of this thread
         const float nan = __int_as_float(0x7fc00000);
         // the two warps that hold a row's halves
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
-        uint32_t n = 0, nseg = 0;                       // steps of the CTA before the segment
+        uint32_t it = 0, nseg = 0;
         bool ok = true;
         for (bool first = true; next_segment(first); first = false, ++nseg) {
-            // ---- the row's query into shared memory (where the outputs before were staged) ----
-            if (!first)
-                asm volatile("bar.sync 5, 256;" ::: "memory");
+            // ---- the row's query into shared memory ----
             const bool real = qi < seg.nq && hi < p.group;
             // its row of q and out
             auto head_row = [&]() -> int64_t { return (w.q0 + seg.t0 + qi) * p.hq + seg.c * p.group + hi; };
@@ -712,78 +698,74 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 mbar_arrive(smem_u32(&bar_q));
             const int len = DENSE ? seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
             float m = -INFINITY, l = 0.0f;                 // the reference that l is relative to
-            const uint32_t n0 = n;
-            n += (uint32_t)(seg.p1 - seg.p0);
-            for (uint32_t i = n0 + ((n0 ^ (uint32_t)half) & 1u); i < n; i += 2) {
-                const int v = seg.p0 + (int)(i - n0);
-                ok = ok && warp_wait(smem_u32(&bar_info[i % kInfo]), (i / kInfo) & 1u, abort_flag);
-                // tokens of the step that the row sees, from its first
+            for (int v = seg.p0; v < seg.p1; ++v, ++it) {
+                ok = ok && warp_wait(smem_u32(&bar_info[it % kInfo]), (it / kInfo) & 1u, abort_flag);
+                // tokens of this thread's half that the row sees, from its first
                 int vis;
                 if (DENSE) {
-                    vis = len - v * kTok;
+                    vis = len - v * 128;
                 } else {
                     int e;
-                    const int64_t tok = list_step(v, e);
-                    vis = (int)max((int64_t)0, min((int64_t)kTok, len - tok));
-                    vis = (u.sp.mask[e] >> qi) & 1u ? vis : 0;
+                    const int64_t tok = list_tile(v, e);
+                    vis = (int)max((int64_t)-1, min((int64_t)128, len - tok));
+                    vis = (u.sp.mask[e] >> qi) & 1u ? vis : -1;
                 }
-                vis = real ? vis : 0;
-                const uint32_t gaps = ok ? s_gap[i % kInfo] : 0u;
-                ok = ok && warp_wait(smem_u32(&bar_s[half]), (i >> 1) & 1u, abort_flag);
+                vis = real ? vis - half * 64 : -1;
+                const uint32_t gaps = ok ? s_gap[it % kInfo] : 0u;
+                ok = ok && warp_wait(smem_u32(&bar_s[half]), it & 1u, abort_flag);
                 if (!ok)
                     break;
                 tc_fence_after();
-                uint32_t x[64];
-                tmem_ld32(st, x);
-                tmem_ld32(st + 32u, x + 32);
-                tc_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bar_read));
-                auto score = [&](int j) { return __uint_as_float(x[j]); };
+                // Two passes over the scores in tensor memory, each a loop over 32 tokens: half
+                // the instructions of one that holds 64 in registers, and the kernel is bound
+                // by fetching them.
                 float mx = -INFINITY;
                 const bool any = __any_sync(0xffffffffu, vis > 0);
-                if (any) {
-                    // rows that see all or nothing need no masks here: a row that sees
-                    // nothing takes an offset that clears its weights
-                    if (__any_sync(0xffffffffu, (vis > 0 && vis < kTok) || gaps != 0)) {
+                // rows that see all or nothing need no masks: a row that sees nothing takes an
+                // offset that clears its weights
+                const bool masks = __any_sync(0xffffffffu, (vis > 0 && vis < 64) || gaps != 0);
+                auto scores = [&](int j0, uint32_t (&x)[32]) {
+                    tmem_ld32(st + (uint32_t)j0, x);
+                    tc_wait_ld();
+                    if (masks) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (j >= vis || ((gaps >> (j >> lb)) & 1u))
+                        for (int j = 0; j < 32; ++j)
+                            if (j0 + j >= vis || ((gaps >> ((half * 64 + j0 + j) >> lb)) & 1u))
                                 x[j] = 0xff800000u;
                     }
-                    float a = max3(score(0), score(1), score(2)), b = max3(score(3), score(4), score(5));
+                };
+                if (any) {
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 64; j0 += 32) {
+                        uint32_t x[32];
+                        scores(j0, x);
+                        auto score = [&](int j) { return __uint_as_float(x[j]); };
+                        float a = max3(mx, score(0), score(1)), b = fmaxf(score(2), score(3));
 #pragma unroll
-                    for (int j = 6; j < 62; j += 4) {
-                        a = max3(a, score(j), score(j + 1));
-                        b = max3(b, score(j + 2), score(j + 3));
+                        for (int j = 4; j < 32; j += 4) {
+                            a = max3(a, score(j), score(j + 1));
+                            b = max3(b, score(j + 2), score(j + 3));
+                        }
+                        mx = fmaxf(a, b);
                     }
-                    mx = fmaxf(max3(a, score(62), score(63)), b);
                     mx = vis > 0 ? mx * qs : -INFINITY;
                 }
-                // this group's weights before are multiplied: their place is free
-                if (i >= 2) {
-                    ok = warp_wait(smem_u32(&bar_pv[half]), ((i >> 1) - 1u) & 1u, abort_flag);
-                    if (!ok)
-                        break;
-                }
-                // the reference, from the step before
+                // the reference, from the half before
                 float ref = -INFINITY;
-                if (i > n0) {
-                    ok = warp_wait(smem_u32(&bar_ref[half ^ 1][quarter]), ((i - 1u) >> 1) & 1u, abort_flag);
+                if (half > 0 || v > seg.p0) {
+                    ok = warp_wait(smem_u32(&bar_ref[half ^ 1][quarter]), (half > 0 ? it : it - 1u) & 1u, abort_flag);
                     if (!ok)
                         break;
                     ref = s_ref[row];
                 }
-                // (-inf + kLazy is -inf: the first visible step sets the reference)
+                // (-inf + kLazy is -inf: the first visible half sets the reference)
                 const bool grow = mx > ref + kLazy;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float alpha = grow ? exp2_approx(ref - mx) : 1.0f;
                     ref = grow ? mx : ref;
-                    if (i > n0) {
-                        // the values of the step before are in the output
-                        ok = warp_wait(smem_u32(&bar_pv[half ^ 1]), ((i - 1u) >> 1) & 1u, abort_flag);
+                    if (half > 0 || v > seg.p0) {
+                        // the values of the half before are in the output
+                        ok = warp_wait(smem_u32(&bar_pv), (uint32_t)(half ^ 1), abort_flag);
                         if (!ok)
                             break;
                         tc_fence_after();
@@ -806,19 +788,20 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 l = m == ref ? l : l * exp2_approx(m - ref);
                 m = ref;
                 if (any) {
-                    // (scores that are not finite of tokens the row does not see can still
-                    // make weights that are not: its output is then computed again)
                     const float off = vis > 0 && m > -INFINITY ? kOff - m : -INFINITY;
                     const uint64_t qs2 = pack2(qs, qs), off2 = pack2(off, off);
                     uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 64; j0 += 32) {
+                        uint32_t x[32];
+                        scores(j0, x);
+                        auto score = [&](int j) { return __uint_as_float(x[j]); };
+                        uint32_t hw[FP8 ? 8 : 16], lw[8];
 #pragma unroll
-                    for (int j = 0; j < 64; j += 16) {
-                        uint32_t hw[FP8 ? 4 : 8], lw[4];
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
+                        for (int e = 0; e < 32; e += 4) {
                             float p0, p1, p2, p3;
-                            unpack2(fma2(pack2(score(j + e), score(j + e + 1)), qs2, off2), p0, p1);
-                            unpack2(fma2(pack2(score(j + e + 2), score(j + e + 3)), qs2, off2), p2, p3);
+                            unpack2(fma2(pack2(score(e), score(e + 1)), qs2, off2), p0, p1);
+                            unpack2(fma2(pack2(score(e + 2), score(e + 3)), qs2, off2), p2, p3);
                             p0 = exp2_approx(p0);
                             p1 = exp2_approx(p1);
                             p2 = exp2_approx(p2);
@@ -832,11 +815,12 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                                 hw[e / 2 + 1] = bf16x2_from_f32(p2, p3);
                             }
                         }
+                        // over columns that have been read
                         if (FP8) {      // 16 columns of hi, 16 of lo
-                            tmem_st4(pt + (uint32_t)(j / 4), hw);
-                            tmem_st4(pt + 16u + (uint32_t)(j / 4), lw);
+                            tmem_st8(st + (uint32_t)(j0 / 4), hw);
+                            tmem_st8(st + 16u + (uint32_t)(j0 / 4), lw);
                         } else {
-                            tmem_st8(pt + (uint32_t)(j / 2), hw);
+                            tmem_st16(st + (uint32_t)(j0 / 2), hw);
                         }
                     }
                     float a, b;
@@ -847,8 +831,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         z[j] = 0u;
-                    tmem_st16(pt, z);
-                    tmem_st16(pt + 16u, z);
+                    tmem_st16(st, z);
+                    tmem_st16(st + 16u, z);
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -871,6 +855,14 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             l = s_row[0][row] + s_row[1][row];
             pair_sync();                              // read before the next segment writes
             const bool empty = seg.p1 <= seg.p0;
+            bool bad = !ok;                           // a row that the CTA could not finish
+            if (!DENSE && !ok) {                      // and that sees anything
+                bad = false;
+                for (int e = 0; e < s_n; ++e)
+                    bad = bad || ((u.sp.mask[e] >> qi) & 1u);
+                m = bad ? m : -INFINITY;
+                l = bad ? l : 0.0f;
+            }
             const float vs = attn_v_scale(p, seg.c);
             const bool piece = DENSE || w.splits > 1;
             const float inv = piece ? vs * (1.0f / (1 << (int)kOff)) : l == 0.0f ? 0.0f : vs / l;
@@ -906,7 +898,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 for (int e = 0; e < 16; ++e) {
                     const float y = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
                     finite = finite && fabsf(y) < INFINITY;
-                    o[e] = __float_as_uint(ok ? y : nan);
+                    o[e] = __float_as_uint(bad ? nan : y);
                 }
                 if (piece) {
                     if (real)
@@ -928,12 +920,12 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             tc_fence_before();
             if (piece) {
                 if (real && half == 0) {
-                    ml[0] = ok ? m : nan;
-                    ml[1] = ok ? l : nan;
+                    ml[0] = bad ? nan : m;
+                    ml[1] = bad ? nan : l;
                 }
             } else {
                 if (real && half == 0 && p.lse)
-                    p.lse[head_row()] = ok ? attn_lse(m, l) : nan;
+                    p.lse[head_row()] = bad ? nan : attn_lse(m, l);
                 __syncwarp();
                 constexpr int kLanes = kD2 / 8;      // 16-byte pieces of a half row
                 for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
@@ -962,10 +954,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     float acc[kD2 / 32] = {};
                     for (int v = seg.p0; v < seg.p1; ++v) {
                         int e;
-                        const int64_t tok0 = list_step(v, e);
+                        const int64_t tok0 = list_tile(v, e);
                         if (!((u.sp.mask[e] >> q2) & 1u))
                             continue;
-                        for (int j = 0; j < kTok && tok0 + j < len2; ++j) {
+                        for (int j = 0; j < 128 && tok0 + j < len2; ++j) {
                             const int32_t pg = attn_page(p, u.sp.toff[u.sp.block[e] >> 24], tok0 + j);
                             if (pg < 0)
                                 continue;

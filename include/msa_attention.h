@@ -36,8 +36,8 @@
  * they are and the weights exp(s - max) rounded to bf16; E4M3 caches are multiplied as
  * stored, against the queries and the weights each split into two E4M3 halves hi + lo
  * under a power-of-two scale (a query reproduced exactly except elements below 2^-9 of
- * the largest of its row or group of rows, a weight to 2^-8 of itself or 2^-14 of the
- * largest).  Results do not depend on which other calls run, and a call repeated with
+ * the largest of its row or group of rows, a weight to 2^-8 + 2^-12 of itself or 2^-14
+ * of the largest).  Results do not depend on which other calls run, and a call repeated with
  * the same arguments gives the same bits.
  *
  * Ownership and threading: as for msa_producer_forward.  The caller owns every buffer,

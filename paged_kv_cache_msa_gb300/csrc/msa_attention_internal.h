@@ -93,8 +93,9 @@ struct AttnTiles {
     int32_t box_rows, oob_page;
 };
 
-// One launch, with programmatic dependent launch: every kernel of these operators waits
-// for the kernels ahead of it before it touches memory, so it may always start early.
+// One launch, with programmatic dependent launch: the first kernel of a call waits for the
+// kernels ahead of it before it touches memory, and what follows starts after that, so
+// each may always start early.
 cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, cudaStream_t stream, void **args);
 
 int attn_decode_heads(int group);

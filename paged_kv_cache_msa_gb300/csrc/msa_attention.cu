@@ -332,10 +332,13 @@ AttnParams params_of(const msa_attention_cfg *cfg, int64_t T, const void *q, con
     p.hkv = cfg->num_kv_heads;
     p.group = cfg->num_q_heads / cfg->num_kv_heads;
     p.page_size = cfg->page_size;
-    p.page_shift = -1;
-    for (int sh = 0; sh < 31; ++sh)
+    p.page_shift = p.block_shift = -1;
+    for (int sh = 0; sh < 31; ++sh) {
         if ((1 << sh) == cfg->page_size)
             p.page_shift = sh;
+        if ((1 << sh) == cfg->block_tokens)
+            p.block_shift = sh;
+    }
     p.block_tokens = cfg->block_tokens;
     p.topk = cfg->topk;
     p.per_head_scales = cfg->scale_mode == MSA_SCALE_PER_HEAD;

@@ -597,7 +597,6 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             if (p.topk_ids && list_q != wk.q) {
                 // the ids that name a block, in order; a repeated one is kept as -1
                 list_q = wk.q;
-                const int64_t nb = (len + p.block_tokens - 1) / p.block_tokens;
                 int32_t a0 = -1, a1 = -1;
                 if (nq * p.topk <= kSmallIds) {
                     a0 = lane < p.topk ? s_ids[wk.q * p.topk + lane] : -1;
@@ -607,20 +606,17 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     a0 = lane < p.topk ? __ldg(ids + lane) : -1;
                     a1 = lane + 32 < p.topk ? __ldg(ids + lane + 32) : -1;
                 }
-                const bool v0 = a0 >= 0 && a0 < nb, v1 = a1 >= 0 && a1 < nb;
+                const bool v0 = a0 >= 0 && (int64_t)a0 * p.block_tokens < len;
+                const bool v1 = a1 >= 0 && (int64_t)a1 * p.block_tokens < len;
                 const uint32_t m0 = __ballot_sync(0xffffffffu, v0), m1 = __ballot_sync(0xffffffffu, v1);
                 const uint32_t below = (1u << lane) - 1u;
-                bool dup0 = false, dup1 = false;       // of an id before it
-                for (int i = 0; i < min(p.topk, 32); ++i) {
-                    const int32_t x = __shfl_sync(0xffffffffu, a0, i);
-                    dup0 |= i < lane && x == a0;
-                    dup1 |= x == a1;
+                const bool dup0 = __match_any_sync(0xffffffffu, a0) & below;       // of an id before it
+                bool dup1 = false;
+                if (p.topk > 32) {
+                    dup1 = __match_any_sync(0xffffffffu, a1) & below;
+                    for (int i = 0; i < 32; ++i)
+                        dup1 |= __shfl_sync(0xffffffffu, a0, i) == a1;
                 }
-                for (int i = 32; i < p.topk; ++i) {
-                    const int32_t x = __shfl_sync(0xffffffffu, a1, i - 32);
-                    dup1 |= i < lane + 32 && x == a1;
-                }
-                __syncwarp();
                 if (v0)
                     s_list[__popc(m0 & below)] = dup0 ? -1 : a0;
                 if (v1)
@@ -634,7 +630,8 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                 int64_t j = v;
                 bool in = true;
                 if (p.topk_ids) {
-                    const int64_t k = (uint32_t)v / (uint32_t)p.block_tokens;   // below 64 * 1024 tokens
+                    const int64_t k = p.block_shift >= 0 ? (uint32_t)v >> p.block_shift
+                                                         : (uint32_t)v / (uint32_t)p.block_tokens;   // below 64 * 1024 tokens
                     const int32_t id = k < cnt ? s_list[k] : -1;
                     in = id >= 0;
                     j = (int64_t)id * p.block_tokens + (v - k * p.block_tokens);

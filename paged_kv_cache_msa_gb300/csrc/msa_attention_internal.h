@@ -42,6 +42,7 @@ struct AttnParams {
     int32_t page_size;
     int32_t page_shift;              // log2(page_size) when a power of two, else -1
     int32_t block_tokens, topk;
+    int32_t block_shift;             // as page_shift
     int32_t per_head_scales;
     float scale_log2;                // softmax_scale * log2(e): scores are kept as powers of two
 };
@@ -127,8 +128,8 @@ __device__ __forceinline__ float attn_v_scale(const AttnParams &p, int c)
 // The page of token j of the history whose table row starts at `off`, or -1.
 __device__ __forceinline__ int32_t attn_page(const AttnParams &p, int64_t off, int64_t j)
 {
-    const int64_t blk = p.page_shift >= 0 ? (j >> p.page_shift) : j / p.page_size;
-    const int64_t i = off + blk;
+    const uint32_t tok = (uint32_t)j;      // below 2^31
+    const int64_t i = off + (p.page_shift >= 0 ? tok >> p.page_shift : tok / (uint32_t)p.page_size);
     if (i < 0 || i >= p.page_table_len)
         return -1;
     const int32_t pg = __ldg(p.page_table + i);
@@ -137,7 +138,8 @@ __device__ __forceinline__ int32_t attn_page(const AttnParams &p, int64_t off, i
 
 __device__ __forceinline__ int32_t attn_page_row(const AttnParams &p, int64_t j)
 {
-    return (int32_t)(p.page_shift >= 0 ? (j & (p.page_size - 1)) : j % p.page_size);
+    const uint32_t tok = (uint32_t)j;
+    return (int32_t)(p.page_shift >= 0 ? tok & (uint32_t)(p.page_size - 1) : tok % (uint32_t)p.page_size);
 }
 
 // two E4M3 codes -> (low code, high code)

@@ -25,7 +25,7 @@ namespace {
 // 8 elements of 16 bits at a time, the alignment that every accepted layout has.  It
 // is bound by its fp32 multiply-adds and serves the layouts that the tensor-core
 // kernels do not take: 64 queries of 16 blocks (64 heads on 8 of 128 dims, E4M3) take it
-// 449 us (the decode kernel 52.5), 8,192 prefill queries 28.7 ms (0.96).
+// 449 us (the decode kernel 52.5), 8,192 prefill queries 28.7 ms (0.93).
 constexpr int kRowThreads = 128;
 constexpr int kRowHeads = 8;
 
@@ -629,7 +629,7 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
         return launch_rows(p, cfg->head_dim, stream);
     const Layout l = layout_of(cfg, num_queries, 0);
     // A tile of the tile kernel lies in one block.  The hint is the caller's, who knows
-    // the queries: 8,192 prefill queries 0.96 ms (4.6 as single queries), 333 77 us (197);
+    // the queries: 8,192 prefill queries 0.93 ms (4.6 as single queries), 333 73 us (197);
     // 64 unrelated ones 85 us (52 as single queries).
     if ((launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % kAttnTokens == 0)
         return run_query_runs(p, maps, l, cfg->head_dim, workspace, stream);

@@ -18,14 +18,15 @@
 // one half are ready while the other's softmax runs, and two CTAs share an SM (half the
 // tensor memory and half the shared memory each).
 // Measured: 8,192 prefill queries in four chunks (64 query heads on 8 of 128 dims, E4M3, 16
-// blocks of 128 tokens each) 0.96 ms, 0.29 of the measured bf16 rate by the tokens that the
+// blocks of 128 tokens each) 0.93 ms, 0.30 of the measured bf16 rate by the tokens that the
 // queries selected.  A tile of 16 queries runs over the union of their lists, 19 to 27
 // blocks, so a third of the products is masked.  Bound by instructions: 55 % of the issue
 // slots, 50 % of the ALU's (the split of the weights is 12 of about 22 instructions for
 // four tokens), tensor pipe 42 %, DRAM 4 %.  What was slower: all 64 scores of a row held
 // in registers (1.04 ms), 64-token tiles with weights beside the scores (1.08), 128-token
 // scores in one MMA group (1.11 to 1.17), separate warps for the two products (1.16).
-// 64 queries behind 8,192 shared tokens: 73 us with their own tokens and the join.
+// About 15,000 of the 130,000 cycles of a CTA go by before its first scores.
+// 64 queries behind 8,192 shared tokens: 71 us with their own tokens and the join.
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
 // output in tensor memory rescaled, which few tiles after the first need.  The groups hand
@@ -409,9 +410,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         seg.p1 = n * (sp + 1) / w.splits;
     }
     // first token of tile v of the list, and its entry
-    auto list_tile = [&](int v, int &e) -> int64_t {
+    auto list_tile = [&](int v, int &e) -> uint32_t {
         e = per_block == 1 ? v : v / per_block;
-        return (int64_t)(u.sp.block[e] & 0xFFFFFF) * p.block_tokens + (v - e * per_block) * 128;
+        return (uint32_t)(u.sp.block[e] & 0xFFFFFF) * (uint32_t)p.block_tokens + (uint32_t)(v - e * per_block) * 128u;
     };
     bool once = true;
     // the next segment of this CTA
@@ -432,50 +433,45 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         uint32_t it = 0;
         bool ok = true;
         for (bool first = true; ok && next_segment(first); first = false) {
-            // A batch of 32 / nbox tiles is looked up at once, a box a lane, one batch ahead:
-            // row in the page, page (one past the last for a box that shows nothing: zeros),
-            // rows that some query sees, and whether the history goes on without a page.
+            // A batch of 32 / nbox tiles is looked up at once, a box a lane: row in the page, page
+            // (one past the last for a box that shows nothing: zeros), rows that some query
+            // sees, and whether the history goes on without a page.  The ring hides the wait.
             const int64_t prefix_off = DENSE ? __ldg(p.prefix_offset + seg.group) : 0;
             const int batch = 32 >> (7 - lb);
-            auto look = [&](int v0, int2 &box, int &nv, bool &gap) {
-                box = make_int2(0, w.oob_page);
-                nv = 0;
-                gap = false;
-                const int v = v0 + (lane >> (7 - lb));
-                if (v >= seg.p1)
-                    return;
-                int64_t tok, off, len;
-                if (DENSE) {
-                    tok = (int64_t)v * 128;
-                    off = prefix_off;
-                    len = seg.len;
-                } else {
-                    int e;
-                    tok = list_tile(v, e);
-                    off = u.sp.toff[u.sp.block[e] >> 24];
-                    len = u.sp.maxlen[u.sp.block[e] >> 24];
-                }
-                tok += (lane & (nbox - 1)) * BR;
-                if (tok >= len)
-                    return;
-                const int32_t pg = attn_page(p, off, tok);
-                gap = pg < 0;
-                if (pg >= 0) {
-                    box = make_int2(attn_page_row(p, tok), pg);
-                    nv = (int)min((int64_t)BR, len - tok);
-                }
-            };
-            int2 boxes, next_boxes;
-            int nvs, next_nvs;
-            bool gaps_of, next_gaps;
-            look(seg.p0, next_boxes, next_nvs, next_gaps);
+            int2 boxes = make_int2(0, 0);
+            int nvs = 0;
+            bool gaps_of = false;
             for (int v = seg.p0; v < seg.p1 && ok; ++v, ++it) {
                 const int k = (v - seg.p0) & (batch - 1);
                 if (k == 0) {
-                    boxes = next_boxes;
-                    nvs = next_nvs;
-                    gaps_of = next_gaps;
-                    look(v + batch, next_boxes, next_nvs, next_gaps);
+                    boxes = make_int2(0, w.oob_page);
+                    nvs = 0;
+                    gaps_of = false;
+                    const int x = v + (lane >> (7 - lb));
+                    if (x < seg.p1) {
+                        uint32_t tok, len;
+                        int64_t off;
+                        if (DENSE) {
+                            tok = (uint32_t)x * 128u;
+                            off = prefix_off;
+                            len = (uint32_t)seg.len;
+                        } else {
+                            int e;
+                            tok = list_tile(x, e);
+                            off = u.sp.toff[u.sp.block[e] >> 24];
+                            len = (uint32_t)u.sp.maxlen[u.sp.block[e] >> 24];
+                        }
+                        tok += (uint32_t)((lane & (nbox - 1)) * BR);
+                        if (tok < len) {
+                            const int32_t pg = attn_page(p, off, tok);
+                            gaps_of = pg < 0;
+                            if (pg >= 0) {
+                                boxes = make_int2(attn_page_row(p, tok), pg);
+                                nvs = (int)min((uint32_t)BR, len - tok);
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
                 const int from = k * nbox + (lane & (nbox - 1));
                 const int2 box = make_int2(__shfl_sync(0xffffffffu, boxes.x, from), __shfl_sync(0xffffffffu, boxes.y, from));
@@ -637,65 +633,78 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         const float nan = __int_as_float(0x7fc00000);
         // the two warps that hold a row's halves
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
+        auto softmax_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
         uint32_t it = 0, nseg = 0;
         bool ok = true;
         for (bool first = true; next_segment(first); first = false, ++nseg) {
-            // ---- the row's query into shared memory ----
+            // ---- the queries into shared memory: 16 rows a warp, 16 bytes a lane ----
             const bool real = qi < seg.nq && hi < p.group;
-            // its row of q and out
-            auto head_row = [&]() -> int64_t { return (w.q0 + seg.t0 + qi) * p.hq + seg.c * p.group + hi; };
+            // a row of q and out
+            auto head_row_of = [&](int r) -> int64_t {
+                return (w.q0 + seg.t0 + (r >> w.gp_shift)) * p.hq + seg.c * p.group + (r & (gp - 1));
+            };
+            auto head_row = [&]() -> int64_t { return head_row_of(row); };
             const float ks = attn_k_scale(p, seg.c) * p.scale_log2;
             float qs = fabsf(ks);                          // a negative scale goes into the query
+            softmax_sync();                                // everyone is through with the segment before
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + head_row() * D) + half * (kD2 / 8);
+                constexpr int kLanes = D / 8, kRows = 32 / kLanes;      // lanes of a row, rows of a load
                 const uint32_t flip = ks < 0.0f ? 0x80008000u : 0u;
-                uint32_t xs[kD2 / 2];
+                const int chunk = lane % kLanes;
 #pragma unroll
-                for (int i = 0; i < kD2 / 8; ++i) {
-                    const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    xs[4 * i] = x.x ^ flip;
-                    xs[4 * i + 1] = x.y ^ flip;
-                    xs[4 * i + 2] = x.z ^ flip;
-                    xs[4 * i + 3] = x.w ^ flip;
-                }
-                float sc = 1.0f;
-                if (FP8) {
-                    // halves hi | lo under the power of two that brings the row's largest
-                    // magnitude (magnitudes compare as integers) into [128, 256)
-                    uint32_t big = 0;
+                for (int i = 0; i < 16 / kRows; i += 4) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int i = 0; i < kD2 / 2; ++i)
-                        big = max(big, max((xs[i] & 0x7FFFu) << 16, xs[i] & 0x7FFF0000u));
-                    s_row[half][row] = __uint_as_float(big);
-                    pair_sync();
-                    big = max(big, __float_as_uint(s_row[half ^ 1][row])) >> 23;
-                    const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
-                    sc = __int_as_float((e2 + 127) << 23);
-                    qs *= __int_as_float((127 - e2) << 23);
-                }
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = (warp - 2) * 16 + (i + j) * kRows + lane / kLanes;
+                        const bool there = (r >> w.gp_shift) < seg.nq && (r & (gp - 1)) < p.group;
+                        x[j] = there ? __ldg(reinterpret_cast<const uint4 *>(p.q + head_row_of(r) * D) + chunk)
+                                     : make_uint4(0, 0, 0, 0);
+                    }
+                    // (the loads of four rows at once, then a loop that is short to fetch)
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = (warp - 2) * 16 + (i + j) * kRows + lane / kLanes;
+                        const uint4 y = x[0];
+                        x[0] = x[1];
+                        x[1] = x[2];
+                        x[2] = x[3];
+                        const uint32_t xs[4] = {y.x ^ flip, y.y ^ flip, y.z ^ flip, y.w ^ flip};
+                        if (FP8) {
+                            // halves hi | lo under the power of two that brings the row's largest
+                            // magnitude (magnitudes compare as integers) into [128, 256)
+                            uint32_t big = 0;
 #pragma unroll
-                for (int i = 0; i < kD2 / 8; ++i) {
-                    const int chunk = half * (kD2 / 8) + i;
-                    if (FP8) {
-                        uint32_t hw[2], lw[2];
+                            for (int k = 0; k < 4; ++k)
+                                big = max(big, max((xs[k] & 0x7FFFu) << 16, xs[k] & 0x7FFF0000u));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x0 = __uint_as_float(xs[4 * i + j] << 16) * sc;
-                            const float x1 = __uint_as_float(xs[4 * i + j] & 0xFFFF0000u) * sc;
-                            const uint32_t h = e4m3x2_from_f32(x0, x1);
-                            const float2 d = attn_e4m3x2_to_f2(h);
-                            const uint32_t l = e4m3x2_from_f32(x0 - d.x, x1 - d.y);
-                            hw[j / 2] = j & 1 ? hw[j / 2] | (h << 16) : h;
-                            lw[j / 2] = j & 1 ? lw[j / 2] | (l << 16) : l;
+                            for (int o = kLanes / 2; o > 0; o >>= 1)
+                                big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            big >>= 23;
+                            const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
+                            const float sc = __int_as_float((e2 + 127) << 23);
+                            uint32_t hw[2], lw[2];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float x0 = __uint_as_float(xs[k] << 16) * sc;
+                                const float x1 = __uint_as_float(xs[k] & 0xFFFF0000u) * sc;
+                                const uint32_t h = e4m3x2_from_f32(x0, x1);
+                                const float2 d = attn_e4m3x2_to_f2(h);
+                                const uint32_t l = e4m3x2_from_f32(x0 - d.x, x1 - d.y);
+                                hw[k / 2] = k & 1 ? hw[k / 2] | (h << 16) : h;
+                                lw[k / 2] = k & 1 ? lw[k / 2] | (l << 16) : l;
+                            }
+                            const uint32_t a = swizzle<S::kSwz>((uint32_t)(r * S::kSwz + chunk * 8));
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + a), "r"(hw[0]), "r"(hw[1]) : "memory");
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + 128 * D + a), "r"(lw[0]), "r"(lw[1])
+                                         : "memory");
+                            if (chunk == 0)
+                                s_row[0][r] = __int_as_float((127 - e2) << 23);
+                        } else {
+                            const uint32_t byte = (uint32_t)chunk * 16, at = byte / S::kSwz, col = byte % S::kSwz;
+                            sts128(qsm + at * (128u * S::kSwz) + swizzle<S::kSwz>((uint32_t)r * S::kSwz + col), xs[0], xs[1],
+                                   xs[2], xs[3]);
                         }
-                        const uint32_t a = swizzle<S::kSwz>((uint32_t)(row * S::kSwz + chunk * 8));
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + a), "r"(hw[0]), "r"(hw[1]) : "memory");
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + 128 * D + a), "r"(lw[0]), "r"(lw[1])
-                                     : "memory");
-                    } else {
-                        const uint32_t byte = (uint32_t)chunk * 16, at = byte / S::kSwz, col = byte % S::kSwz;
-                        sts128(qsm + at * (128u * S::kSwz) + swizzle<S::kSwz>((uint32_t)row * S::kSwz + col), xs[4 * i],
-                               xs[4 * i + 1], xs[4 * i + 2], xs[4 * i + 3]);
                     }
                 }
             }
@@ -703,6 +712,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_u32(&bar_q));
+            if (FP8) {
+                softmax_sync();
+                qs *= s_row[0][row];
+            }
             const int len = DENSE ? seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
             float m = -INFINITY, l = 0.0f;                 // the reference that l is relative to
             for (int v = seg.p0; v < seg.p1; ++v, ++it) {
@@ -713,9 +726,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     vis = len - v * 128;
                 } else {
                     int e;
-                    const int64_t tok = list_tile(v, e);
-                    vis = (int)max((int64_t)-1, min((int64_t)128, len - tok));
-                    vis = (u.sp.mask[e] >> qi) & 1u ? vis : -1;
+                    // a row sees the first token of a block that its query selected
+                    const uint32_t tok = list_tile(v, e);
+                    vis = (u.sp.mask[e] >> qi) & 1u ? (int)((uint32_t)len - tok) : -1;
                 }
                 vis = real ? vis - half * 64 : -1;
                 const uint32_t gaps = ok ? s_gap[it % kInfo] : 0u;
@@ -874,21 +887,20 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             const bool piece = DENSE || w.splits > 1;
             const float inv = piece ? vs * (1.0f / (1 << (int)kOff)) : l == 0.0f ? 0.0f : vs / l;
             l *= 1.0f / (1 << (int)kOff);             // the sum itself
-            float *dst = nullptr, *ml = nullptr;
+            float *slot = nullptr, *dst = nullptr, *ml = nullptr;
+            // output of row r of a piece
+            auto piece_row = [&](int r) -> float * {
+                return DENSE && seg.whole ? w.rows + (head_row_of(r) - w.q0 * p.hq) * (D + 4) : slot + r * D;
+            };
             if (piece) {
-                if (DENSE && seg.whole) {
-                    dst = w.rows + ((int64_t)(seg.t0 + qi) * p.hq + seg.c * p.group + hi) * (D + 4);
-                    ml = dst + D;
-                } else {
-                    const int64_t sl = DENSE ? (seg.began ? (int64_t)gridDim.x : 0) + blockIdx.x : (int64_t)blockIdx.x;
-                    float *base = w.pieces + sl * (int64_t)(128 * (D + 2));
-                    dst = base + row * D;
-                    ml = base + 128 * D + 2 * row;
-                }
+                const int64_t sl = DENSE ? (seg.began ? (int64_t)gridDim.x : 0) + blockIdx.x : (int64_t)blockIdx.x;
+                slot = w.pieces + sl * (int64_t)(128 * (D + 2));
+                dst = piece_row(row);
+                ml = DENSE && seg.whole ? dst + D : slot + 128 * D + 2 * row;
                 dst += half * kD2;
             }
             bool finite = true;
-            // this warp's half rows, in the query tile, which no MMA reads any more
+            // this warp's place for its half rows, in the query tile, which no MMA reads any more
             const uint32_t stage = qsm + (uint32_t)((half * 4 + quarter) * 32 * kD2 * 2);
 #pragma unroll 1
             for (int j = 0; j < kD2; j += 16) {
@@ -908,12 +920,23 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     o[e] = __float_as_uint(bad ? nan : y);
                 }
                 if (piece) {
-                    if (real)
+                    // 16 dims of 32 rows, through shared memory: four lanes a row
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4 *>(dst + j + e) =
-                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                            __uint_as_float(o[e + 3]));
+                    for (int e = 0; e < 16; e += 4)
+                        sts128(stage + (uint32_t)(lane * 64 + (((e / 4) ^ ((lane >> 1) & 3)) << 4)), o[e], o[e + 1], o[e + 2],
+                               o[e + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = lane / 4; k < 32; k += 8) {
+                        const int r = quarter * 32 + k;
+                        uint4 y;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                     : "r"(stage + (uint32_t)(k * 64 + (((lane & 3) ^ ((k >> 1) & 3)) << 4))));
+                        if ((r >> w.gp_shift) < seg.nq && (r & (gp - 1)) < p.group)
+                            *reinterpret_cast<uint4 *>(piece_row(r) + half * kD2 + j + (lane & 3) * 4) = y;
+                    }
+                    __syncwarp();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; e += 8)
@@ -961,7 +984,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     float acc[kD2 / 32] = {};
                     for (int v = seg.p0; v < seg.p1; ++v) {
                         int e;
-                        const int64_t tok0 = list_tile(v, e);
+                        const int64_t tok0 = (int64_t)list_tile(v, e);
                         if (!((u.sp.mask[e] >> q2) & 1u))
                             continue;
                         for (int j = 0; j < 128 && tok0 + j < len2; ++j) {

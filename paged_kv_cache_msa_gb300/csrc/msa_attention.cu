@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kRowThreads) msa_attention_rows_kernel(const _
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int32_t own = max(p.kv_len[t], 0);
+    const int32_t own = attn_len(p, p.kv_len[t], p.table_offset[t]);
     if (tid == 0) {
         s_group = 0x7fffffff;
         s_n = 0;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kRowThreads) msa_attention_rows_kernel(const _
     const bool has_prefix = g >= 0 && g < p.num_groups;
     for (int part = has_prefix ? 0 : 1; part < 2; ++part) {
         const int64_t off = part == 0 ? p.prefix_offset[g] : p.table_offset[t];
-        const int64_t len = part == 0 ? max(p.prefix_len[g], 0) : own;
+        const int64_t len = part == 0 ? attn_len(p, p.prefix_len[g], off) : own;
         const bool sparse = p.topk_ids != nullptr;
         const int64_t total = sparse ? (int64_t)s_n * p.block_tokens : len;
         for (int64_t v0 = 0; v0 < total; v0 += kRowThreads) {

@@ -125,6 +125,17 @@ __device__ __forceinline__ float attn_v_scale(const AttnParams &p, int c)
     return p.v.fp8 ? __ldg(p.scales + (p.per_head_scales ? p.hkv + c : 1)) : 1.0f;
 }
 
+// The tokens of a history of `len` whose table row starts at `off`, without those past the
+// table's end, which no query sees: no length makes a kernel walk further.
+__device__ __forceinline__ int32_t attn_len(const AttnParams &p, int32_t len, int64_t off)
+{
+    constexpr int64_t kFar = (int64_t)1 << 31;       // past any length
+    if (len <= 0 || off >= p.page_table_len || off <= -kFar)
+        return 0;
+    const int64_t pages = p.page_table_len - off;
+    return pages >= kFar ? len : (int32_t)min((int64_t)len, pages * p.page_size);
+}
+
 // The page of token j of the history whose table row starts at `off`, or -1.
 __device__ __forceinline__ int32_t attn_page(const AttnParams &p, int64_t off, int64_t j)
 {

@@ -276,7 +276,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 const int g = g0 + lane;
                 int64_t e64 = g <= n ? (int64_t)__ldg(p.group_start + g) - w.q0 : 0;
                 int32_t e = (int32_t)max((int64_t)0, min(e64, w.nq));
-                const int32_t len = g < n ? max(__ldg(p.prefix_len + g), 0) : 0;
+                const int32_t len = g < n ? attn_len(p, __ldg(p.prefix_len + g), __ldg(p.prefix_offset + g)) : 0;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int32_t x = __shfl_up_sync(0xffffffffu, e, o);

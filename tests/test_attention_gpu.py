@@ -1,4 +1,5 @@
 """The attention operators against their definition in 64 bits (GPU)."""
+import numpy as np
 import pytest
 import torch
 
@@ -388,3 +389,32 @@ def test_a_decode_layer_end_to_end():
     assert torch.equal(a[8:], b[8:]) or (a[8:].view(torch.bfloat16).double() - b[8:].view(torch.bfloat16).double()).abs().max() <= 2.0 ** -7 * b.view(torch.bfloat16).abs().max()
     assert not torch.equal(a[:8], b[:8])
     assert torch.isfinite(a.view(torch.bfloat16)).all()
+
+
+@pytest.mark.parametrize("layout", ["hnd", "odd"])
+@pytest.mark.parametrize("kind", ["decode", "runs", "dense", "prefix"])
+def test_lengths_past_the_table(kind, layout):
+    """Tokens whose table index lies past the table are not visible, however long the
+    history is said to be; neither are those before it."""
+    kw = dict(prefixes=(700,), groups=(0, 3), ids=None) if kind == "prefix" else dict(ids=None) if kind == "dense" else {}
+    lens = (300, 640, 90, 500)
+    p = Problem(51, lens=lens, layout=layout, **kw)
+    n = p.table.numel() * p.page
+    # what the table holds after the start of a row, and the length that says more
+    p.lens = torch.tensor([n - int(o) * p.page for o in p.toff], dtype=torch.int32)
+    p.toff[2] = -3                                    # three pages before the table
+    p.lens[2] = 200 + 3 * p.page
+    if p.groups is not None:
+        p.prefixes = torch.tensor([n - int(p.poff[0]) * p.page], dtype=torch.int32)
+    # every cell that may be seen now is written
+    raw_k, raw_v = p._raw(p.k), p._raw(p.v)
+    for raw in (raw_k, raw_v):
+        raw[(raw & 0x7F) == 0x7F] = 0x11
+    if p.ids is not None:
+        p.ids = p._ids(np.random.default_rng(52), "random")
+    ref = p.reference()
+    p.lens = torch.where(torch.arange(4) == 2, p.lens, torch.tensor(2**31 - 1, dtype=torch.int32))
+    if p.groups is not None:
+        p.prefixes = torch.tensor([2**31 - 1], dtype=torch.int32)
+    flags = B.MSA_LAUNCH_QUERY_RUNS if kind == "runs" else 0
+    p.device().run(flags).check(ref)

@@ -479,11 +479,10 @@ def forward_tensors(cfg: MsaProducerCfg, qkv, positions, slot_mapping, page_tabl
 
 def _tensor(name, t, shape, dtypes, device):
     """Checks a tensor argument of the attention calls: shape, dtype, contiguous, on
-    ``device``; returns its address (None for None).  A small call's time is mostly these
-    checks on the host: about 0.4 us each."""
+    ``device``; returns its address (None for None)."""
     if t is None:
         return None
-    if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
         return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, q on {device}")
@@ -491,19 +490,28 @@ def _tensor(name, t, shape, dtypes, device):
                      f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
 
 
-def _attention_call(forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse, workspace,
-                    num_groups, launch_flags, stream):
-    """Checks the tensors both attention operators have and calls ``forward`` with them on
-    q's device; ``tensors(i32, i64, dev)`` gives the arguments between q and the caches."""
-    import torch
+_attention_types = None      # torch, and the dtypes of q and out, int32, int64, fp32
+
+
+def _on_device(q):
+    """The types and q's device; the latter's context when it is not the current one."""
+    global _attention_types
+    if _attention_types is None:
+        import torch
+        _attention_types = (torch, (torch.bfloat16, torch.int16), (torch.int32,), (torch.int64,),
+                            (torch.float32,))
     dev = q.device
     if dev.type != "cuda":
         raise ValueError(f"q is on {dev}; the attention calls take CUDA tensors")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _attention_call(forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse,
-                                   workspace, num_groups, launch_flags, stream)
-    bf16, i32, i64, f32 = (torch.bfloat16, torch.int16), (torch.int32,), (torch.int64,), (torch.float32,)
+    cuda = _attention_types[0].cuda
+    return dev, None if cuda.current_device() == dev.index else cuda.device(dev)
+
+
+def _attention_tail(cfg, q, dev, scales, out, lse, workspace, num_groups, launch_flags, stream):
+    """Checks what both attention operators have and returns the addresses of q and
+    scales, and the arguments from ``out`` on.  The host's time is a small call's time:
+    about 0.4 us for each tensor's checks."""
+    torch, bf16, i32, i64, f32 = _attention_types
     T, heads = q.shape[0], cfg.num_q_heads
     rows = (T, heads, cfg.head_dim)
     if scales is not None:
@@ -519,9 +527,9 @@ def _attention_call(forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse
         raise ValueError(f"workspace: expected a contiguous tensor on {dev}, got one on {workspace.device}")
     # the handle alone: torch.cuda.current_stream builds a stream object in 2 us
     handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    forward(cfg, T, _tensor("q", q, rows, bf16, dev), *tensors(i32, i64, dev), k_cache, v_cache,
-            scales, _tensor("out", out, rows, bf16, dev), _tensor("lse", lse, (T, heads), f32, dev),
-            workspace.data_ptr() or None, workspace.nbytes, launch_flags, handle)
+    return (_tensor("q", q, rows, bf16, dev), scales,
+            (_tensor("out", out, rows, bf16, dev), _tensor("lse", lse, (T, heads), f32, dev),
+             workspace.data_ptr() or None, workspace.nbytes, launch_flags, handle))
 
 
 def sparse_attention_tensors(cfg: MsaAttentionCfg, q, topk_ids, kv_len, table_offset, page_table,
@@ -531,14 +539,19 @@ def sparse_attention_tensors(cfg: MsaAttentionCfg, q, topk_ids, kv_len, table_of
     MsaCacheDesc).  ``workspace``: a tensor of at least
     ``msa_attention_workspace_bytes(cfg, T)`` bytes, or None to allocate one.  Runs on
     ``stream`` or the current stream of q's device."""
-    def tensors(i32, i64, dev):
-        T = (q.shape[0],)
-        return (_tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
-                _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel(),
-                _tensor("topk_ids", topk_ids, (T[0], cfg.topk), i32, dev))
-
-    _attention_call(msa_sparse_attention_forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse,
-                    workspace, 0, launch_flags, stream)
+    dev, other = _on_device(q)
+    if other is not None:
+        with other:
+            return sparse_attention_tensors(cfg, q, topk_ids, kv_len, table_offset, page_table, k_cache,
+                                            v_cache, scales, out, lse, workspace, launch_flags, stream)
+    _, _, i32, i64, _ = _attention_types
+    q_ptr, scales, rest = _attention_tail(cfg, q, dev, scales, out, lse, workspace, 0, launch_flags, stream)
+    n = q.shape[0]
+    T = (n,)
+    msa_sparse_attention_forward(
+        cfg, n, q_ptr, _tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
+        _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel(),
+        _tensor("topk_ids", topk_ids, (n, cfg.topk), i32, dev), k_cache, v_cache, scales, *rest)
 
 
 def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, prefix_offset, kv_len,
@@ -547,15 +560,20 @@ def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, p
     """msa_prefix_attention_forward on contiguous torch CUDA tensors; the three group
     tensors are None when no prefix is shared.  ``workspace`` and ``stream`` as for
     ``sparse_attention_tensors`` (the bytes also depend on the number of groups)."""
-    n = 0 if prefix_len is None else prefix_len.shape[0]
-
-    def tensors(i32, i64, dev):
-        T = (q.shape[0],)
-        return (n, _tensor("group_start", group_start, (n + 1,), i32, dev),
-                _tensor("prefix_len", prefix_len, (n,), i32, dev),
-                _tensor("prefix_offset", prefix_offset, (n,), i64, dev),
-                _tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
-                _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel())
-
-    _attention_call(msa_prefix_attention_forward, cfg, q, tensors, k_cache, v_cache, scales, out, lse,
-                    workspace, n, launch_flags, stream)
+    dev, other = _on_device(q)
+    if other is not None:
+        with other:
+            return prefix_attention_tensors(cfg, q, group_start, prefix_len, prefix_offset, kv_len,
+                                            table_offset, page_table, k_cache, v_cache, scales, out, lse,
+                                            workspace, launch_flags, stream)
+    _, _, i32, i64, _ = _attention_types
+    g = 0 if prefix_len is None else prefix_len.shape[0]
+    q_ptr, scales, rest = _attention_tail(cfg, q, dev, scales, out, lse, workspace, g, launch_flags, stream)
+    n = q.shape[0]
+    T = (n,)
+    msa_prefix_attention_forward(
+        cfg, n, q_ptr, g, _tensor("group_start", group_start, (g + 1,), i32, dev),
+        _tensor("prefix_len", prefix_len, (g,), i32, dev), _tensor("prefix_offset", prefix_offset, (g,), i64, dev),
+        _tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
+        _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel(),
+        k_cache, v_cache, scales, *rest)

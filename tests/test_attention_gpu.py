@@ -418,3 +418,23 @@ def test_lengths_past_the_table(kind, layout):
         p.prefixes = torch.tensor([2**31 - 1], dtype=torch.int32)
     flags = B.MSA_LAUNCH_QUERY_RUNS if kind == "runs" else 0
     p.device().run(flags).check(ref)
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("kind", ["decode", "runs", "prefix"])
+def test_zero_queries_and_negative_scales(kind, dtype):
+    """A query of zeros weighs its tokens alike; a negative key scale turns the scores."""
+    kw = dict(prefixes=(300,), groups=(0, 5), ids=None) if kind == "prefix" else {}
+    p = Problem(61, lens=(500, 130, 700, 0, 129), seq_of=(0, 1, 1, 1, 0), dtype=dtype, **kw)
+    p.q[1] = 0.0
+    p.q[2, 3:6] = 0.0                                 # some heads of a group
+    p.scales = -p.scales
+    p.device().run(RUNS if kind == "runs" else 0).check()
+
+
+@pytest.mark.parametrize("n", [400, 512])
+def test_a_group_for_every_query(n):
+    """As many groups as the call takes, more than a window of queries."""
+    p = Problem(62, lens=[i % 5 for i in range(n)], prefixes=[(70 * i) % 300 for i in range(n)],
+                groups=list(range(n + 1)), heads=(4, 2), head_dim=64, ids=None)
+    p.device().run().check()

@@ -461,7 +461,7 @@ void make_maps(Maps *m, const AttnParams &p, int head_dim)
     m->oob_page = (int32_t)(p.k.num_pages > p.v.num_pages ? p.k.num_pages : p.v.num_pages);
 }
 
-AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, void *workspace)
+AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace)
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     AttnPieces w;
@@ -473,6 +473,12 @@ AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, voi
     w.heads = attn_decode_heads(p.group);
     w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
     w.ctas = maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas;
+    // Beside its tiles a (query, head chunk) of 8 heads costs about what 256 bytes a token do
+    // (list, softmax, output): 256 short lists of 64-byte rows 17.5 us (18.6 with two items,
+    // 22.8 without), 64 of 128-byte rows 50.9 (51.7).  Chunks of 16 heads, whose tiles take
+    // longer, do better without: 37 lists of 256-byte rows 25.1 us (26.1 with one item), of
+    // 128-byte rows 20.9 (23.5 with two).
+    w.segment = w.heads == 8 ? 256 / (head_dim * (p.k.fp8 ? 1 : 2)) : 0;
     w.box_rows = maps.box_rows;
     w.oob_page = maps.oob_page;
     return w;
@@ -509,7 +515,7 @@ int group_shift(int group)
 msa_status run_decode(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace,
                       cudaStream_t stream)
 {
-    AttnPieces w = pieces_of(p, maps, l, workspace);
+    AttnPieces w = pieces_of(p, maps, l, head_dim, workspace);
     for (w.q0 = 0; w.q0 < p.num_queries; w.q0 += kAttnWindow) {
         w.nq = p.num_queries - w.q0 < kAttnWindow ? p.num_queries - w.q0 : kAttnWindow;
         msa_status s = launched(attn_decode(p, w, head_dim, maps.k, maps.v, stream));
@@ -538,7 +544,7 @@ msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l
     t.ctas = (int32_t)(units * t.splits);
     msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
     if (s == MSA_OK && t.splits > 1)
-        s = launched(attn_join_splits(p, pieces_of(p, maps, l, workspace), t, head_dim, stream));
+        s = launched(attn_join_splits(p, pieces_of(p, maps, l, head_dim, workspace), t, head_dim, stream));
     return s;
 }
 
@@ -547,7 +553,7 @@ msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l
 msa_status run_prefix(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace,
                       cudaStream_t stream)
 {
-    AttnPieces w = pieces_of(p, maps, l, workspace);
+    AttnPieces w = pieces_of(p, maps, l, head_dim, workspace);
     AttnTiles t = tiles_of(p, maps, l, workspace, group_shift(p.group));
     w.joined = 1;
     for (w.q0 = 0; w.q0 < p.num_queries; w.q0 += kAttnWindow) {

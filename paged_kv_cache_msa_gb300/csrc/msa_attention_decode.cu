@@ -30,7 +30,7 @@
 //   warps 5-7  query tiles, in turn, ahead of their use; queries that see nothing
 //   warps 8-15 two softmax and output groups: a thread is a token of each tile, then a dim
 // Measured: 64 queries, 16 blocks of 128 tokens (64 heads on 8 of 128 dims, E4M3, 233 MB)
-// 51.7 us, 4.5 TB/s, 0.66 of the copy rate; one query 12.1 us and 256 short ones 22.8 us,
+// 50.9 us, 4.6 TB/s, 0.67 of the copy rate; one query 12.3 us and 256 short ones 17.5 us,
 // bound by latency: 4.9 us from the dependency wait to the first scores (instructions
 // fetched for the first time, length -> ids -> page -> keys), the softmax of a chunk, the
 // join's launch.  256 bf16 queries of 32 heads on 2 (537 MB): 93 us, 0.85 of the copy rate.
@@ -88,20 +88,22 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
 }
 
 // A chunk: tiles [tile, tile + n) of (query q, head chunk hc), item `it` of the CTA's share.
+// A (query, head chunk) has `segment` items without a tile, then its tiles.
 struct Walk {
-    const int64_t *pre;      // tiles before each query
+    const int64_t *pre;      // items of a head chunk before each query
     int64_t it, end;
     int nq, hcs, q, hc;
-    int32_t nt, tile;        // tiles of the query; the chunk's first
+    int32_t segment, nt, tile;     // nt: tiles of the query; the chunk's first
 
-    __device__ void start(const int64_t *pre_, int nq_, int hcs_, int64_t i0, int64_t i1, int q0)
+    __device__ void start(const int64_t *pre_, int nq_, int hcs_, int32_t segment_, int64_t i0, int64_t i1, int q0)
     {
-        pre = pre_; nq = nq_; hcs = hcs_; it = i0; end = i1; q = q0; hc = 0; nt = 0; tile = 0;
+        pre = pre_; nq = nq_; hcs = hcs_; segment = segment_; it = i0; end = i1; q = q0; hc = 0; nt = 0; tile = 0;
         if (it < end) {
-            const int64_t base = pre[q] * hcs;
-            nt = (int32_t)(pre[q + 1] - pre[q]);
-            hc = (int)div64(it - base, nt);
-            tile = (int32_t)((it - base) - (int64_t)hc * nt);
+            const int64_t base = pre[q] * hcs, items = pre[q + 1] - pre[q];
+            nt = (int32_t)items - segment;
+            hc = (int)div64(it - base, items);
+            tile = max((int32_t)((it - base) - hc * items) - segment, 0);
+            it = base + hc * items + segment + tile;
         }
     }
     __device__ bool done() const { return it >= end; }
@@ -117,13 +119,14 @@ struct Walk {
         tile += n;
         if (tile == nt) {
             tile = 0;
+            it += segment;
             if (++hc == hcs) {
                 hc = 0;
                 do
                     ++q;
                 while (q < nq && pre[q + 1] == pre[q]);
                 if (q < nq)
-                    nt = (int32_t)(pre[q + 1] - pre[q]);
+                    nt = (int32_t)(pre[q + 1] - pre[q]) - segment;
             }
         }
     }
@@ -260,7 +263,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
 
-    // Tiles of each query and their prefix sums, a query a thread.  Lengths, table offsets
+    // Items of a head chunk of each query and their prefix sums, a query a thread.  Lengths, table offsets
     // and the first ids are read in one round of loads; the ids of small batches stay in
     // shared memory for the lists.
     static_assert(kAttnWindow <= kThreads, "a thread holds one query");
@@ -303,6 +306,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     int64_t sum = 0;
     if (tid < nq)
         sum = p.topk_ids ? (s_cnt[tid] * p.block_tokens + 127) / 128 : ((int64_t)len + 127) / 128;
+    sum += sum > 0 ? w.segment : 0;
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -316,14 +320,14 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    int64_t before = inc - sum, tiles = 0;
+    int64_t before = inc - sum, items = 0;
     for (int i = 0; i < (nq + 31) / 32; ++i) {
         before += i < warp ? s_wsum[i] : 0;
-        tiles += s_wsum[i];
+        items += s_wsum[i];
     }
     // equal shares, the last ones shorter or empty
     const int hcs = w.head_chunks;
-    const int64_t total = tiles * hcs, share = div64(total + gridDim.x - 1, gridDim.x);
+    const int64_t total = items * hcs, share = div64(total + gridDim.x - 1, gridDim.x);
     const int64_t i0 = min(total, share * blockIdx.x), i1 = min(total, i0 + share);
     if (tid < nq) {
         if (before * hcs <= i0 && i0 < (before + sum) * hcs)
@@ -339,7 +343,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     }
     __syncthreads();
     Walk wk;
-    wk.start(s_pre, nq, hcs, i0, i1, s_qlo);
+    wk.start(s_pre, nq, hcs, w.segment, i0, i1, s_qlo);
     const int nchunk_heads = (p.group + NH - 1) / NH;      // head chunks of a K/V head
 
     if (warp < 2) {
@@ -952,7 +956,7 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
             pre1 = pre0 + tl.splits - 1;
             prow = ((q % qt) << tl.gp_shift) + hcol;
         } else {
-            const int64_t lo = __ldcg(w.pre + q), nt = __ldcg(w.pre + q + 1) - lo, tiles = __ldcg(w.pre + w.nq);
+            const int64_t lo = __ldcg(w.pre + q), items = __ldcg(w.pre + q + 1) - lo, total = __ldcg(w.pre + w.nq);
             // the group before the first that starts after the query
             int g = -1;
             for (int i0 = 0; i0 <= p.num_groups && g < 0; i0 += 32) {
@@ -961,11 +965,11 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 if (first)
                     g = i0 + __ffs(first) - 1;
             }
-            if (nt > 0) {
-                const int64_t share = div64(tiles * w.head_chunks + w.ctas - 1, w.ctas);
-                const int64_t base = lo * w.head_chunks + (int64_t)(c * nch + hcol / w.heads) * nt;
-                own0 = (int)div64(base, share);
-                own1 = (int)div64(base + nt - 1, share);
+            if (items > 0) {
+                const int64_t share = div64(total * w.head_chunks + w.ctas - 1, w.ctas);
+                const int64_t base = lo * w.head_chunks + (int64_t)(c * nch + hcol / w.heads) * items;
+                own0 = (int)div64(base + w.segment, share);
+                own1 = (int)div64(base + items - 1, share);
             }
             if (--g >= 0) {
                 const int nb = (__ldcg(tl.groups->len + g) + kAttnTokens - 1) / kAttnTokens;

@@ -53,19 +53,21 @@ struct AttnParams {
 //
 // What the decode kernel needs beside AttnParams: a window of queries and its part of the
 // workspace.  CTA i holds the items [share * i, share * (i + 1)) of the list over (query,
-// head chunk, tile), share = ceil(items / ctas); the piece of a (query, head chunk) that
+// head chunk, tile), in which `segment` items without a tile come before the tiles of each
+// (query, head chunk); share = ceil(items / ctas).  The piece of a (query, head chunk) that
 // began in another CTA is in slot i, of one that goes on in the next in slot ctas + i: a
 // slot is [heads][D] of output, then the maxima, then the sums.
 struct AttnPieces {
     int4 *cut;                       // [ctas]: query, head chunk and last CTA of the one that
                                      // began in a CTA and goes on in the next; query -1: none
-    int64_t *pre;                    // [nq + 1]: tiles before each query of the window (joined)
+    int64_t *pre;                    // [nq + 1]: items before each query of the window (joined)
     float *pieces;                   // slots
     float *rows;                     // whole units (joined)
     int64_t q0, nq;                  // the window
     int32_t heads;                   // query heads of a head chunk: 8 or 16
     int32_t head_chunks;             // of all K/V heads
     int32_t ctas;
+    int32_t segment;                 // items that a (query, head chunk) has before its tiles
     int32_t box_rows;                // rows of a TMA box
     int32_t oob_page;                // a page past both caches
     int32_t joined;                  // every piece goes to the workspace

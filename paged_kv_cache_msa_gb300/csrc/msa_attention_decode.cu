@@ -972,11 +972,12 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 own1 = (int)div64(base + items - 1, share);
             }
             if (--g >= 0) {
-                const int nb = (__ldcg(tl.groups->len + g) + kAttnTokens - 1) / kAttnTokens;
+                const int nb = (int)(((uint32_t)__ldcg(tl.groups->len + g) + kAttnTokens - 1) / kAttnTokens);
                 if (nb > 0) {
                     const int at = q - __ldcg(tl.groups->start + g);
                     const int64_t share = __ldcg(&tl.groups->share);
-                    const int64_t base = __ldcg(tl.groups->item + g) + (int64_t)((at / qt) * p.hkv + c) * nb;
+                    const int64_t base = __ldcg(tl.groups->item + g) + kAttnUnit +
+                                         (int64_t)((at / qt) * p.hkv + c) * (nb + kAttnUnit);
                     pre0 = (int)div64(base, share);
                     pre1 = (int)div64(base + nb - 1, share);
                     prow = ((at % qt) << tl.gp_shift) + hcol;

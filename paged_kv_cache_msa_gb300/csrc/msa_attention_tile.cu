@@ -26,7 +26,7 @@
 // in registers (1.04 ms), 64-token tiles with weights beside the scores (1.08), 128-token
 // scores in one MMA group (1.11 to 1.17), separate warps for the two products (1.16).
 // About 15,000 of the 130,000 cycles of a CTA go by before its first scores.
-// 64 queries behind 8,192 shared tokens: 71 us with their own tokens and the join.
+// 64 queries behind 8,192 shared tokens: 65 us with their own tokens and the join.
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
 // output in tensor memory rescaled, which few tiles after the first need.  The groups hand
@@ -160,8 +160,10 @@ struct Segment {
 };
 
 struct DenseWalk {
-    const AttnGroups *tab;    // group g has tiles x K/V heads units of nb 128-token tiles
-    int64_t it, end, base;   // base: items before the unit
+    // group g has tiles x K/V heads units of kAttnUnit items without a tile, then nb
+    // 128-token tiles
+    const AttnGroups *tab;
+    int64_t it, end, base;   // base: the item of the unit's first tile
     int ngroups, hkv, qt, g, unit;
 
     __device__ int nb() const { return (int)(((uint32_t)tab->len[g] + 127u) / 128u); }
@@ -172,9 +174,10 @@ struct DenseWalk {
             unit = 0;
         }
         if (g < ngroups && it < end) {
-            const int n = nb();
+            const int n = nb() + kAttnUnit;
             unit = (int)((it - tab->item[g]) / n);
-            base = tab->item[g] + (int64_t)unit * n;
+            base = tab->item[g] + (int64_t)unit * n + kAttnUnit;
+            it = max(it, base);
         }
     }
     __device__ bool get(Segment &s) const
@@ -296,7 +299,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 int64_t x = 0;
                 if (g < n) {
                     const int q = u.groups.start[g + 1] - u.groups.start[g];
-                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (((int64_t)u.groups.len[g] + 127) / 128);
+                    const int64_t nb = ((int64_t)u.groups.len[g] + 127) / 128;
+                    x = (int64_t)((q + qt - 1) / qt) * p.hkv * (nb > 0 ? nb + kAttnUnit : 0);
                 }
                 int64_t inc = x;
 #pragma unroll

@@ -190,6 +190,21 @@ def build_starved(force: bool = False) -> str:
     return STARVED_LIB_PATH
 
 
+LAGGING_LIB_PATH = os.path.join(OUT_DIR, "libmsa_producer_lagging.so")
+
+
+def build_lagging(force: bool = False) -> str:
+    """Compiles the lagging test library (-DMSA_LAG): after each exchange between the
+    softmax warps of the attention kernels one of them sleeps for 20 us, so that a
+    missing synchronisation between its reads and the others' next writes shows in the
+    results.  Only the tests load it; the product uses build()."""
+    stamp = LAGGING_LIB_PATH + ".sha256"
+    digest = source_digest(("MSA_LAG",))
+    if force or not _fresh(LAGGING_LIB_PATH, stamp, digest):
+        _compile(LAGGING_LIB_PATH, stamp, digest, ["-DMSA_LAG"])
+    return LAGGING_LIB_PATH
+
+
 if __name__ == "__main__":
     defs = [a[2:] for a in sys.argv[1:] if a.startswith("-D")]
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, defines=defs or None))

@@ -212,7 +212,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     __shared__ uint8_t s_nv[kInfo][CH][kMaxBoxes];     // visible rows of the box
     __shared__ int32_t s_list[64];                     // block ids of the list warp's query
     __shared__ float s_qinv[kQSlots];
-    __shared__ float s_red[kGroups][4][16];
+    __shared__ float s_red[kGroups][2][4][16];         // by turns: see group_reduce
     __shared__ int s_qlo;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -660,7 +660,6 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         const int BR = w.box_rows, lb = __ffs(BR) - 1;
         const uint32_t o_tmem = tmem + lane_off + (uint32_t)(kSBufs * S::kSCols + g * N);
         const uint32_t ptile = pbase + (uint32_t)(g * CH * S::kPBytes);
-        float (*red)[16] = s_red[g];
         constexpr float kPScale = FP8 ? 256.0f : 1.0f;   // E4M3 weights use the range up to 448
         float m[NH], l[NH], acc[NH];
         uint32_t k = 0, seg = 0, o_phase = 0;      // k: chunks of this group
@@ -684,13 +683,18 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     acc[h] += FP8 ? __uint_as_float(r[h]) + __uint_as_float(r[NH + h]) : __uint_as_float(r[h]);
             }
         };
-        // reduces a value of each head over the 128 threads of the group; every thread gets all
-        auto group_reduce = [&](float (&v)[NH], auto max_tag) {
+        // reduces a value of each head over the 128 threads of the group; every thread gets all.
+        // Successive calls exchange in two places by turns: a warp that writes one has passed
+        // the barrier of the call before, which every warp reaches after it has read what the
+        // call before that left in the same place.
+        auto group_reduce = [&](float (&v)[NH], uint32_t turn, auto max_tag) {
             constexpr bool MAX = decltype(max_tag)::value;
+            float (*red)[16] = s_red[g][turn & 1u];
             const float x = butterfly<NH, MAX>(v, lane);
             if ((lane & (32 / NH - 1)) == 0)
                 red[quarter][lane / (32 / NH)] = x;
             group_sync();
+            test_lag(quarter == 1);
 #pragma unroll
             for (int h = 0; h < NH; ++h)
                 v[h] = MAX ? fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]))
@@ -758,7 +762,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         mx[h] = fmaxf(mx[h], z[h]);
                 }
             }
-            group_reduce(mx, std::true_type());
+            group_reduce(mx, k, std::true_type());
             if (!first)
                 add_output();
 #pragma unroll
@@ -821,12 +825,11 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             }
             if (last) {
                 // the sum over the tokens while the values are multiplied; then a thread is a dim
-                group_sync();                    // every thread has read the maxima
-                group_reduce(l, std::false_type());
+                group_reduce(l, k + 1, std::false_type());
                 add_output();
                 if (!ok)
                     *abort_flag = 1;
-                group_sync();
+                group_sync();                    // the next maxima come where these sums were
                 // a wait of any warp that ran out spoils the whole (query, head chunk)
                 const bool good = *abort_flag == 0;
                 const float bad = __int_as_float(0x7fc00000);

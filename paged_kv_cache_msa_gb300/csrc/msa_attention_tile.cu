@@ -636,7 +636,10 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
         constexpr int kD2 = D / 2;                      // dims of this thread
         const float nan = __int_as_float(0x7fc00000);
         // the two warps that hold a row's halves
-        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
+        auto pair_sync = [&]() {
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+            test_lag(half == 1);
+        };
         auto softmax_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
         uint32_t it = 0, nseg = 0;
         bool ok = true;

@@ -20,6 +20,18 @@ __device__ __forceinline__ uint64_t globaltimer()
     return t;
 }
 
+// The lagging test build (MSA_LAG) makes one warp of several fall 20 us behind after an
+// exchange through shared memory; nothing in the product.
+__device__ __forceinline__ void test_lag(bool warp)
+{
+#ifdef MSA_LAG
+    if (warp)
+        __nanosleep(20000);
+#else
+    (void)warp;
+#endif
+}
+
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

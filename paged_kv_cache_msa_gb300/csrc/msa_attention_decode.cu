@@ -484,7 +484,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             }
     } else if (warp == 2) {
         // ---------------- MMAs of the scores ----------------
-        constexpr uint32_t kId = mma_idesc(FP8, 128, N, false, false);
+        constexpr uint32_t kId = mma_idesc(!FP8, !FP8, 128, N, false, false);
         constexpr int kKB = 32;                               // bytes of K a step takes of a K-major row
         uint32_t it = 0;
         Turn turn;
@@ -528,7 +528,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
     } else if (warp == 3) {
         // ---------------- MMAs of the values ----------------
-        constexpr uint32_t kId = mma_idesc(FP8, 128, N, true, true);
+        constexpr uint32_t kId = mma_idesc(!FP8, !FP8, 128, N, true, true);
         constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step
         const int BR = w.box_rows, nbox = 128 / BR;
         const uint32_t vring = ring + (uint32_t)(ST * S::kTileBytes);

@@ -7,9 +7,9 @@
 // Per 128 tokens the CTA computes S [128 rows, 128 tokens] = Q . K^T and
 // O [128 rows, D] += P . V, each product read from shared memory as TMA copied it (K-major
 // keys, N-major values) with P as the A operand in tensor memory, where it takes the place
-// of the scores.  E4M3 caches run on kind::f8f6f4 with Q and P split into E4M3 halves
-// hi | lo (twice the MMAs at twice the rate: no conversion of keys or values, and half the
-// bytes in shared memory); bf16 on kind::f16.
+// of the scores.  E4M3 caches run on kind::f8f6f4 with Q split into E4M3 halves hi | lo and P
+// into three E5M2 parts (MMAs at twice the rate: no conversion of keys or values, and half
+// the bytes in shared memory); bf16 on kind::f16.
 //   warp 0     TMA: page lookups one tile ahead, key and value copies
 //   warp 1     MMAs; zeroes value rows past the history before they are multiplied
 //   warps 2-9  softmax and output: two groups of four, a thread per row; group g takes the
@@ -67,7 +67,9 @@ struct TileShape {
 };
 
 constexpr float kLazyBf16 = 8.0f, kLazyFp8 = 4.0f;
-constexpr float kPOffset = 4.0f;    // E4M3 weights are 2^4 times larger: up to 2^8 of 448
+// Weights over E4M3 values are 2^11 times larger, up to 2^15 of E5M2's 57,344: their parts
+// reach down to 2^-28 of the reference.
+constexpr float kPOffset = 11.0f;
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r)
 {
@@ -126,27 +128,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
-}
-
-// Four weights -> their E4M3 halves, four codes each, through f16: 11 bits hold what the
-// halves keep (8), and its pairs convert and subtract two at a time.
-__device__ __forceinline__ void split_weights(float x0, float x1, float x2, float x3, uint32_t &hi, uint32_t &lo)
-{
-    asm("{\n\t.reg .b32 p, q, b, c, d, e;\n\t.reg .b16 h0, h1, l0, l1;\n\t"
-        "cvt.rn.f16x2.f32 p, %3, %2;\n\t"
-        "cvt.rn.f16x2.f32 q, %5, %4;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 h0, p;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 h1, q;\n\t"
-        "mov.b32 %0, {h0, h1};\n\t"
-        "cvt.rn.f16x2.e4m3x2 b, h0;\n\t"
-        "cvt.rn.f16x2.e4m3x2 c, h1;\n\t"
-        "sub.rn.f16x2 d, p, b;\n\t"
-        "sub.rn.f16x2 e, q, c;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 l0, d;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 l1, e;\n\t"
-        "mov.b32 %1, {l0, l1};\n\t}"
-        : "=r"(hi), "=r"(lo)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
 
 // What a CTA works on: rows of the tile, a K/V head and a range of 128-token tiles.
@@ -528,8 +509,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
 #endif
     } else if (warp == 1) {
         // ---------------- MMAs ----------------
-        constexpr uint32_t kIdS = mma_idesc(FP8, 128, 64, false, false);
-        constexpr uint32_t kIdO = mma_idesc(FP8, 128, D, false, true);
+        constexpr uint32_t kIdS = mma_idesc(!FP8, !FP8, 128, 64, false, false);
+        constexpr uint32_t kIdO = mma_idesc(1, !FP8, 128, D, false, true);      // weights E5M2 or bf16
         constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step of the values
         constexpr int kStep = kTok * S::kSwz / 16;
         const int BR = w.box_rows, nbox = 128 / BR;
@@ -605,8 +586,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     tc_fence_after();
                     const uint64_t vd = v_desc + (uint64_t)(s * (uint32_t)(S::kTileBytes / 16) + g * (64 * S::kSwz / 16));
                     const uint32_t pt = tmem + (uint32_t)(g * 64), acc = v > seg.p0 || g > 0;
-                    if (FP8)        // two steps of hi, two of lo against the same values
-                        mma_ts22<kStep>(tmem + 128u, pt, vd, kIdO, acc);
+                    if (FP8)        // two steps, each of three parts against the same values
+                        mma_ts33<kStep>(tmem + 128u, pt, vd, kIdO, acc);
                     else
                         mma_ts4<FP8, 8, kStep>(tmem + 128u, pt, vd, kIdO, acc);
                     mma_commit(smem_u32(&bar_pv));
@@ -823,7 +804,7 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                         uint32_t x[32];
                         scores(j0, x);
                         auto score = [&](int j) { return __uint_as_float(x[j]); };
-                        uint32_t hw[FP8 ? 8 : 16], lw[8];
+                        uint32_t hw[FP8 ? 8 : 16], mw[8], lw[8];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             float p0, p1, p2, p3;
@@ -836,16 +817,17 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                             sum0 = add2(sum0, pack2(p0, p1));
                             sum1 = add2(sum1, pack2(p2, p3));
                             if (FP8) {
-                                split_weights(p0, p1, p2, p3, hw[e / 4], lw[e / 4]);
+                                split_weights(p0, p1, p2, p3, hw[e / 4], mw[e / 4], lw[e / 4]);
                             } else {
                                 hw[e / 2] = bf16x2_from_f32(p0, p1);
                                 hw[e / 2 + 1] = bf16x2_from_f32(p2, p3);
                             }
                         }
                         // over columns that have been read
-                        if (FP8) {      // 16 columns of hi, 16 of lo
-                            tmem_st8(st + (uint32_t)(j0 / 4), hw);
-                            tmem_st8(st + 16u + (uint32_t)(j0 / 4), lw);
+                        if (FP8) {      // 8 columns of each part
+                            tmem_st8(st + (uint32_t)j0, hw);
+                            tmem_st8(st + (uint32_t)j0 + 8u, mw);
+                            tmem_st8(st + (uint32_t)j0 + 16u, lw);
                         } else {
                             tmem_st16(st + (uint32_t)(j0 / 2), hw);
                         }
@@ -859,7 +841,11 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     for (int j = 0; j < 16; ++j)
                         z[j] = 0u;
                     tmem_st16(st, z);
-                    tmem_st16(st + 16u, z);
+                    tmem_st16(st + (FP8 ? 8u : 16u), z);
+                    if (FP8) {          // 24 columns of each step
+                        tmem_st16(st + 32u, z);
+                        tmem_st16(st + 40u, z);
+                    }
                 }
                 tc_wait_st();
                 tc_fence_before();

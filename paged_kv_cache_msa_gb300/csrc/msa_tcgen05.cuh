@@ -140,12 +140,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, int swizzle_bytes, 
     return d;
 }
 
-// Instruction descriptor: fp32 accumulators; E4M3 (kind::f8f6f4) or bf16 (kind::f16)
-// operands; an operand is K-major unless its mn flag is set.
-__host__ __device__ constexpr uint32_t mma_idesc(bool fp8, int m, int n, bool a_mn, bool b_mn)
+// Instruction descriptor: fp32 accumulators; 8-bit (kind::f8f6f4: 0 E4M3, 1 E5M2) or bf16
+// (kind::f16: 1) operands; an operand is K-major unless its mn flag is set.
+__host__ __device__ constexpr uint32_t mma_idesc(uint32_t a_type, uint32_t b_type, int m, int n, bool a_mn, bool b_mn)
 {
-    return (1u << 4) | ((fp8 ? 0u : 1u) << 7) | ((fp8 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
-           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+    return (1u << 4) | (a_type << 7) | (b_type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // One MMA by an elected lane of a converged warp, both operands in shared memory.
@@ -231,19 +231,22 @@ __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint
             : "memory");
 }
 
-// Four E4M3 MMAs with A in tensor memory, 8 columns apart, the third and fourth against the
-// B of the first two, which are BS apart.
+// Six 8-bit MMAs with A in tensor memory: three parts, 8 columns apart, against one B, and
+// three parts 32 columns further against the B that is BS further.
 template <int BS>
-__device__ __forceinline__ void mma_ts22(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_ts33(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred pp, pe;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+        "{\n\t.reg .pred pp, pe;\n\t.reg .b32 a1, a2, a3, a4, a5;\n\t.reg .b64 b1;\n\t"
         "elect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pp, %4, 0;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u64 b1, %2, %5;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u64 b1, %2, %5;\n\t"
+        "add.u32 a3, %1, 32;\n\tadd.u32 a4, %1, 40;\n\tadd.u32 a5, %1, 48;\n\t"
         "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, pp;\n\t"
-        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a1], b1, %3, 1;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a1], %2, %3, 1;\n\t"
         "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a2], %2, %3, 1;\n\t"
-        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a3], b1, %3, 1;\n\t}" ::"r"(d),
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a3], b1, %3, 1;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a4], b1, %3, 1;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a5], b1, %3, 1;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(BS)
         : "memory");
 }
@@ -333,6 +336,34 @@ __device__ __forceinline__ uint32_t e4m3x2_from_f32(float x0, float x1)
     unsigned short c;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x1), "f"(x0));
     return (uint32_t)c;
+}
+
+// Four weights (0 to 2^15) -> three E5M2 parts, four codes each, whose sum is the weight to
+// 2^-9 + 2^-11 of itself or 2^-17, whichever is more: no weight has to be small against its
+// row's largest (two E4M3 parts, of 2^-8, lost what was below 2^-14 of it).  E5M2 is the upper
+// byte of f16, so the first two parts are cut out of f16, each taking three bits, and
+// subtracted exactly; the last is rounded.
+__device__ __forceinline__ void split_weights(float x0, float x1, float x2, float x3, uint32_t &hi, uint32_t &mid,
+                                              uint32_t &lo)
+{
+    asm("{\n\t.reg .b32 p, q, b, c;\n\t.reg .b16 l0, l1;\n\t"
+        "cvt.rn.f16x2.f32 p, %4, %3;\n\t"
+        "cvt.rn.f16x2.f32 q, %6, %5;\n\t"
+        "prmt.b32 %0, p, q, 0x7531;\n\t"
+        "and.b32 b, p, 0xff00ff00;\n\t"
+        "and.b32 c, q, 0xff00ff00;\n\t"
+        "sub.rn.f16x2 p, p, b;\n\t"
+        "sub.rn.f16x2 q, q, c;\n\t"
+        "prmt.b32 %1, p, q, 0x7531;\n\t"
+        "and.b32 b, p, 0xff00ff00;\n\t"
+        "and.b32 c, q, 0xff00ff00;\n\t"
+        "sub.rn.f16x2 p, p, b;\n\t"
+        "sub.rn.f16x2 q, q, c;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 l0, p;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 l1, q;\n\t"
+        "mov.b32 %2, {l0, l1};\n\t}"
+        : "=&r"(hi), "=&r"(mid), "=r"(lo)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
 
 // (x0, x1) -> a bf16 pair, x0 in the low half

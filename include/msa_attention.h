@@ -36,9 +36,8 @@
  * they are and the weights exp(s - max) rounded to bf16; E4M3 caches are multiplied as
  * stored, against the queries split into two E4M3 halves hi + lo under a power-of-two
  * scale (reproduced exactly except elements below 2^-9 of the largest of their row or
- * group of rows) and the weights split into parts: of runs of queries and of prefixes
- * three E5M2 parts (a weight to 2^-9 + 2^-11 of itself or 2^-28 of the largest), of
- * single queries two E4M3 halves (2^-8 + 2^-12 of itself or 2^-18 of the largest).  Results do not depend on which other calls run, and a call repeated with
+ * group of rows) and the weights split into three E5M2 parts (a weight to 2^-9 + 2^-11
+ * of itself or 2^-28 of the largest).  Results do not depend on which other calls run, and a call repeated with
  * the same arguments gives the same bits.
  *
  * Ownership and threading: as for msa_producer_forward.  The caller owns every buffer,

@@ -12,8 +12,8 @@
 //   S [token, head]  = K [128 tokens x D, K-major]  . Q^T [D x heads, K-major]
 //   O [dim, head]    = V^T [D x 128 tokens, M-major] . P [128 tokens x heads, N-major]
 // K and V tiles are multiplied as TMA copied them (128- or 64-byte swizzle).  E4M3 caches
-// run on kind::f8f6f4 with Q and P split into E4M3 halves hi | lo side by side in the
-// columns, so that a tile is still read once from shared memory; bf16 on kind::f16.
+// run on kind::f8f6f4 with Q split into E4M3 halves and P into three E5M2 parts side by side
+// in the columns, so that a tile is still read once from shared memory; bf16 on kind::f16.
 //
 // Up to kChunk tiles of one (query, K/V head) form a chunk, whose scores are held in
 // tensor memory together, so that the maximum is reduced over the 128 threads once a
@@ -63,18 +63,20 @@ struct Shape {
     static constexpr int kSwz = kRowBytes < 128 ? kRowBytes : 128;      // swizzle and TMA box width
     static constexpr int kAtoms = kRowBytes / kSwz;                      // boxes side by side in a row
     static constexpr int kTileBytes = 128 * kRowBytes;
-    static constexpr int kN = FP8 ? 2 * NH : 16;                         // MMA columns: hi | lo, or at least 16
+    static constexpr int kN = FP8 ? 2 * NH : 16;                         // score columns: hi | lo, or at least 16
+    static constexpr int kNO = FP8 ? (3 * NH + 15) / 16 * 16 : 16;       // output columns: three parts, or at least 16
     static constexpr int kChunk = kN == 16 ? 4 : 2;                      // 64 columns of scores
     // Weights of one tile: [token][16 bytes] pieces of the columns.  bf16 weights of 8 heads
     // are the first piece alone, taken twice for the 16 columns.
-    static constexpr int kPBytes = 128 * (FP8 ? kN : NH * 2);
+    static constexpr int kPBytes = 128 * (FP8 ? kNO : NH * 2);
     static constexpr int kQBytes = kN * kRowBytes;
     static constexpr int kRest = 1024 + kGroups * kChunk * kPBytes + kQSlots * kQBytes;
-    static constexpr int kStages = (207 * 1024 - kRest) / kTileBytes / 2;   // of each ring, in what the lists leave
+    // of each ring, in what the lists (17 to 20 KB) leave of 227 KB
+    static constexpr int kStages = ((kChunk == 2 ? 209 : 207) * 1024 - kRest) / kTileBytes / 2;
     static constexpr int kSmem = kRest + 2 * kStages * kTileBytes;
     static constexpr int kSCols = kChunk * kN;                           // columns of one chunk's scores
     static constexpr int kTmem = 512;
-    static_assert(kSBufs * kSCols + kGroups * kN <= kTmem, "tensor memory");
+    static_assert(kSBufs * kSCols + kGroups * kNO <= kTmem, "tensor memory");
     static_assert(kQSlots % kGroups == 0 && kQSlots % kBuilders == 0, "slots");
     static_assert(kQBytes % 1024 == 0 && (kChunk * kPBytes) % 1024 == 0, "swizzle pattern alignment");
 };
@@ -195,7 +197,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
     using S = Shape<D, FP8, NH>;
-    constexpr int ST = S::kStages, N = S::kN, CH = S::kChunk;
+    constexpr int ST = S::kStages, N = S::kN, NO = S::kNO, CH = S::kChunk;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_k_full[ST], bar_k_empty[ST], bar_v_full[ST], bar_v_empty[ST];
     __shared__ __align__(8) uint64_t bar_info_full[kInfo], bar_info_empty[kInfo];
@@ -528,7 +530,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         (void)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_drain), 0));
     } else if (warp == 3) {
         // ---------------- MMAs of the values ----------------
-        constexpr uint32_t kId = mma_idesc(!FP8, !FP8, 128, N, true, true);
+        constexpr uint32_t kId = mma_idesc(!FP8, 1, 128, NO, true, true);     // weights E5M2 or bf16
         constexpr int kTok = FP8 ? 32 : 16;                   // tokens of a step
         const int BR = w.box_rows, nbox = 128 / BR;
         const uint32_t vring = ring + (uint32_t)(ST * S::kTileBytes);
@@ -539,7 +541,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             const int n = wk.count(CH), slot = turn.info(), g = turn.group();
             ok = warp_wait(smem_u32(&bar_info_full[slot]), turn.info_phase(), abort_flag);
             ok = ok && warp_wait(smem_u32(&bar_p_full[g]), turn.chunk() & 1u, abort_flag);
-            const uint32_t d = tmem + (uint32_t)(kSBufs * S::kSCols + g * N);
+            const uint32_t d = tmem + (uint32_t)(kSBufs * S::kSCols + g * NO);
             for (int i = 0; i < n && ok; ++i, ++it) {
                 const uint32_t s = it % ST;
                 ok = warp_wait(smem_u32(&bar_v_full[s]), (it / ST) & 1u, abort_flag);
@@ -658,9 +660,9 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         const int g = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const int BR = w.box_rows, lb = __ffs(BR) - 1;
-        const uint32_t o_tmem = tmem + lane_off + (uint32_t)(kSBufs * S::kSCols + g * N);
+        const uint32_t o_tmem = tmem + lane_off + (uint32_t)(kSBufs * S::kSCols + g * NO);
         const uint32_t ptile = pbase + (uint32_t)(g * CH * S::kPBytes);
-        constexpr float kPScale = FP8 ? 256.0f : 1.0f;   // E4M3 weights use the range up to 448
+        constexpr float kPScale = FP8 ? 32768.0f : 1.0f; // E5M2 parts use the range up to 57,344
         float m[NH], l[NH], acc[NH];
         uint32_t k = 0, seg = 0, o_phase = 0;      // k: chunks of this group
         bool ok = true, first = true;
@@ -671,16 +673,19 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             o_phase ^= 1u;
             if (ok) {
                 tc_fence_after();
-                uint32_t r[N];
-                if (N == 16)
-                    tmem_ld16(o_tmem, r);
-                else
-                    tmem_ld32(o_tmem, r);
-                tc_wait_ld();
-                tc_fence_before();
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
-                    acc[h] += FP8 ? __uint_as_float(r[h]) + __uint_as_float(r[NH + h]) : __uint_as_float(r[h]);
+                for (int part = 0; part < (FP8 ? 3 : 1); ++part) {
+                    uint32_t r[NH];
+                    if (NH == 8)
+                        tmem_ld8(o_tmem + (uint32_t)(part * NH), r);
+                    else
+                        tmem_ld16(o_tmem + (uint32_t)(part * NH), r);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        acc[h] += __uint_as_float(r[h]);
+                }
+                tc_fence_before();
             }
         };
         // reduces a value of each head over the 128 threads of the group; every thread gets all.
@@ -785,22 +790,18 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     }
                     const uint32_t a = ptile + (uint32_t)(i * S::kPBytes + row * 16);
                     if (FP8) {
-                        uint32_t hw[NH / 4], lw[NH / 4];
+                        uint32_t hw[NH / 4], mw[NH / 4], lw[NH / 4];
 #pragma unroll
-                        for (int h = 0; h < NH; h += 4) {
-                            const float x0 = e[h] * kPScale, x1 = e[h + 1] * kPScale, x2 = e[h + 2] * kPScale,
-                                        x3 = e[h + 3] * kPScale;
-                            const uint32_t h01 = e4m3x2_from_f32(x0, x1), h23 = e4m3x2_from_f32(x2, x3);
-                            const float2 d01 = attn_e4m3x2_to_f2(h01), d23 = attn_e4m3x2_to_f2(h23);
-                            hw[h / 4] = h01 | (h23 << 16);
-                            lw[h / 4] = e4m3x2_from_f32(x0 - d01.x, x1 - d01.y) |
-                                        (e4m3x2_from_f32(x2 - d23.x, x3 - d23.y) << 16);
-                        }
+                        for (int h = 0; h < NH; h += 4)
+                            split_weights(e[h] * kPScale, e[h + 1] * kPScale, e[h + 2] * kPScale, e[h + 3] * kPScale,
+                                          hw[h / 4], mw[h / 4], lw[h / 4]);
                         if (NH == 8) {
-                            sts128(a, hw[0], hw[1], lw[0], lw[1]);
+                            sts128(a, hw[0], hw[1], mw[0], mw[1]);
+                            sts128(a + 2048u, lw[0], lw[1], 0u, 0u);     // columns that nobody reads
                         } else {
                             sts128(a, hw[0], hw[1], hw[NH / 4 - 2], hw[NH / 4 - 1]);
-                            sts128(a + 2048u, lw[0], lw[1], lw[NH / 4 - 2], lw[NH / 4 - 1]);
+                            sts128(a + 2048u, mw[0], mw[1], mw[NH / 4 - 2], mw[NH / 4 - 1]);
+                            sts128(a + 4096u, lw[0], lw[1], lw[NH / 4 - 2], lw[NH / 4 - 1]);
                         }
                     } else {
                         uint32_t b[NH / 2];

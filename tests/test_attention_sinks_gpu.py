@@ -124,3 +124,16 @@ def test_query_runs(topk, d, dtype, s, dev):
 @pytest.mark.parametrize("n,dtype", [(8192, "e4m3"), (16384, "e4m3"), (8192, "bf16")])
 def test_behind_a_prefix(n, dtype, s, dev):
     Sink(82, 380, n, n, s, dev=dev, dtype=dtype).dense(True)
+
+
+@pytest.mark.parametrize("s,dev", SHARES)
+@pytest.mark.parametrize("heads,topk,dtype", [((16, 2), 16, "e4m3"), ((16, 1), 64, "e4m3"), ((16, 2), 64, "bf16")])
+def test_single_queries(heads, topk, dtype, s, dev):
+    Sink(83, 50, 300 + 256 * topk, topk * 128, s, heads=heads, dev=dev, dtype=dtype).sparse(topk, 0)
+
+
+@pytest.mark.parametrize("s,dev", SHARES)
+@pytest.mark.parametrize("heads,d", [((8, 1), 64), ((16, 1), 128)])
+def test_long_histories(heads, d, s, dev):
+    """Two lists of 65,536 tokens for each CTA, held whole or in two pieces."""
+    Sink(84, 304, 65536, 65536, s, heads=heads, d=d, dev=dev).dense(False)

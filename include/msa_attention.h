@@ -35,8 +35,7 @@
  * fp32.  Where the products run on the tensor cores, bf16 caches take the queries as
  * they are and the weights exp(s - max) rounded to bf16; E4M3 caches are multiplied as
  * stored, against the queries split into two E4M3 halves hi + lo under a power-of-two
- * scale (reproduced exactly except elements below 2^-9 of the largest of their row or
- * group of rows) and the weights split into three E5M2 parts (a weight to 2^-9 + 2^-11
+ * scale (reproduced exactly except elements below 2^-9 of the largest of their row) and the weights split into three E5M2 parts (a weight to 2^-9 + 2^-11
  * of itself or 2^-28 of the largest).  Results do not depend on which other calls run, and a call repeated with
  * the same arguments gives the same bits.
  *

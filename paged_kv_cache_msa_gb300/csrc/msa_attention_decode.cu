@@ -213,7 +213,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
     __shared__ int2 s_box[kInfo][CH][kMaxBoxes];       // row in the page, page
     __shared__ uint8_t s_nv[kInfo][CH][kMaxBoxes];     // visible rows of the box
     __shared__ int32_t s_list[64];                     // block ids of the list warp's query
-    __shared__ float s_qinv[kQSlots];
+    __shared__ __align__(16) float s_qscale[kQSlots][FP8 ? NH : 4];  // of each head's scores (bf16: the first)
     __shared__ float s_red[kGroups][2][4][16];         // by turns: see group_reduce
     __shared__ int s_qlo;
     __shared__ uint32_t s_tmem;
@@ -406,6 +406,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             const int c = wk.hc / nchunk_heads, h0 = (wk.hc % nchunk_heads) * NH;
             const int nh = min(NH, p.group - h0);
             const uint16_t *src = p.q + ((w.q0 + wk.q) * p.hq + c * p.group + h0) * D;
+            const float ks = attn_k_scale(p, c) * p.scale_log2;
             constexpr int E = D / 32;                       // elements of a lane
             auto load = [&](int h, uint32_t (&v)[E / 2]) {
 #pragma unroll
@@ -414,24 +415,20 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             };
             const uint32_t tile = qbase + x * (uint32_t)S::kQBytes;
             if (FP8) {
-                // halves hi | lo under the power of two that brings the largest magnitude
-                // of the heads into [128, 256): hi has 4 significant bits, lo the next 4
-                uint32_t big = 0;                           // magnitudes compare as integers
-#pragma unroll
+                // halves hi | lo under the power of two that brings the head's largest
+                // magnitude into [128, 256): hi has 4 significant bits, lo the next 4
+#pragma unroll 4
                 for (int h = 0; h < NH; ++h) {
-                    uint32_t v[E / 2];
+                    uint32_t v[E / 2], big = 0, hw = 0, lw = 0;
                     load(h, v);
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e)
+                    for (int e = 0; e < E / 2; ++e)         // magnitudes compare as integers
                         big = max(big, max((v[e] & 0x7FFFu) << 16, v[e] & 0x7FFF0000u));
-                }
-                big = __reduce_max_sync(0xffffffffu, big) >> 23;
-                const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
-                const float sc = __int_as_float((e2 + 127) << 23);
-#pragma unroll 2
-                for (int h = 0; h < NH; ++h) {              // read again, from L1
-                    uint32_t v[E / 2], hw = 0, lw = 0;
-                    load(h, v);
+                    big = __reduce_max_sync(0xffffffffu, big) >> 23;
+                    const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
+                    const float sc = __int_as_float((e2 + 127) << 23);
+                    if (lane == 0)
+                        s_qscale[x][h] = ks * __int_as_float((127 - e2) << 23);
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
                         const float x0 = __uint_as_float(v[e] << 16) * sc, x1 = __uint_as_float(v[e] & 0xFFFF0000u) * sc;
@@ -450,8 +447,6 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         asm volatile("st.shared.b16 [%0], %1;" ::"r"(b), "h"((unsigned short)lw) : "memory");
                     }
                 }
-                if (lane == 0)
-                    s_qinv[x] = __int_as_float((127 - e2) << 23);
             } else {
                 const uint32_t byte = (uint32_t)lane * 2 * E, at = byte / S::kSwz, col = byte % S::kSwz;
 #pragma unroll 4
@@ -464,7 +459,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         sts32(a + 4 * e, v[e]);
                 }
                 if (lane == 0)
-                    s_qinv[x] = 1.0f;
+                    s_qscale[x][0] = ks;
             }
             fence_async_smem();
             __syncwarp();
@@ -666,7 +661,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
         float m[NH], l[NH], acc[NH];
         uint32_t k = 0, seg = 0, o_phase = 0;      // k: chunks of this group
         bool ok = true, first = true;
-        float vs = 1.0f, ks = 1.0f;
+        float vs = 1.0f;
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
         auto add_output = [&]() {   // adds the value products of this group's last chunk
             ok = ok && warp_wait(smem_u32(&bar_o_full[g]), o_phase, abort_flag);
@@ -723,7 +718,6 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     l[h] = 0.0f;
                     acc[h] = 0.0f;
                 }
-                ks = attn_k_scale(p, head) * p.scale_log2;      // in flight while the scores are made
                 vs = attn_v_scale(p, head);
             }
             ok = ok && warp_wait(smem_u32(&bar_info_full[slot]), (k / kGroupInfo) & 1u, abort_flag);
@@ -736,7 +730,6 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             // instruction fetches (2.3 of the 4 cycles a warp instruction took) than
             // reading them twice does.
             const uint32_t sbuf = tmem + lane_off + (uint32_t)(sb * S::kSCols);
-            const float qs = ok ? ks * s_qinv[x] : 0.0f;
             auto scores = [&](int i, float (&z)[NH]) {     // of this thread's token of tile i
                 uint32_t r[N];
                 if (N == 16)
@@ -746,9 +739,15 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                 const bool seen = (row & (BR - 1)) < s_nv[slot][i][row >> lb];
                 tc_wait_ld();
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    z[h] = FP8 ? __uint_as_float(r[h]) + __uint_as_float(r[NH + h]) : __uint_as_float(r[h]);
-                    z[h] = seen ? z[h] * qs : -INFINITY;
+                for (int h0 = 0; h0 < NH; h0 += 4) {
+                    const float4 qs4 = *reinterpret_cast<const float4 *>(&s_qscale[x][FP8 ? h0 : 0]);
+                    const float qs[4] = {qs4.x, qs4.y, qs4.z, qs4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int h = h0 + e;
+                        z[h] = FP8 ? __uint_as_float(r[h]) + __uint_as_float(r[NH + h]) : __uint_as_float(r[h]);
+                        z[h] = seen ? z[h] * qs[FP8 ? e : 0] : -INFINITY;
+                    }
                 }
                 return seen;
             };

@@ -1,0 +1,51 @@
+"""The attention operators on values out of the ordinary (GPU): queries whose heads differ
+in size, infinite and NaN queries, key scales of zero, keys of infinity."""
+import pytest
+import torch
+
+from attention_cases import Problem
+from paged_kv_cache_msa_gb300 import binding as B
+from paged_kv_cache_msa_gb300 import build as build_mod
+
+pytestmark = pytest.mark.gpu
+
+RUNS = B.MSA_LAUNCH_QUERY_RUNS
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build_mod.build()
+    return B.load()
+
+
+def _problem(kind, seed=91, **kw):
+    """Single queries, a run or queries behind prefixes, and the call's flags."""
+    if kind == "prefix":
+        base = dict(lens=(5, 0, 300, 64, 1, 777), prefixes=(700,), groups=(0, 6), ids=None)
+    elif kind == "dense":
+        base = dict(lens=(5, 0, 300, 64, 1, 777), ids=None)
+    elif kind == "runs":
+        base = dict(lens=list(range(700, 740)), seq_of=[0] * 40, ids="near")
+    else:
+        base = dict(lens=(5, 0, 300, 64, 1, 2000, 777))
+    return Problem(seed, **{**base, **kw}), RUNS if kind == "runs" else 0
+
+
+KINDS = ["single", "dense", "runs", "prefix"]
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("heads", [(16, 2), (32, 2)], ids=str)
+@pytest.mark.parametrize("kind", KINDS)
+def test_heads_of_unlike_size(kind, heads, dtype):
+    """A head's result does not depend on the size of the other heads: the same bits when
+    they are 2^17 times larger."""
+    p, flags = _problem(kind, heads=heads, dtype=dtype)
+    small = p.device().run(flags).check()
+    q = p.q.clone()
+    p.q[:, 1] *= 2.0 ** 17
+    p.q[:, 5] *= 2.0 ** 12
+    large = p.device().run(flags)
+    rest = [h for h in range(heads[0]) if h not in (1, 5)]
+    assert torch.equal(large.out[:, rest], small.out[:, rest]) and torch.equal(large.lse[:, rest], small.lse[:, rest])
+    p.q = q

@@ -371,7 +371,7 @@ constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 Layout layout_of(const msa_attention_cfg *cfg, int64_t T, int64_t num_groups)
 {
-    const int64_t nh = attn_decode_heads(cfg->num_q_heads / cfg->num_kv_heads), D = cfg->head_dim;
+    const int64_t nh = attn_decode_heads(cfg->num_q_heads / cfg->num_kv_heads, false), D = cfg->head_dim;
     const int64_t window = T < kAttnWindow ? T : kAttnWindow;
     const int64_t rows = num_groups > 0 ? align256(window * cfg->num_q_heads * (D + 4) * 4) : 0;
     Layout l;
@@ -470,14 +470,13 @@ AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, int
     w.pre = reinterpret_cast<int64_t *>(ws + l.pre);
     w.pieces = reinterpret_cast<float *>(ws + l.pieces);
     w.rows = reinterpret_cast<float *>(ws + l.rows);
-    w.heads = attn_decode_heads(p.group);
+    w.heads = attn_decode_heads(p.group, p.k.fp8);
     w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
     w.ctas = maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas;
     // Beside its tiles a (query, head chunk) of 8 heads costs about what 256 bytes a token do
     // (list, softmax, output): 256 short lists of 64-byte rows 17.5 us (18.6 with two items,
     // 22.8 without), 64 of 128-byte rows 50.9 (51.7).  Chunks of 16 heads, whose tiles take
-    // longer, do better without: 37 lists of 256-byte rows 25.1 us (26.1 with one item), of
-    // 128-byte rows 20.9 (23.5 with two).
+    // longer, do better without: 37 lists of 256-byte rows 25.1 us (26.1 with one item).
     w.segment = w.heads == 8 ? 256 / (head_dim * (p.k.fp8 ? 1 : 2)) : 0;
     w.box_rows = maps.box_rows;
     w.oob_page = maps.oob_page;

@@ -7,8 +7,8 @@
 // The lists, cut into tiles of 128 tokens, are laid end to end over (query, K/V head,
 // tile) and one persistent CTA per SM takes an equal share, so a batch of one query uses
 // as many SMs as it has tiles.  Keys and values are the A operands of the MMAs, whose 128
-// rows they fill whatever the number of query heads on a K/V head; the heads (8 or 16)
-// are the columns:
+// rows they fill whatever the number of query heads on a K/V head; the heads (8, or 16 of
+// bf16 caches) are the columns:
 //   S [token, head]  = K [128 tokens x D, K-major]  . Q^T [D x heads, K-major]
 //   O [dim, head]    = V^T [D x 128 tokens, M-major] . P [128 tokens x heads, N-major]
 // K and V tiles are multiplied as TMA copied them (128- or 64-byte swizzle).  E4M3 caches
@@ -63,16 +63,17 @@ struct Shape {
     static constexpr int kSwz = kRowBytes < 128 ? kRowBytes : 128;      // swizzle and TMA box width
     static constexpr int kAtoms = kRowBytes / kSwz;                      // boxes side by side in a row
     static constexpr int kTileBytes = 128 * kRowBytes;
-    static constexpr int kN = FP8 ? 2 * NH : 16;                         // score columns: hi | lo, or at least 16
-    static constexpr int kNO = FP8 ? (3 * NH + 15) / 16 * 16 : 16;       // output columns: three parts, or at least 16
-    static constexpr int kChunk = kN == 16 ? 4 : 2;                      // 64 columns of scores
+    static_assert(NH == 8 || (NH == 16 && !FP8), "heads of a chunk");
+    static constexpr int kN = 16;                                        // score columns: hi | lo, or 8 or 16 heads
+    static constexpr int kNO = FP8 ? 32 : 16;                            // output columns: three parts of 8, or heads
+    static constexpr int kChunk = 4;                                     // 64 columns of scores
     // Weights of one tile: [token][16 bytes] pieces of the columns.  bf16 weights of 8 heads
     // are the first piece alone, taken twice for the 16 columns.
     static constexpr int kPBytes = 128 * (FP8 ? kNO : NH * 2);
     static constexpr int kQBytes = kN * kRowBytes;
     static constexpr int kRest = 1024 + kGroups * kChunk * kPBytes + kQSlots * kQBytes;
-    // of each ring, in what the lists (17 to 20 KB) leave of 227 KB
-    static constexpr int kStages = ((kChunk == 2 ? 209 : 207) * 1024 - kRest) / kTileBytes / 2;
+    // of each ring, in what the lists (20 KB) leave of 227 KB
+    static constexpr int kStages = (207 * 1024 - kRest) / kTileBytes / 2;
     static constexpr int kSmem = kRest + 2 * kStages * kTileBytes;
     static constexpr int kSCols = kChunk * kN;                           // columns of one chunk's scores
     static constexpr int kTmem = 512;
@@ -732,10 +733,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             const uint32_t sbuf = tmem + lane_off + (uint32_t)(sb * S::kSCols);
             auto scores = [&](int i, float (&z)[NH]) {     // of this thread's token of tile i
                 uint32_t r[N];
-                if (N == 16)
-                    tmem_ld16(sbuf + (uint32_t)(i * N), r);
-                else
-                    tmem_ld32(sbuf + (uint32_t)(i * N), r);
+                tmem_ld16(sbuf + (uint32_t)(i * N), r);
                 const bool seen = (row & (BR - 1)) < s_nv[slot][i][row >> lb];
                 tc_wait_ld();
 #pragma unroll
@@ -789,19 +787,13 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     }
                     const uint32_t a = ptile + (uint32_t)(i * S::kPBytes + row * 16);
                     if (FP8) {
-                        uint32_t hw[NH / 4], mw[NH / 4], lw[NH / 4];
+                        uint32_t hw[2], mw[2], lw[2];
 #pragma unroll
-                        for (int h = 0; h < NH; h += 4)
+                        for (int h = 0; h < 8; h += 4)
                             split_weights(e[h] * kPScale, e[h + 1] * kPScale, e[h + 2] * kPScale, e[h + 3] * kPScale,
                                           hw[h / 4], mw[h / 4], lw[h / 4]);
-                        if (NH == 8) {
-                            sts128(a, hw[0], hw[1], mw[0], mw[1]);
-                            sts128(a + 2048u, lw[0], lw[1], 0u, 0u);     // columns that nobody reads
-                        } else {
-                            sts128(a, hw[0], hw[1], hw[NH / 4 - 2], hw[NH / 4 - 1]);
-                            sts128(a + 2048u, mw[0], mw[1], mw[NH / 4 - 2], mw[NH / 4 - 1]);
-                            sts128(a + 4096u, lw[0], lw[1], lw[NH / 4 - 2], lw[NH / 4 - 1]);
-                        }
+                        sts128(a, hw[0], hw[1], mw[0], mw[1]);
+                        sts128(a + 2048u, lw[0], lw[1], 0u, 0u);         // columns that nobody reads
                     } else {
                         uint32_t b[NH / 2];
 #pragma unroll
@@ -1113,24 +1105,24 @@ cudaError_t launch_decode(const AttnParams &p, const AttnPieces &w, const CUtens
 
 }  // namespace
 
-// Heads a chunk: 16 where a K/V head has more than eight, so that its tokens are read once.
-// 16 heads on each, 16 blocks: 256 queries 94 us (163 in two chunks of eight) for bf16
-// caches, 92 (82) for E4M3, with 32 blocks 153 (172); 37 queries 25.4 (24.6) and 21.7 (17.6).
-int attn_decode_heads(int group) { return group <= 8 ? 8 : 16; }
+// Heads a chunk: 16 where a K/V head of a bf16 cache has more than eight, so that its tokens
+// are read once: 256 queries of 16 heads on each, 16 blocks, 94 us, 163 in two chunks of eight;
+// 37 queries 25.4 and 24.6.  E4M3 caches take eight: 16 heads side by side, 32 and 48 columns
+// of two-tile chunks, were slower or alike (37 queries 25.6 us, 18.1 in two chunks of eight;
+// 256 104 and 87, with 32 blocks 176 and 178; 64 queries of 64 heads on one 55 and 46).
+int attn_decode_heads(int group, bool fp8) { return group <= 8 || fp8 ? 8 : 16; }
 
 cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
                         const CUtensorMap &vmap, cudaStream_t stream)
 {
-    const bool f8 = p.k.fp8, h8 = w.heads == 8;
+    const bool h8 = w.heads == 8;
     if (head_dim == 128)
-        return f8 ? (h8 ? launch_decode<128, true, 8>(p, w, kmap, vmap, stream)
-                        : launch_decode<128, true, 16>(p, w, kmap, vmap, stream))
-                  : (h8 ? launch_decode<128, false, 8>(p, w, kmap, vmap, stream)
-                        : launch_decode<128, false, 16>(p, w, kmap, vmap, stream));
-    return f8 ? (h8 ? launch_decode<64, true, 8>(p, w, kmap, vmap, stream)
-                    : launch_decode<64, true, 16>(p, w, kmap, vmap, stream))
-              : (h8 ? launch_decode<64, false, 8>(p, w, kmap, vmap, stream)
-                    : launch_decode<64, false, 16>(p, w, kmap, vmap, stream));
+        return p.k.fp8 ? launch_decode<128, true, 8>(p, w, kmap, vmap, stream)
+               : h8    ? launch_decode<128, false, 8>(p, w, kmap, vmap, stream)
+                       : launch_decode<128, false, 16>(p, w, kmap, vmap, stream);
+    return p.k.fp8 ? launch_decode<64, true, 8>(p, w, kmap, vmap, stream)
+           : h8    ? launch_decode<64, false, 8>(p, w, kmap, vmap, stream)
+                   : launch_decode<64, false, 16>(p, w, kmap, vmap, stream);
 }
 
 namespace {

@@ -68,7 +68,7 @@ struct AttnPieces {
     float *pieces;                   // slots
     float *rows;                     // whole units (joined)
     int64_t q0, nq;                  // the window
-    int32_t heads;                   // query heads of a head chunk: 8 or 16
+    int32_t heads;                   // query heads of a head chunk: 8 or 16 (attn_decode_heads)
     int32_t head_chunks;             // of all K/V heads
     int32_t ctas;
     int32_t segment;                 // items that a (query, head chunk) has before its tiles
@@ -105,7 +105,7 @@ struct AttnTiles {
 // each may always start early.
 cudaError_t attn_launch(const void *fn, int64_t grid, int block, int smem, cudaStream_t stream, void **args);
 
-int attn_decode_heads(int group);
+int attn_decode_heads(int group, bool fp8);
 cudaError_t attn_decode(const AttnParams &p, const AttnPieces &w, int head_dim, const CUtensorMap &kmap,
                         const CUtensorMap &vmap, cudaStream_t stream);
 cudaError_t attn_tiles(const AttnParams &p, const AttnTiles &w, int head_dim, const CUtensorMap &kmap,

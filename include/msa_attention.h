@@ -25,7 +25,8 @@
  * where ks, vs are the dequantisation scales of an FP8 cache (1 for bf16).  A query
  * that sees no token gets out = 0 and lse = -inf.  Values behind a token that a query
  * does not see (unwritten cache cells, NaN or infinity among them) never reach its
- * result.
+ * result.  A row of q that is not finite has none of its own: over E4M3 caches NaN (out and
+ * lse), over bf16 caches what its scores give.
  *
  * The token of a history at index j lies in page page_table[offset + j / page_size],
  * row j % page_size; a token whose table index falls outside [0, page_table_len) or
@@ -35,8 +36,9 @@
  * fp32.  Where the products run on the tensor cores, bf16 caches take the queries as
  * they are and the weights exp(s - max) rounded to bf16; E4M3 caches are multiplied as
  * stored, against the queries split into two E4M3 halves hi + lo under a power-of-two
- * scale (reproduced exactly except elements below 2^-9 of the largest of their row) and the weights split into three E5M2 parts (a weight to 2^-9 + 2^-11
- * of itself or 2^-28 of the largest).  Results do not depend on which other calls run, and a call repeated with
+ * scale (reproduced exactly except elements below 2^-9 of the largest of their row) and
+ * the weights split into three E5M2 parts (a weight to 2^-9 + 2^-11 of itself or 2^-28 of
+ * the largest).  Results do not depend on which other calls run, and a call repeated with
  * the same arguments gives the same bits.
  *
  * Ownership and threading: as for msa_producer_forward.  The caller owns every buffer,

@@ -428,8 +428,8 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                     big = __reduce_max_sync(0xffffffffu, big) >> 23;
                     const int e2 = big > 0 ? min(7 - ((int)big - 127), 126) : 0;
                     const float sc = __int_as_float((e2 + 127) << 23);
-                    if (lane == 0)
-                        s_qscale[x][h] = ks * __int_as_float((127 - e2) << 23);
+                    if (lane == 0)      // an infinity would saturate: no score of such a head is a number
+                        s_qscale[x][h] = big == 255 ? __int_as_float(0x7fc00000) : ks * __int_as_float((127 - e2) << 23);
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
                         const float x0 = __uint_as_float(v[e] << 16) * sc, x1 = __uint_as_float(v[e] & 0xFFFF0000u) * sc;

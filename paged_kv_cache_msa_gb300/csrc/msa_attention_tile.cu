@@ -678,8 +678,8 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + a), "r"(hw[0]), "r"(hw[1]) : "memory");
                             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qsm + 128 * D + a), "r"(lw[0]), "r"(lw[1])
                                          : "memory");
-                            if (chunk == 0)
-                                s_row[0][r] = __int_as_float((127 - e2) << 23);
+                            if (chunk == 0)     // an infinity would saturate: no score of such a row is a number
+                                s_row[0][r] = big == 255 ? nan : __int_as_float((127 - e2) << 23);
                         } else {
                             const uint32_t byte = (uint32_t)chunk * 16, at = byte / S::kSwz, col = byte % S::kSwz;
                             sts128(qsm + at * (128u * S::kSwz) + swizzle<S::kSwz>((uint32_t)r * S::kSwz + col), xs[0], xs[1],

@@ -49,3 +49,19 @@ def test_heads_of_unlike_size(kind, heads, dtype):
     rest = [h for h in range(heads[0]) if h not in (1, 5)]
     assert torch.equal(large.out[:, rest], small.out[:, rest]) and torch.equal(large.lse[:, rest], small.lse[:, rest])
     p.q = q
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")], ids=str)
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_queries_that_are_not_finite(kind, dtype, bad):
+    """A head of a query that is not finite has no result (NaN; every score it has is
+    infinite or NaN); every other row has the same bits as without it."""
+    p, flags = _problem(kind, heads=(16, 2), dtype=dtype)
+    clean = p.device().run(flags)
+    t, h = 2, 9
+    p.q[t, h, 7] = bad
+    d = p.device().run(flags)
+    assert torch.isnan(d.out[t, h]).all() and torch.isnan(d.lse[t, h])
+    d.out[t, h], d.lse[t, h] = clean.out[t, h], clean.lse[t, h]
+    assert torch.equal(d.out, clean.out) and torch.equal(d.lse, clean.lse)

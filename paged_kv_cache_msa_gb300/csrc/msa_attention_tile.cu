@@ -695,6 +695,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             if (FP8) {
                 softmax_sync();
                 qs *= s_row[0][row];
+                // a scale of 0, or one that comes out as 0: scores are 0 by the smallest normal
+                // too, and the -infinity of a masked one stays what it is
+                qs = qs == 0.0f ? 1.17549435e-38f : qs;
             }
             const int len = DENSE ? seg.len : (qi < seg.nq ? u.sp.len[qi] : 0);
             float m = -INFINITY, l = 0.0f;                 // the reference that l is relative to

@@ -65,3 +65,13 @@ def test_queries_that_are_not_finite(kind, dtype, bad):
     assert torch.isnan(d.out[t, h]).all() and torch.isnan(d.lse[t, h])
     d.out[t, h], d.lse[t, h] = clean.out[t, h], clean.lse[t, h]
     assert torch.equal(d.out, clean.out) and torch.equal(d.lse, clean.lse)
+
+
+@pytest.mark.parametrize("which", ["all", "one head"])
+@pytest.mark.parametrize("bad_pages", [0, 4])
+@pytest.mark.parametrize("kind", KINDS)
+def test_key_scale_of_zero(kind, bad_pages, which):
+    """Every score is 0: the mean of the visible values, and lse = ln of their number."""
+    p, flags = _problem(kind, heads=(16, 4), per_head=True, bad_pages=bad_pages)
+    p.scales[2 if which == "one head" else slice(0, 4)] = 0.0
+    p.device().run(flags).check()

@@ -960,8 +960,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 __syncwarp();
             }
             // ---- rows that values of tokens they do not see may have reached ----
+            // (a row whose sum is NaN, from its own query or keys, has no other result)
             if (!DENSE && ok) {
-                uint32_t again = __ballot_sync(0xffffffffu, real && !finite);
+                uint32_t again = __ballot_sync(0xffffffffu, real && !finite && l == l);
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;

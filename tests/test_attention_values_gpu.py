@@ -75,3 +75,26 @@ def test_key_scale_of_zero(kind, bad_pages, which):
     p, flags = _problem(kind, heads=(16, 4), per_head=True, bad_pages=bad_pages)
     p.scales[2 if which == "one head" else slice(0, 4)] = 0.0
     p.device().run(flags).check()
+
+
+def test_nan_queries_take_no_longer():
+    """Rows without a result are not computed a second time, a token after another."""
+    p, flags = _problem("runs", heads=(16, 2), lens=list(range(2000, 2600)), seq_of=[0] * 600, topk=16)
+
+    def time():
+        d = p.device()
+        best = float("inf")
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            d.run(flags)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return d, best
+
+    _, plain = time()
+    p.q[:] = float("nan")
+    d, nan = time()
+    assert torch.isnan(d.out).all() and torch.isnan(d.lse).all()
+    assert nan < 4 * plain, (nan, plain)

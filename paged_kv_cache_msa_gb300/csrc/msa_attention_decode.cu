@@ -41,6 +41,7 @@
 #include "msa_attention_internal.h"
 #include "msa_tcgen05.cuh"
 
+#include <cfloat>
 #include <cstring>
 #include <type_traits>
 
@@ -715,7 +716,9 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
             if (first) {
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
-                    m[h] = -INFINITY;
+                    // finite, so that a score of -infinity (a token that is not visible, or an
+                    // infinite key) has no weight under any maximum
+                    m[h] = -FLT_MAX;
                     l[h] = 0.0f;
                     acc[h] = 0.0f;
                 }
@@ -747,7 +750,6 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
                         z[h] = seen ? z[h] * qs[FP8 ? e : 0] : -INFINITY;
                     }
                 }
-                return seen;
             };
             float mx[NH];
 #pragma unroll
@@ -758,7 +760,7 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     float z[NH];
-                    (void)scores(i, z);
+                    scores(i, z);
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
                         mx[h] = fmaxf(mx[h], z[h]);
@@ -779,10 +781,10 @@ msa_attention_decode_kernel(const __grid_constant__ AttnParams p, const __grid_c
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     float e[NH];
-                    const bool seen = scores(i, e);
+                    scores(i, e);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        e[h] = seen ? exp2_approx(e[h] - m[h]) : 0.0f;
+                        e[h] = exp2_approx(e[h] - m[h]);
                         l[h] += e[h];
                     }
                     const uint32_t a = ptile + (uint32_t)(i * S::kPBytes + row * 16);

@@ -98,3 +98,27 @@ def test_nan_queries_take_no_longer():
     d, nan = time()
     assert torch.isnan(d.out).all() and torch.isnan(d.lse).all()
     assert nan < 4 * plain, (nan, plain)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_scores_of_minus_infinity(kind):
+    """Tokens whose score is -infinity have no weight: the same bits as when their pages are
+    not there, whole chunks of them among the first; a query that sees no others has out = 0
+    and lse = -inf."""
+    p, flags = _problem(kind, heads=(16, 2), dtype="bf16", topk=8,
+                        **(dict(lens=(2000, 300, 64, 777)) if kind in ("single", "dense") else {}))
+    p.q[:, :, 0] = -p.q[:, :, 0].abs().clamp_min(0.01)
+    row = int(p.toff[0]) if kind != "prefix" else int(p.poff[0])
+    flat = p.table.view(-1)
+    gone = [row + i for i in range(10)]          # ten pages of the first history: 640 tokens
+    if kind in ("single", "dense"):              # and all of the last one
+        gone += [int(p.toff[-1]) + i for i in range(13)]
+    infinite = p.device()
+    k = p.k.clone()
+    k[flat[gone].long(), :, :, 0] = float("inf")
+    infinite.kpool = k.cuda()
+    infinite.k = B.cache_from_tensor(infinite.kpool)
+    infinite.run(flags)
+    flat[gone] = -1
+    absent = p.device().run(flags).check()
+    assert torch.equal(infinite.out, absent.out) and torch.equal(infinite.lse, absent.lse)

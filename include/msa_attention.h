@@ -79,8 +79,16 @@ typedef struct {
 
 /*
  * Bytes of workspace that either operator needs for num_queries queries in num_groups
- * groups (0 for the sparse operator) under cfg; at most a few tens of MB per 1,024
- * queries and bounded for any number of them.  Host-side; enqueues nothing.
+ * groups (0 for the sparse operator) under cfg.  However many queries:
+ *   without groups  less than 4 MB, and up to 26 MB more where a sparse call with
+ *                   MSA_LAUNCH_QUERY_RUNS would split its tiles of queries (a few hundred
+ *                   queries or fewer, block_tokens a multiple of 128; nothing more where
+ *                   topk is 0, as a cfg for prefix attention may have it);
+ *   with groups     less than 55 MB, and two rows of (head_dim + 4) * 4 bytes for each
+ *                   query head of min(num_queries, 384, max(1, 65536 / num_q_heads))
+ *                   queries: 27 MB for 64 heads of 128 dims, at most 70 MB up to 65,536
+ *                   heads.
+ * Host-side; enqueues nothing.
  */
 msa_status msa_attention_workspace_bytes(const msa_attention_cfg *cfg, int64_t num_queries,
                                          int64_t num_groups, int64_t *bytes);

@@ -360,9 +360,56 @@ msa_status launch_rows(const AttnParams &p, int head_dim, cudaStream_t stream)
                                 grid, kRowThreads, 0, stream, args));
 }
 
+int group_shift(int group)
+{
+    int s = 0;
+    while ((1 << s) < group)
+        ++s;
+    return s;
+}
+
+// Runs of queries: log2 of a query's rows in a tile (at most 32 queries and kAttnTileList
+// ids), tiles x K/V heads, and the CTAs that share a tile's blocks where the machine holds
+// `ctas`: a CTA for each, or, where it holds twice as many or more at once, several and a
+// join (8 K/V heads: 40 queries 29 us, 60 with a CTA each; 100: 36, 55; 160: 47, 60; 200, the
+// border: 59, 59).  More than it holds at once would cost: 333 queries 77 us, 92 in three pieces.
+struct Runs {
+    int shift;
+    int64_t units;
+    int32_t splits;
+};
+
+Runs runs_of(int group, int hkv, int topk, int64_t T, int ctas)
+{
+    Runs r;
+    r.shift = group_shift(group);
+    while ((128 >> r.shift) > 32 || (128 >> r.shift) * topk > kAttnTileList)
+        ++r.shift;
+    const int64_t qt = 128 >> r.shift;
+    r.units = (T + qt - 1) / qt * hkv;
+    const int64_t fit = ctas / r.units;
+    r.splits = fit > 1 ? (int32_t)(fit < 16 ? fit : 16) : 1;
+    return r;
+}
+
+// Rows of a tile that T queries can fill, an even number so that slots stay 16-byte aligned.
+int32_t slot_rows_of(int64_t T, int shift)
+{
+    const int64_t rows = T << shift;
+    return rows >= 128 ? 128 : (int32_t)((rows + 1) & ~(int64_t)1);
+}
+
+// Queries of a window behind prefixes, whose rows go to the workspace.
+int64_t prefix_window(int64_t hq)
+{
+    const int64_t n = kAttnWindowRows / hq;
+    return n < 1 ? 1 : n < kAttnWindow ? n : kAttnWindow;
+}
+
 // The workspace: cuts, prefix sums and groups of a window, the decode kernel's slots, the
 // tile kernel's slots, and with groups the whole units' rows of both.  Sizes are those of
-// the largest grids, so that they do not depend on the device.
+// the largest grids, so that they do not depend on the device.  Without groups the slots
+// are those of a sparse call with runs of queries, where its tiles are split.
 struct Layout {
     int64_t pre, groups, pieces, tile_pieces, rows, tile_rows, bytes;
 };
@@ -371,15 +418,25 @@ constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 Layout layout_of(const msa_attention_cfg *cfg, int64_t T, int64_t num_groups)
 {
-    const int64_t nh = attn_decode_heads(cfg->num_q_heads / cfg->num_kv_heads, false), D = cfg->head_dim;
-    const int64_t window = T < kAttnWindow ? T : kAttnWindow;
+    const int group = cfg->num_q_heads / cfg->num_kv_heads;
+    const int64_t nh = attn_decode_heads(group, false), D = cfg->head_dim;
+    const int64_t window = T < prefix_window(cfg->num_q_heads) ? T : prefix_window(cfg->num_q_heads);
     const int64_t rows = num_groups > 0 ? align256(window * cfg->num_q_heads * (D + 4) * 4) : 0;
+    int64_t slots = 0, slot_rows = 0;
+    if (num_groups > 0) {
+        slots = 2 * (2 * kAttnMaxCtas);
+        slot_rows = slot_rows_of(T, group_shift(group));
+    } else if (T > 0 && cfg->topk >= 1 && cfg->topk <= 64 && cfg->block_tokens % kAttnTokens == 0) {
+        const Runs r = runs_of(group, cfg->num_kv_heads, cfg->topk, T, 2 * kAttnMaxCtas);
+        slots = r.splits > 1 ? r.units * r.splits : 0;
+        slot_rows = slot_rows_of(T, r.shift);
+    }
     Layout l;
     l.pre = align256(kAttnMaxCtas * 16);
     l.groups = l.pre + align256((kAttnWindow + 1) * 8);
     l.pieces = l.groups + align256(sizeof(AttnGroups));
     l.tile_pieces = l.pieces + align256(2 * (int64_t)kAttnMaxCtas * nh * (D + 2) * 4);
-    l.rows = l.tile_pieces + align256(2 * (int64_t)(2 * kAttnMaxCtas) * 128 * (D + 2) * 4);
+    l.rows = l.tile_pieces + align256(slots * slot_rows * (D + 2) * 4);
     l.tile_rows = l.rows + rows;
     l.bytes = T == 0 ? 0 : l.tile_rows + rows;
     return l;
@@ -483,6 +540,8 @@ AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, int
     return w;
 }
 
+int tile_ctas(const Maps &maps) { return 2 * (maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas); }   // two a SM
+
 // gp_shift: rows of a query, a power of two that holds the heads on a K/V head.
 AttnTiles tiles_of(const AttnParams &p, const Maps &maps, const Layout &l, void *workspace, int gp_shift)
 {
@@ -495,18 +554,11 @@ AttnTiles tiles_of(const AttnParams &p, const Maps &maps, const Layout &l, void 
     t.nq = p.num_queries;
     t.gp_shift = gp_shift;
     t.splits = 1;
-    t.ctas = 2 * (maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas);     // two a SM
+    t.ctas = tile_ctas(maps);
+    t.slot_rows = slot_rows_of(p.num_queries, gp_shift);
     t.box_rows = maps.box_rows;
     t.oob_page = maps.oob_page;
     return t;
-}
-
-int group_shift(int group)
-{
-    int s = 0;
-    while ((1 << s) < group)
-        ++s;
-    return s;
 }
 
 // Single queries: windows of kAttnWindow queries, each the decode kernel and the join of
@@ -526,21 +578,13 @@ msa_status run_decode(const AttnParams &p, const Maps &maps, const Layout &l, in
     return MSA_OK;
 }
 
-// Runs of queries: a CTA for each tile and K/V head, or, where the machine holds twice as
-// many or more at once, several that share its blocks and a join (8 K/V heads: 40 queries
-// 29 us, 60 with a CTA each; 100: 36, 55; 160: 47, 60; 200, the border: 59, 59).  More than
-// it holds at once would cost: 333 queries 77 us, 92 in three pieces.
 msa_status run_query_runs(const AttnParams &p, const Maps &maps, const Layout &l, int head_dim, void *workspace,
                           cudaStream_t stream)
 {
-    int shift = group_shift(p.group);
-    while ((128 >> shift) > 32 || (128 >> shift) * p.topk > kAttnTileList)
-        ++shift;
-    AttnTiles t = tiles_of(p, maps, l, workspace, shift);
-    const int64_t qt = 128 >> shift, units = (p.num_queries + qt - 1) / qt * p.hkv;
-    const int64_t fit = t.ctas / units;
-    t.splits = fit > 1 ? (int32_t)(fit < 16 ? fit : 16) : 1;
-    t.ctas = (int32_t)(units * t.splits);
+    const Runs r = runs_of(p.group, p.hkv, p.topk, p.num_queries, tile_ctas(maps));
+    AttnTiles t = tiles_of(p, maps, l, workspace, r.shift);
+    t.splits = r.splits;
+    t.ctas = (int32_t)(r.units * r.splits);
     msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));
     if (s == MSA_OK && t.splits > 1)
         s = launched(attn_join_splits(p, pieces_of(p, maps, l, head_dim, workspace), t, head_dim, stream));
@@ -555,8 +599,9 @@ msa_status run_prefix(const AttnParams &p, const Maps &maps, const Layout &l, in
     AttnPieces w = pieces_of(p, maps, l, head_dim, workspace);
     AttnTiles t = tiles_of(p, maps, l, workspace, group_shift(p.group));
     w.joined = 1;
-    for (w.q0 = 0; w.q0 < p.num_queries; w.q0 += kAttnWindow) {
-        w.nq = p.num_queries - w.q0 < kAttnWindow ? p.num_queries - w.q0 : kAttnWindow;
+    const int64_t window = prefix_window(p.hq);
+    for (w.q0 = 0; w.q0 < p.num_queries; w.q0 += window) {
+        w.nq = p.num_queries - w.q0 < window ? p.num_queries - w.q0 : window;
         t.q0 = w.q0;
         t.nq = w.nq;
         msa_status s = launched(attn_tiles(p, t, head_dim, maps.k, maps.v, stream));

@@ -1003,9 +1003,9 @@ msa_attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_con
             a.sums = w.heads;
         } else {
             const int slot = MODE == kJoinSplits ? c0 + i : i > 0 ? c0 + i : tl.ctas + c0;
-            const float *base = tl.pieces + (int64_t)slot * (128 * (D + 2));
+            const float *base = tl.pieces + (int64_t)slot * (tl.slot_rows * (D + 2));
             a.o = base + prow * D;
-            a.m = base + 128 * D + 2 * prow;
+            a.m = base + tl.slot_rows * D + 2 * prow;
             a.stride = D;
             a.mstride = 2;
             a.sums = 1;

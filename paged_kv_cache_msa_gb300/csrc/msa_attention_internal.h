@@ -10,6 +10,7 @@
 
 constexpr int kAttnMaxGroups = 512;
 constexpr int kAttnWindow = 384;     // queries a launch of the tensor-core decode kernel takes
+constexpr int kAttnWindowRows = 65536;       // rows of a window of queries behind prefixes
 constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
 constexpr int kAttnTokens = 128;     // tokens of a tile of keys and values
 // What a tile of queries costs over a prefix beside its tokens (queries, output), in tiles
@@ -88,13 +89,14 @@ struct AttnGroups {
 
 // What the tile kernel needs beside AttnParams.  Sparse: CTA = (tile, K/V head, split), a
 // split tile's piece in slot CTA.  Prefix: items over (group, tile, K/V head, 128 tokens),
-// slots as in AttnPieces.  A slot is [128 rows][D], then [128][maximum, sum].
+// slots as in AttnPieces.  A slot is [slot_rows][D], then [slot_rows][maximum, sum].
 struct AttnTiles {
     AttnGroups *groups;              // prefix
     float *pieces;                   // slots
     float *rows;                     // prefix: whole units
     int64_t q0, nq;                  // the window (sparse: every query)
     int32_t gp_shift;                // log2 of the rows of a query
+    int32_t slot_rows;               // rows that a tile can have, an even number
     int32_t splits;                  // sparse: CTAs that share a tile's blocks
     int32_t ctas;
     int32_t box_rows, oob_page;

@@ -882,9 +882,9 @@ msa_attention_tile_kernel(const __grid_constant__ AttnParams p, const __grid_con
             };
             if (piece) {
                 const int64_t sl = DENSE ? (seg.began ? (int64_t)gridDim.x : 0) + blockIdx.x : (int64_t)blockIdx.x;
-                slot = w.pieces + sl * (int64_t)(128 * (D + 2));
+                slot = w.pieces + sl * (int64_t)(w.slot_rows * (D + 2));
                 dst = piece_row(row);
-                ml = DENSE && seg.whole ? dst + D : slot + 128 * D + 2 * row;
+                ml = DENSE && seg.whole ? dst + D : slot + w.slot_rows * D + 2 * row;
                 dst += half * kD2;
             }
             bool finite = true;

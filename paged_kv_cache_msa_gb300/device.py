@@ -175,10 +175,12 @@ class DecodeLayer:
     producer wrote (its compact index-Q and index-K cache), each token's visible
     history being its position + 1 tokens in its sequence's page-table row.  With
     ``attention``, the sparse attention of the compact Q over the K/V caches and the
-    blocks the indexer selected comes last (``attn_out``, ``attn_lse``)."""
+    blocks the indexer selected comes last (``attn_out``, ``attn_lse``).  Its workspace
+    holds nothing between calls: layers that run one after another on a stream may share
+    one (``attn_workspace=`` another layer's), layers that may run at once may not."""
 
     def __init__(self, dw: DeviceWorkload, max_blocks_per_seq: int, block_tokens: int = 128,
-                 topk: int = 16, attention: bool = False):
+                 topk: int = 16, attention: bool = False, attn_workspace=None):
         import torch
         self.dw = dw
         w = dw.w
@@ -206,8 +208,10 @@ class DecodeLayer:
                                                  block_tokens, topk, scale_mode=s.get("scale_mode", 0))
             self.attn_out = torch.empty_like(dw.q_out)
             self.attn_lse = torch.empty(dw.q_out.shape[:2], dtype=torch.float32, device=dw.device)
-            self.attn_workspace = torch.empty(B.msa_attention_workspace_bytes(self.attn_cfg, T),
-                                              dtype=torch.uint8, device=dw.device)
+            self.attn_workspace = attn_workspace
+            if attn_workspace is None:
+                self.attn_workspace = torch.empty(B.msa_attention_workspace_bytes(self.attn_cfg, T),
+                                                  dtype=torch.uint8, device=dw.device)
 
     def run(self, stream, flags=0, fused=False):
         """The producer, then the indexer on what it wrote (with ``fused``, the
@@ -229,4 +233,4 @@ class DecodeLayer:
                 self.attn_cfg, dw.w.num_tokens, p(dw.q_out), p(self.kv_len), p(self.table_offset),
                 p(dw.page_table), dw.page_table.numel(), p(self.topk_ids), dw.caches["k"], dw.caches["v"],
                 p(dw.scales), p(self.attn_out), p(self.attn_lse), p(self.attn_workspace),
-                self.attn_workspace.numel(), flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)
+                self.attn_workspace.nbytes, flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)

@@ -174,3 +174,48 @@ def test_tensor_functions_check_their_tensors():
     q = torch.zeros(2, 64, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         B.sparse_attention_tensors(cfg(), q, None, None, None, None, None, None, None, None)
+
+
+MB = 10**6
+
+
+@pytest.mark.parametrize("heads", [(64, 8, 128), (8, 2, 64), (1, 1, 128), (128, 1, 64), (1024, 8, 128), (8192, 64, 128),
+                                   (65536, 512, 128), (131072, 1024, 128)], ids=str)
+def test_workspace_bounds(heads):
+    """The sizes that the header states, at few and many heads and queries."""
+    hq, hkv, d = heads
+    c = cfg(num_q_heads=hq, num_kv_heads=hkv, head_dim=d)
+    dense = cfg(num_q_heads=hq, num_kv_heads=hkv, head_dim=d)
+    dense.topk = 0
+    assert B.msa_attention_workspace_bytes(c, 0) == 0 and B.msa_attention_workspace_bytes(c, 0, 3) == 0
+    for T in (1, 2, 7, 16, 33, 64, 100, 190, 256, 384, 385, 1000, 2**14):
+        if T * hkv * -(-hq // hkv // 8) > 2**31 - 1:
+            continue
+        n = B.msa_attention_workspace_bytes(c, T)
+        assert 0 < n < 30 * MB
+        assert n < 4 * MB or T * hkv < 2**12, "tiles that are not split need no pieces"
+        assert 0 < B.msa_attention_workspace_bytes(dense, T) < 4 * MB
+        g = B.msa_attention_workspace_bytes(c, T, 3)
+        rows = min(T, 384, max(1, 65536 // hq))
+        assert n <= g
+        assert g < 55 * MB + 2 * (rows * hq * (d + 4) * 4 + 256)
+        assert g < 125 * MB or hq > 65536
+
+
+def test_one_query_takes_little_workspace():
+    assert B.msa_attention_workspace_bytes(cfg(), 1) < 3 * MB
+    assert B.msa_attention_workspace_bytes(cfg(), 1, 1) < 6 * MB
+    assert B.msa_attention_workspace_bytes(cfg(), 500) < 4 * MB
+
+
+@pytest.mark.parametrize("T", [1, 5, 64, 400, 5000])
+def test_workspace_too_small(T):
+    n, g = B.msa_attention_workspace_bytes(cfg(), T), B.msa_attention_workspace_bytes(cfg(), T, 2)
+    assert 0 < n and 0 < g
+    for flags in (0, B.MSA_LAUNCH_QUERY_RUNS):
+        assert sparse(num_queries=T, workspace_bytes=n - 1, launch_flags=flags) == INV
+        assert sparse(num_queries=T, workspace=None, launch_flags=flags) == INV
+        assert sparse(num_queries=T, workspace=BASE + 8, launch_flags=flags) == MIS
+    assert prefix(num_queries=T, workspace_bytes=g - 1) == INV
+    assert prefix(num_queries=T, workspace=None) == INV
+    assert prefix(num_queries=T, workspace=BASE + 8) == MIS

@@ -13,8 +13,10 @@
  *                                  score, max-pool, top-k block ids, sparse attention);
  *   msa_prefix_attention_forward   dense attention in which groups of queries share a
  *                                  prefix, whose keys and values are read and
- *                                  multiplied once for the whole group; with no group
- *                                  it is plain dense paged attention.
+ *                                  multiplied once for each tile of 128 of the group's
+ *                                  rows (queries times heads on a K/V head) within
+ *                                  windows of up to 384 queries; with no group it is
+ *                                  plain dense paged attention.
  *
  * Per query t and query head h, with c = h / (num_q_heads / num_kv_heads):
  *
@@ -52,7 +54,8 @@
  *
  * Errors: every argument check runs on the host before any launch; a call that
  * returns an error has enqueued nothing and written nothing (MSA_ERR_CUDA from a
- * launch that the CUDA runtime refused: earlier launches of the call may run).
+ * launch that the CUDA runtime refused: earlier launches of the call may run).  Waits
+ * inside the kernels are bounded (2 s); rows that a kernel could not finish are NaN.
  */
 #ifndef MSA_ATTENTION_H
 #define MSA_ATTENTION_H

@@ -89,7 +89,8 @@ typedef enum { MSA_SCALE_PER_TENSOR = 0, MSA_SCALE_PER_HEAD = 1 } msa_scale_mode
                                      of the stream launched without programmatic dependent
                                      launch.  Stage them with plain launches (a copy) before
                                      the run, e.g. once at the start of a decode step. */
-#define MSA_LAUNCH_QUERY_RUNS 4   /* msa_indexer_forward only: the queries come in runs of
+#define MSA_LAUNCH_QUERY_RUNS 4   /* msa_indexer_forward (and, in words of its own,
+                                     msa_sparse_attention_forward): the queries come in runs of
                                      one sequence (consecutive queries with the same
                                      table_offset, as in a prefill chunk), so tiles of 8
                                      or 16 consecutive queries are scored together on the

@@ -178,9 +178,9 @@ STARVED_WAIT_LIMIT_NS = 50_000_000
 
 def build_starved(force: bool = False) -> str:
     """Compiles the starved test library (-DMSA_STARVE, every bounded wait limited to
-    STARVED_WAIT_LIMIT_NS): the projection's TMA warps and the query-run indexer's MMA
-    thread issue nothing, so every wait on their barriers runs out with no copy or
-    MMA in flight.  Only the tests of the timeout path load
+    STARVED_WAIT_LIMIT_NS): the projection's TMA warps, the query-run indexer's MMA
+    thread and the attention's copy warps issue nothing, so every wait on their barriers
+    runs out with no copy or MMA in flight.  Only the tests of the timeout path load
     it; the product uses build()."""
     defs = ("MSA_STARVE", f"MSA_WAIT_LIMIT_NS={STARVED_WAIT_LIMIT_NS}ull")
     stamp = STARVED_LIB_PATH + ".sha256"

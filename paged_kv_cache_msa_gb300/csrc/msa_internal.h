@@ -13,11 +13,14 @@
 #endif
 
 // MSA_STARVE (the starved test build only, never the product): the projection's
-// TMA warps and the query-run indexer's MMA thread issue nothing, so that every
-// wait on their barriers runs out; the tests check that each kernel then stops
-// (the projection without writing, the indexer scoring what it could not finish
-// NaN), reports the timeout and frees its tensor memory.  No copy or MMA is in
-// flight when the waits give up.
+// TMA warps, the query-run indexer's MMA thread and the attention kernels' copy warps
+// issue nothing, so that every wait on their barriers runs out; the tests check that
+// each kernel then stops (the projection without writing, the indexer scoring what it
+// could not finish NaN, the attention with NaN rows), reports the timeout (the
+// projection) and frees its tensor memory.  No copy or MMA is in flight when the waits
+// give up.
+//
+// MSA_LAG (the lagging test build only): see test_lag in msa_tcgen05.cuh.
 
 // Records a detail message for msa_last_error_detail() on this thread.
 void msa_internal_set_detail(const char *msg);

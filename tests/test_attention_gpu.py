@@ -446,3 +446,53 @@ def test_a_group_for_every_query(n):
     p = Problem(62, lens=[i % 5 for i in range(n)], prefixes=[(70 * i) % 300 for i in range(n)],
                 groups=list(range(n + 1)), heads=(4, 2), head_dim=64, ids=None)
     p.device().run().check()
+
+
+def test_a_decode_layer_behind_a_prefix():
+    """Dense attention of a decode layer's queries over its caches, the first eight behind a
+    prefix: the prefix's tokens, then each query's own, against the definition."""
+    from paged_kv_cache_msa_gb300 import workloads as wl
+    from paged_kv_cache_msa_gb300.device import DecodeLayer, DeviceWorkload
+    w = wl.config2_decode64()
+    pools = {k: torch.randint(0, 120, (n,), dtype=torch.uint8, device="cuda") for k, n in w.pools.items()}
+    for raw in pools.values():                         # values of both signs
+        raw[::3] += 128
+    dw = DeviceWorkload(w, pools_on_device=pools)
+    layer = DecodeLayer(dw, 144, attention=True)
+    layer.run(torch.cuda.current_stream())
+    K, V = (pools[k][4096:] for k in ("k", "v"))
+    kc = w.caches["k"]
+    table = dw.page_table.flatten()
+    own, toff = layer.kv_len.tolist(), layer.table_offset.tolist()
+    longest = max(range(64), key=lambda i: own[i])
+    plen, prow = min(500, own[longest]), toff[longest]
+    out, lse = torch.empty_like(dw.q_out), torch.empty(64, 64, device="cuda")
+    B.prefix_attention_tensors(layer.attn_cfg, dw.q_out, torch.tensor([0, 8], dtype=torch.int32, device="cuda"),
+                               torch.tensor([plen], dtype=torch.int32, device="cuda"),
+                               torch.tensor([prow], dtype=torch.int64, device="cuda"), layer.kv_len, layer.table_offset,
+                               dw.page_table, dw.caches["k"], dw.caches["v"], dw.scales, out, lse)
+    q, got = dw.q_out.view(torch.bfloat16).double(), out.view(torch.bfloat16).double()
+
+    def rows(pool, spans, scale):
+        pg = torch.cat([table[off + torch.arange(n, device="cuda") // 64] for off, n in spans]).long()
+        at = torch.cat([torch.arange(n, device="cuda") % 64 for _, n in spans])
+        base = pg * kc.stride_page + at * kc.stride_token
+        heads = torch.arange(8, device="cuda") * kc.stride_head
+        idx = base[:, None, None] + heads[None, :, None] + torch.arange(128, device="cuda")
+        return pool[idx].view(torch.float8_e4m3fn).double() * scale
+
+    for t in (0, 3, 7, 8, 40, 63):
+        spans = [(prow, plen)] * (t < 8) + [(toff[t], own[t])]
+        k, v = (rows(pool, spans, float(w.scales[i])) for i, pool in enumerate((K, V)))
+        qt = q[t].view(8, 8, 128)
+        z = torch.einsum("hgd,nhd->hgn", qt, k) * 128 ** -0.5
+        ref_lse = torch.logsumexp(z, -1)
+        p = z.softmax(-1)
+        ref = torch.einsum("hgn,nhd->hgd", p, v)
+        mean = torch.einsum("hgn,nhd->hgd", p, v.abs())
+        # scores: fp32 accumulation, and the query halves' floor of each row; weights: 2^-8
+        mag = torch.einsum("hgd,nhd->hgn", qt.abs(), k.abs()).amax(-1) * 128 ** -0.5
+        ds = mag * 2.0 ** -16 + 2.0 ** -17 * 128 ** -0.5 * qt.abs().amax(-1) * k.abs().sum(2).amax(0)[:, None]
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * ds[..., None]) * mean
+        assert ((got[t].view(8, 8, 128) - ref).abs() <= tol).all(), t
+        assert ((lse[t].view(8, 8).double() - ref_lse).abs() <= ds + 2.0 ** -20 * (1 + ref_lse.abs())).all(), t

@@ -122,3 +122,47 @@ def test_scores_of_minus_infinity(kind):
     flat[gone] = -1
     absent = p.device().run(flags).check()
     assert torch.equal(infinite.out, absent.out) and torch.equal(infinite.lse, absent.lse)
+
+
+@pytest.mark.parametrize("dtype,bad", [("e4m3", "nan"), ("bf16", "nan"), ("bf16", "inf")])
+@pytest.mark.parametrize("n", [40, 900], ids=["split", "whole"])
+def test_keys_of_unseen_tokens(n, dtype, bad):
+    """A key of NaN or infinity: the queries of a run that do not see its token are as
+    without it, although their tile multiplies it; those that do have no finite result or
+    (a score of -infinity) give the token no weight."""
+    p = Problem(92, lens=list(range(2000, 2000 + n)), seq_of=[0] * n, heads=(16, 8), dtype=dtype, ids="near", topk=4)
+    clean = p.device().run(RUNS)
+    tok = 2000 + n // 2                     # from the middle query on it is visible
+    pg, row = int(p.table[0, tok // p.page]), tok % p.page
+    dirty = p.device()
+    raw = p.k.clone().view(torch.uint8) if dtype == "e4m3" else p.k.clone()
+    raw[pg, 3, row, 5] = 0x7F if dtype == "e4m3" else float(bad)
+    dirty.kpool = (raw.view(torch.float8_e4m3fn) if dtype == "e4m3" else raw).contiguous().cuda()
+    dirty.k = B.cache_from_tensor(dirty.kpool)
+    dirty.run(RUNS)
+    sees = torch.zeros(n, 16, dtype=torch.bool)
+    for t in range(n):
+        if int(p.lens[t]) > tok and (p.ids[t] == tok // p.block).any():
+            sees[t, 6:8] = True             # the two query heads on K/V head 3
+    assert sees.any() and not sees.all()
+    if bad == "inf":                        # the sign of the score is that of the query's element
+        none = sees & (p.q[:, :, 5] < 0)
+        sees &= p.q[:, :, 5] >= 0
+        assert torch.isfinite(dirty.out.cpu()[none]).all() and torch.isfinite(dirty.lse.cpu()[none]).all()
+        assert torch.isnan(dirty.out.cpu()[sees]).all()
+        sees |= none
+    else:
+        assert torch.isnan(dirty.out.cpu()[sees]).all() and torch.isnan(dirty.lse.cpu()[sees]).all()
+    # rows computed again round their weights otherwise: each call is within the tolerance
+    # of the definition, so they are within twice of one another
+    rest = ~sees
+    assert torch.equal(dirty.lse.cpu()[rest], clean.lse.cpu()[rest])
+    a, b = clean.out.cpu().double(), dirty.out.cpu().double()
+    assert torch.isfinite(b[rest]).all()
+    some = rest & (torch.arange(n) % 37 == 0)[:, None] if n > 100 else rest
+    at = torch.nonzero(some.any(1)).flatten().tolist()
+    q = Problem(92, lens=list(range(2000, 2000 + n)), seq_of=[0] * n, heads=(16, 8), dtype=dtype, ids="near", topk=4)
+    q.q, q.lens, q.toff, q.ids, q.T = q.q[at], q.lens[at], q.toff[at], q.ids[at], len(at)
+    out, _, tol, _ = q.reference()
+    for x in (a, b):
+        assert ((x[at] - out).abs()[rest[at]] <= tol[rest[at]]).all()

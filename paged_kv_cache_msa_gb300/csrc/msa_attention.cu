@@ -25,7 +25,7 @@ namespace {
 // 8 elements of 16 bits at a time, the alignment that every accepted layout has.  It
 // is bound by its fp32 multiply-adds and serves the layouts that the tensor-core
 // kernels do not take: 64 queries of 16 blocks (64 heads on 8 of 128 dims, E4M3) take it
-// 449 us (the decode kernel 52.5), 8,192 prefill queries 28.7 ms (0.93).
+// 473 us (the decode kernel 52), 8,192 prefill queries 30.2 ms (1.00).
 constexpr int kRowThreads = 128;
 constexpr int kRowHeads = 8;
 
@@ -371,8 +371,9 @@ int group_shift(int group)
 // Runs of queries: log2 of a query's rows in a tile (at most 32 queries and kAttnTileList
 // ids), tiles x K/V heads, and the CTAs that share a tile's blocks where the machine holds
 // `ctas`: a CTA for each, or, where it holds twice as many or more at once, several and a
-// join (8 K/V heads: 40 queries 29 us, 60 with a CTA each; 100: 36, 55; 160: 47, 60; 200, the
-// border: 59, 59).  More than it holds at once would cost: 333 queries 77 us, 92 in three pieces.
+// join (8 K/V heads: 40 queries 26 us, 64 with a CTA each; 100: 33, 58; 160: 45, 63; 200, the
+// border: 57.6, 62.6 with one, 57.5 with two).  More than it holds at once would cost: 333
+// queries 78 us, 88 in two pieces, 81 in three.
 struct Runs {
     int shift;
     int64_t units;
@@ -531,9 +532,10 @@ AttnPieces pieces_of(const AttnParams &p, const Maps &maps, const Layout &l, int
     w.head_chunks = p.hkv * ((p.group + w.heads - 1) / w.heads);
     w.ctas = maps.sms < kAttnMaxCtas ? maps.sms : kAttnMaxCtas;
     // Beside its tiles a (query, head chunk) of 8 heads costs about what 256 bytes a token do
-    // (list, softmax, output): 256 short lists of 64-byte rows 17.5 us (18.6 with two items,
-    // 22.8 without), 64 of 128-byte rows 50.9 (51.7).  Chunks of 16 heads, whose tiles take
-    // longer, do better without: 37 lists of 256-byte rows 25.1 us (26.1 with one item).
+    // (list, softmax, output): 256 short lists of 64-byte rows 19.6 us (20.4 with two items,
+    // 26.4 without), 64 of 128-byte rows 52 (53.4 with one, 55 without).  Chunks of 16 heads,
+    // whose tiles take longer, do better without: 37 lists of 256-byte rows 25.2 us (27.7 with
+    // one item).
     w.segment = w.heads == 8 ? 256 / (head_dim * (p.k.fp8 ? 1 : 2)) : 0;
     w.box_rows = maps.box_rows;
     w.oob_page = maps.oob_page;
@@ -679,8 +681,8 @@ extern "C" msa_status msa_sparse_attention_forward(const msa_attention_cfg *cfg,
         return launch_rows(p, cfg->head_dim, stream);
     const Layout l = layout_of(cfg, num_queries, 0);
     // A tile of the tile kernel lies in one block.  The hint is the caller's, who knows
-    // the queries: 8,192 prefill queries 0.93 ms (4.6 as single queries), 333 73 us (197);
-    // 64 unrelated ones 85 us (52 as single queries).
+    // the queries: 8,192 prefill queries 1.00 ms (4.9 as single queries), 333 78 us (211);
+    // 64 unrelated ones 82 us (52 as single queries).
     if ((launch_flags & MSA_LAUNCH_QUERY_RUNS) && cfg->block_tokens % kAttnTokens == 0)
         return run_query_runs(p, maps, l, cfg->head_dim, workspace, stream);
     return run_decode(p, maps, l, cfg->head_dim, workspace, stream);

@@ -30,10 +30,10 @@
 //   warps 5-7  query tiles, in turn, ahead of their use; queries that see nothing
 //   warps 8-15 two softmax and output groups: a thread is a token of each tile, then a dim
 // Measured: 64 queries, 16 blocks of 128 tokens (64 heads on 8 of 128 dims, E4M3, 233 MB)
-// 50.9 us, 4.6 TB/s, 0.67 of the copy rate; one query 12.3 us and 256 short ones 17.5 us,
+// 52 us, 4.5 TB/s, 0.66 of the copy rate; one query 13.3 us and 256 short ones 19.6 us,
 // bound by latency: 4.9 us from the dependency wait to the first scores (instructions
 // fetched for the first time, length -> ids -> page -> keys), the softmax of a chunk, the
-// join's launch.  256 bf16 queries of 32 heads on 2 (537 MB): 93 us, 0.85 of the copy rate.
+// join's launch.  256 bf16 queries of 32 heads on 2 (524 MB): 94 us, 0.82 of the copy rate.
 // A (query, K/V head) that one CTA holds whole is written as bf16 right away; the pieces
 // of one that is cut between CTAs (at most two a CTA) go to the workspace, and a second,
 // dependent kernel joins them.

@@ -15,7 +15,7 @@ constexpr int kAttnMaxCtas = 192;    // its CTAs (one per SM) at most
 constexpr int kAttnTokens = 128;     // tokens of a tile of keys and values
 // What a tile of queries costs over a prefix beside its tokens (queries, output), in tiles
 // of tokens: a CTA's share of the tile kernel counts it.  64 queries behind 8,192 tokens
-// 64.9 us (69.2 without, 66.0 with three), six behind 65,536 66.5 (66.1, 68.0).
+// 69.0 us (73.1 without, 70.3 with three), six behind 65,536 72.7 (74.1, 73.0).
 constexpr int kAttnUnit = 2;
 constexpr int kAttnTileList = 1024;  // (query, id) pairs of a sparse tile
 

@@ -18,15 +18,18 @@
 // one half are ready while the other's softmax runs, and two CTAs share an SM (half the
 // tensor memory and half the shared memory each).
 // Measured: 8,192 prefill queries in four chunks (64 query heads on 8 of 128 dims, E4M3, 16
-// blocks of 128 tokens each) 0.93 ms, 0.30 of the measured bf16 rate by the tokens that the
+// blocks of 128 tokens each) 1.00 ms, 0.28 of the measured bf16 rate by the tokens that the
 // queries selected.  A tile of 16 queries runs over the union of their lists, 19 to 27
-// blocks, so a third of the products is masked.  Bound by instructions: 55 % of the issue
-// slots, 50 % of the ALU's (the split of the weights is 12 of about 22 instructions for
-// four tokens), tensor pipe 42 %, DRAM 4 %.  What was slower: all 64 scores of a row held
-// in registers (1.04 ms), 64-token tiles with weights beside the scores (1.08), 128-token
-// scores in one MMA group (1.11 to 1.17), separate warps for the two products (1.16).
-// About 15,000 of the 130,000 cycles of a CTA go by before its first scores.
-// 64 queries behind 8,192 shared tokens: 65 us with their own tokens and the join.
+// blocks, so a third of the products is masked.  Nothing is full: 55 % of the issue slots,
+// 48 % of the ALU's (the split of the weights is 15 of about 25 instructions for four
+// tokens), tensor pipe 51 %, DRAM 4 %; a tile is a chain of scores, maximum, weights and
+// values, which two CTAs an SM do not hide.  Weights in two E4M3 halves took 0.93 ms (4,400
+// cycles a tile), but lost those below 2^-14 of a row's largest.  With them were slower: all
+// 64 scores of a row held in registers (1.04 ms), 64-token tiles with weights beside the
+// scores (1.08), 128-token scores in one MMA group (1.11 to 1.17), separate warps for the two
+// products (1.16).
+// About 15,000 of a CTA's cycles go by before its first scores.
+// 64 queries behind 8,192 shared tokens: 69 us with their own tokens and the join.
 // The running maximum is a reference that follows the true one lazily: weights are taken
 // relative to it until the true maximum is kLazy powers of two above, and only then is the
 // output in tensor memory rescaled, which few tiles after the first need.  The groups hand

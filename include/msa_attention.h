@@ -28,8 +28,9 @@
  * that sees no token gets out = 0 and lse = -inf.  Values behind a token that a query
  * does not see (unwritten cache cells, NaN or infinity among them) never reach its
  * result.  A token whose score is -infinity (an infinite key of a bf16 cache) has no
- * weight, as one that is not visible.  A row of q that is not finite has no result of its
- * own: over E4M3 caches NaN (out and lse), over bf16 caches what its scores give.
+ * weight, as one that is not visible.  A row of q that is not finite and sees a token has
+ * no result of its own: over E4M3 keys NaN (out and lse), over bf16 keys what its scores
+ * give.
  *
  * The token of a history at index j lies in page page_table[offset + j / page_size],
  * row j % page_size; a token whose table index falls outside [0, page_table_len) or

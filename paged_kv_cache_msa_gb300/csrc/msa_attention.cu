@@ -92,7 +92,9 @@ __global__ void __launch_bounds__(kRowThreads) msa_attention_rows_kernel(const _
     const float qs = p.scale_log2 * attn_k_scale(p, c);
     for (int i = tid; i < kRowHeads * D; i += kRowThreads) {
         const int h = i / D;
-        s_q[h][i % D] = h < nh ? __uint_as_float((uint32_t)p.q[(t * p.hq + h0 + h) * D + i % D] << 16) : 0.0f;
+        const float x = h < nh ? __uint_as_float((uint32_t)p.q[(t * p.hq + h0 + h) * D + i % D] << 16) : 0.0f;
+        // over E4M3 keys no score of an infinite query is a number, as on the tensor cores
+        s_q[h][i % D] = p.k.fp8 && fabsf(x) == INFINITY ? __int_as_float(0x7fc00000) : x;
     }
     __syncthreads();
     for (int i = tid; i <= p.num_groups && p.num_groups > 0; i += kRowThreads)

@@ -166,3 +166,18 @@ def test_keys_of_unseen_tokens(n, dtype, bad):
     out, _, tol, _ = q.reference()
     for x in (a, b):
         assert ((x[at] - out).abs()[rest[at]] <= tol[rest[at]]).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")], ids=str)
+@pytest.mark.parametrize("layout", ["hnd", "odd"])
+@pytest.mark.parametrize("v_dtype", ["e4m3", "bf16"])
+def test_infinite_queries_of_one_token(v_dtype, layout, bad):
+    """Over an E4M3 cache an infinite query has no result even where its only score is
+    -infinity, in the kernel for every layout as on the tensor cores."""
+    p = Problem(93, lens=(1, 1, 0), heads=(16, 2), v_dtype=v_dtype, layout=layout)
+    p.q[:, 9, 7] = bad
+    d = p.device().run()
+    assert torch.isnan(d.out[:2, 9]).all() and torch.isnan(d.lse[:2, 9]).all()
+    assert (d.out[2] == 0).all() and torch.isneginf(d.lse[2]).all()
+    rest = [h for h in range(16) if h != 9]
+    assert torch.isfinite(d.out[:, rest]).all()

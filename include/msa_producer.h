@@ -191,6 +191,50 @@ msa_status msa_producer_validate(const msa_producer_cfg *cfg, int64_t num_tokens
                                  const float *scales, int32_t launch_flags);
 
 /*
+ * The producer with rotary positions of several axes, as images and video have them (time,
+ * height, width): pair k of the rotary dims turns by
+ *
+ *     positions[pair_axis[k]][t] * f_k
+ *
+ * instead of positions[t] * f_k.  Tokens of text have the same position on every axis.
+ *
+ *   pair_axis   the axis of each of the rotary_dim / 2 pairs, in any arrangement: sections
+ *               one after another, or axes taking turns.  Entries behind them must be 0.
+ *   restart     0: f_k = rope_theta^(-2k / rotary_dim), as with one axis.
+ *               1: the frequencies restart in each axis: the i-th of an axis's n pairs has
+ *               f = rope_theta^(-i / n).
+ *
+ * The whole turns of an angle are dropped in integers, so that it is right to 2^-25 of a turn
+ * and 2^-52 of itself at every int32 position, negative ones among them
+ * (msa_producer_forward's fp32 angles are right to 2^-24 of themselves).  Everything else is
+ * as for msa_producer_forward.
+ */
+#define MSA_ROPE_MAX_AXES 4
+
+typedef struct {
+    int32_t num_axes;        /* 1..MSA_ROPE_MAX_AXES */
+    int32_t restart;         /* 0 or 1 */
+    uint8_t pair_axis[64];   /* < num_axes for the first rotary_dim / 2, then 0 */
+    int32_t reserved[2];     /* must be 0 */
+} msa_rope_axes;
+
+/*
+ * positions      device int32 [num_axes, positions_stride]: row a holds the tokens' positions
+ *                on axis a; positions_stride >= num_tokens, in elements.
+ * Other arguments, the launch flags and errors as for msa_producer_forward.
+ */
+msa_status msa_producer_axes_forward(const msa_producer_cfg *cfg, const msa_rope_axes *axes,
+                                     int64_t num_tokens, const void *qkv, int64_t qkv_row_stride,
+                                     const int32_t *positions, int64_t positions_stride,
+                                     const int64_t *slot_mapping, const int32_t *page_table,
+                                     int64_t page_table_len, const void *q_norm_w,
+                                     const void *k_norm_w, const void *idx_q_norm_w,
+                                     const void *idx_k_norm_w, void *q_out, void *idx_q_out,
+                                     const msa_cache_desc *k_cache, const msa_cache_desc *v_cache,
+                                     const msa_cache_desc *idx_k_cache, const float *scales,
+                                     int32_t launch_flags, cudaStream_t stream);
+
+/*
  * Launch shape the forward call would use on the current device: CTAs, threads
  * per CTA and dynamic shared memory bytes.  Returns MSA_ERR_CUDA when the device
  * cannot be queried.  Host-side; enqueues nothing.

@@ -4,8 +4,8 @@ Every step of the producer runs in the CUDA library ``lib/libmsa_producer.so``;
 this module only turns Python/torch arguments into the C call.  There is no CPU
 or eager fallback: if the library has not been built, every call raises.
 
-Names follow ``include/msa_producer.h``, ``include/msa_projection.h`` and
-``include/msa_attention.h``.
+Names follow the headers in ``include/``: ``msa_producer.h``, ``msa_projection.h``,
+``msa_attention.h``, ``msa_norm.h`` and ``msa_adapter.h``.
 """
 from __future__ import annotations
 
@@ -39,7 +39,9 @@ EXPORTED = ("msa_producer_forward", "msa_producer_validate", "msa_producer_launc
             "msa_status_string",
             "msa_last_error_detail", "msa_projection_forward", "msa_projection_validate",
             "msa_checked_violations", "msa_attention_workspace_bytes",
-            "msa_sparse_attention_forward", "msa_prefix_attention_forward")
+            "msa_sparse_attention_forward", "msa_prefix_attention_forward",
+            "msa_norm_forward", "msa_adapter_workspace_bytes", "msa_adapter_forward",
+            "msa_producer_axes_forward")
 
 MSA_STATUS_WAIT_TIMEOUT = 1
 
@@ -106,6 +108,41 @@ class MsaAttentionCfg(ctypes.Structure):
     ]
 
 
+class MsaNormCfg(ctypes.Structure):
+    _fields_ = [
+        ("hidden_size", ctypes.c_int32),
+        ("rms_eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32 * 2),
+    ]
+
+
+MSA_ADAPTER_MAX_SLICES = 8
+
+
+class MsaAdapterCfg(ctypes.Structure):
+    _fields_ = [
+        ("hidden_size", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("num_adapters", ctypes.c_int32),
+        ("hidden_dtype", ctypes.c_int32),
+        ("num_slices", ctypes.c_int32),
+        ("slice_end", ctypes.c_int32 * MSA_ADAPTER_MAX_SLICES),
+        ("reserved", ctypes.c_int32 * 3),
+    ]
+
+
+MSA_ROPE_MAX_AXES = 4
+
+
+class MsaRopeAxes(ctypes.Structure):
+    _fields_ = [
+        ("num_axes", ctypes.c_int32),
+        ("restart", ctypes.c_int32),
+        ("pair_axis", ctypes.c_uint8 * 64),
+        ("reserved", ctypes.c_int32 * 2),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -161,6 +198,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.msa_prefix_attention_forward.argtypes = [attnp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64,
                                                    cachep, cachep, vp, vp, vp, vp, i64, i32, vp]
         L.msa_prefix_attention_forward.restype = ctypes.c_int
+        L.msa_norm_forward.argtypes = [ctypes.POINTER(MsaNormCfg), i64, vp, i64, vp, i64, vp, vp, i64, vp,
+                                       i64, vp, i64, vp, i32, vp]
+        L.msa_norm_forward.restype = ctypes.c_int
+        adapterp = ctypes.POINTER(MsaAdapterCfg)
+        L.msa_adapter_workspace_bytes.argtypes = [adapterp, i64, ctypes.POINTER(i64)]
+        L.msa_adapter_workspace_bytes.restype = ctypes.c_int
+        L.msa_adapter_forward.argtypes = [adapterp, i64, vp, i64, vp, vp, i64, vp, vp, vp, vp, i64, vp, i64,
+                                          vp, i64, i32, vp]
+        L.msa_adapter_forward.restype = ctypes.c_int
+        L.msa_producer_axes_forward.argtypes = [cfgp, ctypes.POINTER(MsaRopeAxes), i64, vp, i64, vp, i64, vp,
+                                                vp, i64, vp, vp, vp, vp, vp, vp, cachep, cachep, cachep, vp,
+                                                i32, vp]
+        L.msa_producer_axes_forward.restype = ctypes.c_int
         L.msa_host_buffer_device_address.argtypes = [vp, ctypes.POINTER(ctypes.c_void_p)]
         L.msa_host_buffer_device_address.restype = ctypes.c_int
         L.msa_checked_violations.argtypes = [ctypes.POINTER(ctypes.c_uint64), i32]
@@ -403,6 +453,103 @@ def msa_prefix_attention_forward(cfg, num_queries, q, num_groups, group_start, p
     return s
 
 
+def make_norm_cfg(hidden_size, rms_eps=1e-6) -> MsaNormCfg:
+    c = MsaNormCfg()
+    c.hidden_size, c.rms_eps = int(hidden_size), float(rms_eps)
+    return c
+
+
+def msa_norm_forward(cfg, num_tokens, x, x_stride, residual, residual_stride, weight, residual_out,
+                     residual_out_stride, out, out_stride, codes, codes_stride, scales, launch_flags=0,
+                     stream=0, check=True) -> int:
+    """The C entry point; pointers are integers or None.  Raises MsaError unless the
+    call returns MSA_OK (``check=False`` returns the status)."""
+    s = (_lib or load()).msa_norm_forward(
+        ctypes.byref(cfg) if cfg is not None else None, int(num_tokens), x, int(x_stride), residual,
+        int(residual_stride), weight, residual_out, int(residual_out_stride), out, int(out_stride), codes,
+        int(codes_stride), scales, int(launch_flags), stream)
+    if check and s != MSA_OK:
+        raise MsaError(s, "msa_norm_forward", last_error_detail())
+    return s
+
+
+def make_adapter_cfg(hidden_size, slice_ends, rank, num_adapters, hidden_dtype=MSA_DTYPE_BF16) -> MsaAdapterCfg:
+    """``slice_ends``: the column at which each slice of the rows ends, the width last."""
+    ends = [int(e) for e in slice_ends]
+    if not 1 <= len(ends) <= MSA_ADAPTER_MAX_SLICES:
+        raise ValueError(f"{len(ends)} slices (1..{MSA_ADAPTER_MAX_SLICES})")
+    c = MsaAdapterCfg()
+    c.hidden_size, c.rank, c.num_adapters = int(hidden_size), int(rank), int(num_adapters)
+    c.hidden_dtype, c.num_slices = int(hidden_dtype), len(ends)
+    for i, e in enumerate(ends):
+        c.slice_end[i] = e
+    return c
+
+
+def msa_adapter_workspace_bytes(cfg, num_tokens) -> int:
+    """Bytes of workspace the adapter call needs."""
+    n = ctypes.c_int64(0)
+    s = load().msa_adapter_workspace_bytes(ctypes.byref(cfg) if cfg is not None else None, int(num_tokens),
+                                           ctypes.byref(n))
+    if s != MSA_OK:
+        raise MsaError(s, "msa_adapter_workspace_bytes", last_error_detail())
+    return int(n.value)
+
+
+def msa_adapter_forward(cfg, num_tokens, hidden, hidden_stride, hidden_scales, down, down_stride, up,
+                        adapter_ids, adapter_scales, rows, rows_stride, out, out_stride, workspace,
+                        workspace_bytes, launch_flags=0, stream=0, check=True) -> int:
+    """The C entry point; pointers are integers or None.  Raises MsaError unless the
+    call returns MSA_OK (``check=False`` returns the status)."""
+    s = (_lib or load()).msa_adapter_forward(
+        ctypes.byref(cfg) if cfg is not None else None, int(num_tokens), hidden, int(hidden_stride),
+        hidden_scales, down, int(down_stride), up, adapter_ids, adapter_scales, rows, int(rows_stride), out,
+        int(out_stride), workspace, int(workspace_bytes), int(launch_flags), stream)
+    if check and s != MSA_OK:
+        raise MsaError(s, "msa_adapter_forward", last_error_detail())
+    return s
+
+
+def make_rope_axes(pairs, interleaved=False, restart=False) -> MsaRopeAxes:
+    """Rotary positions of several axes.  ``pairs``: how many of the rotary pairs turn with
+    each axis, in sections one after another, or with ``interleaved`` axes taking turns (an
+    axis whose pairs are used up falls out); the sum is rotary_dim / 2.  ``restart``: the
+    frequencies restart in each axis."""
+    left = [int(n) for n in pairs]
+    if not 1 <= len(left) <= MSA_ROPE_MAX_AXES or min(left) < 0 or sum(left) > 64:
+        raise ValueError(f"pairs {tuple(pairs)}: 1 to {MSA_ROPE_MAX_AXES} axes of at most 64 pairs together")
+    a = MsaRopeAxes()
+    a.num_axes, a.restart = len(left), int(bool(restart))
+    if interleaved:
+        order = []
+        while sum(left):
+            for i in range(len(left)):
+                if left[i]:
+                    left[i] -= 1
+                    order.append(i)
+    else:
+        order = [i for i, n in enumerate(left) for _ in range(n)]
+    for k, i in enumerate(order):
+        a.pair_axis[k] = i
+    return a
+
+
+def msa_producer_axes_forward(cfg, axes, num_tokens, qkv, qkv_row_stride, positions, positions_stride,
+                              slot_mapping, page_table, page_table_len, q_norm_w, k_norm_w, idx_q_norm_w,
+                              idx_k_norm_w, q_out, idx_q_out, k_cache, v_cache, idx_k_cache, scales,
+                              launch_flags=0, stream=0, check=True) -> int:
+    """The C entry point; pointers are integers or None.  Raises MsaError unless the
+    call returns MSA_OK (``check=False`` returns the status)."""
+    s = (_lib or load()).msa_producer_axes_forward(
+        ctypes.byref(cfg) if cfg is not None else None, _ref(axes), int(num_tokens), qkv, int(qkv_row_stride),
+        positions, int(positions_stride), slot_mapping, page_table, int(page_table_len), q_norm_w, k_norm_w,
+        idx_q_norm_w, idx_k_norm_w, q_out, idx_q_out, _ref(k_cache), _ref(v_cache), _ref(idx_k_cache), scales,
+        int(launch_flags), stream)
+    if check and s != MSA_OK:
+        raise MsaError(s, "msa_producer_axes_forward", last_error_detail())
+    return s
+
+
 def msa_checked_violations(reset: bool = True):
     """Stores skipped by a checked build since the last reset (synchronises the
     device); None for a normal build."""
@@ -493,7 +640,7 @@ def _tensor(name, t, shape, dtypes, device):
 _attention_types = None      # torch, and the dtypes of q and out, int32, int64, fp32
 
 
-def _on_device(q):
+def _on_device(q, name="q"):
     """The types and q's device; the latter's context when it is not the current one."""
     global _attention_types
     if _attention_types is None:
@@ -502,7 +649,7 @@ def _on_device(q):
                             (torch.float32,))
     dev = q.device
     if dev.type != "cuda":
-        raise ValueError(f"q is on {dev}; the attention calls take CUDA tensors")
+        raise ValueError(f"{name} is on {dev}; the calls take CUDA tensors")
     cuda = _attention_types[0].cuda
     return dev, None if cuda.current_device() == dev.index else cuda.device(dev)
 
@@ -577,3 +724,129 @@ def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, p
         _tensor("kv_len", kv_len, T, i32, dev), _tensor("table_offset", table_offset, T, i64, dev),
         _tensor("page_table", page_table, page_table.shape, i32, dev), page_table.numel(),
         k_cache, v_cache, scales, *rest)
+
+
+# ---------------------------------------------------------------------------
+# the input side of a layer: norm, adapters, the producer with several axes
+# ---------------------------------------------------------------------------
+
+_fp8_types = None
+
+
+def _types_8bit():
+    global _fp8_types
+    if _fp8_types is None:
+        import torch
+        _fp8_types = (torch.float8_e4m3fn, torch.uint8)
+    return _fp8_types
+
+
+def _rows(name, t, n, k, dtypes, device):
+    """Checks a tensor of n rows of k elements, rows any stride apart; returns its address and
+    row stride (None, 0 for None)."""
+    if t is None:
+        return None, 0
+    if t.dtype in dtypes and t.shape == (n, k) and t.device == device and (t.stride(1) == 1 or k == 1):
+        return t.data_ptr(), t.stride(0) if n > 1 else -(-k // 16) * 16
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name}: expected a {dtypes[0]} tensor of shape {(n, k)} with unit column stride, "
+                     f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+
+
+def _stream_handle(dev, stream):
+    # the handle alone: torch.cuda.current_stream builds a stream object in 2 us
+    return _attention_types[0]._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def norm_tensors(cfg: MsaNormCfg, x, weight, residual=None, residual_out=None, out=None, codes=None,
+                 scales=None, launch_flags=0, stream=None) -> None:
+    """msa_norm_forward on torch CUDA tensors: x, residual, residual_out and out bf16 [T, K],
+    codes E4M3 [T, K] (float8_e4m3fn or uint8), rows any stride apart; weight bf16 [K] and
+    scales fp32 [T] contiguous.  residual_out may be residual.  Runs on ``stream`` or the
+    current stream of x's device."""
+    dev, other = _on_device(x, "x")
+    if other is not None:
+        with other:
+            return norm_tensors(cfg, x, weight, residual, residual_out, out, codes, scales, launch_flags, stream)
+    _, bf16, _, _, f32 = _attention_types
+    n, k = x.shape[0], cfg.hidden_size
+    msa_norm_forward(cfg, n, *_rows("x", x, n, k, bf16, dev), *_rows("residual", residual, n, k, bf16, dev),
+                     _tensor("weight", weight, (k,), bf16, dev),
+                     *_rows("residual_out", residual_out, n, k, bf16, dev), *_rows("out", out, n, k, bf16, dev),
+                     *_rows("codes", codes, n, k, _types_8bit(), dev), _tensor("scales", scales, (n,), f32, dev),
+                     launch_flags, _stream_handle(dev, stream))
+
+
+def adapter_tensors(cfg: MsaAdapterCfg, hidden, down, up, adapter_ids, rows, out, hidden_scales=None,
+                    adapter_scales=None, workspace=None, launch_flags=0, stream=None) -> None:
+    """msa_adapter_forward on torch CUDA tensors: hidden [T, K] bf16 or E4M3 as the cfg says, rows
+    and out bf16 [T, W] (rows any stride apart; out may be rows), down bf16 [num_adapters,
+    num_slices * rank, K] (its rows any one stride apart), up bf16 [num_adapters, W, rank],
+    adapter_ids int32 [T], hidden_scales fp32 [T], adapter_scales fp32 [num_adapters].
+    ``workspace``: a tensor of at least ``msa_adapter_workspace_bytes(cfg, T)`` bytes, or None
+    to allocate one.  Runs on ``stream`` or the current stream of hidden's device."""
+    dev, other = _on_device(hidden, "hidden")
+    if other is not None:
+        with other:
+            return adapter_tensors(cfg, hidden, down, up, adapter_ids, rows, out, hidden_scales, adapter_scales,
+                                   workspace, launch_flags, stream)
+    torch, bf16, i32, _, f32 = _attention_types
+    n, k, r, a = hidden.shape[0], cfg.hidden_size, cfg.rank, cfg.num_adapters
+    width, sr = cfg.slice_end[cfg.num_slices - 1], cfg.num_slices * r
+    if down.dim() != 3 or (a > 1 and down.stride(0) != sr * down.stride(1)):
+        raise ValueError(f"down: expected [num_adapters, num_slices * rank, K] with its rows one stride apart, "
+                         f"got {tuple(down.shape)}, strides {down.stride()}")
+    if workspace is None:
+        nbytes = msa_adapter_workspace_bytes(cfg, n)
+        with torch.cuda.stream(stream):          # None: the current stream
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}, got one on {workspace.device}")
+    if down.shape[0] != a:
+        raise ValueError(f"down: expected {a} adapters, got {down.shape[0]}")
+    down_ptr, down_stride = _rows("down", down.flatten(0, 1), a * sr, k, bf16, dev)
+    msa_adapter_forward(cfg, n,
+                        *_rows("hidden", hidden, n, k, bf16 if cfg.hidden_dtype == MSA_DTYPE_BF16 else _types_8bit(), dev),
+                        _tensor("hidden_scales", hidden_scales, (n,), f32, dev), down_ptr, down_stride,
+                        _tensor("up", up, (a, width, r), bf16, dev), _tensor("adapter_ids", adapter_ids, (n,), i32, dev),
+                        _tensor("adapter_scales", adapter_scales, (a,), f32, dev),
+                        *_rows("rows", rows, n, width, bf16, dev), *_rows("out", out, n, width, bf16, dev),
+                        workspace.data_ptr() or None, workspace.nbytes, launch_flags, _stream_handle(dev, stream))
+
+
+def forward_axes_tensors(cfg: MsaProducerCfg, axes: MsaRopeAxes, qkv, positions, slot_mapping, page_table,
+                         norm_weights, q_out, idx_q_out, k_cache, v_cache, idx_k_cache, scales, launch_flags=0,
+                         stream=None) -> None:
+    """msa_producer_axes_forward on torch CUDA tensors: ``positions`` int32 [num_axes, T] with unit
+    column stride, everything else as for ``forward_tensors``, and checked.  Runs on ``stream``
+    or the current stream of qkv's device."""
+    dev, other = _on_device(qkv, "qkv")
+    if other is not None:
+        with other:
+            return forward_axes_tensors(cfg, axes, qkv, positions, slot_mapping, page_table, norm_weights, q_out,
+                                        idx_q_out, k_cache, v_cache, idx_k_cache, scales, launch_flags, stream)
+    _, bf16, i32, i64, f32 = _attention_types
+    n, d = qkv.shape[0], cfg.head_dim
+    width = (cfg.num_q_heads + 2 * cfg.num_kv_heads + cfg.num_idx_q_heads + cfg.num_idx_k_heads) * d
+    if qkv.dim() != 2 or qkv.shape[1] < width or (qkv.stride(1) != 1 and qkv.shape[1] > 1) or qkv.dtype not in bf16:
+        raise ValueError(f"qkv: expected bf16 rows of at least {width} elements, got {qkv.dtype} {tuple(qkv.shape)}, "
+                         f"strides {qkv.stride()}")
+    if positions.shape != (axes.num_axes, n) or positions.dtype not in i32 or positions.device != dev or \
+            (n > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions: expected int32 {(axes.num_axes, n)} on {dev} with unit column stride, got "
+                         f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
+    if scales is not None:
+        ns = 2 * cfg.num_kv_heads + cfg.num_idx_k_heads if cfg.scale_mode == MSA_SCALE_PER_HEAD else 3
+        if scales.dim() != 1 or scales.shape[0] < ns:
+            raise ValueError(f"scales: expected at least {ns} values, got shape {tuple(scales.shape)}")
+        scales = _tensor("scales", scales, scales.shape, f32, dev)
+    weights = [_tensor("norm weight", w, (d,), bf16, dev) for w in norm_weights]
+    msa_producer_axes_forward(
+        cfg, axes, n, qkv.data_ptr(), qkv.stride(0) if n > 1 else max(qkv.stride(0), width), positions.data_ptr(),
+        max(positions.stride(0), n), _tensor("slot_mapping", slot_mapping, (n,), i64, dev),
+        None if page_table is None else _tensor("page_table", page_table, page_table.shape, i32, dev),
+        0 if page_table is None else page_table.numel(), *weights,
+        _tensor("q_out", q_out, (n, cfg.num_q_heads, d), bf16, dev),
+        _tensor("idx_q_out", idx_q_out, (n, cfg.num_idx_q_heads, d), bf16, dev), k_cache, v_cache, idx_k_cache,
+        scales, launch_flags, _stream_handle(dev, stream))

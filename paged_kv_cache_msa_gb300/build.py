@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("msa_producer.cu", "msa_indexer.cu", "msa_projection.cu",
                                                     "msa_attention.cu", "msa_attention_decode.cu",
-                                                    "msa_attention_tile.cu")]
+                                                    "msa_attention_tile.cu", "msa_norm.cu", "msa_adapter.cu")]
 HEADERS = [os.path.join(PKG, "csrc", n) for n in ("msa_internal.h", "msa_attention_internal.h",
                                                     "msa_tcgen05.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
@@ -74,7 +74,8 @@ def _link_flags() -> list:
 
 
 DEPENDENCIES = SOURCES + HEADERS + [os.path.join(INCLUDE, h) for h in ("msa_producer.h", "msa_projection.h",
-                                                                         "msa_attention.h")]
+                                                                         "msa_attention.h", "msa_norm.h",
+                                                                         "msa_adapter.h")]
 STAMP_PATH = LIB_PATH + ".sha256"
 
 

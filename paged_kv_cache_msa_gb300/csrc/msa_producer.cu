@@ -132,6 +132,16 @@ struct Params {
 #endif
 };
 
+// The same with rotary positions of several axes.  Pair k turns by positions[axis[k]][t] *
+// turns[k] / 2^64 full turns: the product modulo 2^64 drops the whole turns exactly, so that an
+// angle is right to 2^-25 of a turn and 2^-52 of itself (what the frequency in double is off)
+// for every int32 position; a fp32 product loses 2^-24 of the angle: 0.01 at position 200,000.
+struct AxesParams : Params {
+    int64_t positions_stride;       // elements between two axes
+    uint64_t turns[kMaxRotaryHalf];
+    uint8_t axis[kMaxRotaryHalf];
+};
+
 #ifdef MSA_CHECKED
 // Checked build: a global store whose bytes leave its destination's extent is
 // skipped and counted here (read by msa_checked_violations).
@@ -537,16 +547,89 @@ struct MetaPipe {
     }
 };
 
+// The same with positions of several axes.  A thread's table entries are of one frequency,
+// k = tid % 64, for the tokens tid / 64 + m * NT / 64 of a group, so that its frequency and
+// its axis are taken from the parameters once (read with lane-dependent indexes, they come one
+// address at a time).
+template <int NT>
+struct AxesMetaPipe : MetaPipe<NT> {
+    using Base = MetaPipe<NT>;
+    static_assert(NT % kMaxRotaryHalf == 0, "table entries");
+    uint64_t turn;
+    const int32_t *pos;             // the axis's positions from the CTA's first token on; nullptr: no entries
+
+    __device__ __forceinline__ static int place_of(int tid, int m)
+    {
+        return tid / kMaxRotaryHalf + m * (NT / kMaxRotaryHalf);
+    }
+    __device__ __forceinline__ void load_positions(int tid, int64_t G, int64_t ntok, int64_t gbase)
+    {
+#pragma unroll
+        for (int m = 0; m < Base::ME; ++m) {
+            const int64_t i = gbase + place_of(tid, m);
+            this->pos_n[m] = pos && i < ntok ? __ldg(pos + i * G) : 0;
+        }
+    }
+    __device__ __forceinline__ void start(const AxesParams &p, int tid, int64_t t0, int64_t G, int64_t ntok)
+    {
+        const int k = tid % kMaxRotaryHalf;
+        turn = p.turns[k];
+        pos = k < p.rotary_dim / 2 ? p.positions + p.axis[k] * p.positions_stride + t0 : nullptr;
+        if (tid < kGroup) {
+            this->ls_n = this->load_slot(p, t0, G, ntok, tid);
+            this->pte_n = table_entry(p, this->ls_n);
+            this->ls_nn = this->load_slot(p, t0, G, ntok, kGroup + tid);
+        }
+        load_positions(tid, G, ntok, 0);
+    }
+    __device__ __forceinline__ void compute(const AxesParams &p, int tid, int64_t ntok, int64_t gbase,
+                                            TokenMeta (*s_meta)[kGroup],
+                                            float (*s_cs)[kGroup][2][kMaxRotaryHalf], int b)
+    {
+        if (tid < kGroup)
+            s_meta[b][tid] = place(p, this->ls_n, this->pte_n);
+#pragma unroll
+        for (int m = 0; m < Base::ME; ++m)
+            if (pos && gbase + place_of(tid, m) < ntok) {
+                const uint64_t turns = (uint64_t)(int64_t)this->pos_n[m] * turn;
+                float sn, c;
+                sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &c);
+                s_cs[b][place_of(tid, m)][0][tid % kMaxRotaryHalf] = c;
+                s_cs[b][place_of(tid, m)][1][tid % kMaxRotaryHalf] = sn;
+            }
+    }
+    __device__ __forceinline__ void prefetch(const AxesParams &p, int tid, int64_t t0, int64_t G, int64_t ntok,
+                                             int64_t gbase)
+    {
+        if (tid < kGroup) {
+            this->ls_n = this->ls_nn;
+            this->pte_n = table_entry(p, this->ls_n);
+            this->ls_nn = this->load_slot(p, t0, G, ntok, gbase + kGroup + tid);
+        }
+        load_positions(tid, G, ntok, gbase);
+    }
+};
+
+template <int NT, class P>
+struct PipeOf {
+    using type = MetaPipe<NT>;
+};
+template <int NT>
+struct PipeOf<NT, AxesParams> {
+    using type = AxesMetaPipe<NT>;
+};
+
 // ---------------------------------------------------------------------------
 // the producer kernel, rows staged by the compute threads (cp.async)
 // ---------------------------------------------------------------------------
 //
 // A CTA takes the tokens blockIdx.x + i * gridDim.x, i = 0, 1, ...  in groups of
 // kGroup.  Each thread copies the 16-byte pieces of the rows that it later reads
-// into a kStages-deep shared-memory ring, one token ahead.
-template <int D, int NT>
+// into a kStages-deep shared-memory ring, one token ahead.  P: Params, or AxesParams for rotary
+// positions of several axes.
+template <int D, int NT, class P>
 __global__ void __launch_bounds__(NT, MSA_MIN_CTAS_PER_SM * 256 / NT)
-msa_producer_kernel(const __grid_constant__ Params p)
+msa_producer_kernel(const __grid_constant__ P p)
 {
     constexpr int L = D / 16;
     constexpr int RPP = NT / L;                       // head rows per pass
@@ -604,7 +687,7 @@ msa_producer_kernel(const __grid_constant__ Params p)
         }
     };
 
-    MetaPipe<NT> meta;
+    typename PipeOf<NT, P>::type meta;
     // ---- prologue ----
     // Under programmatic dependent launch the first group's metadata is computed
     // before waiting on the previous kernel and the rows are read after it.
@@ -874,13 +957,14 @@ struct Variant {
     int id;
 };
 
-template <int D, int NT>
-Variant variant_of(int id)
-{
-    return Variant{reinterpret_cast<const void *>(&msa_producer_kernel<D, NT>), NT, id};
-}
+constexpr int kNumVariants = 12;    // six launch shapes, with one axis and with several
 
-constexpr int kNumVariants = 6;
+template <int D, int NT>
+Variant variant_of(int id, bool axes)
+{
+    return axes ? Variant{reinterpret_cast<const void *>(&msa_producer_kernel<D, NT, AxesParams>), NT, id + 6}
+                : Variant{reinterpret_cast<const void *>(&msa_producer_kernel<D, NT, Params>), NT, id};
+}
 
 int64_t htot_of(const msa_producer_cfg *cfg)
 {
@@ -889,17 +973,17 @@ int64_t htot_of(const msa_producer_cfg *cfg)
 }
 
 // Threads per CTA: enough lanes for one pass over a token's head rows, at most 256.
-Variant pick_variant(const msa_producer_cfg *cfg)
+Variant pick_variant(const msa_producer_cfg *cfg, bool axes)
 {
     const int64_t lanes = htot_of(cfg) * (cfg->head_dim / 16);
     if (cfg->head_dim == 128) {
-        if (lanes <= 64) return variant_of<128, 64>(0);
-        if (lanes <= 128) return variant_of<128, 128>(1);
-        return variant_of<128, 256>(2);
+        if (lanes <= 64) return variant_of<128, 64>(0, axes);
+        if (lanes <= 128) return variant_of<128, 128>(1, axes);
+        return variant_of<128, 256>(2, axes);
     }
-    if (lanes <= 64) return variant_of<64, 64>(3);
-    if (lanes <= 128) return variant_of<64, 128>(4);
-    return variant_of<64, 256>(5);
+    if (lanes <= 64) return variant_of<64, 64>(3, axes);
+    if (lanes <= 128) return variant_of<64, 128>(4, axes);
+    return variant_of<64, 256>(5, axes);
 }
 
 constexpr int kMaxDevices = 64;
@@ -914,9 +998,9 @@ DeviceInfo g_dev[kMaxDevices];
 // limit) and returns the launch shape.  Host-side queries only; nothing is
 // enqueued, so this is safe while a stream is being captured.
 msa_status launch_shape(const msa_producer_cfg *cfg, int64_t T, int32_t flags, Variant *v,
-                        int *grid, int *smem)
+                        int *grid, int *smem, bool axes = false)
 {
-    *v = pick_variant(cfg);
+    *v = pick_variant(cfg, axes);
     const int64_t row_bytes = htot_of(cfg) * cfg->head_dim * 2;
     *smem = (int)(kStages * row_bytes);
     int dev = 0;
@@ -976,42 +1060,71 @@ void fill_cache(CacheArgs &a, const msa_cache_desc *c)
     a.pad = 0;
 }
 
-}  // namespace
+// ---------------------------------------------------------------------------
+// host side: rotary positions of several axes
+// ---------------------------------------------------------------------------
 
-extern "C" {
-
-msa_status msa_producer_validate(const msa_producer_cfg *cfg, int64_t num_tokens, const void *qkv,
-                                 int64_t qkv_row_stride, const int32_t *positions,
-                                 const int64_t *slot_mapping, const int32_t *page_table,
-                                 int64_t page_table_len, const void *q_norm_w, const void *k_norm_w,
-                                 const void *idx_q_norm_w, const void *idx_k_norm_w, void *q_out,
-                                 void *idx_q_out, const msa_cache_desc *k_cache,
-                                 const msa_cache_desc *v_cache, const msa_cache_desc *idx_k_cache,
-                                 const float *scales, int32_t launch_flags)
+// The checks of msa_producer_axes_forward beside the producer's.
+msa_status validate_axes(const msa_producer_cfg *cfg, const msa_rope_axes *axes, int64_t T, int64_t positions_stride)
 {
-    return validate(cfg, num_tokens, qkv, qkv_row_stride, positions, slot_mapping, page_table,
-                    page_table_len, q_norm_w, k_norm_w, idx_q_norm_w, idx_k_norm_w, q_out,
-                    idx_q_out, k_cache, v_cache, idx_k_cache, scales, launch_flags);
+    const int half = cfg->rotary_dim / 2;
+    if (axes->num_axes < 1)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "num_axes %d", axes->num_axes);
+    if (axes->num_axes > MSA_ROPE_MAX_AXES)
+        return fail(MSA_ERR_UNSUPPORTED, "num_axes %d (at most %d)", axes->num_axes, MSA_ROPE_MAX_AXES);
+    if (axes->restart != 0 && axes->restart != 1)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "restart %d (0 or 1)", axes->restart);
+    if (axes->reserved[0] != 0 || axes->reserved[1] != 0)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "axes reserved fields must be 0");
+    for (int k = 0; k < kMaxRotaryHalf; ++k)
+        if (axes->pair_axis[k] >= (k < half ? axes->num_axes : 1))
+            return fail(MSA_ERR_INVALID_ARGUMENT, "pair_axis[%d] is %d (%d pairs, %d axes)", k, axes->pair_axis[k],
+                        half, axes->num_axes);
+    if (T > 0 && positions_stride < T)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "positions_stride %lld < num_tokens %lld", (long long)positions_stride,
+                    (long long)T);
+    int64_t tmp;
+    if (!mul_add_ok(positions_stride, (int64_t)axes->num_axes * 4, 0, &tmp))
+        return fail(MSA_ERR_OFFSET_OVERFLOW, "positions_stride overflows int64");
+    return MSA_OK;
 }
 
-msa_status msa_producer_forward(const msa_producer_cfg *cfg, int64_t num_tokens, const void *qkv,
-                                int64_t qkv_row_stride, const int32_t *positions,
-                                const int64_t *slot_mapping, const int32_t *page_table,
-                                int64_t page_table_len, const void *q_norm_w, const void *k_norm_w,
-                                const void *idx_q_norm_w, const void *idx_k_norm_w, void *q_out,
-                                void *idx_q_out, const msa_cache_desc *k_cache,
-                                const msa_cache_desc *v_cache, const msa_cache_desc *idx_k_cache,
-                                const float *scales, int32_t launch_flags, cudaStream_t stream)
+// The axis of each pair, and its frequency in 2^-64 turns a position.
+void fill_axes(AxesParams &p, const msa_producer_cfg *cfg, const msa_rope_axes *axes)
+{
+    const int half = cfg->rotary_dim / 2;
+    int count[MSA_ROPE_MAX_AXES] = {}, seen[MSA_ROPE_MAX_AXES] = {};
+    for (int k = 0; k < half; ++k)
+        ++count[axes->pair_axis[k]];
+    for (int k = 0; k < half; ++k) {
+        const int a = axes->pair_axis[k];
+        const double e = axes->restart ? (double)seen[a]++ / count[a] : (double)k / half;
+        const double turns = std::fmod(std::pow((double)cfg->rope_theta, -e) * 0.15915494309189533577, 1.0);
+        p.axis[k] = (uint8_t)a;
+        p.turns[k] = (uint64_t)std::ldexp(turns, 64);
+    }
+}
+
+// Both entry points: axes is nullptr for positions of one axis.
+msa_status launch(const msa_rope_axes *axes, int64_t positions_stride, const msa_producer_cfg *cfg, int64_t num_tokens, const void *qkv, int64_t qkv_row_stride,
+                  const int32_t *positions, const int64_t *slot_mapping, const int32_t *page_table,
+                  int64_t page_table_len, const void *q_norm_w, const void *k_norm_w,
+                  const void *idx_q_norm_w, const void *idx_k_norm_w, void *q_out, void *idx_q_out,
+                  const msa_cache_desc *k_cache, const msa_cache_desc *v_cache,
+                  const msa_cache_desc *idx_k_cache, const float *scales, int32_t launch_flags,
+                  cudaStream_t stream)
 {
     msa_status s = validate(cfg, num_tokens, qkv, qkv_row_stride, positions, slot_mapping,
                             page_table, page_table_len, q_norm_w, k_norm_w, idx_q_norm_w,
                             idx_k_norm_w, q_out, idx_q_out, k_cache, v_cache, idx_k_cache, scales,
                             launch_flags);
+    if (s == MSA_OK && axes)
+        s = validate_axes(cfg, axes, num_tokens, positions_stride);
     if (s != MSA_OK || num_tokens == 0)
         return s;
 
-    Params p;
-    memset(&p, 0, sizeof p);
+    AxesParams p;    // its Params alone where there are no axes
+    memset(static_cast<void *>(&p), 0, sizeof p);
     p.qkv = static_cast<const uint16_t *>(qkv);
     p.row_stride = qkv_row_stride;
     p.positions = positions;
@@ -1060,6 +1173,10 @@ msa_status msa_producer_forward(const msa_producer_cfg *cfg, int64_t num_tokens,
                                                 cfg->page_size);
 #endif
     p.rms_eps = cfg->rms_eps;
+    if (axes) {
+        p.positions_stride = positions_stride;
+        fill_axes(p, cfg, axes);
+    }
     // RoPE frequencies theta^(-2k/rd), evaluated in double and rounded once
     for (int k = 0; k < cfg->rotary_dim / 2; ++k)
         p.inv_freq[k] = (float)(1.0 / std::pow((double)cfg->rope_theta,
@@ -1067,7 +1184,7 @@ msa_status msa_producer_forward(const msa_producer_cfg *cfg, int64_t num_tokens,
 
     Variant v;
     int grid = 0, smem = 0;
-    s = launch_shape(cfg, num_tokens, launch_flags, &v, &grid, &smem);
+    s = launch_shape(cfg, num_tokens, launch_flags, &v, &grid, &smem, axes != nullptr);
     if (s != MSA_OK)
         return s;
 
@@ -1084,11 +1201,59 @@ msa_status msa_producer_forward(const msa_producer_cfg *cfg, int64_t num_tokens,
         lc.attrs = attr;
         lc.numAttrs = 1;
     }
-    void *args[] = {&p};
+    void *args[] = {axes ? static_cast<void *>(&p) : static_cast<Params *>(&p)};
     cudaError_t e = cudaLaunchKernelExC(&lc, v.fn, args);
     if (e != cudaSuccess)
         return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
     return MSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+msa_status msa_producer_validate(const msa_producer_cfg *cfg, int64_t num_tokens, const void *qkv,
+                                 int64_t qkv_row_stride, const int32_t *positions,
+                                 const int64_t *slot_mapping, const int32_t *page_table,
+                                 int64_t page_table_len, const void *q_norm_w, const void *k_norm_w,
+                                 const void *idx_q_norm_w, const void *idx_k_norm_w, void *q_out,
+                                 void *idx_q_out, const msa_cache_desc *k_cache,
+                                 const msa_cache_desc *v_cache, const msa_cache_desc *idx_k_cache,
+                                 const float *scales, int32_t launch_flags)
+{
+    return validate(cfg, num_tokens, qkv, qkv_row_stride, positions, slot_mapping, page_table,
+                    page_table_len, q_norm_w, k_norm_w, idx_q_norm_w, idx_k_norm_w, q_out,
+                    idx_q_out, k_cache, v_cache, idx_k_cache, scales, launch_flags);
+}
+
+msa_status msa_producer_forward(const msa_producer_cfg *cfg, int64_t num_tokens, const void *qkv,
+                                int64_t qkv_row_stride, const int32_t *positions,
+                                const int64_t *slot_mapping, const int32_t *page_table,
+                                int64_t page_table_len, const void *q_norm_w, const void *k_norm_w,
+                                const void *idx_q_norm_w, const void *idx_k_norm_w, void *q_out,
+                                void *idx_q_out, const msa_cache_desc *k_cache,
+                                const msa_cache_desc *v_cache, const msa_cache_desc *idx_k_cache,
+                                const float *scales, int32_t launch_flags, cudaStream_t stream)
+{
+    return launch(nullptr, 0, cfg, num_tokens, qkv, qkv_row_stride, positions, slot_mapping, page_table,
+                  page_table_len, q_norm_w, k_norm_w, idx_q_norm_w, idx_k_norm_w, q_out, idx_q_out, k_cache,
+                  v_cache, idx_k_cache, scales, launch_flags, stream);
+}
+
+msa_status msa_producer_axes_forward(const msa_producer_cfg *cfg, const msa_rope_axes *axes, int64_t num_tokens,
+                                     const void *qkv, int64_t qkv_row_stride, const int32_t *positions,
+                                     int64_t positions_stride, const int64_t *slot_mapping,
+                                     const int32_t *page_table, int64_t page_table_len, const void *q_norm_w,
+                                     const void *k_norm_w, const void *idx_q_norm_w, const void *idx_k_norm_w,
+                                     void *q_out, void *idx_q_out, const msa_cache_desc *k_cache,
+                                     const msa_cache_desc *v_cache, const msa_cache_desc *idx_k_cache,
+                                     const float *scales, int32_t launch_flags, cudaStream_t stream)
+{
+    if (!axes)
+        return fail(MSA_ERR_INVALID_ARGUMENT, "axes is NULL");
+    return launch(axes, positions_stride, cfg, num_tokens, qkv, qkv_row_stride, positions, slot_mapping, page_table,
+                  page_table_len, q_norm_w, k_norm_w, idx_q_norm_w, idx_k_norm_w, q_out, idx_q_out, k_cache,
+                  v_cache, idx_k_cache, scales, launch_flags, stream);
 }
 
 msa_status msa_producer_launch_shape(const msa_producer_cfg *cfg, int64_t num_tokens,

@@ -1,0 +1,259 @@
+"""Low-rank adapters beside a packed projection against their formula in 64 bits (GPU).
+
+Tolerance.  With A = sum_i |up| sum_k |hidden| |down| (times the scales), fp32 sums of K and of rank
+products are off by at most (K + rank + 8) 2^-24 A, and u's two bf16 parts by 2^-16 A; then the
+output's rounding, 2^-8 of it."""
+import pytest
+import torch
+
+from paged_kv_cache_msa_gb300 import binding as B
+from paged_kv_cache_msa_gb300 import build as build_mod
+
+pytestmark = pytest.mark.gpu
+
+PACKED = (8192, 9216, 10240, 11264, 11392)      # the big shapes' sections
+SMALL = (512, 640, 768, 896, 960)               # the small shapes'
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build_mod.build()
+    return B.load()
+
+
+def wide(x, pad, fill):
+    """The same rows, 16 * pad elements further apart than whole vectors need, `fill` between."""
+    t, k = x.shape
+    w = torch.full((t, -(-k // 16) * 16 + 16 * pad), 0, dtype=torch.uint8, device="cuda").to(x.dtype)
+    w.view(torch.uint8).fill_(fill)
+    w[:, :k] = x
+    return w[:, :k]
+
+
+class Case:
+    def __init__(self, ids, k=256, ends=SMALL, rank=16, adapters=4, fp8=False, scaled=True, pad=0, seed=0, alpha=True):
+        self.ids = torch.tensor(ids, dtype=torch.int32, device="cuda")
+        t, w, s = len(ids), ends[-1], len(ends)
+        self.n, self.k, self.ends, self.rank, self.adapters = t, k, ends, rank, adapters
+        gen = torch.Generator(device="cuda").manual_seed(91 + seed)
+        x = torch.randn(t, k, generator=gen, device="cuda") * 2
+        x = x.to(torch.float8_e4m3fn) if fp8 else x.bfloat16()
+        self.hidden = wide(x, pad, 0x7F)                    # NaN behind the rows
+        self.hidden_scales = 0.1 + torch.rand(t, generator=gen, device="cuda") if scaled else None
+        d = torch.randn(adapters * s * rank, k, generator=gen, device="cuda") / k ** 0.5
+        self.down = wide(d.bfloat16(), pad, 0xFF).unflatten(0, (adapters, s * rank))
+        self.up = torch.randn(adapters, w, rank, generator=gen, device="cuda").bfloat16()
+        self.alpha = torch.randn(adapters, generator=gen, device="cuda") if alpha else None
+        self.rows = wide((3 * torch.randn(t, w, generator=gen, device="cuda")).bfloat16(), pad, 0x21)
+        self.raw = torch.full((t + 2, -(-w // 16) * 16 + 16 * pad), 0, dtype=torch.int16, device="cuda").fill_(0x4242)
+        self.out = self.raw.view(torch.bfloat16)[1:-1, :w]
+        self.cfg = B.make_adapter_cfg(k, ends, rank, adapters, B.MSA_DTYPE_FP8_E4M3 if fp8 else B.MSA_DTYPE_BF16)
+        n = B.msa_adapter_workspace_bytes(self.cfg, t)
+        self.ws_raw = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")    # NaN
+        self.ws = self.ws_raw[256:256 + n]
+
+    def run(self, flags=0, stream=None, out=None, workspace="own"):
+        B.adapter_tensors(self.cfg, self.hidden, self.down, self.up, self.ids, self.rows, self.out if out is None else out,
+                          hidden_scales=self.hidden_scales, adapter_scales=self.alpha,
+                          workspace=self.ws if workspace == "own" else workspace, launch_flags=flags, stream=stream)
+        return self
+
+    def formula(self, rows=None):
+        """out, and what its tolerance goes by, in 64 bits."""
+        rows = self.rows if rows is None else rows
+        x = self.hidden.to(torch.float64)
+        if self.hidden_scales is not None:
+            x = x * self.hidden_scales.double()[:, None]
+        out, size = rows.double().clone(), torch.zeros(self.n, self.ends[-1], dtype=torch.float64, device="cuda")
+        start = [0, *self.ends]
+        for a in range(self.adapters):
+            on = self.ids == a
+            c = 1.0 if self.alpha is None else float(self.alpha[a])
+            for s in range(len(self.ends)):
+                d = self.down[a, s * self.rank:(s + 1) * self.rank].double()
+                up, cols = self.up[a, start[s]:start[s + 1]].double(), slice(start[s], start[s + 1])
+                out[on, cols] += c * (x[on] @ d.T @ up.T)
+                size[on, cols] = abs(c) * (x[on].abs() @ d.abs().T @ up.abs().T)
+        return out, size
+
+    def check(self, out=None, rows=None):
+        got = self.out if out is None else out
+        want, size = self.formula(rows)
+        tol = 2.0 ** -8 * want.abs() + size * ((self.k + self.rank + 8) * 2.0 ** -24 + 2.0 ** -16)
+        off = ((got.double() - want).abs() - tol)
+        assert (off <= 0).all(), float(off.max())
+        none = (self.ids < 0) | (self.ids >= self.adapters)
+        base = self.rows if rows is None else rows
+        assert torch.equal(got[none].view(torch.int16), base[none].view(torch.int16))
+        assert (self.raw[0] == 0x4242).all() and (self.raw[-1] == 0x4242).all()
+        assert (self.raw[1:-1, self.ends[-1]:] == 0x4242).all()
+        assert (self.ws_raw[:256] == 0xFF).all() and (self.ws_raw[-256:] == 0xFF).all()
+        return self
+
+
+def mixed(t, n, seed=5):
+    """Adapters in no order, ids outside on both sides among them."""
+    gen = torch.Generator().manual_seed(seed + t)
+    ids = torch.randint(-1, n + 1, (t,), generator=gen).tolist()
+    if t > 3:
+        ids[2], ids[3] = 2**31 - 1, -2**31
+    return ids
+
+
+def runs(t, n):
+    return [(i * (n + 1)) // t - 1 for i in range(t)]
+
+
+@pytest.mark.parametrize("t", [1, 2, 15, 16, 17, 64, 127, 128, 129, 300, 1000])
+@pytest.mark.parametrize("order", [mixed, runs], ids=["mixed", "runs"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_batches(t, order, fp8):
+    Case(order(t, 4), fp8=fp8, seed=t).run().check()
+
+
+@pytest.mark.parametrize("k", [1, 5, 8, 16, 40, 63, 64, 65, 127, 200, 1000, 1001, 2049, 6144])
+@pytest.mark.parametrize("t", [5, 400])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_hidden_sizes(k, t, fp8):
+    Case(runs(t, 3), k=k, adapters=3, fp8=fp8, pad=1, seed=k).run().check()
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 56, 64, 96, 128])
+@pytest.mark.parametrize("t", [3, 150, 700])
+@pytest.mark.parametrize("ends", [(960,), (64, 72), (64, 640, 704, 1024)], ids=str)
+def test_ranks_and_slices(rank, t, ends):
+    Case(runs(t, 4), k=320, ends=ends, rank=rank, seed=rank).run().check()
+
+
+@pytest.mark.parametrize("ends", [(8,), (64,), (56,), (64, 128, 192, 256, 320, 384, 448, 456), (200,), (1000,), (4096, 4104)], ids=str)
+@pytest.mark.parametrize("t", [1, 33, 260])
+def test_widths(ends, t):
+    Case(mixed(t, 4), k=96, ends=ends, rank=8, pad=2, seed=t).run().check()
+
+
+@pytest.mark.parametrize("t", [1, 64, 2048])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_packed_projection(t, fp8):
+    """The big shapes' hidden size and packed row."""
+    Case(mixed(t, 24) if t <= 64 else runs(t, 5), k=6144, ends=PACKED, adapters=24, fp8=fp8).run().check()
+
+
+def test_many_adapters_in_one_batch():
+    Case([i % 130 for i in range(260)], k=128, rank=8, adapters=130).run().check()
+    Case([i % 130 for i in range(520)], k=128, rank=8, adapters=130).run().check()
+
+
+@pytest.mark.parametrize("t", [1, 40, 600])
+def test_one_adapter_and_none(t):
+    Case([0] * t, adapters=1).run().check()
+    Case([-1] * t, adapters=1).run().check()
+    Case([7] * t, adapters=1).run().check()
+
+
+@pytest.mark.parametrize("kw", [dict(scaled=False), dict(alpha=False), dict(scaled=False, alpha=False, fp8=True)], ids=str)
+def test_without_scales(kw):
+    Case(mixed(50, 4), **kw).run().check()
+    Case(runs(500, 4), **kw).run().check()
+
+
+@pytest.mark.parametrize("t", [6, 64, 300, 1200])
+def test_in_place(t):
+    c = Case(mixed(t, 4), pad=1).run().check()
+    rows = c.rows.clone()
+    want = c.out.clone()
+    c.run(out=c.rows)
+    assert torch.equal(c.rows, want)
+    c.check(out=c.rows, rows=rows)
+
+
+@pytest.mark.parametrize("t", [20, 64, 300, 1000])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_one_requests_values_stay_its_own(t, bad):
+    """What is not finite in an adapter, in a request's hidden states, scales or rows reaches only the
+    rows of that adapter or request."""
+    for what in ("down", "up", "alpha", "hidden", "hidden_scales", "rows"):
+        c = Case(mixed(t, 4), pad=1)
+        c.run()
+        clean = c.out.clone()
+        if what in ("down", "up", "alpha"):
+            getattr(c, what)[2] = bad
+            mine = c.ids == 2
+        else:
+            getattr(c, what)[1] = bad
+            mine = torch.arange(t, device="cuda") == 1
+        c.run()
+        assert torch.equal(c.out[~mine].view(torch.int16), clean[~mine].view(torch.int16)), what
+        touched = mine & (c.ids >= 0) & (c.ids < 4) if what != "rows" else mine
+        assert not c.out[touched].isfinite().any(), what
+
+
+def test_repeated_calls_give_the_same_bits():
+    for t in (64, 900):
+        c = Case(mixed(t, 4), k=1000).run()
+        first = c.out.clone()
+        c.ws.fill_(0x7F)
+        c.out.zero_()
+        c.run()
+        assert torch.equal(first.view(torch.int16), c.out.view(torch.int16))
+
+
+def test_no_tokens_and_own_workspace():
+    c = Case([0, 1, 2])
+    c.run(workspace=None).check()
+    e = Case([])
+    e.run(workspace=None)
+
+
+def test_other_stream_and_graph():
+    """On a stream of its own behind the work that makes the rows; captured and replayed with other
+    rows and other requests' adapters in the same tensors."""
+    for t in (64, 500):
+        c = Case(mixed(t, 4), k=512)
+        s = torch.cuda.Stream()
+        keep = c.rows.clone()
+        for flags in (0, B.MSA_LAUNCH_PDL):
+            c.rows.zero_()
+            c.out.zero_()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(2_000_000)
+                c.rows.copy_(keep)
+                c.run(flags)
+            s.synchronize()
+            c.check()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                c.run(flags)
+                c.run(flags)
+            for ids in (mixed(t, 4, seed=8), [-1] * t, runs(t, 4), mixed(t, 4)):
+                c.ids.copy_(torch.tensor(ids, dtype=torch.int32))
+                g.replay()
+                torch.cuda.synchronize()
+                c.check()
+
+
+def test_two_streams_with_their_own_workspaces():
+    cases = [Case(runs(700, 4), k=1024, seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(cases, streams):
+            c.run(stream=s)
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    c = Case([0, 1, 2, 3])
+    good = dict(cfg=c.cfg, hidden=c.hidden, down=c.down, up=c.up, adapter_ids=c.ids, rows=c.rows, out=c.out,
+                hidden_scales=c.hidden_scales, adapter_scales=c.alpha, workspace=c.ws)
+    B.adapter_tensors(**good)
+    for bad in (dict(hidden=c.hidden[:, :-1]), dict(hidden=c.hidden.float()), dict(down=c.down[:3]), dict(down=c.down[:, ::2]),
+                dict(up=c.up.transpose(1, 2)), dict(adapter_ids=c.ids.long()), dict(rows=c.rows[:3]), dict(out=c.out.cpu()),
+                dict(hidden_scales=c.hidden_scales[:3]), dict(adapter_scales=c.alpha.double()), dict(workspace=c.ws.cpu()),
+                dict(down=c.down[0])):
+        with pytest.raises(ValueError):
+            B.adapter_tensors(**dict(good, **bad))
+    with pytest.raises(B.MsaError):
+        B.adapter_tensors(**dict(good, workspace=c.ws[:256]))

@@ -1,12 +1,16 @@
 // Low-rank adapters of many requests beside a shared projection (include/msa_adapter.h).
 //
-// Two kernels: the down-projection of every token with its own adapter into a workspace, and
-// the up-projection added to the rows.
+// Two kernels: every token's hidden state through its own adapter's down-projection into a
+// workspace (partial sums over pieces of K), and the up-projection of their sum added to the
+// rows.  Both take tiles of 16 tokens in any order and go through the distinct adapters of a
+// tile, one MMA (m16n8k16) tile of 16 tokens for each: a token of another adapter has a row of
+// its own in the MMA, which is left out, so nothing passes from one request to another.
+// Reading an adapter is what a decode batch costs (65 MB for 64 tokens over 48 adapters of
+// rank 16), and reading and writing the rows what a prefill costs; both are bound by HBM.
 
 #include "msa_adapter.h"
 #include "msa_internal.h"
 
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <cstdarg>
@@ -16,6 +20,10 @@
 
 namespace {
 
+constexpr int kTile = 16;            // tokens of a tile: the MMA's M
+constexpr int kDownWarps = 8;        // warps of a CTA of the down-projection, each a piece of its K
+constexpr int kUnitK = 64;           // K elements a warp takes at a time: 128 bytes of bf16
+
 struct Params {
     const uint8_t *hidden;
     const float *hidden_scales;
@@ -24,73 +32,319 @@ struct Params {
     const float *adapter_scales;
     const uint16_t *rows;
     uint16_t *out;
-    float *u;                        // [T, S * r]
+    float *u;                        // [splits, T, S * r]: sums over pieces of K
     int64_t hidden_stride, down_stride, rows_stride, out_stride;   // elements
     int64_t num_tokens;
     int32_t hidden_size, width, rank, num_adapters, num_slices, fp8;
+    int32_t splits;                  // pieces of K
+    int32_t n_blocks, n_tiles;       // blocks of down rows, tiles of 8 rows in a block
+    int32_t chunk;                   // columns of a warp's share of the up-projection
     int32_t slice_end[MSA_ADAPTER_MAX_SLICES];
 };
 
-__device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
-
-__device__ __forceinline__ uint16_t f32_to_bf16(float x)
+__device__ __forceinline__ float2 unpack2(uint32_t v)
 {
-    uint16_t h;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
-    return h;
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
-// A warp for each (token, row of down): lanes along K.
-__global__ void __launch_bounds__(256) msa_adapter_down_kernel(const __grid_constant__ Params p)
+// (x0, x1) -> a bf16 pair, x0 in the low half
+__device__ __forceinline__ uint32_t pack_bf16x2(float x0, float x1)
 {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
+    return d;
+}
+
+// Two E4M3 codes (the low half of c) -> a bf16 pair: exact, since bf16 holds every E4M3 value.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
+    float lo, hi;
+    asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The adapters of a tile of 16 tokens: a lane's token is lane % 16.
+struct Tile {
+    int id;              // this lane's adapter, -1: none
+    uint32_t same;       // the tile's tokens with the same one
+    uint32_t leaders;    // the first token of each distinct adapter
+};
+
+__device__ __forceinline__ Tile tile_of(const Params &p, int64_t t0)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t t = t0 + (lane & 15);
+    Tile w;
+    w.id = t < p.num_tokens ? p.ids[t] : -1;
+    if (w.id < 0 || w.id >= p.num_adapters)
+        w.id = -1;
+    w.same = __match_any_sync(0xffffffffu, w.id) & 0xffffu;
+    w.leaders = __ballot_sync(0xffffffffu, w.id >= 0 && lane == __ffs(w.same) - 1);
+    return w;
+}
+
+// 8 elements of a row from k on as bf16 pairs, zeros from K on; k is a multiple of 8.
+template <bool FP8>
+__device__ __forceinline__ uint4 load_hidden(const Params &p, int64_t row, int k)
+{
+    const int n = p.hidden_size - k;
+    if (n <= 0)
+        return make_uint4(0, 0, 0, 0);
+    if (FP8) {
+        const uint8_t *src = p.hidden + row * p.hidden_stride + k;
+        uint2 c = make_uint2(0, 0);
+        if (n >= 8)
+            c = __ldg(reinterpret_cast<const uint2 *>(src));
+        else
+            for (int j = 0; j < n; ++j)
+                (j < 4 ? c.x : c.y) |= (uint32_t)src[j] << (8 * (j & 3));
+        return make_uint4(e4m3x2_to_bf16x2(c.x & 0xffffu), e4m3x2_to_bf16x2(c.x >> 16),
+                          e4m3x2_to_bf16x2(c.y & 0xffffu), e4m3x2_to_bf16x2(c.y >> 16));
+    }
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.hidden) + row * p.hidden_stride + k;
+    if (n >= 8)
+        return __ldg(reinterpret_cast<const uint4 *>(src));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (j < n)
+            w[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 load_down(const Params &p, const uint16_t *row, int k)
+{
+    const int n = p.hidden_size - k;
+    if (n >= 8)
+        return __ldg(reinterpret_cast<const uint4 *>(row + k));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (j < n)
+            w[j / 2] |= (uint32_t)row[k + j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------
+// the down-projection of a tile of 16 tokens
+// ---------------------------------------------------------------------------
+//
+// A CTA takes one distinct adapter of a tile (blockIdx.y), a block of up to 8 * NT of its rows
+// and a piece of K, which its warps share; their sums meet in shared memory.  A lane holds 8
+// neighbouring elements of K of a token's row and of an adapter's row: the MMA's order of K
+// is free as long as both operands agree, so 16-byte loads are its fragments as they come.
+template <bool FP8, int NT>
+__global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const __grid_constant__ Params p)
+{
+    __shared__ float s_sum[kDownWarps][kTile][8 * NT];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int64_t t = blockIdx.x;
-    const int a = p.ids[t];
-    if (a < 0 || a >= p.num_adapters)
-        return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int64_t t0 = (int64_t)blockIdx.x * kTile;
+    const Tile tile = tile_of(p, t0);
+    uint32_t left = tile.leaders;
+    for (unsigned j = 0; j < blockIdx.y; ++j)
+        left &= left - 1;
+    if (!left)
+        return;                      // the tile has fewer adapters
+    const int leader = __ffs(left) - 1;
+    const int a = __shfl_sync(0xffffffffu, tile.id, leader);
+    const uint32_t mine = __shfl_sync(0xffffffffu, tile.same, leader);
+    const bool row0 = (mine >> g) & 1, row1 = (mine >> (g + 8)) & 1;
+
     const int n = p.num_slices * p.rank;
-    const float c = (p.hidden_scales ? p.hidden_scales[t] : 1.0f) * (p.adapter_scales ? p.adapter_scales[a] : 1.0f);
-    for (int i = threadIdx.x / 32; i < n; i += 8) {
-        const uint16_t *row = p.down + ((int64_t)a * n + i) * p.down_stride;
-        float s = 0.0f;
-        for (int k = threadIdx.x % 32; k < p.hidden_size; k += 32) {
-            const int64_t e = t * p.hidden_stride + k;
-            __nv_fp8_e4m3 code;
-            code.__x = p.fp8 ? p.hidden[e] : 0;
-            const float x = p.fp8 ? float(code) : bf16_to_f32(reinterpret_cast<const uint16_t *>(p.hidden)[e]);
-            s = fmaf(x, bf16_to_f32(row[k]), s);
+    const int block = blockIdx.z % p.n_blocks, split = blockIdx.z / p.n_blocks;
+    const int n0 = block * p.n_tiles * 8;
+    const uint16_t *rows[NT];        // nullptr: none
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int r = n0 + 8 * i + g;
+        rows[i] = i < p.n_tiles && r < n ? p.down + ((int64_t)a * n + r) * p.down_stride : nullptr;
+    }
+    const int units = (p.hidden_size + kUnitK - 1) / kUnitK;
+    const int piece = split * kDownWarps + warp, pieces = p.splits * kDownWarps;
+    const int first = (int)((int64_t)units * piece / pieces), last = (int)((int64_t)units * (piece + 1) / pieces);
+
+    float acc[NT][4] = {};
+    for (int u = first; u < last; ++u) {
+        uint4 x[2][2], w[NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = u * kUnitK + 32 * h + 8 * q;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                w[i][h] = rows[i] ? load_down(p, rows[i], k) : none;
+            x[0][h] = row0 ? load_hidden<FP8>(p, t0 + g, k) : none;
+            x[1][h] = row1 ? load_hidden<FP8>(p, t0 + g + 8, k) : none;
         }
-        for (int o = 16; o > 0; o >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (threadIdx.x % 32 == 0)
-            p.u[t * n + i] = s * c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t lo[4] = {x[0][h].x, x[1][h].x, x[0][h].y, x[1][h].y};
+            const uint32_t hi[4] = {x[0][h].z, x[1][h].z, x[0][h].w, x[1][h].w};
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                mma(acc[i], lo, w[i][h].x, w[i][h].y);
+                mma(acc[i], hi, w[i][h].z, w[i][h].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        *reinterpret_cast<float2 *>(&s_sum[warp][g][8 * i + 2 * q]) = make_float2(acc[i][0], acc[i][1]);
+        *reinterpret_cast<float2 *>(&s_sum[warp][g + 8][8 * i + 2 * q]) = make_float2(acc[i][2], acc[i][3]);
+    }
+    __syncthreads();
+    const float c = p.adapter_scales ? p.adapter_scales[a] : 1.0f;
+    for (int e = threadIdx.x; e < kTile * 8 * NT; e += 32 * kDownWarps) {
+        const int r = e / (8 * NT), i = e % (8 * NT);
+        if (!((mine >> r) & 1) || i >= 8 * p.n_tiles || n0 + i >= n)
+            continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kDownWarps; ++v)
+            sum += s_sum[v][r][i];
+        const int64_t t = t0 + r;
+        p.u[((int64_t)split * p.num_tokens + t) * n + n0 + i] = sum * c * (p.hidden_scales ? p.hidden_scales[t] : 1.0f);
     }
 }
 
-// A thread for each output.
+// ---------------------------------------------------------------------------
+// the up-projection, added to the rows
+// ---------------------------------------------------------------------------
+//
+// A warp takes a tile of 16 tokens and `chunk` columns, 32 at a time (a slice ends at a multiple
+// of 64).  Column 8 (n / 2) + 2 i + n % 2 of the 32 is column n of the MMA's i-th tile, so that a
+// lane's four accumulators of a row are 8 neighbouring columns: 16-byte loads and stores of the
+// rows.  u is summed over the pieces of K, in their order, and split into two bf16 parts: one
+// would put an error of 2^-9 of the adapter's share on every output.  RC: ceil(rank / 16).
+template <int RC>
 __global__ void __launch_bounds__(256) msa_adapter_up_kernel(const __grid_constant__ Params p)
 {
+    constexpr int AU = RC == 1 ? 4 : RC == 2 ? 2 : 1;     // adapters whose rows are loaded together
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int64_t t = blockIdx.x;
-    const int a = p.ids[t];
-    const bool on = a >= 0 && a < p.num_adapters;
-    for (int j = threadIdx.x; j < p.width; j += 256) {
-        const uint16_t r = p.rows[t * p.rows_stride + j];
-        if (!on) {
-            p.out[t * p.out_stride + j] = r;
-            continue;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
+    const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t0 = item % tiles * kTile;
+    const int64_t from = item / tiles * p.chunk;
+    if (from >= p.width)
+        return;
+    const int end = (int)min((int64_t)p.width, from + p.chunk);
+    const Tile tile = tile_of(p, t0);
+    const int id[2] = {__shfl_sync(0xffffffffu, tile.id, g), __shfl_sync(0xffffffffu, tile.id, g + 8)};
+    const bool copy = p.out != p.rows;
+    const int n = p.num_slices * p.rank;
+
+    uint32_t hi[RC][4], lo[RC][4];
+    int slice = -1;
+    for (int c = (int)from; c < end; c += 32) {
+        const int col = c + 8 * q;
+        uint4 row[2] = {};
+        bool put[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t t = t0 + g + 8 * h;
+            put[h] = t < p.num_tokens && col < end && (copy || id[h] >= 0);
+            if (put[h])
+                row[h] = *reinterpret_cast<const uint4 *>(p.rows + t * p.rows_stride + col);
         }
-        int s = 0;
-        while (j >= p.slice_end[s])
-            ++s;
-        const uint16_t *up = p.up + ((int64_t)a * p.width + j) * p.rank;
-        const float *u = p.u + (t * p.num_slices + s) * p.rank;
-        float d = 0.0f;
-        for (int i = 0; i < p.rank; ++i)
-            d = fmaf(u[i], bf16_to_f32(up[i]), d);
-        p.out[t * p.out_stride + j] = f32_to_bf16(bf16_to_f32(r) + d);
+        if (slice < 0 || c >= p.slice_end[slice]) {
+            do
+                ++slice;
+            while (c >= p.slice_end[slice]);
+#pragma unroll
+            for (int k = 0; k < RC; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (id[h] >= 0 && 16 * k + 4 * q < p.rank) {
+                        const float *src = p.u + (t0 + g + 8 * h) * n + slice * p.rank + 16 * k + 4 * q;
+                        for (int s = 0; s < p.splits; ++s) {
+                            const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)s * p.num_tokens * n);
+                            u = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+                        }
+                    }
+                    const uint32_t a = pack_bf16x2(u.x, u.y), b = pack_bf16x2(u.z, u.w);
+                    const float2 a2 = unpack2(a), b2 = unpack2(b);
+                    // (an infinite part has no remainder)
+                    auto rest = [](float v, float part) { return isinf(part) ? 0.0f : v - part; };
+                    hi[k][h] = a;
+                    hi[k][h + 2] = b;
+                    lo[k][h] = pack_bf16x2(rest(u.x, a2.x), rest(u.y, a2.y));
+                    lo[k][h + 2] = pack_bf16x2(rest(u.z, b2.x), rest(u.w, b2.y));
+                }
+        }
+        float sum[4][4] = {};
+        for (uint32_t left = tile.leaders; left;) {
+            int ad[AU];
+            uint2 b[AU][4][RC];
+#pragma unroll
+            for (int j = 0; j < AU; ++j) {
+                const int leader = left ? __ffs(left) - 1 : 0;
+                ad[j] = left ? __shfl_sync(0xffffffffu, tile.id, leader) : -2;
+                left &= left - 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = c + 8 * (g >> 1) + 2 * i + (g & 1);
+#pragma unroll
+                    for (int k = 0; k < RC; ++k) {
+                        b[j][i][k] = make_uint2(0, 0);
+                        if (ad[j] >= 0 && r < end && 16 * k + 4 * q < p.rank)
+                            b[j][i][k] = __ldg(reinterpret_cast<const uint2 *>(
+                                p.up + ((int64_t)ad[j] * p.width + r) * p.rank + 16 * k + 4 * q));
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < AU; ++j) {
+                if (ad[j] < 0)
+                    break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float acc[4] = {};
+#pragma unroll
+                    for (int k = 0; k < RC; ++k) {
+                        mma(acc, hi[k], b[j][i][k].x, b[j][i][k].y);
+                        mma(acc, lo[k], b[j][i][k].x, b[j][i][k].y);
+                    }
+                    if (id[0] == ad[j]) {
+                        sum[i][0] = acc[0];
+                        sum[i][1] = acc[1];
+                    }
+                    if (id[1] == ad[j]) {
+                        sum[i][2] = acc[2];
+                        sum[i][3] = acc[3];
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!put[h])
+                continue;
+            uint32_t w[4] = {row[h].x, row[h].y, row[h].z, row[h].w};
+            if (id[h] >= 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = unpack2(w[i]);
+                    w[i] = pack_bf16x2(v.x + sum[i][2 * h], v.y + sum[i][2 * h + 1]);
+                }
+            *reinterpret_cast<uint4 *>(p.out + (t0 + g + 8 * h) * p.out_stride + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
@@ -150,9 +404,30 @@ msa_status check_cfg(const msa_adapter_cfg *cfg, int64_t T)
 
 int width_of(const msa_adapter_cfg *cfg) { return cfg->slice_end[cfg->num_slices - 1]; }
 
+// How the down-projection's work is cut.
+struct Cut {
+    int n_blocks, n_tiles;   // blocks of at most 64 rows of down, tiles of 8 rows in each
+    int splits;              // pieces of K
+};
+
+Cut cut_of(const msa_adapter_cfg *cfg, int64_t T)
+{
+    Cut c;
+    const int tiles = cfg->num_slices * cfg->rank / 8;
+    c.n_blocks = (tiles + 7) / 8;
+    c.n_tiles = (tiles + c.n_blocks - 1) / c.n_blocks;
+    // so many pieces that a batch whose tokens all have adapters of their own fills the GPU, and
+    // no fewer than a unit of K for each warp
+    const int64_t units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
+    const int64_t most = (units + kDownWarps - 1) / kDownWarps, ctas = (T > 0 ? T : 1) * c.n_blocks;
+    const int64_t want = (2 * 152 + ctas - 1) / ctas;
+    c.splits = (int)(want < most ? want : most);
+    return c;
+}
+
 int64_t workspace_needed(const msa_adapter_cfg *cfg, int64_t T)
 {
-    return T * cfg->num_slices * cfg->rank * 4;
+    return cut_of(cfg, T).splits * T * cfg->num_slices * cfg->rank * 4;
 }
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -267,9 +542,35 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     p.num_slices = cfg->num_slices;
     p.fp8 = cfg->hidden_dtype == MSA_DTYPE_FP8_E4M3;
     memcpy(p.slice_end, cfg->slice_end, sizeof p.slice_end);
-    const msa_status d = launch(msa_adapter_down_kernel, dim3((unsigned)num_tokens), 256, 0,
+    const Cut c = cut_of(cfg, num_tokens);
+    p.splits = c.splits;
+    p.n_blocks = c.n_blocks;
+    p.n_tiles = c.n_tiles;
+    using Kernel = void (*)(Params);
+    static const Kernel downs[2][4] = {
+        {msa_adapter_down_kernel<false, 2>, msa_adapter_down_kernel<false, 4>, msa_adapter_down_kernel<false, 6>,
+         msa_adapter_down_kernel<false, 8>},
+        {msa_adapter_down_kernel<true, 2>, msa_adapter_down_kernel<true, 4>, msa_adapter_down_kernel<true, 6>,
+         msa_adapter_down_kernel<true, 8>}};
+    const int64_t tiles = (num_tokens + kTile - 1) / kTile;
+    const dim3 grid((unsigned)tiles, (unsigned)(num_tokens < kTile ? num_tokens : kTile),
+                    (unsigned)(c.n_blocks * c.splits));
+    const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], grid, 32 * kDownWarps, 0,
                                 launch_flags & MSA_LAUNCH_PDL, stream, p);
-    return d != MSA_OK ? d : launch(msa_adapter_up_kernel, dim3((unsigned)num_tokens), 256, 0, true, stream, p);
+    if (d != MSA_OK)
+        return d;
+
+    // Columns of a warp: so few that the warps fill the GPU, at most 256 (u is read once for them).
+    p.chunk = 32;
+    while (p.chunk < 256 && tiles * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152 * 8)
+        p.chunk *= 2;
+    const int64_t items = tiles * ((p.width + p.chunk - 1) / p.chunk);
+    const int warps = items < 2 * 152 ? 1 : items < 16 * 152 ? 4 : 8;
+    static const Kernel ups[4] = {msa_adapter_up_kernel<1>, msa_adapter_up_kernel<2>, msa_adapter_up_kernel<4>,
+                                  msa_adapter_up_kernel<8>};
+    const int rc = (p.rank + 15) / 16;
+    return launch(ups[rc <= 1 ? 0 : rc <= 2 ? 1 : rc <= 4 ? 2 : 3], dim3((unsigned)((items + warps - 1) / warps)),
+                  32 * warps, 0, true, stream, p);
 }
 
 }  // extern "C"

@@ -15,9 +15,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("msa_producer.cu", "msa_indexer.cu", "msa_projection.cu",
                                                     "msa_attention.cu", "msa_attention_decode.cu",
-                                                    "msa_attention_tile.cu", "msa_norm.cu", "msa_adapter.cu")]
+                                                    "msa_attention_tile.cu", "msa_norm.cu", "msa_adapter.cu",
+                                                    "msa_adapter_tile.cu")]
 HEADERS = [os.path.join(PKG, "csrc", n) for n in ("msa_internal.h", "msa_attention_internal.h",
-                                                    "msa_tcgen05.cuh")]
+                                                    "msa_adapter_internal.h", "msa_tcgen05.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB_NAME = "libmsa_producer.so"

@@ -8,8 +8,7 @@
 // Reading an adapter is what a decode batch costs (65 MB for 64 tokens over 48 adapters of
 // rank 16), and reading and writing the rows what a prefill costs; both are bound by HBM.
 
-#include "msa_adapter.h"
-#include "msa_internal.h"
+#include "msa_adapter_internal.h"
 
 #include <cuda_runtime.h>
 
@@ -22,49 +21,12 @@ namespace {
 
 constexpr int kTile = 16;            // tokens of a tile: the MMA's M
 constexpr int kDownWarps = 8;        // warps of a CTA of the down-projection, each a piece of its K
+constexpr int64_t kWideTokens = 256; // tokens from which the down-projection takes tiles of 128
 constexpr int kUnitK = 64;           // K elements a warp takes at a time: 128 bytes of bf16
-
-struct Params {
-    const uint8_t *hidden;
-    const float *hidden_scales;
-    const uint16_t *down, *up;
-    const int32_t *ids;
-    const float *adapter_scales;
-    const uint16_t *rows;
-    uint16_t *out;
-    float *u;                        // [splits, T, S * r]: sums over pieces of K
-    int64_t hidden_stride, down_stride, rows_stride, out_stride;   // elements
-    int64_t num_tokens;
-    int32_t hidden_size, width, rank, num_adapters, num_slices, fp8;
-    int32_t splits;                  // pieces of K
-    int32_t n_blocks, n_tiles;       // blocks of down rows, tiles of 8 rows in a block
-    int32_t chunk;                   // columns of a warp's share of the up-projection
-    int32_t slice_end[MSA_ADAPTER_MAX_SLICES];
-};
 
 __device__ __forceinline__ float2 unpack2(uint32_t v)
 {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
-
-// (x0, x1) -> a bf16 pair, x0 in the low half
-__device__ __forceinline__ uint32_t pack_bf16x2(float x0, float x1)
-{
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
-    return d;
-}
-
-// Two E4M3 codes (the low half of c) -> a bf16 pair: exact, since bf16 holds every E4M3 value.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c)
-{
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
-    float lo, hi;
-    asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    return pack_bf16x2(lo, hi);
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -82,7 +44,7 @@ struct Tile {
     uint32_t leaders;    // the first token of each distinct adapter
 };
 
-__device__ __forceinline__ Tile tile_of(const Params &p, int64_t t0)
+__device__ __forceinline__ Tile tile_of(const AdapterParams &p, int64_t t0)
 {
     const int lane = threadIdx.x & 31;
     const int64_t t = t0 + (lane & 15);
@@ -97,7 +59,7 @@ __device__ __forceinline__ Tile tile_of(const Params &p, int64_t t0)
 
 // 8 elements of a row from k on as bf16 pairs, zeros from K on; k is a multiple of 8.
 template <bool FP8>
-__device__ __forceinline__ uint4 load_hidden(const Params &p, int64_t row, int k)
+__device__ __forceinline__ uint4 load_hidden(const AdapterParams &p, int64_t row, int k)
 {
     const int n = p.hidden_size - k;
     if (n <= 0)
@@ -110,8 +72,8 @@ __device__ __forceinline__ uint4 load_hidden(const Params &p, int64_t row, int k
         else
             for (int j = 0; j < n; ++j)
                 (j < 4 ? c.x : c.y) |= (uint32_t)src[j] << (8 * (j & 3));
-        return make_uint4(e4m3x2_to_bf16x2(c.x & 0xffffu), e4m3x2_to_bf16x2(c.x >> 16),
-                          e4m3x2_to_bf16x2(c.y & 0xffffu), e4m3x2_to_bf16x2(c.y >> 16));
+        return make_uint4(adapter_e4m3x2(c.x & 0xffffu), adapter_e4m3x2(c.x >> 16),
+                          adapter_e4m3x2(c.y & 0xffffu), adapter_e4m3x2(c.y >> 16));
     }
     const uint16_t *src = reinterpret_cast<const uint16_t *>(p.hidden) + row * p.hidden_stride + k;
     if (n >= 8)
@@ -124,7 +86,7 @@ __device__ __forceinline__ uint4 load_hidden(const Params &p, int64_t row, int k
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint4 load_down(const Params &p, const uint16_t *row, int k)
+__device__ __forceinline__ uint4 load_down(const AdapterParams &p, const uint16_t *row, int k)
 {
     const int n = p.hidden_size - k;
     if (n >= 8)
@@ -146,7 +108,7 @@ __device__ __forceinline__ uint4 load_down(const Params &p, const uint16_t *row,
 // neighbouring elements of K of a token's row and of an adapter's row: the MMA's order of K
 // is free as long as both operands agree, so 16-byte loads are its fragments as they come.
 template <bool FP8, int NT>
-__global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const __grid_constant__ AdapterParams p)
 {
     __shared__ float s_sum[kDownWarps][kTile][8 * NT];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -225,15 +187,18 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
 // the up-projection, added to the rows
 // ---------------------------------------------------------------------------
 //
-// A warp takes a tile of 16 tokens and `chunk` columns, 32 at a time (a slice ends at a multiple
-// of 64).  Column 8 (n / 2) + 2 i + n % 2 of the 32 is column n of the MMA's i-th tile, so that a
-// lane's four accumulators of a row are 8 neighbouring columns: 16-byte loads and stores of the
-// rows.  u is summed over the pieces of K, in their order, and split into two bf16 parts: one
-// would put an error of 2^-9 of the adapter's share on every output.  RC: ceil(rank / 16).
-template <int RC>
-__global__ void __launch_bounds__(256) msa_adapter_up_kernel(const __grid_constant__ Params p)
+// A warp takes a tile of 16 tokens and `chunk` columns, 32 * HB at a time (a slice ends at a
+// multiple of 64).  Column 8 (n / 2) + 2 i + n % 2 of 32 is column n of the MMA's i-th tile, so
+// that a lane's four accumulators of a row are 8 neighbouring columns: 16-byte loads and stores
+// of the rows.  u is summed over the pieces of K, in their order, and split into two bf16 parts:
+// one would put an error of 2^-9 of the adapter's share on every output.
+//   RC  ceil(rank / 16)
+//   AU  adapters whose rows are loaded together (a decode batch, whose tiles have many)
+//   HB  pieces of 32 columns at a time, the next ones' rows loaded meanwhile where there are two
+template <int RC, int AU, int HB>
+__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
-    constexpr int AU = RC == 1 ? 4 : RC == 2 ? 2 : 1;     // adapters whose rows are loaded together
+    constexpr int LB = RC <= 2 ? HB : 1;             // pieces whose adapter rows are loaded together
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -248,19 +213,39 @@ __global__ void __launch_bounds__(256) msa_adapter_up_kernel(const __grid_consta
     const int id[2] = {__shfl_sync(0xffffffffu, tile.id, g), __shfl_sync(0xffffffffu, tile.id, g + 8)};
     const bool copy = p.out != p.rows;
     const int n = p.num_slices * p.rank;
+    bool live[2];
+    const uint16_t *src[2];
+    uint16_t *dst[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t t = t0 + g + 8 * h;
+        live[h] = t < p.num_tokens && (copy || id[h] >= 0);
+        src[h] = p.rows + t * p.rows_stride + 8 * q;
+        dst[h] = p.out + t * p.out_stride + 8 * q;
+    }
+    auto load_rows = [&](uint4 (&row)[HB][2], int c) {
+#pragma unroll
+        for (int b = 0; b < HB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (live[h] && c + 32 * b + 8 * q < end)
+                    row[b][h] = *reinterpret_cast<const uint4 *>(src[h] + c + 32 * b);
+    };
 
     uint32_t hi[RC][4], lo[RC][4];
+    uint4 next[HB][2] = {};
+    if (HB > 1)
+        load_rows(next, (int)from);
     int slice = -1;
-    for (int c = (int)from; c < end; c += 32) {
-        const int col = c + 8 * q;
-        uint4 row[2] = {};
-        bool put[2];
+    for (int c = (int)from; c < end; c += 32 * HB) {
+        uint4 row[HB][2];
+        if (HB > 1) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t t = t0 + g + 8 * h;
-            put[h] = t < p.num_tokens && col < end && (copy || id[h] >= 0);
-            if (put[h])
-                row[h] = *reinterpret_cast<const uint4 *>(p.rows + t * p.rows_stride + col);
+            for (int b = 0; b < HB; ++b)
+                row[b][0] = next[b][0], row[b][1] = next[b][1];
+            load_rows(next, c + 32 * HB);
+        } else {
+            load_rows(row, c);
         }
         if (slice < 0 || c >= p.slice_end[slice]) {
             do
@@ -272,79 +257,90 @@ __global__ void __launch_bounds__(256) msa_adapter_up_kernel(const __grid_consta
                 for (int h = 0; h < 2; ++h) {
                     float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (id[h] >= 0 && 16 * k + 4 * q < p.rank) {
-                        const float *src = p.u + (t0 + g + 8 * h) * n + slice * p.rank + 16 * k + 4 * q;
+                        const float *part = p.u + (t0 + g + 8 * h) * n + slice * p.rank + 16 * k + 4 * q;
                         for (int s = 0; s < p.splits; ++s) {
-                            const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)s * p.num_tokens * n);
+                            const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
                             u = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
                         }
                     }
-                    const uint32_t a = pack_bf16x2(u.x, u.y), b = pack_bf16x2(u.z, u.w);
+                    const uint32_t a = adapter_bf16x2(u.x, u.y), b = adapter_bf16x2(u.z, u.w);
                     const float2 a2 = unpack2(a), b2 = unpack2(b);
                     // (an infinite part has no remainder)
                     auto rest = [](float v, float part) { return isinf(part) ? 0.0f : v - part; };
                     hi[k][h] = a;
                     hi[k][h + 2] = b;
-                    lo[k][h] = pack_bf16x2(rest(u.x, a2.x), rest(u.y, a2.y));
-                    lo[k][h + 2] = pack_bf16x2(rest(u.z, b2.x), rest(u.w, b2.y));
+                    lo[k][h] = adapter_bf16x2(rest(u.x, a2.x), rest(u.y, a2.y));
+                    lo[k][h + 2] = adapter_bf16x2(rest(u.z, b2.x), rest(u.w, b2.y));
                 }
         }
-        float sum[4][4] = {};
+        float sum[HB][4][4] = {};
         for (uint32_t left = tile.leaders; left;) {
             int ad[AU];
-            uint2 b[AU][4][RC];
 #pragma unroll
             for (int j = 0; j < AU; ++j) {
                 const int leader = left ? __ffs(left) - 1 : 0;
                 ad[j] = left ? __shfl_sync(0xffffffffu, tile.id, leader) : -2;
                 left &= left - 1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = c + 8 * (g >> 1) + 2 * i + (g & 1);
-#pragma unroll
-                    for (int k = 0; k < RC; ++k) {
-                        b[j][i][k] = make_uint2(0, 0);
-                        if (ad[j] >= 0 && r < end && 16 * k + 4 * q < p.rank)
-                            b[j][i][k] = __ldg(reinterpret_cast<const uint2 *>(
-                                p.up + ((int64_t)ad[j] * p.width + r) * p.rank + 16 * k + 4 * q));
-                    }
-                }
             }
 #pragma unroll
-            for (int j = 0; j < AU; ++j) {
-                if (ad[j] < 0)
-                    break;
+            for (int b0 = 0; b0 < HB; b0 += LB) {
+                uint2 w[AU][LB][4][RC];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float acc[4] = {};
+                for (int j = 0; j < AU; ++j)
 #pragma unroll
-                    for (int k = 0; k < RC; ++k) {
-                        mma(acc, hi[k], b[j][i][k].x, b[j][i][k].y);
-                        mma(acc, lo[k], b[j][i][k].x, b[j][i][k].y);
-                    }
-                    if (id[0] == ad[j]) {
-                        sum[i][0] = acc[0];
-                        sum[i][1] = acc[1];
-                    }
-                    if (id[1] == ad[j]) {
-                        sum[i][2] = acc[2];
-                        sum[i][3] = acc[3];
-                    }
+                    for (int b = 0; b < LB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = c + 32 * (b0 + b) + 8 * (g >> 1) + 2 * i + (g & 1);
+                            const uint16_t *up = p.up + ((int64_t)ad[j] * p.width + r) * p.rank + 4 * q;
+#pragma unroll
+                            for (int k = 0; k < RC; ++k) {
+                                w[j][b][i][k] = make_uint2(0, 0);
+                                if (ad[j] >= 0 && r < end && 16 * k + 4 * q < p.rank)
+                                    w[j][b][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 16 * k));
+                            }
+                        }
+#pragma unroll
+                for (int j = 0; j < AU; ++j) {
+                    if (ad[j] < 0)
+                        break;
+#pragma unroll
+                    for (int b = 0; b < LB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float acc[4] = {};
+#pragma unroll
+                            for (int k = 0; k < RC; ++k) {
+                                mma(acc, hi[k], w[j][b][i][k].x, w[j][b][i][k].y);
+                                mma(acc, lo[k], w[j][b][i][k].x, w[j][b][i][k].y);
+                            }
+                            if (id[0] == ad[j]) {
+                                sum[b0 + b][i][0] = acc[0];
+                                sum[b0 + b][i][1] = acc[1];
+                            }
+                            if (id[1] == ad[j]) {
+                                sum[b0 + b][i][2] = acc[2];
+                                sum[b0 + b][i][3] = acc[3];
+                            }
+                        }
                 }
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!put[h])
-                continue;
-            uint32_t w[4] = {row[h].x, row[h].y, row[h].z, row[h].w};
-            if (id[h] >= 0)
+        for (int b = 0; b < HB; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v = unpack2(w[i]);
-                    w[i] = pack_bf16x2(v.x + sum[i][2 * h], v.y + sum[i][2 * h + 1]);
-                }
-            *reinterpret_cast<uint4 *>(p.out + (t0 + g + 8 * h) * p.out_stride + col) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+            for (int h = 0; h < 2; ++h) {
+                if (!live[h] || c + 32 * b + 8 * q >= end)
+                    continue;
+                uint32_t w[4] = {row[b][h].x, row[b][h].y, row[b][h].z, row[b][h].w};
+                if (id[h] >= 0)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = unpack2(w[i]);
+                        w[i] = adapter_bf16x2(v.x + sum[b][i][2 * h], v.y + sum[b][i][2 * h + 1]);
+                    }
+                *reinterpret_cast<uint4 *>(dst[h] + c + 32 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
     }
 }
 
@@ -406,7 +402,8 @@ int width_of(const msa_adapter_cfg *cfg) { return cfg->slice_end[cfg->num_slices
 
 // How the down-projection's work is cut.
 struct Cut {
-    int n_blocks, n_tiles;   // blocks of at most 64 rows of down, tiles of 8 rows in each
+    bool wide;               // tiles of 128 tokens (msa_adapter_tile.cu); else of 16
+    int n_blocks, n_tiles;   // tiles of 16: blocks of at most 64 rows of down, tiles of 8 rows in each
     int splits;              // pieces of K
 };
 
@@ -416,12 +413,24 @@ Cut cut_of(const msa_adapter_cfg *cfg, int64_t T)
     const int tiles = cfg->num_slices * cfg->rank / 8;
     c.n_blocks = (tiles + 7) / 8;
     c.n_tiles = (tiles + c.n_blocks - 1) / c.n_blocks;
-    // so many pieces that a batch whose tokens all have adapters of their own fills the GPU, and
-    // no fewer than a unit of K for each warp
     const int64_t units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
-    const int64_t most = (units + kDownWarps - 1) / kDownWarps, ctas = (T > 0 ? T : 1) * c.n_blocks;
-    const int64_t want = (2 * 152 + ctas - 1) / ctas;
+    c.wide = T >= kWideTokens;
+    int64_t most, want;
+    if (c.wide) {
+        // two CTAs on an SM, at least four units of K in each piece
+        const int64_t ctas = (T + 127) / 128;
+        most = units / 4 < 4 ? units / 4 : 4;
+        want = 2 * 152 / ctas;
+    } else {
+        // so many pieces that a batch whose tokens all have adapters of their own fills the GPU, and
+        // no fewer than a unit of K for each warp
+        const int64_t ctas = (T > 0 ? T : 1) * c.n_blocks;
+        most = (units + kDownWarps - 1) / kDownWarps;
+        want = (2 * 152 + ctas - 1) / ctas;
+    }
     c.splits = (int)(want < most ? want : most);
+    if (c.splits < 1)
+        c.splits = 1;
     return c;
 }
 
@@ -439,7 +448,7 @@ bool fits(int64_t a, int64_t b, int64_t c)
     return !__builtin_mul_overflow(a, b, &m) && !__builtin_mul_overflow(m, c, &m);
 }
 
-msa_status check_args(const msa_adapter_cfg *cfg, int64_t T, const Params &p, const void *workspace,
+msa_status check_args(const msa_adapter_cfg *cfg, int64_t T, const AdapterParams &p, const void *workspace,
                       int64_t workspace_bytes, int32_t flags)
 {
     const msa_status s = check_cfg(cfg, T);
@@ -474,7 +483,7 @@ msa_status check_args(const msa_adapter_cfg *cfg, int64_t T, const Params &p, co
     return MSA_OK;
 }
 
-msa_status launch(void (*kernel)(Params), dim3 grid, int threads, int smem, bool pdl, cudaStream_t stream, Params &p)
+msa_status launch(void (*kernel)(AdapterParams), dim3 grid, int threads, int smem, bool pdl, cudaStream_t stream, AdapterParams &p)
 {
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
@@ -516,7 +525,7 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
                                int64_t out_stride, void *workspace, int64_t workspace_bytes,
                                int32_t launch_flags, cudaStream_t stream)
 {
-    Params p;
+    AdapterParams p;
     memset(&p, 0, sizeof p);
     p.hidden = static_cast<const uint8_t *>(hidden);
     p.hidden_scales = hidden_scales;
@@ -546,31 +555,39 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     p.splits = c.splits;
     p.n_blocks = c.n_blocks;
     p.n_tiles = c.n_tiles;
-    using Kernel = void (*)(Params);
+    using Kernel = void (*)(AdapterParams);
     static const Kernel downs[2][4] = {
         {msa_adapter_down_kernel<false, 2>, msa_adapter_down_kernel<false, 4>, msa_adapter_down_kernel<false, 6>,
          msa_adapter_down_kernel<false, 8>},
         {msa_adapter_down_kernel<true, 2>, msa_adapter_down_kernel<true, 4>, msa_adapter_down_kernel<true, 6>,
          msa_adapter_down_kernel<true, 8>}};
     const int64_t tiles = (num_tokens + kTile - 1) / kTile;
-    const dim3 grid((unsigned)tiles, (unsigned)(num_tokens < kTile ? num_tokens : kTile),
-                    (unsigned)(c.n_blocks * c.splits));
-    const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], grid, 32 * kDownWarps, 0,
-                                launch_flags & MSA_LAUNCH_PDL, stream, p);
-    if (d != MSA_OK)
-        return d;
+    cudaError_t e = cudaSuccess;
+    if (!c.wide || !adapter_down_tiles(p, launch_flags & MSA_LAUNCH_PDL, stream, &e)) {
+        const dim3 grid((unsigned)tiles, (unsigned)(num_tokens < kTile ? num_tokens : kTile),
+                        (unsigned)(c.n_blocks * c.splits));
+        const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], grid, 32 * kDownWarps, 0,
+                                    launch_flags & MSA_LAUNCH_PDL, stream, p);
+        if (d != MSA_OK)
+            return d;
+    }
+    if (e != cudaSuccess)
+        return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
 
-    // Columns of a warp: so few that the warps fill the GPU, at most 256 (u is read once for them).
+    // Columns of a warp: so few that the warps fill the GPU, at most 512 (u is read once for them).
     p.chunk = 32;
-    while (p.chunk < 256 && tiles * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152 * 8)
+    while (p.chunk < 512 && tiles * ((p.width + p.chunk - 1) / p.chunk) > 16 * 152)
         p.chunk *= 2;
     const int64_t items = tiles * ((p.width + p.chunk - 1) / p.chunk);
     const int warps = items < 2 * 152 ? 1 : items < 16 * 152 ? 4 : 8;
-    static const Kernel ups[4] = {msa_adapter_up_kernel<1>, msa_adapter_up_kernel<2>, msa_adapter_up_kernel<4>,
-                                  msa_adapter_up_kernel<8>};
+    static const Kernel ups[2][4] = {
+        {msa_adapter_up_kernel<1, 4, 1>, msa_adapter_up_kernel<2, 2, 1>, msa_adapter_up_kernel<4, 1, 1>,
+         msa_adapter_up_kernel<8, 1, 1>},
+        {msa_adapter_up_kernel<1, 1, 2>, msa_adapter_up_kernel<2, 1, 2>, msa_adapter_up_kernel<4, 1, 2>,
+         msa_adapter_up_kernel<8, 1, 2>}};
     const int rc = (p.rank + 15) / 16;
-    return launch(ups[rc <= 1 ? 0 : rc <= 2 ? 1 : rc <= 4 ? 2 : 3], dim3((unsigned)((items + warps - 1) / warps)),
-                  32 * warps, 0, true, stream, p);
+    return launch(ups[p.chunk > 32][rc <= 1 ? 0 : rc <= 2 ? 1 : rc <= 4 ? 2 : 3],
+                  dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, true, stream, p);
 }
 
 }  // extern "C"

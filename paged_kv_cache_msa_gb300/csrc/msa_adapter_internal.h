@@ -1,0 +1,57 @@
+// Shared by the adapter operator's translation units (not exported).
+#pragma once
+
+#include "msa_adapter.h"
+#include "msa_internal.h"
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+struct AdapterParams {
+    const uint8_t *hidden;
+    const float *hidden_scales;
+    const uint16_t *down, *up;
+    const int32_t *ids;
+    const float *adapter_scales;
+    const uint16_t *rows;
+    uint16_t *out;
+    float *u;                        // [splits, T, S * r]: sums over pieces of K
+    int64_t hidden_stride, down_stride, rows_stride, out_stride;   // elements
+    int64_t num_tokens;
+    int32_t hidden_size, width, rank, num_adapters, num_slices, fp8;
+    int32_t splits;                  // pieces of K
+    int32_t n_blocks, n_tiles;       // blocks of down rows, tiles of 8 rows in a block
+    int32_t chunk;                   // columns of a warp's share of the up-projection
+    int32_t slice_end[MSA_ADAPTER_MAX_SLICES];
+};
+
+// The down-projection in tiles of 128 tokens (msa_adapter_tile.cu) into p.u, pieces of K as
+// p.splits says; false when TMA does not take the layout (nothing is enqueued then).
+bool adapter_down_tiles(const AdapterParams &p, bool pdl, cudaStream_t stream, cudaError_t *error);
+
+#ifdef __CUDACC__
+namespace {
+
+// (x0, x1) -> a bf16 pair, x0 in the low half
+__device__ __forceinline__ uint32_t adapter_bf16x2(float x0, float x1)
+{
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
+    return d;
+}
+
+// Two E4M3 codes (the low half of c) -> a bf16 pair: exact, since bf16 holds every E4M3 value.
+__device__ __forceinline__ uint32_t adapter_e4m3x2(uint32_t c)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
+    float lo, hi;
+    asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    return adapter_bf16x2(lo, hi);
+}
+
+}  // namespace
+#endif

@@ -1,0 +1,36 @@
+"""The adapters' bounded waits, in the starved test build (GPU): no copy is issued, every wait on
+one runs out, and the kernel must stop, leave NaN in the rows of every request with an adapter (the
+others' as they were) and free its tensor memory: the same call on the normal library right after
+must be right."""
+import pytest
+import torch
+
+from paged_kv_cache_msa_gb300 import binding as B
+from paged_kv_cache_msa_gb300 import build as build_mod
+from test_adapter_gpu import Case, mixed, runs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def libs():
+    normal = B.load(build_mod.build())
+    starved = B.load(build_mod.build_starved())
+    saved = B._lib
+    yield normal, starved
+    B._lib = saved
+
+
+@pytest.mark.parametrize("order", [mixed, runs], ids=["mixed", "runs"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_stops_and_writes_nan(libs, order, fp8):
+    normal, starved = libs
+    c = Case(order(1100, 3), k=1000, adapters=3, fp8=fp8)
+    B._lib = starved
+    c.run()
+    torch.cuda.synchronize()
+    on = (c.ids >= 0) & (c.ids < 3)
+    assert c.out[on].isnan().all()
+    assert torch.equal(c.out[~on].view(torch.int16), c.rows[~on].view(torch.int16))
+    B._lib = normal
+    c.run().check()

@@ -263,14 +263,8 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
                             u = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
                         }
                     }
-                    const uint32_t a = adapter_bf16x2(u.x, u.y), b = adapter_bf16x2(u.z, u.w);
-                    const float2 a2 = unpack2(a), b2 = unpack2(b);
-                    // (an infinite part has no remainder)
-                    auto rest = [](float v, float part) { return isinf(part) ? 0.0f : v - part; };
-                    hi[k][h] = a;
-                    hi[k][h + 2] = b;
-                    lo[k][h] = adapter_bf16x2(rest(u.x, a2.x), rest(u.y, a2.y));
-                    lo[k][h + 2] = adapter_bf16x2(rest(u.z, b2.x), rest(u.w, b2.y));
+                    adapter_split(u.x, u.y, hi[k][h], lo[k][h]);
+                    adapter_split(u.z, u.w, hi[k][h + 2], lo[k][h + 2]);
                 }
         }
         float sum[HB][4][4] = {};
@@ -419,7 +413,7 @@ Cut cut_of(const msa_adapter_cfg *cfg, int64_t T)
     if (c.wide) {
         // two CTAs on an SM, at least four units of K in each piece
         const int64_t ctas = (T + 127) / 128;
-        most = units / 4 < 4 ? units / 4 : 4;
+        most = units / 4 < kAdapterWideSplits ? units / 4 : kAdapterWideSplits;
         want = 2 * 152 / ctas;
     } else {
         // so many pieces that a batch whose tokens all have adapters of their own fills the GPU, and
@@ -573,6 +567,9 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     }
     if (e != cudaSuccess)
         return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+
+    if (c.wide && adapter_up_tiles(p, stream, &e))
+        return e == cudaSuccess ? MSA_OK : fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
 
     // Columns of a warp: so few that the warps fill the GPU, at most 512 (u is read once for them).
     p.chunk = 32;

@@ -8,6 +8,8 @@
 
 #include <cstdint>
 
+constexpr int kAdapterWideSplits = 4;    // pieces of K at most where tiles are of 128 tokens
+
 struct AdapterParams {
     const uint8_t *hidden;
     const float *hidden_scales;
@@ -30,6 +32,9 @@ struct AdapterParams {
 // p.splits says; false when TMA does not take the layout (nothing is enqueued then).
 bool adapter_down_tiles(const AdapterParams &p, bool pdl, cudaStream_t stream, cudaError_t *error);
 
+// The up-projection in tiles of 128 tokens from p.u, added to the rows; false as above.
+bool adapter_up_tiles(const AdapterParams &p, cudaStream_t stream, cudaError_t *error);
+
 #ifdef __CUDACC__
 namespace {
 
@@ -39,6 +44,15 @@ __device__ __forceinline__ uint32_t adapter_bf16x2(float x0, float x1)
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
     return d;
+}
+
+// (x0, x1) as two bf16 pairs whose sum is right to 2^-16 of each: x rounded, and what is left of
+// it (nothing of an infinite one).
+__device__ __forceinline__ void adapter_split(float x0, float x1, uint32_t &hi, uint32_t &lo)
+{
+    hi = adapter_bf16x2(x0, x1);
+    const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
+    lo = adapter_bf16x2(isinf(h0) ? 0.0f : x0 - h0, isinf(h1) ? 0.0f : x1 - h1);
 }
 
 // Two E4M3 codes (the low half of c) -> a bf16 pair: exact, since bf16 holds every E4M3 value.

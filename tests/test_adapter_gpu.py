@@ -257,3 +257,15 @@ def test_tensors_that_do_not_fit_are_refused():
             B.adapter_tensors(**dict(good, **bad))
     with pytest.raises(B.MsaError):
         B.adapter_tensors(**dict(good, workspace=c.ws[:256]))
+
+
+def test_tiles_of_several_adapters_over_many_blocks():
+    """Large batches of wide rows whose tiles of 128 tokens have one adapter, several or none: what
+    the groups of warps that take blocks by turns must keep apart."""
+    for seed in range(8):
+        gen = torch.Generator().manual_seed(seed)
+        edges = torch.cat([torch.tensor([0, 2048]), torch.randint(1, 2048, (4 + 5 * seed,), generator=gen)]).sort().values
+        ids = []
+        for i, n in enumerate(edges.diff().tolist()):
+            ids += [i % 7 - 1] * n
+        Case(ids, k=128, ends=PACKED, adapters=6, rank=(16, 32, 64, 96)[seed % 4], seed=seed).run().check()

@@ -187,18 +187,21 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
 // the up-projection, added to the rows
 // ---------------------------------------------------------------------------
 //
-// A warp takes a tile of 16 tokens and `chunk` columns, 32 * HB at a time (a slice ends at a
-// multiple of 64).  Column 8 (n / 2) + 2 i + n % 2 of 32 is column n of the MMA's i-th tile, so
-// that a lane's four accumulators of a row are 8 neighbouring columns: 16-byte loads and stores
-// of the rows.  u is summed over the pieces of K, in their order, and split into two bf16 parts:
-// one would put an error of 2^-9 of the adapter's share on every output.
-//   RC  ceil(rank / 16)
-//   AU  adapters whose rows are loaded together (a decode batch, whose tiles have many)
-//   HB  pieces of 32 columns at a time, the next ones' rows loaded meanwhile where there are two
-template <int RC, int AU, int HB>
+// A warp takes a tile of 16 tokens and `chunk` columns, 32 at a time (a slice ends at a multiple
+// of 64).  Column 8 (n / 2) + 2 i + n % 2 of the 32 is column n of the MMA's i-th tile, so that a
+// lane's four accumulators of a row are 8 neighbouring columns: 16-byte loads and stores of the
+// rows, which the accumulators begin with.  u is summed over the pieces of K, in their order, and
+// split into two bf16 parts: one would put an error of 2^-9 of the adapter's share on every
+// output.
+//   RC      ceil(rank / 16), rounded up to a power of two
+//   STREAM  many tiles, whose rows are what costs: the next blocks' rows, and the next rows of
+//           the first adapter of up, are loaded ahead.  Otherwise a tile's adapters are what costs,
+//           and AU of them are loaded together.
+template <int RC, bool STREAM>
 __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
-    constexpr int LB = RC <= 2 ? HB : 1;             // pieces whose adapter rows are loaded together
+    constexpr int AU = STREAM || RC > 2 ? 1 : 4 / RC;
+    constexpr bool kAhead = STREAM && RC <= 2;       // rows of up loaded a block ahead
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -212,6 +215,9 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
     const Tile tile = tile_of(p, t0);
     const int id[2] = {__shfl_sync(0xffffffffu, tile.id, g), __shfl_sync(0xffffffffu, tile.id, g + 8)};
     const bool copy = p.out != p.rows;
+    if (!copy && !tile.leaders)
+        return;
+    const int first = tile.leaders ? __shfl_sync(0xffffffffu, tile.id, __ffs(tile.leaders) - 1) : -1;
     const int n = p.num_slices * p.rank;
     bool live[2];
     const uint16_t *src[2];
@@ -223,40 +229,76 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
         src[h] = p.rows + t * p.rows_stride + 8 * q;
         dst[h] = p.out + t * p.out_stride + 8 * q;
     }
-    auto load_rows = [&](uint4 (&row)[HB][2], int c) {
+    auto load_rows = [&](uint4 (&row)[2], int c) {
 #pragma unroll
-        for (int b = 0; b < HB; ++b)
+        for (int h = 0; h < 2; ++h) {
+            row[h] = make_uint4(0, 0, 0, 0);
+            if (live[h] && c + 8 * q < end)
+                row[h] = *reinterpret_cast<const uint4 *>(src[h] + c);
+        }
+    };
+    // rows of up: element 4 q of row 8 (g / 2) + g % 2, of which tile i has the one 2 i further
+    const int up_at = (8 * (g >> 1) + (g & 1)) * p.rank + 4 * q;
+    uint32_t within = 0;                             // bit k: 16 k + 4 q is below the rank
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (live[h] && c + 32 * b + 8 * q < end)
-                    row[b][h] = *reinterpret_cast<const uint4 *>(src[h] + c + 32 * b);
+    for (int k = 0; k < RC; ++k)
+        within |= (uint32_t)(16 * k + 4 * q < p.rank) << k;
+    auto load_up = [&](uint2 (&w)[4][RC], int a, int c) {
+        const uint16_t *up = p.up + ((int64_t)a * p.width + c) * p.rank + up_at;
+        const bool whole = c + 32 <= end;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < RC; ++k) {
+                w[i][k] = make_uint2(0, 0);
+                if ((within >> k & 1u) && (whole || c + 8 * (g >> 1) + (g & 1) + 2 * i < end))
+                    w[i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * p.rank + 16 * k));
+            }
     };
 
     uint32_t hi[RC][4], lo[RC][4];
-    uint4 next[HB][2] = {};
-    if (HB > 1)
-        load_rows(next, (int)from);
-    int slice = -1;
-    for (int c = (int)from; c < end; c += 32 * HB) {
-        uint4 row[HB][2];
-        if (HB > 1) {
+    uint4 next[2][2];
+    uint2 up_next[4][RC];
+    if (STREAM) {
+        load_rows(next[0], (int)from);
+        load_rows(next[1], (int)from + 32);
+        if (kAhead && first >= 0)
+            load_up(up_next, first, (int)from);
+    }
+    int slice = -1, slice_end = 0;
+    for (int c = (int)from; c < end; c += 32) {
+        uint4 row[2];
+        uint2 w[AU][4][RC];
+        if (STREAM) {
 #pragma unroll
-            for (int b = 0; b < HB; ++b)
-                row[b][0] = next[b][0], row[b][1] = next[b][1];
-            load_rows(next, c + 32 * HB);
+            for (int h = 0; h < 2; ++h) {
+                row[h] = next[0][h];
+                next[0][h] = next[1][h];
+            }
+            load_rows(next[1], c + 64);
         } else {
             load_rows(row, c);
         }
-        if (slice < 0 || c >= p.slice_end[slice]) {
+        if (kAhead && first >= 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < RC; ++k)
+                    w[0][i][k] = up_next[i][k];
+            if (c + 32 < end)
+                load_up(up_next, first, c + 32);
+        }
+        if (c >= slice_end) {
             do
                 ++slice;
             while (c >= p.slice_end[slice]);
+            slice_end = p.slice_end[slice];
 #pragma unroll
             for (int k = 0; k < RC; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (id[h] >= 0 && 16 * k + 4 * q < p.rank) {
+                    if (id[h] >= 0 && (within >> k & 1u)) {
                         const float *part = p.u + (t0 + g + 8 * h) * n + slice * p.rank + 16 * k + 4 * q;
                         for (int s = 0; s < p.splits; ++s) {
                             const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
@@ -267,74 +309,48 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
                     adapter_split(u.z, u.w, hi[k][h + 2], lo[k][h + 2]);
                 }
         }
-        float sum[HB][4][4] = {};
-        for (uint32_t left = tile.leaders; left;) {
+        uint32_t out[2][4] = {{row[0].x, row[0].y, row[0].z, row[0].w}, {row[1].x, row[1].y, row[1].z, row[1].w}};
+        const uint32_t in[2][4] = {{row[0].x, row[0].y, row[0].z, row[0].w}, {row[1].x, row[1].y, row[1].z, row[1].w}};
+        auto add = [&](int a, const uint2 (&up)[4][RC]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 r0 = unpack2(in[0][i]), r1 = unpack2(in[1][i]);
+                float acc[4] = {r0.x, r0.y, r1.x, r1.y};
+#pragma unroll
+                for (int k = 0; k < RC; ++k) {
+                    mma(acc, hi[k], up[i][k].x, up[i][k].y);
+                    mma(acc, lo[k], up[i][k].x, up[i][k].y);
+                }
+                if (id[0] == a)
+                    out[0][i] = adapter_bf16x2(acc[0], acc[1]);
+                if (id[1] == a)
+                    out[1][i] = adapter_bf16x2(acc[2], acc[3]);
+            }
+        };
+        uint32_t left = tile.leaders;
+        if (kAhead && left) {
+            add(first, w[0]);
+            left &= left - 1;
+        }
+        while (left) {
             int ad[AU];
 #pragma unroll
             for (int j = 0; j < AU; ++j) {
                 const int leader = left ? __ffs(left) - 1 : 0;
                 ad[j] = left ? __shfl_sync(0xffffffffu, tile.id, leader) : -2;
                 left &= left - 1;
+                if (ad[j] >= 0)
+                    load_up(w[j], ad[j], c);
             }
 #pragma unroll
-            for (int b0 = 0; b0 < HB; b0 += LB) {
-                uint2 w[AU][LB][4][RC];
-#pragma unroll
-                for (int j = 0; j < AU; ++j)
-#pragma unroll
-                    for (int b = 0; b < LB; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = c + 32 * (b0 + b) + 8 * (g >> 1) + 2 * i + (g & 1);
-                            const uint16_t *up = p.up + ((int64_t)ad[j] * p.width + r) * p.rank + 4 * q;
-#pragma unroll
-                            for (int k = 0; k < RC; ++k) {
-                                w[j][b][i][k] = make_uint2(0, 0);
-                                if (ad[j] >= 0 && r < end && 16 * k + 4 * q < p.rank)
-                                    w[j][b][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 16 * k));
-                            }
-                        }
-#pragma unroll
-                for (int j = 0; j < AU; ++j) {
-                    if (ad[j] < 0)
-                        break;
-#pragma unroll
-                    for (int b = 0; b < LB; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float acc[4] = {};
-#pragma unroll
-                            for (int k = 0; k < RC; ++k) {
-                                mma(acc, hi[k], w[j][b][i][k].x, w[j][b][i][k].y);
-                                mma(acc, lo[k], w[j][b][i][k].x, w[j][b][i][k].y);
-                            }
-                            if (id[0] == ad[j]) {
-                                sum[b0 + b][i][0] = acc[0];
-                                sum[b0 + b][i][1] = acc[1];
-                            }
-                            if (id[1] == ad[j]) {
-                                sum[b0 + b][i][2] = acc[2];
-                                sum[b0 + b][i][3] = acc[3];
-                            }
-                        }
-                }
-            }
+            for (int j = 0; j < AU; ++j)
+                if (ad[j] >= 0)
+                    add(ad[j], w[j]);
         }
 #pragma unroll
-        for (int b = 0; b < HB; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!live[h] || c + 32 * b + 8 * q >= end)
-                    continue;
-                uint32_t w[4] = {row[b][h].x, row[b][h].y, row[b][h].z, row[b][h].w};
-                if (id[h] >= 0)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 v = unpack2(w[i]);
-                        w[i] = adapter_bf16x2(v.x + sum[b][i][2 * h], v.y + sum[b][i][2 * h + 1]);
-                    }
-                *reinterpret_cast<uint4 *>(dst[h] + c + 32 * b) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+        for (int h = 0; h < 2; ++h)
+            if (live[h] && c + 8 * q < end)
+                *reinterpret_cast<uint4 *>(dst[h] + c) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
     }
 }
 
@@ -568,9 +584,6 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     if (e != cudaSuccess)
         return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
 
-    if (c.wide && adapter_up_tiles(p, stream, &e))
-        return e == cudaSuccess ? MSA_OK : fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
-
     // Columns of a warp: so few that the warps fill the GPU, at most 512 (u is read once for them).
     p.chunk = 32;
     while (p.chunk < 512 && tiles * ((p.width + p.chunk - 1) / p.chunk) > 16 * 152)
@@ -578,10 +591,10 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     const int64_t items = tiles * ((p.width + p.chunk - 1) / p.chunk);
     const int warps = items < 2 * 152 ? 1 : items < 16 * 152 ? 4 : 8;
     static const Kernel ups[2][4] = {
-        {msa_adapter_up_kernel<1, 4, 1>, msa_adapter_up_kernel<2, 2, 1>, msa_adapter_up_kernel<4, 1, 1>,
-         msa_adapter_up_kernel<8, 1, 1>},
-        {msa_adapter_up_kernel<1, 1, 2>, msa_adapter_up_kernel<2, 1, 2>, msa_adapter_up_kernel<4, 1, 2>,
-         msa_adapter_up_kernel<8, 1, 2>}};
+        {msa_adapter_up_kernel<1, false>, msa_adapter_up_kernel<2, false>, msa_adapter_up_kernel<4, false>,
+         msa_adapter_up_kernel<8, false>},
+        {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>, msa_adapter_up_kernel<4, true>,
+         msa_adapter_up_kernel<8, true>}};
     const int rc = (p.rank + 15) / 16;
     return launch(ups[p.chunk > 32][rc <= 1 ? 0 : rc <= 2 ? 1 : rc <= 4 ? 2 : 3],
                   dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, true, stream, p);

@@ -32,9 +32,6 @@ struct AdapterParams {
 // p.splits says; false when TMA does not take the layout (nothing is enqueued then).
 bool adapter_down_tiles(const AdapterParams &p, bool pdl, cudaStream_t stream, cudaError_t *error);
 
-// The up-projection in tiles of 128 tokens from p.u, added to the rows; false as above.
-bool adapter_up_tiles(const AdapterParams &p, cudaStream_t stream, cudaError_t *error);
-
 #ifdef __CUDACC__
 namespace {
 

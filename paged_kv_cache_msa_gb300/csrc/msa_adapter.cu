@@ -194,16 +194,18 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
 // split into two bf16 parts: one would put an error of 2^-9 of the adapter's share on every
 // output.
 //   RC      ceil(rank / 16), rounded up to a power of two
-//   STREAM  many tiles, whose rows are what costs: the next blocks' rows, and the next rows of
-//           the first adapter of up, are loaded ahead.  Otherwise a tile's adapters are what costs,
-//           and AU of them are loaded together.
-template <int RC, bool STREAM>
+//   EXACT   the rank is 16 RC: offsets into up are constants, and no lane is beyond it
+//   STREAM  many tiles, whose rows are what costs: a tile whose tokens share one adapter (all but
+//           the borders of a prefill's chunks) goes through a loop of its own, with the rows of
+//           the two next blocks and the next rows of up loaded ahead, without choices between
+//           adapters
+template <int RC, bool EXACT, bool STREAM>
 __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
-    constexpr int AU = STREAM || RC > 2 ? 1 : 4 / RC;
-    constexpr bool kAhead = STREAM && RC <= 2;       // rows of up loaded a block ahead
+    constexpr int AU = RC > 2 ? 1 : 4 / RC;          // adapters of a tile loaded together
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" :::);
+    const int rank = EXACT ? 16 * RC : p.rank;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
     const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -217,8 +219,7 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
     const bool copy = p.out != p.rows;
     if (!copy && !tile.leaders)
         return;
-    const int first = tile.leaders ? __shfl_sync(0xffffffffu, tile.id, __ffs(tile.leaders) - 1) : -1;
-    const int n = p.num_slices * p.rank;
+    const int n = p.num_slices * rank;
     bool live[2];
     const uint16_t *src[2];
     uint16_t *dst[2];
@@ -229,123 +230,131 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
         src[h] = p.rows + t * p.rows_stride + 8 * q;
         dst[h] = p.out + t * p.out_stride + 8 * q;
     }
-    auto load_rows = [&](uint4 (&row)[2], int c) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            row[h] = make_uint4(0, 0, 0, 0);
-            if (live[h] && c + 8 * q < end)
-                row[h] = *reinterpret_cast<const uint4 *>(src[h] + c);
-        }
-    };
     // rows of up: element 4 q of row 8 (g / 2) + g % 2, of which tile i has the one 2 i further
-    const int up_at = (8 * (g >> 1) + (g & 1)) * p.rank + 4 * q;
+    const int up_row = 8 * (g >> 1) + (g & 1), up_at = up_row * rank + 4 * q;
     uint32_t within = 0;                             // bit k: 16 k + 4 q is below the rank
 #pragma unroll
     for (int k = 0; k < RC; ++k)
-        within |= (uint32_t)(16 * k + 4 * q < p.rank) << k;
-    auto load_up = [&](uint2 (&w)[4][RC], int a, int c) {
-        const uint16_t *up = p.up + ((int64_t)a * p.width + c) * p.rank + up_at;
-        const bool whole = c + 32 <= end;
+        within |= (uint32_t)(16 * k + 4 * q < rank) << k;
+    auto load_up = [&](uint2 (&w)[4][RC], const uint16_t *up, int rows) {    // `rows` from tile 0's on are there
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int k = 0; k < RC; ++k) {
-                w[i][k] = make_uint2(0, 0);
-                if ((within >> k & 1u) && (whole || c + 8 * (g >> 1) + (g & 1) + 2 * i < end))
-                    w[i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * p.rank + 16 * k));
-            }
+            for (int k = 0; k < RC; ++k)
+                if (!EXACT && !(within >> k & 1u))
+                    w[i][k] = make_uint2(0, 0);
+                else if (2 * i < rows)
+                    w[i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * rank + 16 * k));
     };
-
     uint32_t hi[RC][4], lo[RC][4];
-    uint4 next[2][2];
-    uint2 up_next[4][RC];
-    if (STREAM) {
-        load_rows(next[0], (int)from);
-        load_rows(next[1], (int)from + 32);
-        if (kAhead && first >= 0)
-            load_up(up_next, first, (int)from);
-    }
     int slice = -1, slice_end = 0;
-    for (int c = (int)from; c < end; c += 32) {
-        uint4 row[2];
-        uint2 w[AU][4][RC];
-        if (STREAM) {
+    auto load_u = [&](int c) {                       // of the slice of column c
+        do
+            ++slice;
+        while (c >= p.slice_end[slice]);
+        slice_end = p.slice_end[slice];
+#pragma unroll
+        for (int k = 0; k < RC; ++k)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                row[h] = next[0][h];
-                next[0][h] = next[1][h];
-            }
-            load_rows(next[1], c + 64);
-        } else {
-            load_rows(row, c);
-        }
-        if (kAhead && first >= 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < RC; ++k)
-                    w[0][i][k] = up_next[i][k];
-            if (c + 32 < end)
-                load_up(up_next, first, c + 32);
-        }
-        if (c >= slice_end) {
-            do
-                ++slice;
-            while (c >= p.slice_end[slice]);
-            slice_end = p.slice_end[slice];
-#pragma unroll
-            for (int k = 0; k < RC; ++k)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (id[h] >= 0 && (within >> k & 1u)) {
-                        const float *part = p.u + (t0 + g + 8 * h) * n + slice * p.rank + 16 * k + 4 * q;
-                        for (int s = 0; s < p.splits; ++s) {
-                            const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
-                            u = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-                        }
+                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (id[h] >= 0 && (EXACT || (within >> k & 1u))) {
+                    const float *part = p.u + (t0 + g + 8 * h) * n + slice * rank + 16 * k + 4 * q;
+                    for (int s = 0; s < p.splits; ++s) {
+                        const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
+                        u = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
                     }
-                    adapter_split(u.x, u.y, hi[k][h], lo[k][h]);
-                    adapter_split(u.z, u.w, hi[k][h + 2], lo[k][h + 2]);
                 }
-        }
-        uint32_t out[2][4] = {{row[0].x, row[0].y, row[0].z, row[0].w}, {row[1].x, row[1].y, row[1].z, row[1].w}};
-        const uint32_t in[2][4] = {{row[0].x, row[0].y, row[0].z, row[0].w}, {row[1].x, row[1].y, row[1].z, row[1].w}};
-        auto add = [&](int a, const uint2 (&up)[4][RC]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 r0 = unpack2(in[0][i]), r1 = unpack2(in[1][i]);
-                float acc[4] = {r0.x, r0.y, r1.x, r1.y};
-#pragma unroll
-                for (int k = 0; k < RC; ++k) {
-                    mma(acc, hi[k], up[i][k].x, up[i][k].y);
-                    mma(acc, lo[k], up[i][k].x, up[i][k].y);
-                }
-                if (id[0] == a)
-                    out[0][i] = adapter_bf16x2(acc[0], acc[1]);
-                if (id[1] == a)
-                    out[1][i] = adapter_bf16x2(acc[2], acc[3]);
+                adapter_split(u.x, u.y, hi[k][h], lo[k][h]);
+                adapter_split(u.z, u.w, hi[k][h + 2], lo[k][h + 2]);
             }
-        };
-        uint32_t left = tile.leaders;
-        if (kAhead && left) {
-            add(first, w[0]);
-            left &= left - 1;
+    };
+    // two words of a row pair (tokens g and g + 8) of tile i, and what the adapter adds
+    auto sums = [&](float (&acc)[4], uint32_t r0, uint32_t r1, const uint2 (&w)[RC]) {
+        const float2 a = unpack2(r0), b = unpack2(r1);
+        acc[0] = a.x, acc[1] = a.y, acc[2] = b.x, acc[3] = b.y;
+#pragma unroll
+        for (int k = 0; k < RC; ++k) {
+            mma(acc, hi[k], w[k].x, w[k].y);
+            mma(acc, lo[k], w[k].x, w[k].y);
         }
-        while (left) {
+    };
+
+    int c = (int)from;
+    const uint32_t all = __shfl_sync(0xffffffffu, tile.same, 0);
+    if (STREAM && all == 0xffffu && tile.leaders) {
+        const uint16_t *up = p.up + ((int64_t)__shfl_sync(0xffffffffu, tile.id, 0) * p.width + c) * rank + up_at;
+        uint4 next[2][2];                            // rows of this block and the next
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (c + 32 * b + 8 * q < end)
+                    next[b][h] = *reinterpret_cast<const uint4 *>(src[h] + c + 32 * b);
+        uint2 w[4][RC];
+        load_up(w, up, c + up_row < end ? end - c - up_row : 0);
+#pragma unroll 2
+        for (; c + 32 <= end; c += 32) {
+            const uint4 r0 = next[0][0], r1 = next[0][1];
+            next[0][0] = next[1][0];
+            next[0][1] = next[1][1];
+            if (c + 64 + 8 * q < end) {
+                next[1][0] = *reinterpret_cast<const uint4 *>(src[0] + c + 64);
+                next[1][1] = *reinterpret_cast<const uint4 *>(src[1] + c + 64);
+            }
+            if (c >= slice_end)
+                load_u(c);
+            float acc[4][4];
+            sums(acc[0], r0.x, r1.x, w[0]);
+            sums(acc[1], r0.y, r1.y, w[1]);
+            sums(acc[2], r0.z, r1.z, w[2]);
+            sums(acc[3], r0.w, r1.w, w[3]);
+            up += 32 * rank;
+            if (c + 64 <= end)
+                load_up(w, up, 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4 *>(dst[h] + c) =
+                    make_uint4(adapter_bf16x2(acc[0][2 * h], acc[0][2 * h + 1]), adapter_bf16x2(acc[1][2 * h], acc[1][2 * h + 1]),
+                               adapter_bf16x2(acc[2][2 * h], acc[2][2 * h + 1]), adapter_bf16x2(acc[3][2 * h], acc[3][2 * h + 1]));
+        }
+    }
+    for (; c < end; c += 32) {                       // any tile; of the loop above, what is left of a row
+        uint32_t in[2][4] = {}, out[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (live[h] && c + 8 * q < end) {
+                const uint4 r = *reinterpret_cast<const uint4 *>(src[h] + c);
+                in[h][0] = r.x, in[h][1] = r.y, in[h][2] = r.z, in[h][3] = r.w;
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[0][i] = in[0][i], out[1][i] = in[1][i];
+        if (c >= slice_end)
+            load_u(c);
+        for (uint32_t left = tile.leaders; left;) {
             int ad[AU];
+            uint2 w[AU][4][RC];
 #pragma unroll
             for (int j = 0; j < AU; ++j) {
                 const int leader = left ? __ffs(left) - 1 : 0;
                 ad[j] = left ? __shfl_sync(0xffffffffu, tile.id, leader) : -2;
                 left &= left - 1;
                 if (ad[j] >= 0)
-                    load_up(w[j], ad[j], c);
+                    load_up(w[j], p.up + ((int64_t)ad[j] * p.width + c) * rank + up_at, end - c - up_row);
             }
 #pragma unroll
             for (int j = 0; j < AU; ++j)
                 if (ad[j] >= 0)
-                    add(ad[j], w[j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float acc[4];
+                        sums(acc, in[0][i], in[1][i], w[j][i]);
+                        if (id[0] == ad[j])
+                            out[0][i] = adapter_bf16x2(acc[0], acc[1]);
+                        if (id[1] == ad[j])
+                            out[1][i] = adapter_bf16x2(acc[2], acc[3]);
+                    }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -590,14 +599,15 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
         p.chunk *= 2;
     const int64_t items = tiles * ((p.width + p.chunk - 1) / p.chunk);
     const int warps = items < 2 * 152 ? 1 : items < 16 * 152 ? 4 : 8;
-    static const Kernel ups[2][4] = {
-        {msa_adapter_up_kernel<1, false>, msa_adapter_up_kernel<2, false>, msa_adapter_up_kernel<4, false>,
-         msa_adapter_up_kernel<8, false>},
-        {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>, msa_adapter_up_kernel<4, true>,
-         msa_adapter_up_kernel<8, true>}};
-    const int rc = (p.rank + 15) / 16;
-    return launch(ups[p.chunk > 32][rc <= 1 ? 0 : rc <= 2 ? 1 : rc <= 4 ? 2 : 3],
-                  dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, true, stream, p);
+#define MSA_UPS(EXACT, STREAM)                                                            \
+    {msa_adapter_up_kernel<1, EXACT, STREAM>, msa_adapter_up_kernel<2, EXACT, STREAM>, \
+     msa_adapter_up_kernel<4, EXACT, STREAM>, msa_adapter_up_kernel<8, EXACT, STREAM>}
+    static const Kernel ups[2][2][4] = {{MSA_UPS(false, false), MSA_UPS(false, true)},
+                                        {MSA_UPS(true, false), MSA_UPS(true, true)}};
+#undef MSA_UPS
+    const int chunks = (p.rank + 15) / 16, rc = chunks <= 1 ? 0 : chunks <= 2 ? 1 : chunks <= 4 ? 2 : 3;
+    return launch(ups[p.rank == 16 << rc][p.chunk > 32][rc], dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0,
+                  true, stream, p);
 }
 
 }  // extern "C"

@@ -195,60 +195,42 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
 // output.
 //   RC      ceil(rank / 16), rounded up to a power of two
 //   EXACT   the rank is 16 RC: offsets into up are constants, and no lane is beyond it
-//   STREAM  many tiles, whose rows are what costs: a tile whose tokens share one adapter (all but
-//           the borders of a prefill's chunks) goes through a loop of its own, with the rows of
-//           the two next blocks and the next rows of up loaded ahead, without choices between
-//           adapters
-template <int RC, bool EXACT, bool STREAM>
-__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
-{
-    constexpr int AU = RC > 2 ? 1 : 4 / RC;          // adapters of a tile loaded together
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
-    const int rank = EXACT ? 16 * RC : p.rank;
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
-    const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t t0 = item % tiles * kTile;
-    const int64_t from = item / tiles * p.chunk;
-    if (from >= p.width)
-        return;
-    const int end = (int)min((int64_t)p.width, from + p.chunk);
-    const Tile tile = tile_of(p, t0);
-    const int id[2] = {__shfl_sync(0xffffffffu, tile.id, g), __shfl_sync(0xffffffffu, tile.id, g + 8)};
-    const bool copy = p.out != p.rows;
-    if (!copy && !tile.leaders)
-        return;
-    const int n = p.num_slices * rank;
-    bool live[2];
+
+// What a warp has of its tile of tokens and of u.
+template <int RC, bool EXACT>
+struct UpTile {
+    int rank, n, g, q;
+    bool live[2];                    // rows g and g + 8 are read and written
+    int id[2];
     const uint16_t *src[2];
     uint16_t *dst[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t t = t0 + g + 8 * h;
-        live[h] = t < p.num_tokens && (copy || id[h] >= 0);
-        src[h] = p.rows + t * p.rows_stride + 8 * q;
-        dst[h] = p.out + t * p.out_stride + 8 * q;
-    }
-    // rows of up: element 4 q of row 8 (g / 2) + g % 2, of which tile i has the one 2 i further
-    const int up_row = 8 * (g >> 1) + (g & 1), up_at = up_row * rank + 4 * q;
-    uint32_t within = 0;                             // bit k: 16 k + 4 q is below the rank
-#pragma unroll
-    for (int k = 0; k < RC; ++k)
-        within |= (uint32_t)(16 * k + 4 * q < rank) << k;
-    auto load_up = [&](uint2 (&w)[4][RC], const uint16_t *up, int rows) {    // `rows` from tile 0's on are there
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < RC; ++k)
-                if (!EXACT && !(within >> k & 1u))
-                    w[i][k] = make_uint2(0, 0);
-                else if (2 * i < rows)
-                    w[i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * rank + 16 * k));
-    };
+    const float *u[2];               // nullptr: no adapter
     uint32_t hi[RC][4], lo[RC][4];
-    int slice = -1, slice_end = 0;
-    auto load_u = [&](int c) {                       // of the slice of column c
+    int slice, slice_end;
+
+    __device__ __forceinline__ void init(const AdapterParams &p, const Tile &tile, int64_t t0)
+    {
+        rank = EXACT ? 16 * RC : p.rank;
+        n = p.num_slices * rank;
+        g = (threadIdx.x & 31) >> 2;
+        q = threadIdx.x & 3;
+        slice = -1;
+        slice_end = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t t = t0 + g + 8 * h;
+            id[h] = __shfl_sync(0xffffffffu, tile.id, g + 8 * h);
+            live[h] = t < p.num_tokens && (p.out != p.rows || id[h] >= 0);
+            src[h] = p.rows + t * p.rows_stride + 8 * q;
+            dst[h] = p.out + t * p.out_stride + 8 * q;
+            u[h] = id[h] >= 0 ? p.u + t * n : nullptr;
+        }
+    }
+    // the parts of u for the slice of column c, when that is another one
+    __device__ __forceinline__ void slice_of(const AdapterParams &p, int c)
+    {
+        if (c < slice_end)
+            return;
         do
             ++slice;
         while (c >= p.slice_end[slice]);
@@ -257,81 +239,69 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
         for (int k = 0; k < RC; ++k)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (id[h] >= 0 && (EXACT || (within >> k & 1u))) {
-                    const float *part = p.u + (t0 + g + 8 * h) * n + slice * rank + 16 * k + 4 * q;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (u[h] && (EXACT || 16 * k + 4 * q < rank)) {
+                    const float *part = u[h] + slice * rank + 16 * k + 4 * q;
                     for (int s = 0; s < p.splits; ++s) {
-                        const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
-                        u = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+                        const float4 x = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
+                        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
                     }
                 }
-                adapter_split(u.x, u.y, hi[k][h], lo[k][h]);
-                adapter_split(u.z, u.w, hi[k][h + 2], lo[k][h + 2]);
+                adapter_split(v.x, v.y, hi[k][h], lo[k][h]);
+                adapter_split(v.z, v.w, hi[k][h + 2], lo[k][h + 2]);
             }
-    };
-    // two words of a row pair (tokens g and g + 8) of tile i, and what the adapter adds
-    auto sums = [&](float (&acc)[4], uint32_t r0, uint32_t r1, const uint2 (&w)[RC]) {
+    }
+    // a word of the rows g and g + 8, of the MMA's tile i, with what an adapter's rows w add
+    __device__ __forceinline__ void add(uint32_t r0, uint32_t r1, const uint2 (&w)[RC], uint32_t &o0, uint32_t &o1) const
+    {
         const float2 a = unpack2(r0), b = unpack2(r1);
-        acc[0] = a.x, acc[1] = a.y, acc[2] = b.x, acc[3] = b.y;
+        float acc[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
         for (int k = 0; k < RC; ++k) {
             mma(acc, hi[k], w[k].x, w[k].y);
             mma(acc, lo[k], w[k].x, w[k].y);
         }
-    };
-
-    int c = (int)from;
-    const uint32_t all = __shfl_sync(0xffffffffu, tile.same, 0);
-    if (STREAM && all == 0xffffu && tile.leaders) {
-        const uint16_t *up = p.up + ((int64_t)__shfl_sync(0xffffffffu, tile.id, 0) * p.width + c) * rank + up_at;
-        uint4 next[2][2];                            // rows of this block and the next
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (c + 32 * b + 8 * q < end)
-                    next[b][h] = *reinterpret_cast<const uint4 *>(src[h] + c + 32 * b);
-        uint2 w[4][RC];
-        load_up(w, up, c + up_row < end ? end - c - up_row : 0);
-#pragma unroll 2
-        for (; c + 32 <= end; c += 32) {
-            const uint4 r0 = next[0][0], r1 = next[0][1];
-            next[0][0] = next[1][0];
-            next[0][1] = next[1][1];
-            if (c + 64 + 8 * q < end) {
-                next[1][0] = *reinterpret_cast<const uint4 *>(src[0] + c + 64);
-                next[1][1] = *reinterpret_cast<const uint4 *>(src[1] + c + 64);
-            }
-            if (c >= slice_end)
-                load_u(c);
-            float acc[4][4];
-            sums(acc[0], r0.x, r1.x, w[0]);
-            sums(acc[1], r0.y, r1.y, w[1]);
-            sums(acc[2], r0.z, r1.z, w[2]);
-            sums(acc[3], r0.w, r1.w, w[3]);
-            up += 32 * rank;
-            if (c + 64 <= end)
-                load_up(w, up, 8);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4 *>(dst[h] + c) =
-                    make_uint4(adapter_bf16x2(acc[0][2 * h], acc[0][2 * h + 1]), adapter_bf16x2(acc[1][2 * h], acc[1][2 * h + 1]),
-                               adapter_bf16x2(acc[2][2 * h], acc[2][2 * h + 1]), adapter_bf16x2(acc[3][2 * h], acc[3][2 * h + 1]));
-        }
+        o0 = adapter_bf16x2(acc[0], acc[1]);
+        o1 = adapter_bf16x2(acc[2], acc[3]);
     }
-    for (; c < end; c += 32) {                       // any tile; of the loop above, what is left of a row
+};
+
+// Columns [c, end) of any tile: for each distinct adapter its rows of up, AU adapters' at once.
+template <int RC, bool EXACT>
+__device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT> &t, const Tile &tile, int c, int end)
+{
+    constexpr int AU = RC > 2 ? 1 : 4 / RC;
+    const int up_row = 8 * (t.g >> 1) + (t.g & 1);
+    if (!tile.leaders) {                             // a copy
+        for (; c < end; c += 128) {
+            uint4 r[4][2];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (t.live[h] && c + 32 * b + 8 * t.q < end)
+                        r[b][h] = *reinterpret_cast<const uint4 *>(t.src[h] + c + 32 * b);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (t.live[h] && c + 32 * b + 8 * t.q < end)
+                        *reinterpret_cast<uint4 *>(t.dst[h] + c + 32 * b) = r[b][h];
+        }
+        return;
+    }
+    for (; c < end; c += 32) {
         uint32_t in[2][4] = {}, out[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (live[h] && c + 8 * q < end) {
-                const uint4 r = *reinterpret_cast<const uint4 *>(src[h] + c);
+            if (t.live[h] && c + 8 * t.q < end) {
+                const uint4 r = *reinterpret_cast<const uint4 *>(t.src[h] + c);
                 in[h][0] = r.x, in[h][1] = r.y, in[h][2] = r.z, in[h][3] = r.w;
             }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             out[0][i] = in[0][i], out[1][i] = in[1][i];
-        if (c >= slice_end)
-            load_u(c);
+        t.slice_of(p, c);
         for (uint32_t left = tile.leaders; left;) {
             int ad[AU];
             uint2 w[AU][4][RC];
@@ -340,26 +310,173 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
                 const int leader = left ? __ffs(left) - 1 : 0;
                 ad[j] = left ? __shfl_sync(0xffffffffu, tile.id, leader) : -2;
                 left &= left - 1;
-                if (ad[j] >= 0)
-                    load_up(w[j], p.up + ((int64_t)ad[j] * p.width + c) * rank + up_at, end - c - up_row);
+                const uint16_t *up = p.up + ((int64_t)ad[j] * p.width + c + up_row) * t.rank + 4 * t.q;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < RC; ++k) {
+                        w[j][i][k] = make_uint2(0, 0);
+                        if (ad[j] >= 0 && c + up_row + 2 * i < end && (EXACT || 16 * k + 4 * t.q < t.rank))
+                            w[j][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * t.rank + 16 * k));
+                    }
             }
 #pragma unroll
             for (int j = 0; j < AU; ++j)
                 if (ad[j] >= 0)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float acc[4];
-                        sums(acc, in[0][i], in[1][i], w[j][i]);
-                        if (id[0] == ad[j])
-                            out[0][i] = adapter_bf16x2(acc[0], acc[1]);
-                        if (id[1] == ad[j])
-                            out[1][i] = adapter_bf16x2(acc[2], acc[3]);
+                        uint32_t o0, o1;
+                        t.add(in[0][i], in[1][i], w[j][i], o0, o1);
+                        if (t.id[0] == ad[j])
+                            out[0][i] = o0;
+                        if (t.id[1] == ad[j])
+                            out[1][i] = o1;
                     }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (live[h] && c + 8 * q < end)
-                *reinterpret_cast<uint4 *>(dst[h] + c) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+            if (t.live[h] && c + 8 * t.q < end)
+                *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+    }
+}
+
+template <int RC, bool EXACT>
+__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
+    const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t0 = item % tiles * kTile, from = item / tiles * p.chunk;
+    if (from >= p.width)
+        return;
+    const Tile tile = tile_of(p, t0);
+    if (p.out == p.rows && !tile.leaders)
+        return;
+    UpTile<RC, EXACT> t;
+    t.init(p, tile, t0);
+    up_any(p, t, tile, (int)from, (int)min((int64_t)p.width, from + p.chunk));
+}
+
+// The same for many tiles, whose rows are what costs (8,192 of 11,392 are 373 MB, 56 us at the
+// copy rate).  A CTA takes eight tiles (128 tokens) and `chunk` columns.  Where they share one
+// adapter -- all but the borders of a prefill's chunks -- its rows of up go through shared memory,
+// kUpStage columns ahead of those that are computed, and a warp has the rows of its next two
+// blocks of 32 columns in flight.  The 32-byte pieces of a row of up are placed so that the rows
+// 0, 1, 8 and 9 (16, 17, 24 and 25), of which a half warp loads a piece each, lie on different
+// banks: the two rows 2 apart go elsewhere (ranks up to 16), or the piece's number is changed.
+constexpr int kUpStage = 128;        // columns of a stage of up
+
+template <int RC>
+__device__ __forceinline__ uint32_t up_piece(int row, int k)       // byte offset of piece k of a row of a stage
+{
+    const uint32_t r = (uint32_t)row, far = r >> 3 & 1u;
+    if (RC == 1)
+        return 32u * ((r & ~10u) | far << 1 | (r >> 1 & 1u) << 3);
+    return 32u * ((r * RC + (uint32_t)k) ^ (RC == 2 ? far : (r & 1u) | far << 1));
+}
+
+// From row 8 a + b to row 8 a + b + 2 i (b 0 or 1) of a stage.
+template <int RC>
+__device__ constexpr uint32_t up_step(int i)
+{
+    return RC == 1 ? 32u * ((i & 1) * 8 + (i >> 1) * 4) : 32u * RC * 2 * i;
+}
+
+template <int RC, bool EXACT>
+__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_kernel(const __grid_constant__ AdapterParams p)
+{
+    extern __shared__ __align__(128) uint8_t s_up[];                 // two stages
+    constexpr uint32_t kStageBytes = 32u * RC * kUpStage;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int64_t groups = (p.num_tokens + 8 * kTile - 1) / (8 * kTile);
+    const int64_t t0 = blockIdx.x % groups * (8 * kTile) + warp * kTile;
+    const int from = (int)(blockIdx.x / groups) * p.chunk, end = min(p.width, from + p.chunk);
+    Tile tile = tile_of(p, t0);
+    const int first = __ldg(p.ids + blockIdx.x % groups * (8 * kTile));
+    // (tokens behind the last one go with any)
+    const bool mine = __all_sync(0xffffffffu, tile.id == first || t0 + (tid & 15) >= p.num_tokens);
+    if (!__syncthreads_and(mine && first >= 0 && first < p.num_adapters)) {
+        if (t0 < p.num_tokens && (p.out != p.rows || tile.leaders)) {
+            UpTile<RC, EXACT> t;
+            t.init(p, tile, t0);
+            up_any(p, t, tile, from, end);
+        }
+        return;
+    }
+    UpTile<RC, EXACT> t;
+    t.init(p, tile, t0);
+    const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(s_up);
+    // 16-byte halves of pieces; zeros beyond the rank and the last column
+    auto stage = [&](int c, uint32_t dst) {
+        const uint16_t *up = p.up + ((int64_t)first * p.width + c) * t.rank;
+        for (int e = tid; e < kUpStage * 2 * RC; e += 256) {
+            const int row = e / (2 * RC), h = e % (2 * RC);
+            const bool there = c + row < end && (EXACT || 8 * h < t.rank);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + up_piece<RC>(row, h >> 1) + 16u * (h & 1)),
+                         "l"(there ? up + row * t.rank + 8 * h : p.up), "r"(there ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    stage(from, s0);
+    if (from + kUpStage < end)
+        stage(from + kUpStage, s0 + kStageBytes);
+    uint4 next[2][2] = {};           // rows of this block of 32 columns and the next
+    auto load_rows = [&](uint4 (&row)[2], int c) {
+        if (c + 8 * t.q < end)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (t.live[h])
+                    row[h] = *reinterpret_cast<const uint4 *>(t.src[h] + c);
+    };
+    load_rows(next[0], from);
+    load_rows(next[1], from + 32);
+    const int up_row = 8 * (t.g >> 1) + (t.g & 1);
+    uint32_t at[RC];                 // of this lane's piece k of row up_row
+#pragma unroll
+    for (int k = 0; k < RC; ++k)
+        at[k] = s0 + up_piece<RC>(up_row, k) + 8u * t.q;
+    for (int c0 = from, it = 0; c0 < end; c0 += kUpStage, ++it) {
+        if (c0 + kUpStage < end)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        const uint32_t base = (uint32_t)(it & 1) * kStageBytes;
+#pragma unroll 2
+        for (int b = 0; b < kUpStage / 32; ++b) {
+            const int c = c0 + 32 * b;
+            if (c >= end)
+                break;
+            const uint4 r0 = next[0][0], r1 = next[0][1];
+            next[0][0] = next[1][0];
+            next[0][1] = next[1][1];
+            load_rows(next[1], c + 64);
+            t.slice_of(p, c);
+            const uint32_t in[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
+            uint32_t out[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint2 w[RC];
+#pragma unroll
+                for (int k = 0; k < RC; ++k)
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                 : "=r"(w[k].x), "=r"(w[k].y)
+                                 : "r"(at[k] + base + (uint32_t)b * (1024u * RC) + up_step<RC>(i)));
+                t.add(in[0][i], in[1][i], w, out[0][i], out[1][i]);
+            }
+            if (c + 8 * t.q < end)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (t.live[h])
+                        *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+        }
+        __syncthreads();
+        if (c0 + 2 * kUpStage < end)
+            stage(c0 + 2 * kUpStage, s0 + base);
     }
 }
 
@@ -593,21 +710,33 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     if (e != cudaSuccess)
         return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
 
-    // Columns of a warp: so few that the warps fill the GPU, at most 512 (u is read once for them).
-    p.chunk = 32;
-    while (p.chunk < 512 && tiles * ((p.width + p.chunk - 1) / p.chunk) > 16 * 152)
-        p.chunk *= 2;
-    const int64_t items = tiles * ((p.width + p.chunk - 1) / p.chunk);
-    const int warps = items < 2 * 152 ? 1 : items < 16 * 152 ? 4 : 8;
-#define MSA_UPS(EXACT, STREAM)                                                            \
-    {msa_adapter_up_kernel<1, EXACT, STREAM>, msa_adapter_up_kernel<2, EXACT, STREAM>, \
-     msa_adapter_up_kernel<4, EXACT, STREAM>, msa_adapter_up_kernel<8, EXACT, STREAM>}
-    static const Kernel ups[2][2][4] = {{MSA_UPS(false, false), MSA_UPS(false, true)},
-                                        {MSA_UPS(true, false), MSA_UPS(true, true)}};
-#undef MSA_UPS
     const int chunks = (p.rank + 15) / 16, rc = chunks <= 1 ? 0 : chunks <= 2 ? 1 : chunks <= 4 ? 2 : 3;
-    return launch(ups[p.rank == 16 << rc][p.chunk > 32][rc], dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0,
-                  true, stream, p);
+    const bool exact = p.rank == 16 << rc;
+    // Columns of a warp: so few that the warps fill the GPU.
+    const int64_t pieces = (p.width + 31) / 32;
+    if (tiles * pieces <= 16 * 152) {
+        static const Kernel ups[2][4] = {{msa_adapter_up_kernel<1, false>, msa_adapter_up_kernel<2, false>,
+                                          msa_adapter_up_kernel<4, false>, msa_adapter_up_kernel<8, false>},
+                                         {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>,
+                                          msa_adapter_up_kernel<4, true>, msa_adapter_up_kernel<8, true>}};
+        p.chunk = 32;
+        const int64_t items = tiles * pieces;
+        const int warps = items < 2 * 152 ? 1 : 4;
+        return launch(ups[exact][rc], dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, true, stream, p);
+    }
+    static const Kernel ups[2][4] = {{msa_adapter_up_stream_kernel<1, false>, msa_adapter_up_stream_kernel<2, false>,
+                                      msa_adapter_up_stream_kernel<4, false>, msa_adapter_up_stream_kernel<8, false>},
+                                     {msa_adapter_up_stream_kernel<1, true>, msa_adapter_up_stream_kernel<2, true>,
+                                      msa_adapter_up_stream_kernel<4, true>, msa_adapter_up_stream_kernel<8, true>}};
+    const int smem = 2 * (32 << rc) * kUpStage;
+    const int64_t groups = (tiles + 7) / 8;
+    p.chunk = kUpStage;
+    while (p.chunk < 512 && groups * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152)
+        p.chunk *= 2;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(ups[exact][rc]), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+    return launch(ups[exact][rc], dim3((unsigned)(groups * ((p.width + p.chunk - 1) / p.chunk))), 256, smem, true, stream, p);
 }
 
 }  // extern "C"

@@ -219,6 +219,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.msa_status_string.restype = ctypes.c_char_p
         L.msa_last_error_detail.argtypes = []
         L.msa_last_error_detail.restype = ctypes.c_char_p
+        # addresses of the entry points that the extension msa_marshal calls
+        L.entries = {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+                     for n in ("msa_norm_forward", "msa_adapter_forward", "msa_producer_axes_forward")}
         if path is None:
             _lib = L
         return L
@@ -640,7 +643,7 @@ def _tensor(name, t, shape, dtypes, device):
 _attention_types = None      # torch, and the dtypes of q and out, int32, int64, fp32
 
 
-def _on_device(q, name="q"):
+def _on_device(q):
     """The types and q's device; the latter's context when it is not the current one."""
     global _attention_types
     if _attention_types is None:
@@ -649,7 +652,7 @@ def _on_device(q, name="q"):
                             (torch.float32,))
     dev = q.device
     if dev.type != "cuda":
-        raise ValueError(f"{name} is on {dev}; the calls take CUDA tensors")
+        raise ValueError(f"q is on {dev}; the attention calls take CUDA tensors")
     cuda = _attention_types[0].cuda
     return dev, None if cuda.current_device() == dev.index else cuda.device(dev)
 
@@ -729,34 +732,28 @@ def prefix_attention_tensors(cfg: MsaAttentionCfg, q, group_start, prefix_len, p
 # ---------------------------------------------------------------------------
 # the input side of a layer: norm, adapters, the producer with several axes
 # ---------------------------------------------------------------------------
+#
+# Their tensors are checked by the extension msa_marshal (csrc/msa_marshal.cpp).
 
-_fp8_types = None
-
-
-def _types_8bit():
-    global _fp8_types
-    if _fp8_types is None:
-        import torch
-        _fp8_types = (torch.float8_e4m3fn, torch.uint8)
-    return _fp8_types
+_marshal = None
 
 
-def _rows(name, t, n, k, dtypes, device):
-    """Checks a tensor of n rows of k elements, rows any stride apart; returns its address and
-    row stride (None, 0 for None)."""
-    if t is None:
-        return None, 0
-    if t.dtype in dtypes and t.shape == (n, k) and t.device == device and (t.stride(1) == 1 or k == 1):
-        return t.data_ptr(), t.stride(0) if n > 1 else -(-k // 16) * 16
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    raise ValueError(f"{name}: expected a {dtypes[0]} tensor of shape {(n, k)} with unit column stride, "
-                     f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+def _marshaller():
+    """The extension (raises if it has not been built)."""
+    global _marshal
+    if _marshal is None:
+        import importlib.util
 
-
-def _stream_handle(dev, stream):
-    # the handle alone: torch.cuda.current_stream builds a stream object in 2 us
-    return _attention_types[0]._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+        import torch  # noqa: F401  (its libraries, which the extension links to)
+        path = _build.MARSHAL_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"the extension is not built ({path}); build it with "
+                               "`python -m paged_kv_cache_msa_gb300.build`")
+        spec = importlib.util.spec_from_file_location("msa_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _marshal = module
+    return _marshal
 
 
 def norm_tensors(cfg: MsaNormCfg, x, weight, residual=None, residual_out=None, out=None, codes=None,
@@ -765,17 +762,11 @@ def norm_tensors(cfg: MsaNormCfg, x, weight, residual=None, residual_out=None, o
     codes E4M3 [T, K] (float8_e4m3fn or uint8), rows any stride apart; weight bf16 [K] and
     scales fp32 [T] contiguous.  residual_out may be residual.  Runs on ``stream`` or the
     current stream of x's device."""
-    dev, other = _on_device(x, "x")
-    if other is not None:
-        with other:
-            return norm_tensors(cfg, x, weight, residual, residual_out, out, codes, scales, launch_flags, stream)
-    _, bf16, _, _, f32 = _attention_types
-    n, k = x.shape[0], cfg.hidden_size
-    msa_norm_forward(cfg, n, *_rows("x", x, n, k, bf16, dev), *_rows("residual", residual, n, k, bf16, dev),
-                     _tensor("weight", weight, (k,), bf16, dev),
-                     *_rows("residual_out", residual_out, n, k, bf16, dev), *_rows("out", out, n, k, bf16, dev),
-                     *_rows("codes", codes, n, k, _types_8bit(), dev), _tensor("scales", scales, (n,), f32, dev),
-                     launch_flags, _stream_handle(dev, stream))
+    s = (_marshal or _marshaller()).norm((_lib or load()).entries["msa_norm_forward"], cfg, x, weight, residual,
+                                         residual_out, out, codes, scales, launch_flags,
+                                         None if stream is None else stream.cuda_stream)
+    if s != MSA_OK:
+        raise MsaError(s, "msa_norm_forward", last_error_detail())
 
 
 def adapter_tensors(cfg: MsaAdapterCfg, hidden, down, up, adapter_ids, rows, out, hidden_scales=None,
@@ -786,33 +777,18 @@ def adapter_tensors(cfg: MsaAdapterCfg, hidden, down, up, adapter_ids, rows, out
     adapter_ids int32 [T], hidden_scales fp32 [T], adapter_scales fp32 [num_adapters].
     ``workspace``: a tensor of at least ``msa_adapter_workspace_bytes(cfg, T)`` bytes, or None
     to allocate one.  Runs on ``stream`` or the current stream of hidden's device."""
-    dev, other = _on_device(hidden, "hidden")
-    if other is not None:
-        with other:
-            return adapter_tensors(cfg, hidden, down, up, adapter_ids, rows, out, hidden_scales, adapter_scales,
-                                   workspace, launch_flags, stream)
-    torch, bf16, i32, _, f32 = _attention_types
-    n, k, r, a = hidden.shape[0], cfg.hidden_size, cfg.rank, cfg.num_adapters
-    width, sr = cfg.slice_end[cfg.num_slices - 1], cfg.num_slices * r
-    if down.dim() != 3 or (a > 1 and down.stride(0) != sr * down.stride(1)):
-        raise ValueError(f"down: expected [num_adapters, num_slices * rank, K] with its rows one stride apart, "
-                         f"got {tuple(down.shape)}, strides {down.stride()}")
     if workspace is None:
-        nbytes = msa_adapter_workspace_bytes(cfg, n)
-        with torch.cuda.stream(stream):          # None: the current stream
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on {dev}, got one on {workspace.device}")
-    if down.shape[0] != a:
-        raise ValueError(f"down: expected {a} adapters, got {down.shape[0]}")
-    down_ptr, down_stride = _rows("down", down.flatten(0, 1), a * sr, k, bf16, dev)
-    msa_adapter_forward(cfg, n,
-                        *_rows("hidden", hidden, n, k, bf16 if cfg.hidden_dtype == MSA_DTYPE_BF16 else _types_8bit(), dev),
-                        _tensor("hidden_scales", hidden_scales, (n,), f32, dev), down_ptr, down_stride,
-                        _tensor("up", up, (a, width, r), bf16, dev), _tensor("adapter_ids", adapter_ids, (n,), i32, dev),
-                        _tensor("adapter_scales", adapter_scales, (a,), f32, dev),
-                        *_rows("rows", rows, n, width, bf16, dev), *_rows("out", out, n, width, bf16, dev),
-                        workspace.data_ptr() or None, workspace.nbytes, launch_flags, _stream_handle(dev, stream))
+        import torch
+        if hidden.device.type != "cuda":
+            raise ValueError(f"hidden is on {hidden.device}; the calls take CUDA tensors")
+        nbytes = msa_adapter_workspace_bytes(cfg, hidden.shape[0])
+        with torch.cuda.device(hidden.device), torch.cuda.stream(stream):     # None: the current stream
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
+    s = (_marshal or _marshaller()).adapter((_lib or load()).entries["msa_adapter_forward"], cfg, hidden, down, up,
+                                            adapter_ids, rows, out, hidden_scales, adapter_scales, workspace,
+                                            launch_flags, None if stream is None else stream.cuda_stream)
+    if s != MSA_OK:
+        raise MsaError(s, "msa_adapter_forward", last_error_detail())
 
 
 def forward_axes_tensors(cfg: MsaProducerCfg, axes: MsaRopeAxes, qkv, positions, slot_mapping, page_table,
@@ -821,32 +797,10 @@ def forward_axes_tensors(cfg: MsaProducerCfg, axes: MsaRopeAxes, qkv, positions,
     """msa_producer_axes_forward on torch CUDA tensors: ``positions`` int32 [num_axes, T] with unit
     column stride, everything else as for ``forward_tensors``, and checked.  Runs on ``stream``
     or the current stream of qkv's device."""
-    dev, other = _on_device(qkv, "qkv")
-    if other is not None:
-        with other:
-            return forward_axes_tensors(cfg, axes, qkv, positions, slot_mapping, page_table, norm_weights, q_out,
-                                        idx_q_out, k_cache, v_cache, idx_k_cache, scales, launch_flags, stream)
-    _, bf16, i32, i64, f32 = _attention_types
-    n, d = qkv.shape[0], cfg.head_dim
-    width = (cfg.num_q_heads + 2 * cfg.num_kv_heads + cfg.num_idx_q_heads + cfg.num_idx_k_heads) * d
-    if qkv.dim() != 2 or qkv.shape[1] < width or (qkv.stride(1) != 1 and qkv.shape[1] > 1) or qkv.dtype not in bf16:
-        raise ValueError(f"qkv: expected bf16 rows of at least {width} elements, got {qkv.dtype} {tuple(qkv.shape)}, "
-                         f"strides {qkv.stride()}")
-    if positions.shape != (axes.num_axes, n) or positions.dtype not in i32 or positions.device != dev or \
-            (n > 1 and positions.stride(1) != 1):
-        raise ValueError(f"positions: expected int32 {(axes.num_axes, n)} on {dev} with unit column stride, got "
-                         f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
-    if scales is not None:
-        ns = 2 * cfg.num_kv_heads + cfg.num_idx_k_heads if cfg.scale_mode == MSA_SCALE_PER_HEAD else 3
-        if scales.dim() != 1 or scales.shape[0] < ns:
-            raise ValueError(f"scales: expected at least {ns} values, got shape {tuple(scales.shape)}")
-        scales = _tensor("scales", scales, scales.shape, f32, dev)
-    weights = [_tensor("norm weight", w, (d,), bf16, dev) for w in norm_weights]
-    msa_producer_axes_forward(
-        cfg, axes, n, qkv.data_ptr(), qkv.stride(0) if n > 1 else max(qkv.stride(0), width), positions.data_ptr(),
-        max(positions.stride(0), n), _tensor("slot_mapping", slot_mapping, (n,), i64, dev),
-        None if page_table is None else _tensor("page_table", page_table, page_table.shape, i32, dev),
-        0 if page_table is None else page_table.numel(), *weights,
-        _tensor("q_out", q_out, (n, cfg.num_q_heads, d), bf16, dev),
-        _tensor("idx_q_out", idx_q_out, (n, cfg.num_idx_q_heads, d), bf16, dev), k_cache, v_cache, idx_k_cache,
-        scales, launch_flags, _stream_handle(dev, stream))
+    wq, wk, wiq, wik = norm_weights
+    s = (_marshal or _marshaller()).producer_axes(
+        (_lib or load()).entries["msa_producer_axes_forward"], cfg, axes, qkv, positions, slot_mapping, page_table,
+        wq, wk, wiq, wik, q_out, idx_q_out, k_cache, v_cache, idx_k_cache, scales, launch_flags,
+        None if stream is None else stream.cuda_stream)
+    if s != MSA_OK:
+        raise MsaError(s, "msa_producer_axes_forward", last_error_detail())

@@ -1,7 +1,8 @@
 """Builds the producer's C-ABI shared library for sm_103a with nvcc, in-tree.
 
-Output: ``paged_kv_cache_msa_gb300/lib/libmsa_producer.so`` (git-ignored).  Run as
-``python -m paged_kv_cache_msa_gb300.build`` or call ``build()``.
+Output: ``paged_kv_cache_msa_gb300/lib/libmsa_producer.so`` and, for torch callers,
+``lib/msa_marshal.so`` (both git-ignored).  Run as ``python -m
+paged_kv_cache_msa_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
 
@@ -102,6 +103,58 @@ def _fresh(lib: str, stamp: str, digest: str) -> bool:
         return f.read().strip() == digest
 
 
+# The CPython extension that turns torch tensors into C arguments (csrc/msa_marshal.cpp): host
+# code alone, by g++ beside nvcc.
+MARSHAL_SOURCE = os.path.join(PKG, "csrc", "msa_marshal.cpp")
+MARSHAL_PATH = os.path.join(OUT_DIR, "msa_marshal.so")
+
+
+def marshal_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(cuda_home(), "include"), "-isystem", inc, "-isystem",
+            os.path.join(inc, "torch", "csrc", "api", "include"),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", out, MARSHAL_SOURCE, "-L", lib,
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+
+
+def marshal_digest() -> str:
+    import torch
+    h = hashlib.sha256()
+    for path in [MARSHAL_SOURCE] + [os.path.join(INCLUDE, n) for n in sorted(os.listdir(INCLUDE))]:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    h.update(" ".join([torch.__version__, sys.version] + marshal_command("OUT")).encode())
+    return h.hexdigest()
+
+
+def _start_marshal(force: bool):
+    """Starts the extension's compiler unless it is up to date; finish with _finish_marshal."""
+    digest = marshal_digest()
+    if not force and _fresh(MARSHAL_PATH, MARSHAL_PATH + ".sha256", digest):
+        return None
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = f"{MARSHAL_PATH}.{os.getpid()}.tmp"
+    cmd = marshal_command(tmp)
+    return tmp, digest, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish_marshal(job) -> None:
+    if job is None:
+        return
+    tmp, digest, cmd, proc = job
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + out)
+    os.replace(tmp, MARSHAL_PATH)
+    with open(MARSHAL_PATH + ".sha256", "w") as f:
+        f.write(digest)
+
+
 def _compile(lib: str, stamp: str, digest: str, extra, verbose: bool = False,
              split: bool = True) -> None:
     """Compiles each translation unit to an object in parallel, then links them."""
@@ -154,8 +207,13 @@ def build(force: bool = False, verbose: bool = False, defines=None) -> str:
     if os.environ.get("MSA_NO_BUILD") == "1" and os.path.exists(LIB_PATH):
         return LIB_PATH
     digest = source_digest(defines)
+    try:
+        job = _start_marshal(force)
+    except ImportError:              # without torch there is nothing to marshal
+        job = None
     if force or not _fresh(LIB_PATH, STAMP_PATH, digest):
         _compile(LIB_PATH, STAMP_PATH, digest, [f"-D{d}" for d in defines], verbose)
+    _finish_marshal(job)
     return LIB_PATH
 
 

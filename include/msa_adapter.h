@@ -65,8 +65,8 @@ msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_t
  *                aligned, strides multiples of 8, >= W.  out may be rows (with the same
  *                stride); otherwise they must not overlap.
  * workspace      device, 256-byte aligned, msa_adapter_workspace_bytes(cfg, num_tokens) bytes.
- * launch_flags   MSA_LAUNCH_PDL: the first kernel is launched with programmatic dependent
- *                launch too (the later ones are in any case).
+ * launch_flags   MSA_LAUNCH_PDL: accepted; the kernels are launched with programmatic dependent
+ *                launch in any case.
  *
  * num_tokens at most 2^24; 0 returns MSA_OK and launches nothing.
  */

@@ -19,8 +19,7 @@
  * NaN (and out as the formula gives it); a row of zeros with rms_eps 0 gives NaN.
  *
  * Ownership and threading: as for msa_producer_forward.  One kernel is enqueued, which
- * reads and writes memory only after the kernels ahead of it on the stream are complete,
- * whether or not it is launched with programmatic dependent launch.
+ * reads and writes memory only after the kernels ahead of it on the stream are complete.
  */
 #ifndef MSA_NORM_H
 #define MSA_NORM_H
@@ -48,7 +47,8 @@ typedef struct {
  * out            device bf16 [num_tokens, out_stride], or NULL: not written.
  * codes, scales  device E4M3 [num_tokens, codes_stride] and fp32 [num_tokens], or both
  *                NULL: not written.  At least one of out and codes is given.
- * launch_flags   MSA_LAUNCH_PDL: programmatic dependent launch.
+ * launch_flags   MSA_LAUNCH_PDL: accepted; the kernel is launched with programmatic dependent
+ *                launch in any case.
  *
  * Row strides are in elements, at least K, and multiples of 8 (of codes: 16); the five
  * arrays of rows are 16-byte aligned.  Elements of a row from K on are neither read nor

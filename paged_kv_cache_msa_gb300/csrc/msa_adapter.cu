@@ -266,13 +266,26 @@ struct UpTile {
     }
 };
 
+// What the down-projection has written may be read from here on.  The rows, the adapters and the
+// ids may be read before: the down-projection's CTAs let this kernel start after they have waited
+// for the kernels ahead.
+__device__ __forceinline__ void wait_for_u()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+}
+
 // Columns [c, end) of any tile: for each distinct adapter its rows of up, AU adapters' at once.
+// `waited`: wait_for_u has been called; otherwise this does, once its first loads are under way.
 template <int RC, bool EXACT>
-__device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT> &t, const Tile &tile, int c, int end)
+__device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT> &t, const Tile &tile, int c, int end,
+                                       bool waited)
 {
     constexpr int AU = RC > 2 ? 1 : 4 / RC;
     const int up_row = 8 * (t.g >> 1) + (t.g & 1);
     if (!tile.leaders) {                             // a copy
+        if (!waited)
+            wait_for_u();
         for (; c < end; c += 128) {
             uint4 r[4][2];
 #pragma unroll
@@ -298,13 +311,10 @@ __device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT>
                 const uint4 r = *reinterpret_cast<const uint4 *>(t.src[h] + c);
                 in[h][0] = r.x, in[h][1] = r.y, in[h][2] = r.z, in[h][3] = r.w;
             }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            out[0][i] = in[0][i], out[1][i] = in[1][i];
-        t.slice_of(p, c);
-        for (uint32_t left = tile.leaders; left;) {
-            int ad[AU];
-            uint2 w[AU][4][RC];
+        uint32_t left = tile.leaders;
+        int ad[AU];
+        uint2 w[AU][4][RC];
+        auto load = [&]() {                          // the next AU adapters
 #pragma unroll
             for (int j = 0; j < AU; ++j) {
                 const int leader = left ? __ffs(left) - 1 : 0;
@@ -320,6 +330,17 @@ __device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT>
                             w[j][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * t.rank + 16 * k));
                     }
             }
+        };
+        load();
+        if (!waited) {
+            wait_for_u();
+            waited = true;
+        }
+        t.slice_of(p, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[0][i] = in[0][i], out[1][i] = in[1][i];
+        for (;;) {
 #pragma unroll
             for (int j = 0; j < AU; ++j)
                 if (ad[j] >= 0)
@@ -332,6 +353,9 @@ __device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT>
                         if (t.id[1] == ad[j])
                             out[1][i] = o1;
                     }
+            if (!left)
+                break;
+            load();
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -343,19 +367,17 @@ __device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT>
 template <int RC, bool EXACT>
 __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
     const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
     const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int64_t t0 = item % tiles * kTile, from = item / tiles * p.chunk;
-    if (from >= p.width)
+    const Tile tile = tile_of(p, from < p.width ? t0 : p.num_tokens);
+    if (from >= p.width || (p.out == p.rows && !tile.leaders)) {     // nothing to do; no CTA finishes before its wait
+        wait_for_u();
         return;
-    const Tile tile = tile_of(p, t0);
-    if (p.out == p.rows && !tile.leaders)
-        return;
+    }
     UpTile<RC, EXACT> t;
     t.init(p, tile, t0);
-    up_any(p, t, tile, (int)from, (int)min((int64_t)p.width, from + p.chunk));
+    up_any(p, t, tile, (int)from, (int)min((int64_t)p.width, from + p.chunk), false);
 }
 
 // The same for many tiles, whose rows are what costs (8,192 of 11,392 are 373 MB, 56 us at the
@@ -388,8 +410,6 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
 {
     extern __shared__ __align__(128) uint8_t s_up[];                 // two stages
     constexpr uint32_t kStageBytes = 32u * RC * kUpStage;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t groups = (p.num_tokens + 8 * kTile - 1) / (8 * kTile);
     const int64_t t0 = blockIdx.x % groups * (8 * kTile) + warp * kTile;
@@ -402,7 +422,9 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
         if (t0 < p.num_tokens && (p.out != p.rows || tile.leaders)) {
             UpTile<RC, EXACT> t;
             t.init(p, tile, t0);
-            up_any(p, t, tile, from, end);
+            up_any(p, t, tile, from, end, false);
+        } else {
+            wait_for_u();
         }
         return;
     }
@@ -434,6 +456,7 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
     };
     load_rows(next[0], from);
     load_rows(next[1], from + 32);
+    wait_for_u();
     const int up_row = 8 * (t.g >> 1) + (t.g & 1);
     uint32_t at[RC];                 // of this lane's piece k of row up_row
 #pragma unroll
@@ -558,11 +581,12 @@ Cut cut_of(const msa_adapter_cfg *cfg, int64_t T)
         most = units / 4 < kAdapterWideSplits ? units / 4 : kAdapterWideSplits;
         want = 2 * 152 / ctas;
     } else {
-        // so many pieces that a batch whose tokens all have adapters of their own fills the GPU, and
-        // no fewer than a unit of K for each warp
+        // so many pieces that a batch whose tokens all have adapters of their own fills the GPU once
+        // (two CTAs an SM; 64 tokens over 48 adapters in 1.2 rounds 25.1 us, in one 23), and no fewer
+        // than a unit of K for each warp
         const int64_t ctas = (T > 0 ? T : 1) * c.n_blocks;
         most = (units + kDownWarps - 1) / kDownWarps;
-        want = (2 * 152 + ctas - 1) / ctas;
+        want = 2 * 152 / ctas;
     }
     c.splits = (int)(want < most ? want : most);
     if (c.splits < 1)
@@ -619,7 +643,7 @@ msa_status check_args(const msa_adapter_cfg *cfg, int64_t T, const AdapterParams
     return MSA_OK;
 }
 
-msa_status launch(void (*kernel)(AdapterParams), dim3 grid, int threads, int smem, bool pdl, cudaStream_t stream, AdapterParams &p)
+msa_status launch(void (*kernel)(AdapterParams), dim3 grid, int threads, int smem, cudaStream_t stream, AdapterParams &p)
 {
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
@@ -631,7 +655,7 @@ msa_status launch(void (*kernel)(AdapterParams), dim3 grid, int threads, int sme
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = pdl ? 1 : 0;
+    lc.numAttrs = 1;
     void *args[] = {&p};
     const cudaError_t e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(kernel), args);
     if (e != cudaSuccess)
@@ -699,11 +723,11 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
          msa_adapter_down_kernel<true, 8>}};
     const int64_t tiles = (num_tokens + kTile - 1) / kTile;
     cudaError_t e = cudaSuccess;
-    if (!c.wide || !adapter_down_tiles(p, launch_flags & MSA_LAUNCH_PDL, stream, &e)) {
+    if (!c.wide || !adapter_down_tiles(p, stream, &e)) {
         const dim3 grid((unsigned)tiles, (unsigned)(num_tokens < kTile ? num_tokens : kTile),
                         (unsigned)(c.n_blocks * c.splits));
         const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], grid, 32 * kDownWarps, 0,
-                                    launch_flags & MSA_LAUNCH_PDL, stream, p);
+                                    stream, p);
         if (d != MSA_OK)
             return d;
     }
@@ -722,7 +746,7 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
         p.chunk = 32;
         const int64_t items = tiles * pieces;
         const int warps = items < 2 * 152 ? 1 : 4;
-        return launch(ups[exact][rc], dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, true, stream, p);
+        return launch(ups[exact][rc], dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, stream, p);
     }
     static const Kernel ups[2][4] = {{msa_adapter_up_stream_kernel<1, false>, msa_adapter_up_stream_kernel<2, false>,
                                       msa_adapter_up_stream_kernel<4, false>, msa_adapter_up_stream_kernel<8, false>},
@@ -736,7 +760,7 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     e = cudaFuncSetAttribute(reinterpret_cast<const void *>(ups[exact][rc]), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
-    return launch(ups[exact][rc], dim3((unsigned)(groups * ((p.width + p.chunk - 1) / p.chunk))), 256, smem, true, stream, p);
+    return launch(ups[exact][rc], dim3((unsigned)(groups * ((p.width + p.chunk - 1) / p.chunk))), 256, smem, stream, p);
 }
 
 }  // extern "C"

@@ -30,7 +30,7 @@ struct AdapterParams {
 
 // The down-projection in tiles of 128 tokens (msa_adapter_tile.cu) into p.u, pieces of K as
 // p.splits says; false when TMA does not take the layout (nothing is enqueued then).
-bool adapter_down_tiles(const AdapterParams &p, bool pdl, cudaStream_t stream, cudaError_t *error);
+bool adapter_down_tiles(const AdapterParams &p, cudaStream_t stream, cudaError_t *error);
 
 #ifdef __CUDACC__
 namespace {

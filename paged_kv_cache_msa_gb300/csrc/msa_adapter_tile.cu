@@ -345,7 +345,7 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
 
 }  // namespace
 
-bool adapter_down_tiles(const AdapterParams &p, bool pdl, cudaStream_t stream, cudaError_t *error)
+bool adapter_down_tiles(const AdapterParams &p, cudaStream_t stream, cudaError_t *error)
 {
     *error = cudaSuccess;
     const int rows = p.num_slices * p.rank;
@@ -388,7 +388,7 @@ bool adapter_down_tiles(const AdapterParams &p, bool pdl, cudaStream_t stream, c
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = pdl ? 1 : 0;
+    lc.numAttrs = 1;
     AdapterParams params = p;
     void *args[] = {&params, &s, &xmap, &wmap};
     *error = cudaLaunchKernelExC(&lc, fn, args);

@@ -387,7 +387,7 @@ extern "C" msa_status msa_norm_forward(const msa_norm_cfg *cfg, int64_t num_toke
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = launch_flags & MSA_LAUNCH_PDL ? 1 : 0;
+    lc.numAttrs = 1;
     void *args[] = {&p};
     const cudaError_t e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(kernels[v - 1]), args);
     if (e != cudaSuccess)

@@ -269,3 +269,31 @@ def test_tiles_of_several_adapters_over_many_blocks():
         for i, n in enumerate(edges.diff().tolist()):
             ids += [i % 7 - 1] * n
         Case(ids, k=128, ends=PACKED, adapters=6, rank=(16, 32, 64, 96)[seed % 4], seed=seed).run().check()
+
+
+@pytest.mark.parametrize("t", [3, 64, 700])
+def test_a_chain_in_place(t):
+    """Calls that each add to what the one before wrote, hidden states made by the kernel just ahead:
+    the bits of the same calls with the device idle between them."""
+    c = Case(mixed(t, 4), k=512)
+    start, src = c.rows.clone(), c.hidden.clone()
+
+    def steps(between):
+        c.rows.copy_(start)
+        for i in range(12):
+            torch.mul(src, 1.0 + i / 8, out=c.hidden) if not between else c.hidden.copy_(src * (1.0 + i / 8))
+            between and torch.cuda.synchronize()
+            c.run(out=c.rows)
+            between and torch.cuda.synchronize()
+        return c.rows.clone()
+
+    want = steps(True)
+    for _ in range(3):
+        assert torch.equal(steps(False).view(torch.int16), want.view(torch.int16))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = steps(False)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))

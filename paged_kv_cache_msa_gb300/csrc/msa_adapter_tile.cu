@@ -24,6 +24,7 @@ constexpr int kM = 128;                       // tokens of a tile
 constexpr int kBlockK = 64;                   // K elements of a stage: 128 bytes of bf16
 constexpr int kMaxStages = 8;
 constexpr int kWorkers = 8;                   // conversion and epilogue warps
+constexpr int kPieces = 4 * kM / (32 * kWorkers);   // pieces of 16 codes of a K block a thread has
 constexpr int kThreads = 64 + 32 * kWorkers;
 constexpr int kAhead = 4;                     // K blocks of E4M3 values loaded ahead
 constexpr uint32_t kTileX = kM * 128;
@@ -85,6 +86,13 @@ __device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void commit_one(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
 }
 
 // 16 codes of a row from k on, zeros from K on
@@ -261,19 +269,19 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
         for (int pass = pass0; pass < count; pass += pass_step, ++done) {
             const int a = s_list[pass];
             if (FP8) {
-                // this thread's pieces of 16 codes: of rows w / 4 and 64 + w / 4
+                // this thread's pieces of 16 codes: of row w / 4, and of rows that many further
                 const int col = 16 * (w & 3);
-                const uint8_t *src[2];
+                const uint8_t *src[kPieces];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = (w >> 2) + 64 * h;
+                for (int h = 0; h < kPieces; ++h) {
+                    const int r = (w >> 2) + 8 * kWorkers * h;
                     src[h] = s_id[r] == a ? p.hidden + (t0 + r) * p.hidden_stride : nullptr;
                 }
-                uint4 next[kAhead][2];
+                uint4 next[kAhead][kPieces];
 #pragma unroll
                 for (int d = 0; d < kAhead; ++d)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < kPieces; ++h)
                         next[d][h] = src[h] && k0 + d < k1 ? load_codes(src[h], (k0 + d) * kBlockK + col, p.hidden_size)
                                                            : make_uint4(0, 0, 0, 0);
                 for (int kb = k0; ok && kb < k1; kb += kAhead) {
@@ -286,9 +294,9 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
                             break;
                         const uint32_t x = ring + st.at * s.stage_bytes;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < kPieces; ++h) {
                             const uint4 c = next[d][h];
-                            const uint32_t off = (uint32_t)((w >> 2) + 64 * h) * 128u + 2u * (uint32_t)col;
+                            const uint32_t off = (uint32_t)((w >> 2) + 8 * kWorkers * h) * 128u + 2u * (uint32_t)col;
                             sts128(x + swizzle<128>(off), adapter_e4m3x2(c.x & 0xffffu), adapter_e4m3x2(c.x >> 16),
                                    adapter_e4m3x2(c.y & 0xffffu), adapter_e4m3x2(c.y >> 16));
                             sts128(x + swizzle<128>(off + 16u), adapter_e4m3x2(c.z & 0xffffu), adapter_e4m3x2(c.z >> 16),
@@ -310,21 +318,39 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
             float *dst = p.u + ((int64_t)blockIdx.y * p.num_tokens + t) * rows;
             if (ok)
                 tc_fence_after();
-            for (int col = 16 * part; col < rows; col += 32) {
+            // Through the ring, which is free after the last pass, so that four lanes write 64
+            // bytes of a row (each lane a row of its own: 7.5 us more of 32); rows 80 bytes apart lie
+            // on different banks.  An earlier pass, of a tile of many adapters, writes its rows as
+            // they are.
+            const bool last = pass + pass_step >= count;
+            const uint32_t buf = ring + (uint32_t)(warp - 2) * (32u * 80u);
+            for (int col = 16 * part; col < rows; col += 16 * (kWorkers / 4)) {
                 uint32_t v[16];
                 if (ok) {
                     tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col, v);
                     tc_wait_ld();
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (mine && col + 4 * j < rows) {
-                        float f[4];
+                for (int e = 0; e < 16; ++e)
+                    v[e] = ok ? __float_as_uint(c * __uint_as_float(v[e])) : 0x7fc00000u;
+                if (last) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            f[e] = ok ? c * __uint_as_float(v[4 * j + e]) : __int_as_float(0x7fc00000);
-                        *reinterpret_cast<float4 *>(dst + col + 4 * j) = make_float4(f[0], f[1], f[2], f[3]);
+                    for (int j = 0; j < 4; ++j)
+                        sts128(buf + (uint32_t)lane * 80u + 16u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = quarter * 32 + 8 * j + (lane >> 2), at = col + 4 * (lane & 3);
+                        const uint4 x = lds128(buf + (uint32_t)(8 * j + (lane >> 2)) * 80u + 16u * (lane & 3));
+                        if (s_id[r] == a && at < rows)
+                            *reinterpret_cast<uint4 *>(p.u + ((int64_t)blockIdx.y * p.num_tokens + t0 + r) * rows + at) = x;
                     }
+                } else if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + 4 * j < rows)
+                            *reinterpret_cast<uint4 *>(dst + col + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
                 __syncwarp();
             }
             tc_fence_before();

@@ -382,9 +382,10 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(co
 
 // The same for many tiles, whose rows are what costs (8,192 of 11,392 are 373 MB, 56 us at the
 // copy rate).  A CTA takes eight tiles (128 tokens) and `chunk` columns.  Where they share one
-// adapter -- all but the borders of a prefill's chunks -- its rows of up go through shared memory,
-// kUpStage columns ahead of those that are computed, and a warp has the rows of its next two
-// blocks of 32 columns in flight.  The 32-byte pieces of a row of up are placed so that the rows
+// adapter -- all but the borders of a prefill's chunks -- its rows of up and the tokens' rows go
+// through shared memory, kUpStage columns ahead of those that are computed: a lane copies the
+// pieces of rows that it uses, 8 KB a warp, 128 KB an SM in flight (with two blocks of 32 columns
+// in registers, 32 KB an SM, 80 us and not 70).  The 32-byte pieces of a row of up are placed so that the rows
 // 0, 1, 8 and 9 (16, 17, 24 and 25), of which a half warp loads a piece each, lie on different
 // banks: the two rows 2 apart go elsewhere (ranks up to 16), or the piece's number is changed.
 constexpr int kUpStage = 128;        // columns of a stage of up
@@ -408,8 +409,8 @@ __device__ constexpr uint32_t up_step(int i)
 template <int RC, bool EXACT>
 __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_kernel(const __grid_constant__ AdapterParams p)
 {
-    extern __shared__ __align__(128) uint8_t s_up[];                 // two stages
-    constexpr uint32_t kStageBytes = 32u * RC * kUpStage;
+    extern __shared__ __align__(128) uint8_t s_up[];                 // two stages of up, two of each warp's rows
+    constexpr uint32_t kStageBytes = 32u * RC * kUpStage, kRowBytes = 16u * 32u * 2u * (kUpStage / 32);
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t groups = (p.num_tokens + 8 * kTile - 1) / (8 * kTile);
     const int64_t t0 = blockIdx.x % groups * (8 * kTile) + warp * kTile;
@@ -431,31 +432,33 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
     UpTile<RC, EXACT> t;
     t.init(p, tile, t0);
     const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(s_up);
-    // 16-byte halves of pieces; zeros beyond the rank and the last column
-    auto stage = [&](int c, uint32_t dst) {
+    const uint32_t s_rows = s0 + 2u * kStageBytes + (uint32_t)warp * (2u * kRowBytes) + 16u * (uint32_t)(tid & 31);
+    // 16 bytes, zeros where there is nothing
+    auto copy16 = [](uint32_t to, const uint16_t *from, bool there) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+    };
+    auto stage = [&](int c, uint32_t buf) {
+#pragma unroll
+        for (int b = 0; b < kUpStage / 32; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool there = t.live[h] && c + 32 * b + 8 * t.q < end;
+                copy16(s_rows + buf * kRowBytes + (uint32_t)(2 * b + h) * 512u, there ? t.src[h] + c + 32 * b : p.rows, there);
+            }
+        // halves of pieces of up
         const uint16_t *up = p.up + ((int64_t)first * p.width + c) * t.rank;
-        for (int e = tid; e < kUpStage * 2 * RC; e += 256) {
-            const int row = e / (2 * RC), h = e % (2 * RC);
+#pragma unroll
+        for (int e0 = 0; e0 < kUpStage * 2 * RC; e0 += 256) {
+            const int e = e0 + tid, row = e / (2 * RC), h = e % (2 * RC);
             const bool there = c + row < end && (EXACT || 8 * h < t.rank);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + up_piece<RC>(row, h >> 1) + 16u * (h & 1)),
-                         "l"(there ? up + row * t.rank + 8 * h : p.up), "r"(there ? 16 : 0)
-                         : "memory");
+            copy16(s0 + buf * kStageBytes + up_piece<RC>(row, h >> 1) + 16u * (h & 1), there ? up + row * t.rank + 8 * h : p.up,
+                   there);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    stage(from, s0);
+    stage(from, 0);
     if (from + kUpStage < end)
-        stage(from + kUpStage, s0 + kStageBytes);
-    uint4 next[2][2] = {};           // rows of this block of 32 columns and the next
-    auto load_rows = [&](uint4 (&row)[2], int c) {
-        if (c + 8 * t.q < end)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (t.live[h])
-                    row[h] = *reinterpret_cast<const uint4 *>(t.src[h] + c);
-    };
-    load_rows(next[0], from);
-    load_rows(next[1], from + 32);
+        stage(from + kUpStage, 1);
     wait_for_u();
     const int up_row = 8 * (t.g >> 1) + (t.g & 1);
     uint32_t at[RC];                 // of this lane's piece k of row up_row
@@ -468,19 +471,19 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
         else
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        const uint32_t base = (uint32_t)(it & 1) * kStageBytes;
+        const uint32_t buf = (uint32_t)(it & 1);
 #pragma unroll 2
         for (int b = 0; b < kUpStage / 32; ++b) {
             const int c = c0 + 32 * b;
             if (c >= end)
                 break;
-            const uint4 r0 = next[0][0], r1 = next[0][1];
-            next[0][0] = next[1][0];
-            next[0][1] = next[1][1];
-            load_rows(next[1], c + 64);
             t.slice_of(p, c);
-            const uint32_t in[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
-            uint32_t out[2][4];
+            uint32_t in[2][4], out[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(in[h][0]), "=r"(in[h][1]), "=r"(in[h][2]), "=r"(in[h][3])
+                             : "r"(s_rows + buf * kRowBytes + (uint32_t)(2 * b + h) * 512u));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint2 w[RC];
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
                 for (int k = 0; k < RC; ++k)
                     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                                  : "=r"(w[k].x), "=r"(w[k].y)
-                                 : "r"(at[k] + base + (uint32_t)b * (1024u * RC) + up_step<RC>(i)));
+                                 : "r"(at[k] + buf * kStageBytes + (uint32_t)b * (1024u * RC) + up_step<RC>(i)));
                 t.add(in[0][i], in[1][i], w, out[0][i], out[1][i]);
             }
             if (c + 8 * t.q < end)
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
         }
         __syncthreads();
         if (c0 + 2 * kUpStage < end)
-            stage(c0 + 2 * kUpStage, s0 + base);
+            stage(c0 + 2 * kUpStage, buf);
     }
 }
 
@@ -752,10 +755,10 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
                                       msa_adapter_up_stream_kernel<4, false>, msa_adapter_up_stream_kernel<8, false>},
                                      {msa_adapter_up_stream_kernel<1, true>, msa_adapter_up_stream_kernel<2, true>,
                                       msa_adapter_up_stream_kernel<4, true>, msa_adapter_up_stream_kernel<8, true>}};
-    const int smem = 2 * (32 << rc) * kUpStage;
+    const int smem = 2 * (32 << rc) * kUpStage + 8 * 2 * (16 * 32 * 2 * (kUpStage / 32));
     const int64_t groups = (tiles + 7) / 8;
     p.chunk = kUpStage;
-    while (p.chunk < 512 && groups * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152)
+    while (p.chunk < 1024 && groups * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152)
         p.chunk *= 2;
     e = cudaFuncSetAttribute(reinterpret_cast<const void *>(ups[exact][rc]), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)

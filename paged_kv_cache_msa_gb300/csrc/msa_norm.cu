@@ -27,7 +27,10 @@
 namespace {
 
 constexpr int kMaxHidden = 16384;
-constexpr int kMaxVecs = 4;                 // vectors of 8 elements a thread
+constexpr int kMaxVecs = 7;                 // vectors of 8 elements a thread
+// Registers of a thread that has V vectors, and the warps of it that an SM holds.
+constexpr int kRegs[kMaxVecs + 1] = {0, 64, 64, 64, 80, 96, 112, 128};
+constexpr int warps_of(int v) { return 16384 / (32 * kRegs[v]) * 4; }
 constexpr int kWarpRows = 8;                // rows of one warp each share a CTA
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
 constexpr float kHuge = 3.0e38f;
@@ -160,7 +163,7 @@ __device__ __forceinline__ void partial_sums(const float2 (&h)[V][4], const uint
 }
 
 template <int V>
-__global__ void __launch_bounds__(V == 3 ? 256 : V == 4 ? 512 : 1024)
+__global__ void __maxnreg__(kRegs[V])
 msa_norm_kernel(const __grid_constant__ Params p)
 {
     const int tpr = p.threads_per_row, warps = tpr >> 5;
@@ -368,16 +371,28 @@ extern "C" msa_status msa_norm_forward(const msa_norm_cfg *cfg, int64_t num_toke
     p.eps = cfg->rms_eps;
     p.inv_hidden = 1.0f / (float)p.hidden;
 
-    // Threads of a row: so many that a thread has few vectors where the rows are few and the
-    // chain of one row counts; otherwise so few that several rows are in flight on an SM.
+    // Vectors of a thread.  Rows whose warps fit onto the GPU twice with one vector each: one, since
+    // the chain of a row is what takes time (one token of 6,144 2.4 us; 777 of 1,001 2.45 us, 2.95 with
+    // four).  Otherwise those with which an SM has most vectors in flight, whole rows of its resident
+    // warps: 8,192 x 6,144 takes 55.5 us with three (3,072 vectors an SM), 58.6 with four, of 80
+    // registers (3,072 too), 60.4 with three of 73 (2,304); rows of 1,536 run at 0.99 of the copy rate
+    // with three each and at 0.59 with one.
     int v = 1;
-    while (v < kMaxVecs && (p.vecs + v - 1) / v > (num_tokens <= 304 ? 1024 : 256))
-        ++v;
+    if (p.vecs > 1024 || num_tokens * ((p.vecs + 31) / 32) > 2 * 152 * warps_of(1)) {
+        int best = 0;
+        for (int i = 1; i <= kMaxVecs; ++i) {
+            const int wpr = (p.vecs + 32 * i - 1) / (32 * i), flying = warps_of(i) / wpr * p.vecs;
+            if (flying > best) {
+                best = flying;
+                v = i;
+            }
+        }
+    }
     p.threads_per_row = ((p.vecs + v - 1) / v + 31) / 32 * 32;
     const int rows = p.threads_per_row == 32 ? kWarpRows : 1;
     using Kernel = void (*)(Params);
-    static const Kernel kernels[kMaxVecs] = {msa_norm_kernel<1>, msa_norm_kernel<2>, msa_norm_kernel<3>,
-                                             msa_norm_kernel<4>};
+    static const Kernel kernels[kMaxVecs] = {msa_norm_kernel<1>, msa_norm_kernel<2>, msa_norm_kernel<3>, msa_norm_kernel<4>,
+                                             msa_norm_kernel<5>, msa_norm_kernel<6>, msa_norm_kernel<7>};
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
     lc.gridDim = dim3((unsigned)((num_tokens + rows - 1) / rows));

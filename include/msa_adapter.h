@@ -40,7 +40,7 @@ extern "C" {
 typedef struct {
     int32_t hidden_size;    /* K >= 1 */
     int32_t rank;           /* a multiple of 8, 8..128 */
-    int32_t num_adapters;   /* >= 1 */
+    int32_t num_adapters;   /* 1..16384 */
     int32_t hidden_dtype;   /* msa_dtype of hidden: bf16 or E4M3 */
     int32_t num_slices;     /* 1..MSA_ADAPTER_MAX_SLICES; num_slices * rank <= 512 */
     int32_t slice_end[MSA_ADAPTER_MAX_SLICES]; /* ascending; all but the last multiples of 64,
@@ -49,7 +49,8 @@ typedef struct {
 } msa_adapter_cfg;
 
 /* Bytes of workspace msa_adapter_forward needs for num_tokens tokens under cfg: less than
- * 1 MB, and at most 16 * num_slices * rank bytes a token.  Host-side; enqueues nothing. */
+ * 2 MB and 512 bytes an adapter, and at most 16 * num_slices * rank + 80 bytes a token.
+ * Host-side; enqueues nothing. */
 msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_tokens, int64_t *bytes);
 
 /*
@@ -57,7 +58,7 @@ msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_t
  *                stride (elements) a multiple of 16 bytes, >= K.  Elements from K on are not read.
  * hidden_scales  device fp32 [num_tokens], or NULL: 1.
  * down           device bf16 [num_adapters, num_slices * rank, down_stride], 16-byte aligned,
- *                down_stride a multiple of 8, >= K.
+ *                down_stride a multiple of 8, >= K, below 2^39.
  * up             device bf16 [num_adapters, W, rank], 16-byte aligned.
  * adapter_ids    device int32 [num_tokens], in any order.
  * adapter_scales device fp32 [num_adapters], or NULL: 1.

@@ -1,12 +1,17 @@
 // Low-rank adapters of many requests beside a shared projection (include/msa_adapter.h).
 //
-// Two kernels: every token's hidden state through its own adapter's down-projection into a
-// workspace (partial sums over pieces of K), and the up-projection of their sum added to the
-// rows.  Both take tiles of 16 tokens in any order and go through the distinct adapters of a
-// tile, one MMA (m16n8k16) tile of 16 tokens for each: a token of another adapter has a row of
-// its own in the MMA, which is left out, so nothing passes from one request to another.
-// Reading an adapter is what a decode batch costs (65 MB for 64 tokens over 48 adapters of
-// rank 16), and reading and writing the rows what a prefill costs; both are bound by HBM.
+// Up to three kernels:
+//   sort   the tokens by adapter, in tiles of 16 or 128 of one adapter each (not for one tile of
+//          tokens, whose distinct adapters a warp finds by itself).  Reading an adapter costs more
+//          than anything else in a decode batch, and in no order of the tokens is it read more
+//          often than once a tile: 512 tokens over 16 adapters, mixed, took 100 us in tiles of
+//          consecutive tokens that go through their distinct adapters.
+//   down   every token's hidden state through its adapter's down-projection, into a workspace
+//          (partial sums over pieces of K)
+//   up     the up-projection of their sum, added to the rows
+// A tile's tokens share the MMA's B operand, its adapter; each has a row of its own, so nothing
+// passes from one request to another.  Reading the adapters bounds a decode batch (65 MB for 64
+// tokens over 48 adapters of rank 16), reading and writing the rows a prefill: both HBM.
 
 #include "msa_adapter_internal.h"
 
@@ -21,8 +26,9 @@ namespace {
 
 constexpr int kTile = 16;            // tokens of a tile: the MMA's M
 constexpr int kDownWarps = 8;        // warps of a CTA of the down-projection, each a piece of its K
-constexpr int64_t kWideTokens = 256; // tokens from which the down-projection takes tiles of 128
 constexpr int kUnitK = 64;           // K elements a warp takes at a time: 128 bytes of bf16
+constexpr int kFill = 2 * 152;       // CTAs that fill the GPU at two an SM
+constexpr int kMaxAdapters = 16384;  // the sort counts them in shared memory
 
 __device__ __forceinline__ float2 unpack2(uint32_t v)
 {
@@ -37,25 +43,148 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The adapters of a tile of 16 tokens: a lane's token is lane % 16.
-struct Tile {
-    int id;              // this lane's adapter, -1: none
-    uint32_t same;       // the tile's tokens with the same one
-    uint32_t leaders;    // the first token of each distinct adapter
-};
-
-__device__ __forceinline__ Tile tile_of(const AdapterParams &p, int64_t t0)
+// The next kernel may start once this one has waited for those ahead.  So whatever they wrote may
+// be read before a later kernel's own wait; only what this call's kernels write may not.
+__device__ __forceinline__ void wait_for_kernels_ahead()
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = t0 + (lane & 15);
-    Tile w;
-    w.id = t < p.num_tokens ? p.ids[t] : -1;
-    if (w.id < 0 || w.id >= p.num_adapters)
-        w.id = -1;
-    w.same = __match_any_sync(0xffffffffu, w.id) & 0xffffu;
-    w.leaders = __ballot_sync(0xffffffffu, w.id >= 0 && lane == __ffs(w.same) - 1);
-    return w;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" :::);
 }
+
+// ---------------------------------------------------------------------------
+// the tokens by adapter
+// ---------------------------------------------------------------------------
+
+// One CTA: counts, the adapters' first tiles, then each token's place.  Tokens of one warp with the
+// same adapter (a prefill's chunk) take their places with one atomic.  Which of an adapter's tokens
+// share a tile depends on the order of the warps; no token's result depends on that.
+__global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_constant__ AdapterParams p)
+{
+    extern __shared__ int s_place[];                 // a count, then the next place, of each adapter; the last: none
+    __shared__ int s_sum[32];
+    wait_for_kernels_ahead();
+    const int tid = threadIdx.x, lane = tid & 31, n = p.num_adapters + 1;
+    const int64_t T = p.num_tokens;
+    for (int a = tid; a < n; a += 1024)
+        s_place[a] = 0;
+    __syncthreads();
+    auto adapter_of = [&](int64_t t) {
+        const int a = t < T ? __ldg(p.ids + t) : -2;
+        return t < T && (a < 0 || a >= p.num_adapters) ? n - 1 : a;
+    };
+    for (int64_t t0 = tid - lane; t0 < T; t0 += 1024) {
+        const int a = adapter_of(t0 + lane);
+        const uint32_t same = __match_any_sync(0xffffffffu, a);
+        if (a >= 0 && lane == __ffs(same) - 1)
+            atomicAdd(&s_place[a], __popc(same));
+    }
+    __syncthreads();
+    // tiles before each adapter's: a run of adapters a thread
+    const int ts = p.tile_tokens, per = (n + 1023) / 1024, a0 = min(n, tid * per), a1 = min(n, a0 + per);
+    int sum = 0;
+    for (int a = a0; a < a1; ++a)
+        sum += (s_place[a] + ts - 1) / ts;
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o)
+            before += x;
+    }
+    if (lane == 31)
+        s_sum[tid >> 5] = before;
+    __syncthreads();
+    if (tid < 32) {
+        int x = s_sum[tid];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (tid >= o)
+                x += y;
+        }
+        s_sum[tid] = x;
+    }
+    __syncthreads();
+    int tile = before - sum + (tid >= 32 ? s_sum[(tid >> 5) - 1] : 0);
+    for (int a = a0; a < a1; ++a) {
+        const int count = s_place[a], tiles = (count + ts - 1) / ts;
+        if (a == n - 1) {
+            p.head->with_adapter = tile;
+            p.head->tiles = tile + tiles;
+            // so many pieces of K that the down-projection fills the GPU once
+            const int units = max(1, tile * p.n_blocks);
+            p.head->splits = max(1, min(p.max_splits, kFill / units));
+        }
+        s_place[a] = tile * ts;
+        for (int i = count; i < tiles * ts; ++i)
+            p.tokens[tile * ts + i] = -1;
+        tile += tiles;
+    }
+    __syncthreads();
+    for (int64_t t0 = tid - lane; t0 < T; t0 += 1024) {
+        const int a = adapter_of(t0 + lane);
+        const uint32_t same = __match_any_sync(0xffffffffu, a);
+        const int leader = __ffs(same) - 1;
+        int at = 0;
+        if (a >= 0 && lane == leader)
+            at = atomicAdd(&s_place[a], __popc(same));
+        at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+        if (a >= 0) {
+            p.tokens[at] = (int)(t0 + lane);
+            if (at % ts == 0)
+                p.adapters[at / ts] = a == n - 1 ? -1 : a;
+        }
+    }
+}
+
+// The tiles of 16 tokens of one adapter, from the sort, or (p.tokens nullptr: at most 16 tokens)
+// found by each warp.  Those without an adapter come last.
+struct Tiles {
+    int with_adapter, all, splits;
+    int id;              // at most 16 tokens: this lane's token's adapter, and
+    uint32_t same;       // the tokens with the same one
+    uint32_t leaders;    // the first token of each distinct adapter
+
+    __device__ __forceinline__ void load(const AdapterParams &p)
+    {
+        if (p.tokens) {
+            with_adapter = p.head->with_adapter;
+            all = p.head->tiles;
+            splits = p.head->splits;
+            return;
+        }
+        const int lane = threadIdx.x & 31, t = lane & 15;
+        id = t < p.num_tokens ? p.ids[t] : -1;
+        if (id < 0 || id >= p.num_adapters)
+            id = -1;
+        same = __match_any_sync(0xffffffffu, id) & 0xffffu;
+        leaders = __ballot_sync(0xffffffffu, id >= 0 && lane == __ffs(same) - 1);
+        with_adapter = __popc(leaders);
+        all = with_adapter + (__any_sync(0xffffffffu, id < 0 && t < p.num_tokens) ? 1 : 0);
+        splits = max(1, min(p.max_splits, kFill / max(1, with_adapter * p.n_blocks)));
+    }
+    // The adapter of a tile, and this lane's token (of slot lane % 16), -1 without one.
+    __device__ __forceinline__ void get(const AdapterParams &p, int tile, int &adapter, int &token) const
+    {
+        const int slot = threadIdx.x & 15;
+        if (p.tokens) {
+            adapter = p.adapters[tile];
+            token = p.tokens[tile * kTile + slot];
+            return;
+        }
+        uint32_t left = leaders;
+        for (int j = 0; j < tile; ++j)
+            left &= left - 1;
+        if (left) {
+            const int leader = __ffs(left) - 1;
+            adapter = __shfl_sync(0xffffffffu, id, leader);
+            token = __shfl_sync(0xffffffffu, same, leader) >> slot & 1u ? slot : -1;
+        } else {
+            adapter = -1;
+            token = id < 0 && slot < p.num_tokens ? slot : -1;
+        }
+    }
+};
 
 // 8 elements of a row from k on as bf16 pairs, zeros from K on; k is a multiple of 8.
 template <bool FP8>
@@ -100,86 +229,86 @@ __device__ __forceinline__ uint4 load_down(const AdapterParams &p, const uint16_
 }
 
 // ---------------------------------------------------------------------------
-// the down-projection of a tile of 16 tokens
+// the down-projection of tiles of 16 tokens
 // ---------------------------------------------------------------------------
 //
-// A CTA takes one distinct adapter of a tile (blockIdx.y), a block of up to 8 * NT of its rows
-// and a piece of K, which its warps share; their sums meet in shared memory.  A lane holds 8
-// neighbouring elements of K of a token's row and of an adapter's row: the MMA's order of K
-// is free as long as both operands agree, so 16-byte loads are its fragments as they come.
+// A CTA takes a tile, a block of up to 8 * NT of its adapter's rows and a piece of K, which its
+// warps share; their sums meet in shared memory.  A lane holds 8 neighbouring elements of K of a
+// token's row and of an adapter's row: the MMA's order of K is free as long as both operands
+// agree, so 16-byte loads are its fragments as they come.
 template <bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const __grid_constant__ AdapterParams p)
 {
     __shared__ float s_sum[kDownWarps][kTile][8 * NT];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
+    wait_for_kernels_ahead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int64_t t0 = (int64_t)blockIdx.x * kTile;
-    const Tile tile = tile_of(p, t0);
-    uint32_t left = tile.leaders;
-    for (unsigned j = 0; j < blockIdx.y; ++j)
-        left &= left - 1;
-    if (!left)
-        return;                      // the tile has fewer adapters
-    const int leader = __ffs(left) - 1;
-    const int a = __shfl_sync(0xffffffffu, tile.id, leader);
-    const uint32_t mine = __shfl_sync(0xffffffffu, tile.same, leader);
-    const bool row0 = (mine >> g) & 1, row1 = (mine >> (g + 8)) & 1;
-
     const int n = p.num_slices * p.rank;
-    const int block = blockIdx.z % p.n_blocks, split = blockIdx.z / p.n_blocks;
-    const int n0 = block * p.n_tiles * 8;
-    const uint16_t *rows[NT];        // nullptr: none
+    Tiles tiles;
+    tiles.load(p);
+    const int work = tiles.with_adapter * p.n_blocks * tiles.splits;
+    for (int item = blockIdx.x; item < work; item += gridDim.x) {
+        const int block = item % p.n_blocks, split = item / p.n_blocks % tiles.splits;
+        int a, token;
+        tiles.get(p, item / p.n_blocks / tiles.splits, a, token);
+        const int tok[2] = {__shfl_sync(0xffffffffu, token, g), __shfl_sync(0xffffffffu, token, g + 8)};
+        const int n0 = block * p.n_tiles * 8;
+        const uint16_t *rows[NT];        // nullptr: none
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int r = n0 + 8 * i + g;
-        rows[i] = i < p.n_tiles && r < n ? p.down + ((int64_t)a * n + r) * p.down_stride : nullptr;
-    }
-    const int units = (p.hidden_size + kUnitK - 1) / kUnitK;
-    const int piece = split * kDownWarps + warp, pieces = p.splits * kDownWarps;
-    const int first = (int)((int64_t)units * piece / pieces), last = (int)((int64_t)units * (piece + 1) / pieces);
-
-    float acc[NT][4] = {};
-    for (int u = first; u < last; ++u) {
-        uint4 x[2][2], w[NT][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = u * kUnitK + 32 * h + 8 * q;
-            const uint4 none = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                w[i][h] = rows[i] ? load_down(p, rows[i], k) : none;
-            x[0][h] = row0 ? load_hidden<FP8>(p, t0 + g, k) : none;
-            x[1][h] = row1 ? load_hidden<FP8>(p, t0 + g + 8, k) : none;
+        for (int i = 0; i < NT; ++i) {
+            const int r = n0 + 8 * i + g;
+            rows[i] = i < p.n_tiles && r < n ? p.down + ((int64_t)a * n + r) * p.down_stride : nullptr;
         }
+        const int units = (p.hidden_size + kUnitK - 1) / kUnitK;
+        const int piece = split * kDownWarps + warp, pieces = tiles.splits * kDownWarps;
+        const int first = (int)((int64_t)units * piece / pieces), last = (int)((int64_t)units * (piece + 1) / pieces);
+
+        float acc[NT][4] = {};
+        for (int u = first; u < last; ++u) {
+            uint4 x[2][2], w[NT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t lo[4] = {x[0][h].x, x[1][h].x, x[0][h].y, x[1][h].y};
-            const uint32_t hi[4] = {x[0][h].z, x[1][h].z, x[0][h].w, x[1][h].w};
+            for (int h = 0; h < 2; ++h) {
+                const int k = u * kUnitK + 32 * h + 8 * q;
+                const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                mma(acc[i], lo, w[i][h].x, w[i][h].y);
-                mma(acc[i], hi, w[i][h].z, w[i][h].w);
+                for (int i = 0; i < NT; ++i)
+                    w[i][h] = rows[i] ? load_down(p, rows[i], k) : none;
+                x[0][h] = tok[0] >= 0 ? load_hidden<FP8>(p, tok[0], k) : none;
+                x[1][h] = tok[1] >= 0 ? load_hidden<FP8>(p, tok[1], k) : none;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t lo[4] = {x[0][h].x, x[1][h].x, x[0][h].y, x[1][h].y};
+                const uint32_t hi[4] = {x[0][h].z, x[1][h].z, x[0][h].w, x[1][h].w};
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    mma(acc[i], lo, w[i][h].x, w[i][h].y);
+                    mma(acc[i], hi, w[i][h].z, w[i][h].w);
+                }
             }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<float2 *>(&s_sum[warp][g][8 * i + 2 * q]) = make_float2(acc[i][0], acc[i][1]);
-        *reinterpret_cast<float2 *>(&s_sum[warp][g + 8][8 * i + 2 * q]) = make_float2(acc[i][2], acc[i][3]);
-    }
-    __syncthreads();
-    const float c = p.adapter_scales ? p.adapter_scales[a] : 1.0f;
-    for (int e = threadIdx.x; e < kTile * 8 * NT; e += 32 * kDownWarps) {
-        const int r = e / (8 * NT), i = e % (8 * NT);
-        if (!((mine >> r) & 1) || i >= 8 * p.n_tiles || n0 + i >= n)
-            continue;
-        float sum = 0.0f;
+        for (int i = 0; i < NT; ++i) {
+            *reinterpret_cast<float2 *>(&s_sum[warp][g][8 * i + 2 * q]) = make_float2(acc[i][0], acc[i][1]);
+            *reinterpret_cast<float2 *>(&s_sum[warp][g + 8][8 * i + 2 * q]) = make_float2(acc[i][2], acc[i][3]);
+        }
+        __syncthreads();
+        const float c = p.adapter_scales ? p.adapter_scales[a] : 1.0f;
+        // a warp writes the rows of tokens 2 warp and 2 warp + 1
 #pragma unroll
-        for (int v = 0; v < kDownWarps; ++v)
-            sum += s_sum[v][r][i];
-        const int64_t t = t0 + r;
-        p.u[((int64_t)split * p.num_tokens + t) * n + n0 + i] = sum * c * (p.hidden_scales ? p.hidden_scales[t] : 1.0f);
+        for (int h = 0; h < 2; ++h) {
+            const int r = 2 * warp + h, t = __shfl_sync(0xffffffffu, token, r);
+            if (t < 0)
+                continue;
+            const float scale = c * (p.hidden_scales ? p.hidden_scales[t] : 1.0f);
+            for (int i = lane; i < 8 * p.n_tiles && n0 + i < n; i += 32) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kDownWarps; ++v)
+                    sum += s_sum[v][r][i];
+                p.u[((int64_t)split * p.num_tokens + t) * n + n0 + i] = sum * scale;
+            }
+        }
+        __syncthreads();                 // the sums are read
     }
 }
 
@@ -187,12 +316,11 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
 // the up-projection, added to the rows
 // ---------------------------------------------------------------------------
 //
-// A warp takes a tile of 16 tokens and `chunk` columns, 32 at a time (a slice ends at a multiple
-// of 64).  Column 8 (n / 2) + 2 i + n % 2 of the 32 is column n of the MMA's i-th tile, so that a
-// lane's four accumulators of a row are 8 neighbouring columns: 16-byte loads and stores of the
-// rows, which the accumulators begin with.  u is summed over the pieces of K, in their order, and
-// split into two bf16 parts: one would put an error of 2^-9 of the adapter's share on every
-// output.
+// Columns are taken 32 at a time (a slice ends at a multiple of 64).  Column 8 (n / 2) + 2 i +
+// n % 2 of the 32 is column n of the MMA's i-th tile, so that a lane's four accumulators of a row
+// are 8 neighbouring columns: 16-byte loads and stores of the rows, which the accumulators begin
+// with.  u is summed over the pieces of K, in their order, and split into two bf16 parts: one
+// would put an error of 2^-9 of the adapter's share on every output.
 //   RC      ceil(rank / 16), rounded up to a power of two
 //   EXACT   the rank is 16 RC: offsets into up are constants, and no lane is beyond it
 
@@ -201,14 +329,14 @@ template <int RC, bool EXACT>
 struct UpTile {
     int rank, n, g, q;
     bool live[2];                    // rows g and g + 8 are read and written
-    int id[2];
     const uint16_t *src[2];
     uint16_t *dst[2];
     const float *u[2];               // nullptr: no adapter
     uint32_t hi[RC][4], lo[RC][4];
     int slice, slice_end;
 
-    __device__ __forceinline__ void init(const AdapterParams &p, const Tile &tile, int64_t t0)
+    // `token`: of slot lane % 16, -1 without one
+    __device__ __forceinline__ void init(const AdapterParams &p, int token, bool adapter)
     {
         rank = EXACT ? 16 * RC : p.rank;
         n = p.num_slices * rank;
@@ -218,16 +346,15 @@ struct UpTile {
         slice_end = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t t = t0 + g + 8 * h;
-            id[h] = __shfl_sync(0xffffffffu, tile.id, g + 8 * h);
-            live[h] = t < p.num_tokens && (p.out != p.rows || id[h] >= 0);
+            const int64_t t = __shfl_sync(0xffffffffu, token, g + 8 * h);
+            live[h] = t >= 0;
             src[h] = p.rows + t * p.rows_stride + 8 * q;
             dst[h] = p.out + t * p.out_stride + 8 * q;
-            u[h] = id[h] >= 0 ? p.u + t * n : nullptr;
+            u[h] = live[h] && adapter ? p.u + t * n : nullptr;
         }
     }
     // the parts of u for the slice of column c, when that is another one
-    __device__ __forceinline__ void slice_of(const AdapterParams &p, int c)
+    __device__ __forceinline__ void slice_of(const AdapterParams &p, int c, int splits)
     {
         if (c < slice_end)
             return;
@@ -242,7 +369,7 @@ struct UpTile {
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (u[h] && (EXACT || 16 * k + 4 * q < rank)) {
                     const float *part = u[h] + slice * rank + 16 * k + 4 * q;
-                    for (int s = 0; s < p.splits; ++s) {
+                    for (int s = 0; s < splits; ++s) {
                         const float4 x = *reinterpret_cast<const float4 *>(part + (int64_t)s * p.num_tokens * n);
                         v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
                     }
@@ -266,128 +393,78 @@ struct UpTile {
     }
 };
 
-// What the down-projection has written may be read from here on.  The rows, the adapters and the
-// ids may be read before: the down-projection's CTAs let this kernel start after they have waited
-// for the kernels ahead.
-__device__ __forceinline__ void wait_for_u()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" :::);
-}
-
-// Columns [c, end) of any tile: for each distinct adapter its rows of up, AU adapters' at once.
-// `waited`: wait_for_u has been called; otherwise this does, once its first loads are under way.
+// A warp takes a tile and 32 * PC columns, whose rows of up and of the tokens are loaded at once
+// before it waits for u.
 template <int RC, bool EXACT>
-__device__ __forceinline__ void up_any(const AdapterParams &p, UpTile<RC, EXACT> &t, const Tile &tile, int c, int end,
-                                       bool waited)
+__global__ void __launch_bounds__(128, RC <= 2 ? 4 : 2) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
-    constexpr int AU = RC > 2 ? 1 : 4 / RC;
-    const int up_row = 8 * (t.g >> 1) + (t.g & 1);
-    if (!tile.leaders) {                             // a copy
-        if (!waited)
-            wait_for_u();
-        for (; c < end; c += 128) {
-            uint4 r[4][2];
+    constexpr int PC = RC == 1 ? 4 : RC == 2 ? 2 : 1;
+    Tiles tiles;
+    tiles.load(p);
+    const int count = p.out != p.rows ? tiles.all : tiles.with_adapter;
+    const int chunks = (p.width + 32 * PC - 1) / (32 * PC);
+    const int64_t work = (int64_t)count * chunks;
+    bool waited = false;
+    for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); item < work; item += (int64_t)gridDim.x * 4) {
+        const int c0 = (int)(item % chunks) * (32 * PC), end = min(p.width, c0 + 32 * PC);
+        int a, token;
+        tiles.get(p, (int)(item / chunks), a, token);
+        UpTile<RC, EXACT> t;
+        t.init(p, token, a >= 0);
+        const int up_row = 8 * (t.g >> 1) + (t.g & 1);
+        uint32_t in[PC][2][4];
+        uint2 w[PC][4][RC];
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < PC; ++b) {
+            const int c = c0 + 32 * b;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (t.live[h] && c + 32 * b + 8 * t.q < end)
-                        r[b][h] = *reinterpret_cast<const uint4 *>(t.src[h] + c + 32 * b);
+            for (int h = 0; h < 2; ++h)
+                if (t.live[h] && c + 8 * t.q < end) {
+                    const uint4 r = *reinterpret_cast<const uint4 *>(t.src[h] + c);
+                    in[b][h][0] = r.x, in[b][h][1] = r.y, in[b][h][2] = r.z, in[b][h][3] = r.w;
+                }
+            const uint16_t *up = p.up + ((int64_t)a * p.width + c + up_row) * t.rank + 4 * t.q;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (t.live[h] && c + 32 * b + 8 * t.q < end)
-                        *reinterpret_cast<uint4 *>(t.dst[h] + c + 32 * b) = r[b][h];
+                for (int k = 0; k < RC; ++k) {
+                    w[b][i][k] = make_uint2(0, 0);
+                    if (a >= 0 && c + up_row + 2 * i < end && (EXACT || 16 * k + 4 * t.q < t.rank))
+                        w[b][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * t.rank + 16 * k));
+                }
         }
-        return;
-    }
-    for (; c < end; c += 32) {
-        uint32_t in[2][4] = {}, out[2][4];
+        if (!waited)
+            wait_for_kernels_ahead();
+        waited = true;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (t.live[h] && c + 8 * t.q < end) {
-                const uint4 r = *reinterpret_cast<const uint4 *>(t.src[h] + c);
-                in[h][0] = r.x, in[h][1] = r.y, in[h][2] = r.z, in[h][3] = r.w;
-            }
-        uint32_t left = tile.leaders;
-        int ad[AU];
-        uint2 w[AU][4][RC];
-        auto load = [&]() {                          // the next AU adapters
-#pragma unroll
-            for (int j = 0; j < AU; ++j) {
-                const int leader = left ? __ffs(left) - 1 : 0;
-                ad[j] = left ? __shfl_sync(0xffffffffu, tile.id, leader) : -2;
-                left &= left - 1;
-                const uint16_t *up = p.up + ((int64_t)ad[j] * p.width + c + up_row) * t.rank + 4 * t.q;
+        for (int b = 0; b < PC; ++b) {
+            const int c = c0 + 32 * b;
+            if (c >= end)
+                break;
+            if (a >= 0) {
+                t.slice_of(p, c, tiles.splits);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int k = 0; k < RC; ++k) {
-                        w[j][i][k] = make_uint2(0, 0);
-                        if (ad[j] >= 0 && c + up_row + 2 * i < end && (EXACT || 16 * k + 4 * t.q < t.rank))
-                            w[j][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * t.rank + 16 * k));
-                    }
+                    t.add(in[b][0][i], in[b][1][i], w[b][i], in[b][0][i], in[b][1][i]);
             }
-        };
-        load();
-        if (!waited) {
-            wait_for_u();
-            waited = true;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (t.live[h] && c + 8 * t.q < end)
+                    *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(in[b][h][0], in[b][h][1], in[b][h][2], in[b][h][3]);
         }
-        t.slice_of(p, c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            out[0][i] = in[0][i], out[1][i] = in[1][i];
-        for (;;) {
-#pragma unroll
-            for (int j = 0; j < AU; ++j)
-                if (ad[j] >= 0)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t o0, o1;
-                        t.add(in[0][i], in[1][i], w[j][i], o0, o1);
-                        if (t.id[0] == ad[j])
-                            out[0][i] = o0;
-                        if (t.id[1] == ad[j])
-                            out[1][i] = o1;
-                    }
-            if (!left)
-                break;
-            load();
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (t.live[h] && c + 8 * t.q < end)
-                *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
     }
+    if (!waited)                         // no CTA finishes before its wait
+        wait_for_kernels_ahead();
 }
 
-template <int RC, bool EXACT>
-__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
-{
-    const int64_t tiles = (p.num_tokens + kTile - 1) / kTile;
-    const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t t0 = item % tiles * kTile, from = item / tiles * p.chunk;
-    const Tile tile = tile_of(p, from < p.width ? t0 : p.num_tokens);
-    if (from >= p.width || (p.out == p.rows && !tile.leaders)) {     // nothing to do; no CTA finishes before its wait
-        wait_for_u();
-        return;
-    }
-    UpTile<RC, EXACT> t;
-    t.init(p, tile, t0);
-    up_any(p, t, tile, (int)from, (int)min((int64_t)p.width, from + p.chunk), false);
-}
-
-// The same for many tiles, whose rows are what costs (8,192 of 11,392 are 373 MB, 56 us at the
-// copy rate).  A CTA takes eight tiles (128 tokens) and `chunk` columns.  Where they share one
-// adapter -- all but the borders of a prefill's chunks -- its rows of up and the tokens' rows go
-// through shared memory, kUpStage columns ahead of those that are computed: a lane copies the
-// pieces of rows that it uses, 8 KB a warp, 128 KB an SM in flight (with two blocks of 32 columns
-// in registers, 32 KB an SM, 80 us and not 70).  The 32-byte pieces of a row of up are placed so that the rows
-// 0, 1, 8 and 9 (16, 17, 24 and 25), of which a half warp loads a piece each, lie on different
-// banks: the two rows 2 apart go elsewhere (ranks up to 16), or the piece's number is changed.
+// The same for tiles of 128 tokens, whose rows are what costs (8,192 of 11,392 are 373 MB, 56 us
+// at the copy rate).  A CTA takes a tile and `chunk` columns, a warp 16 of its tokens.  The
+// adapter's rows of up and the tokens' rows go through shared memory, kUpStage columns ahead of
+// those that are computed: a lane copies the pieces of rows that it uses, 8 KB a warp, 128 KB an
+// SM in flight (with two blocks of 32 columns in registers, 32 KB an SM, 80 us and not 70).  The
+// 32-byte pieces of a row of up are placed so that the rows 0, 1, 8 and 9 (16, 17, 24 and 25), of
+// which a half warp loads a piece each, lie on different banks: the two rows 2 apart go elsewhere
+// (ranks up to 16), or the piece's number is changed.
 constexpr int kUpStage = 128;        // columns of a stage of up
 
 template <int RC>
@@ -411,99 +488,98 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
 {
     extern __shared__ __align__(128) uint8_t s_up[];                 // two stages of up, two of each warp's rows
     constexpr uint32_t kStageBytes = 32u * RC * kUpStage, kRowBytes = 16u * 32u * 2u * (kUpStage / 32);
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int64_t groups = (p.num_tokens + 8 * kTile - 1) / (8 * kTile);
-    const int64_t t0 = blockIdx.x % groups * (8 * kTile) + warp * kTile;
-    const int from = (int)(blockIdx.x / groups) * p.chunk, end = min(p.width, from + p.chunk);
-    Tile tile = tile_of(p, t0);
-    const int first = __ldg(p.ids + blockIdx.x % groups * (8 * kTile));
-    // (tokens behind the last one go with any)
-    const bool mine = __all_sync(0xffffffffu, tile.id == first || t0 + (tid & 15) >= p.num_tokens);
-    if (!__syncthreads_and(mine && first >= 0 && first < p.num_adapters)) {
-        if (t0 < p.num_tokens && (p.out != p.rows || tile.leaders)) {
-            UpTile<RC, EXACT> t;
-            t.init(p, tile, t0);
-            up_any(p, t, tile, from, end, false);
-        } else {
-            wait_for_u();
-        }
-        return;
-    }
-    UpTile<RC, EXACT> t;
-    t.init(p, tile, t0);
+    const int tid = threadIdx.x, warp = tid >> 5, splits = p.head->splits;
+    const int count = p.out != p.rows ? p.head->tiles : p.head->with_adapter;
+    const int chunks = (p.width + p.chunk - 1) / p.chunk;
+    const int64_t work = (int64_t)count * chunks;
     const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(s_up);
     const uint32_t s_rows = s0 + 2u * kStageBytes + (uint32_t)warp * (2u * kRowBytes) + 16u * (uint32_t)(tid & 31);
-    // 16 bytes, zeros where there is nothing
-    auto copy16 = [](uint32_t to, const uint16_t *from, bool there) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
-    };
-    auto stage = [&](int c, uint32_t buf) {
+    bool waited = false;
+    for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
+        const int tile = (int)(item % count), from = (int)(item / count) * p.chunk, end = min(p.width, from + p.chunk);
+        const int a = p.adapters[tile];
+        UpTile<RC, EXACT> t;
+        t.init(p, p.tokens[tile * 128 + warp * kTile + (tid & 15)], a >= 0);
+        // 16 bytes, zeros where there is nothing
+        auto copy16 = [](uint32_t to, const uint16_t *from, bool there) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+        };
+        auto stage = [&](int c, uint32_t buf) {
 #pragma unroll
-        for (int b = 0; b < kUpStage / 32; ++b)
+            for (int b = 0; b < kUpStage / 32; ++b)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool there = t.live[h] && c + 32 * b + 8 * t.q < end;
-                copy16(s_rows + buf * kRowBytes + (uint32_t)(2 * b + h) * 512u, there ? t.src[h] + c + 32 * b : p.rows, there);
+                for (int h = 0; h < 2; ++h) {
+                    const bool there = t.live[h] && c + 32 * b + 8 * t.q < end;
+                    copy16(s_rows + buf * kRowBytes + (uint32_t)(2 * b + h) * 512u, there ? t.src[h] + c + 32 * b : p.rows, there);
+                }
+            // halves of pieces of up
+            if (a >= 0) {
+                const uint16_t *up = p.up + ((int64_t)a * p.width + c) * t.rank;
+#pragma unroll
+                for (int e0 = 0; e0 < kUpStage * 2 * RC; e0 += 256) {
+                    const int e = e0 + tid, row = e / (2 * RC), h = e % (2 * RC);
+                    const bool there = c + row < end && (EXACT || 8 * h < t.rank);
+                    copy16(s0 + buf * kStageBytes + up_piece<RC>(row, h >> 1) + 16u * (h & 1),
+                           there ? up + row * t.rank + 8 * h : p.up, there);
+                }
             }
-        // halves of pieces of up
-        const uint16_t *up = p.up + ((int64_t)first * p.width + c) * t.rank;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        stage(from, 0);
+        if (from + kUpStage < end)
+            stage(from + kUpStage, 1);
+        if (!waited)
+            wait_for_kernels_ahead();
+        waited = true;
+        const int up_row = 8 * (t.g >> 1) + (t.g & 1);
+        uint32_t at[RC];                 // of this lane's piece k of row up_row
 #pragma unroll
-        for (int e0 = 0; e0 < kUpStage * 2 * RC; e0 += 256) {
-            const int e = e0 + tid, row = e / (2 * RC), h = e % (2 * RC);
-            const bool there = c + row < end && (EXACT || 8 * h < t.rank);
-            copy16(s0 + buf * kStageBytes + up_piece<RC>(row, h >> 1) + 16u * (h & 1), there ? up + row * t.rank + 8 * h : p.up,
-                   there);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    stage(from, 0);
-    if (from + kUpStage < end)
-        stage(from + kUpStage, 1);
-    wait_for_u();
-    const int up_row = 8 * (t.g >> 1) + (t.g & 1);
-    uint32_t at[RC];                 // of this lane's piece k of row up_row
-#pragma unroll
-    for (int k = 0; k < RC; ++k)
-        at[k] = s0 + up_piece<RC>(up_row, k) + 8u * t.q;
-    for (int c0 = from, it = 0; c0 < end; c0 += kUpStage, ++it) {
-        if (c0 + kUpStage < end)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
-        const uint32_t buf = (uint32_t)(it & 1);
+        for (int k = 0; k < RC; ++k)
+            at[k] = s0 + up_piece<RC>(up_row, k) + 8u * t.q;
+        for (int c0 = from, it = 0; c0 < end; c0 += kUpStage, ++it) {
+            if (c0 + kUpStage < end)
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+            const uint32_t buf = (uint32_t)(it & 1);
 #pragma unroll 2
-        for (int b = 0; b < kUpStage / 32; ++b) {
-            const int c = c0 + 32 * b;
-            if (c >= end)
-                break;
-            t.slice_of(p, c);
-            uint32_t in[2][4], out[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(in[h][0]), "=r"(in[h][1]), "=r"(in[h][2]), "=r"(in[h][3])
-                             : "r"(s_rows + buf * kRowBytes + (uint32_t)(2 * b + h) * 512u));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint2 w[RC];
-#pragma unroll
-                for (int k = 0; k < RC; ++k)
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                 : "=r"(w[k].x), "=r"(w[k].y)
-                                 : "r"(at[k] + buf * kStageBytes + (uint32_t)b * (1024u * RC) + up_step<RC>(i)));
-                t.add(in[0][i], in[1][i], w, out[0][i], out[1][i]);
-            }
-            if (c + 8 * t.q < end)
+            for (int b = 0; b < kUpStage / 32; ++b) {
+                const int c = c0 + 32 * b;
+                if (c >= end)
+                    break;
+                uint32_t r[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (t.live[h])
-                        *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3])
+                                 : "r"(s_rows + buf * kRowBytes + (uint32_t)(2 * b + h) * 512u));
+                if (a >= 0) {
+                    t.slice_of(p, c, splits);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint2 w[RC];
+#pragma unroll
+                        for (int k = 0; k < RC; ++k)
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                         : "=r"(w[k].x), "=r"(w[k].y)
+                                         : "r"(at[k] + buf * kStageBytes + (uint32_t)b * (1024u * RC) + up_step<RC>(i)));
+                        t.add(r[0][i], r[1][i], w, r[0][i], r[1][i]);
+                    }
+                }
+                if (c + 8 * t.q < end)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (t.live[h])
+                            *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(r[h][0], r[h][1], r[h][2], r[h][3]);
+            }
+            __syncthreads();
+            if (c0 + 2 * kUpStage < end)
+                stage(c0 + 2 * kUpStage, buf);
         }
-        __syncthreads();
-        if (c0 + 2 * kUpStage < end)
-            stage(c0 + 2 * kUpStage, buf);
     }
+    if (!waited)
+        wait_for_kernels_ahead();
 }
 
 // ---------------------------------------------------------------------------
@@ -537,6 +613,8 @@ msa_status check_cfg(const msa_adapter_cfg *cfg, int64_t T)
         return fail(MSA_ERR_UNSUPPORTED, "rank %d (multiples of 8, at most 128)", cfg->rank);
     if (cfg->num_adapters < 1)
         return fail(MSA_ERR_INVALID_ARGUMENT, "num_adapters %d", cfg->num_adapters);
+    if (cfg->num_adapters > kMaxAdapters)
+        return fail(MSA_ERR_UNSUPPORTED, "num_adapters %d (at most %d)", cfg->num_adapters, kMaxAdapters);
     if (cfg->hidden_dtype != MSA_DTYPE_BF16 && cfg->hidden_dtype != MSA_DTYPE_FP8_E4M3)
         return fail(MSA_ERR_UNSUPPORTED, "hidden_dtype %d", cfg->hidden_dtype);
     if (cfg->num_slices < 1 || cfg->num_slices > MSA_ADAPTER_MAX_SLICES)
@@ -562,45 +640,45 @@ msa_status check_cfg(const msa_adapter_cfg *cfg, int64_t T)
 
 int width_of(const msa_adapter_cfg *cfg) { return cfg->slice_end[cfg->num_slices - 1]; }
 
-// How the down-projection's work is cut.
-struct Cut {
+// How a call's work is cut, and what its workspace holds.
+struct Plan {
     bool wide;               // tiles of 128 tokens (msa_adapter_tile.cu); else of 16
+    bool sorted;             // more than one tile of tokens
     int n_blocks, n_tiles;   // tiles of 16: blocks of at most 64 rows of down, tiles of 8 rows in each
-    int splits;              // pieces of K
+    int max_splits;          // pieces of K
+    int64_t tiles;           // at most
+    int64_t adapters, tokens, u, bytes;      // offsets into the workspace
 };
 
-Cut cut_of(const msa_adapter_cfg *cfg, int64_t T)
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
 {
-    Cut c;
-    const int tiles = cfg->num_slices * cfg->rank / 8;
-    c.n_blocks = (tiles + 7) / 8;
-    c.n_tiles = (tiles + c.n_blocks - 1) / c.n_blocks;
-    const int64_t units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
-    c.wide = T >= kWideTokens;
-    int64_t most, want;
-    if (c.wide) {
-        // two CTAs on an SM, at least four units of K in each piece
-        const int64_t ctas = (T + 127) / 128;
-        most = units / 4 < kAdapterWideSplits ? units / 4 : kAdapterWideSplits;
-        want = 2 * 152 / ctas;
-    } else {
-        // so many pieces that a batch whose tokens all have adapters of their own fills the GPU once
-        // (two CTAs an SM; 64 tokens over 48 adapters in 1.2 rounds 25.1 us, in one 23), and no fewer
-        // than a unit of K for each warp
-        const int64_t ctas = (T > 0 ? T : 1) * c.n_blocks;
-        most = (units + kDownWarps - 1) / kDownWarps;
-        want = 2 * 152 / ctas;
-    }
-    c.splits = (int)(want < most ? want : most);
-    if (c.splits < 1)
-        c.splits = 1;
+    Plan c;
+    const int64_t rows = (int64_t)cfg->num_slices * cfg->rank, units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
+    // 512 tokens of three adapters of rank 16, 11,392 wide: 19.6 us in wide tiles, 23.6 in narrow
+    // ones; of rank 8 and a hidden size of 1,000, 12.9 and 9.8.
+    c.wide = T >= 192 && rows * cfg->hidden_size >= 65536;
+    c.sorted = T > kTile;
+    const int ts = c.wide ? 128 : kTile;
+    c.tiles = T / ts + (T < cfg->num_adapters + 1 ? T : cfg->num_adapters + 1);
+    c.n_blocks = c.wide ? 1 : (int)((rows / 8 + 7) / 8);
+    c.n_tiles = (int)((rows / 8 + c.n_blocks - 1) / c.n_blocks);
+    // no fewer than a unit of K for each warp of 8, four for a wide tile; and what the fewest tiles
+    // that T tokens can make would take to fill the GPU
+    const int64_t most = c.wide ? (units / 4 < 4 ? units / 4 : 4) : (units + kDownWarps - 1) / kDownWarps;
+    const int64_t want = kFill / (((T + ts - 1) / ts > 0 ? (T + ts - 1) / ts : 1) * c.n_blocks);
+    c.max_splits = (int)(want < most ? want : most);
+    if (c.max_splits < 1)
+        c.max_splits = 1;
+    c.adapters = c.sorted ? 256 : 0;
+    c.tokens = c.adapters + (c.sorted ? align256(c.tiles * 4) : 0);
+    c.u = c.tokens + (c.sorted ? align256(c.tiles * ts * 4) : 0);
+    c.bytes = T == 0 ? 0 : c.u + c.max_splits * T * rows * 4;
     return c;
 }
 
-int64_t workspace_needed(const msa_adapter_cfg *cfg, int64_t T)
-{
-    return cut_of(cfg, T).splits * T * cfg->num_slices * cfg->rank * 4;
-}
+int64_t workspace_needed(const msa_adapter_cfg *cfg, int64_t T) { return plan_of(cfg, T).bytes; }
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -638,6 +716,8 @@ msa_status check_args(const msa_adapter_cfg *cfg, int64_t T, const AdapterParams
     if (!fits(T, p.hidden_stride, 2) || !fits(T, p.rows_stride, 2) || !fits(T, p.out_stride, 2) ||
         !fits((int64_t)cfg->num_adapters * cfg->num_slices * cfg->rank, p.down_stride, 2))
         return fail(MSA_ERR_OFFSET_OVERFLOW, "an extent overflows int64");
+    if (p.down_stride >= (int64_t)1 << 39)           // TMA's limit is 2^40 bytes
+        return fail(MSA_ERR_UNSUPPORTED, "down_stride %lld (below 2^39)", (long long)p.down_stride);
     if (!workspace || workspace_bytes < workspace_needed(cfg, T))
         return fail(MSA_ERR_INVALID_ARGUMENT, "workspace: %lld bytes, %lld needed",
                     (long long)(workspace ? workspace_bytes : 0), (long long)workspace_needed(cfg, T));
@@ -698,7 +778,6 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     p.adapter_scales = adapter_scales;
     p.rows = static_cast<const uint16_t *>(rows);
     p.out = static_cast<uint16_t *>(out);
-    p.u = static_cast<float *>(workspace);
     p.hidden_stride = hidden_stride;
     p.down_stride = down_stride;
     p.rows_stride = rows_stride;
@@ -714,56 +793,69 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     p.num_slices = cfg->num_slices;
     p.fp8 = cfg->hidden_dtype == MSA_DTYPE_FP8_E4M3;
     memcpy(p.slice_end, cfg->slice_end, sizeof p.slice_end);
-    const Cut c = cut_of(cfg, num_tokens);
-    p.splits = c.splits;
+    const Plan c = plan_of(cfg, num_tokens);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.head = reinterpret_cast<AdapterHead *>(ws);
+    p.adapters = reinterpret_cast<int32_t *>(ws + c.adapters);
+    p.tokens = c.sorted ? reinterpret_cast<int32_t *>(ws + c.tokens) : nullptr;
+    p.u = reinterpret_cast<float *>(ws + c.u);
+    p.tile_tokens = c.wide ? 128 : kTile;
+    p.max_splits = c.max_splits;
     p.n_blocks = c.n_blocks;
     p.n_tiles = c.n_tiles;
     using Kernel = void (*)(AdapterParams);
-    static const Kernel downs[2][4] = {
-        {msa_adapter_down_kernel<false, 2>, msa_adapter_down_kernel<false, 4>, msa_adapter_down_kernel<false, 6>,
-         msa_adapter_down_kernel<false, 8>},
-        {msa_adapter_down_kernel<true, 2>, msa_adapter_down_kernel<true, 4>, msa_adapter_down_kernel<true, 6>,
-         msa_adapter_down_kernel<true, 8>}};
-    const int64_t tiles = (num_tokens + kTile - 1) / kTile;
-    cudaError_t e = cudaSuccess;
-    if (!c.wide || !adapter_down_tiles(p, stream, &e)) {
-        const dim3 grid((unsigned)tiles, (unsigned)(num_tokens < kTile ? num_tokens : kTile),
-                        (unsigned)(c.n_blocks * c.splits));
-        const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], grid, 32 * kDownWarps, 0,
-                                    stream, p);
+    auto allow = [](Kernel k, int smem) {
+        return cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    };
+    if (c.sorted) {
+        const int smem = (p.num_adapters + 1) * 4;
+        if (smem > 48 * 1024 && allow(msa_adapter_sort_kernel, smem) != cudaSuccess)
+            return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed");
+        const msa_status d = launch(msa_adapter_sort_kernel, dim3(1), 1024, smem, stream, p);
         if (d != MSA_OK)
             return d;
     }
-    if (e != cudaSuccess)
-        return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+    if (c.wide) {
+        const cudaError_t e = adapter_down_tiles(p, c.tiles, stream);
+        if (e != cudaSuccess)
+            return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+    } else {
+        static const Kernel downs[2][4] = {
+            {msa_adapter_down_kernel<false, 2>, msa_adapter_down_kernel<false, 4>, msa_adapter_down_kernel<false, 6>,
+             msa_adapter_down_kernel<false, 8>},
+            {msa_adapter_down_kernel<true, 2>, msa_adapter_down_kernel<true, 4>, msa_adapter_down_kernel<true, 6>,
+             msa_adapter_down_kernel<true, 8>}};
+        const int64_t work = c.tiles * c.n_blocks * c.max_splits;
+        const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], dim3((unsigned)(work < kFill ? work : kFill)),
+                                    32 * kDownWarps, 0, stream, p);
+        if (d != MSA_OK)
+            return d;
+    }
 
-    const int chunks = (p.rank + 15) / 16, rc = chunks <= 1 ? 0 : chunks <= 2 ? 1 : chunks <= 4 ? 2 : 3;
+    const int k16 = (p.rank + 15) / 16, rc = k16 <= 1 ? 0 : k16 <= 2 ? 1 : k16 <= 4 ? 2 : 3;
     const bool exact = p.rank == 16 << rc;
-    // Columns of a warp: so few that the warps fill the GPU.
-    const int64_t pieces = (p.width + 31) / 32;
-    if (tiles * pieces <= 16 * 152) {
+    if (!c.wide) {
         static const Kernel ups[2][4] = {{msa_adapter_up_kernel<1, false>, msa_adapter_up_kernel<2, false>,
                                           msa_adapter_up_kernel<4, false>, msa_adapter_up_kernel<8, false>},
                                          {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>,
                                           msa_adapter_up_kernel<4, true>, msa_adapter_up_kernel<8, true>}};
-        p.chunk = 32;
-        const int64_t items = tiles * pieces;
-        const int warps = items < 2 * 152 ? 1 : 4;
-        return launch(ups[exact][rc], dim3((unsigned)((items + warps - 1) / warps)), 32 * warps, 0, stream, p);
+        const int columns = rc == 0 ? 128 : rc == 1 ? 64 : 32;
+        const int64_t ctas = (c.tiles * ((p.width + columns - 1) / columns) + 3) / 4;
+        return launch(ups[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 128, 0, stream, p);
     }
     static const Kernel ups[2][4] = {{msa_adapter_up_stream_kernel<1, false>, msa_adapter_up_stream_kernel<2, false>,
                                       msa_adapter_up_stream_kernel<4, false>, msa_adapter_up_stream_kernel<8, false>},
                                      {msa_adapter_up_stream_kernel<1, true>, msa_adapter_up_stream_kernel<2, true>,
                                       msa_adapter_up_stream_kernel<4, true>, msa_adapter_up_stream_kernel<8, true>}};
     const int smem = 2 * (32 << rc) * kUpStage + 8 * 2 * (16 * 32 * 2 * (kUpStage / 32));
-    const int64_t groups = (tiles + 7) / 8;
+    const int64_t groups = (num_tokens + 127) / 128;
     p.chunk = kUpStage;
     while (p.chunk < 1024 && groups * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152)
         p.chunk *= 2;
-    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(ups[exact][rc]), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
-    return launch(ups[exact][rc], dim3((unsigned)(groups * ((p.width + p.chunk - 1) / p.chunk))), 256, smem, stream, p);
+    const int64_t ctas = c.tiles * ((p.width + p.chunk - 1) / p.chunk);
+    if (allow(ups[exact][rc], smem) != cudaSuccess)
+        return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed");
+    return launch(ups[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 256, smem, stream, p);
 }
 
 }  // extern "C"

@@ -8,7 +8,12 @@
 
 #include <cstdint>
 
-constexpr int kAdapterWideSplits = 4;    // pieces of K at most where tiles are of 128 tokens
+// What the sort says of a call's tiles of tokens.
+struct AdapterHead {
+    int32_t with_adapter;    // tiles of tokens of one adapter
+    int32_t tiles;           // and, behind them, those of tokens without one
+    int32_t splits;          // pieces of K of the down-projection
+};
 
 struct AdapterParams {
     const uint8_t *hidden;
@@ -18,19 +23,22 @@ struct AdapterParams {
     const float *adapter_scales;
     const uint16_t *rows;
     uint16_t *out;
+    AdapterHead *head;
+    int32_t *adapters;               // of each tile, -1: none
+    int32_t *tokens;                 // [tiles, tile_tokens], -1: none; nullptr: at most 16 tokens, not sorted
     float *u;                        // [splits, T, S * r]: sums over pieces of K
     int64_t hidden_stride, down_stride, rows_stride, out_stride;   // elements
     int64_t num_tokens;
     int32_t hidden_size, width, rank, num_adapters, num_slices, fp8;
-    int32_t splits;                  // pieces of K
+    int32_t tile_tokens;             // 16 or 128
+    int32_t max_splits;              // pieces of K at most
     int32_t n_blocks, n_tiles;       // blocks of down rows, tiles of 8 rows in a block
-    int32_t chunk;                   // columns of a warp's share of the up-projection
+    int32_t chunk;                   // columns of a CTA's share of the up-projection
     int32_t slice_end[MSA_ADAPTER_MAX_SLICES];
 };
 
-// The down-projection in tiles of 128 tokens (msa_adapter_tile.cu) into p.u, pieces of K as
-// p.splits says; false when TMA does not take the layout (nothing is enqueued then).
-bool adapter_down_tiles(const AdapterParams &p, cudaStream_t stream, cudaError_t *error);
+// The down-projection of tiles of 128 tokens (msa_adapter_tile.cu) into p.u; at most `tiles`.
+cudaError_t adapter_down_tiles(const AdapterParams &p, int64_t tiles, cudaStream_t stream);
 
 #ifdef __CUDACC__
 namespace {

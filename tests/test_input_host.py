@@ -124,6 +124,7 @@ def adapter(**over):
     (dict(workspace=at(8) + 16), MISALIGNED),
     (dict(rows_stride=2**62), OVERFLOW),
     (dict(down_stride=2**62), OVERFLOW),
+    (dict(down_stride=2**39), UNSUPPORTED),
     (dict(workspace=None), INVALID),
     (dict(workspace_bytes=16), INVALID),
     (dict(launch_flags=B.MSA_LAUNCH_QUERY_RUNS), INVALID),
@@ -135,7 +136,7 @@ def test_adapter_refuses(over, status):
 
 @pytest.mark.parametrize("name,value,status", [
     ("hidden_size", 0, INVALID), ("rank", 0, INVALID), ("rank", 12, UNSUPPORTED), ("rank", 136, UNSUPPORTED),
-    ("rank", 128, UNSUPPORTED), ("num_adapters", 0, INVALID), ("hidden_dtype", 2, UNSUPPORTED),
+    ("rank", 128, UNSUPPORTED), ("num_adapters", 0, INVALID), ("num_adapters", 16385, UNSUPPORTED), ("hidden_dtype", 2, UNSUPPORTED),
     ("num_slices", 0, INVALID), ("num_slices", 9, INVALID), ("num_slices", 4, INVALID),
     ("slice_end", (1, 8192), INVALID), ("slice_end", (0, 8200), UNSUPPORTED), ("slice_end", (4, 11390), UNSUPPORTED),
     ("slice_end", (0, 0), INVALID), ("slice_end", (7, 64), INVALID), ("reserved", (2, 1), INVALID),
@@ -149,9 +150,12 @@ def test_adapter_cfg_refuses(name, value, status):
 @pytest.mark.parametrize("rank,slices", [(8, 1), (16, 5), (64, 8), (128, 4)])
 @pytest.mark.parametrize("t", [0, 1, 63, 64, 65, 1000, 8192, 2**24])
 def test_adapter_workspace_bounds(rank, slices, t):
-    """What the header promises: less than 1 MB and at most 16 * num_slices * rank bytes a token."""
-    n = B.msa_adapter_workspace_bytes(adapter_cfg(rank=rank, slice_ends=[64 * (i + 1) for i in range(slices)]), t)
-    assert 0 <= n < 2**20 + 16 * slices * rank * t
+    """What the header promises: less than 2 MB and 512 bytes an adapter, and at most 16 * num_slices *
+    rank + 80 bytes a token."""
+    for adapters in (1, 48, 16384):
+        cfg = adapter_cfg(rank=rank, slice_ends=[64 * (i + 1) for i in range(slices)], num_adapters=adapters)
+        n = B.msa_adapter_workspace_bytes(cfg, t)
+        assert 0 <= n < 2 * 2**20 + 512 * adapters + (16 * slices * rank + 80) * t
 
 
 # ---------------------------------------------------------------------------

@@ -49,7 +49,7 @@ typedef struct {
 } msa_adapter_cfg;
 
 /* Bytes of workspace msa_adapter_forward needs for num_tokens tokens under cfg: less than
- * 2 MB and 512 bytes an adapter, and at most 16 * num_slices * rank + 80 bytes a token.
+ * 2 MB and 512 bytes an adapter, and at most 32 * num_slices * rank + 80 bytes a token.
  * Host-side; enqueues nothing. */
 msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_tokens, int64_t *bytes);
 

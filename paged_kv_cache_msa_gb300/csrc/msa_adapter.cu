@@ -28,6 +28,7 @@ constexpr int kTile = 16;            // tokens of a tile: the MMA's M
 constexpr int kDownWarps = 8;        // warps of a CTA of the down-projection, each a piece of its K
 constexpr int kUnitK = 64;           // K elements a warp takes at a time: 128 bytes of bf16
 constexpr int kFill = 2 * 152;       // CTAs that fill the GPU at two an SM
+constexpr int kSortKept = 8;         // tokens of a thread of the sort that it loads once
 constexpr int kMaxAdapters = 16384;  // the sort counts them in shared memory
 
 __device__ __forceinline__ float2 unpack2(uint32_t v)
@@ -63,24 +64,38 @@ __global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_con
     extern __shared__ int s_place[];                 // a count, then the next place, of each adapter; the last: none
     __shared__ int s_sum[32];
     wait_for_kernels_ahead();
-    const int tid = threadIdx.x, lane = tid & 31, n = p.num_adapters + 1;
+    const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x, n = p.num_adapters + 1;
     const int64_t T = p.num_tokens;
-    for (int a = tid; a < n; a += 1024)
+    // this thread's first tokens' adapters, loaded at once and kept for the second pass
+    int mine[kSortKept];
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i)
+        mine[i] = (int64_t)i * nt + tid < T ? __ldg(p.ids + (int64_t)i * nt + tid) : -1;
+    for (int a = tid; a < n; a += nt)
         s_place[a] = 0;
     __syncthreads();
-    auto adapter_of = [&](int64_t t) {
-        const int a = t < T ? __ldg(p.ids + t) : -2;
-        return t < T && (a < 0 || a >= p.num_adapters) ? n - 1 : a;
+    // f(token, adapter, n - 1 without one; -1 behind the last token), a warp's tokens at once
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < kSortKept; ++i) {
+            const int64_t t = (int64_t)i * nt + tid;
+            if (t - lane >= T)
+                break;
+            f(t, t >= T ? -1 : mine[i] < 0 || mine[i] >= p.num_adapters ? n - 1 : mine[i]);
+        }
+        for (int64_t t = (int64_t)kSortKept * nt + tid; t - lane < T; t += nt) {
+            const int a = t < T ? __ldg(p.ids + t) : -1;
+            f(t, t >= T ? -1 : a < 0 || a >= p.num_adapters ? n - 1 : a);
+        }
     };
-    for (int64_t t0 = tid - lane; t0 < T; t0 += 1024) {
-        const int a = adapter_of(t0 + lane);
+    each([&](int64_t, int a) {
         const uint32_t same = __match_any_sync(0xffffffffu, a);
         if (a >= 0 && lane == __ffs(same) - 1)
             atomicAdd(&s_place[a], __popc(same));
-    }
+    });
     __syncthreads();
     // tiles before each adapter's: a run of adapters a thread
-    const int ts = p.tile_tokens, per = (n + 1023) / 1024, a0 = min(n, tid * per), a1 = min(n, a0 + per);
+    const int ts = p.tile_tokens, per = (n + nt - 1) / nt, a0 = min(n, tid * per), a1 = min(n, a0 + per);
     int sum = 0;
     for (int a = a0; a < a1; ++a)
         sum += (s_place[a] + ts - 1) / ts;
@@ -95,7 +110,7 @@ __global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_con
         s_sum[tid >> 5] = before;
     __syncthreads();
     if (tid < 32) {
-        int x = s_sum[tid];
+        int x = tid < nt / 32 ? s_sum[tid] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -121,8 +136,7 @@ __global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_con
         tile += tiles;
     }
     __syncthreads();
-    for (int64_t t0 = tid - lane; t0 < T; t0 += 1024) {
-        const int a = adapter_of(t0 + lane);
+    each([&](int64_t t, int a) {
         const uint32_t same = __match_any_sync(0xffffffffu, a);
         const int leader = __ffs(same) - 1;
         int at = 0;
@@ -130,11 +144,11 @@ __global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_con
             at = atomicAdd(&s_place[a], __popc(same));
         at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
         if (a >= 0) {
-            p.tokens[at] = (int)(t0 + lane);
+            p.tokens[at] = (int)t;
             if (at % ts == 0)
                 p.adapters[at / ts] = a == n - 1 ? -1 : a;
         }
-    }
+    });
 }
 
 // The tiles of 16 tokens of one adapter, from the sort, or (p.tokens nullptr: at most 16 tokens)
@@ -656,9 +670,13 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
 {
     Plan c;
     const int64_t rows = (int64_t)cfg->num_slices * cfg->rank, units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
-    // 512 tokens of three adapters of rank 16, 11,392 wide: 19.6 us in wide tiles, 23.6 in narrow
-    // ones; of rank 8 and a hidden size of 1,000, 12.9 and 9.8.
-    c.wide = T >= 192 && rows * cfg->hidden_size >= 65536;
+    // Narrow tiles read the hidden states once for each block of 64 rows of down, and make E4M3 ones
+    // bf16 each time.  Sides meet (6,144 wide hidden states, 11,392 wide rows, three adapters): bf16, 80
+    // rows at 2,000 tokens (41.7 us in narrow tiles, 40.2 in wide ones; 24.8 and 30.1 at 1,024), 320 rows
+    // at 128 (31.0 and 28.9; 96.7 and 51.5 at 1,024); E4M3, 80 rows at 256 (19.2 and 17.7); bf16, 160
+    // rows of 1,000 elements at 1,200 (13.6 and 15.2 at 1,024, 19.5 and 15.7 at 1,536).
+    const int64_t blocks = (rows + 63) / 64;
+    c.wide = T > kTile && T * cfg->hidden_size >= (blocks > 2 || cfg->hidden_dtype != MSA_DTYPE_BF16 ? 1200000 : 12000000);
     c.sorted = T > kTile;
     const int ts = c.wide ? 128 : kTile;
     c.tiles = T / ts + (T < cfg->num_adapters + 1 ? T : cfg->num_adapters + 1);
@@ -666,7 +684,7 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
     c.n_tiles = (int)((rows / 8 + c.n_blocks - 1) / c.n_blocks);
     // no fewer than a unit of K for each warp of 8, four for a wide tile; and what the fewest tiles
     // that T tokens can make would take to fill the GPU
-    const int64_t most = c.wide ? (units / 4 < 4 ? units / 4 : 4) : (units + kDownWarps - 1) / kDownWarps;
+    const int64_t most = c.wide ? (units / 4 < 8 ? units / 4 : 8) : (units + kDownWarps - 1) / kDownWarps;
     const int64_t want = kFill / (((T + ts - 1) / ts > 0 ? (T + ts - 1) / ts : 1) * c.n_blocks);
     c.max_splits = (int)(want < most ? want : most);
     if (c.max_splits < 1)
@@ -811,7 +829,10 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
         const int smem = (p.num_adapters + 1) * 4;
         if (smem > 48 * 1024 && allow(msa_adapter_sort_kernel, smem) != cudaSuccess)
             return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed");
-        const msa_status d = launch(msa_adapter_sort_kernel, dim3(1), 1024, smem, stream, p);
+        // as many threads as have something to do: barriers of 1,024 take 1 us more
+        const int64_t most = num_tokens > p.num_adapters + 1 ? num_tokens : p.num_adapters + 1;
+        const int threads = most >= 1024 ? 1024 : (int)((most + 31) / 32 * 32);
+        const msa_status d = launch(msa_adapter_sort_kernel, dim3(1), threads, smem, stream, p);
         if (d != MSA_OK)
             return d;
     }

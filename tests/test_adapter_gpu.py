@@ -297,3 +297,109 @@ def test_a_chain_in_place(t):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+# Tiles of 128 tokens are taken from 1.2 million hidden values on (E4M3, or more than 128 rows of
+# down; 12 million otherwise).
+
+def wide_case(order, t=1300, k=1000, rank=64, adapters=4, **kw):
+    assert t * k >= 1200000 and rank > 24
+    return Case(order(t, adapters), k=k, rank=rank, adapters=adapters, **kw)
+
+
+@pytest.mark.parametrize("t,k", [(30001, 40), (19000, 64), (18500, 65), (6100, 200), (1300, 1000), (1201, 1001), (640, 2049),
+                                 (200, 6144), (129, 9600), (128, 9600), (127, 9600), (80, 15500)])
+@pytest.mark.parametrize("rank", [32, 40])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_wide_sizes(t, k, rank, fp8):
+    wide_case(runs if t % 2 else mixed, t, k, rank, fp8=fp8, pad=1, seed=k).run().check()
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 48, 56, 64, 72, 96])
+@pytest.mark.parametrize("order", [mixed, runs], ids=["mixed", "runs"])
+def test_wide_ranks(rank, order):
+    Case(order(1500, 3), k=1000, rank=rank, adapters=3, fp8=True).run().check()
+
+
+@pytest.mark.parametrize("ends", [(8,), (72,), (64, 128, 192, 256, 320, 384, 448, 456), (1000,), (4096, 4104)], ids=str)
+def test_wide_widths(ends):
+    Case(mixed(1500, 4), k=1000, ends=ends, rank=56 if len(ends) > 4 else 128, fp8=True, pad=2).run().check()
+
+
+def test_wide_without_scales_or_adapters():
+    wide_case(mixed, scaled=False, alpha=False).run().check()
+    for ids in (0, -1, 9):
+        Case([ids] * 1300, k=1000, rank=64, adapters=1).run().check()
+
+
+def test_wide_in_place_and_repeated():
+    c = wide_case(mixed, pad=1).run().check()
+    rows, want = c.rows.clone(), c.out.clone()
+    c.ws.fill_(0x7F)
+    c.out.zero_()
+    c.run()
+    assert torch.equal(c.out.view(torch.int16), want.view(torch.int16))
+    c.run(out=c.rows)
+    assert torch.equal(c.rows, want)
+    c.check(out=c.rows, rows=rows)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_wide_requests_values_stay_their_own(bad, fp8):
+    for what in ("down", "up", "alpha", "hidden", "hidden_scales", "rows"):
+        if fp8 and what == "hidden" and bad == float("inf"):
+            continue                                          # E4M3 has no infinity
+        c = wide_case(mixed, pad=1, fp8=fp8).run()
+        clean = c.out.clone()
+        if what in ("down", "up", "alpha"):
+            getattr(c, what)[2] = bad
+            mine = c.ids == 2
+        else:
+            getattr(c, what)[1] = torch.tensor(bad).to(getattr(c, what).dtype)
+            mine = torch.arange(c.n, device="cuda") == 1
+        c.run()
+        assert torch.equal(c.out[~mine].view(torch.int16), clean[~mine].view(torch.int16)), what
+        touched = mine & (c.ids >= 0) & (c.ids < 4) if what != "rows" else mine
+        assert not c.out[touched].isfinite().any(), what
+
+
+def test_wide_chain_and_graph():
+    """Calls in place one after another, other requests' adapters between them, eager and replayed."""
+    c = wide_case(mixed)
+    start = c.rows.clone()
+    orders = [torch.tensor(o, dtype=torch.int32, device="cuda") for o in (mixed(1300, 4), runs(1300, 4), [-1] * 1300, [2] * 1300)]
+
+    def steps(between):
+        c.rows.copy_(start)
+        for o in orders * 2:
+            c.ids.copy_(o)
+            between and torch.cuda.synchronize()
+            c.run(out=c.rows)
+            between and torch.cuda.synchronize()
+        return c.rows.clone()
+
+    want = steps(True)
+    assert torch.equal(steps(False).view(torch.int16), want.view(torch.int16))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = steps(False)
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("t", [17, 500, 3000])
+def test_thousands_of_adapters(t):
+    """Most of them unused; every token another one."""
+    gen = torch.Generator().manual_seed(t)
+    ids = torch.randint(-20, 16384 + 20, (t,), generator=gen).tolist()
+    Case(ids, k=64, ends=(64,), rank=8, adapters=16384).run().check()
+    Case([(i * 7) % 4099 for i in range(t)], k=512, ends=(64,), rank=32, adapters=4099, fp8=True).run().check()
+
+
+def test_more_tokens_than_the_sort_keeps():
+    """Tokens beyond those that the sorting threads hold in registers."""
+    Case(mixed(20000, 5), k=24, ends=(64, 72), rank=8, adapters=5).run().check()
+    wide_case(mixed, 40001, 32, adapters=3, ends=(128,)).run().check()

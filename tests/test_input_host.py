@@ -150,12 +150,12 @@ def test_adapter_cfg_refuses(name, value, status):
 @pytest.mark.parametrize("rank,slices", [(8, 1), (16, 5), (64, 8), (128, 4)])
 @pytest.mark.parametrize("t", [0, 1, 63, 64, 65, 1000, 8192, 2**24])
 def test_adapter_workspace_bounds(rank, slices, t):
-    """What the header promises: less than 2 MB and 512 bytes an adapter, and at most 16 * num_slices *
+    """What the header promises: less than 2 MB and 512 bytes an adapter, and at most 32 * num_slices *
     rank + 80 bytes a token."""
     for adapters in (1, 48, 16384):
         cfg = adapter_cfg(rank=rank, slice_ends=[64 * (i + 1) for i in range(slices)], num_adapters=adapters)
         n = B.msa_adapter_workspace_bytes(cfg, t)
-        assert 0 <= n < 2 * 2**20 + 512 * adapters + (16 * slices * rank + 80) * t
+        assert 0 <= n < 2 * 2**20 + 512 * adapters + (32 * slices * rank + 80) * t
 
 
 # ---------------------------------------------------------------------------

@@ -27,6 +27,7 @@ namespace {
 constexpr int kTile = 16;            // tokens of a tile: the MMA's M
 constexpr int kDownWarps = 8;        // warps of a CTA of the down-projection, each a piece of its K
 constexpr int kUnitK = 64;           // K elements a warp takes at a time: 128 bytes of bf16
+constexpr int kUpWarps = 16 * 152;   // warps that fill the GPU in the up-projection
 constexpr int kFill = 2 * 152;       // CTAs that fill the GPU at two an SM
 constexpr int kSortKept = 8;         // tokens of a thread of the sort that it loads once
 constexpr int kMaxAdapters = 16384;  // the sort counts them in shared memory
@@ -200,11 +201,12 @@ struct Tiles {
     }
 };
 
-// 8 elements of a row from k on as bf16 pairs, zeros from K on; k is a multiple of 8.
-template <bool FP8>
+// 8 elements of a row from k on as bf16 pairs, zeros from K on; k is a multiple of 8.  WHOLE: all
+// of them are there.
+template <bool FP8, bool WHOLE>
 __device__ __forceinline__ uint4 load_hidden(const AdapterParams &p, int64_t row, int k)
 {
-    const int n = p.hidden_size - k;
+    const int n = WHOLE ? 8 : p.hidden_size - k;
     if (n <= 0)
         return make_uint4(0, 0, 0, 0);
     if (FP8) {
@@ -246,12 +248,12 @@ __device__ __forceinline__ uint4 load_down(const AdapterParams &p, const uint16_
 // the down-projection of tiles of 16 tokens
 // ---------------------------------------------------------------------------
 //
-// A CTA takes a tile, a block of up to 8 * NT of its adapter's rows and a piece of K, which its
+// A CTA takes a tile, a block of up to 8 * NT (48) of its adapter's rows and a piece of K, which its
 // warps share; their sums meet in shared memory.  A lane holds 8 neighbouring elements of K of a
 // token's row and of an adapter's row: the MMA's order of K is free as long as both operands
 // agree, so 16-byte loads are its fragments as they come.
 template <bool FP8, int NT>
-__global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const __grid_constant__ AdapterParams p)
+__global__ void __launch_bounds__(32 * kDownWarps, 2) msa_adapter_down_kernel(const __grid_constant__ AdapterParams p)
 {
     __shared__ float s_sum[kDownWarps][kTile][8 * NT];
     wait_for_kernels_ahead();
@@ -264,31 +266,24 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
         const int block = item % p.n_blocks, split = item / p.n_blocks % tiles.splits;
         int a, token;
         tiles.get(p, item / p.n_blocks / tiles.splits, a, token);
-        const int tok[2] = {__shfl_sync(0xffffffffu, token, g), __shfl_sync(0xffffffffu, token, g + 8)};
-        const int n0 = block * p.n_tiles * 8;
-        const uint16_t *rows[NT];        // nullptr: none
+        // (a slot without a token takes slot 0's along, and so do the rows of a short block's last tiles:
+        // loads without branches between them, of lines that are there already)
+        const int some = __shfl_sync(0xffffffffu, token, __ffs(__ballot_sync(0xffffffffu, token >= 0)) - 1);
+        const int filled = token >= 0 ? token : some;
+        const int tok[2] = {__shfl_sync(0xffffffffu, filled, g), __shfl_sync(0xffffffffu, filled, g + 8)};
+        const int n0 = block * p.n_tiles * 8, nt = min(p.n_tiles, (n - n0) / 8);     // the rank is a multiple of 8
+        const uint16_t *down = p.down + ((int64_t)a * n + n0 + g) * p.down_stride;
+        int64_t at[NT];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int r = n0 + 8 * i + g;
-            rows[i] = i < p.n_tiles && r < n ? p.down + ((int64_t)a * n + r) * p.down_stride : nullptr;
-        }
+        for (int i = 0; i < NT; ++i)
+            at[i] = i < nt ? i * 8 * p.down_stride : 0;
         const int units = (p.hidden_size + kUnitK - 1) / kUnitK;
         const int piece = split * kDownWarps + warp, pieces = tiles.splits * kDownWarps;
         const int first = (int)((int64_t)units * piece / pieces), last = (int)((int64_t)units * (piece + 1) / pieces);
 
         float acc[NT][4] = {};
-        for (int u = first; u < last; ++u) {
-            uint4 x[2][2], w[NT][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = u * kUnitK + 32 * h + 8 * q;
-                const uint4 none = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    w[i][h] = rows[i] ? load_down(p, rows[i], k) : none;
-                x[0][h] = tok[0] >= 0 ? load_hidden<FP8>(p, tok[0], k) : none;
-                x[1][h] = tok[1] >= 0 ? load_hidden<FP8>(p, tok[1], k) : none;
-            }
+        uint4 x[2][2], w[NT][2];
+        auto multiply = [&]() {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t lo[4] = {x[0][h].x, x[1][h].x, x[0][h].y, x[1][h].y};
@@ -299,6 +294,34 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
                     mma(acc[i], hi, w[i][h].z, w[i][h].w);
                 }
             }
+        };
+        const int whole = min(last, p.hidden_size / kUnitK);       // units without a tail
+        const uint16_t *wp = down + first * kUnitK + 8 * q;
+        for (int u = first; u < whole; ++u, wp += kUnitK) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[i][h] = __ldg(reinterpret_cast<const uint4 *>(wp + at[i] + 32 * h));
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    x[r][h] = load_hidden<FP8, true>(p, tok[r], u * kUnitK + 32 * h + 8 * q);
+            multiply();
+        }
+        for (int u = max(first, whole); u < last; ++u) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = u * kUnitK + 32 * h + 8 * q;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    w[i][h] = load_down(p, down + at[i], k);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    x[r][h] = load_hidden<FP8, false>(p, tok[r], k);
+            }
+            multiply();
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -314,7 +337,7 @@ __global__ void __launch_bounds__(32 * kDownWarps) msa_adapter_down_kernel(const
             if (t < 0)
                 continue;
             const float scale = c * (p.hidden_scales ? p.hidden_scales[t] : 1.0f);
-            for (int i = lane; i < 8 * p.n_tiles && n0 + i < n; i += 32) {
+            for (int i = lane; i < 8 * nt; i += 32) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int v = 0; v < kDownWarps; ++v)
@@ -407,8 +430,8 @@ struct UpTile {
     }
 };
 
-// A warp takes a tile and 32 * PC columns, whose rows of up and of the tokens are loaded at once
-// before it waits for u.
+// A warp takes a tile and `chunk` columns, 32 * PC at a time, whose rows of up and of the tokens
+// are loaded at once; the first of them before it waits for u.
 template <int RC, bool EXACT>
 __global__ void __launch_bounds__(128, RC <= 2 ? 4 : 2) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
@@ -416,55 +439,60 @@ __global__ void __launch_bounds__(128, RC <= 2 ? 4 : 2) msa_adapter_up_kernel(co
     Tiles tiles;
     tiles.load(p);
     const int count = p.out != p.rows ? tiles.all : tiles.with_adapter;
-    const int chunks = (p.width + 32 * PC - 1) / (32 * PC);
+    const int chunks = (p.width + p.chunk - 1) / p.chunk;
     const int64_t work = (int64_t)count * chunks;
     bool waited = false;
     for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); item < work; item += (int64_t)gridDim.x * 4) {
-        const int c0 = (int)(item % chunks) * (32 * PC), end = min(p.width, c0 + 32 * PC);
+        const int from = (int)(item % chunks) * p.chunk, end = min(p.width, from + p.chunk);
         int a, token;
         tiles.get(p, (int)(item / chunks), a, token);
         UpTile<RC, EXACT> t;
         t.init(p, token, a >= 0);
         const int up_row = 8 * (t.g >> 1) + (t.g & 1);
-        uint32_t in[PC][2][4];
-        uint2 w[PC][4][RC];
+        for (int c0 = from; c0 < end; c0 += 32 * PC) {
+            uint32_t in[PC][2][4];
+            uint2 w[PC][4][RC];
 #pragma unroll
-        for (int b = 0; b < PC; ++b) {
-            const int c = c0 + 32 * b;
+            for (int b = 0; b < PC; ++b) {
+                const int c = c0 + 32 * b;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (t.live[h] && c + 8 * t.q < end) {
-                    const uint4 r = *reinterpret_cast<const uint4 *>(t.src[h] + c);
-                    in[b][h][0] = r.x, in[b][h][1] = r.y, in[b][h][2] = r.z, in[b][h][3] = r.w;
-                }
-            const uint16_t *up = p.up + ((int64_t)a * p.width + c + up_row) * t.rank + 4 * t.q;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < RC; ++k) {
-                    w[b][i][k] = make_uint2(0, 0);
-                    if (a >= 0 && c + up_row + 2 * i < end && (EXACT || 16 * k + 4 * t.q < t.rank))
-                        w[b][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * t.rank + 16 * k));
-                }
-        }
-        if (!waited)
-            wait_for_kernels_ahead();
-        waited = true;
-#pragma unroll
-        for (int b = 0; b < PC; ++b) {
-            const int c = c0 + 32 * b;
-            if (c >= end)
-                break;
-            if (a >= 0) {
-                t.slice_of(p, c, tiles.splits);
+                for (int h = 0; h < 2; ++h)
+                    if (t.live[h] && c + 8 * t.q < end) {
+                        const uint4 r = *reinterpret_cast<const uint4 *>(t.src[h] + c);
+                        in[b][h][0] = r.x, in[b][h][1] = r.y, in[b][h][2] = r.z, in[b][h][3] = r.w;
+                    }
+                if (a < 0)
+                    continue;
+                const uint16_t *up = p.up + ((int64_t)a * p.width + c + up_row) * t.rank + 4 * t.q;
+                const bool whole = EXACT && c + 32 <= end;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    t.add(in[b][0][i], in[b][1][i], w[b][i], in[b][0][i], in[b][1][i]);
-            }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (t.live[h] && c + 8 * t.q < end)
-                    *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(in[b][h][0], in[b][h][1], in[b][h][2], in[b][h][3]);
+                    for (int k = 0; k < RC; ++k)
+                        if (whole || (c + up_row + 2 * i < end && (EXACT || 16 * k + 4 * t.q < t.rank)))
+                            w[b][i][k] = __ldg(reinterpret_cast<const uint2 *>(up + 2 * i * t.rank + 16 * k));
+                        else
+                            w[b][i][k] = make_uint2(0, 0);
+            }
+            if (!waited)
+                wait_for_kernels_ahead();
+            waited = true;
+#pragma unroll
+            for (int b = 0; b < PC; ++b) {
+                const int c = c0 + 32 * b;
+                if (c >= end)
+                    break;
+                if (a >= 0) {
+                    t.slice_of(p, c, tiles.splits);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        t.add(in[b][0][i], in[b][1][i], w[b][i], in[b][0][i], in[b][1][i]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (t.live[h] && c + 8 * t.q < end)
+                        *reinterpret_cast<uint4 *>(t.dst[h] + c) = make_uint4(in[b][h][0], in[b][h][1], in[b][h][2], in[b][h][3]);
+            }
         }
     }
     if (!waited)                         // no CTA finishes before its wait
@@ -658,7 +686,7 @@ int width_of(const msa_adapter_cfg *cfg) { return cfg->slice_end[cfg->num_slices
 struct Plan {
     bool wide;               // tiles of 128 tokens (msa_adapter_tile.cu); else of 16
     bool sorted;             // more than one tile of tokens
-    int n_blocks, n_tiles;   // tiles of 16: blocks of at most 64 rows of down, tiles of 8 rows in each
+    int n_blocks, n_tiles;   // tiles of 16: blocks of at most 48 rows of down (two CTAs an SM), tiles of 8 rows in each
     int max_splits;          // pieces of K
     int64_t tiles;           // at most
     int64_t adapters, tokens, u, bytes;      // offsets into the workspace
@@ -670,7 +698,7 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
 {
     Plan c;
     const int64_t rows = (int64_t)cfg->num_slices * cfg->rank, units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
-    // Narrow tiles read the hidden states once for each block of 64 rows of down, and make E4M3 ones
+    // Narrow tiles read the hidden states once for each block of 48 rows of down, and make E4M3 ones
     // bf16 each time.  Sides meet (6,144 wide hidden states, 11,392 wide rows, three adapters): bf16, 80
     // rows at 2,000 tokens (41.7 us in narrow tiles, 40.2 in wide ones; 24.8 and 30.1 at 1,024), 320 rows
     // at 128 (31.0 and 28.9; 96.7 and 51.5 at 1,024); E4M3, 80 rows at 256 (19.2 and 17.7); bf16, 160
@@ -680,7 +708,7 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
     c.sorted = T > kTile;
     const int ts = c.wide ? 128 : kTile;
     c.tiles = T / ts + (T < cfg->num_adapters + 1 ? T : cfg->num_adapters + 1);
-    c.n_blocks = c.wide ? 1 : (int)((rows / 8 + 7) / 8);
+    c.n_blocks = c.wide ? 1 : (int)((rows / 8 + 5) / 6);
     c.n_tiles = (int)((rows / 8 + c.n_blocks - 1) / c.n_blocks);
     // no fewer than a unit of K for each warp of 8, four for a wide tile; and what the fewest tiles
     // that T tokens can make would take to fill the GPU
@@ -841,11 +869,9 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
         if (e != cudaSuccess)
             return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
     } else {
-        static const Kernel downs[2][4] = {
-            {msa_adapter_down_kernel<false, 2>, msa_adapter_down_kernel<false, 4>, msa_adapter_down_kernel<false, 6>,
-             msa_adapter_down_kernel<false, 8>},
-            {msa_adapter_down_kernel<true, 2>, msa_adapter_down_kernel<true, 4>, msa_adapter_down_kernel<true, 6>,
-             msa_adapter_down_kernel<true, 8>}};
+        static const Kernel downs[2][3] = {
+            {msa_adapter_down_kernel<false, 2>, msa_adapter_down_kernel<false, 4>, msa_adapter_down_kernel<false, 6>},
+            {msa_adapter_down_kernel<true, 2>, msa_adapter_down_kernel<true, 4>, msa_adapter_down_kernel<true, 6>}};
         const int64_t work = c.tiles * c.n_blocks * c.max_splits;
         const msa_status d = launch(downs[p.fp8][(c.n_tiles - 1) / 2], dim3((unsigned)(work < kFill ? work : kFill)),
                                     32 * kDownWarps, 0, stream, p);
@@ -860,8 +886,11 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
                                           msa_adapter_up_kernel<4, false>, msa_adapter_up_kernel<8, false>},
                                          {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>,
                                           msa_adapter_up_kernel<4, true>, msa_adapter_up_kernel<8, true>}};
-        const int columns = rc == 0 ? 128 : rc == 1 ? 64 : 32;
-        const int64_t ctas = (c.tiles * ((p.width + columns - 1) / columns) + 3) / 4;
+        // columns of a warp: what it loads at once, or more where the warps are enough all the same
+        p.chunk = rc == 0 ? 128 : rc == 1 ? 64 : 32;
+        while (p.chunk < 512 && c.tiles * ((p.width + p.chunk - 1) / p.chunk) > kUpWarps)
+            p.chunk *= 2;
+        const int64_t ctas = (c.tiles * ((p.width + p.chunk - 1) / p.chunk) + 3) / 4;
         return launch(ups[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 128, 0, stream, p);
     }
     static const Kernel ups[2][4] = {{msa_adapter_up_stream_kernel<1, false>, msa_adapter_up_stream_kernel<2, false>,

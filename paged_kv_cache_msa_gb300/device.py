@@ -169,6 +169,86 @@ class DeviceProjection:
         return self.rows_out.cpu().numpy().view(np.uint16)
 
 
+class LayerInput:
+    """The input side of an MSA layer for up to ``max_tokens`` tokens: the residual's addition and
+    the norm, which makes the projection's E4M3 operand with a scale for each token; the packed
+    projection; the requests' low-rank adapters on its rows; and the producer, with rotary
+    positions of one axis or several.
+
+    ``weight`` E4M3 [W, K] and ``weight_scales`` fp32 [W] are the projection's, ``norm_w`` bf16 [K]
+    the layer's norm, ``head_norms`` the producer's four, ``caches`` its (k, v, idx_k) MsaCacheDesc,
+    ``scales`` theirs.  ``axes``: an MsaRopeAxes for positions [num_axes, T], else positions are [T].
+    ``adapters``: (down, up, adapter_scales) tensors as ``binding.adapter_tensors`` takes them, the
+    slices being the row's sections.  Without adapters and axes the producer runs in the
+    projection's epilogue and the rows never leave the chip."""
+
+    def __init__(self, cfg: B.MsaProducerCfg, max_tokens: int, weight, weight_scales, norm_w, head_norms, caches, scales,
+                 axes=None, adapters=None, rms_eps: float = 1e-6):
+        import torch
+        W, K = weight.shape
+        dev, D = weight.device, cfg.head_dim
+        sections = [cfg.num_q_heads, cfg.num_kv_heads, cfg.num_kv_heads, cfg.num_idx_q_heads, cfg.num_idx_k_heads]
+        assert W == sum(sections) * D and weight.stride(1) == 1
+        self.cfg, self.weight, self.weight_scales, self.norm_w = cfg, weight, weight_scales, norm_w
+        self.head_norms, self.caches, self.scales, self.axes, self.adapters = head_norms, caches, scales, axes, adapters
+        self.norm_cfg = B.make_norm_cfg(K, rms_eps)
+        self.codes = torch.empty((max_tokens, -(-K // 16) * 16), dtype=torch.uint8, device=dev)[:, :K]
+        self.hidden_scales = torch.empty(max_tokens, dtype=torch.float32, device=dev)
+        self.q_out = torch.empty((max_tokens, cfg.num_q_heads, D), dtype=torch.bfloat16, device=dev)
+        self.idx_q_out = torch.empty((max_tokens, cfg.num_idx_q_heads, D), dtype=torch.bfloat16, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.rows = None
+        if axes is not None or adapters is not None:
+            self.rows = torch.empty((max_tokens, W), dtype=torch.bfloat16, device=dev)
+            # rows alone: index-K heads whose cache is absent, so that nothing else is written
+            self.rows_cfg = B.make_cfg(0, 0, 0, W // D, D, 0, cfg.rope_style, cfg.page_size)
+        if adapters is not None:
+            down, up, _ = adapters
+            ends = [sum(sections[:i + 1]) * D for i, n in enumerate(sections) if n > 0]
+            self.adapter_cfg = B.make_adapter_cfg(K, ends, up.shape[2], up.shape[0], B.MSA_DTYPE_FP8_E4M3)
+            nbytes = max(B.msa_adapter_workspace_bytes(self.adapter_cfg, n)
+                         for n in {max_tokens} | {1 << i for i in range(max_tokens.bit_length())})
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+    def _project(self, cfg, n, positions, slots, page_table, norms, q, iq, caches, scales, rows, stream):
+        p = lambda t: None if t is None else int(t.data_ptr())
+        B.msa_projection_forward(
+            cfg, n, p(self.codes), self.codes.shape[1], self.codes.stride(0), p(self.weight), self.weight.stride(0),
+            B.MSA_DTYPE_FP8_E4M3, p(self.hidden_scales), p(self.weight_scales), p(positions), p(slots), p(page_table),
+            0 if page_table is None else page_table.numel(), *(p(w) for w in norms), p(q), p(iq), *caches, p(scales),
+            p(rows), 0 if rows is None else rows.stride(0), p(self.status), stream=stream.cuda_stream)
+
+    def run(self, x, residual, positions, slot_mapping, page_table, adapter_ids=None, launch_flags=0, stream=None):
+        """For x and residual bf16 [T, K]: residual becomes their sum; q_out and idx_q_out [:T] and the
+        caches are written.  adapter_ids int32 [T] (with adapters); launch_flags: the producer's."""
+        import torch
+        n = x.shape[0]
+        if stream is None:
+            stream = torch.cuda.current_stream(x.device)
+        codes, hidden_scales = self.codes[:n], self.hidden_scales[:n]
+        q, iq = self.q_out[:n], self.idx_q_out[:n]
+        B.norm_tensors(self.norm_cfg, x, self.norm_w, residual=residual, residual_out=residual, codes=codes,
+                       scales=hidden_scales, stream=stream)
+        if self.rows is None:
+            self._project(self.cfg, n, positions, slot_mapping, page_table, self.head_norms, q, iq, self.caches,
+                          self.scales, None, stream)
+            return
+        rows = self.rows[:n]
+        # (nothing is turned or placed: any positions and slots will do)
+        self._project(self.rows_cfg, n, positions, slot_mapping, None, (None,) * 4, None, None, (None,) * 3, None, rows,
+                      stream)
+        if self.adapters is not None:
+            down, up, adapter_scales = self.adapters
+            B.adapter_tensors(self.adapter_cfg, codes, down, up, adapter_ids, rows, rows, hidden_scales=hidden_scales,
+                              adapter_scales=adapter_scales, workspace=self.workspace, stream=stream)
+        args = (rows, positions, slot_mapping, page_table, self.head_norms, q, iq, *self.caches, self.scales,
+                launch_flags, stream)
+        if self.axes is None:
+            B.forward_tensors(self.cfg, *args)
+        else:
+            B.forward_axes_tensors(self.cfg, self.axes, *args)
+
+
 class DecodeLayer:
     """One MSA decode layer's hot path on the device: the producer (rows -> compact
     Q / index-Q, K/V/index-K into the caches) followed by the indexer on what the

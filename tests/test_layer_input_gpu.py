@@ -1,0 +1,157 @@
+"""The input side of a layer as it is used (GPU): residual and norm, projection, adapters, producer,
+one after another on a stream and in a graph.  Each step's output is checked against its formula in
+64 bits, of the values that the step before gave it."""
+import pytest
+import torch
+
+from paged_kv_cache_msa_gb300 import binding as B
+from paged_kv_cache_msa_gb300 import build as build_mod
+from paged_kv_cache_msa_gb300.device import LayerInput
+from test_adapter_gpu import mixed, runs
+from test_norm_gpu import F32, check_codes, expected
+from test_rope_axes_gpu import BIG, TINY, Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build_mod.build()
+    return B.load()
+
+
+class Layer:
+    """A layer's weights, adapters and caches; the producer's part is a Case of the rotary tests."""
+
+    def __init__(self, n, shape, k, rank, adapters=4, axes=True, with_adapters=True, order=mixed, seed=0, max_tokens=None):
+        gen = torch.Generator(device="cuda").manual_seed(400 + seed)
+        d = shape[-1]
+        c = self.case = Case(n, shape, (d // 8, d // 8, d // 4), per_head=True, seed=seed, theta=5e6)
+        if not axes:
+            c.positions.copy_((torch.arange(n, device="cuda") % 64).to(torch.int32).expand(3, -1))
+        W, sr = c.width, 5 * rank
+        self.n, self.k = n, k
+        self.x = (2 * torch.randn(n, k, generator=gen, device="cuda")).bfloat16()
+        self.residual = (3 * torch.randn(n, k, generator=gen, device="cuda")).bfloat16()
+        self.norm_w = (0.5 + torch.rand(k, generator=gen, device="cuda")).bfloat16()
+        # (rows 16 bytes apart at least, as the projection wants them)
+        padded = torch.zeros(W, -(-k // 16) * 16, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        self.weight = padded[:, :k]
+        self.weight.view(torch.uint8).copy_(
+            (8 * torch.randn(W, k, generator=gen, device="cuda")).to(torch.float8_e4m3fn).view(torch.uint8))
+        self.weight_scales = (0.5 + torch.rand(W, generator=gen, device="cuda")) / 8 / k ** 0.5
+        self.down = (torch.randn(adapters, sr, k, generator=gen, device="cuda") / k ** 0.5).bfloat16()
+        self.up = torch.randn(adapters, W, rank, generator=gen, device="cuda").bfloat16()
+        self.alpha = 0.5 + torch.rand(adapters, generator=gen, device="cuda")
+        self.ids = torch.tensor(order(n, adapters), dtype=torch.int32, device="cuda") if with_adapters else None
+        self.adapters = (self.down, self.up, self.alpha) if with_adapters else None
+        self.desc = [B.cache_from_tensor(p) for p in c.pools]
+        self.layer = LayerInput(c.cfg, max_tokens or n, self.weight.view(torch.uint8), self.weight_scales, self.norm_w,
+                                c.weights, self.desc, c.scales, axes=c.axes if axes else None, adapters=self.adapters)
+        self.axes = axes
+
+    def run(self, flags=0, stream=None):
+        c = self.case
+        self.before = self.residual.clone()
+        pos = c.positions if self.axes else c.positions[0].contiguous()
+        self.layer.run(self.x, self.residual, pos, c.slots, c.table, self.ids, flags, stream)
+        return self
+
+    def check(self, before=None):
+        c, layer, n = self.case, self.layer, self.n
+        before = self.before if before is None else before
+        assert int(layer.status) == 0
+        assert torch.equal(self.residual, (self.x.float() + before.float()).bfloat16())
+        codes = layer.codes[:n].view(torch.float8_e4m3fn)
+        _, y, s = expected(self.x, before, self.norm_w, 1e-6)
+        check_codes(codes, layer.hidden_scales[:n], y, s)
+        if layer.rows is None:
+            return self
+        # rows: the projection of the codes, rounded to bf16 (2^-8), then the adapter's share, rounded
+        # again; fp32 sums of K products are off by K 2^-24 of their magnitudes' sum at most
+        h = codes.to(torch.float64) * layer.hidden_scales[:n, None].double()
+        w = self.weight.to(torch.float64) * self.weight_scales[:, None].double()
+        row = h @ w.T
+        tol = 2.0 ** -8 * row.abs() + (self.k + 4) * 2.0 ** -24 * (h.abs() @ w.abs().T)
+        if self.ids is not None:
+            d, hq, hkv, hiq, hik = c.shape[-1], *c.shape[:4]
+            ends, rank = [0], self.up.shape[2]
+            for heads in (hq, hkv, hkv, hiq, hik):
+                ends.append(ends[-1] + heads * d)
+            for a in range(self.up.shape[0]):
+                on = self.ids == a
+                for i in range(5):
+                    cols = slice(ends[i], ends[i + 1])
+                    dn, up = self.down[a, i * rank:(i + 1) * rank].double(), self.up[a, cols].double()
+                    row[on, cols] += float(self.alpha[a]) * (h[on] @ dn.T @ up.T)
+                    size = float(self.alpha[a]) * (h[on].abs() @ dn.abs().T @ up.abs().T)
+                    tol[on, cols] += size * ((self.k + rank + 8) * 2.0 ** -24 + 2.0 ** -16)
+            tol += 2.0 ** -8 * row.abs() + 2.0 ** -8 * tol
+        assert ((layer.rows[:n].double() - row).abs() <= tol).all()
+        c.rows, c.q, c.iq = layer.rows[:n], layer.q_out[:n], layer.idx_q_out[:n]
+        if self.axes:
+            c.check()
+        return self
+
+
+@pytest.mark.parametrize("n", [1, 7, 64, 300])
+@pytest.mark.parametrize("shape,k,rank", [(TINY, 320, 8), (TINY, 1000, 64), (BIG, 512, 16)], ids=["tiny", "tiny64", "big"])
+@pytest.mark.parametrize("flags", [0, B.MSA_LAUNCH_PERSISTENT])
+def test_steps(n, shape, k, rank, flags):
+    Layer(n, shape, k, rank, seed=n).run(flags).check()
+
+
+def test_prefill():
+    """Chunks of requests with an adapter each; wide tiles of the adapters, the projection's 2-SM kernel."""
+    Layer(1500, TINY, 2048, 32, order=runs).run(B.MSA_LAUNCH_PERSISTENT).check()
+
+
+def test_axes_alone_and_adapters_alone():
+    Layer(90, BIG, 512, 16, with_adapters=False).run().check()
+    Layer(90, BIG, 512, 16, axes=False).run().check()
+
+
+def test_neither_is_the_fused_projection():
+    """Without adapters and axes the producer runs in the projection's epilogue: the same compact Q,
+    up to a step of the rows' rounding, as through the rows."""
+    a = Layer(40, TINY, 512, 8, axes=False, with_adapters=False).run().check()
+    b = Layer(40, TINY, 512, 8, axes=False, order=lambda n, _: [-1] * n).run().check()
+    assert a.layer.rows is None
+    # rows a bf16 step apart (2^-7 of them) move a head's values by that, and by as much through its norm
+    size = b.layer.q_out[:40].double().abs().amax(-1, keepdim=True)
+    assert ((a.layer.q_out[:40].double() - b.layer.q_out[:40].double()).abs() <= 2.0 ** -5 * size).all()
+
+
+def test_graph_of_two_layers():
+    """Two layers one after another, the second on the first one's residual, on a side stream and in a
+    graph that is replayed with other requests, positions and adapters."""
+    one, two = Layer(64, TINY, 512, 16, seed=1, max_tokens=100), Layer(64, TINY, 512, 16, seed=2)
+    two.residual = one.residual
+    start = one.residual.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    one.run(stream=s)
+    two.run(stream=s)
+    s.synchronize()
+    two.check(before=(one.x.float() + start.float()).bfloat16())
+    one.residual = (one.x.float() + start.float()).bfloat16()
+    one.check(before=start)
+    one.residual = two.residual
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        one.run(B.MSA_LAUNCH_PERSISTENT | B.MSA_LAUNCH_PDL)
+        two.run(B.MSA_LAUNCH_PERSISTENT | B.MSA_LAUNCH_PDL)
+    for seed in (3, 4):
+        for i, layer in enumerate((one, two)):
+            new = Layer(64, TINY, 512, 16, seed=10 * seed + i)
+            layer.x.copy_(new.x)
+            layer.ids.copy_(new.ids)
+            layer.case.positions.copy_(new.case.positions)
+        one.residual.copy_(start)
+        g.replay()
+        torch.cuda.synchronize()
+        middle = (one.x.float() + start.float()).bfloat16()
+        two.check(before=middle)
+        one.residual = middle
+        one.check(before=start)
+        one.residual = two.residual

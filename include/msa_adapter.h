@@ -15,7 +15,7 @@
  * and zero columns of up.  msa_producer_forward (or msa_producer_axes_forward) of out is
  * the layer's producer with every request's adapter.
  *
- * Arithmetic: sums are fp32.  Where the second product runs on the tensor cores, u is split
+ * Arithmetic: sums are fp32.  The second product runs on the tensor cores, where u is split
  * into two bf16 parts, hi + lo (right to 2^-16 of each).  Results do not depend on which
  * other calls run, and a call repeated with the same arguments gives the same bits.
  *
@@ -48,9 +48,9 @@ typedef struct {
     int32_t reserved[3];    /* must be 0 */
 } msa_adapter_cfg;
 
-/* Bytes of workspace msa_adapter_forward needs for num_tokens tokens under cfg: less than
- * 2 MB and 512 bytes an adapter, and at most 32 * num_slices * rank + 80 bytes a token.
- * Host-side; enqueues nothing. */
+/* Bytes of workspace that serve msa_adapter_forward for any number of tokens up to num_tokens
+ * under cfg: less than 2 MB and 512 bytes an adapter, and at most 32 * num_slices * rank + 80
+ * bytes a token.  Host-side; enqueues nothing. */
 msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_tokens, int64_t *bytes);
 
 /*
@@ -65,7 +65,7 @@ msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_t
  * rows, out      device bf16 [num_tokens, rows_stride], [num_tokens, out_stride]; 16-byte
  *                aligned, strides multiples of 8, >= W.  out may be rows (with the same
  *                stride); otherwise they must not overlap.
- * workspace      device, 256-byte aligned, msa_adapter_workspace_bytes(cfg, num_tokens) bytes.
+ * workspace      device, 256-byte aligned; msa_adapter_workspace_bytes(cfg, num_tokens) bytes do.
  * launch_flags   MSA_LAUNCH_PDL: accepted; the kernels are launched with programmatic dependent
  *                launch in any case.
  *

@@ -490,7 +490,7 @@ def make_adapter_cfg(hidden_size, slice_ends, rank, num_adapters, hidden_dtype=M
 
 
 def msa_adapter_workspace_bytes(cfg, num_tokens) -> int:
-    """Bytes of workspace the adapter call needs."""
+    """Bytes of workspace that serve adapter calls of any number of tokens up to num_tokens."""
     n = ctypes.c_int64(0)
     s = load().msa_adapter_workspace_bytes(ctypes.byref(cfg) if cfg is not None else None, int(num_tokens),
                                            ctypes.byref(n))

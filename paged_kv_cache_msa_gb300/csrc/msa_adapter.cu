@@ -694,17 +694,24 @@ struct Plan {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
+// The elements of hidden states from which on a call of more than 16 tokens takes wide tiles.
+//
+// Narrow tiles read the hidden states once for each block of 48 rows of down, and make E4M3 ones
+// bf16 each time.  Sides meet (6,144 wide hidden states, 11,392 wide rows, three adapters): bf16, 80
+// rows at 2,000 tokens (41.7 us in narrow tiles, 40.2 in wide ones; 24.8 and 30.1 at 1,024), 320 rows
+// at 128 (31.0 and 28.9; 96.7 and 51.5 at 1,024); E4M3, 80 rows at 256 (19.2 and 17.7); bf16, 160
+// rows of 1,000 elements at 1,200 (13.6 and 15.2 at 1,024, 19.5 and 15.7 at 1,536).
+int64_t wide_from(const msa_adapter_cfg *cfg)
+{
+    const bool many = cfg->num_slices * cfg->rank > 2 * 64;
+    return many || cfg->hidden_dtype != MSA_DTYPE_BF16 ? 1200000 : 12000000;
+}
+
 Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
 {
     Plan c;
     const int64_t rows = (int64_t)cfg->num_slices * cfg->rank, units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
-    // Narrow tiles read the hidden states once for each block of 48 rows of down, and make E4M3 ones
-    // bf16 each time.  Sides meet (6,144 wide hidden states, 11,392 wide rows, three adapters): bf16, 80
-    // rows at 2,000 tokens (41.7 us in narrow tiles, 40.2 in wide ones; 24.8 and 30.1 at 1,024), 320 rows
-    // at 128 (31.0 and 28.9; 96.7 and 51.5 at 1,024); E4M3, 80 rows at 256 (19.2 and 17.7); bf16, 160
-    // rows of 1,000 elements at 1,200 (13.6 and 15.2 at 1,024, 19.5 and 15.7 at 1,536).
-    const int64_t blocks = (rows + 63) / 64;
-    c.wide = T > kTile && T * cfg->hidden_size >= (blocks > 2 || cfg->hidden_dtype != MSA_DTYPE_BF16 ? 1200000 : 12000000);
+    c.wide = T > kTile && T * cfg->hidden_size >= wide_from(cfg);
     c.sorted = T > kTile;
     const int ts = c.wide ? 128 : kTile;
     c.tiles = T / ts + (T < cfg->num_adapters + 1 ? T : cfg->num_adapters + 1);
@@ -725,6 +732,22 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
 }
 
 int64_t workspace_needed(const msa_adapter_cfg *cfg, int64_t T) { return plan_of(cfg, T).bytes; }
+
+// The most that any call of up to T tokens needs.  What a call needs grows with its tokens but where
+// a tile more leaves fewer pieces of K, or where wide tiles begin.
+int64_t workspace_for(const msa_adapter_cfg *cfg, int64_t T)
+{
+    int64_t most = workspace_needed(cfg, T);
+    const auto at = [&](int64_t t) {
+        const int64_t n = t < T ? workspace_needed(cfg, t) : 0;
+        most = n > most ? n : most;
+    };
+    for (const int ts : {kTile, 128})
+        for (int64_t t = ts; t < T && t <= (int64_t)kFill * ts; t += ts)
+            at(t);
+    at((wide_from(cfg) - 1) / cfg->hidden_size);
+    return most;
+}
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -803,7 +826,7 @@ msa_status msa_adapter_workspace_bytes(const msa_adapter_cfg *cfg, int64_t num_t
         return s;
     if (!bytes)
         return fail(MSA_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = workspace_needed(cfg, num_tokens);
+    *bytes = workspace_for(cfg, num_tokens);
     return MSA_OK;
 }
 

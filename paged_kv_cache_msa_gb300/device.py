@@ -206,8 +206,7 @@ class LayerInput:
             down, up, _ = adapters
             ends = [sum(sections[:i + 1]) * D for i, n in enumerate(sections) if n > 0]
             self.adapter_cfg = B.make_adapter_cfg(K, ends, up.shape[2], up.shape[0], B.MSA_DTYPE_FP8_E4M3)
-            nbytes = max(B.msa_adapter_workspace_bytes(self.adapter_cfg, n)
-                         for n in {max_tokens} | {1 << i for i in range(max_tokens.bit_length())})
+            nbytes = B.msa_adapter_workspace_bytes(self.adapter_cfg, max_tokens)
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
     def _project(self, cfg, n, positions, slots, page_table, norms, q, iq, caches, scales, rows, stream):

@@ -158,6 +158,20 @@ def test_adapter_workspace_bounds(rank, slices, t):
         assert 0 <= n < 2 * 2**20 + 512 * adapters + (32 * slices * rank + 80) * t
 
 
+@pytest.mark.parametrize("rank,slices", [(8, 1), (16, 5), (64, 5), (128, 4)])
+@pytest.mark.parametrize("k", [64, 6144, 40000])
+@pytest.mark.parametrize("dtype", [B.MSA_DTYPE_BF16, B.MSA_DTYPE_FP8_E4M3])
+def test_adapter_workspace_serves_fewer_tokens(rank, slices, k, dtype):
+    """A workspace for n tokens serves every call of fewer: never fewer bytes for more tokens, across
+    the step to wide tiles and the counts at which a tile more leaves fewer pieces of K."""
+    cfg = adapter_cfg(hidden_size=k, rank=rank, hidden_dtype=dtype, num_adapters=3,
+                      slice_ends=[64 * (i + 1) for i in range(slices)])
+    sizes = [B.msa_adapter_workspace_bytes(cfg, t) for t in range(0, 2600)]
+    assert sizes == sorted(sizes)
+    sizes = [B.msa_adapter_workspace_bytes(cfg, t) for t in range(0, 400_000, 977)]
+    assert sizes == sorted(sizes)
+
+
 # ---------------------------------------------------------------------------
 # the producer with several axes
 # ---------------------------------------------------------------------------

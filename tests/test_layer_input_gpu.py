@@ -155,3 +155,12 @@ def test_graph_of_two_layers():
         one.residual = middle
         one.check(before=start)
         one.residual = two.residual
+
+
+@pytest.mark.parametrize("n", [1, 16, 17, 33, 100, 500])
+def test_fewer_tokens_than_the_layers(n):
+    layer = Layer(n, TINY, 1000, 64, seed=n, max_tokens=1300)
+    rows = layer.layer.rows
+    rows.fill_(7.0)
+    layer.run().check()
+    assert (rows[n:] == 7.0).all(), "rows behind the last token"

@@ -46,6 +46,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <type_traits>
 #include <mutex>
 
 // Resident 256-thread CTAs per SM the register budget is sized for (3: 80 registers).
@@ -642,6 +643,11 @@ msa_producer_kernel(const __grid_constant__ P p)
     __shared__ __align__(16) TokenMeta s_meta[2][kGroup];
     __shared__ float s_inv[kMaxHeadScales];   // 1 / scale of every FP8 cache (per tensor or head)
 
+    // A small call with several axes is launched with programmatic dependent launch without
+    // MSA_LAUNCH_PDL too (see launch()).  Then it waits for the kernels ahead before it reads
+    // anything or lets the next one start: what it and later kernels may see is as after a plain launch.
+    if (std::is_same_v<P, AxesParams> && !p.pdl)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 #if MSA_PDL_EARLY_TRIGGER
     asm volatile("griddepcontrol.launch_dependents;" :::);
 #endif
@@ -1227,7 +1233,11 @@ msa_status launch(const msa_rope_axes *axes, int64_t positions_stride, const msa
     lc.dynamicSmemBytes = (size_t)smem;
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
-    if (launch_flags & MSA_LAUNCH_PDL) {
+    // Without the flag, small calls with several axes hide their launch this way and wait at once.  Calls
+    // one after another on a stream, and in a graph, plain and so launched (us, rows of 22 KB): 64 tokens
+    // 8.2 and 5.5, graph 5.5 and 5.1; 152 tokens 8.2 and 5.8, 5.8 and 5.4; at more than a token an SM
+    // they win and lose (304: 10.3 and 8.9, but 7.9 and 8.3; 1,999: 23.0 and 24.0, 21.5 and 22.6).
+    if ((axes && num_tokens <= 152) || (launch_flags & MSA_LAUNCH_PDL)) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         lc.attrs = attr;

@@ -29,6 +29,7 @@ constexpr int kDownWarps = 8;        // warps of a CTA of the down-projection, e
 constexpr int kUnitK = 64;           // K elements a warp takes at a time: 128 bytes of bf16
 constexpr int kUpWarps = 16 * 152;   // warps that fill the GPU in the up-projection
 constexpr int kFill = 2 * 152;       // CTAs that fill the GPU at two an SM
+constexpr int kListed = 128;         // tokens that a CTA puts into tiles by itself
 constexpr int kSortKept = 8;         // tokens of a thread of the sort that it loads once
 constexpr int kMaxAdapters = 16384;  // the sort counts them in shared memory
 
@@ -152,15 +153,26 @@ __global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_con
     });
 }
 
-// The tiles of 16 tokens of one adapter, from the sort, or (p.tokens nullptr: at most 16 tokens)
-// found by each warp.  Those without an adapter come last.
+// The tiles of up to kListed tokens, which every CTA makes for itself: a thread has a token, whose
+// place is the number of tokens before it with the same adapter.
+struct TileList {
+    int id[kListed];                 // -1: none, -2: behind the last token
+    int adapter[kListed];            // of a tile
+    int heads[2][kListed / 32];      // of each warp, with an adapter and without
+    uint8_t tile[kListed][kListed / kTile];   // of an adapter's first token: its tiles
+    uint8_t token[kListed][kTile];   // 255: none
+};
+
+// The tiles of 16 tokens of one adapter: from the sort (p.tokens), from a list in shared memory, or
+// (at most 16 tokens) found by each warp.  Those without an adapter come last.
 struct Tiles {
     int with_adapter, all, splits;
     int id;              // at most 16 tokens: this lane's token's adapter, and
     uint32_t same;       // the tokens with the same one
     uint32_t leaders;    // the first token of each distinct adapter
 
-    __device__ __forceinline__ void load(const AdapterParams &p)
+    // by all threads of a CTA, kListed or more
+    __device__ __forceinline__ void load(const AdapterParams &p, TileList &s)
     {
         if (p.tokens) {
             with_adapter = p.head->with_adapter;
@@ -168,23 +180,91 @@ struct Tiles {
             splits = p.head->splits;
             return;
         }
-        const int lane = threadIdx.x & 31, t = lane & 15;
-        id = t < p.num_tokens ? p.ids[t] : -1;
-        if (id < 0 || id >= p.num_adapters)
-            id = -1;
-        same = __match_any_sync(0xffffffffu, id) & 0xffffu;
-        leaders = __ballot_sync(0xffffffffu, id >= 0 && lane == __ffs(same) - 1);
-        with_adapter = __popc(leaders);
-        all = with_adapter + (__any_sync(0xffffffffu, id < 0 && t < p.num_tokens) ? 1 : 0);
+        const int lane = threadIdx.x & 31;
+        if (p.num_tokens <= kTile) {
+            const int t = lane & 15;
+            id = t < p.num_tokens ? p.ids[t] : -1;
+            if (id < 0 || id >= p.num_adapters)
+                id = -1;
+            same = __match_any_sync(0xffffffffu, id) & 0xffffu;
+            leaders = __ballot_sync(0xffffffffu, id >= 0 && lane == __ffs(same) - 1);
+            with_adapter = __popc(leaders);
+            all = with_adapter + (__any_sync(0xffffffffu, id < 0 && t < p.num_tokens) ? 1 : 0);
+        } else {
+            make(p, s);
+        }
         splits = max(1, min(p.max_splits, kFill / max(1, with_adapter * p.n_blocks)));
     }
+    __device__ __forceinline__ void make(const AdapterParams &p, TileList &s)
+    {
+        const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+        const bool there = t < p.num_tokens;         // at most kListed
+        int a = -2;
+        if (there) {
+            a = p.ids[t];
+            a = a < 0 || a >= p.num_adapters ? -1 : a;
+        }
+        if (t < kListed) {
+            s.id[t] = a;
+            reinterpret_cast<uint4 *>(s.token)[t] = make_uint4(~0u, ~0u, ~0u, ~0u);
+        }
+        __syncthreads();
+        // the tokens before this one with the same adapter, and the first of all
+        const uint32_t below = (1u << lane) - 1u, mine = __match_any_sync(0xffffffffu, a);
+        int before = __popc(mine & below), root = 32 * warp + __ffs(mine) - 1;
+#pragma unroll
+        for (int v = kListed / 32 - 2; v >= 0; --v)
+            if (v < warp && 32 * warp < kListed) {
+                uint32_t same = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int4 x = reinterpret_cast<const int4 *>(s.id + 32 * v)[j];
+                    same |= (x.x == a ? 1u << 4 * j : 0u) | (x.y == a ? 2u << 4 * j : 0u) |
+                            (x.z == a ? 4u << 4 * j : 0u) | (x.w == a ? 8u << 4 * j : 0u);
+                }
+                before += __popc(same);
+                if (same)
+                    root = 32 * v + __ffs(same) - 1;
+            }
+        const bool first = there && before % kTile == 0;
+        const uint32_t some = __ballot_sync(0xffffffffu, first && a >= 0), none = __ballot_sync(0xffffffffu, first && a < 0);
+        if (lane == 0 && t < kListed) {
+            s.heads[0][warp] = __popc(some);
+            s.heads[1][warp] = __popc(none);
+        }
+        __syncthreads();
+        int at[2] = {0, 0}, total[2] = {0, 0};
+#pragma unroll
+        for (int v = 0; v < kListed / 32; ++v)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                at[i] += v < warp ? s.heads[i][v] : 0;
+                total[i] += s.heads[i][v];
+            }
+        with_adapter = total[0];
+        all = total[0] + total[1];
+        if (first) {
+            const int tile = a >= 0 ? at[0] + __popc(some & below) : total[0] + at[1] + __popc(none & below);
+            s.tile[root][before / kTile] = (uint8_t)tile;
+            s.adapter[tile] = a;
+        }
+        __syncthreads();
+        if (there)
+            s.token[s.tile[root][before / kTile]][before % kTile] = (uint8_t)t;
+        __syncthreads();
+    }
     // The adapter of a tile, and this lane's token (of slot lane % 16), -1 without one.
-    __device__ __forceinline__ void get(const AdapterParams &p, int tile, int &adapter, int &token) const
+    __device__ __forceinline__ void get(const AdapterParams &p, const TileList &s, int tile, int &adapter, int &token) const
     {
         const int slot = threadIdx.x & 15;
         if (p.tokens) {
             adapter = p.adapters[tile];
             token = p.tokens[tile * kTile + slot];
+            return;
+        }
+        if (p.num_tokens > kTile) {
+            adapter = s.adapter[tile];
+            token = s.token[tile][slot] == 255 ? -1 : s.token[tile][slot];
             return;
         }
         uint32_t left = leaders;
@@ -256,16 +336,17 @@ template <bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kDownWarps, 2) msa_adapter_down_kernel(const __grid_constant__ AdapterParams p)
 {
     __shared__ float s_sum[kDownWarps][kTile][8 * NT];
+    __shared__ __align__(16) TileList s_tiles;
     wait_for_kernels_ahead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int n = p.num_slices * p.rank;
     Tiles tiles;
-    tiles.load(p);
+    tiles.load(p, s_tiles);
     const int work = tiles.with_adapter * p.n_blocks * tiles.splits;
     for (int item = blockIdx.x; item < work; item += gridDim.x) {
         const int block = item % p.n_blocks, split = item / p.n_blocks % tiles.splits;
         int a, token;
-        tiles.get(p, item / p.n_blocks / tiles.splits, a, token);
+        tiles.get(p, s_tiles, item / p.n_blocks / tiles.splits, a, token);
         // (a slot without a token takes slot 0's along, and so do the rows of a short block's last tiles:
         // loads without branches between them, of lines that are there already)
         const int some = __shfl_sync(0xffffffffu, token, __ffs(__ballot_sync(0xffffffffu, token >= 0)) - 1);
@@ -436,8 +517,9 @@ template <int RC, bool EXACT>
 __global__ void __launch_bounds__(128, RC <= 2 ? 4 : 2) msa_adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
     constexpr int PC = RC == 1 ? 4 : RC == 2 ? 2 : 1;
+    __shared__ __align__(16) TileList s_tiles;
     Tiles tiles;
-    tiles.load(p);
+    tiles.load(p, s_tiles);
     const int count = p.out != p.rows ? tiles.all : tiles.with_adapter;
     const int chunks = (p.width + p.chunk - 1) / p.chunk;
     const int64_t work = (int64_t)count * chunks;
@@ -445,7 +527,7 @@ __global__ void __launch_bounds__(128, RC <= 2 ? 4 : 2) msa_adapter_up_kernel(co
     for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); item < work; item += (int64_t)gridDim.x * 4) {
         const int from = (int)(item % chunks) * p.chunk, end = min(p.width, from + p.chunk);
         int a, token;
-        tiles.get(p, (int)(item / chunks), a, token);
+        tiles.get(p, s_tiles, (int)(item / chunks), a, token);
         UpTile<RC, EXACT> t;
         t.init(p, token, a >= 0);
         const int up_row = 8 * (t.g >> 1) + (t.g & 1);
@@ -712,7 +794,7 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
     Plan c;
     const int64_t rows = (int64_t)cfg->num_slices * cfg->rank, units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
     c.wide = T > kTile && T * cfg->hidden_size >= wide_from(cfg);
-    c.sorted = T > kTile;
+    c.sorted = c.wide || T > kListed;
     const int ts = c.wide ? 128 : kTile;
     c.tiles = T / ts + (T < cfg->num_adapters + 1 ? T : cfg->num_adapters + 1);
     c.n_blocks = c.wide ? 1 : (int)((rows / 8 + 5) / 6);

@@ -403,3 +403,14 @@ def test_more_tokens_than_the_sort_keeps():
     """Tokens beyond those that the sorting threads hold in registers."""
     Case(mixed(20000, 5), k=24, ends=(64, 72), rank=8, adapters=5).run().check()
     wide_case(mixed, 40001, 32, adapters=3, ends=(128,)).run().check()
+
+
+@pytest.mark.parametrize("t", [17, 31, 32, 33, 63, 65, 95, 96, 97, 128])
+@pytest.mark.parametrize("order", [lambda t, n: [0] * t, lambda t, n: [-1] * t, lambda t, n: [n] * (t - 1) + [n - 1],
+                                   lambda t, n: [i % 2 - 1 for i in range(t)], lambda t, n: [(5 * i) % n for i in range(t)],
+                                   lambda t, n: [i * n // t for i in range(t)][::-1]],
+                         ids=["one", "none", "last", "every other", "several", "chunks"])
+def test_tiles_of_up_to_128_tokens(t, order):
+    """Batches whose tiles every CTA makes by itself: one adapter's tiles over several warps' tokens."""
+    for n in (3, 131):
+        Case(order(t, n), k=40, ends=(64, 72), rank=8, adapters=n).run().check()

@@ -1,17 +1,21 @@
 // Low-rank adapters of many requests beside a shared projection (include/msa_adapter.h).
 //
 // Up to three kernels:
-//   sort   the tokens by adapter, in tiles of 16 or 128 of one adapter each (not for one tile of
-//          tokens, whose distinct adapters a warp finds by itself).  Reading an adapter costs more
-//          than anything else in a decode batch, and in no order of the tokens is it read more
-//          often than once a tile: 512 tokens over 16 adapters, mixed, took 100 us in tiles of
-//          consecutive tokens that go through their distinct adapters.
+//   sort   the tokens by adapter, in tiles of 16 or 128 of one adapter each (up to 128 tokens are
+//          put into tiles by every CTA of the next kernels: 64 tokens over 48 adapters take 18.2 us,
+//          19.3 with the sort, 64 over 3 adapters 9.5 and 11.2, 128 over 3 10.9 and 11.4).  Reading
+//          an adapter costs more than anything else in a decode batch, and in no order of the tokens
+//          is it read more often than once a tile: 512 tokens over 16 adapters, mixed, took 100 us
+//          in tiles of consecutive tokens that go through their distinct adapters.
 //   down   every token's hidden state through its adapter's down-projection, into a workspace
 //          (partial sums over pieces of K)
 //   up     the up-projection of their sum, added to the rows
 // A tile's tokens share the MMA's B operand, its adapter; each has a row of its own, so nothing
 // passes from one request to another.  Reading the adapters bounds a decode batch (65 MB for 64
-// tokens over 48 adapters of rank 16), reading and writing the rows a prefill: both HBM.
+// tokens over 48 adapters of rank 16), reading and writing the rows a prefill: both HBM.  One
+// kernel in the place of two, clusters of 8 or 16 CTAs that share a tile's K and join its sums
+// through distributed shared memory, took 9.5 us for one token and 31.7 for those 64 (5.7 and
+// 18.2): fewer warps read a tile, in rounds of loads that wait 2 us each.
 
 #include "msa_adapter_internal.h"
 

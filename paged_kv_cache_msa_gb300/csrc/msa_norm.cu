@@ -5,11 +5,11 @@
 // for about ten operations, so HBM bandwidth bounds it, and at a few tokens the chain of
 // one load, one reduction over the row and one store.
 //   * A row is read once, into the registers of `threads_per_row` threads: vectors of 8
-//     elements, up to four a thread, all their loads issued before the first is used.
+//     elements, up to seven a thread, all their loads issued before the first is used.
 //   * The largest |y| needs no second pass: y = fl(fl(h w) r) with r > 0, and rounding is
 //     monotone, so max |y| = fl(max |fl(h w)| r), and the sum of squares and the maximum of
-//     |h w| go through one reduction with one barrier (none for rows of one warp).  The maximum is taken of the bit
-//     patterns, which order as the magnitudes do, NaN above infinity.
+//     |h w| go through one reduction with one barrier (none for rows of one warp).  The maximum
+//     is taken of the bit patterns, which order as the magnitudes do, NaN above infinity.
 //   * A row's partial sums are added in the order of the warps by every thread: the result
 //     does not depend on the schedule.
 

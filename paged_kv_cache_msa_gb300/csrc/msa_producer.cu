@@ -1144,7 +1144,8 @@ void fill_axes(AxesParams &p, const msa_producer_cfg *cfg, const msa_rope_axes *
 }
 
 // Both entry points: axes is nullptr for positions of one axis.
-msa_status launch(const msa_rope_axes *axes, int64_t positions_stride, const msa_producer_cfg *cfg, int64_t num_tokens, const void *qkv, int64_t qkv_row_stride,
+msa_status launch(const msa_rope_axes *axes, int64_t positions_stride, const msa_producer_cfg *cfg,
+                  int64_t num_tokens, const void *qkv, int64_t qkv_row_stride,
                   const int32_t *positions, const int64_t *slot_mapping, const int32_t *page_table,
                   int64_t page_table_len, const void *q_norm_w, const void *k_norm_w,
                   const void *idx_q_norm_w, const void *idx_k_norm_w, void *q_out, void *idx_q_out,

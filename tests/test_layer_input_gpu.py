@@ -164,3 +164,89 @@ def test_fewer_tokens_than_the_layers(n):
     rows.fill_(7.0)
     layer.run().check()
     assert (rows[n:] == 7.0).all(), "rows behind the last token"
+
+
+def test_no_tokens():
+    layer = Layer(5, TINY, 512, 16)
+    c = layer.case
+    before = [p.clone() for p in c.pools]
+    layer.layer.run(layer.x[:0], layer.residual[:0], c.positions[:, :0].contiguous(), c.slots[:0], c.table,
+                    layer.ids[:0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(p.view(torch.uint8), b.view(torch.uint8)) for p, b in zip(c.pools, before))
+
+
+@pytest.mark.parametrize("n", [3, 100, 700])
+def test_streams_that_fork_and_join(n):
+    """What a layer reads and writes is made and used by other streams around it: the input by a copy on
+    one, the ids by a copy on another, the results read on the first, called one by one and in a graph."""
+    layer = Layer(n, TINY, 2048, 32, seed=n)
+    new = [Layer(n, TINY, 2048, 32, seed=n + s) for s in (1, 2)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    x, ids, residual = layer.x.clone(), layer.ids.clone(), layer.residual.clone()
+    rows, q = torch.empty_like(layer.layer.rows), torch.empty_like(layer.layer.q_out)
+
+    def step():
+        here = torch.cuda.current_stream()
+        a.wait_stream(here)
+        b.wait_stream(here)
+        with torch.cuda.stream(b):
+            layer.ids.fill_(-7)
+            layer.ids.copy_(ids)
+            layer.residual.copy_(residual)
+        with torch.cuda.stream(a):
+            layer.x.zero_()
+            layer.x.copy_(x)
+            a.wait_stream(b)
+            layer.run(stream=a)
+        here.wait_stream(a)
+        rows.copy_(layer.layer.rows)
+        q.copy_(layer.layer.q_out)
+
+    def check(before):
+        torch.cuda.synchronize()
+        layer.check(before=before)
+        assert torch.equal(rows, layer.layer.rows) and torch.equal(q, layer.layer.q_out)
+
+    torch.cuda.synchronize()
+    step()
+    check(residual)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for other in new:
+        x.copy_(other.x)
+        ids.copy_(other.ids)
+        residual.copy_(other.residual)
+        g.replay()
+        check(residual)
+
+
+def test_two_layers_at_once():
+    """Two threads, a layer and a stream each."""
+    import threading
+    layers = [Layer(200, TINY, 1000, 64, seed=s) for s in (5, 6)]
+    torch.cuda.synchronize()
+    start = [layer.residual.clone() for layer in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(layer, begin, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    layer.residual.copy_(begin)
+                    layer.run(stream=stream)
+        except Exception as e:       # shown below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(layers, start, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for layer, begin in zip(layers, start):
+        layer.check(before=begin)

@@ -414,3 +414,30 @@ def test_tiles_of_up_to_128_tokens(t, order):
     """Batches whose tiles every CTA makes by itself: one adapter's tiles over several warps' tokens."""
     for n in (3, 131):
         Case(order(t, n), k=40, ends=(64, 72), rank=8, adapters=n).run().check()
+
+
+@pytest.mark.parametrize("t", [1, 20, 200, 1300])
+def test_every_e4m3_value(t):
+    """Every finite code, in every place of a word, through a down-projection that picks single elements
+    out and an up-projection that passes them on: exact but for the output's rounding, none at all here
+    (an E4M3 value times a power of two).  A NaN code makes its own element of the row NaN."""
+    k, rank = 2048, 64
+    cfg = B.make_adapter_cfg(k, (64, 128, 192), rank, 1, B.MSA_DTYPE_FP8_E4M3)
+    at = torch.arange(t, device="cuda")[:, None] * 37 + torch.arange(k, device="cuda")
+    codes = ((at + at // 256) % 256).to(torch.uint8)
+    codes[codes & 0x7F == 0x7F] = 0
+    values = codes.view(torch.float8_e4m3fn).double()
+    up = torch.zeros(1, 192, rank, dtype=torch.bfloat16, device="cuda")
+    up[0, torch.arange(192), torch.arange(192) % 64] = 4.0
+    rows, out = torch.zeros(t, 192, dtype=torch.bfloat16, device="cuda"), torch.empty(t, 192, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(t, dtype=torch.int32, device="cuda")
+    ws = torch.empty(B.msa_adapter_workspace_bytes(cfg, t), dtype=torch.uint8, device="cuda")
+    for first in (0, 192, 1024, k - 192):
+        down = torch.zeros(1, 3 * rank, k, dtype=torch.bfloat16, device="cuda")
+        down[0, torch.arange(192), first + torch.arange(192)] = 1.0
+        B.adapter_tensors(cfg, codes, down, up, ids, rows, out, workspace=ws)
+        assert torch.equal(out.double(), 4 * values[:, first:first + 192])
+    codes[t // 2, 5] = 0xFF
+    B.adapter_tensors(cfg, codes, down, up, ids, rows, out, workspace=ws)
+    nan = out.isnan().any(1)
+    assert nan[t // 2] and int(nan.sum()) == 1

@@ -37,6 +37,12 @@ constexpr int kListed = 128;         // tokens that a CTA puts into tiles by its
 constexpr int kSortKept = 8;         // tokens of a thread of the sort that it loads once
 constexpr int kMaxAdapters = 16384;  // the sort counts them in shared memory
 
+// CTAs that a down-projection's pieces of K are to fill.  Wide tiles have fewer and longer pieces: a CTA
+// an SM, although two fit (8,192 tokens of rank 32 105.7 us for 109.6, of rank 16 96.3 for 101.5; 5,000
+// bf16 ones of rank 48 108 for 129; 4,000 of rank 8 53.0 for 52.3): each has a start, an
+// epilogue and its partial sums to write and to read.
+__host__ __device__ constexpr int fill_of(bool narrow) { return narrow ? kFill : kFill / 2; }
+
 __device__ __forceinline__ float2 unpack2(uint32_t v)
 {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(1024) msa_adapter_sort_kernel(const __grid_con
             p.head->tiles = tile + tiles;
             // so many pieces of K that the down-projection fills the GPU once
             const int units = max(1, tile * p.n_blocks);
-            p.head->splits = max(1, min(p.max_splits, kFill / units));
+            p.head->splits = max(1, min(p.max_splits, fill_of(ts == kTile) / units));
         }
         s_place[a] = tile * ts;
         for (int i = count; i < tiles * ts; ++i)
@@ -806,7 +812,7 @@ Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
     // no fewer than a unit of K for each warp of 8, four for a wide tile; and what the fewest tiles
     // that T tokens can make would take to fill the GPU
     const int64_t most = c.wide ? (units / 4 < 8 ? units / 4 : 8) : (units + kDownWarps - 1) / kDownWarps;
-    const int64_t want = kFill / (((T + ts - 1) / ts > 0 ? (T + ts - 1) / ts : 1) * c.n_blocks);
+    const int64_t want = fill_of(!c.wide) / (((T + ts - 1) / ts > 0 ? (T + ts - 1) / ts : 1) * c.n_blocks);
     c.max_splits = (int)(want < most ? want : most);
     if (c.max_splits < 1)
         c.max_splits = 1;

@@ -1014,9 +1014,17 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
                                       msa_adapter_up_stream_kernel<4, true>, msa_adapter_up_stream_kernel<8, true>}};
     const int smem = 2 * (32 << rc) * kUpStage + 8 * 2 * (16 * 32 * 2 * (kUpStage / 32));
     const int64_t groups = (num_tokens + 127) / 128;
+    // Each chunk reads all parts of u again, max_splits * rank * 4 bytes a token and slice beside its own
+    // 4 a column: chunks grow until that is a quarter, while there are two CTAs an SM (2,048 tokens
+    // of rank 64 64.2 us without and 55.4 with, 1,024 of rank 32 33.8 and 30.0, 512 of rank 96 47.1 and 40.7;
+    // for 4,000 of rank 8, whose u is small, as large chunks take 57.2 for 54.8).
     p.chunk = kUpStage;
-    while (p.chunk < 1024 && groups * ((p.width + p.chunk - 1) / p.chunk) > 8 * 152)
+    while (p.chunk < 1024) {
+        const int64_t items = groups * ((p.width + p.chunk - 1) / p.chunk);
+        if (items <= 2 * 152 || (items <= 8 * 152 && p.chunk >= 4 * p.max_splits * p.rank))
+            break;
         p.chunk *= 2;
+    }
     const int64_t ctas = c.tiles * ((p.width + p.chunk - 1) / p.chunk);
     if (allow(ups[exact][rc], smem) != cudaSuccess)
         return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed");

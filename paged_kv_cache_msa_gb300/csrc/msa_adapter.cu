@@ -21,6 +21,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -810,24 +811,30 @@ struct Plan {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// The elements of hidden states from which on a call of more than 16 tokens takes wide tiles.
+// The tokens from which on a call takes wide tiles.
 //
-// Narrow tiles read the hidden states once for each block of 48 rows of down, and make E4M3 ones
-// bf16 each time.  Sides meet (6,144 wide hidden states, 11,392 wide rows, three adapters): bf16, 80
-// rows at 2,000 tokens (41.7 us in narrow tiles, 40.2 in wide ones; 24.8 and 30.1 at 1,024), 320 rows
-// at 128 (31.0 and 28.9; 96.7 and 51.5 at 1,024); E4M3, 80 rows at 256 (19.2 and 17.7); bf16, 160
-// rows of 1,000 elements at 1,200 (13.6 and 15.2 at 1,024, 19.5 and 15.7 at 1,536).
+// Narrow tiles read the hidden states once for each block of 48 rows of down and an adapter once for 16
+// tokens, wide ones start later and have fewer CTAs.  Where the sides meet, T^2 * rows * K is 2.5e11 to
+// 9e11, of bf16 and E4M3 (6,144 wide hidden states and 11,392 wide rows, three adapters' chunks, narrow
+// and wide us: 80 rows 27.1 and 27.3 at 1,000 tokens, 160 rows 21.6 and 22.2 at 500, 37.1 and 31.6 at
+// 1,000, 320 rows 20.1 and 30.7 at 300, 31.6 and 29.8 at 500, 54.2 and 38.9 at 1,000; 1,000 and 960 wide,
+// 160 rows 13.4 and 15.0 at 1,500, 17.0 and 15.8 at 2,000).  Adapters in no order fill wide
+// tiles badly below 56 tokens each (16 of them, 320 rows: 37.4 and 60.6 at 500 tokens, 60.2 and 61.0 at
+// 1,000); a batch of 900 tokens or more is rather a prefill's chunks.
 int64_t wide_from(const msa_adapter_cfg *cfg)
 {
-    const bool many = cfg->num_slices * cfg->rank > 2 * 64;
-    return many || cfg->hidden_dtype != MSA_DTYPE_BF16 ? 1200000 : 12000000;
+    const double rows = (double)cfg->num_slices * cfg->rank;
+    const int64_t tokens = (int64_t)std::ceil(std::sqrt(5e11 / (rows * cfg->hidden_size)));
+    const int64_t mixed = 56 * (int64_t)(cfg->num_adapters < 16 ? cfg->num_adapters : 16);
+    const int64_t from = tokens > mixed ? tokens : mixed;
+    return from > kTile + 1 ? from : kTile + 1;
 }
 
 Plan plan_of(const msa_adapter_cfg *cfg, int64_t T)
 {
     Plan c;
     const int64_t rows = (int64_t)cfg->num_slices * cfg->rank, units = (cfg->hidden_size + kUnitK - 1) / kUnitK;
-    c.wide = T > kTile && T * cfg->hidden_size >= wide_from(cfg);
+    c.wide = T >= wide_from(cfg);
     c.sorted = c.wide || T > kListed;
     const int ts = c.wide ? 128 : kTile;
     c.tiles = T / ts + (T < cfg->num_adapters + 1 ? T : cfg->num_adapters + 1);
@@ -861,7 +868,7 @@ int64_t workspace_for(const msa_adapter_cfg *cfg, int64_t T)
     for (const int ts : {kTile, 128})
         for (int64_t t = ts; t < T && t <= (int64_t)kFill * ts; t += ts)
             at(t);
-    at((wide_from(cfg) - 1) / cfg->hidden_size);
+    at(wide_from(cfg) - 1);
     return most;
 }
 

@@ -299,8 +299,8 @@ def test_a_chain_in_place(t):
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
-# Tiles of 128 tokens are taken from 1.2 million hidden values on (E4M3, or more than 128 rows of
-# down; 12 million otherwise).
+# Tiles of 128 tokens are taken from T^2 * rows of down * K of 5e11 and 56 tokens an adapter (up to 16
+# of them) on.  Sizes below that are batches that tiles of 16 must hold as well.
 
 def wide_case(order, t=1300, k=1000, rank=64, adapters=4, **kw):
     assert t * k >= 1200000 and rank > 24
@@ -441,3 +441,32 @@ def test_every_e4m3_value(t):
     B.adapter_tensors(cfg, codes, down, up, ids, rows, out, workspace=ws)
     nan = out.isnan().any(1)
     assert nan[t // 2] and int(nan.sum()) == 1
+
+
+def wide_tiles(order, t, k, ends=SMALL, rank=32, adapters=3, **kw):
+    assert t * t * len(ends) * rank * k >= 5e11 and t >= 56 * min(adapters, 16)
+    return Case(order(t, adapters), k=k, ends=ends, rank=rank, adapters=adapters, **kw)
+
+
+@pytest.mark.parametrize("t,k", [(1400, 2049), (1801, 1001), (1800, 1000), (2200, 650), (700, 9000), (550, 15500)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_wide_tiles_of_other_sizes(t, k, fp8):
+    wide_tiles(runs if t % 4 else mixed, t, k, fp8=fp8, pad=1, seed=k).run().check()
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 40])
+@pytest.mark.parametrize("order", [mixed, runs], ids=["mixed", "runs"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_wide_tiles_of_small_ranks(rank, order, fp8):
+    wide_tiles(order, 3600, 1000, rank=rank, fp8=fp8).run().check()
+
+
+@pytest.mark.parametrize("ends", [(8,), (72,), (1000,), (4096, 4104)], ids=str)
+def test_wide_tiles_of_few_slices(ends):
+    wide_tiles(mixed, 2100, 1000, ends=ends, rank=128, fp8=True, pad=2).run().check()
+
+
+@pytest.mark.parametrize("t", [895, 896, 897])
+def test_many_adapters_at_the_step_to_wide_tiles(t):
+    wide_tiles(mixed, 896, 4000, rank=40, adapters=40)
+    Case(mixed(t, 40), k=4000, rank=40, adapters=40, fp8=True).run().check()

@@ -106,6 +106,11 @@ def test_prefill():
     Layer(1500, TINY, 2048, 32, order=runs).run(B.MSA_LAUNCH_PERSISTENT).check()
 
 
+def test_longer_prefill():
+    """Sizes of the adapters' wide tiles."""
+    Layer(2000, TINY, 2048, 32, order=runs, seed=9).run(B.MSA_LAUNCH_PERSISTENT).check()
+
+
 def test_axes_alone_and_adapters_alone():
     Layer(90, BIG, 512, 16, with_adapters=False).run().check()
     Layer(90, BIG, 512, 16, axes=False).run().check()

@@ -2,8 +2,8 @@
 //
 // Up to three kernels:
 //   sort   the tokens by adapter, in tiles of 16 or 128 of one adapter each (up to 128 tokens are
-//          put into tiles by every CTA of the next kernels: 64 tokens over 48 adapters take 18.2 us,
-//          19.3 with the sort, 64 over 3 adapters 9.5 and 11.2, 128 over 3 10.9 and 11.4).  Reading
+//          put into tiles by every CTA of the next kernels: 64 tokens over 48 adapters take 18.1 us,
+//          1.1 more with the sort, 64 over 3 adapters 8.5 and 1.7 more, 128 over 3 10.1 and 0.5).  Reading
 //          an adapter costs more than anything else in a decode batch, and in no order of the tokens
 //          is it read more often than once a tile: 512 tokens over 16 adapters, mixed, took 100 us
 //          in tiles of consecutive tokens that go through their distinct adapters.
@@ -14,8 +14,8 @@
 // passes from one request to another.  Reading the adapters bounds a decode batch (65 MB for 64
 // tokens over 48 adapters of rank 16), reading and writing the rows a prefill: both HBM.  One
 // kernel in the place of two, clusters of 8 or 16 CTAs that share a tile's K and join its sums
-// through distributed shared memory, took 9.5 us for one token and 31.7 for those 64 (5.7 and
-// 18.2): fewer warps read a tile, in rounds of loads that wait 2 us each.
+// through distributed shared memory, took 9.5 us for one token and 31.7 for those 64 (5.6 and
+// 18.1): fewer warps read a tile, in rounds of loads that wait 2 us each.
 
 #include "msa_adapter_internal.h"
 

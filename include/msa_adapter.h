@@ -16,7 +16,8 @@
  * the layer's producer with every request's adapter.
  *
  * Arithmetic: sums are fp32.  The second product runs on the tensor cores, where u is split
- * into two bf16 parts, hi + lo (right to 2^-16 of each).  Results do not depend on which
+ * into three bf16 parts that hold all of its bits; so an element of up that is infinite makes
+ * its outputs NaN, where the formula in fp32 has NaN or an infinity.  Results do not depend on which
  * other calls run, and a call repeated with the same arguments gives the same bits.
  *
  * Ownership and threading: as for msa_producer_forward; the workspace as the attention

@@ -51,13 +51,17 @@ __device__ __forceinline__ uint32_t adapter_bf16x2(float x0, float x1)
     return d;
 }
 
-// (x0, x1) as two bf16 pairs whose sum is right to 2^-16 of each: x rounded, and what is left of
-// it (nothing of an infinite one).
-__device__ __forceinline__ void adapter_split(float x0, float x1, uint32_t &hi, uint32_t &lo)
+// (x0, x1) as three bf16 pairs whose sum is (x0, x1), all 24 bits of them (down to bf16's smallest,
+// 2^-133): 8 bits cut off at a time, what is left of an infinity being nothing.
+__device__ __forceinline__ void adapter_split(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo)
 {
-    hi = adapter_bf16x2(x0, x1);
-    const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
-    lo = adapter_bf16x2(isinf(h0) ? 0.0f : x0 - h0, isinf(h1) ? 0.0f : x1 - h1);
+    const auto top = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); };
+    const auto pair = [](float x, float y) { return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632); };
+    hi = pair(x0, x1);
+    x0 = isinf(x0) ? 0.0f : x0 - top(x0);
+    x1 = isinf(x1) ? 0.0f : x1 - top(x1);
+    mid = pair(x0, x1);
+    lo = pair(x0 - top(x0), x1 - top(x1));
 }
 
 // Two E4M3 codes (the low half of c) -> a bf16 pair: exact, since bf16 holds every E4M3 value.

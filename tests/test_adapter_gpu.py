@@ -470,3 +470,41 @@ def test_wide_tiles_of_few_slices(ends):
 def test_many_adapters_at_the_step_to_wide_tiles(t):
     wide_tiles(mixed, 896, 4000, rank=40, adapters=40)
     Case(mixed(t, 40), k=4000, rank=40, adapters=40, fp8=True).run().check()
+
+
+def from_rule(rows, k, adapters=1):
+    """The tokens from which on a call takes tiles of 128."""
+    return max(int((5e11 / (rows * k)) ** 0.5) + 1, 56 * min(adapters, 16))
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("t", [1, 20, 200, "wide"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_all_bits_of_u(rank, t, fp8):
+    """u of 21 significant bits, put together from whole numbers of 7 bits (E4M3: 20 bits of 4), less
+    another u of its upper bits: what is left, a number of 7 bits (4), is exact in every step."""
+    k, bits = 2048, 4 if fp8 else 7
+    pieces, pairs = 20 // bits if fp8 else 21 // bits, rank // 2
+    t = from_rule(rank, k) if t == "wide" else t
+    two = rank % 16 == 0                                 # two slices of half the rank each
+    cfg = B.make_adapter_cfg(k, (64, 136) if two else (136,), rank // 2 if two else rank, 1,
+                             B.MSA_DTYPE_FP8_E4M3 if fp8 else B.MSA_DTYPE_BF16)
+    slices, per = cfg.num_slices, cfg.rank // 2          # pairs of rows of down in a slice
+    gen = torch.Generator(device="cuda").manual_seed(rank)
+    x = torch.zeros(t, k, device="cuda")
+    x[:, :pieces * pairs] = torch.randint(1, 2 ** bits, (t, pieces * pairs), generator=gen, device="cuda").float()
+    down = torch.zeros(1, slices * cfg.rank, k, device="cuda")
+    for m in range(pairs):                               # rows 2 m and 2 m + 1: all pieces, and all but the last
+        for i in range(pieces):
+            down[0, 2 * m:2 * m + 1 + (i < pieces - 1), pieces * m + i] = 2.0 ** (-bits * i)
+    col = torch.arange(136, device="cuda")
+    pair = col % per
+    up = torch.zeros(1, 136, cfg.rank, device="cuda")
+    up[0, col, 2 * pair], up[0, col, 2 * pair + 1] = 1.0, -1.0
+    rows = torch.zeros(t, 136, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(rows)
+    hidden = x.to(torch.float8_e4m3fn if fp8 else torch.bfloat16)
+    assert torch.equal(hidden.float(), x)
+    B.adapter_tensors(cfg, hidden, down.bfloat16(), up.bfloat16(), torch.zeros(t, dtype=torch.int32, device="cuda"), rows, out)
+    last = pieces * (pair + (per * (col >= 64) if slices == 2 else 0)) + pieces - 1
+    assert torch.equal(out.double(), x[:, last].double() * 2.0 ** (-bits * (pieces - 1)))

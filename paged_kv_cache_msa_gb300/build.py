@@ -250,6 +250,22 @@ def build_starved(force: bool = False) -> str:
     return STARVED_LIB_PATH
 
 
+GIVEN_UP_LIB_PATH = os.path.join(OUT_DIR, "libmsa_producer_given_up.so")
+
+
+def build_given_up(force: bool = False) -> str:
+    """Compiles a second test library of the timeout path (-DMSA_GIVE_UP, every bounded wait
+    limited to STARVED_WAIT_LIMIT_NS): the warps that make the adapters' hidden states give up
+    at once, as if their first wait had run out, while the copy warp's copies land.  Only the
+    tests load it; the product uses build()."""
+    defs = ("MSA_GIVE_UP", f"MSA_WAIT_LIMIT_NS={STARVED_WAIT_LIMIT_NS}ull")
+    stamp = GIVEN_UP_LIB_PATH + ".sha256"
+    digest = source_digest(defs)
+    if force or not _fresh(GIVEN_UP_LIB_PATH, stamp, digest):
+        _compile(GIVEN_UP_LIB_PATH, stamp, digest, [f"-D{d}" for d in defs])
+    return GIVEN_UP_LIB_PATH
+
+
 LAGGING_LIB_PATH = os.path.join(OUT_DIR, "libmsa_producer_lagging.so")
 
 

@@ -233,7 +233,11 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
         const int r0 = w / kPerRow, col = (w % kPerRow) * (kBlockK / kPerRow);
         Ring st(ST);
         uint32_t done = 0;
+#ifdef MSA_GIVE_UP
+        bool ok = false;
+#else
         bool ok = true;
+#endif
         for (int item = blockIdx.x; item < work; item += gridDim.x, ++done) {
             const int tile = item / splits, split = item % splits, k0 = first_block(split), k1 = first_block(split + 1);
             const int a = p.adapters[tile];
@@ -291,8 +295,9 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
                 tc_fence_after();
             // Through the ring, which is free after the last item, so that four lanes write 64 bytes of
             // a row (each lane a row of its own: 7.5 us more of 32); rows 80 bytes apart lie on
-            // different banks.  An earlier item writes its rows as they are.
-            const bool last = item + (int)gridDim.x >= work;
+            // different banks.  An earlier item writes its rows as they are, and so does one that a wait
+            // ran out for: copies may still be landing in the ring.
+            const bool last = ok && item + (int)gridDim.x >= work;
             const uint32_t buf = ring + (uint32_t)(warp - 2) * (32u * 80u);
             int out[4];
 #pragma unroll

@@ -34,3 +34,25 @@ def test_stops_and_writes_nan(libs, order, fp8):
     assert torch.equal(c.out[~on].view(torch.int16), c.rows[~on].view(torch.int16))
     B._lib = normal
     c.run().check()
+
+
+@pytest.mark.parametrize("rank,k", [(64, 1000), (24, 2100), (96, 640)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_gives_up_while_copies_land(libs, rank, k, fp8):
+    """Rows that are given up with copies in flight are NaN, not what the copies bring: every row,
+    over many calls.  (Nothing else uses the memory that the copies land in.)"""
+    normal, _ = libs
+    given_up = B.load(build_mod.build_given_up())
+    c = Case(runs(2048, 3), k=k, adapters=3, rank=rank, fp8=fp8)
+    on = (c.ids >= 0) & (c.ids < 3)
+    B._lib = given_up
+    try:
+        for _ in range(3):
+            c.out.zero_()
+            c.run()
+            torch.cuda.synchronize()
+            assert c.out[on].isnan().all()
+            assert torch.equal(c.out[~on].view(torch.int16), c.rows[~on].view(torch.int16))
+    finally:
+        B._lib = normal
+    c.run().check()

@@ -1584,6 +1584,18 @@ EncodeTiledFn encoder()
     return g_encode;
 }
 
+// Calls the driver's encoder, which wants a context of the calling thread: a host thread whose
+// first CUDA call this is has none until the runtime binds the current device's.
+template <class F>
+bool encoded(F encode)
+{
+    CUresult r = encode();
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = encode();
+    return r == CUDA_SUCCESS;
+}
+
 // A [rows, cols] matrix of bf16 (elem_size 2) or 8-bit codes (1) with a row stride
 // of `stride` elements, read in boxes of box_rows x 128 bytes with the 128-byte
 // swizzle; out-of-range elements read as zero.
@@ -1597,11 +1609,12 @@ bool encode_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, in
     cuuint64_t strides[1] = {(cuuint64_t)stride * (cuuint64_t)elem_size};
     cuuint32_t box[2] = {(cuuint32_t)(kBKBytes / elem_size), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return enc(m, elem_size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-               const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encoded([&] {
+        return enc(m, elem_size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                   const_cast<void *>(base), dims, strides, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 void fill_cache(CacheArgs &a, const msa_cache_desc *c)
@@ -1693,10 +1706,12 @@ bool msa_internal_encode_tiled(CUtensorMap *m, const void *base, int elem_size, 
         if (i + 1 < rank)
             st[i] = (cuuint64_t)strides[i];
     }
-    return enc(m, elem_size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
-               const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encoded([&] {
+        return enc(m, elem_size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
+                   const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 extern "C" msa_status msa_projection_validate(

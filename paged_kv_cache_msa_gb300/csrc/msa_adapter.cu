@@ -21,6 +21,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -921,7 +922,51 @@ msa_status check_args(const msa_adapter_cfg *cfg, int64_t T, const AdapterParams
     return MSA_OK;
 }
 
-msa_status launch(void (*kernel)(AdapterParams), dim3 grid, int threads, int smem, cudaStream_t stream, AdapterParams &p)
+using Kernel = void (*)(AdapterParams);
+
+// by rank: 16, 32, 64, 128 exactly, or up to them
+const Kernel kUpKernels[2][4] = {{msa_adapter_up_kernel<1, false>, msa_adapter_up_kernel<2, false>,
+                                  msa_adapter_up_kernel<4, false>, msa_adapter_up_kernel<8, false>},
+                                 {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>,
+                                  msa_adapter_up_kernel<4, true>, msa_adapter_up_kernel<8, true>}};
+const Kernel kUpStreamKernels[2][4] = {{msa_adapter_up_stream_kernel<1, false>, msa_adapter_up_stream_kernel<2, false>,
+                                        msa_adapter_up_stream_kernel<4, false>, msa_adapter_up_stream_kernel<8, false>},
+                                       {msa_adapter_up_stream_kernel<1, true>, msa_adapter_up_stream_kernel<2, true>,
+                                        msa_adapter_up_stream_kernel<4, true>, msa_adapter_up_stream_kernel<8, true>}};
+
+// Dynamic shared memory of the streaming up-projection.
+constexpr int up_stream_smem(int rc) { return 2 * (32 << rc) * kUpStage + 8 * 2 * (16 * 32 * 2 * (kUpStage / 32)); }
+
+// Lets the kernels have as much shared memory as any call of theirs takes, once on each device.  (A
+// limit is a kernel's, for all threads: one set for each call could fall below what another
+// thread's call is about to launch with.)
+cudaError_t allow_shared_memory(bool wide)
+{
+    static std::atomic<uint64_t> done[2];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done[wide].load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    auto allow = [&](Kernel k, int smem) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    };
+    allow(msa_adapter_sort_kernel, (kMaxAdapters + 1) * 4);
+    for (int rc = 0; wide && rc < 4; ++rc) {
+        allow(kUpStreamKernels[0][rc], up_stream_smem(rc));
+        allow(kUpStreamKernels[1][rc], up_stream_smem(rc));
+    }
+    if (wide && e == cudaSuccess)
+        e = adapter_tile_allow();
+    if (e == cudaSuccess)
+        done[wide].fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+msa_status launch(Kernel kernel, dim3 grid, int threads, int smem, cudaStream_t stream, AdapterParams &p)
 {
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
@@ -998,14 +1043,17 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     p.max_splits = c.max_splits;
     p.n_blocks = c.n_blocks;
     p.n_tiles = c.n_tiles;
-    using Kernel = void (*)(AdapterParams);
-    auto allow = [](Kernel k, int smem) {
-        return cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    };
+    // all that can fail ahead of the first launch
+    AdapterTilePlan tile_plan;
+    if (c.sorted) {
+        const cudaError_t e = allow_shared_memory(c.wide);
+        if (e != cudaSuccess)
+            return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+    }
+    if (c.wide && !adapter_tile_plan(p, &tile_plan))
+        return fail(MSA_ERR_CUDA, "down: no tensor map");
     if (c.sorted) {
         const int smem = (p.num_adapters + 1) * 4;
-        if (smem > 48 * 1024 && allow(msa_adapter_sort_kernel, smem) != cudaSuccess)
-            return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed");
         // as many threads as have something to do: barriers of 1,024 take 1 us more
         const int64_t most = num_tokens > p.num_adapters + 1 ? num_tokens : p.num_adapters + 1;
         const int threads = most >= 1024 ? 1024 : (int)((most + 31) / 32 * 32);
@@ -1014,7 +1062,7 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
             return d;
     }
     if (c.wide) {
-        const cudaError_t e = adapter_down_tiles(p, c.tiles, stream);
+        const cudaError_t e = adapter_tile_launch(p, tile_plan, c.tiles, stream);
         if (e != cudaSuccess)
             return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
     } else {
@@ -1031,22 +1079,13 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     const int k16 = (p.rank + 15) / 16, rc = k16 <= 1 ? 0 : k16 <= 2 ? 1 : k16 <= 4 ? 2 : 3;
     const bool exact = p.rank == 16 << rc;
     if (!c.wide) {
-        static const Kernel ups[2][4] = {{msa_adapter_up_kernel<1, false>, msa_adapter_up_kernel<2, false>,
-                                          msa_adapter_up_kernel<4, false>, msa_adapter_up_kernel<8, false>},
-                                         {msa_adapter_up_kernel<1, true>, msa_adapter_up_kernel<2, true>,
-                                          msa_adapter_up_kernel<4, true>, msa_adapter_up_kernel<8, true>}};
         // columns of a warp: what it loads at once, or more where the warps are enough all the same
         p.chunk = rc == 0 ? 128 : rc == 1 ? 64 : 32;
         while (p.chunk < 512 && c.tiles * ((p.width + p.chunk - 1) / p.chunk) > kUpWarps)
             p.chunk *= 2;
         const int64_t ctas = (c.tiles * ((p.width + p.chunk - 1) / p.chunk) + 3) / 4;
-        return launch(ups[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 128, 0, stream, p);
+        return launch(kUpKernels[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 128, 0, stream, p);
     }
-    static const Kernel ups[2][4] = {{msa_adapter_up_stream_kernel<1, false>, msa_adapter_up_stream_kernel<2, false>,
-                                      msa_adapter_up_stream_kernel<4, false>, msa_adapter_up_stream_kernel<8, false>},
-                                     {msa_adapter_up_stream_kernel<1, true>, msa_adapter_up_stream_kernel<2, true>,
-                                      msa_adapter_up_stream_kernel<4, true>, msa_adapter_up_stream_kernel<8, true>}};
-    const int smem = 2 * (32 << rc) * kUpStage + 8 * 2 * (16 * 32 * 2 * (kUpStage / 32));
     const int64_t groups = (num_tokens + 127) / 128;
     // Each chunk reads all parts of u again, max_splits * rank * 4 bytes a token and slice beside its own
     // 4 a column: chunks grow until that is a quarter, while there are two CTAs an SM (2,048 tokens
@@ -1060,9 +1099,8 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
         p.chunk *= 2;
     }
     const int64_t ctas = c.tiles * ((p.width + p.chunk - 1) / p.chunk);
-    if (allow(ups[exact][rc], smem) != cudaSuccess)
-        return fail(MSA_ERR_CUDA, "cudaFuncSetAttribute failed");
-    return launch(ups[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 256, smem, stream, p);
+    return launch(kUpStreamKernels[exact][rc], dim3((unsigned)(ctas < 8 * 152 ? ctas : 8 * 152)), 256, up_stream_smem(rc),
+                  stream, p);
 }
 
 }  // extern "C"

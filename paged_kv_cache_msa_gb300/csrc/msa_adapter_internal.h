@@ -37,8 +37,24 @@ struct AdapterParams {
     int32_t slice_end[MSA_ADAPTER_MAX_SLICES];
 };
 
-// The down-projection of tiles of 128 tokens (msa_adapter_tile.cu) into p.u; at most `tiles`.
-cudaError_t adapter_down_tiles(const AdapterParams &p, int64_t tiles, cudaStream_t stream);
+// The down-projection of tiles of 128 tokens (msa_adapter_tile.cu) into p.u: what it is launched
+// with, made ahead of the call's first launch, and its launch for at most `tiles`.
+struct AdapterTileShape {
+    int32_t n;           // rows of down an MMA pair takes: a multiple of 16 (32 where two boxes)
+    int32_t boxes;       // 1 or 2 of at most 256 rows
+    int32_t stages;
+    int32_t tmem;        // columns allocated
+    uint32_t stage_bytes;
+};
+
+struct AdapterTilePlan {
+    AdapterTileShape shape;
+    CUtensorMap down;
+};
+
+cudaError_t adapter_tile_allow();        // its shared memory, on the current device
+bool adapter_tile_plan(const AdapterParams &p, AdapterTilePlan *plan);
+cudaError_t adapter_tile_launch(const AdapterParams &p, const AdapterTilePlan &plan, int64_t tiles, cudaStream_t stream);
 
 #ifdef __CUDACC__
 namespace {

@@ -26,14 +26,8 @@ constexpr int kMaxStages = 8;
 constexpr int kWorkers = 8;                   // conversion and epilogue warps
 constexpr int kThreads = 64 + 32 * kWorkers;
 constexpr uint32_t kTileX = kM * 128;
-
-struct TileShape {
-    int32_t n;           // rows of down an MMA pair takes: a multiple of 16 (32 where two boxes)
-    int32_t boxes;       // 1 or 2 of at most 256 rows
-    int32_t stages;
-    int32_t tmem;        // columns allocated
-    uint32_t stage_bytes;
-};
+constexpr uint32_t kHalfSm = 108 * 1024;      // shared memory of a CTA's ring, two on an SM; one has twice that
+constexpr int kMaxSmem = 2 * kHalfSm + 1024;
 
 // A place in a ring of n stages or buffers, and the parity of its phase.  (Counted on: divisions
 // by a number that is not known to the compiler cost every role 0.1 us each.)
@@ -111,7 +105,7 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t *row, int k, int hidde
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads)
-msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __grid_constant__ TileShape s,
+msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __grid_constant__ AdapterTileShape s,
                              const __grid_constant__ CUtensorMap wmap)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -351,10 +345,21 @@ msa_adapter_down_tile_kernel(const __grid_constant__ AdapterParams p, const __gr
 
 }  // namespace
 
-cudaError_t adapter_down_tiles(const AdapterParams &p, int64_t tiles, cudaStream_t stream)
+cudaError_t adapter_tile_allow()
+{
+    for (const void *fn : {reinterpret_cast<const void *>(&msa_adapter_down_tile_kernel<true>),
+                           reinterpret_cast<const void *>(&msa_adapter_down_tile_kernel<false>)}) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+bool adapter_tile_plan(const AdapterParams &p, AdapterTilePlan *plan)
 {
     const int rows = p.num_slices * p.rank;
-    TileShape s;
+    AdapterTileShape &s = plan->shape;
     s.boxes = rows > 256 ? 2 : 1;
     s.n = (rows + 16 * s.boxes - 1) / (16 * s.boxes) * (16 * s.boxes);
     s.tmem = 32;
@@ -362,34 +367,31 @@ cudaError_t adapter_down_tiles(const AdapterParams &p, int64_t tiles, cudaStream
         s.tmem *= 2;
     s.stage_bytes = kTileX + (uint32_t)s.n * 128u;
     // two CTAs on an SM where at least three stages fit into half of its shared memory
-    const uint32_t halfsm = 108 * 1024;
-    s.stages = (int)((3 * s.stage_bytes <= halfsm ? halfsm : 2 * halfsm) / s.stage_bytes);
+    s.stages = (int)((3 * s.stage_bytes <= kHalfSm ? kHalfSm : 2 * kHalfSm) / s.stage_bytes);
     if (s.stages > kMaxStages)
         s.stages = kMaxStages;
     const int64_t wdims[2] = {p.hidden_size, (int64_t)p.num_adapters * rows}, wstride[1] = {2 * p.down_stride};
     const int32_t wbox[2] = {kBlockK, s.n / s.boxes};
-    CUtensorMap wmap;
-    if (!msa_internal_encode_tiled(&wmap, p.down, 2, 2, wdims, wstride, wbox, 128))
-        return cudaErrorNotSupported;
+    return msa_internal_encode_tiled(&plan->down, p.down, 2, 2, wdims, wstride, wbox, 128);
+}
+
+cudaError_t adapter_tile_launch(const AdapterParams &p, const AdapterTilePlan &plan, int64_t tiles, cudaStream_t stream)
+{
+    const AdapterTileShape &s = plan.shape;
     const void *fn = p.fp8 ? reinterpret_cast<const void *>(&msa_adapter_down_tile_kernel<true>)
                            : reinterpret_cast<const void *>(&msa_adapter_down_tile_kernel<false>);
-    const int smem = s.stages * (int)s.stage_bytes + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return e;
-    const int64_t work = tiles * p.max_splits, fill = 3 * s.stage_bytes <= halfsm ? 2 * 152 : 152;
+    const int64_t work = tiles * p.max_splits, fill = 3 * s.stage_bytes <= kHalfSm ? 2 * 152 : 152;
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
     lc.gridDim = dim3((unsigned)(work < fill ? work : fill));
     lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = (size_t)smem;
+    lc.dynamicSmemBytes = (size_t)s.stages * s.stage_bytes + 1024;
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    AdapterParams params = p;
-    void *args[] = {&params, &s, &wmap};
+    void *args[] = {const_cast<AdapterParams *>(&p), const_cast<AdapterTileShape *>(&s), const_cast<CUtensorMap *>(&plan.down)};
     return cudaLaunchKernelExC(&lc, fn, args);
 }

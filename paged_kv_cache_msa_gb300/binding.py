@@ -9,6 +9,7 @@ Names follow the headers in ``include/``: ``msa_producer.h``, ``msa_projection.h
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -591,6 +592,18 @@ def _ptr(t):
     return None if t is None else int(t.data_ptr())
 
 
+_here = contextlib.nullcontext()
+
+
+def on_device(dev):
+    """A context in which ``dev`` is the current CUDA device, as the C calls want that of their
+    stream and pointers to be."""
+    import torch
+    if dev.type != "cuda" or dev.index in (None, torch.cuda.current_device()):
+        return _here
+    return torch.cuda.device(dev)
+
+
 def cache_from_tensor(t, dtype: int | None = None) -> MsaCacheDesc:
     """Descriptor of a cache given as a (possibly non-contiguous) tensor view
     [num_pages, num_heads, page_size, head_dim] with unit dim stride.  The dtype
@@ -614,17 +627,19 @@ def forward_tensors(cfg: MsaProducerCfg, qkv, positions, slot_mapping, page_tabl
                     stream=None) -> None:
     """msa_producer_forward on torch CUDA tensors.  ``qkv`` is [T, >= width] bf16
     with unit column stride; ``norm_weights`` a 4-tuple (q, k, idx_q, idx_k);
-    caches are MsaCacheDesc (or None).  Runs on ``stream`` or the current stream."""
+    caches are MsaCacheDesc (or None).  Runs on ``stream`` or the current stream of
+    qkv's device."""
     import torch
     assert qkv.dim() == 2 and qkv.stride(1) == 1
     if stream is None:
         stream = torch.cuda.current_stream(qkv.device)
     pt_len = 0 if page_table is None else page_table.numel()
     wq, wk, wiq, wik = norm_weights
-    msa_producer_forward(cfg, qkv.shape[0], _ptr(qkv), qkv.stride(0), _ptr(positions),
-                         _ptr(slot_mapping), _ptr(page_table), pt_len, _ptr(wq), _ptr(wk),
-                         _ptr(wiq), _ptr(wik), _ptr(q_out), _ptr(idx_q_out), k_cache, v_cache,
-                         idx_k_cache, _ptr(scales), launch_flags, stream.cuda_stream)
+    with on_device(qkv.device):
+        msa_producer_forward(cfg, qkv.shape[0], _ptr(qkv), qkv.stride(0), _ptr(positions),
+                             _ptr(slot_mapping), _ptr(page_table), pt_len, _ptr(wq), _ptr(wk),
+                             _ptr(wiq), _ptr(wik), _ptr(q_out), _ptr(idx_q_out), k_cache, v_cache,
+                             idx_k_cache, _ptr(scales), launch_flags, stream.cuda_stream)
 
 
 def _tensor(name, t, shape, dtypes, device):

@@ -211,11 +211,13 @@ class LayerInput:
 
     def _project(self, cfg, n, positions, slots, page_table, norms, q, iq, caches, scales, rows, stream):
         p = lambda t: None if t is None else int(t.data_ptr())
-        B.msa_projection_forward(
-            cfg, n, p(self.codes), self.codes.shape[1], self.codes.stride(0), p(self.weight), self.weight.stride(0),
-            B.MSA_DTYPE_FP8_E4M3, p(self.hidden_scales), p(self.weight_scales), p(positions), p(slots), p(page_table),
-            0 if page_table is None else page_table.numel(), *(p(w) for w in norms), p(q), p(iq), *caches, p(scales),
-            p(rows), 0 if rows is None else rows.stride(0), p(self.status), stream=stream.cuda_stream)
+        with B.on_device(self.weight.device):
+            B.msa_projection_forward(
+                cfg, n, p(self.codes), self.codes.shape[1], self.codes.stride(0), p(self.weight), self.weight.stride(0),
+                B.MSA_DTYPE_FP8_E4M3, p(self.hidden_scales), p(self.weight_scales), p(positions), p(slots),
+                p(page_table), 0 if page_table is None else page_table.numel(), *(p(w) for w in norms), p(q), p(iq),
+                *caches, p(scales), p(rows), 0 if rows is None else rows.stride(0), p(self.status),
+                stream=stream.cuda_stream)
 
     def run(self, x, residual, positions, slot_mapping, page_table, adapter_ids=None, launch_flags=0, stream=None):
         """For x and residual bf16 [T, K]: residual becomes their sum; q_out and idx_q_out [:T] and the

@@ -1,0 +1,131 @@
+"""The layer's input side on the host, with no GPU: on which device its calls run, and what it
+refuses.  The C entry points are stand-ins, and so are the tensors: they have a device, a shape
+and strides, and no memory."""
+import contextlib
+
+import pytest
+import torch
+
+from paged_kv_cache_msa_gb300 import binding as B
+from paged_kv_cache_msa_gb300.device import LayerInput
+
+DEV = torch.device("cuda", 1)
+
+
+class Tensor:
+    """A row-major tensor on a device that this machine need not have."""
+
+    def __init__(self, shape, dtype, device=DEV, strides=None, address=1 << 20):
+        self.shape, self.dtype, self.device, self.address = torch.Size(shape), dtype, torch.device(device), address
+        if strides is None:
+            strides = [1]
+            for n in reversed(shape[1:]):
+                strides.insert(0, strides[0] * n)
+            strides = strides[:len(shape)]
+        self.strides = tuple(strides)
+        self.is_cuda = self.device.type == "cuda"
+
+    def data_ptr(self):
+        return self.address
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self.strides if i is None else self.strides[i]
+
+    def numel(self):
+        return self.shape.numel()
+
+    def size(self, i):
+        return self.shape[i]
+
+    def is_contiguous(self):
+        return self.strides == Tensor(self.shape, self.dtype).strides or self.numel() == 0
+
+    def __getitem__(self, at):
+        at = at if isinstance(at, tuple) else (at,)
+        shape = [len(range(n)[s]) for n, s in zip(self.shape, at)] + list(self.shape[len(at):])
+        return Tensor(shape, self.dtype, self.device, self.strides, self.address)
+
+
+class Stream:
+    cuda_stream, device = 0, DEV
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """Two devices, of which 0 is current: the calls made, each with the device that was current."""
+    state = {"current": 0, "calls": []}
+
+    @contextlib.contextmanager
+    def device(d):
+        before, state["current"] = state["current"], torch.device(d).index
+        yield
+        state["current"] = before
+
+    def record(name):
+        def call(*a, **k):
+            state["calls"].append((name, state["current"]))
+            return B.MSA_OK
+        return call
+
+    make = lambda shape, dtype=torch.float32, device=None: Tensor(
+        (shape,) if isinstance(shape, int) else tuple(shape), dtype, device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["current"])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream())
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(torch, "zeros", make)
+    for name in ("msa_projection_forward", "msa_producer_forward"):
+        monkeypatch.setattr(B, name, record(name))
+    # (these set the device themselves, in the extension)
+    for name in ("norm_tensors", "adapter_tensors", "forward_axes_tensors"):
+        monkeypatch.setattr(B, name, record(name))
+    monkeypatch.setattr(B, "msa_adapter_workspace_bytes", lambda cfg, n: 4096)
+    return state
+
+
+BF16, F32, I32, I64, U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+D, K, T, RANK = 64, 256, 6, 16
+HEADS = (8, 2, 2, 2, 1)
+W = sum(HEADS) * D
+
+
+def cfg():
+    return B.make_cfg(8, 2, 2, 1, D, D // 2, B.MSA_ROPE_NEOX, 64)
+
+
+def layer(max_tokens=16, adapters=False, axes=False, **over):
+    a = dict(weight=Tensor((W, K), U8), weight_scales=Tensor((W,), F32), norm_w=Tensor((K,), BF16),
+             head_norms=[Tensor((D,), BF16)] * 4, caches=(None, None, None), scales=Tensor((3,), F32),
+             axes=B.make_rope_axes((4, 4, 8)) if axes else None,
+             adapters=(Tensor((3, 5 * RANK, K), BF16), Tensor((3, W, RANK), BF16), Tensor((3,), F32)) if adapters else None)
+    a.update(over)
+    return LayerInput(cfg(), max_tokens, **a)
+
+
+def run(lay, n=T, **over):
+    a = dict(x=Tensor((n, K), BF16), residual=Tensor((n, K), BF16),
+             positions=Tensor((3, n) if lay.axes is not None else (n,), I32), slot_mapping=Tensor((n,), I64),
+             page_table=Tensor((12,), I32), adapter_ids=Tensor((n,), I32) if lay.adapters is not None else None)
+    a.update(over)
+    lay.run(**a)
+
+
+@pytest.mark.parametrize("adapters", [False, True])
+@pytest.mark.parametrize("axes", [False, True])
+@pytest.mark.parametrize("stream", [None, Stream()], ids=["current", "given"])
+def test_calls_run_on_the_tensors_device(gpu, adapters, axes, stream):
+    run(layer(adapters=adapters, axes=axes), stream=stream)
+    raw = [c for c in gpu["calls"] if c[0] in ("msa_projection_forward", "msa_producer_forward")]
+    assert len(raw) == (1 if axes or not adapters else 2)
+    assert all(dev == 1 for _, dev in raw), raw
+    assert gpu["current"] == 0
+
+
+def test_producer_runs_on_the_rows_device(gpu):
+    q = Tensor((T, 8, D), BF16)
+    B.forward_tensors(cfg(), Tensor((T, W), BF16), Tensor((T,), I32), Tensor((T,), I64), None, (None,) * 4, q, q, None,
+                      None, None, None)
+    assert gpu["calls"] == [("msa_producer_forward", 1)] and gpu["current"] == 0

@@ -169,6 +169,22 @@ class DeviceProjection:
         return self.rows_out.cpu().numpy().view(np.uint16)
 
 
+def _checked(name, t, shape, kinds, dev, contiguous=True, optional=False):
+    """``t``, if it is a tensor of one of the dtypes ``kinds`` and of ``shape`` on ``dev`` (rows any
+    stride apart unless ``contiguous``), else a ValueError."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    rows = t.is_contiguous() if contiguous else t.dim() < 2 or t.stride(-1 % t.dim()) == 1 or t.shape[-1] < 2
+    if t.dtype not in kinds or tuple(t.shape) != tuple(shape) or not rows:
+        raise ValueError(f"{name}: expected a {'contiguous' if contiguous else 'unit column stride'} {kinds[0]} tensor of "
+                         f"shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    return t
+
+
 class LayerInput:
     """The input side of an MSA layer for up to ``max_tokens`` tokens: the residual's addition and
     the norm, which makes the projection's E4M3 operand with a scale for each token; the packed
@@ -180,15 +196,48 @@ class LayerInput:
     ``scales`` theirs.  ``axes``: an MsaRopeAxes for positions [num_axes, T], else positions are [T].
     ``adapters``: (down, up, adapter_scales) tensors as ``binding.adapter_tensors`` takes them, the
     slices being the row's sections.  Without adapters and axes the producer runs in the
-    projection's epilogue and the rows never leave the chip."""
+    projection's epilogue and the rows never leave the chip.
+
+    A layer keeps one set of buffers: its runs (and replays of graphs of them) follow one another.
+    Tensors that do not fit are a ValueError, before anything is enqueued."""
 
     def __init__(self, cfg: B.MsaProducerCfg, max_tokens: int, weight, weight_scales, norm_w, head_norms, caches, scales,
                  axes=None, adapters=None, rms_eps: float = 1e-6):
         import torch
-        W, K = weight.shape
+        bf16, e4m3, f32 = (torch.bfloat16, torch.int16), (torch.float8_e4m3fn, torch.uint8), (torch.float32,)
         dev, D = weight.device, cfg.head_dim
         sections = [cfg.num_q_heads, cfg.num_kv_heads, cfg.num_kv_heads, cfg.num_idx_q_heads, cfg.num_idx_k_heads]
-        assert W == sum(sections) * D and weight.stride(1) == 1
+        if dev.type != "cuda":
+            raise ValueError(f"weight is on {dev}; a layer takes CUDA tensors")
+        if weight.dim() != 2:
+            raise ValueError(f"weight: expected [W, K], got {tuple(weight.shape)}")
+        W, K = sum(sections) * D, weight.shape[1]
+        _checked("weight", weight, (W, K), e4m3, dev, contiguous=False)
+        if weight.data_ptr() % 16 or weight.stride(0) % 16 or weight.stride(0) < K:
+            raise ValueError(f"weight: 16-byte aligned rows, a stride that is a multiple of 16, got strides {weight.stride()}")
+        _checked("weight_scales", weight_scales, (W,), f32, dev, optional=True)
+        _checked("norm_w", norm_w, (K,), bf16, dev)
+        for name, w in zip(("q", "k", "idx_q", "idx_k"), head_norms, strict=True):
+            _checked(f"head_norms ({name})", w, (D,), bf16, dev, optional=True)
+        if scales is not None:
+            ns = 2 * cfg.num_kv_heads + cfg.num_idx_k_heads if cfg.scale_mode == B.MSA_SCALE_PER_HEAD else 3
+            if scales.dim() != 1 or scales.shape[0] < ns:
+                raise ValueError(f"scales: expected at least {ns} values, got shape {tuple(scales.shape)}")
+            _checked("scales", scales, scales.shape, f32, dev)
+        if adapters is not None:
+            down, up, adapter_scales = adapters
+            if up.dim() != 3 or down.dim() != 3:
+                raise ValueError(f"adapters: expected down [n, slices * rank, K] and up [n, W, rank], got "
+                                 f"{tuple(down.shape)} and {tuple(up.shape)}")
+            n, rank, slices = up.shape[0], up.shape[2], sum(heads > 0 for heads in sections)
+            _checked("adapters (up)", up, (n, W, rank), bf16, dev)
+            _checked("adapters (down)", down, (n, slices * rank, K), bf16, dev, contiguous=False)
+            if n > 1 and down.stride(0) != slices * rank * down.stride(1) or down.stride(1) % 8 or down.stride(1) < K or \
+                    down.data_ptr() % 16:
+                raise ValueError(f"adapters (down): 16-byte aligned rows one stride apart, a multiple of 8, got strides "
+                                 f"{down.stride()}")
+            _checked("adapters (scales)", adapter_scales, (n,), f32, dev, optional=True)
+        self.max_tokens = max_tokens
         self.cfg, self.weight, self.weight_scales, self.norm_w = cfg, weight, weight_scales, norm_w
         self.head_norms, self.caches, self.scales, self.axes, self.adapters = head_norms, caches, scales, axes, adapters
         self.norm_cfg = B.make_norm_cfg(K, rms_eps)
@@ -220,10 +269,32 @@ class LayerInput:
                 stream=stream.cuda_stream)
 
     def run(self, x, residual, positions, slot_mapping, page_table, adapter_ids=None, launch_flags=0, stream=None):
-        """For x and residual bf16 [T, K]: residual becomes their sum; q_out and idx_q_out [:T] and the
-        caches are written.  adapter_ids int32 [T] (with adapters); launch_flags: the producer's."""
+        """For x and residual bf16 [T, K], T at most max_tokens: residual becomes their sum; q_out and
+        idx_q_out [:T] and the caches are written.  positions int32, slot_mapping int64 [T],
+        page_table int32 or None; adapter_ids int32 [T] with adapters, else None; launch_flags: the
+        producer's, where it is a launch of its own (with axes or adapters)."""
         import torch
-        n = x.shape[0]
+        if x.dim() != 2:
+            raise ValueError(f"x: expected [T, K], got {tuple(x.shape)}")
+        n, dev, i32 = x.shape[0], self.weight.device, (torch.int32,)
+        if n > self.max_tokens:
+            raise ValueError(f"{n} tokens; the layer was made for {self.max_tokens}")
+        if self.axes is None:
+            _checked("positions", positions, (n,), i32, dev)
+        else:
+            axes = self.axes.num_axes
+            _checked("positions", positions, (axes, n), i32, dev, contiguous=False)
+            if axes > 1 and n > 0 and positions.stride(0) < n:
+                raise ValueError(f"positions: {n} tokens an axis, axes {positions.stride(0)} apart")
+        _checked("slot_mapping", slot_mapping, (n,), (torch.int64,), dev)
+        if page_table is not None:
+            _checked("page_table", page_table, page_table.shape, i32, dev)
+        if self.adapters is not None:
+            _checked("adapter_ids", adapter_ids, (n,), i32, dev)
+        elif adapter_ids is not None:
+            raise ValueError("adapter_ids for a layer without adapters")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"a stream of {stream.device}, tensors on {dev}")
         if stream is None:
             stream = torch.cuda.current_stream(x.device)
         codes, hidden_scales = self.codes[:n], self.hidden_scales[:n]
@@ -248,6 +319,17 @@ class LayerInput:
             B.forward_tensors(self.cfg, *args)
         else:
             B.forward_axes_tensors(self.cfg, self.axes, *args)
+
+    def check_status(self, stream=None):
+        """Waits for the runs on ``stream`` (the current one) and raises a RuntimeError if a wait inside
+        their projections has run out since the last call of this (a failure of the hardware, never
+        expected): what those runs wrote is then incomplete."""
+        import torch
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.weight.device)):
+            bits = int(self.status.item())
+            self.status.zero_()
+        if bits:
+            raise RuntimeError(f"a projection did not finish (status {bits:#x})")
 
 
 class DecodeLayer:

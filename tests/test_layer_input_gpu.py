@@ -255,3 +255,40 @@ def test_two_layers_at_once():
     assert not errors, errors
     for layer, begin in zip(layers, start):
         layer.check(before=begin)
+
+
+def test_refused_runs_leave_everything_as_it_was():
+    layer = Layer(20, TINY, 512, 16)
+    c = layer.case
+    state = [layer.residual, layer.layer.codes, layer.layer.rows, layer.layer.q_out, *c.pools]
+    before = [t.clone() for t in state]
+    good = dict(x=layer.x, residual=layer.residual, positions=c.positions, slot_mapping=c.slots, page_table=c.table,
+                adapter_ids=layer.ids)
+    for bad in (dict(positions=c.positions.long()), dict(slot_mapping=c.slots.int()), dict(adapter_ids=layer.ids.long()),
+                dict(page_table=c.table.long()), dict(adapter_ids=None), dict(x=layer.x[:19]), dict(residual=layer.residual.float())):
+        with pytest.raises(ValueError):
+            layer.layer.run(**dict(good, **bad))
+    torch.cuda.synchronize()
+    for t, b in zip(state, before):
+        assert torch.equal(t.view(torch.uint8), b.view(torch.uint8))
+    layer.run().check()
+
+
+def test_a_projection_that_did_not_finish_is_reported():
+    """In the starved test build no copy is issued and the projection's waits run out."""
+    layer = Layer(20, TINY, 512, 16)
+    normal = B._lib
+    start = layer.residual.clone()
+    B._lib = B.load(build_mod.build_starved())
+    try:
+        layer.run()
+        with pytest.raises(RuntimeError, match="did not finish"):
+            layer.layer.check_status()
+    finally:
+        B._lib = normal
+    layer.residual.copy_(start)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    layer.run(stream=s)
+    layer.layer.check_status(s)
+    layer.check()

@@ -96,11 +96,11 @@ def cfg():
     return B.make_cfg(8, 2, 2, 1, D, D // 2, B.MSA_ROPE_NEOX, 64)
 
 
-def layer(max_tokens=16, adapters=False, axes=False, **over):
+def layer(max_tokens=16, with_adapters=False, with_axes=False, **over):
     a = dict(weight=Tensor((W, K), U8), weight_scales=Tensor((W,), F32), norm_w=Tensor((K,), BF16),
              head_norms=[Tensor((D,), BF16)] * 4, caches=(None, None, None), scales=Tensor((3,), F32),
-             axes=B.make_rope_axes((4, 4, 8)) if axes else None,
-             adapters=(Tensor((3, 5 * RANK, K), BF16), Tensor((3, W, RANK), BF16), Tensor((3,), F32)) if adapters else None)
+             axes=B.make_rope_axes((4, 4, 8)) if with_axes else None,
+             adapters=(Tensor((3, 5 * RANK, K), BF16), Tensor((3, W, RANK), BF16), Tensor((3,), F32)) if with_adapters else None)
     a.update(over)
     return LayerInput(cfg(), max_tokens, **a)
 
@@ -117,7 +117,7 @@ def run(lay, n=T, **over):
 @pytest.mark.parametrize("axes", [False, True])
 @pytest.mark.parametrize("stream", [None, Stream()], ids=["current", "given"])
 def test_calls_run_on_the_tensors_device(gpu, adapters, axes, stream):
-    run(layer(adapters=adapters, axes=axes), stream=stream)
+    run(layer(with_adapters=adapters, with_axes=axes), stream=stream)
     raw = [c for c in gpu["calls"] if c[0] in ("msa_projection_forward", "msa_producer_forward")]
     assert len(raw) == (1 if axes or not adapters else 2)
     assert all(dev == 1 for _, dev in raw), raw
@@ -129,3 +129,63 @@ def test_producer_runs_on_the_rows_device(gpu):
     B.forward_tensors(cfg(), Tensor((T, W), BF16), Tensor((T,), I32), Tensor((T,), I64), None, (None,) * 4, q, q, None,
                       None, None, None)
     assert gpu["calls"] == [("msa_producer_forward", 1)] and gpu["current"] == 0
+
+
+@pytest.mark.parametrize("over", [
+    dict(weight=Tensor((W, K), BF16)), dict(weight=Tensor((W - D, K), U8)), dict(weight=Tensor((W, K), U8, "cpu")),
+    dict(weight=Tensor((W * K,), U8)), dict(weight=Tensor((W, K), U8, strides=(1, W))),
+    dict(weight=Tensor((W, K), U8, strides=(K + 8, 1))), dict(weight=Tensor((W, K), U8, address=(1 << 20) + 8)),
+    dict(weight_scales=Tensor((W,), BF16)), dict(weight_scales=Tensor((W - 1,), F32)),
+    dict(weight_scales=Tensor((W,), F32, "cuda:0")), dict(weight_scales=Tensor((W,), F32, strides=(2,))),
+    dict(norm_w=Tensor((K + 1,), BF16)), dict(norm_w=Tensor((K,), F32)), dict(norm_w=None),
+    dict(head_norms=[Tensor((D,), BF16)] * 3), dict(head_norms=[Tensor((D,), F32)] * 4),
+    dict(head_norms=[None, None, None, Tensor((D // 2,), BF16)]), dict(scales=Tensor((2,), F32)),
+    dict(scales=Tensor((3,), torch.float64)), dict(scales=Tensor((1, 3), F32)), dict(scales=Tensor((3,), F32, "cpu")),
+    dict(adapters=(Tensor((3, 5 * RANK, K), BF16), Tensor((3, W, RANK), F32), None)),
+    dict(adapters=(Tensor((3, 4 * RANK, K), BF16), Tensor((3, W, RANK), BF16), None)),
+    dict(adapters=(Tensor((2, 5 * RANK, K), BF16), Tensor((3, W, RANK), BF16), None)),
+    dict(adapters=(Tensor((3, 5 * RANK, K), BF16), Tensor((3, W, RANK), BF16), Tensor((2,), F32))),
+    dict(adapters=(Tensor((3, 5 * RANK, K), BF16, strides=(5 * RANK * K + 8, K, 1)), Tensor((3, W, RANK), BF16), None)),
+    dict(adapters=(Tensor((3, 5 * RANK, K), BF16, strides=(5 * RANK * (K + 4), K + 4, 1)), Tensor((3, W, RANK), BF16), None)),
+    dict(adapters=(Tensor((5 * RANK, K), BF16), Tensor((W, RANK), BF16), None)),
+], ids=lambda o: next(iter(o)))
+def test_a_layers_tensors_that_do_not_fit(gpu, over):
+    with pytest.raises(ValueError):
+        layer(**over)
+
+
+@pytest.mark.parametrize("axes", [False, True])
+@pytest.mark.parametrize("over", [
+    dict(positions=Tensor((T,), I64)), dict(positions=Tensor((3, T), I64)), dict(positions=Tensor((T - 1,), I32)),
+    dict(positions=Tensor((2, T), I32)), dict(positions=Tensor((3, T), I32, strides=(1, 3))),
+    dict(positions=Tensor((3, T), I32, strides=(0, 1))), dict(positions=Tensor((T,), I32, strides=(2,))),
+    dict(positions=Tensor((T,), I32, "cpu")), dict(positions=None), dict(slot_mapping=Tensor((T,), I32)),
+    dict(slot_mapping=Tensor((T + 1,), I64)), dict(slot_mapping=Tensor((T,), I64, "cuda:0")), dict(slot_mapping=None),
+    dict(slot_mapping=Tensor((T,), I64, strides=(2,))), dict(page_table=Tensor((12,), I64)),
+    dict(page_table=Tensor((12,), I32, strides=(2,))), dict(page_table=Tensor((12,), I32, "cpu")),
+    dict(adapter_ids=Tensor((T,), I64)), dict(adapter_ids=Tensor((T - 1,), I32)), dict(adapter_ids=None),
+    dict(x=Tensor((K,), BF16)), dict(stream=type("Other", (), dict(cuda_stream=0, device=torch.device("cuda", 0)))()),
+], ids=lambda o: next(iter(o)))
+def test_a_runs_tensors_that_do_not_fit(gpu, axes, over):
+    """Refused before the first call, which adds to the residual where it is."""
+    lay = layer(with_adapters=True, with_axes=axes)
+    with pytest.raises(ValueError):
+        run(lay, **over)
+    assert gpu["calls"] == []
+
+
+def test_more_tokens_than_the_layers(gpu):
+    with pytest.raises(ValueError):
+        run(layer(max_tokens=5))
+    with pytest.raises(ValueError):
+        run(layer(), adapter_ids=Tensor((T,), I32))         # no adapters
+    assert gpu["calls"] == []
+
+
+def test_tensors_that_do_fit(gpu):
+    """Raw words in the place of 8- and 16-bit floats, rows and axes further apart, optional tensors left out."""
+    run(layer(with_adapters=True, with_axes=True, weight=Tensor((W, K), torch.float8_e4m3fn, strides=(K + 16, 1)), weight_scales=None,
+              norm_w=Tensor((K,), torch.int16), head_norms=[None] * 4, scales=Tensor((9,), F32)),
+        positions=Tensor((3, T), I32, strides=(T + 5, 1)), page_table=None)
+    run(layer(scales=None), n=1, page_table=Tensor((3, 4), I32))
+    run(layer(with_axes=True), n=0)

@@ -41,13 +41,14 @@ extern "C" {
 #define MSA_ADAPTER_MAX_SLICES 8
 
 typedef struct {
-    int32_t hidden_size;    /* K >= 1 */
+    int32_t hidden_size;    /* K: 1..2^30 */
     int32_t rank;           /* a multiple of 8, 8..128 */
     int32_t num_adapters;   /* 1..16384 */
     int32_t hidden_dtype;   /* msa_dtype of hidden: bf16 or E4M3 */
     int32_t num_slices;     /* 1..MSA_ADAPTER_MAX_SLICES; num_slices * rank <= 512 */
     int32_t slice_end[MSA_ADAPTER_MAX_SLICES]; /* ascending; all but the last multiples of 64,
-                               the last (the width W) a multiple of 8; then 0 */
+                               the last (the width W) a multiple of 8, at most
+                               2^30; then 0 */
     int32_t reserved[3];    /* must be 0 */
 } msa_adapter_cfg;
 

@@ -750,6 +750,7 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) msa_adapter_up_stream_ke
 // ---------------------------------------------------------------------------
 
 constexpr int64_t kMaxTokens = 1 << 24;
+constexpr int32_t kMaxSize = 1 << 30;    // of K and W: a tile or a chunk more is an int32 too
 
 msa_status fail(msa_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 msa_status fail(msa_status s, const char *fmt, ...)
@@ -770,6 +771,8 @@ msa_status check_cfg(const msa_adapter_cfg *cfg, int64_t T)
         return fail(MSA_ERR_INVALID_ARGUMENT, "cfg is NULL");
     if (cfg->hidden_size < 1)
         return fail(MSA_ERR_INVALID_ARGUMENT, "hidden_size %d", cfg->hidden_size);
+    if (cfg->hidden_size > kMaxSize)
+        return fail(MSA_ERR_UNSUPPORTED, "hidden_size %d (at most 2^30)", cfg->hidden_size);
     if (cfg->rank < 1)
         return fail(MSA_ERR_INVALID_ARGUMENT, "rank %d", cfg->rank);
     if (cfg->rank % 8 || cfg->rank > 128)
@@ -790,6 +793,8 @@ msa_status check_cfg(const msa_adapter_cfg *cfg, int64_t T)
             return fail(MSA_ERR_INVALID_ARGUMENT, "slice_end[%d] is %d", s, end);
         if (end % (last ? 8 : 64))
             return fail(MSA_ERR_UNSUPPORTED, "slice_end[%d] is %d (a multiple of %d)", s, end, last ? 8 : 64);
+        if (end > kMaxSize)
+            return fail(MSA_ERR_UNSUPPORTED, "slice_end[%d] is %d (at most 2^30)", s, end);
     }
     for (int i = 0; i < 3; ++i)
         if (cfg->reserved[i] != 0)

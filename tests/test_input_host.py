@@ -251,3 +251,17 @@ def test_tensor_functions_take_cuda_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         B.forward_axes_tensors(B.make_cfg(1, 0, 0, 0, 64), good_axes(), x, ids, ids, None, (None,) * 4, x, None, None,
                                None, None, None)
+
+
+def test_adapter_sizes_are_bounded():
+    """Sizes up to 2^30 are taken (here up to the workspace, which is too small), larger ones refused:
+    a tile of K or a chunk of W more would pass 32 bits."""
+    most, wide = 2**30, dict.fromkeys(("hidden_stride", "down_stride", "rows_stride", "out_stride"), 2**31)
+    for cfg in (adapter_cfg(hidden_size=most), adapter_cfg(slice_ends=[64, most]), adapter_cfg(slice_ends=[most])):
+        assert B.msa_adapter_workspace_bytes(cfg, 16) > 0
+        assert adapter(cfg=cfg, workspace_bytes=16, **wide) == INVALID and "workspace" in B.last_error_detail()
+    for cfg in (adapter_cfg(hidden_size=most + 1), adapter_cfg(hidden_size=2**31 - 1), adapter_cfg(slice_ends=[64, most + 8]),
+                adapter_cfg(slice_ends=[2**31 - 8]), adapter_cfg(slice_ends=[most + 64, most + 128])):
+        assert adapter(cfg=cfg, **wide) == UNSUPPORTED, B.last_error_detail()
+        with pytest.raises(B.MsaError):
+            B.msa_adapter_workspace_bytes(cfg, 16)

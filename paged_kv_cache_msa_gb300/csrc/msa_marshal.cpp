@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstdint>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -168,6 +169,8 @@ int flags_of(PyObject *o)
     const long v = PyLong_AsLong(o);
     if (v == -1 && PyErr_Occurred())
         throw PythonError();
+    if (v < INT32_MIN || v > INT32_MAX)
+        throw BadArgument("launch_flags: " + std::to_string(v));
     return (int)v;
 }
 

@@ -207,3 +207,16 @@ def test_tensors_that_do_not_fit_are_refused():
         B.norm_tensors(cfg, x, w[:63], **good)
     with pytest.raises(B.MsaError):
         B.norm_tensors(cfg, x, w)
+
+
+def test_flags_that_are_no_flags():
+    """Also those whose low 32 bits are."""
+    cfg, x, w = B.make_norm_cfg(64), make(4, 64), make(1, 64)[0].contiguous()
+    out = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    for flags in (2**32, 2**32 + B.MSA_LAUNCH_PDL, 2**31, -2**32, 2**40):
+        with pytest.raises(ValueError):
+            B.norm_tensors(cfg, x, w, out=out, launch_flags=flags)
+    for flags in (64, -1):
+        with pytest.raises(B.MsaError):
+            B.norm_tensors(cfg, x, w, out=out, launch_flags=flags)
+    assert (out == 0).all()

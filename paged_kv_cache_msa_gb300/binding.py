@@ -762,8 +762,8 @@ def _marshaller():
         import torch  # noqa: F401  (its libraries, which the extension links to)
         path = _build.MARSHAL_PATH
         if not os.path.exists(path):
-            raise RuntimeError(f"the extension is not built ({path}); build it with "
-                               "`python -m paged_kv_cache_msa_gb300.build`")
+            raise RuntimeError(f"the extension is not built ({path}): " + (_build.marshal_missing() or "build it with "
+                               "`python -m paged_kv_cache_msa_gb300.build`"))
         spec = importlib.util.spec_from_file_location("msa_marshal", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -132,8 +132,33 @@ def marshal_digest() -> str:
     return h.hexdigest()
 
 
+def marshal_missing() -> str | None:
+    """What the extension would need and this machine lacks; None where it can be built.  The
+    library and its C entry points need none of it."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return "torch is not installed"
+    if torch.version.cuda is None:
+        return "torch is built without CUDA"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers are not installed"
+    return None
+
+
+def _remove(*paths) -> None:
+    for path in paths:
+        if os.path.exists(path):
+            os.remove(path)
+
+
 def _start_marshal(force: bool):
-    """Starts the extension's compiler unless it is up to date; finish with _finish_marshal."""
+    """Starts the extension's compiler unless it is up to date or cannot be built here (then none is
+    left from before); finish with _finish_marshal or _stop_marshal."""
+    if marshal_missing():
+        _remove(MARSHAL_PATH, MARSHAL_PATH + ".sha256")
+        return None
     digest = marshal_digest()
     if not force and _fresh(MARSHAL_PATH, MARSHAL_PATH + ".sha256", digest):
         return None
@@ -149,10 +174,20 @@ def _finish_marshal(job) -> None:
     tmp, digest, cmd, proc = job
     out, _ = proc.communicate()
     if proc.returncode != 0:
+        _remove(tmp)
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + out)
     os.replace(tmp, MARSHAL_PATH)
     with open(MARSHAL_PATH + ".sha256", "w") as f:
         f.write(digest)
+
+
+def _stop_marshal(job) -> None:
+    if job is None:
+        return
+    tmp, _, _, proc = job
+    proc.kill()
+    proc.communicate()
+    _remove(tmp)
 
 
 def _compile(lib: str, stamp: str, digest: str, extra, verbose: bool = False,
@@ -201,18 +236,20 @@ def build(force: bool = False, verbose: bool = False, defines=None) -> str:
     and defines (a content hash, see ``source_digest``); returns its path.
     ``defines``: extra -D tuning macros (e.g. MSA_MIN_CTAS_PER_SM=4); by default the
     space-separated list in the MSA_BUILD_DEFINES environment variable (empty: the
-    tuned defaults).  With MSA_NO_BUILD=1 an existing library is used as it is."""
+    tuned defaults).  The extension for torch callers is left out where marshal_missing()
+    says so.  With MSA_NO_BUILD=1 an existing library is used as it is."""
     if defines is None:
         defines = tuple(os.environ.get("MSA_BUILD_DEFINES", "").split())
     if os.environ.get("MSA_NO_BUILD") == "1" and os.path.exists(LIB_PATH):
         return LIB_PATH
     digest = source_digest(defines)
+    job = _start_marshal(force)
     try:
-        job = _start_marshal(force)
-    except ImportError:              # without torch there is nothing to marshal
-        job = None
-    if force or not _fresh(LIB_PATH, STAMP_PATH, digest):
-        _compile(LIB_PATH, STAMP_PATH, digest, [f"-D{d}" for d in defines], verbose)
+        if force or not _fresh(LIB_PATH, STAMP_PATH, digest):
+            _compile(LIB_PATH, STAMP_PATH, digest, [f"-D{d}" for d in defines], verbose)
+    except BaseException:
+        _stop_marshal(job)
+        raise
     _finish_marshal(job)
     return LIB_PATH
 

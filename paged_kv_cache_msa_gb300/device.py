@@ -195,14 +195,16 @@ class LayerInput:
     the layer's norm, ``head_norms`` the producer's four, ``caches`` its (k, v, idx_k) MsaCacheDesc,
     ``scales`` theirs.  ``axes``: an MsaRopeAxes for positions [num_axes, T], else positions are [T].
     ``adapters``: (down, up, adapter_scales) tensors as ``binding.adapter_tensors`` takes them, the
-    slices being the row's sections.  Without adapters and axes the producer runs in the
+    slices being the row's sections.  ``adapter_hidden``: the MSA_DTYPE of the hidden states that the
+    adapters read, the projection's E4M3 operand or bf16 rows, which the norm then writes beside it (2
+    bytes an element more; the layer's ``hidden``).  Without adapters and axes the producer runs in the
     projection's epilogue and the rows never leave the chip.
 
     A layer keeps one set of buffers: its runs (and replays of graphs of them) follow one another.
     Tensors that do not fit are a ValueError, before anything is enqueued."""
 
     def __init__(self, cfg: B.MsaProducerCfg, max_tokens: int, weight, weight_scales, norm_w, head_norms, caches, scales,
-                 axes=None, adapters=None, rms_eps: float = 1e-6):
+                 axes=None, adapters=None, rms_eps: float = 1e-6, adapter_hidden: int = B.MSA_DTYPE_FP8_E4M3):
         import torch
         bf16, e4m3, f32 = (torch.bfloat16, torch.int16), (torch.float8_e4m3fn, torch.uint8), (torch.float32,)
         dev, D = weight.device, cfg.head_dim
@@ -237,6 +239,8 @@ class LayerInput:
                 raise ValueError(f"adapters (down): 16-byte aligned rows one stride apart, a multiple of 8, got strides "
                                  f"{down.stride()}")
             _checked("adapters (scales)", adapter_scales, (n,), f32, dev, optional=True)
+        if adapter_hidden not in (B.MSA_DTYPE_FP8_E4M3, B.MSA_DTYPE_BF16):
+            raise ValueError(f"adapter_hidden: {adapter_hidden}")
         self.max_tokens = max_tokens
         self.cfg, self.weight, self.weight_scales, self.norm_w = cfg, weight, weight_scales, norm_w
         self.head_norms, self.caches, self.scales, self.axes, self.adapters = head_norms, caches, scales, axes, adapters
@@ -246,6 +250,9 @@ class LayerInput:
         self.q_out = torch.empty((max_tokens, cfg.num_q_heads, D), dtype=torch.bfloat16, device=dev)
         self.idx_q_out = torch.empty((max_tokens, cfg.num_idx_q_heads, D), dtype=torch.bfloat16, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.hidden = None
+        if adapters is not None and adapter_hidden == B.MSA_DTYPE_BF16:
+            self.hidden = torch.empty((max_tokens, -(-K // 8) * 8), dtype=torch.bfloat16, device=dev)[:, :K]
         self.rows = None
         if axes is not None or adapters is not None:
             self.rows = torch.empty((max_tokens, W), dtype=torch.bfloat16, device=dev)
@@ -254,7 +261,7 @@ class LayerInput:
         if adapters is not None:
             down, up, _ = adapters
             ends = [sum(sections[:i + 1]) * D for i, n in enumerate(sections) if n > 0]
-            self.adapter_cfg = B.make_adapter_cfg(K, ends, up.shape[2], up.shape[0], B.MSA_DTYPE_FP8_E4M3)
+            self.adapter_cfg = B.make_adapter_cfg(K, ends, up.shape[2], up.shape[0], adapter_hidden)
             nbytes = B.msa_adapter_workspace_bytes(self.adapter_cfg, max_tokens)
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
@@ -299,7 +306,8 @@ class LayerInput:
             stream = torch.cuda.current_stream(x.device)
         codes, hidden_scales = self.codes[:n], self.hidden_scales[:n]
         q, iq = self.q_out[:n], self.idx_q_out[:n]
-        B.norm_tensors(self.norm_cfg, x, self.norm_w, residual=residual, residual_out=residual, codes=codes,
+        hidden = None if self.hidden is None else self.hidden[:n]
+        B.norm_tensors(self.norm_cfg, x, self.norm_w, residual=residual, residual_out=residual, out=hidden, codes=codes,
                        scales=hidden_scales, stream=stream)
         if self.rows is None:
             self._project(self.cfg, n, positions, slot_mapping, page_table, self.head_norms, q, iq, self.caches,
@@ -311,7 +319,8 @@ class LayerInput:
                       stream)
         if self.adapters is not None:
             down, up, adapter_scales = self.adapters
-            B.adapter_tensors(self.adapter_cfg, codes, down, up, adapter_ids, rows, rows, hidden_scales=hidden_scales,
+            of, of_scales = (codes, hidden_scales) if hidden is None else (hidden, None)
+            B.adapter_tensors(self.adapter_cfg, of, down, up, adapter_ids, rows, rows, hidden_scales=of_scales,
                               adapter_scales=adapter_scales, workspace=self.workspace, stream=stream)
         args = (rows, positions, slot_mapping, page_table, self.head_norms, q, iq, *self.caches, self.scales,
                 launch_flags, stream)

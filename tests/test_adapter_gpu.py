@@ -508,3 +508,46 @@ def test_all_bits_of_u(rank, t, fp8):
     B.adapter_tensors(cfg, hidden, down.bfloat16(), up.bfloat16(), torch.zeros(t, dtype=torch.int32, device="cuda"), rows, out)
     last = pieces * (pair + (per * (col >= 64) if slices == 2 else 0)) + pieces - 1
     assert torch.equal(out.double(), x[:, last].double() * 2.0 ** (-bits * (pieces - 1)))
+
+
+@pytest.mark.parametrize("t", [2, 64, 300, 1300])
+@pytest.mark.parametrize("graph", [False, True])
+def test_everything_made_by_the_kernel_just_ahead(t, graph):
+    """Rows, ids, hidden states and the adapters themselves, written by copies right ahead of each call and
+    other ones for each: the bits of the same calls with the device idle in between."""
+    steps = 8
+    c = Case(mixed(t, 4), k=1000, rank=64, adapters=4)
+    gen = torch.Generator(device="cuda").manual_seed(t)
+    pick = [torch.randint(-1, 5, (t,), generator=gen, device="cuda").int() for _ in range(steps)]
+    turn = lambda x, i: x.roll(i + 1, 0)
+    made = [(turn(c.rows, i).contiguous(), turn(c.hidden, i).contiguous(), turn(c.up, i).contiguous(),
+             turn(c.down, i).contiguous()) for i in range(steps)]
+    outs = [torch.zeros_like(c.rows) for _ in range(steps)]
+
+    def run(idle):
+        for i in range(steps):
+            rows, hidden, up, down = made[i]
+            # (the last copy ahead of the call is another one each time)
+            copies = [(c.ids, pick[i]), (c.rows, rows), (c.up, up), (c.down, down), (c.hidden, hidden)]
+            for j in range(len(copies)):
+                to, of = copies[(j + i) % len(copies)]
+                to.copy_(of)
+            if idle:
+                torch.cuda.synchronize()
+            c.run(out=outs[i])
+            if idle:
+                torch.cuda.synchronize()
+
+    run(True)
+    want = [o.clone() for o in outs]
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(False)
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        g.replay() if graph else run(False)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o.view(torch.int16), w.view(torch.int16))

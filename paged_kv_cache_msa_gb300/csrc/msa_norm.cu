@@ -28,8 +28,9 @@ namespace {
 
 constexpr int kMaxHidden = 16384;
 constexpr int kMaxVecs = 7;                 // vectors of 8 elements a thread
-// Registers of a thread that has V vectors, and the warps of it that an SM holds.
-constexpr int kRegs[kMaxVecs + 1] = {0, 64, 64, 64, 80, 96, 112, 128};
+// Registers of a thread that has V vectors, and the warps of it that an SM holds.  (Six vectors, of 112
+// registers, never have most in flight: no row takes them.)
+constexpr int kRegs[kMaxVecs + 1] = {0, 64, 64, 64, 80, 96, 0, 128};
 constexpr int warps_of(int v) { return 16384 / (32 * kRegs[v]) * 4; }
 constexpr int kWarpRows = 8;                // rows of one warp each share a CTA
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
@@ -374,25 +375,27 @@ extern "C" msa_status msa_norm_forward(const msa_norm_cfg *cfg, int64_t num_toke
     // Vectors of a thread.  Rows whose warps fit onto the GPU twice with one vector each: one, since
     // the chain of a row is what takes time (one token of 6,144 2.4 us; 777 of 1,001 2.45 us, 2.95 with
     // four).  Otherwise those with which an SM has most vectors in flight, whole rows of its resident
-    // warps: 8,192 x 6,144 takes 55.5 us with three (3,072 vectors an SM), 58.6 with four, of 80
-    // registers (3,072 too), 60.4 with three of 73 (2,304); rows of 1,536 run at 0.99 of the copy rate
-    // with three each and at 0.59 with one.
-    int v = 1;
+    // warps: 8,192 x 6,144 takes 55.5 us with three, 58.6 with four, of 80 registers (as many in flight),
+    // 60.4 with three of 73 registers (three quarters as many); rows of 1,536 run at 0.99 of the copy
+    // rate with three each and at 0.59 with one.
+    using Kernel = void (*)(Params);
+    struct Choice { int vecs; Kernel kernel; };
+    static const Choice choices[] = {{1, msa_norm_kernel<1>}, {2, msa_norm_kernel<2>}, {3, msa_norm_kernel<3>},
+                                     {4, msa_norm_kernel<4>}, {5, msa_norm_kernel<5>}, {7, msa_norm_kernel<7>}};
+    Choice chosen = choices[0];
     if (p.vecs > 1024 || num_tokens * ((p.vecs + 31) / 32) > 2 * 152 * warps_of(1)) {
         int best = 0;
-        for (int i = 1; i <= kMaxVecs; ++i) {
-            const int wpr = (p.vecs + 32 * i - 1) / (32 * i), flying = warps_of(i) / wpr * p.vecs;
+        for (const Choice &c : choices) {
+            const int wpr = (p.vecs + 32 * c.vecs - 1) / (32 * c.vecs), flying = warps_of(c.vecs) / wpr * p.vecs;
             if (flying > best) {
                 best = flying;
-                v = i;
+                chosen = c;
             }
         }
     }
+    const int v = chosen.vecs;
     p.threads_per_row = ((p.vecs + v - 1) / v + 31) / 32 * 32;
     const int rows = p.threads_per_row == 32 ? kWarpRows : 1;
-    using Kernel = void (*)(Params);
-    static const Kernel kernels[kMaxVecs] = {msa_norm_kernel<1>, msa_norm_kernel<2>, msa_norm_kernel<3>, msa_norm_kernel<4>,
-                                             msa_norm_kernel<5>, msa_norm_kernel<6>, msa_norm_kernel<7>};
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);
     lc.gridDim = dim3((unsigned)((num_tokens + rows - 1) / rows));
@@ -404,7 +407,7 @@ extern "C" msa_status msa_norm_forward(const msa_norm_cfg *cfg, int64_t num_toke
     lc.attrs = attr;
     lc.numAttrs = 1;
     void *args[] = {&p};
-    const cudaError_t e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(kernels[v - 1]), args);
+    const cudaError_t e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(chosen.kernel), args);
     if (e != cudaSuccess)
         return fail(MSA_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
     return MSA_OK;

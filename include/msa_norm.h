@@ -9,12 +9,14 @@
  *     residual_out    = bf16_rne(h)
  *     y[j]            = h[j] * weight[j] / sqrt(sum_j h[j]^2 / K + rms_eps)
  *     out             = bf16_rne(y)
- *     scales[t]       = max(max_j |y[j]|, 2^-100) / 448
- *     codes           = e4m3_rne(y / scales[t])
+ *     scales[t]       = max(max_j |y[j]|, 2^-100) * (1 / 448)
+ *     codes           = e4m3_rne(y * (1 / scales[t]))
  *
  * codes and scales are an E4M3 operand of msa_projection_forward (hidden and
  * hidden_scales).  The norm is taken of h before its rounding to bf16.  Arithmetic is
- * fp32; a row whose sum of squares leaves the range of fp32 is scaled by a power of two
+ * fp32, the two reciprocals among it: a quotient is right to 2^-22, so that a code as near to
+ * a tie may be its neighbour.  y is (h * weight) times the reciprocal root: h * weight has to be in
+ * the range of fp32.  A row whose sum of squares leaves that range is scaled by a power of two
  * first, so its norm is right too.  A row that holds a NaN or an infinity gets the scale
  * NaN (and out as the formula gives it); a row of zeros with rms_eps 0 gives NaN.
  *

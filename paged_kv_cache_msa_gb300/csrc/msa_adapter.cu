@@ -2,7 +2,7 @@
 //
 // Up to three kernels:
 //   sort   the tokens by adapter, in tiles of 16 or 128 of one adapter each (up to 128 tokens are
-//          put into tiles by every CTA of the next kernels: 64 tokens over 48 adapters take 18.1 us,
+//          put into tiles by every CTA of the next kernels: 64 tokens over 48 adapters took 18.1 us,
 //          1.1 more with the sort, 64 over 3 adapters 8.5 and 1.7 more, 128 over 3 10.1 and 0.5).  Reading
 //          an adapter costs more than anything else in a decode batch, and in no order of the tokens
 //          is it read more often than once a tile: 512 tokens over 16 adapters, mixed, took 100 us
@@ -15,7 +15,7 @@
 // tokens over 48 adapters of rank 16), reading and writing the rows a prefill: both HBM.  One
 // kernel in the place of two, clusters of 8 or 16 CTAs that share a tile's K and join its sums
 // through distributed shared memory, took 9.5 us for one token and 31.7 for those 64 (5.6 and
-// 18.1): fewer warps read a tile, in rounds of loads that wait 2 us each.
+// 18.7): fewer warps read a tile, in rounds of loads that wait 2 us each.
 
 #include "msa_adapter_internal.h"
 
@@ -635,7 +635,8 @@ __global__ void __launch_bounds__(128, RC <= 2 ? 4 : 2) msa_adapter_up_kernel(co
 // at the copy rate).  A CTA takes a tile and `chunk` columns, a warp 16 of its tokens.  The
 // adapter's rows of up and the tokens' rows go through shared memory, kUpStage columns ahead of
 // those that are computed: a lane copies the pieces of rows that it uses, 8 KB a warp, 128 KB an
-// SM in flight (with two blocks of 32 columns in registers, 32 KB an SM, 80 us and not 70).  The
+// SM in flight (with two blocks of 32 columns in registers, 32 KB an SM, 80 us and not 70; from rank 33
+// on, whose registers leave one CTA an SM, 64 KB).  The
 // 32-byte pieces of a row of up are placed so that the rows 0, 1, 8 and 9 (16, 17, 24 and 25), of
 // which a half warp loads a piece each, lie on different banks: the two rows 2 apart go elsewhere
 // (ranks up to 16), or the piece's number is changed.
@@ -822,7 +823,7 @@ int width_of(const msa_adapter_cfg *cfg) { return cfg->slice_end[cfg->num_slices
 // How a call's work is cut, and what its workspace holds.
 struct Plan {
     bool wide;               // tiles of 128 tokens (msa_adapter_tile.cu); else of 16
-    bool sorted;             // more than one tile of tokens
+    bool sorted;             // by a kernel: more than 128 tokens, or wide tiles
     int n_blocks, n_tiles;   // tiles of 16: blocks of at most 48 rows of down (two CTAs an SM), tiles of 8 rows in each
     int max_splits;          // pieces of K
     int64_t tiles;           // at most
@@ -840,7 +841,9 @@ int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 // 1,000, 320 rows 20.1 and 30.7 at 300, 31.6 and 29.8 at 500, 54.2 and 38.9 at 1,000; 1,000 and 960 wide,
 // 160 rows 13.4 and 15.0 at 1,500, 17.0 and 15.8 at 2,000).  Adapters in no order fill wide
 // tiles badly below 56 tokens each (16 of them, 320 rows: 37.4 and 60.6 at 500 tokens, 60.2 and 61.0 at
-// 1,000); a batch of 900 tokens or more is rather a prefill's chunks.
+// 1,000); a batch of 900 tokens or more is taken for a prefill's chunks.  That is a guess: the rule sees
+// the table, not how many of its adapters a batch has.  One request's 600 tokens beside a table of 16
+// or more take narrow tiles, 900 requests of one token each wide ones.
 int64_t wide_from(const msa_adapter_cfg *cfg)
 {
     const double rows = (double)cfg->num_slices * cfg->rank;
@@ -1104,7 +1107,7 @@ msa_status msa_adapter_forward(const msa_adapter_cfg *cfg, int64_t num_tokens, c
     }
     const int64_t groups = (num_tokens + 127) / 128;
     // Each chunk reads all parts of u again, max_splits * rank * 4 bytes a token and slice beside its own
-    // 4 a column: chunks grow until that is a quarter, while there are two CTAs an SM (2,048 tokens
+    // 4 a column: chunks grow until that is a quarter, while there are two CTAs for each SM (2,048 tokens
     // of rank 64 64.2 us without and 55.4 with, 1,024 of rank 32 33.8 and 30.0, 512 of rank 96 47.1 and 40.7;
     // for 4,000 of rank 8, whose u is small, as large chunks take 57.2 for 54.8).
     p.chunk = kUpStage;

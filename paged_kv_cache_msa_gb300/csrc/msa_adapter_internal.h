@@ -25,7 +25,7 @@ struct AdapterParams {
     uint16_t *out;
     AdapterHead *head;
     int32_t *adapters;               // of each tile, -1: none
-    int32_t *tokens;                 // [tiles, tile_tokens], -1: none; nullptr: at most 16 tokens, not sorted
+    int32_t *tokens;                 // [tiles, tile_tokens], -1: none; nullptr: at most 128 tokens, not sorted
     float *u;                        // [splits, T, S * r]: sums over pieces of K
     int64_t hidden_stride, down_stride, rows_stride, out_stride;   // elements
     int64_t num_tokens;

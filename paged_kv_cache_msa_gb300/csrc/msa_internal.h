@@ -13,12 +13,14 @@
 #endif
 
 // MSA_STARVE (the starved test build only, never the product): the projection's
-// TMA warps, the query-run indexer's MMA thread and the attention kernels' copy warps
-// issue nothing, so that every wait on their barriers runs out; the tests check that
+// TMA warps, the query-run indexer's MMA thread and the attention and adapter kernels' copy
+// warps issue nothing, so that every wait on their barriers runs out; the tests check that
 // each kernel then stops (the projection without writing, the indexer scoring what it
-// could not finish NaN, the attention with NaN rows), reports the timeout (the
+// could not finish NaN, the attention and the adapters with NaN rows), reports the timeout (the
 // projection) and frees its tensor memory.  No copy or MMA is in flight when the waits
 // give up.
+//
+// MSA_GIVE_UP (a second test build of this): see msa_adapter_tile.cu.
 //
 // MSA_LAG (the lagging test build only): see test_lag in msa_tcgen05.cuh.
 

@@ -70,7 +70,8 @@ class DeviceWorkload:
         import torch
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
-        return B.msa_producer_forward(*self.args(launch_flags, num_tokens), stream=stream.cuda_stream)
+        with B.on_device(self.device):
+            return B.msa_producer_forward(*self.args(launch_flags, num_tokens), stream=stream.cuda_stream)
 
     def outputs_to_host(self):
         q = self.q_out.cpu().numpy().view(np.uint16)
@@ -114,10 +115,11 @@ class DeviceIndexer:
         args = (self.cfg, self.w.idx_q.shape[0], p(self.idx_q), p(self.kv_len),
                 p(self.table_offset), p(self.page_table), self.page_table.numel(), self.cache,
                 p(self.k_scale), p(self.block_scores), p(self.topk_ids))
-        if fused:
-            return B.msa_indexer_forward_fused(*args, p(self.counters), launch_flags,
-                                               stream=stream.cuda_stream)
-        return B.msa_indexer_forward(*args, launch_flags, stream=stream.cuda_stream)
+        with B.on_device(self.device):
+            if fused:
+                return B.msa_indexer_forward_fused(*args, p(self.counters), launch_flags,
+                                                   stream=stream.cuda_stream)
+            return B.msa_indexer_forward(*args, launch_flags, stream=stream.cuda_stream)
 
 
 class DeviceProjection:
@@ -160,7 +162,8 @@ class DeviceProjection:
         import torch
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
-        return B.msa_projection_forward(*self.args(), stream=stream.cuda_stream)
+        with B.on_device(self.device):
+            return B.msa_projection_forward(*self.args(), stream=stream.cuda_stream)
 
     def outputs_to_host(self):
         return self.dw.outputs_to_host()
@@ -395,14 +398,15 @@ class DecodeLayer:
         args = (self.cfg, dw.w.num_tokens, p(dw.idx_q_out), p(self.kv_len), p(self.table_offset),
                 p(dw.page_table), dw.page_table.numel(), dw.caches["idx_k"], p(self.k_scale),
                 p(self.block_scores), p(self.topk_ids))
-        if fused:
-            B.msa_indexer_forward_fused(*args, p(self.counters), flags & B.MSA_LAUNCH_PDL,
-                                        stream=stream.cuda_stream)
-        else:
-            B.msa_indexer_forward(*args, flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)
-        if self.attn_cfg is not None:
-            B.msa_sparse_attention_forward(
-                self.attn_cfg, dw.w.num_tokens, p(dw.q_out), p(self.kv_len), p(self.table_offset),
-                p(dw.page_table), dw.page_table.numel(), p(self.topk_ids), dw.caches["k"], dw.caches["v"],
-                p(dw.scales), p(self.attn_out), p(self.attn_lse), p(self.attn_workspace),
-                self.attn_workspace.nbytes, flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)
+        with B.on_device(dw.device):
+            if fused:
+                B.msa_indexer_forward_fused(*args, p(self.counters), flags & B.MSA_LAUNCH_PDL,
+                                            stream=stream.cuda_stream)
+            else:
+                B.msa_indexer_forward(*args, flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)
+            if self.attn_cfg is not None:
+                B.msa_sparse_attention_forward(
+                    self.attn_cfg, dw.w.num_tokens, p(dw.q_out), p(self.kv_len), p(self.table_offset),
+                    p(dw.page_table), dw.page_table.numel(), p(self.topk_ids), dw.caches["k"], dw.caches["v"],
+                    p(dw.scales), p(self.attn_out), p(self.attn_lse), p(self.attn_workspace),
+                    self.attn_workspace.nbytes, flags & B.MSA_LAUNCH_PDL, stream=stream.cuda_stream)

@@ -75,10 +75,11 @@ class HostPipeline:
             self.s_comp.wait_event(st["h2d"])
             if st["used"]:
                 self.s_comp.wait_event(st["d2h"])         # last outputs of this slot copied out
-            B.msa_producer_forward(self.cfg, n, p(st["qkv"]), self.row_stride, p(st["pos"]),
-                                   p(st["slot"]), p(self.page_table), pt_len, p(wq), p(wk),
-                                   p(wiq), p(wik), p(st["q"]), p(st["iq"]), kc, vc, ikc,
-                                   p(self.scales), self.flags, self.s_comp.cuda_stream)
+            with B.on_device(self.device):
+                B.msa_producer_forward(self.cfg, n, p(st["qkv"]), self.row_stride, p(st["pos"]),
+                                       p(st["slot"]), p(self.page_table), pt_len, p(wq), p(wk),
+                                       p(wiq), p(wik), p(st["q"]), p(st["iq"]), kc, vc, ikc,
+                                       p(self.scales), self.flags, self.s_comp.cuda_stream)
             st["comp"].record(self.s_comp)
             with torch.cuda.stream(self.s_out):
                 self.s_out.wait_event(st["comp"])
@@ -105,8 +106,9 @@ class HostPipeline:
         wq, wk, wiq, wik = self.weights
         kc, vc, ikc = self.caches
         pt_len = 0 if self.page_table is None else self.page_table.numel()
-        B.msa_producer_forward(self.cfg, T, dev[0], self.row_stride, dev[1], dev[2],
-                               p(self.page_table), pt_len, p(wq), p(wk), p(wiq), p(wik),
-                               dev[3], dev[4], kc, vc, ikc, p(self.scales), self.flags,
-                               self.s_comp.cuda_stream)
+        with B.on_device(self.device):
+            B.msa_producer_forward(self.cfg, T, dev[0], self.row_stride, dev[1], dev[2],
+                                   p(self.page_table), pt_len, p(wq), p(wk), p(wiq), p(wik),
+                                   dev[3], dev[4], kc, vc, ikc, p(self.scales), self.flags,
+                                   self.s_comp.cuda_stream)
         self.s_comp.synchronize()

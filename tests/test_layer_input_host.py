@@ -189,3 +189,38 @@ def test_tensors_that_do_fit(gpu):
         positions=Tensor((3, T), I32, strides=(T + 5, 1)), page_table=None)
     run(layer(scales=None), n=1, page_table=Tensor((3, 4), I32))
     run(layer(with_axes=True), n=0)
+
+
+def made(cls, **attributes):
+    """An object of a class without its constructor, which copies to the GPU."""
+    obj = cls.__new__(cls)
+    for name, value in attributes.items():
+        setattr(obj, name, value)
+    return obj
+
+
+def test_the_other_helpers_run_on_their_device(gpu, monkeypatch):
+    from paged_kv_cache_msa_gb300 import device as dev_mod
+    from paged_kv_cache_msa_gb300.pipeline import HostPipeline
+    names = ("msa_producer_forward", "msa_projection_forward", "msa_indexer_forward", "msa_indexer_forward_fused",
+             "msa_sparse_attention_forward")
+    for name in names:
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **k: gpu["calls"].append((_n, gpu["current"])))
+    monkeypatch.setattr(B, "msa_host_buffer_device_address", lambda p: p)
+    t, s = Tensor((T,), I32), Stream()
+    work = type("Work", (), dict(num_tokens=T, idx_q=t))()
+    dw = made(dev_mod.DeviceWorkload, w=work, device=DEV, args=lambda *a: (), idx_q_out=t, q_out=t, page_table=t,
+              scales=t, caches=dict(k=None, v=None, idx_k=None))
+    dw.run()
+    made(dev_mod.DeviceProjection, device=DEV, args=lambda: ()).run()
+    own = dict(device=DEV, cfg=None, idx_q=t, kv_len=t, table_offset=t, page_table=t, cache=None, k_scale=t, block_scores=t,
+               topk_ids=t, counters=t)
+    for fused in (False, True):
+        made(dev_mod.DeviceIndexer, w=work, **own).run(fused=fused)
+        lse = type("Bytes", (Tensor,), dict(nbytes=64))((T,), U8)
+        made(dev_mod.DecodeLayer, dw=dw, attn_cfg=cfg(), attn_out=t, attn_lse=t, attn_workspace=lse, **own).run(s, fused=fused)
+    stream = type("S", (Stream,), dict(synchronize=lambda self: None))()
+    made(HostPipeline, device=DEV, cfg=None, row_stride=W, weights=(None,) * 4, caches=(None,) * 3, scales=t, page_table=None,
+         flags=0, s_comp=stream).run_zero_copy(t, t, t, t, t)
+    assert len(gpu["calls"]) == 1 + 1 + 2 + 2 * 3 + 1 and {n for n, _ in gpu["calls"]} == set(names)
+    assert all(d == 1 for _, d in gpu["calls"]), gpu["calls"]

@@ -16,8 +16,8 @@
  * the layer's producer with every request's adapter.
  *
  * Arithmetic: sums are fp32.  The second product runs on the tensor cores, where u is split
- * into three bf16 parts that hold all of its bits; so an element of up that is infinite makes
- * its outputs NaN, where the formula in fp32 has NaN or an infinity.  Results do not depend on which
+ * into three bf16 parts that hold all of its bits; a part may be 0, so that an infinite element of
+ * up gives NaN where the formula in fp32 has an infinity.  Results do not depend on which
  * other calls run, and a call repeated with the same arguments gives the same bits.  A wait inside
  * a kernel that runs out of time (a failure of the hardware, never expected) makes the outputs of
  * its tokens NaN.
